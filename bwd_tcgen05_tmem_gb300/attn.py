@@ -32,7 +32,10 @@ EXPORTED = ["attn_fwd_workspace_size", "attn_bwd_workspace_size", "attn_fwd", "a
             "attn_lse_merge", "attn_cp_relayout",
             "attn_query_status", "attn_last_error", "attn_last_launch_count",
             "attn_debug_inject", "attn_host_arena_size", "attn_fwd_bwd_host",
-            "attn_fwd_bwd_host_stages", "attn_bwd_path"]
+            "attn_fwd_bwd_host_stages", "attn_bwd_path",
+            "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_size",
+            "attn_kv_plan", "attn_kv_write", "attn_kv_read", "attn_kv_decode",
+            "attn_kv_decode_workspace_size"]
 # attn_fwd_bwd_host_stages stage bits
 HOST_UPLOAD, HOST_COMPUTE, HOST_DOWNLOAD, HOST_ALL = 1, 2, 4, 7
 # attn_bwd_path results: which backward kernels run (and the stage order)
@@ -67,6 +70,51 @@ class Params(ctypes.Structure):
         ("accumulate", ctypes.c_int),
         ("seqused_q", ctypes.c_void_p), ("seqused_k", ctypes.c_void_p),
         ("bwd_ds", ctypes.c_int),
+    ]
+
+
+class QkParams(ctypes.Structure):
+    """Mirror of attn_qk_params_t."""
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
+        ("batch", ctypes.c_int), ("seqlen", ctypes.c_int), ("heads_q", ctypes.c_int),
+        ("heads_k", ctypes.c_int), ("head_dim", ctypes.c_int),
+        ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("norm", ctypes.c_int),
+        ("max_pos", ctypes.c_int), ("eps", ctypes.c_float),
+        ("stride_q", ctypes.c_int64 * 3), ("stride_k", ctypes.c_int64 * 3),
+        ("stride_qo", ctypes.c_int64 * 3), ("stride_ko", ctypes.c_int64 * 3),
+        ("stride_dqo", ctypes.c_int64 * 3), ("stride_dko", ctypes.c_int64 * 3),
+    ]
+
+
+class KvPlanParams(ctypes.Structure):
+    """Mirror of attn_kv_plan_params_t."""
+    _fields_ = [
+        ("batch", ctypes.c_int), ("cols", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("rows", ctypes.c_int), ("n_free", ctypes.c_int),
+        ("table_stride", ctypes.c_int64),
+    ]
+
+
+class Kv4CacheDesc(ctypes.Structure):
+    """Mirror of attn_kv4_cache_t."""
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("heads_kv", ctypes.c_int),
+        ("d_qk", ctypes.c_int), ("d_v", ctypes.c_int),
+    ]
+
+
+class Kv4DecodeParams(ctypes.Structure):
+    """Mirror of attn_kv4_decode_params_t."""
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("o_dtype", ctypes.c_int), ("batch", ctypes.c_int),
+        ("seqlen_q", ctypes.c_int), ("heads_q", ctypes.c_int),
+        ("stride_q", ctypes.c_int64 * 3), ("stride_o", ctypes.c_int64 * 3),
+        ("cols", ctypes.c_int), ("table_stride", ctypes.c_int64),
+        ("window_left", ctypes.c_int), ("sinks", ctypes.c_int),
+        ("softmax_scale", ctypes.c_float),
     ]
 
 
@@ -122,6 +170,25 @@ def load():
         lib.attn_fwd_bwd_host.restype = ctypes.c_int
         lib.attn_fwd_bwd_host_stages.argtypes = [P] + [vp] * 9 + [vp, sz, ctypes.c_uint, vp]
         lib.attn_fwd_bwd_host_stages.restype = ctypes.c_int
+        QP = ctypes.POINTER(QkParams)
+        lib.attn_qk_norm_rope.argtypes = [QP] + [vp] * 11
+        lib.attn_qk_norm_rope.restype = ctypes.c_int
+        lib.attn_qk_norm_rope_bwd_workspace_size.argtypes = [QP]
+        lib.attn_qk_norm_rope_bwd_workspace_size.restype = sz
+        lib.attn_qk_norm_rope_bwd.argtypes = [QP] + [vp] * 14 + [sz, vp, vp]
+        lib.attn_qk_norm_rope_bwd.restype = ctypes.c_int
+        lib.attn_kv_plan.argtypes = [ctypes.POINTER(KvPlanParams)] + [vp] * 12
+        lib.attn_kv_plan.restype = ctypes.c_int
+        C = ctypes.POINTER(Kv4CacheDesc)
+        for name in ("attn_kv_write", "attn_kv_read"):
+            fn = getattr(lib, name)
+            fn.argtypes = [C, ctypes.c_int, ctypes.c_int, vp, i64p, vp, i64p, vp, vp, vp]
+            fn.restype = ctypes.c_int
+        D = ctypes.POINTER(Kv4DecodeParams)
+        lib.attn_kv_decode_workspace_size.argtypes = [D, C]
+        lib.attn_kv_decode_workspace_size.restype = sz
+        lib.attn_kv_decode.argtypes = [D, C] + [vp] * 6 + [sz, vp, vp]
+        lib.attn_kv_decode.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -417,3 +484,165 @@ def cp_relayout(src, dst, *, to_heads, cp, stream=None):
     _check(load().attn_cp_relayout(int(bool(to_heads)), cp, seqlen, heads, d, src.element_size(),
                                    _ptr(src), s_src, _ptr(dst), s_dst, _stream(stream)))
     return dst
+
+
+# ----------------------------------------------------- norm and rotation of q and k
+
+def on_device(t, *others):
+    """The device of CUDA tensor ``t``, on which ``others`` (None apart) must lie too."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    dev = t.device
+    for o in others:
+        if o is not None and o.device != dev:
+            raise ValueError(f"tensors are on {dev} and {o.device}")
+    return dev
+
+
+def launch(device, stream, fn, *args):
+    """fn(*args, stream) with ``device`` current; raises on an error status."""
+    if device.index == torch.cuda.current_device():
+        s = stream if stream is not None else torch.cuda.current_stream()
+        _check(fn(*args, s.cuda_stream))
+        return
+    with torch.cuda.device(device):
+        s = stream if stream is not None else torch.cuda.current_stream()
+        _check(fn(*args, s.cuda_stream))
+
+
+def ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def new(shape, dtype, device, stream):
+    """A new tensor for work on ``stream`` (None: the current one): memory of that
+    stream, so that it is not handed out again while the work is under way."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _qk_strides(t):
+    if t is None:
+        return (0, 0, 0)
+    if t.stride(-1) != 1:
+        raise ValueError("the head-dim axis must be contiguous")
+    s = t.stride()
+    return (0, s[0], s[1]) if len(s) == 3 else s[:3]
+
+
+def _qk_params(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, qo, ko, dqo, dko, status):
+    thd = q.dim() == 3
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [batch, seqlen, heads, d] or [total, heads, d]")
+    b, s = (1, q.shape[0]) if thd else q.shape[:2]
+    hq, d = q.shape[-2:]
+    hk = 0 if k is None else k.shape[-2]
+    for name, t, like in (("k", k, None), ("q_out", qo, q), ("k_out", ko, k), ("dq_out", dqo, q),
+                          ("dk_out", dko, k)):
+        if t is None:
+            continue
+        want = like.shape if like is not None else (*q.shape[:-2], hk, d)
+        if t.shape != want:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(want)}")
+        if t.dtype != q.dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, q has {q.dtype}")
+    rot = max_pos = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin must both be given or None")
+    if cos is not None:
+        if (cos.shape != sin.shape or cos.dim() != 2 or cos.dtype != torch.float32
+                or sin.dtype != torch.float32 or not cos.is_contiguous() or not sin.is_contiguous()):
+            raise ValueError("cos and sin must be contiguous float32 [max_pos, rotary_dim / 2]")
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    if positions is not None and (positions.dtype != torch.int32 or positions.numel() != b * s
+                                  or not positions.is_contiguous()):
+        raise ValueError("positions must be contiguous int32, one for each token")
+    wdt = None
+    for w in (wq, wk):
+        if w is None:
+            continue
+        if w.shape != (d,) or not w.is_contiguous() or (wdt is not None and w.dtype != wdt):
+            raise ValueError("norm weights must be contiguous [head_dim] and of one dtype")
+        wdt = w.dtype
+    if status is not None and status.dtype != torch.int32:
+        raise ValueError("status must be an int32 tensor")
+    return QkParams(_code(q.dtype), FP32 if wdt is None else _code(wdt), b, s, hq, hk, d, rot,
+                    int(bool(interleaved)), int(bool(norm)), max_pos, eps, _qk_strides(q),
+                    _qk_strides(k), _qk_strides(qo), _qk_strides(ko), _qk_strides(dqo),
+                    _qk_strides(dko))
+
+
+def qk_norm_rope(q, k, cos, sin, *, positions=None, wq=None, wk=None, norm=True, eps=1e-6,
+                 interleaved=False, q_out=None, k_out=None, status=None, stream=None):
+    """Norm of each query and key head and rotation by its position, in one
+    pass (attn_qk_norm_rope).  Returns (q_out, k_out).
+
+    q [B, S, Hq, d] or [T, Hq, d]; k likewise or None; cos, sin: float32
+    [max_pos, rotary_dim / 2], or None for no rotation; positions: int32 [B, S]
+    or [T], negative for padding rows (left as they are in ``q_out`` and
+    ``k_out``), or None for 0, 1, ...; wq, wk: [d] or None.  ``q_out=q`` works
+    in place.  ``status``: int32 device word (see include/attn.h), or None."""
+    lib = load()
+    dev = on_device(q, k, cos, sin, positions, wq, wk, q_out, k_out, status)
+    if q_out is None:
+        q_out = new(q.shape, q.dtype, dev, stream)
+    if k_out is None and k is not None:
+        k_out = new(k.shape, q.dtype, dev, stream)
+    p = _qk_params(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, q_out, k_out, None,
+                   None, status)
+    launch(dev, stream, lib.attn_qk_norm_rope, p, ptr(q), ptr(k), ptr(wq), ptr(wk), ptr(cos),
+           ptr(sin), ptr(positions), ptr(q_out), ptr(k_out), ptr(status))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, cos, sin, dq_out, dk_out, *, positions=None, wq=None, wk=None,
+                     norm=True, eps=1e-6, interleaved=False, dq=None, dk=None, dwq=None,
+                     dwk=None, workspace=None, status=None, stream=None):
+    """Gradient of qk_norm_rope: (dq, dk, dwq, dwk) from its inputs q, k and the
+    gradients of its outputs.  dwq and dwk are float32 [d] (None without
+    weights); rows of padding tokens are left as they are in dq and dk."""
+    lib = load()
+    dev = on_device(q, k, cos, sin, dq_out, dk_out, positions, wq, wk, dq, dk, dwq, dwk,
+                    workspace, status)
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out must both be given or None")
+    if dq is None:
+        dq = new(q.shape, q.dtype, dev, stream)
+    if dk is None and k is not None:
+        dk = new(k.shape, q.dtype, dev, stream)
+    if wq is not None and dwq is None:
+        dwq = new(q.shape[-1:], torch.float32, dev, stream)
+    if wk is not None and dwk is None:
+        dwk = new(q.shape[-1:], torch.float32, dev, stream)
+    for w in (dwq, dwk):
+        if w is not None and (w.dtype != torch.float32 or w.shape != q.shape[-1:] or not w.is_contiguous()):
+            raise ValueError("weight gradients must be contiguous float32 [head_dim]")
+    p = _qk_params(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, dq, dk, dq_out,
+                   dk_out, status)
+    if workspace is None:
+        workspace = new(_sized(dev, lib.attn_qk_norm_rope_bwd_workspace_size, p), torch.uint8, dev,
+                        stream)
+    launch(dev, stream, lib.attn_qk_norm_rope_bwd, p, ptr(q), ptr(k), ptr(wq), ptr(wk), ptr(cos),
+           ptr(sin), ptr(positions), ptr(dq_out), ptr(dk_out), ptr(dq), ptr(dk), ptr(dwq), ptr(dwk),
+           ptr(workspace), workspace.numel() * workspace.element_size(), ptr(status))
+    return dq, dk, dwq, dwk
+
+
+def _sized(device, fn, *args):
+    """fn(*args) with ``device`` current (workspace sizes follow its SM count)."""
+    if device.index == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
+def rope_tables(max_pos, rotary_dim, *, base=10000.0, device="cuda"):
+    """cos, sin (float32 [max_pos, rotary_dim / 2]) of the angles pos *
+    base^(-2 i / rotary_dim), computed in float64: an angle of 10^6 has an
+    error of 0.03 in float32."""
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64, device=device)
+    ang = (torch.arange(max_pos, dtype=torch.float64, device=device)[:, None]
+           * base ** (-2.0 * i / rotary_dim))
+    return ang.cos().float(), ang.sin().float()

@@ -9,6 +9,7 @@
 #include <cstring>
 
 #include "../../include/attn.h"
+#include "api.h"
 #include "bwd.h"
 #include "kcommon.cuh"
 
@@ -58,6 +59,10 @@ attn_status_t cuda_fail(cudaError_t e, const char* what) {
   return fail(ATTN_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+}  // namespace
+
+// What the other translation units that hold C entry points use (api.h).
+namespace attn {
 int num_sms() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
@@ -69,6 +74,26 @@ int num_sms() {
   if (dev >= 0 && dev < 64) cache[dev] = n;
   return n;
 }
+void api_begin() {
+  g_err[0] = 0;
+  g_launches = 0;
+}
+attn_status_t api_fail(attn_status_t s, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return s;
+}
+attn_status_t api_launched(cudaError_t e, int n, const char* what) {
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  g_launches += n;
+  return ATTN_OK;
+}
+}  // namespace attn
+
+namespace {
+using attn::num_sms;
 
 constexpr size_t kStatusBytes = 256;
 
@@ -919,6 +944,9 @@ attn_status_t attn_query_status(const void* ws, attn_stream_t stream) {
   if (v == attn::DEV_BAD_SEQLENS)
     return fail(ATTN_ERR_BAD_METADATA, "device check: cu_seqlens inconsistent");
   if (v == attn::DEV_TIMEOUT) return fail(ATTN_ERR_TIMEOUT, "device wait exceeded its limit");
+  if (v == attn::DEV_BAD_INDEX)
+    return fail(ATTN_ERR_BAD_METADATA,
+                "device check: a length, position, slot or page is out of range");
   if (v == attn::DEV_WORKSPACE)
     return fail(ATTN_ERR_WORKSPACE, "device check: score tiles exceed the workspace");
   return fail(ATTN_ERR_CUDA, "device status %d", v);

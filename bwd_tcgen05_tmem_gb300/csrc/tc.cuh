@@ -28,6 +28,7 @@ enum : int {
   DEV_BAD_SEQLENS = 2,  // cu_seqlens failed validation
   DEV_TMEM = 3,         // TMEM allocation returned an unusable address
   DEV_WORKSPACE = 4,    // the score tiles of the wide backward exceed the workspace
+  DEV_BAD_INDEX = 5,    // a length, position, slot or page is out of range
 };
 
 // Wall-clock limit of one wait (ns).  A healthy wait lasts microseconds.

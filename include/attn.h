@@ -1,6 +1,7 @@
 /*
  * attn.h -- C ABI of libattn.so: fused causal scaled-dot-product attention
- * (forward, backward, LSE merge) for NVIDIA GB300 (sm_103a).
+ * (forward, backward, LSE merge), the norm and rotation of its queries and
+ * keys, and attention over a paged 4-bit cache, for NVIDIA GB300 (sm_103a).
  *
  * Sources for the operations (web pages on Blackwell attention backends):
  *  - TransformerEngine PR #3527, "cuDNN FROST attention backend for head_dim in
@@ -59,7 +60,8 @@ typedef enum {
   ATTN_ERR_UNSUPPORTED = 2,  /* valid request this library refuses (head dim, dtype mix) */
   ATTN_ERR_ALIGNMENT = 3,    /* pointer or stride not 16-byte aligned as required */
   ATTN_ERR_WORKSPACE = 4,    /* workspace missing or smaller than *_workspace_size() */
-  ATTN_ERR_BAD_METADATA = 5, /* device check: cu_seqlens inconsistent (status word) */
+  ATTN_ERR_BAD_METADATA = 5, /* device check: cu_seqlens inconsistent, or an index out of
+                                range (status word) */
   ATTN_ERR_TIMEOUT = 6,      /* device wait exceeded its time limit (status word) */
   ATTN_ERR_CUDA = 7          /* a CUDA runtime call failed; see attn_last_error() */
 } attn_status_t;
@@ -331,6 +333,182 @@ attn_status_t attn_lse_merge(int n_parts, const float* const* o_parts,
 attn_status_t attn_cp_relayout(int to_heads, int cp, int64_t seqlen, int heads, int d,
                                int elem_bytes, const void* src, const int64_t src_strides[3],
                                void* dst, const int64_t dst_strides[3], attn_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Around the attention calls: queries and keys before them, and a cache of
+ * keys and values held in 4 bits for attention of a few new tokens at a time.
+ *
+ * These entry points take an optional device word `status` (int32, or NULL).
+ * It is sticky: a call never clears it, and sets it to a non-zero value when
+ * the device meets a length, position, slot or page that is out of range;
+ * attn_query_status(status) reports that as ATTN_ERR_BAD_METADATA.  Zero it
+ * once and look at it when convenient.  Nothing out of range is read or
+ * written either way.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Norm of each query and key head and rotation by its position, in one pass.
+ * For every row x (token, head; head_dim elements), in FP32:
+ *     y = x / sqrt(mean(x^2) + eps) * w        (norm = 0: y = x, w = NULL)
+ *     z = y turned by the angles of the token's position on its first
+ *         rotary_dim elements: pairs (i, i + rotary_dim/2), or (2i, 2i+1) with
+ *         interleaved = 1:  (a, b) -> (a cos - b sin, b cos + a sin)
+ * rounded once to dtype.  cos/sin: FP32 [max_pos][rotary_dim/2], contiguous,
+ * 16-byte aligned (make them in FP64: angles of far positions need it).
+ * positions: int32 [batch][seqlen], contiguous, or NULL for 0, 1, .. in each
+ * sequence (packed THD tensors: batch 1, seqlen = total).  A negative position
+ * marks padding: its rows are neither read nor written.  A position >= max_pos
+ * gives NaN rows and sets the status word.
+ * w_q / w_k: [head_dim] of w_dtype (FP32 or dtype), or NULL for ones.
+ * q, k (and their strides) as in attn_fwd; heads_k may be 0 (queries alone),
+ * then the k arguments are ignored.  Views of one projection are fine.
+ * z may be written over x (q_out == q with the same strides); any other
+ * overlap of an output is refused.
+ * head_dim 64, 128, 192, 256 or 512; rotary_dim a multiple of 16 up to head_dim, or 0.
+ */
+typedef struct {
+  attn_dtype_t dtype;    /* q, k, q_out, k_out and gradients: BF16 or FP16 */
+  attn_dtype_t w_dtype;  /* norm weights: FP32 or == dtype */
+  int batch, seqlen, heads_q, heads_k, head_dim;
+  int rotary_dim, interleaved, norm, max_pos;
+  float eps;
+  int64_t stride_q[3], stride_k[3];       /* {batch, token, head}, in elements */
+  int64_t stride_qo[3], stride_ko[3];     /* q_out, k_out; backward: dq, dk */
+  int64_t stride_dqo[3], stride_dko[3];   /* backward: gradients of q_out, k_out */
+} attn_qk_params_t;
+attn_status_t attn_qk_norm_rope(const attn_qk_params_t* p, const void* q, const void* k,
+                                const void* w_q, const void* w_k, const float* cos,
+                                const float* sin, const int32_t* positions, void* q_out,
+                                void* k_out, int32_t* status, attn_stream_t stream);
+/*
+ * Its gradient, from q, k and the gradients of q_out, k_out: dq, dk (dtype) and
+ * the weights' dw_q, dw_k (FP32 [head_dim], summed over all tokens and heads,
+ * overwritten; NULL where not wanted).  Rows at negative positions get no
+ * gradient (dq, dk untouched there) and add nothing to dw.  The order of the
+ * sums is fixed: bitwise reproducible.  dq may be written over the gradient of
+ * q_out (same strides), not over q.  workspace: 256-byte aligned,
+ * attn_qk_norm_rope_bwd_workspace_size(p) bytes (of the current device).
+ */
+size_t attn_qk_norm_rope_bwd_workspace_size(const attn_qk_params_t* p);
+attn_status_t attn_qk_norm_rope_bwd(const attn_qk_params_t* p, const void* q, const void* k,
+                                    const void* w_q, const void* w_k, const float* cos,
+                                    const float* sin, const int32_t* positions,
+                                    const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                    float* dw_q, float* dw_k, void* workspace,
+                                    size_t workspace_bytes, int32_t* status,
+                                    attn_stream_t stream);
+
+/*
+ * Where the new tokens of a step go.  Request b holds context[b] tokens and
+ * gets fresh[b] more; its page table is row b of block_table (int32,
+ * [batch][cols], rows table_stride apart; page_size tokens a page).
+ *   cu_seqlens [batch+1]: prefix sums of fresh;  seq_lens [batch]: context + fresh
+ *   positions, slots [rows]: of the new tokens, packed in order of the requests
+ *     (slot = page * page_size + position % page_size); rows past the last token are -1
+ * With free_pages (int32 [n_free]) the pages that the new tokens need beyond
+ * those held, ceil((context + fresh) / page_size) - ceil(context / page_size)
+ * a request, are taken in order from free_pages[free_head[0] ..], written into
+ * block_table, and free_head_out[0] = free_head[0] + pages taken.  With
+ * free_pages NULL the table is only read (a map of tokens that have pages
+ * already) and free_head, free_head_out are ignored.
+ * Out of range (status word): lengths that are negative or longer than cols *
+ * page_size (the request counts as empty), more tokens than rows (the rest is
+ * left out), pages outside [0, num_pages) or past n_free (slot -1, table entry -1).
+ * The inputs are not changed (block_table apart), so a call can be repeated.
+ * No output may overlap an input or another output.  batch <= 8192; page_size a power of two, 16 to
+ * 256; cols * page_size <= 2^30; num_pages * page_size < 2^31.
+ */
+typedef struct {
+  int batch, cols, page_size, num_pages, rows, n_free;
+  int64_t table_stride;
+} attn_kv_plan_params_t;
+attn_status_t attn_kv_plan(const attn_kv_plan_params_t* p, const int32_t* context,
+                           const int32_t* fresh, int32_t* block_table,
+                           const int32_t* free_pages, const int32_t* free_head,
+                           int32_t* cu_seqlens, int32_t* seq_lens, int32_t* positions,
+                           int32_t* slots, int32_t* free_head_out, int32_t* status,
+                           attn_stream_t stream);
+
+/*
+ * A cache of keys and values in 4 bits.  For a row x (one token, one kv head)
+ * and each 32 neighbouring elements of it:
+ *     s = bf16(max|x| / 7),  code = clamp(round(x / s), -7, 7) + 8,  value = (code - 8) s
+ * (round to nearest, ties to even; s = 0: codes 8).  A group that holds an
+ * infinity or a NaN reads back as NaN.  Arrays, contiguous and 16-byte aligned,
+ * G = d / 32:
+ *     codes  [num_pages][heads_kv][page_size][d / 2] bytes
+ *     scales [num_pages][heads_kv][page_size][G]     bf16
+ * A K row is 4 G words: word c G + g holds dims 32 g + 8 c .. + 7; a V row is
+ * 8 G half-words: half-word r G + g holds dims 32 g + 4 r .. + 3; lowest
+ * nibble first (the order in which attn_kv_decode reads them).
+ * (d_qk, d_v): (64,64) (128,128) (192,128) (256,256).  page_size a power of
+ * two, 16 to 256; num_pages * page_size < 2^31.
+ */
+typedef struct {
+  void* k_codes;
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+  int num_pages, page_size, heads_kv, d_qk, d_v;
+} attn_kv4_cache_t;
+
+/*
+ * Rows into the cache and back.  k [tokens][heads_kv][d_qk], v
+ * [tokens][heads_kv][d_v] of dtype (BF16 or FP16), strides {token, head} in
+ * elements (multiples of 8), 16-byte aligned.  Token t lives at slots[t] (page *
+ * page_size + offset); a negative slot leaves token t out (write: nothing is
+ * stored; read: its row stays as it was); one past the cache does too, and sets
+ * the status word.  A write's slots must differ from each other: of rows
+ * written to one slot in one call, parts of either may remain.
+ * Values are rounded once to dtype when read.
+ */
+attn_status_t attn_kv_write(const attn_kv4_cache_t* cache, attn_dtype_t dtype, int tokens,
+                             const void* k, const int64_t stride_k[2], const void* v,
+                             const int64_t stride_v[2], const int32_t* slots, int32_t* status,
+                             attn_stream_t stream);
+attn_status_t attn_kv_read(const attn_kv4_cache_t* cache, attn_dtype_t dtype, int tokens,
+                            void* k, const int64_t stride_k[2], void* v,
+                            const int64_t stride_v[2], const int32_t* slots, int32_t* status,
+                            attn_stream_t stream);
+
+/*
+ * Attention of the last seqlen_q tokens of each sequence (1 to 256: a decode
+ * step, drafted tokens, a short chunk) over the 4-bit cache.  Sequence b holds
+ * seq_lens[b] tokens, those seqlen_q among them, in the pages of row b of
+ * block_table.  Query i stands at pos = seq_lens[b] - seqlen_q + i and sees
+ * tokens j <= pos with window_left < 0, or j >= pos - window_left, or
+ * j < sinks (a sliding window whose first tokens stay visible).
+ *     o   [batch][seqlen_q][heads_q][d_v] of o_dtype, lse FP32 [batch][heads_q][seqlen_q]
+ * (natural log; a query that sees nothing, of an empty sequence or at a
+ * negative position, gets O = 0, LSE = -inf).  Entries of the table past a
+ * sequence's last page, and what a page holds past its last token, are not
+ * looked at.  Sums are FP32; probabilities times V's scales are rounded to
+ * dtype for the second product.  The result does not depend on other
+ * sequences' lengths beyond the order of its sums, and is bitwise
+ * reproducible for the same call on the same device.
+ * Lengths are read on the device: a captured call serves any lengths.
+ * seq_lens out of [0, cols * page_size] count as 0 and set the status word; so
+ * does a page outside the cache (that sequence's result is then undefined).
+ * workspace: 256-byte aligned, attn_kv_decode_workspace_size() bytes (of the
+ * current device); it needs no preparation, and calls that may overlap in
+ * time need one each.
+ */
+typedef struct {
+  attn_dtype_t dtype;    /* q: BF16 or FP16 */
+  attn_dtype_t o_dtype;  /* == dtype, or FP32 */
+  int batch, seqlen_q, heads_q;  /* heads_q % heads_kv == 0, heads_q / heads_kv <= 128 */
+  int64_t stride_q[3], stride_o[3]; /* {batch, token, head} */
+  int cols;              /* columns of block_table; cols * page_size <= 2^30 */
+  int64_t table_stride;  /* elements between its rows */
+  int window_left, sinks;
+  float softmax_scale;
+} attn_kv4_decode_params_t;
+size_t attn_kv_decode_workspace_size(const attn_kv4_decode_params_t* p,
+                                      const attn_kv4_cache_t* cache);
+attn_status_t attn_kv_decode(const attn_kv4_decode_params_t* p, const attn_kv4_cache_t* cache,
+                              const void* q, const int32_t* block_table,
+                              const int32_t* seq_lens, void* o, float* lse, void* workspace,
+                              size_t workspace_bytes, int32_t* status, attn_stream_t stream);
 
 /* Synchronises `stream` and returns the status word in `workspace`
  * (ATTN_OK, ATTN_ERR_BAD_METADATA, ATTN_ERR_TIMEOUT or, for the head-dim-512

@@ -1,0 +1,279 @@
+"""attn.qk_norm_rope and its gradient on the GPU against the float64 form.
+
+Tolerances, from the arithmetic.  One rounding to the type: u |z| (u = 2^-8 bf16,
+2^-11 fp16, half a step), 2^-25 for fp16 values below its normal range.  FP32
+inside: the norm's sum has at most 48 terms a lane and 5 exchanges, a product
+chain of 3 and a turn of 3 operations follow, each at most 2^-24: under 64 *
+2^-24 = 2^-18 of the turned pair's length.  The gradient has two such sums:
+2^-17 of the sizes that cancel.  A sum over n rows adds at most n + 64 roundings."""
+import pytest
+import torch
+
+import kvref
+from bwd_tcgen05_tmem_gb300 import attn
+
+pytestmark = pytest.mark.gpu
+UNIT = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+BF, FP = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from bwd_tcgen05_tmem_gb300 import build
+    build.build()
+    attn.load()
+
+
+def make(b, s, hq, hk, d, dt, seed, wdt=torch.float32, spread=True):
+    """q, k as slices of one projection, weights, gradients, positions."""
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *n: torch.randn(*n, generator=g)  # noqa: E731
+    x = r(b, s, hq + hk + 1, d)
+    if spread:  # rows of very different sizes
+        x = x * torch.exp2(torch.randint(-8, 9, (b, s, hq + hk + 1, 1), generator=g).float())
+    qkv = x.to(dt).cuda()
+    pos = torch.randint(0, 5000, (b, s), generator=g, dtype=torch.int32).cuda()
+    return dict(q=qkv[:, :, :hq], k=qkv[:, :, hq:hq + hk], wq=(1 + 0.3 * r(d)).to(wdt).cuda(),
+                wk=(1 + 0.3 * r(d)).to(wdt).cuda(), dqo=r(b, s, hq, d).to(dt).cuda(),
+                dko=r(b, s, hk, d).to(dt).cuda(), pos=pos)
+
+
+def close(got, want, tol):
+    got = got.double()
+    assert torch.isfinite(got).all()
+    over = (got - want).abs() - tol
+    assert (over <= 0).all(), (float(over.max()), float(tol.flatten()[over.argmax()]))
+
+
+def pair_length(y, rot, inter):
+    """sqrt of both squares of the pair that each element is turned with."""
+    one = torch.ones(y.shape[:-2] + (rot // 2,), dtype=torch.float64, device=y.device)
+    sq = kvref.turn(y.pow(2), one * 0, one, inter)  # (a, b) -> (-b, a)
+    return (y.pow(2) + torch.where(torch.arange(y.shape[-1], device=y.device) < rot, sq.abs(), 0 * sq)).sqrt()
+
+
+def check(m, cos, sin, inter, norm=True, weights=True, eps=1e-6, positions=True, b3=False):
+    dt, d = m["q"].dtype, m["q"].shape[-1]
+    u = UNIT[dt]
+    rot = 0 if cos is None else 2 * cos.shape[1]
+    wq, wk = (m["wq"], m["wk"]) if weights else (None, None)
+    pos = m["pos"] if positions else None
+    ts = [m["q"], m["k"], m["dqo"], m["dko"]]
+    if b3:  # packed tensors
+        ts = [t[0] for t in ts]
+        pos = pos[0]
+    kw = dict(positions=pos, wq=wq, wk=wk, norm=norm, eps=eps, interleaved=inter)
+    zq, zk = attn.qk_norm_rope(ts[0], ts[1], cos, sin, **kw)
+    grads = attn.qk_norm_rope_bwd(ts[0], ts[1], cos, sin, ts[2], ts[3], **kw)
+    again = attn.qk_norm_rope_bwd(ts[0], ts[1], cos, sin, ts[2], ts[3], **kw)
+    torch.cuda.synchronize()
+    for a, b in zip(grads, again):
+        assert (a is None and b is None) or torch.equal(a, b)
+    at = (m["pos"] if positions else torch.arange(m["q"].shape[1], device="cuda").expand(m["q"].shape[:2])).long()
+    c, s = (cos[at].double(), sin[at].double()) if rot else (None, None)
+    n_rows = m["q"].shape[0] * m["q"].shape[1]
+    for x, w, z, dz, dx, dw in ((m["q"], wq, zq, m["dqo"], grads[0], grads[2]),
+                                (m["k"], wk, zk, m["dko"], grads[1], grads[3])):
+        z, dx = z.view(x.shape), dx.view(x.shape)
+        x64 = x.double().requires_grad_()
+        w64 = None if w is None else w.double().requires_grad_()
+        want = kvref.norm_rope(x64, w64, c, s, norm, eps, inter)
+        y = kvref.norm_rope(x64, w64, None, None, norm, eps, inter).detach()
+        length = pair_length(y, rot, inter) if rot else y.abs()
+        close(z, want.detach(), u * want.detach().abs() + 2.0 ** -18 * length + 2.0 ** -25)
+        (want * dz.double()).sum().backward()
+        # the sizes that cancel in dx = r (g - x r^2 mean(g x))
+        gl = pair_length(dz.double(), rot, inter) if rot else dz.double().abs()
+        gl = gl if w is None else gl * w.double().abs()
+        r = 1 / torch.sqrt(x.double().pow(2).mean(-1, keepdim=True) + eps) if norm else torch.ones_like(x.double()[..., :1])
+        size = r * (gl + (x.double().abs() * r * r * (gl * x.double().abs()).mean(-1, keepdim=True) if norm else 0))
+        close(dx, x64.grad, u * x64.grad.abs() + 2.0 ** -17 * size + 2.0 ** -25)
+        if w is not None:
+            total = (gl / w.double().abs() * (x.double() * r).abs()).sum((0, 1, 2))
+            close(dw, w64.grad, 2.0 ** -24 * (n_rows * x.shape[2] + 64) * total)
+        else:
+            assert dw is None
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("d,rot,inter", [(64, 64, False), (64, 32, True), (128, 128, False), (128, 128, True),
+                                         (128, 16, False), (192, 192, False), (192, 64, True), (192, 96, False),
+                                         (256, 256, True), (256, 64, False), (512, 512, False), (512, 256, True)])
+def test_dims(d, rot, inter, dt):
+    cos, sin = attn.rope_tables(5000, rot)
+    check(make(2, 37, 5, 2, d, dt, seed=d + rot), cos, sin, inter)
+
+
+@pytest.mark.parametrize("b,s,hq,hk", [(1, 1, 1, 1), (1, 1, 32, 8), (3, 1, 7, 7), (1, 301, 17, 1), (5, 3, 128, 2)])
+def test_sizes_and_heads(b, s, hq, hk):
+    cos, sin = attn.rope_tables(5000, 128)
+    check(make(b, s, hq, hk, 128, BF, seed=s + hq), cos, sin, False)
+
+
+@pytest.mark.parametrize("kw", [dict(norm=False, weights=False), dict(weights=False), dict(eps=0.1),
+                                dict(positions=False), dict(norm=False, weights=False, positions=False)])
+def test_without_norm_weights_or_positions(kw):
+    cos, sin = attn.rope_tables(5000, 128)
+    check(make(2, 19, 4, 2, 128, FP, seed=9), cos, sin, False, **kw)
+
+
+def test_norm_alone_and_16_bit_weights():
+    check(make(2, 19, 4, 2, 256, BF, seed=10), None, None, False)
+    cos, sin = attn.rope_tables(5000, 64)
+    check(make(2, 19, 4, 2, 64, BF, seed=11, wdt=BF), cos, sin, True)
+    check(make(1, 19, 4, 2, 192, FP, seed=12, wdt=FP), cos, sin, True)
+
+
+def test_packed():
+    cos, sin = attn.rope_tables(5000, 128)
+    check(make(1, 77, 4, 2, 128, BF, seed=13), cos, sin, False, b3=True)
+
+
+def test_queries_alone_and_in_place():
+    m = make(2, 50, 6, 2, 128, BF, seed=14)
+    cos, sin = attn.rope_tables(5000, 128)
+    kw = dict(positions=m["pos"], wq=m["wq"], wk=m["wk"])
+    zq, zk = attn.qk_norm_rope(m["q"], m["k"], cos, sin, **kw)
+    only, none = attn.qk_norm_rope(m["q"], None, cos, sin, positions=m["pos"], wq=m["wq"])
+    assert none is None and torch.equal(only, zq)
+    full = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], **kw)
+    part = attn.qk_norm_rope_bwd(m["q"], None, cos, sin, m["dqo"], None, positions=m["pos"], wq=m["wq"])
+    assert torch.equal(full[0], part[0]) and part[1] is None and part[3] is None
+    n = m["q"].shape[0] * m["q"].shape[1] * m["q"].shape[2]
+    assert torch.allclose(full[2], part[2], rtol=0, atol=float(2.0 ** -23 * n * full[2].abs().max()))
+    # the gradient over the incoming one, the forward over the projection
+    dqo, dko = m["dqo"].clone(), m["dko"].clone()
+    attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, dqo, dko, dq=dqo, dk=dko, **kw)
+    assert torch.equal(dqo, full[0]) and torch.equal(dko, full[1])
+    attn.qk_norm_rope(m["q"], m["k"], cos, sin, q_out=m["q"], k_out=m["k"], **kw)
+    assert torch.equal(m["q"], zq) and torch.equal(m["k"], zk)
+
+
+def test_padding_rows_stay_and_add_nothing():
+    m = make(2, 40, 4, 2, 128, BF, seed=15)
+    cos, sin = attn.rope_tables(5000, 128)
+    pad = torch.zeros(2, 40, dtype=torch.bool)
+    pad[0, 33:], pad[1, 5], pad[1, 12:20] = True, True, True
+    m["pos"][pad.cuda()] = -1
+    kw = dict(positions=m["pos"], wq=m["wq"], wk=m["wk"])
+    held = [torch.full_like(t, 7.0) for t in (m["dqo"], m["dko"])]
+    z = attn.qk_norm_rope(m["q"], m["k"], cos, sin, q_out=held[0].clone(), k_out=held[1].clone(), **kw)
+    g = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], dq=held[0].clone(), dk=held[1].clone(), **kw)
+    poison = {n: t.clone() for n, t in m.items()}
+    for n in ("q", "k", "dqo", "dko"):
+        poison[n][pad.cuda()] = float("nan")
+    z2 = attn.qk_norm_rope(poison["q"], poison["k"], cos, sin, q_out=held[0].clone(), k_out=held[1].clone(), **kw)
+    g2 = attn.qk_norm_rope_bwd(poison["q"], poison["k"], cos, sin, poison["dqo"], poison["dko"],
+                               dq=held[0].clone(), dk=held[1].clone(), **kw)
+    for a, b in zip((*z, *g), (*z2, *g2)):
+        assert torch.equal(a, b)
+    for t in (*z, g[0], g[1]):
+        assert (t[pad.cuda()] == 7.0).all() and torch.isfinite(t).all()
+
+
+def test_positions_outside_the_tables_give_nan_and_a_status():
+    m = make(1, 9, 4, 2, 128, BF, seed=16)
+    cos, sin = attn.rope_tables(5000, 128)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(wq=m["wq"], wk=m["wk"], status=status)
+    attn.qk_norm_rope(m["q"], m["k"], cos, sin, positions=m["pos"], **kw)
+    attn.query_status(status)
+    m["pos"][0, 4], m["pos"][0, 6] = 5000, 2 ** 31 - 1
+    z = attn.qk_norm_rope(m["q"], m["k"], cos, sin, positions=m["pos"], **kw)
+    for t in z:
+        assert torch.isnan(t[0, [4, 6]]).all() and torch.isfinite(t[0, [0, 1, 2, 3, 5, 7, 8]]).all()
+    with pytest.raises(attn.AttnError, match="out of range"):
+        attn.query_status(status)
+
+
+def test_offsets_past_32_bits_and_broadcast_input():
+    """Tokens 2^28 elements apart, and one row broadcast to all heads."""
+    d, far = 128, 1 << 28
+    big = torch.zeros(9 * far + 4 * d, dtype=BF, device="cuda")
+    q = big.as_strided((1, 10, 4, d), (0, far, d, 1))
+    g = torch.Generator().manual_seed(17)
+    x = torch.randn(1, 10, 4, d, generator=g).to(BF).cuda()
+    q.copy_(x)
+    cos, sin = attn.rope_tables(16, d)
+    z, _ = attn.qk_norm_rope(q, None, cos, sin)
+    w, _ = attn.qk_norm_rope(x, None, cos, sin)
+    assert torch.equal(z, w)
+    attn.qk_norm_rope(x, None, cos, sin, q_out=q)
+    assert torch.equal(q, w)
+    one = x[:, :, :1].expand(1, 10, 4, d)
+    z, _ = attn.qk_norm_rope(one, None, cos, sin)
+    assert torch.equal(z, w[:, :, :1].expand(1, 10, 4, d))
+
+
+def test_captured_and_on_another_stream():
+    m = make(2, 33, 8, 2, 128, BF, seed=18)
+    cos, sin = attn.rope_tables(5000, 128)
+    kw = dict(positions=m["pos"], wq=m["wq"], wk=m["wk"])
+
+    def step():
+        z = attn.qk_norm_rope(m["q"], m["k"], cos, sin, **kw)
+        return (*z, *attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], **kw))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    m["q"].mul_(2)
+    m["dko"].neg_()
+    m["pos"].add_(-1).clamp_(min=-1)
+    graph.replay()
+    torch.cuda.synchronize()
+    live = (m["pos"] >= 0)
+    want = step()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b) if a.dim() == 1 else torch.equal(a[live], b[live])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    z = attn.qk_norm_rope(m["q"], m["k"], cos, sin, stream=side, **kw)
+    g = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], stream=side, **kw)
+    side.synchronize()
+    for a, b in zip((*z, *g), want):
+        assert torch.equal(a, b) if a.dim() == 1 else torch.equal(a[live], b[live])
+
+
+def test_no_rows():
+    cos, sin = attn.rope_tables(16, 128)
+    q = torch.empty(2, 0, 4, 128, dtype=BF, device="cuda")
+    w = torch.ones(128, device="cuda")
+    z = attn.qk_norm_rope(q, q, cos, sin, wq=w, wk=w)
+    g = attn.qk_norm_rope_bwd(q, q, cos, sin, q, q, wq=w, wk=w)
+    assert z[0].shape == q.shape and (g[2] == 0).all() and (g[3] == 0).all()
+    with pytest.raises(ValueError, match="shape"):
+        attn.qk_norm_rope(q, q[..., :64], cos, sin)
+
+
+def test_with_attention_training():
+    """norm + rotation, attention forward and backward, and their gradient,
+    against float64 autograd of the whole.  Bound: the relative L2 bound 0.008 of
+    the attention gradients, plus the roundings of q, k and of their gradients."""
+    import math
+    b, s, hq, hk, d = 1, 192, 4, 2, 128
+    m = make(b, s, hq, hk, d, BF, seed=19, spread=False)
+    g = torch.Generator().manual_seed(20)
+    v, do = (torch.randn(b, s, h, d, generator=g).to(BF).cuda() for h in (hk, hq))
+    cos, sin = attn.rope_tables(5000, d)
+    kw = dict(positions=m["pos"], wq=m["wq"], wk=m["wk"])
+    q, k = attn.qk_norm_rope(m["q"], m["k"], cos, sin, **kw)
+    o, lse = attn.fwd(q, k, v)
+    dq, dk, dv = attn.bwd(q, k, v, o, do, lse)
+    got = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, dq, dk, **kw)
+    torch.cuda.synchronize()
+    x = [m[n].double().requires_grad_() for n in ("q", "k", "wq", "wk")]
+    c, sn = cos[m["pos"].long()].double(), sin[m["pos"].long()].double()
+    q64 = kvref.norm_rope(x[0], x[2], c, sn, True, 1e-6, False).transpose(1, 2)
+    k64 = kvref.norm_rope(x[1], x[3], c, sn, True, 1e-6, False).transpose(1, 2).repeat_interleave(hq // hk, 1)
+    sc = q64 @ k64.transpose(-1, -2) / math.sqrt(d)
+    sc = sc.masked_fill(torch.ones(s, s, device="cuda").triu(1).bool(), -math.inf)
+    o64 = (sc.softmax(-1) @ v.double().transpose(1, 2).repeat_interleave(hq // hk, 1)).transpose(1, 2)
+    (o64 * do.double()).sum().backward()
+    for t, w in ((o, o64.detach()), *zip(got, [y.grad for y in x])):
+        rel = float((t.double() - w).norm() / w.norm())
+        assert rel < 0.008 + 4 * 2.0 ** -8 / 3 ** 0.5, rel
