@@ -12,17 +12,20 @@
 //     rows for each kv head, and this side wastes the least;
 //   * codes go from shared memory to operand registers without a detour: the
 //     cache is laid out (see kvcache.cu) so that a lane's vectors hold exactly
-//     the codes of its operand registers.  A code becomes a 16-bit number by
-//     placing it in the mantissa of 128 (bf16) or 1024 (fp16) and subtracting
-//     136 or 1032: exact, two at a time.
+//     the codes of its operand registers.  Two codes become two fp16 numbers by
+//     one mask into the mantissa of 1024 and one exact fused multiply-add
+//     (1024 + c - 1032, or (1024 + 16 c) / 16 - 72: the second form saves the
+//     shift of every other code).
 //     K: pairs of one register are dims n, n + 4 of a word of one token.
 //     V: they are the same dim of two tokens (one byte permute joins the
 //     half-words of both);
+//   * both products are in fp16, which holds q and the probabilities better
+//     than bf16 where the range allows: a bf16 q row is held times a power of
+//     two that brings its largest element to 2^13 .. 2^14 (exact, but for
+//     elements 2^27 times smaller), and a warp keeps a power of two that brings
+//     the largest probability times V scale of its tokens to 2^13 .. 2^14;
 //   * scales stay out of the operands: K's multiply the FP32 products of each
-//     32-dim group, V's multiply the probabilities before these are rounded to
-//     the type of q.  bf16 takes any scale; for fp16 a warp keeps a power of two
-//     that brings the largest product of its tokens to 2^13 .. 2^14, so that
-//     small values or small probabilities do not fall below fp16's range.
+//     32-dim group, V's multiply the probabilities before these are rounded.
 //
 // S^T = K Q^T leaves probabilities with tokens along the operand's rows; the
 // second product O^T = V^T P^T wants them along its depth: movmatrix
@@ -47,7 +50,7 @@ namespace attn {
 constexpr int kTile = 32;   // tokens of a warp's tile
 constexpr int kWarps = 8;   // warps of a block
 constexpr int kUnit = kTile * kWarps;
-constexpr int kExpMin = -100, kExpMax = 100;  // exponents of V's scales told apart (FP16)
+constexpr int kExpMin = -100, kExpMax = 100;  // exponents of V's scales told apart
 
 template <int DQK, int DV, int NT>
 struct DecShape {
@@ -57,7 +60,9 @@ struct DecShape {
   static constexpr int kKc = kTile * DQK / 2, kVc = kTile * DV / 2;
   static constexpr int kKs = kTile * GK * 2, kVs = kTile * GV * 2;
   static constexpr int kStage = kKc + kVc + kKs + kVs;  // a multiple of 128
-  static constexpr int kStages = DQK > 192 ? 2 : 3;
+  // blocks of an SM: as many as its registers hold
+  static constexpr int kBlocks = (NT == 1 && DV <= 128) || DV == 64 ? 2 : 1;
+  static constexpr int kStages = kBlocks == 2 || DQK > 192 ? 2 : 3;
   static constexpr int kRing = kWarps * kStages * kStage;
   // the join of the warps: O [row][dim] of 8 warps, and their maxima and sums
   static constexpr int kJoin = kWarps * kRows * (DV + 2) * 4;
@@ -96,42 +101,36 @@ __device__ __forceinline__ int tile_token(const SeqRange& s, int v) {
 }
 
 // ----------------------------------------------------------------- operands
-template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  if (BF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Codes n (low half) and n + 4 (high half) of a word, as numbers -8 .. 7.
-template <bool BF16>
-__device__ __forceinline__ uint32_t codes2(uint32_t w, int n) {
-  uint32_t r;
-  if (BF16) {
-    asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xEA;" : "=r"(r) : "r"(w >> (4 * n)));
-    const __nv_bfloat162 o = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&r),
-                                     __nv_bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308)));
-    return *reinterpret_cast<const uint32_t*>(&o);
+// The 8 codes of a word as fp16 numbers -8 .. 7: pair n is codes n (low half)
+// and n + 4 (high half).
+__device__ __forceinline__ void codes8(uint32_t w, uint32_t (&p)[4]) {
+  const __half2 low = __half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));       // 1032
+  const __half2 sixteenth = __half2(__ushort_as_half(0x2c00), __ushort_as_half(0x2c00));
+  const __half2 high = __half2(__ushort_as_half(0xd480), __ushort_as_half(0xd480));      // -72
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t v = i ? w >> 8 : w;
+    uint32_t x, y;
+    asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xEA;" : "=r"(x) : "r"(v));  // 1024 + code
+    asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xEA;" : "=r"(y) : "r"(v));  // 1024 + 16 code
+    const __half2 f = __hsub2(*reinterpret_cast<__half2*>(&x), low);
+    const __half2 g = __hfma2(*reinterpret_cast<__half2*>(&y), sixteenth, high);
+    p[2 * i] = *reinterpret_cast<const uint32_t*>(&f);
+    p[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&g);
   }
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xEA;" : "=r"(r) : "r"(w >> (4 * n)));
-  const __half2 o = __hsub2(*reinterpret_cast<__half2*>(&r),
-                            __half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408)));
-  return *reinterpret_cast<const uint32_t*>(&o);
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
@@ -170,7 +169,7 @@ __device__ __forceinline__ int row_token(int r) {
 
 // ----------------------------------------------------------------- the kernel
 template <bool BF16, int DQK, int DV, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 1) attn_kv_decode_kernel(
+__global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks) attn_kv_decode_kernel(
     const __grid_constant__ DecodeParams p) {
   using S = DecShape<DQK, DV, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -262,6 +261,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kv_decode_kernel(
 
     // ---- query operand: qf[nt][g][i] holds dims (8c + i, 8c + i + 4) of group g
     uint32_t qf[NT][S::GK][4];
+    float xs[NT][2];  // from products to scores in base 2, of columns 2c, 2c + 1
     int jhi[NT][2], jlo[NT][2];  // visible keys of the lane's columns 2c, 2c + 1
     const int row0 = rb * S::kRows;
 #pragma unroll
@@ -269,15 +269,46 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kv_decode_kernel(
       const int row = row0 + t * 8 + r;
       const int qi = row / p.group, qh = kvh * p.group + row % p.group;
       const uint16_t* src = (const uint16_t*)p.q + b * p.q_b + qi * p.q_t + qh * p.q_h + 8 * c;
+      uint4 qv[S::GK];
+      uint32_t top = 0;
 #pragma unroll
       for (int g = 0; g < S::GK; ++g) {
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (row < p.rows) v = *reinterpret_cast<const uint4*>(src + 32 * g);
-        qf[t][g][0] = __byte_perm(v.x, v.z, 0x5410);
-        qf[t][g][1] = __byte_perm(v.x, v.z, 0x7632);
-        qf[t][g][2] = __byte_perm(v.y, v.w, 0x5410);
-        qf[t][g][3] = __byte_perm(v.y, v.w, 0x7632);
+        if (BF16) {
+          qv[g] = v;
+          // magnitudes as bits are ordered
+          uint32_t mx = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                 __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+          top = max(top, max(mx & 0xffffu, mx >> 16));
+        } else {
+          qf[t][g][0] = __byte_perm(v.x, v.z, 0x5410);
+          qf[t][g][1] = __byte_perm(v.x, v.z, 0x7632);
+          qf[t][g][2] = __byte_perm(v.y, v.w, 0x5410);
+          qf[t][g][3] = __byte_perm(v.y, v.w, 0x7632);
+        }
       }
+      float unit = 1.0f;  // q is held times 1 / unit
+      if (BF16) {
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int ex = min(max((int)(top >> 7) - 127 - 13, -100), 100);  // largest at 2^13 .. 2^14
+        unit = __uint_as_float((uint32_t)(127 + ex) << 23);
+        const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+        for (int g = 0; g < S::GK; ++g) {
+          const uint32_t w[4] = {qv[g].x, qv[g].y, qv[g].z, qv[g].w};
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            f[i] = inv * __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qf[t][g][i] = Pack<false>::two(f[i], f[i + 4]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        xs[t][e] = p.scale_log2 * __shfl_sync(0xffffffffu, unit, (2 * c + e) * 4);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int cr = row0 + t * 8 + 2 * c + e;
@@ -293,7 +324,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kv_decode_kernel(
 
     float o[NT][S::GV][2][4];  // O^T: dims 32 g + 4 r + {0,1}, {2,3}; columns 2c, 2c + 1
     float m[NT][2], l[NT][2];
-    int vexp = kExpMin;  // FP16: O is held times 2^(14 - vexp)
+    int vexp = kExpMin;  // O is held times 2^(14 - vexp)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -386,14 +417,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kv_decode_kernel(
             for (int t = 0; t < NT; ++t)
 #pragma unroll
               for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
+            uint32_t a[4], bk[4];
+            codes8(ka[g], a);
+            codes8(kb[g], bk);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t a0 = codes2<BF16>(ka[g], 2 * h), a1 = codes2<BF16>(kb[g], 2 * h);
-              const uint32_t a2 = codes2<BF16>(ka[g], 2 * h + 1), a3 = codes2<BF16>(kb[g], 2 * h + 1);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
               for (int t = 0; t < NT; ++t)
-                mma16816<BF16>(acc[t], a0, a1, a2, a3, qf[t][g][2 * h], qf[t][g][2 * h + 1]);
-            }
+                mma16816(acc[t], a[2 * h], bk[2 * h], a[2 * h + 1], bk[2 * h + 1],
+                         qf[t][g][2 * h], qf[t][g][2 * h + 1]);
             const float fa = scale_of(sa, g), fb = scale_of(sb, g);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -417,7 +449,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kv_decode_kernel(
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 float& y = x[mt][t][2 * h + e];
-                y *= p.scale_log2;
+                y *= xs[t][e];
                 if (!whole) {
                   const int j = t0 + mt * 16 + h * 8 + row_token(r);
                   if (j > jhi[t][e] || (j < jlo[t][e] && j >= p.sinks)) y = -INFINITY;
@@ -443,7 +475,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kv_decode_kernel(
               }
             l[t][e] = fmaf(l[t][e], alpha[t][e], sum);
           }
-        // ---- V's scales; FP16: the power of two that fits their largest
+        // ---- V's scales, and the power of two that fits their largest
         uint32_t vs[2][2][S::GV / 2];  // of tokens r and r + 8 of both blocks
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -451,8 +483,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kv_decode_kernel(
           for (int h = 0; h < 2; ++h)
             lds_words<S::GV / 2>(st + S::kKc + S::kVc + S::kKs +
                                      (mt * 16 + h * 8 + row_token(r)) * 2 * S::GV, vs[mt][h]);
-        float kf = 1.0f;
-        if (!BF16) {
+        float kf;
+        {
           float mx = 0.0f;
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
@@ -505,8 +537,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kv_decode_kernel(
             const uint32_t z1 = __byte_perm(v2[g >> 1], v3[g >> 1], sel);
             const float fa = scale_of(vs[mt][0], g) * kf, fb = scale_of(vs[mt][1], g) * kf;
             uint32_t a[4], bq[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = codes2<BF16>(z0, i), bq[i] = codes2<BF16>(z1, i);
+            codes8(z0, a);
+            codes8(z1, bq);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               // a masked token's scale is not looked at: it may be anything
@@ -518,10 +550,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kv_decode_kernel(
                 p2 = x[mt][t][2] == 0.0f ? 0.0f : p2;
                 p3 = x[mt][t][3] == 0.0f ? 0.0f : p3;
               }
-              const uint32_t b0 = transpose8x8(Pack<BF16>::two(p0, p1));
-              const uint32_t b1 = transpose8x8(Pack<BF16>::two(p2, p3));
-              mma16816<BF16>(o[t][g][0], a[0], a[1], bq[0], bq[1], b0, b1);
-              mma16816<BF16>(o[t][g][1], a[2], a[3], bq[2], bq[3], b0, b1);
+              const uint32_t b0 = transpose8x8(Pack<false>::two(p0, p1));
+              const uint32_t b1 = transpose8x8(Pack<false>::two(p2, p3));
+              mma16816(o[t][g][0], a[0], a[1], bq[0], bq[1], b0, b1);
+              mma16816(o[t][g][1], a[2], a[3], bq[2], bq[3], b0, b1);
             }
           }
         }
@@ -538,7 +570,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_kv_decode_kernel(
     float* jo = reinterpret_cast<float*>(smem);                      // [warp][row][DV]
     float* jm = jo + kWarps * S::kRows * DV;                         // [warp][row]
     float* jl = jm + kWarps * S::kRows;                              // [warp][row]
-    const float back = BF16 ? 1.0f : __uint_as_float((uint32_t)(127 - 14 + vexp) << 23);
+    const float back = __uint_as_float((uint32_t)(127 - 14 + vexp) << 23);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -703,7 +735,8 @@ int decode_blocks(const DecodeParams& p, int num_sms) {
   // no more than the longest possible lists of units
   const int64_t cap = ((int64_t)p.cols << p.c.page_shift) / kUnit + 2;
   const int64_t units = cap * p.batch * p.c.heads * p.row_blocks;
-  return (int)std::min<int64_t>(num_sms, std::max<int64_t>(units, 1));
+  const int per_sm = (decode_col_tiles(p.rows, p.c.d_v) == 1 && p.c.d_v <= 128) || p.c.d_v == 64 ? 2 : 1;
+  return (int)std::min<int64_t>((int64_t)num_sms * per_sm, std::max<int64_t>(units, 1));
 }
 
 size_t decode_partial_floats(int rows_per_block, int d_v) {
