@@ -48,9 +48,13 @@
 namespace attn {
 
 constexpr int kTile = 32;   // tokens of a warp's tile
-constexpr int kWarps = 8;   // warps of a block
+constexpr int kWarps = 8;   // of a block
 constexpr int kUnit = kTile * kWarps;
+constexpr int kSlots = 4;   // of the join
 constexpr int kExpMin = -100, kExpMax = 100;  // exponents of V's scales told apart
+
+// whether 128 registers hold a lane's share
+__host__ __device__ constexpr bool light(int dv, int nt) { return dv * nt <= 128; }
 
 template <int DQK, int DV, int NT>
 struct DecShape {
@@ -61,12 +65,13 @@ struct DecShape {
   static constexpr int kKs = kTile * GK * 2, kVs = kTile * GV * 2;
   static constexpr int kStage = kKc + kVc + kKs + kVs;  // a multiple of 128
   // blocks of an SM: as many as its registers hold
-  static constexpr int kBlocks = (NT == 1 && DV <= 128) || DV == 64 ? 2 : 1;
-  static constexpr int kStages = kBlocks == 2 || DQK > 192 ? 2 : 3;
+  static constexpr int kBlocks = light(DV, NT) ? 2 : 1;
+  static constexpr int kStages = DQK == 64 || (kBlocks == 1 && DQK < 256) ? 3 : 2;
   static constexpr int kRing = kWarps * kStages * kStage;
-  // the join of the warps: O [row][dim] of 8 warps, and their maxima and sums
-  static constexpr int kJoin = kWarps * kRows * (DV + 2) * 4;
-  static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin) + 1024;
+  // the join of the warps: O [slot][row][dim], and (twice) maxima and sums [warp][row]
+  static constexpr int kJoin = kSlots * kRows * DV * 4;
+  static constexpr int kStats = 2 * 2 * kWarps * kRows * 4;
+  static constexpr int kSmem = kRing + kJoin + kStats;
 };
 
 // ----------------------------------------------------------------- geometry
@@ -88,16 +93,19 @@ __device__ __forceinline__ SeqRange seq_range(const DecodeParams& p, int b) {
   // the first query's window starts at len - seqlen_q - window_left
   const int64_t w = p.window_left < 0 ? 0 : (int64_t)s.len - p.seqlen_q - p.window_left;
   s.lo = w > 0 ? (int)(w / kTile) : 0;
-  if (s.len == 0) s.lo = 0;
   const int sink_tiles = (int)(((int64_t)p.sinks + kTile - 1) / kTile);
   s.n_sink = min(sink_tiles, s.lo);
   s.tiles = s.n_sink + (s.len + kTile - 1) / kTile - s.lo;
   return s;
 }
-__device__ __forceinline__ int units_of(const SeqRange& s) { return (s.tiles + kWarps - 1) / kWarps; }
 // first token of the v-th tile
 __device__ __forceinline__ int tile_token(const SeqRange& s, int v) {
   return (v < s.n_sink ? v : s.lo + v - s.n_sink) * kTile;
+}
+// blocks that share a call's tiles: no more than give each of their warps one
+__host__ __device__ inline long long used_blocks(long long tiles, int grid) {
+  const long long n = (tiles + kWarps - 1) / kWarps;
+  return n < grid ? n : grid;
 }
 
 // ----------------------------------------------------------------- operands
@@ -108,23 +116,35 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the same with a zero accumulator
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1,
+                                               uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 
-// The 8 codes of a word as fp16 numbers -8 .. 7: pair n is codes n (low half)
-// and n + 4 (high half).
+// The 8 codes of a word as pairs of fp16 numbers: pair n holds codes n and n + 4,
+// times 2^-24 for even n, 2^-20 for odd n (fp16 numbers below the normal range,
+// which the products take exactly).
 __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&p)[4]) {
-  const __half2 low = __half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));       // 1032
-  const __half2 sixteenth = __half2(__ushort_as_half(0x2c00), __ushort_as_half(0x2c00));
-  const __half2 high = __half2(__ushort_as_half(0xd480), __ushort_as_half(0xd480));      // -72
+  p[0] = w & 0x000f000fu;
+  p[1] = w & 0x00f000f0u;
+  w >>= 8;
+  p[2] = w & 0x000f000fu;
+  p[3] = w & 0x00f000f0u;
+}
+// -8 in both units
+constexpr uint32_t kLow8 = 0x80088008u, kHigh8 = 0x80808080u;
+// codes8 less 8 each: exact
+__device__ __forceinline__ void signed8(uint32_t w, uint32_t (&p)[4]) {
+  codes8(w, p);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t v = i ? w >> 8 : w;
-    uint32_t x, y;
-    asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xEA;" : "=r"(x) : "r"(v));  // 1024 + code
-    asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xEA;" : "=r"(y) : "r"(v));  // 1024 + 16 code
-    const __half2 f = __hsub2(*reinterpret_cast<__half2*>(&x), low);
-    const __half2 g = __hfma2(*reinterpret_cast<__half2*>(&y), sixteenth, high);
-    p[2 * i] = *reinterpret_cast<const uint32_t*>(&f);
-    p[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&g);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t o = i & 1 ? kHigh8 : kLow8;
+    const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&p[i]), *reinterpret_cast<const __half2*>(&o));
+    p[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
 }
 
@@ -167,19 +187,278 @@ __device__ __forceinline__ int row_token(int r) {
   return (r & 1) ? 4 + ((r >> 1) ^ 1) : r >> 1;
 }
 
-// ----------------------------------------------------------------- the kernel
-template <bool BF16, int DQK, int DV, int NT>
-__global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks) attn_kv_decode_kernel(
-    const __grid_constant__ DecodeParams p) {
+// A power of two from its exponent (-126 .. 127).
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// ----------------------------------------------------------------- a tile
+// What a lane holds of its warp's piece: the query operand, O^T, and for its
+// columns 2c, 2c + 1 (query rows) of each block of 8 the running statistics.
+template <int DQK, int DV, int NT>
+struct Piece {
   using S = DecShape<DQK, DV, NT>;
+  // dims (8c + i, 8c + i + 4) of group g; those of odd i (whose codes come in
+  // sixteenfold units) divided by 16
+  uint32_t qf[NT][S::GK][4];
+  float xs[NT][2];               // from products to scores in base 2
+  float o[NT][S::GV][2][4];      // dims 32 g + 4 r + {0,1}, {2,3} (odd ones 16 fold)
+  float m[NT][2], l[NT][2];      // reference exponent; this lane's share of the sum
+  int vexp;                      // O is held times 2^(14 - 24 - vexp)
+};
+
+// WHOLE: every query of the block sees every token of the tile.
+template <bool WHOLE, int DQK, int DV, int NT>
+__device__ __forceinline__ void do_tile(Piece<DQK, DV, NT>& z, const uint8_t* st,
+                                        const DecodeParams& p, int len, int row0, int t0, int r,
+                                        int c) {
+  using S = DecShape<DQK, DV, NT>;
+  float x[2][NT][4];  // S^T of two blocks of 16 tokens: rows r, r + 8
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+    const int ta = mt * 16 + row_token(r), tb = ta + 8;
+    uint32_t ka[S::GK], kb[S::GK], sa[S::GK / 2], sb[S::GK / 2];
+    lds_words<S::GK>(st + ta * (DQK / 2) + c * 4 * S::GK, ka);
+    lds_words<S::GK>(st + tb * (DQK / 2) + c * 4 * S::GK, kb);
+    lds_words<S::GK / 2>(st + S::kKc + S::kVc + ta * 2 * S::GK, sa);
+    lds_words<S::GK / 2>(st + S::kKc + S::kVc + tb * 2 * S::GK, sb);
+#pragma unroll
+    for (int g = 0; g < S::GK; ++g) {
+      float acc[NT][4];
+      uint32_t a[4], b[4];
+      codes8(ka[g], a);
+      codes8(kb[g], b);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint32_t* q = z.qf[t][g];
+        mma16816_first(acc[t], kLow8, kLow8, kHigh8, kHigh8, q[0], q[1]);
+        mma16816(acc[t], kLow8, kLow8, kHigh8, kHigh8, q[2], q[3]);
+        mma16816(acc[t], a[0], b[0], a[1], b[1], q[0], q[1]);
+        mma16816(acc[t], a[2], b[2], a[3], b[3], q[2], q[3]);
+      }
+      const float fa = scale_of(sa, g), fb = scale_of(sb, g);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        x[mt][t][0] = g ? fmaf(acc[t][0], fa, x[mt][t][0]) : acc[t][0] * fa;
+        x[mt][t][1] = g ? fmaf(acc[t][1], fa, x[mt][t][1]) : acc[t][1] * fa;
+        x[mt][t][2] = g ? fmaf(acc[t][2], fb, x[mt][t][2]) : acc[t][2] * fb;
+        x[mt][t][3] = g ? fmaf(acc[t][3], fb, x[mt][t][3]) : acc[t][3] * fb;
+      }
+    }
+  }
+  // ---- V's scales of tokens r and r + 8 of both blocks
+  uint32_t vs[2][2][S::GV / 2];
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      lds_words<S::GV / 2>(st + S::kKc + S::kVc + S::kKs +
+                               (mt * 16 + h * 8 + row_token(r)) * 2 * S::GV, vs[mt][h]);
+  // ---- running softmax in base 2.  The reference m of a column moves only
+  // when a score passes it by more than 1: probabilities stay below 2, and most
+  // tiles need no exchange between lanes.
+  bool move = false;
+  float mx[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      mx[t][e] = -INFINITY;
+      int hi = 0, lo = 0;
+      if (!WHOLE) {  // the tokens that this column's query sees
+        const int row = row0 + t * 8 + 2 * c + e;
+        const int pos = len - p.seqlen_q + row / p.group;
+        hi = row < p.rows ? pos : -1;
+        lo = p.window_left < 0 ? 0 : max(0, pos - p.window_left);
+      }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float& y = x[mt][t][2 * h + e];
+          y *= z.xs[t][e];
+          if (!WHOLE) {
+            const int j = t0 + mt * 16 + h * 8 + row_token(r);
+            if (j > hi || (j < lo && j >= p.sinks)) y = -INFINITY;
+          }
+          mx[t][e] = fmaxf(mx[t][e], y);
+        }
+      move |= mx[t][e] > z.m[t][e] + 1.0f;
+    }
+  // the largest scale (NaN apart) of the tokens that a query sees
+  float top = 0.0f;
+  if (WHOLE) {
+    __nv_bfloat162 w = *reinterpret_cast<__nv_bfloat162*>(&vs[0][0][0]);
+#pragma unroll
+    for (int i = 1; i < 4 * (S::GV / 2); ++i)
+      w = __hmax2(w, *reinterpret_cast<__nv_bfloat162*>(&vs[i / (2 * (S::GV / 2))][i / (S::GV / 2) % 2][i % (S::GV / 2)]));
+    const uint32_t u = *reinterpret_cast<uint32_t*>(&w);
+    top = fmaxf(scale_of(&u, 0), scale_of(&u, 1));
+  } else {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        bool seen = false;  // else the scales may be anything
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          seen |= x[mt][t][2 * h] != -INFINITY || x[mt][t][2 * h + 1] != -INFINITY;
+#pragma unroll
+        for (int g = 0; g < S::GV; ++g)
+          if (seen) top = fmaxf(top, scale_of(vs[mt][h], g));
+      }
+  }
+  move |= (int)(__float_as_uint(top) >> 23) - 126 > z.vexp;
+  if (__any_sync(0xffffffffu, move)) {
+    float f = 1.0f;
+    {
+      const uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+      const int e = min(max((int)(u >> 23) - 126, kExpMin), kExpMax);
+      if (e > z.vexp) {
+        f = pow2(max(z.vexp - e, -126));
+        z.vexp = e;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float y = mx[t][e];
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+        y = fmaxf(y, z.m[t][e]);
+        const float a = z.m[t][e] == -INFINITY ? 0.0f : ex2(z.m[t][e] - y);
+        z.m[t][e] = y;
+        z.l[t][e] *= a;
+#pragma unroll
+        for (int g = 0; g < S::GV; ++g)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            z.o[t][g][h][e] *= a * f;
+            z.o[t][g][h][2 + e] *= a * f;
+          }
+      }
+  }
+  const float kf = pow2(14 - z.vexp);  // products below 2^15
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float ms = z.m[t][e] == -INFINITY ? 0.0f : z.m[t][e];  // nothing seen yet
+      float sum = 0.0f;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float& y = x[mt][t][2 * h + e];
+          y = ex2(y - ms);
+          sum += y;
+          y *= kf;
+        }
+      z.l[t][e] += sum;
+    }
+  // ---- O^T += V^T P^T
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+    uint32_t v0[S::GV / 2], v1[S::GV / 2], v2[S::GV / 2], v3[S::GV / 2];
+    const uint8_t* vb = st + S::kKc + r * 2 * S::GV;
+    const int te = mt * 16 + row_token(2 * c), to = mt * 16 + row_token(2 * c + 1);
+    lds_words<S::GV / 2>(vb + te * (DV / 2), v0);
+    lds_words<S::GV / 2>(vb + to * (DV / 2), v1);
+    lds_words<S::GV / 2>(vb + (te + 8) * (DV / 2), v2);
+    lds_words<S::GV / 2>(vb + (to + 8) * (DV / 2), v3);
+#pragma unroll
+    for (int g = 0; g < S::GV; ++g) {
+      const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;
+      uint32_t a[4], b[4];
+      signed8(__byte_perm(v0[g >> 1], v1[g >> 1], sel), a);
+      signed8(__byte_perm(v2[g >> 1], v3[g >> 1], sel), b);
+      const float fa = scale_of(vs[mt][0], g), fb = scale_of(vs[mt][1], g);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float p0 = x[mt][t][0] * fa, p1 = x[mt][t][1] * fa;
+        float p2 = x[mt][t][2] * fb, p3 = x[mt][t][3] * fb;
+        if (!WHOLE) {  // a masked token's scale is not looked at: it may be anything
+          p0 = x[mt][t][0] == 0.0f ? 0.0f : p0;
+          p1 = x[mt][t][1] == 0.0f ? 0.0f : p1;
+          p2 = x[mt][t][2] == 0.0f ? 0.0f : p2;
+          p3 = x[mt][t][3] == 0.0f ? 0.0f : p3;
+        }
+        const uint32_t b0 = transpose8x8(Pack<false>::two(p0, p1));
+        const uint32_t b1 = transpose8x8(Pack<false>::two(p2, p3));
+        mma16816(z.o[t][g][0], a[0], a[1], b[0], b[1], b0, b1);
+        mma16816(z.o[t][g][1], a[2], a[3], b[2], b[3], b0, b1);
+      }
+    }
+  }
+}
+
+// Four dims of a finished row: O = acc / sum, LSE = (mx + log2 sum) ln 2.
+template <bool BF16>
+__device__ __forceinline__ void write_row(const DecodeParams& p, int b, int kvh, int row, int d4,
+                                          float4 acc, float mx, float sum) {
+  const int qi = row / p.group, qh = kvh * p.group + row % p.group;
+  // no visible token: sum is 0 (it is NaN where all scores are)
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (sum == 0.0f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+  if (sum != sum) acc.x = acc.y = acc.z = acc.w = sum;
+  const int64_t off = b * p.o_b + qi * p.o_t + qh * p.o_h + d4 * 4;
+  if (p.o_f32)
+    *reinterpret_cast<float4*>((float*)p.o + off) = acc;
+  else
+    *reinterpret_cast<uint2*>((uint16_t*)p.o + off) =
+        make_uint2(Pack<BF16>::two(acc.x, acc.y), Pack<BF16>::two(acc.z, acc.w));
+  if (d4 == 0)
+    p.lse[((int64_t)b * p.heads_q + qh) * p.seqlen_q + qi] =
+        sum == 0.0f ? -INFINITY : ((mx == -INFINITY ? 0.0f : mx) + log2f(sum)) * 0.6931471805599453f;
+}
+
+// ----------------------------------------------------------------- the kernel
+// A place in the list of tiles: tile v of an item of a sequence.
+struct Cursor {
+  int b, item, v;
+  SeqRange sr;
+};
+// A warp's next tiles, kUnit tokens apart.
+struct __align__(16) Strip {
+  const int32_t* row;  // of the block table
+  int token, left;
+  int head_row, len;   // first row of the kv head in a page; tokens of the sequence
+};
+// One array of the cache, and where a stage holds its part.
+struct __align__(16) Array {
+  const uint8_t* base;
+  uint32_t page, width;  // bytes of a page, of a row
+  int off;
+};
+// Moves `n` tiles on.  Past the end of the list (lengths that changed under the
+// call): b = batch.
+__device__ __forceinline__ void advance(const DecodeParams& p, int per_seq, Cursor& k, int n) {
+  k.v += n;
+  while (k.b < p.batch && k.v >= k.sr.tiles) {
+    k.v -= k.sr.tiles;
+    if (k.sr.tiles == 0 || ++k.item == per_seq) {
+      k.item = 0;
+      if (++k.b < p.batch) k.sr = seq_range(p, k.b);
+    }
+  }
+}
+
+template <bool BF16, int DQK, int DV, int NT>
+__global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
+    attn_kv_decode_kernel(const __grid_constant__ DecodeParams p) {
+  using S = DecShape<DQK, DV, NT>;
+  constexpr int kThreads = kWarps * 32;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kWarps][S::kStages];
+  __shared__ Cursor cursor[kWarps + 1];  // of each warp's copies; of the next piece
+  __shared__ Strip strip[kWarps];
+  __shared__ Array array[4];
   __shared__ int abort_flag;
   __shared__ long long s_sum[kWarps];
-  __shared__ long long s_before;  // units before s_b
+  __shared__ long long s_before;  // tiles before sequence s_b
   __shared__ int s_b;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r = lane >> 2, c = lane & 3;
   const Abort ab{&abort_flag, p.status, kWaitLimitNs};
   if (tid == 0) {
     abort_flag = 0;
@@ -189,10 +468,10 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks) a
       for (int s = 0; s < S::kStages; ++s) mbar_init(&full[w][s], 1);
     fence_barrier_init();
   }
-  // ---- the list of units, and this block's run of it
+  // ---- the list of tiles, and this block's run of it
   const int per_seq = p.c.heads * p.row_blocks;  // items of a sequence
   long long mine = 0;
-  for (int b = tid; b < p.batch; b += kWarps * 32) mine += units_of(seq_range(p, b));
+  for (int b = tid; b < p.batch; b += kThreads) mine += seq_range(p, b).tiles;
 #pragma unroll
   for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) s_sum[warp] = mine;
@@ -201,15 +480,15 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks) a
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) all += s_sum[w];
   all *= per_seq;
-  const long long nblk = all < (long long)gridDim.x ? all : (long long)gridDim.x;
+  const long long nblk = used_blocks(all, gridDim.x);
   if (blockIdx.x == 0 && tid == 0) *p.total = all;
   if ((long long)blockIdx.x >= nblk) return;
   const long long first = all * blockIdx.x / nblk, last = all * (blockIdx.x + 1) / nblk;
-  // the sequence that holds unit `first`
+  // the sequence that holds tile `first`
   long long before = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += kWarps * 32) {
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
     const int b = b0 + tid;
-    const long long n = b < p.batch ? (long long)units_of(seq_range(p, b)) * per_seq : 0;
+    const long long n = b < p.batch ? (long long)seq_range(p, b).tiles * per_seq : 0;
     long long inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -231,38 +510,123 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks) a
     __syncthreads();
     if (s_b < p.batch) break;
   }
-  int b = s_b;
-  if (b >= p.batch) return;  // lengths that changed under the call
-  long long at = first;              // next unit
-  long long seq_first = s_before;    // first unit of sequence b
+  const int first_b = s_b;
+  if (first_b >= p.batch) return;  // lengths that changed under the call
+  const int n_run = (int)(last - first);  // tiles of the run; tile i is warp i % kWarps's
 
+  const int r = lane >> 2, c = lane & 3;
   uint8_t* ring = smem + warp * (S::kStages * S::kStage);
-  uint32_t phase = 0;  // of this warp's stages: fills so far
+  float* jo = reinterpret_cast<float*>(smem + S::kRing);             // [slot][row][DV]
+  float* stats = reinterpret_cast<float*>(smem + S::kRing + S::kJoin);
+  int used = 0, filled = 0, pieces = 0;
   bool ok = true;
-  while (at < last) {
-    SeqRange sr = seq_range(p, b);
-    int nu = units_of(sr);
-    while (at >= seq_first + (long long)nu * per_seq) {  // sequences without units
-      seq_first += (long long)nu * per_seq;
-      if (++b >= p.batch) return;
-      sr = seq_range(p, b);
-      nu = units_of(sr);
-    }
-    const int item = (int)((at - seq_first) / nu);
-    const int kvh = item / p.row_blocks, rb = item - kvh * p.row_blocks;
-    const long long item_first = seq_first + (long long)item * nu;
-    const int u0 = (int)(at - item_first);
-    const int u1 = (int)(last - item_first < nu ? last - item_first : nu);
-    at = item_first + u1;
-    if (u0 == 0 && tid == 0) {  // where the item lies, for the join
-      long long* info = reinterpret_cast<long long*>(p.info);
-      info[(int64_t)b * per_seq + item] = item_first;
-    }
 
-    // ---- query operand: qf[nt][g][i] holds dims (8c + i, 8c + i + 4) of group g
-    uint32_t qf[NT][S::GK][4];
-    float xs[NT][2];  // from products to scores in base 2, of columns 2c, 2c + 1
-    int jhi[NT][2], jlo[NT][2];  // visible keys of the lane's columns 2c, 2c + 1
+  // ---- copies.  A warp feeds its own ring, across the pieces of the run: lane
+  // 4 h + i copies array i of the tile's page h (pages of 16 tokens: a tile
+  // spans two), so that a tile costs the warp few instructions.  Where the next
+  // tile lies is looked up one tile ahead.
+  const int left_total = n_run > warp ? (n_run - warp + kWarps - 1) / kWarps : 0;  // this warp's tiles
+  const int tok = min(p.c.page_size, kTile);  // tokens of a copy
+  const int lanes = tok < kTile ? 8 : 4;
+  if (tid < 4) {
+    const int width = tid == 0 ? DQK / 2 : tid == 1 ? DV / 2 : tid == 2 ? 2 * S::GK : 2 * S::GV;
+    const int off = tid == 0 ? 0 : tid == 1 ? S::kKc : tid == 2 ? S::kKc + S::kVc : S::kKc + S::kVc + S::kKs;
+    array[tid] = Array{p.src[tid], (uint32_t)(p.c.heads * p.c.page_size * width), (uint32_t)width, off};
+  }
+  if (lane == 0) {
+    Cursor k;
+    k.b = first_b;
+    k.sr = seq_range(p, first_b);
+    const long long v = first - s_before;
+    k.item = k.sr.tiles ? (int)(v / k.sr.tiles) : 0;
+    k.v = k.sr.tiles ? (int)(v % k.sr.tiles) : 0;
+    if (k.item >= per_seq) k.b = p.batch;  // lengths that changed under the call
+    if (warp == 0) {
+      advance(p, per_seq, k, 0);
+      cursor[kWarps] = k;
+    }
+    advance(p, per_seq, k, warp);
+    cursor[warp] = k;
+    strip[warp].left = 0;
+  }
+  __syncthreads();
+  int next_page = 0, next_row = -1;  // page, and row within the page's [head][token] (-1: none)
+  const uint32_t lane_mask = (1u << lanes) - 1u;
+  auto look_up = [&]() {  // lanes 0 .. lanes - 1
+    Strip t = strip[warp];
+    if (t.left == 0) {  // a new strip: tiles in a row, kWarps apart
+      if (lane == 0) {
+        Cursor k = cursor[warp];
+        t.left = 1;
+        t.token = -1;  // no tile (lengths that changed under the call)
+        if (k.b < p.batch) {
+          const int end = k.v < k.sr.n_sink ? k.sr.n_sink : k.sr.tiles;
+          t.row = p.table + (int64_t)k.b * p.table_stride;
+          t.token = tile_token(k.sr, k.v);
+          t.left = (end - k.v + kWarps - 1) / kWarps;
+          t.head_row = (k.item / p.row_blocks) * p.c.page_size;
+          t.len = k.sr.len;
+          advance(p, per_seq, k, t.left * kWarps);
+          cursor[warp] = k;
+        }
+        strip[warp] = t;
+      }
+      __syncwarp(lane_mask);
+      t = strip[warp];
+    }
+    const int t0 = t.token + (lane >> 2) * tok;
+    next_row = -1;
+    if (t.token >= 0 && t0 < t.len) {
+      next_page = t.row[t0 >> p.c.page_shift];
+      next_row = t.head_row + (t0 & (p.c.page_size - 1));
+    }
+    __syncwarp(lane_mask);
+    if (lane == 0) {
+      strip[warp].token = t.token + kUnit;
+      strip[warp].left = t.left - 1;
+    }
+  };
+  auto copy = [&]() {  // lanes 0 .. lanes - 1
+    const int s = filled % S::kStages;
+    uint64_t* bar = &full[warp][s];
+    const bool good = next_row >= 0 && (unsigned)next_page < (unsigned)p.c.num_pages;
+    if (!good && next_row >= 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+    const uint32_t pages = __popc(__ballot_sync(lane_mask, good)) / 4;
+    if (lane == 0)
+      mbar_arrive_tx(bar, pages * (uint32_t)tok * (DQK / 2 + DV / 2 + 2 * S::GK + 2 * S::GV));
+    __syncwarp(lane_mask);
+    if (good) {
+      const Array y = array[lane & 3];
+      const uint8_t* src = y.base + (uint64_t)(uint32_t)next_page * y.page + (uint64_t)(uint32_t)next_row * y.width;
+      bulk_load(ring + s * S::kStage + y.off + (lane >> 2) * tok * y.width, src, tok * y.width, bar);
+    }
+  };
+  if (lane < lanes && left_total > 0) {
+    look_up();
+    for (; filled < left_total && filled < S::kStages; ++filled) {
+      copy();
+      __syncwarp(lane_mask);
+      if (filled + 1 < left_total) look_up();
+    }
+  }
+  filled = min(left_total, S::kStages);
+  for (int done_tiles = 0; done_tiles < n_run;) {
+    // the piece: every warp goes by the same copy of the lengths, so that all
+    // of them meet the same barriers
+    const Cursor k = cursor[kWarps];
+    if (k.b >= p.batch) break;
+    const SeqRange sr = k.sr;
+    const int b = k.b, item = k.item, v0 = k.v, v1 = min(sr.tiles, v0 + n_run - done_tiles);
+    const int kvh = item / p.row_blocks, rb = item - kvh * p.row_blocks;
+    // this warp's first tile: the run's tile i is warp i % kWarps's
+    const int skew = (warp - done_tiles % kWarps + kWarps) % kWarps;
+    if (v0 == 0 && tid == 0) {  // where the item lies, for the join
+      long long* info = reinterpret_cast<long long*>(p.info);
+      info[(int64_t)b * per_seq + item] = first + done_tiles;
+    }
+    done_tiles += v1 - v0;
+
+    Piece<DQK, DV, NT> z;
     const int row0 = rb * S::kRows;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -270,363 +634,163 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks) a
       const int qi = row / p.group, qh = kvh * p.group + row % p.group;
       const uint16_t* src = (const uint16_t*)p.q + b * p.q_b + qi * p.q_t + qh * p.q_h + 8 * c;
       uint4 qv[S::GK];
-      uint32_t top = 0;
+      uint32_t top = 0;  // largest magnitude: as bits they are ordered
 #pragma unroll
       for (int g = 0; g < S::GK; ++g) {
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (row < p.rows) v = *reinterpret_cast<const uint4*>(src + 32 * g);
-        if (BF16) {
-          qv[g] = v;
-          // magnitudes as bits are ordered
-          uint32_t mx = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                 __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-          top = max(top, max(mx & 0xffffu, mx >> 16));
-        } else {
-          qf[t][g][0] = __byte_perm(v.x, v.z, 0x5410);
-          qf[t][g][1] = __byte_perm(v.x, v.z, 0x7632);
-          qf[t][g][2] = __byte_perm(v.y, v.w, 0x5410);
-          qf[t][g][3] = __byte_perm(v.y, v.w, 0x7632);
-        }
+        qv[g] = v;
+        const uint32_t mx = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        top = max(top, max(mx & 0xffffu, mx >> 16));
       }
-      float unit = 1.0f;  // q is held times 1 / unit
-      if (BF16) {
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int ex = min(max((int)(top >> 7) - 127 - 13, -100), 100);  // largest at 2^13 .. 2^14
-        unit = __uint_as_float((uint32_t)(127 + ex) << 23);
-        const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t tf = __float_as_uint(Pack<BF16>::to_f((uint16_t)top));
+      const int ex = min(max((int)(tf >> 23) - 127 - 13, -100), 100);  // largest at 2^13 .. 2^14
+      const float inv = pow2(-ex);
 #pragma unroll
-        for (int g = 0; g < S::GK; ++g) {
-          const uint32_t w[4] = {qv[g].x, qv[g].y, qv[g].z, qv[g].w};
-          float f[8];
+      for (int g = 0; g < S::GK; ++g) {
+        const uint32_t w[4] = {qv[g].x, qv[g].y, qv[g].z, qv[g].w};
+        float f[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            f[i] = inv * __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
+        for (int i = 0; i < 8; ++i)
+          f[i] = Pack<BF16>::to_f((uint16_t)(w[i >> 1] >> (16 * (i & 1)))) * ((i & 1) ? inv * 0.0625f : inv);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) qf[t][g][i] = Pack<false>::two(f[i], f[i + 4]);
-        }
+        for (int i = 0; i < 4; ++i) z.qf[t][g][i] = Pack<false>::two(f[i], f[i + 4]);
       }
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        xs[t][e] = p.scale_log2 * __shfl_sync(0xffffffffu, unit, (2 * c + e) * 4);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int cr = row0 + t * 8 + 2 * c + e;
-        const int pos = sr.len - p.seqlen_q + cr / p.group;
-        jhi[t][e] = cr < p.rows ? pos : -1;
-        jlo[t][e] = p.window_left < 0 ? 0 : max(0, pos - p.window_left);
+        z.xs[t][e] = p.scale_log2 * 16777216.0f * __shfl_sync(0xffffffffu, pow2(ex), (2 * c + e) * 4);
+        z.m[t][e] = -INFINITY;
+        z.l[t][e] = 0.0f;
       }
-    }
-    // every query of the item sees token j if j <= pos_lo and (j >= pos_hi -
-    // window_left or j < sinks)
-    const int pos_lo = sr.len - p.seqlen_q + row0 / p.group;
-    const int pos_hi = sr.len - p.seqlen_q + (min(row0 + S::kRows, p.rows) - 1) / p.group;
-
-    float o[NT][S::GV][2][4];  // O^T: dims 32 g + 4 r + {0,1}, {2,3}; columns 2c, 2c + 1
-    float m[NT][2], l[NT][2];
-    int vexp = kExpMin;  // O is held times 2^(14 - vexp)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) m[t][e] = -INFINITY, l[t][e] = 0.0f;
 #pragma unroll
       for (int g = 0; g < S::GV; ++g)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[t][g][h][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) z.o[t][g][h][e] = 0.0f;
     }
+    z.vexp = kExpMin;
+    // every query of the item sees token j if j <= pos_lo and (j >= pos_hi -
+    // window_left or j < sinks); columns past the last row hold zeros, and what
+    // they sum up is not written
+    const int pos_lo = sr.len - p.seqlen_q + row0 / p.group;
+    const int pos_hi = sr.len - p.seqlen_q + (min(row0 + S::kRows, p.rows) - 1) / p.group;
 
-    // ---- this warp's tiles of the piece: v = (u0 + k) * 8 + warp, k < u1 - u0
-    const int n = u1 - u0;
-    int pages[2] = {-1, -1};  // of tile 32 * (k / 32) + lane; a tile spans one or two pages
-    auto issue = [&](int k) {  // whole warp
-      if ((k & 31) == 0) {
-        const int v = (u0 + k + lane) * kWarps + warp;
-        pages[0] = pages[1] = -1;
-        if (k + lane < n && v < sr.tiles) {
-          const int t0 = tile_token(sr, v);
-          const int32_t* row = p.table + (int64_t)b * p.table_stride;
-          pages[0] = row[t0 >> p.c.page_shift];
-          if (p.c.page_size < kTile && t0 + p.c.page_size < sr.len)
-            pages[1] = row[(t0 >> p.c.page_shift) + 1];
-          if ((unsigned)pages[0] >= (unsigned)p.c.num_pages ||
-              (p.c.page_size < kTile && t0 + p.c.page_size < sr.len &&
-               (unsigned)pages[1] >= (unsigned)p.c.num_pages)) {
-            if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
-          }
-        }
-      }
-      const int v = (u0 + k) * kWarps + warp;
-      const int pg0 = __shfl_sync(0xffffffffu, pages[0], k & 31);
-      const int pg1 = __shfl_sync(0xffffffffu, pages[1], k & 31);
-      if (lane == 0) {
-        const int s = (int)(phase % S::kStages);
-        uint8_t* st = ring + s * S::kStage;
-        const int t0 = v < sr.tiles ? tile_token(sr, v) : 0;
-        const int tok = min(p.c.page_size, kTile);  // tokens of a copy
-        const bool a0 = (unsigned)pg0 < (unsigned)p.c.num_pages;
-        const bool a1 = tok < kTile && (unsigned)pg1 < (unsigned)p.c.num_pages;
-        const uint32_t bytes = (uint32_t)tok * (DQK / 2 + DV / 2 + 2 * S::GK + 2 * S::GV);
-        mbar_arrive_tx(&full[warp][s], bytes * ((a0 ? 1 : 0) + (a1 ? 1 : 0)));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!(h ? a1 : a0)) continue;
-          const int64_t row = ((int64_t)(h ? pg1 : pg0) * p.c.heads + kvh) * p.c.page_size +
-                              (h ? 0 : t0 & (p.c.page_size - 1));
-          bulk_load(st + h * tok * (DQK / 2), p.c.k_codes + row * (DQK / 2), tok * (DQK / 2), &full[warp][s]);
-          bulk_load(st + S::kKc + h * tok * (DV / 2), p.c.v_codes + row * (DV / 2), tok * (DV / 2), &full[warp][s]);
-          bulk_load(st + S::kKc + S::kVc + h * tok * 2 * S::GK, p.c.k_scales + row * S::GK, tok * 2 * S::GK, &full[warp][s]);
-          bulk_load(st + S::kKc + S::kVc + S::kKs + h * tok * 2 * S::GV, p.c.v_scales + row * S::GV, tok * 2 * S::GV, &full[warp][s]);
-        }
-      }
-      ++phase;
-    };
-    int issued = 0;
-    uint32_t used = phase;  // stage of the next tile to use
-    for (; issued < n && issued < S::kStages; ++issued) issue(issued);
-
-    for (int k = 0; k < n && ok; ++k, ++used) {
-      const int s = (int)(used % S::kStages);
-      ok = mbar_wait_warp(&full[warp][s], (used / S::kStages) & 1u, ab);
+    const int whole_hi = pos_lo - (kTile - 1);
+    const int whole_lo = p.window_left < 0 ? 0 : pos_hi - p.window_left;
+    for (int v = v0 + skew; v < v1; v += kWarps, ++used) {
+      const int s = used % S::kStages;
+      ok = ok && mbar_wait_warp(&full[warp][s], (uint32_t)(used / S::kStages) & 1u, ab);
       if (!ok) break;
       const uint8_t* st = ring + s * S::kStage;
-      const int v = (u0 + k) * kWarps + warp;
-      if (v < sr.tiles) {
-        const int t0 = tile_token(sr, v);
-        // (columns past the last row hold zeros: what they sum up is not written)
-        const bool whole = t0 + kTile - 1 <= pos_lo &&
-                           (p.window_left < 0 || t0 >= pos_hi - p.window_left || t0 + kTile <= p.sinks);
-        float x[2][NT][4];  // S^T of two blocks of 16 tokens: rows r, r + 8
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const int ta = mt * 16 + row_token(r), tb = ta + 8;
-          uint32_t ka[S::GK], kb[S::GK], sa[S::GK / 2], sb[S::GK / 2];
-          lds_words<S::GK>(st + ta * (DQK / 2) + c * 4 * S::GK, ka);
-          lds_words<S::GK>(st + tb * (DQK / 2) + c * 4 * S::GK, kb);
-          lds_words<S::GK / 2>(st + S::kKc + S::kVc + ta * 2 * S::GK, sa);
-          lds_words<S::GK / 2>(st + S::kKc + S::kVc + tb * 2 * S::GK, sb);
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[mt][t][e] = 0.0f;
-#pragma unroll
-          for (int g = 0; g < S::GK; ++g) {
-            float acc[NT][4];
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
-            uint32_t a[4], bk[4];
-            codes8(ka[g], a);
-            codes8(kb[g], bk);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int t = 0; t < NT; ++t)
-                mma16816(acc[t], a[2 * h], bk[2 * h], a[2 * h + 1], bk[2 * h + 1],
-                         qf[t][g][2 * h], qf[t][g][2 * h + 1]);
-            const float fa = scale_of(sa, g), fb = scale_of(sb, g);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              x[mt][t][0] = fmaf(acc[t][0], fa, x[mt][t][0]);
-              x[mt][t][1] = fmaf(acc[t][1], fa, x[mt][t][1]);
-              x[mt][t][2] = fmaf(acc[t][2], fb, x[mt][t][2]);
-              x[mt][t][3] = fmaf(acc[t][3], fb, x[mt][t][3]);
-            }
-          }
-        }
-        // ---- running softmax in base 2
-        float alpha[NT][2];
-        bool moved = false;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float& y = x[mt][t][2 * h + e];
-                y *= xs[t][e];
-                if (!whole) {
-                  const int j = t0 + mt * 16 + h * 8 + row_token(r);
-                  if (j > jhi[t][e] || (j < jlo[t][e] && j >= p.sinks)) y = -INFINITY;
-                }
-                mx = fmaxf(mx, y);
-              }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float mn = fmaxf(m[t][e], mx);
-            const float ms = mn == -INFINITY ? 0.0f : mn;  // nothing seen yet
-            alpha[t][e] = ex2(m[t][e] - ms);
-            moved |= mn != m[t][e];
-            m[t][e] = mn;
-            float sum = 0.0f;
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float& y = x[mt][t][2 * h + e];
-                y = ex2(y - ms);
-                sum += y;
-              }
-            l[t][e] = fmaf(l[t][e], alpha[t][e], sum);
-          }
-        // ---- V's scales, and the power of two that fits their largest
-        uint32_t vs[2][2][S::GV / 2];  // of tokens r and r + 8 of both blocks
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            lds_words<S::GV / 2>(st + S::kKc + S::kVc + S::kKs +
-                                     (mt * 16 + h * 8 + row_token(r)) * 2 * S::GV, vs[mt][h]);
-        float kf;
-        {
-          float mx = 0.0f;
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              bool seen = whole;  // a token no query sees: its scales may be anything
-#pragma unroll
-              for (int t = 0; t < NT; ++t) seen |= x[mt][t][2 * h] != 0.0f || x[mt][t][2 * h + 1] != 0.0f;
-              float sm = 0.0f;
-#pragma unroll
-              for (int g = 0; g < S::GV; ++g) sm = fmaxf(sm, scale_of(vs[mt][h], g));
-              if (seen) mx = fmaxf(mx, sm);
-            }
-          // positive numbers: their bits are ordered
-          const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
-          const int e = min(max((int)(top >> 23) - 126, kExpMin), kExpMax);
-          if (e > vexp) {
-            const float f = __uint_as_float((uint32_t)(127 + max(vexp - e, -126)) << 23);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) alpha[t][0] *= f, alpha[t][1] *= f;
-            moved = true;
-            vexp = e;
-          }
-          kf = __uint_as_float((uint32_t)(127 + 14 - vexp) << 23);
-        }
-        if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int g = 0; g < S::GV; ++g)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[t][g][h][e] *= alpha[t][e & 1];
-        }
-        // ---- O^T += V^T P^T
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          uint32_t v0[S::GV / 2], v1[S::GV / 2], v2[S::GV / 2], v3[S::GV / 2];
-          const uint8_t* vb = st + S::kKc + r * 2 * S::GV;
-          const int te = mt * 16 + row_token(2 * c), to = mt * 16 + row_token(2 * c + 1);
-          lds_words<S::GV / 2>(vb + te * (DV / 2), v0);
-          lds_words<S::GV / 2>(vb + to * (DV / 2), v1);
-          lds_words<S::GV / 2>(vb + (te + 8) * (DV / 2), v2);
-          lds_words<S::GV / 2>(vb + (to + 8) * (DV / 2), v3);
-#pragma unroll
-          for (int g = 0; g < S::GV; ++g) {
-            const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;
-            const uint32_t z0 = __byte_perm(v0[g >> 1], v1[g >> 1], sel);
-            const uint32_t z1 = __byte_perm(v2[g >> 1], v3[g >> 1], sel);
-            const float fa = scale_of(vs[mt][0], g) * kf, fb = scale_of(vs[mt][1], g) * kf;
-            uint32_t a[4], bq[4];
-            codes8(z0, a);
-            codes8(z1, bq);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              // a masked token's scale is not looked at: it may be anything
-              float p0 = x[mt][t][0] * fa, p1 = x[mt][t][1] * fa;
-              float p2 = x[mt][t][2] * fb, p3 = x[mt][t][3] * fb;
-              if (!whole) {
-                p0 = x[mt][t][0] == 0.0f ? 0.0f : p0;
-                p1 = x[mt][t][1] == 0.0f ? 0.0f : p1;
-                p2 = x[mt][t][2] == 0.0f ? 0.0f : p2;
-                p3 = x[mt][t][3] == 0.0f ? 0.0f : p3;
-              }
-              const uint32_t b0 = transpose8x8(Pack<false>::two(p0, p1));
-              const uint32_t b1 = transpose8x8(Pack<false>::two(p2, p3));
-              mma16816(o[t][g][0], a[0], a[1], bq[0], bq[1], b0, b1);
-              mma16816(o[t][g][1], a[2], a[3], bq[2], bq[3], b0, b1);
-            }
-          }
-        }
-      }
+      const int t0 = tile_token(sr, v);
+      const bool whole = t0 <= whole_hi && (t0 >= whole_lo || t0 + kTile <= p.sinks);
+      if (whole)
+        do_tile<true>(z, st, p, sr.len, row0, t0, r, c);
+      else
+        do_tile<false>(z, st, p, sr.len, row0, t0, r, c);
       __syncwarp();
-      if (issued < n) issue(issued), ++issued;
+      if (filled < left_total) {
+        if (lane < lanes) {
+          copy();
+          if (filled + 1 < left_total) look_up();
+        }
+        ++filled;
+      }
     }
-    if (!ok) {  // let the copies in flight land before the block ends
-      for (; used != phase; ++used)
-        mbar_wait_quiet(&full[warp][used % S::kStages], (used / S::kStages) & 1u, ab.limit_ns);
-    }
-    // ---- join the warps through the (drained) ring
-    if (__syncthreads_or(!ok)) return;
-    float* jo = reinterpret_cast<float*>(smem);                      // [warp][row][DV]
-    float* jm = jo + kWarps * S::kRows * DV;                         // [warp][row]
-    float* jl = jm + kWarps * S::kRows;                              // [warp][row]
-    const float back = __uint_as_float((uint32_t)(127 - 14 + vexp) << 23);
+
+    // ---- join the warps.  A failed wait skips the tiles, never a barrier.
+    float* jm = stats + (pieces & 1) * (2 * kWarps * S::kRows);  // [warp][row]
+    float* jl = jm + kWarps * S::kRows;
+    ++pieces;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float sum = l[t][e];
+        float sum = z.l[t][e];
         sum += __shfl_xor_sync(0xffffffffu, sum, 4);
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int row = t * 8 + 2 * c + e;
-        if (r == 0) jm[warp * S::kRows + row] = m[t][e], jl[warp * S::kRows + row] = sum;
-#pragma unroll
-        for (int g = 0; g < S::GV; ++g)
-          *reinterpret_cast<float4*>(jo + (warp * S::kRows + row) * DV + 32 * g + 4 * r) =
-              make_float4(o[t][g][0][e] * back, o[t][g][0][2 + e] * back, o[t][g][1][e] * back,
-                          o[t][g][1][2 + e] * back);
+        if (r == 0) jm[warp * S::kRows + row] = z.m[t][e], jl[warp * S::kRows + row] = sum;
       }
     __syncthreads();
-    const bool done = u0 == 0 && u1 == nu;  // the whole item: no partial result
-    float* part = p.partial + ((int64_t)blockIdx.x * 2 + (u0 == 0 ? 1 : 0)) * (S::kRows * (DV + 2));
+    if (tid == 0) {  // (read by all before this barrier, and again after the next)
+      Cursor n = k;
+      advance(p, per_seq, n, v1 - v0);
+      cursor[kWarps] = n;
+    }
+    const float back = pow2(24 - 14 + z.vexp);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // to the common maximum
+        const int row = t * 8 + 2 * c + e;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, jm[w * S::kRows + row]);
+        const float f = z.m[t][e] == -INFINITY ? 0.0f : ex2(z.m[t][e] - mx) * back;
+#pragma unroll
+        for (int g = 0; g < S::GV; ++g)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) z.o[t][g][h][e] *= f, z.o[t][g][h][2 + e] *= f * 0.0625f;
+      }
+#pragma unroll
+    for (int round = 0; round * kSlots < kWarps; ++round) {
+      if (warp / kSlots == round) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int g = 0; g < S::GV; ++g) {
+              float4* dst = reinterpret_cast<float4*>(
+                  jo + ((warp % kSlots) * S::kRows + t * 8 + 2 * c + e) * DV + 32 * g + 4 * r);
+              float4 y = make_float4(z.o[t][g][0][e], z.o[t][g][0][2 + e], z.o[t][g][1][e], z.o[t][g][1][2 + e]);
+              if (round > 0) {
+                const float4 u = *dst;
+                y.x += u.x, y.y += u.y, y.z += u.z, y.w += u.w;
+              }
+              *dst = y;
+            }
+      }
+      __syncthreads();
+    }
+    const bool done = v0 == 0 && v1 == sr.tiles;  // the whole item: no partial result
+    float* part = p.partial + ((int64_t)blockIdx.x * 2 + (v0 == 0 ? 1 : 0)) * (S::kRows * (DV + 2));
     for (int i = tid; i < S::kRows * (DV / 4); i += kWarps * 32) {
       const int row = i / (DV / 4), d4 = i % (DV / 4);
       float mx = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, jm[w * S::kRows + row]);
-      const float ms = mx == -INFINITY ? 0.0f : mx;
       float sum = 0.0f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(jm[w * S::kRows + row] - ms);
+        const float mw = jm[w * S::kRows + row];
+        // a NaN sum of a warp without a maximum (all its scores NaN) counts too
+        sum = fmaf(jl[w * S::kRows + row], mw == -INFINITY ? 1.0f : ex2(mw - mx), sum);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < (kSlots < kWarps ? kSlots : kWarps); ++w) {
         const float4 y = *reinterpret_cast<const float4*>(jo + (w * S::kRows + row) * DV + d4 * 4);
-        sum = fmaf(jl[w * S::kRows + row], f, sum);
-        acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y);
-        acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
+        acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
       }
       if (!done) {
         *reinterpret_cast<float4*>(part + row * DV + d4 * 4) = acc;
         if (d4 == 0) part[S::kRows * DV + row] = mx, part[S::kRows * (DV + 1) + row] = sum;
       } else if (row0 + row < p.rows) {
-        const int qi = (row0 + row) / p.group, qh = kvh * p.group + (row0 + row) % p.group;
-        const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
-        acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-        const int64_t off = b * p.o_b + qi * p.o_t + qh * p.o_h + d4 * 4;
-        if (p.o_f32)
-          *reinterpret_cast<float4*>((float*)p.o + off) = acc;
-        else
-          *reinterpret_cast<uint2*>((uint16_t*)p.o + off) =
-              make_uint2(Pack<BF16>::two(acc.x, acc.y), Pack<BF16>::two(acc.z, acc.w));
-        if (d4 == 0)
-          p.lse[((int64_t)b * p.heads_q + qh) * p.seqlen_q + qi] =
-              mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+        write_row<BF16>(p, b, kvh, row0 + row, d4, acc, mx, sum);
       }
     }
-    fence_proxy_async();  // these plain accesses come before the next copies into the ring
-    __syncthreads();
+    // (after a failed wait the other pieces' barriers are still met)
   }
+  // (after a failed wait) let the copies in flight land before the block ends
+  for (; used < filled; ++used)
+    mbar_wait_quiet(&full[warp][used % S::kStages], (uint32_t)(used / S::kStages) & 1u, ab.limit_ns);
 }
 
 // ----------------------------------------------------------------- the join
@@ -636,18 +800,18 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks) a
 // sums are then added in warp order.
 template <bool BF16, int DV, int ROWS>
 __global__ void __launch_bounds__(256) attn_kv_join_kernel(const __grid_constant__ DecodeParams p,
-                                                            int blocks) {
+                                                           int blocks) {
   __shared__ float sm_m[8][ROWS], sm_l[8][ROWS];
   extern __shared__ float so[];  // [8][ROWS * DV]
   const int per_seq = p.c.heads * p.row_blocks;
   const int b = (int)(blockIdx.x / per_seq), item = (int)(blockIdx.x % per_seq);
   const int kvh = item / p.row_blocks, row0 = (item - kvh * p.row_blocks) * ROWS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nu = units_of(seq_range(p, b));
+  const int nu = seq_range(p, b).tiles;
   int k0 = 0, np = 0;
   if (nu > 0) {
     const long long all = *p.total;
-    const long long nblk = all < blocks ? all : blocks;
+    const long long nblk = used_blocks(all, blocks);
     const long long a = reinterpret_cast<const long long*>(p.info)[blockIdx.x], z = a + nu - 1;
     // block k has units [all k / nblk, all (k + 1) / nblk): the block of unit u
     auto block_of = [&](long long u) {
@@ -682,7 +846,8 @@ __global__ void __launch_bounds__(256) attn_kv_join_kernel(const __grid_constant
     float f = 0.0f;
     if (lane < ROWS) {
       const float mx = sm_m[0][lane];
-      f = ex2(pc[ROWS * DV + lane] - (mx == -INFINITY ? 0.0f : mx));
+      const float mp = pc[ROWS * DV + lane];
+      f = mp == -INFINITY ? 1.0f : ex2(mp - mx);  // (a piece without a maximum: zeros, or NaN)
       sum = fmaf(pc[ROWS * (DV + 1) + lane], f, sum);
     }
 #pragma unroll
@@ -709,34 +874,20 @@ __global__ void __launch_bounds__(256) attn_kv_join_kernel(const __grid_constant
       y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
       s += sm_l[w][row];
     }
-    const float mx = sm_m[0][row];
-    const float inv = mx == -INFINITY ? 0.0f : 1.0f / s;
-    y.x *= inv, y.y *= inv, y.z *= inv, y.w *= inv;
-    const int qi = (row0 + row) / p.group, qh = kvh * p.group + (row0 + row) % p.group;
-    const int64_t off = b * p.o_b + qi * p.o_t + qh * p.o_h + d4 * 4;
-    if (p.o_f32)
-      *reinterpret_cast<float4*>((float*)p.o + off) = y;
-    else
-      *reinterpret_cast<uint2*>((uint16_t*)p.o + off) =
-          make_uint2(Pack<BF16>::two(y.x, y.y), Pack<BF16>::two(y.z, y.w));
-    if (d4 == 0)
-      p.lse[((int64_t)b * p.heads_q + qh) * p.seqlen_q + qi] =
-          mx == -INFINITY ? -INFINITY : (mx + log2f(s)) * 0.6931471805599453f;
+    write_row<BF16>(p, b, kvh, row0 + row, d4, y, sm_m[0][row], s);
   }
 }
 
 // ----------------------------------------------------------------- launches
-int decode_col_tiles(int rows, int d_v) {
-  (void)d_v;
-  return rows > 8 ? 2 : 1;
-}
+// (At d_v 256 a lane's share of O for 16 rows would not fit its registers.)
+int decode_col_tiles(int rows, int d_v) { return rows > 8 && d_v < 256 ? 2 : 1; }
 
 int decode_blocks(const DecodeParams& p, int num_sms) {
-  // no more than the longest possible lists of units
-  const int64_t cap = ((int64_t)p.cols << p.c.page_shift) / kUnit + 2;
-  const int64_t units = cap * p.batch * p.c.heads * p.row_blocks;
-  const int per_sm = (decode_col_tiles(p.rows, p.c.d_v) == 1 && p.c.d_v <= 128) || p.c.d_v == 64 ? 2 : 1;
-  return (int)std::min<int64_t>((int64_t)num_sms * per_sm, std::max<int64_t>(units, 1));
+  // no more than the longest possible list of tiles keeps busy
+  const int64_t tiles = (((int64_t)p.cols << p.c.page_shift) + kTile - 1) / kTile;
+  const int per_sm = light(p.c.d_v, decode_col_tiles(p.rows, p.c.d_v)) ? 2 : 1;
+  return (int)std::max<int64_t>(
+      used_blocks(tiles * p.batch * p.c.heads * p.row_blocks, num_sms * per_sm), 1);
 }
 
 size_t decode_partial_floats(int rows_per_block, int d_v) {
@@ -768,10 +919,11 @@ cudaError_t dec_launch(const DecodeParams& p, int blocks, cudaStream_t st) {
 
 template <bool BF16, int NT>
 cudaError_t dec_dims(const DecodeParams& p, int blocks, cudaStream_t st) {
+  if constexpr (NT == 1)
+    if (p.c.d_qk == 256 && p.c.d_v == 256) return dec_launch<BF16, 256, 256, 1>(p, blocks, st);
   if (p.c.d_qk == 64 && p.c.d_v == 64) return dec_launch<BF16, 64, 64, NT>(p, blocks, st);
   if (p.c.d_qk == 128 && p.c.d_v == 128) return dec_launch<BF16, 128, 128, NT>(p, blocks, st);
   if (p.c.d_qk == 192 && p.c.d_v == 128) return dec_launch<BF16, 192, 128, NT>(p, blocks, st);
-  if (p.c.d_qk == 256 && p.c.d_v == 256) return dec_launch<BF16, 256, 256, NT>(p, blocks, st);
   return cudaErrorNotSupported;
 }
 
