@@ -84,7 +84,6 @@ cudaError_t launch_kv4_read(const KvRowsParams& p, bool bf16, int num_sms, cudaS
 
 struct DecodeParams {
   Kv4 c;
-  const uint8_t* src[4];  // the cache's arrays: K codes, V codes, K scales, V scales
   const void* q;
   void* o;
   float* lse;  // [batch][heads_q][seqlen_q]

@@ -617,10 +617,6 @@ attn_status_t attn_kv_decode(const attn_kv4_decode_params_t* p, const attn_kv4_c
     for (int j = i + 1; j < 4; ++j)
       if (regions_overlap(out[i], out[j])) return api_fail(ATTN_ERR_INVALID_ARG, "outputs overlap");
   }
-  kp.src[0] = kp.c.k_codes;
-  kp.src[1] = kp.c.v_codes;
-  kp.src[2] = (const uint8_t*)kp.c.k_scales;
-  kp.src[3] = (const uint8_t*)kp.c.v_scales;
   kp.q = q;
   kp.o = o;
   kp.lse = lse;

@@ -51,7 +51,7 @@ constexpr int kTile = 32;   // tokens of a warp's tile
 constexpr int kWarps = 8;   // of a block
 constexpr int kUnit = kTile * kWarps;
 constexpr int kSlots = 4;   // of the join
-constexpr int kExpMin = -100, kExpMax = 100;  // exponents of V's scales told apart
+constexpr int kExpMin = -80, kExpMax = 100;  // exponents of V's scales told apart
 
 // whether 128 registers hold a lane's share
 __host__ __device__ constexpr bool light(int dv, int nt) { return dv * nt <= 128; }
@@ -116,13 +116,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// the same with a zero accumulator
-__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1,
-                                               uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+// d = c + a b
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1,
+                                         const float (&c)[4]) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%10,%10,%10,%10};"
+      "{%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+        "f"(c[3]));
 }
 
 // The 8 codes of a word as pairs of fp16 numbers: pair n holds codes n and n + 4,
@@ -201,8 +203,11 @@ struct Piece {
   uint32_t qf[NT][S::GK][4];
   float xs[NT][2];               // from products to scores in base 2
   float o[NT][S::GV][2][4];      // dims 32 g + 4 r + {0,1}, {2,3} (odd ones 16 fold)
-  float m[NT][2], l[NT][2];      // reference exponent; this lane's share of the sum
-  int vexp;                      // O is held times 2^(14 - 24 - vexp)
+  // A score x (base 2) counts as 2^(x + ref), ref = kf - m: m is the column's
+  // reference, kf = 14 - e with 2^e above V's scales so far.  l: this lane's
+  // share of the sum; O is held times 2^-24.
+  float ref[NT][2], l[NT][2];
+  float lim, vlim;               // kf + 1; 2^e
 };
 
 // WHOLE: every query of the block sees every token of the tile.
@@ -212,37 +217,139 @@ __device__ __forceinline__ void do_tile(Piece<DQK, DV, NT>& z, const uint8_t* st
                                         int c) {
   using S = DecShape<DQK, DV, NT>;
   float x[2][NT][4];  // S^T of two blocks of 16 tokens: rows r, r + 8
+  uint32_t sa[2][S::GK / 2], sb[2][S::GK / 2];
+  uint32_t ka[2][S::GK], kb[2][S::GK];
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt) {
     const int ta = mt * 16 + row_token(r), tb = ta + 8;
-    uint32_t ka[S::GK], kb[S::GK], sa[S::GK / 2], sb[S::GK / 2];
-    lds_words<S::GK>(st + ta * (DQK / 2) + c * 4 * S::GK, ka);
-    lds_words<S::GK>(st + tb * (DQK / 2) + c * 4 * S::GK, kb);
-    lds_words<S::GK / 2>(st + S::kKc + S::kVc + ta * 2 * S::GK, sa);
-    lds_words<S::GK / 2>(st + S::kKc + S::kVc + tb * 2 * S::GK, sb);
+    lds_words<S::GK>(st + ta * (DQK / 2) + c * 4 * S::GK, ka[mt]);
+    lds_words<S::GK>(st + tb * (DQK / 2) + c * 4 * S::GK, kb[mt]);
+    lds_words<S::GK / 2>(st + S::kKc + S::kVc + ta * 2 * S::GK, sa[mt]);
+    lds_words<S::GK / 2>(st + S::kKc + S::kVc + tb * 2 * S::GK, sb[mt]);
+  }
 #pragma unroll
-    for (int g = 0; g < S::GK; ++g) {
-      float acc[NT][4];
+  for (int g = 0; g < S::GK; ++g) {
+    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float low[NT][4];  // what the codes' offset of 8 adds up to
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const uint32_t* q = z.qf[t][g];
+      mma16816(low[t], kLow8, kLow8, kHigh8, kHigh8, q[0], q[1], zero);
+      mma16816(low[t], kLow8, kLow8, kHigh8, kHigh8, q[2], q[3]);
+    }
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
       uint32_t a[4], b[4];
-      codes8(ka[g], a);
-      codes8(kb[g], b);
+      codes8(ka[mt][g], a);
+      codes8(kb[mt][g], b);
+      const float fa = scale_of(sa[mt], g), fb = scale_of(sb[mt], g);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const uint32_t* q = z.qf[t][g];
-        mma16816_first(acc[t], kLow8, kLow8, kHigh8, kHigh8, q[0], q[1]);
-        mma16816(acc[t], kLow8, kLow8, kHigh8, kHigh8, q[2], q[3]);
-        mma16816(acc[t], a[0], b[0], a[1], b[1], q[0], q[1]);
-        mma16816(acc[t], a[2], b[2], a[3], b[3], q[2], q[3]);
-      }
-      const float fa = scale_of(sa, g), fb = scale_of(sb, g);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        x[mt][t][0] = g ? fmaf(acc[t][0], fa, x[mt][t][0]) : acc[t][0] * fa;
-        x[mt][t][1] = g ? fmaf(acc[t][1], fa, x[mt][t][1]) : acc[t][1] * fa;
-        x[mt][t][2] = g ? fmaf(acc[t][2], fb, x[mt][t][2]) : acc[t][2] * fb;
-        x[mt][t][3] = g ? fmaf(acc[t][3], fb, x[mt][t][3]) : acc[t][3] * fb;
+        float acc[4];
+        mma16816(acc, a[0], b[0], a[1], b[1], q[0], q[1], low[t]);
+        mma16816(acc, a[2], b[2], a[3], b[3], q[2], q[3]);
+        x[mt][t][0] = g ? fmaf(acc[0], fa, x[mt][t][0]) : acc[0] * fa;
+        x[mt][t][1] = g ? fmaf(acc[1], fa, x[mt][t][1]) : acc[1] * fa;
+        x[mt][t][2] = g ? fmaf(acc[2], fb, x[mt][t][2]) : acc[2] * fb;
+        x[mt][t][3] = g ? fmaf(acc[3], fb, x[mt][t][3]) : acc[3] * fb;
       }
     }
+  }
+  // ---- running softmax in base 2.  The reference of a column moves only when
+  // a score passes it by more than 1: probabilities stay below 2 (times 2^kf, and
+  // times V's scales below 2^15), and most tiles need no exchange between lanes.
+  bool move = false;
+  float mx[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (!WHOLE) {  // the tokens that this column's query sees
+        const int row = row0 + t * 8 + 2 * c + e;
+        const int pos = len - p.seqlen_q + row / p.group;
+        const int hi = row < p.rows ? pos : -1;
+        const int lo = p.window_left < 0 ? 0 : max(0, pos - p.window_left);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = t0 + i * 8 + row_token(r);
+          if (j > hi || (j < lo && j >= p.sinks)) x[i >> 1][t][2 * (i & 1) + e] = -INFINITY;
+        }
+      }
+      mx[t][e] = z.xs[t][e] * fmaxf(fmax3(x[0][t][e], x[0][t][2 + e], x[1][t][e]), x[1][t][2 + e]);
+      move |= mx[t][e] + z.ref[t][e] > z.lim;
+    }
+  // the largest scale (NaN apart) of the tokens that a query sees: lane i looks
+  // at token i
+  float top;
+  {
+    const int lane = r * 4 + c;
+    uint32_t w[S::GV / 2];
+    lds_words<S::GV / 2>(st + S::kKc + S::kVc + S::kKs + lane * 2 * S::GV, w);
+    __nv_bfloat162 y = *reinterpret_cast<__nv_bfloat162*>(&w[0]);
+#pragma unroll
+    for (int i = 1; i < S::GV / 2; ++i) y = __hmax2(y, *reinterpret_cast<__nv_bfloat162*>(&w[i]));
+    const uint32_t u = *reinterpret_cast<uint32_t*>(&y);
+    top = fmaxf(scale_of(&u, 0), scale_of(&u, 1));
+    if (!WHOLE) {  // a token that no query sees: its scales may be anything
+      const int j = t0 + lane;
+      const int hi = len - p.seqlen_q + (min(row0 + S::kRows, p.rows) - 1) / p.group;
+      const int lo = p.window_left < 0 ? 0 : len - p.seqlen_q + row0 / p.group - p.window_left;
+      if (j > hi || (j < lo && j >= p.sinks)) top = 0.0f;
+    }
+  }
+  move |= top >= z.vlim;
+  if (__any_sync(0xffffffffu, move)) {
+    const float kf_old = z.lim - 1.0f;
+    float f = 1.0f;
+    {
+      // (positive numbers: their bits are ordered)
+      const uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(top, 0.0f)));
+      const int e = min(max((int)(u >> 23) - 126, kExpMin), kExpMax), e_old = 15 - (int)z.lim;
+      if (e > e_old) {
+        f = pow2(max(e_old - e, -126));
+        z.lim = (float)(15 - e);
+        z.vlim = pow2(e);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float m = kf_old - z.ref[t][e];
+        float y = mx[t][e];
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+        y = fmaxf(y, m);
+        const float a = ex2(m - y) * f;
+        z.ref[t][e] = z.lim - 1.0f - y;
+        z.l[t][e] *= a;
+#pragma unroll
+        for (int g = 0; g < S::GV; ++g)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            z.o[t][g][h][e] *= a;
+            z.o[t][g][h][2 + e] *= a;
+          }
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const uint64_t xs = f2_pack(z.xs[t][0], z.xs[t][1]), ref = f2_pack(z.ref[t][0], z.ref[t][1]);
+    uint64_t sum = f2_pack(z.l[t][0], z.l[t][1]);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float& y0 = x[mt][t][2 * h];
+        float& y1 = x[mt][t][2 * h + 1];
+        f2_unpack(f2_fma(f2_pack(y0, y1), xs, ref), y0, y1);
+        y0 = ex2(y0);
+        y1 = ex2(y1);
+        sum = f2_add(sum, f2_pack(y0, y1));
+      }
+    f2_unpack(sum, z.l[t][0], z.l[t][1]);
   }
   // ---- V's scales of tokens r and r + 8 of both blocks
   uint32_t vs[2][2][S::GV / 2];
@@ -252,110 +359,6 @@ __device__ __forceinline__ void do_tile(Piece<DQK, DV, NT>& z, const uint8_t* st
     for (int h = 0; h < 2; ++h)
       lds_words<S::GV / 2>(st + S::kKc + S::kVc + S::kKs +
                                (mt * 16 + h * 8 + row_token(r)) * 2 * S::GV, vs[mt][h]);
-  // ---- running softmax in base 2.  The reference m of a column moves only
-  // when a score passes it by more than 1: probabilities stay below 2, and most
-  // tiles need no exchange between lanes.
-  bool move = false;
-  float mx[NT][2];
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      mx[t][e] = -INFINITY;
-      int hi = 0, lo = 0;
-      if (!WHOLE) {  // the tokens that this column's query sees
-        const int row = row0 + t * 8 + 2 * c + e;
-        const int pos = len - p.seqlen_q + row / p.group;
-        hi = row < p.rows ? pos : -1;
-        lo = p.window_left < 0 ? 0 : max(0, pos - p.window_left);
-      }
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float& y = x[mt][t][2 * h + e];
-          y *= z.xs[t][e];
-          if (!WHOLE) {
-            const int j = t0 + mt * 16 + h * 8 + row_token(r);
-            if (j > hi || (j < lo && j >= p.sinks)) y = -INFINITY;
-          }
-          mx[t][e] = fmaxf(mx[t][e], y);
-        }
-      move |= mx[t][e] > z.m[t][e] + 1.0f;
-    }
-  // the largest scale (NaN apart) of the tokens that a query sees
-  float top = 0.0f;
-  if (WHOLE) {
-    __nv_bfloat162 w = *reinterpret_cast<__nv_bfloat162*>(&vs[0][0][0]);
-#pragma unroll
-    for (int i = 1; i < 4 * (S::GV / 2); ++i)
-      w = __hmax2(w, *reinterpret_cast<__nv_bfloat162*>(&vs[i / (2 * (S::GV / 2))][i / (S::GV / 2) % 2][i % (S::GV / 2)]));
-    const uint32_t u = *reinterpret_cast<uint32_t*>(&w);
-    top = fmaxf(scale_of(&u, 0), scale_of(&u, 1));
-  } else {
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        bool seen = false;  // else the scales may be anything
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          seen |= x[mt][t][2 * h] != -INFINITY || x[mt][t][2 * h + 1] != -INFINITY;
-#pragma unroll
-        for (int g = 0; g < S::GV; ++g)
-          if (seen) top = fmaxf(top, scale_of(vs[mt][h], g));
-      }
-  }
-  move |= (int)(__float_as_uint(top) >> 23) - 126 > z.vexp;
-  if (__any_sync(0xffffffffu, move)) {
-    float f = 1.0f;
-    {
-      const uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-      const int e = min(max((int)(u >> 23) - 126, kExpMin), kExpMax);
-      if (e > z.vexp) {
-        f = pow2(max(z.vexp - e, -126));
-        z.vexp = e;
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float y = mx[t][e];
-        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
-        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-        y = fmaxf(y, z.m[t][e]);
-        const float a = z.m[t][e] == -INFINITY ? 0.0f : ex2(z.m[t][e] - y);
-        z.m[t][e] = y;
-        z.l[t][e] *= a;
-#pragma unroll
-        for (int g = 0; g < S::GV; ++g)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            z.o[t][g][h][e] *= a * f;
-            z.o[t][g][h][2 + e] *= a * f;
-          }
-      }
-  }
-  const float kf = pow2(14 - z.vexp);  // products below 2^15
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float ms = z.m[t][e] == -INFINITY ? 0.0f : z.m[t][e];  // nothing seen yet
-      float sum = 0.0f;
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float& y = x[mt][t][2 * h + e];
-          y = ex2(y - ms);
-          sum += y;
-          y *= kf;
-        }
-      z.l[t][e] += sum;
-    }
   // ---- O^T += V^T P^T
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt) {
@@ -375,8 +378,9 @@ __device__ __forceinline__ void do_tile(Piece<DQK, DV, NT>& z, const uint8_t* st
       const float fa = scale_of(vs[mt][0], g), fb = scale_of(vs[mt][1], g);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float p0 = x[mt][t][0] * fa, p1 = x[mt][t][1] * fa;
-        float p2 = x[mt][t][2] * fb, p3 = x[mt][t][3] * fb;
+        float p0, p1, p2, p3;
+        f2_unpack(f2_mul(f2_pack(x[mt][t][0], x[mt][t][2]), f2_pack(fa, fb)), p0, p2);
+        f2_unpack(f2_mul(f2_pack(x[mt][t][1], x[mt][t][3]), f2_pack(fa, fb)), p1, p3);
         if (!WHOLE) {  // a masked token's scale is not looked at: it may be anything
           p0 = x[mt][t][0] == 0.0f ? 0.0f : p0;
           p1 = x[mt][t][1] == 0.0f ? 0.0f : p1;
@@ -410,10 +414,21 @@ __device__ __forceinline__ void write_row(const DecodeParams& p, int b, int kvh,
         make_uint2(Pack<BF16>::two(acc.x, acc.y), Pack<BF16>::two(acc.z, acc.w));
   if (d4 == 0)
     p.lse[((int64_t)b * p.heads_q + qh) * p.seqlen_q + qi] =
-        sum == 0.0f ? -INFINITY : ((mx == -INFINITY ? 0.0f : mx) + log2f(sum)) * 0.6931471805599453f;
+        sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
 }
 
 // ----------------------------------------------------------------- the kernel
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+               "l"((uint64_t)__cvta_generic_to_global(src))
+               : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the last N groups of this thread
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // A place in the list of tiles: tile v of an item of a sequence.
 struct Cursor {
   int b, item, v;
@@ -422,14 +437,8 @@ struct Cursor {
 // A warp's next tiles, kUnit tokens apart.
 struct __align__(16) Strip {
   const int32_t* row;  // of the block table
-  int token, left;
-  int head_row, len;   // first row of the kv head in a page; tokens of the sequence
-};
-// One array of the cache, and where a stage holds its part.
-struct __align__(16) Array {
-  const uint8_t* base;
-  uint32_t page, width;  // bytes of a page, of a row
-  int off;
+  int token, left;     // of the tile looked up last; tiles after it
+  int row_in, len;     // row within a page's [head][token]; tokens of the sequence
 };
 // Moves `n` tiles on.  Past the end of the list (lengths that changed under the
 // call): b = batch.
@@ -450,23 +459,15 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
   using S = DecShape<DQK, DV, NT>;
   constexpr int kThreads = kWarps * 32;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full[kWarps][S::kStages];
   __shared__ Cursor cursor[kWarps + 1];  // of each warp's copies; of the next piece
   __shared__ Strip strip[kWarps];
-  __shared__ Array array[4];
-  __shared__ int abort_flag;
   __shared__ long long s_sum[kWarps];
   __shared__ long long s_before;  // tiles before sequence s_b
   __shared__ int s_b;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Abort ab{&abort_flag, p.status, kWaitLimitNs};
   if (tid == 0) {
-    abort_flag = 0;
     s_b = p.batch;
     s_before = 0;
-    for (int w = 0; w < kWarps; ++w)
-      for (int s = 0; s < S::kStages; ++s) mbar_init(&full[w][s], 1);
-    fence_barrier_init();
   }
   // ---- the list of tiles, and this block's run of it
   const int per_seq = p.c.heads * p.row_blocks;  // items of a sequence
@@ -518,21 +519,12 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
   uint8_t* ring = smem + warp * (S::kStages * S::kStage);
   float* jo = reinterpret_cast<float*>(smem + S::kRing);             // [slot][row][DV]
   float* stats = reinterpret_cast<float*>(smem + S::kRing + S::kJoin);
-  int used = 0, filled = 0, pieces = 0;
-  bool ok = true;
-
-  // ---- copies.  A warp feeds its own ring, across the pieces of the run: lane
-  // 4 h + i copies array i of the tile's page h (pages of 16 tokens: a tile
-  // spans two), so that a tile costs the warp few instructions.  Where the next
-  // tile lies is looked up one tile ahead.
+  // ---- copies.  A warp feeds its own ring, across the pieces of the run, by
+  // 16-byte asynchronous copies of all its lanes (a tile of one array is one
+  // run of bytes); it waits for its own copies alone.  Where the next tile lies
+  // is looked up one tile ahead.
   const int left_total = n_run > warp ? (n_run - warp + kWarps - 1) / kWarps : 0;  // this warp's tiles
-  const int tok = min(p.c.page_size, kTile);  // tokens of a copy
-  const int lanes = tok < kTile ? 8 : 4;
-  if (tid < 4) {
-    const int width = tid == 0 ? DQK / 2 : tid == 1 ? DV / 2 : tid == 2 ? 2 * S::GK : 2 * S::GV;
-    const int off = tid == 0 ? 0 : tid == 1 ? S::kKc : tid == 2 ? S::kKc + S::kVc : S::kKc + S::kVc + S::kKs;
-    array[tid] = Array{p.src[tid], (uint32_t)(p.c.heads * p.c.page_size * width), (uint32_t)width, off};
-  }
+  const bool small = p.c.page_size < kTile;  // a tile spans two pages
   if (lane == 0) {
     Cursor k;
     k.b = first_b;
@@ -547,69 +539,86 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     }
     advance(p, per_seq, k, warp);
     cursor[warp] = k;
-    strip[warp].left = 0;
   }
   __syncthreads();
-  int next_page = 0, next_row = -1;  // page, and row within the page's [head][token] (-1: none)
-  const uint32_t lane_mask = (1u << lanes) - 1u;
-  auto look_up = [&]() {  // lanes 0 .. lanes - 1
-    Strip t = strip[warp];
-    if (t.left == 0) {  // a new strip: tiles in a row, kWarps apart
+  if (lane == 0) strip[warp].left = 0;
+  int next_page = 0;  // of the tile to copy next (its first one, where it spans two)
+  auto look_up = [&]() {
+    __syncwarp();
+    if (strip[warp].left == 0) {  // a new strip: tiles in a row, kWarps apart
+      __syncwarp();
       if (lane == 0) {
         Cursor k = cursor[warp];
-        t.left = 1;
-        t.token = -1;  // no tile (lengths that changed under the call)
+        Strip t{p.table, 0, 1, 0, 0};  // no tile (lengths that changed under the call)
         if (k.b < p.batch) {
           const int end = k.v < k.sr.n_sink ? k.sr.n_sink : k.sr.tiles;
           t.row = p.table + (int64_t)k.b * p.table_stride;
-          t.token = tile_token(k.sr, k.v);
+          t.token = tile_token(k.sr, k.v) - kUnit;
           t.left = (end - k.v + kWarps - 1) / kWarps;
-          t.head_row = (k.item / p.row_blocks) * p.c.page_size;
+          // (kUnit is a multiple of the page size: the same for every tile)
+          t.row_in = (k.item / p.row_blocks) * p.c.page_size + (t.token & (p.c.page_size - 1));
           t.len = k.sr.len;
           advance(p, per_seq, k, t.left * kWarps);
           cursor[warp] = k;
         }
         strip[warp] = t;
       }
-      __syncwarp(lane_mask);
-      t = strip[warp];
+      __syncwarp();
     }
-    const int t0 = t.token + (lane >> 2) * tok;
-    next_row = -1;
-    if (t.token >= 0 && t0 < t.len) {
-      next_page = t.row[t0 >> p.c.page_shift];
-      next_row = t.head_row + (t0 & (p.c.page_size - 1));
-    }
-    __syncwarp(lane_mask);
-    if (lane == 0) {
-      strip[warp].token = t.token + kUnit;
-      strip[warp].left = t.left - 1;
+    const int token = strip[warp].token + kUnit, left = strip[warp].left - 1;
+    if (token < strip[warp].len) next_page = strip[warp].row[token >> p.c.page_shift];
+    __syncwarp();
+    if (lane == 0) strip[warp].token = token, strip[warp].left = left;
+  };
+  // Chunks of 16 bytes of a stage: K codes, V codes, scales; `half`: only those
+  // of its first (0) or last (1) 16 tokens, 2: all.
+  auto copy_rows = [&](uint8_t* st, int page, int row, int half) {
+    const int64_t at = (int64_t)page * (p.c.heads * p.c.page_size) + row - (half == 1 ? 16 : 0);
+    const uint8_t* k = p.c.k_codes + at * (DQK / 2) + lane * 16;
+    const uint8_t* v = p.c.v_codes + at * (DV / 2) + lane * 16;
+    const uint32_t dst = smem_u32(st) + lane * 16;
+#pragma unroll
+    for (int i = 0; i < DQK / 32; ++i)
+      if (half == 2 || i / (DQK / 64) == half) copy16(dst + i * 512, k + i * 512);
+#pragma unroll
+    for (int i = 0; i < DV / 32; ++i)
+      if (half == 2 || i / (DV / 64) == half) copy16(dst + S::kKc + i * 512, v + i * 512);
+#pragma unroll
+    for (int i = 0; i < (DQK + DV) / 8; i += 32) {
+      const int j = lane + i;
+      const bool is_k = j < DQK / 8;
+      const int o = is_k ? j : j - DQK / 8;
+      const uint8_t* src = is_k ? (const uint8_t*)(p.c.k_scales + at * S::GK)
+                                : (const uint8_t*)(p.c.v_scales + at * S::GV);
+      if (j < (DQK + DV) / 8 && (half == 2 || o / (is_k ? DQK / 16 : DV / 16) == half))
+        copy16(dst + S::kKc + S::kVc + i * 16, src + o * 16);
     }
   };
-  auto copy = [&]() {  // lanes 0 .. lanes - 1
-    const int s = filled % S::kStages;
-    uint64_t* bar = &full[warp][s];
-    const bool good = next_row >= 0 && (unsigned)next_page < (unsigned)p.c.num_pages;
-    if (!good && next_row >= 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
-    const uint32_t pages = __popc(__ballot_sync(lane_mask, good)) / 4;
-    if (lane == 0)
-      mbar_arrive_tx(bar, pages * (uint32_t)tok * (DQK / 2 + DV / 2 + 2 * S::GK + 2 * S::GV));
-    __syncwarp(lane_mask);
-    if (good) {
-      const Array y = array[lane & 3];
-      const uint8_t* src = y.base + (uint64_t)(uint32_t)next_page * y.page + (uint64_t)(uint32_t)next_row * y.width;
-      bulk_load(ring + s * S::kStage + y.off + (lane >> 2) * tok * y.width, src, tok * y.width, bar);
+  auto copy = [&](int s) {
+    __syncwarp();
+    uint8_t* st = ring + s * S::kStage;
+    const int token = strip[warp].token, row = strip[warp].row_in, len = strip[warp].len;
+    if (token >= len) return;
+    bool bad = (unsigned)next_page >= (unsigned)p.c.num_pages;
+    if (!bad) copy_rows(st, next_page, row, small ? 0 : 2);
+    if (small && token + p.c.page_size < len) {
+      const int page = strip[warp].row[(token >> p.c.page_shift) + 1];
+      if ((unsigned)page < (unsigned)p.c.num_pages)
+        copy_rows(st, page, row, 1);
+      else
+        bad = true;
     }
+    if (bad && lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
   };
-  if (lane < lanes && left_total > 0) {
-    look_up();
-    for (; filled < left_total && filled < S::kStages; ++filled) {
-      copy();
-      __syncwarp(lane_mask);
-      if (filled + 1 < left_total) look_up();
+  int used = 0, pieces = 0;
+  if (left_total > 0) look_up();
+  for (int i = 0; i < S::kStages; ++i) {
+    if (i < left_total) {
+      copy(i);
+      if (i + 1 < left_total) look_up();
     }
+    copies_end();
   }
-  filled = min(left_total, S::kStages);
   for (int done_tiles = 0; done_tiles < n_run;) {
     // the piece: every warp goes by the same copy of the lengths, so that all
     // of them meet the same barriers
@@ -662,7 +671,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         z.xs[t][e] = p.scale_log2 * 16777216.0f * __shfl_sync(0xffffffffu, pow2(ex), (2 * c + e) * 4);
-        z.m[t][e] = -INFINITY;
+        z.ref[t][e] = 1e30f;  // nothing seen yet: a reference below any score
         z.l[t][e] = 0.0f;
       }
 #pragma unroll
@@ -672,7 +681,8 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
 #pragma unroll
           for (int e = 0; e < 4; ++e) z.o[t][g][h][e] = 0.0f;
     }
-    z.vexp = kExpMin;
+    z.lim = (float)(15 - kExpMin);
+    z.vlim = pow2(kExpMin);
     // every query of the item sees token j if j <= pos_lo and (j >= pos_hi -
     // window_left or j < sinks); columns past the last row hold zeros, and what
     // they sum up is not written
@@ -681,10 +691,11 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
 
     const int whole_hi = pos_lo - (kTile - 1);
     const int whole_lo = p.window_left < 0 ? 0 : pos_hi - p.window_left;
-    for (int v = v0 + skew; v < v1; v += kWarps, ++used) {
+    for (int v = v0 + skew; v < v1; v += kWarps) {
       const int s = used % S::kStages;
-      ok = ok && mbar_wait_warp(&full[warp][s], (uint32_t)(used / S::kStages) & 1u, ab);
-      if (!ok) break;
+      ++used;
+      copies_wait<S::kStages - 1>();
+      __syncwarp();
       const uint8_t* st = ring + s * S::kStage;
       const int t0 = tile_token(sr, v);
       const bool whole = t0 <= whole_hi && (t0 >= whole_lo || t0 + kTile <= p.sinks);
@@ -693,16 +704,14 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
       else
         do_tile<false>(z, st, p, sr.len, row0, t0, r, c);
       __syncwarp();
-      if (filled < left_total) {
-        if (lane < lanes) {
-          copy();
-          if (filled + 1 < left_total) look_up();
-        }
-        ++filled;
+      if (used - 1 + S::kStages < left_total) {
+        copy(s);
+        if (used + S::kStages < left_total) look_up();
       }
+      copies_end();
     }
 
-    // ---- join the warps.  A failed wait skips the tiles, never a barrier.
+    // ---- join the warps
     float* jm = stats + (pieces & 1) * (2 * kWarps * S::kRows);  // [warp][row]
     float* jl = jm + kWarps * S::kRows;
     ++pieces;
@@ -715,7 +724,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int row = t * 8 + 2 * c + e;
-        if (r == 0) jm[warp * S::kRows + row] = z.m[t][e], jl[warp * S::kRows + row] = sum;
+        if (r == 0) jm[warp * S::kRows + row] = -z.ref[t][e], jl[warp * S::kRows + row] = sum;
       }
     __syncthreads();
     if (tid == 0) {  // (read by all before this barrier, and again after the next)
@@ -723,8 +732,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
       advance(p, per_seq, n, v1 - v0);
       cursor[kWarps] = n;
     }
-    const float back = pow2(24 - 14 + z.vexp);
-#pragma unroll
+    #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {  // to the common maximum
@@ -732,7 +740,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
         float mx = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, jm[w * S::kRows + row]);
-        const float f = z.m[t][e] == -INFINITY ? 0.0f : ex2(z.m[t][e] - mx) * back;
+        const float f = ex2(-z.ref[t][e] - mx) * 16777216.0f;
 #pragma unroll
         for (int g = 0; g < S::GV; ++g)
 #pragma unroll
@@ -769,9 +777,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
       float sum = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float mw = jm[w * S::kRows + row];
-        // a NaN sum of a warp without a maximum (all its scores NaN) counts too
-        sum = fmaf(jl[w * S::kRows + row], mw == -INFINITY ? 1.0f : ex2(mw - mx), sum);
+        sum = fmaf(jl[w * S::kRows + row], ex2(jm[w * S::kRows + row] - mx), sum);
       }
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -786,11 +792,8 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
         write_row<BF16>(p, b, kvh, row0 + row, d4, acc, mx, sum);
       }
     }
-    // (after a failed wait the other pieces' barriers are still met)
   }
-  // (after a failed wait) let the copies in flight land before the block ends
-  for (; used < filled; ++used)
-    mbar_wait_quiet(&full[warp][used % S::kStages], (uint32_t)(used / S::kStages) & 1u, ab.limit_ns);
+  copies_wait<0>();
 }
 
 // ----------------------------------------------------------------- the join
@@ -846,8 +849,7 @@ __global__ void __launch_bounds__(256) attn_kv_join_kernel(const __grid_constant
     float f = 0.0f;
     if (lane < ROWS) {
       const float mx = sm_m[0][lane];
-      const float mp = pc[ROWS * DV + lane];
-      f = mp == -INFINITY ? 1.0f : ex2(mp - mx);  // (a piece without a maximum: zeros, or NaN)
+      f = ex2(pc[ROWS * DV + lane] - mx);
       sum = fmaf(pc[ROWS * (DV + 1) + lane], f, sum);
     }
 #pragma unroll
