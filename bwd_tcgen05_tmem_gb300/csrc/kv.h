@@ -95,7 +95,7 @@ struct DecodeParams {
   int o_f32;
   int* info;       // per item: its first unit and its units
   float* partial;  // per block: two pieces of an item
-  int64_t* total;  // units of the call
+  int64_t* total;  // units of the call; blocks that share them
   int* status;
 };
 // Tiles of query columns (8 each) that one block of a call takes.

@@ -51,6 +51,7 @@ constexpr int kTile = 32;   // tokens of a warp's tile
 constexpr int kWarps = 8;   // of a block
 constexpr int kUnit = kTile * kWarps;
 constexpr int kSlots = 4;   // of the join
+constexpr int kItemCost = 12;  // in tiles: what an item costs a block besides them
 constexpr int kExpMin = -80, kExpMax = 100;  // exponents of V's scales told apart
 
 // whether 128 registers hold a lane's share
@@ -97,6 +98,15 @@ __device__ __forceinline__ SeqRange seq_range(const DecodeParams& p, int b) {
   s.n_sink = min(sink_tiles, s.lo);
   s.tiles = s.n_sink + (s.len + kTile - 1) / kTile - s.lo;
   return s;
+}
+// An item's share of the list of work: its tiles, and kItemCost for what a block
+// does once for each item (q, the join of the warps).
+__host__ __device__ __forceinline__ int units_of(int tiles) { return tiles ? tiles + kItemCost : 0; }
+// tiles before position u of a sequence's items
+__device__ __forceinline__ long long tiles_before(int tiles, long long u) {
+  if (tiles == 0) return 0;
+  const int n = units_of(tiles), x = (int)(u % n) - kItemCost;
+  return u / n * tiles + (x > 0 ? x : 0);
 }
 // first token of the v-th tile
 __device__ __forceinline__ int tile_token(const SeqRange& s, int v) {
@@ -433,6 +443,7 @@ __device__ __forceinline__ void copies_wait() {  // all but the last N groups of
 struct Cursor {
   int b, item, v;
   SeqRange sr;
+  long long first_unit;  // of the sequence
 };
 // A warp's next tiles, kUnit tokens apart.
 struct __align__(16) Strip {
@@ -448,6 +459,7 @@ __device__ __forceinline__ void advance(const DecodeParams& p, int per_seq, Curs
     k.v -= k.sr.tiles;
     if (k.sr.tiles == 0 || ++k.item == per_seq) {
       k.item = 0;
+      k.first_unit += (long long)units_of(k.sr.tiles) * per_seq;
       if (++k.b < p.batch) k.sr = seq_range(p, k.b);
     }
   }
@@ -461,59 +473,73 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Cursor cursor[kWarps + 1];  // of each warp's copies; of the next piece
   __shared__ Strip strip[kWarps];
-  __shared__ long long s_sum[kWarps];
-  __shared__ long long s_before;  // tiles before sequence s_b
+  __shared__ long long s_sum[2 * kWarps], s_tiles[2];
+  __shared__ long long s_before;  // units before sequence s_b
   __shared__ int s_b;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     s_b = p.batch;
-    s_before = 0;
+    s_before = s_tiles[0] = s_tiles[1] = 0;
   }
-  // ---- the list of tiles, and this block's run of it
+  // ---- the list of work, and this block's run of it
   const int per_seq = p.c.heads * p.row_blocks;  // items of a sequence
-  long long mine = 0;
-  for (int b = tid; b < p.batch; b += kThreads) mine += seq_range(p, b).tiles;
+  long long units = 0, tiles = 0;
+  for (int b = tid; b < p.batch; b += kThreads) {
+    const int n = seq_range(p, b).tiles;
+    units += units_of(n);
+    tiles += n;
+  }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s_sum[warp] = mine;
+  for (int o = 16; o; o >>= 1) {
+    units += __shfl_xor_sync(0xffffffffu, units, o);
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+  }
+  if (lane == 0) s_sum[warp] = units, s_sum[kWarps + warp] = tiles;
   __syncthreads();
-  long long all = 0;
+  long long all = 0, all_tiles = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) all += s_sum[w];
+  for (int w = 0; w < kWarps; ++w) all += s_sum[w], all_tiles += s_sum[kWarps + w];
   all *= per_seq;
-  const long long nblk = used_blocks(all, gridDim.x);
-  if (blockIdx.x == 0 && tid == 0) *p.total = all;
+  const long long nblk = used_blocks(all_tiles * per_seq, gridDim.x);
+  if (blockIdx.x == 0 && tid == 0) p.total[0] = all, p.total[1] = nblk;
   if ((long long)blockIdx.x >= nblk) return;
   const long long first = all * blockIdx.x / nblk, last = all * (blockIdx.x + 1) / nblk;
-  // the sequence that holds tile `first`
-  long long before = 0;
+  // the sequence that holds unit `first`, and the tiles before `first` and `last`
+  long long before_u = 0, before_t = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
     const int b = b0 + tid;
-    const long long n = b < p.batch ? (long long)seq_range(p, b).tiles * per_seq : 0;
-    long long inc = n;
+    const int nt = b < p.batch ? seq_range(p, b).tiles : 0;
+    const long long n = (long long)units_of(nt) * per_seq, m = (long long)nt * per_seq;
+    long long iu = n, it = m;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
+      const long long x = __shfl_up_sync(0xffffffffu, iu, o), y = __shfl_up_sync(0xffffffffu, it, o);
+      if (lane >= o) iu += x, it += y;
     }
     __syncthreads();
-    if (lane == 31) s_sum[warp] = inc;
+    if (lane == 31) s_sum[warp] = iu, s_sum[kWarps + warp] = it;
     __syncthreads();
-    long long off = before;
+    long long u0 = before_u - n, t0 = before_t - m;
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) off += s_sum[w];
-      before += s_sum[w];
+      if (w < warp) u0 += s_sum[w], t0 += s_sum[kWarps + w];
+      before_u += s_sum[w];
+      before_t += s_sum[kWarps + w];
     }
-    if (first >= off + inc - n && first < off + inc) {
+    u0 += iu;
+    t0 += it;  // units and tiles before sequence b
+    if (first >= u0 && first < u0 + n) {
       s_b = b;
-      s_before = off + inc - n;
+      s_before = u0;
+      s_tiles[0] = t0 + tiles_before(nt, first - u0);
     }
+    if (last > u0 && last <= u0 + n) s_tiles[1] = t0 + tiles_before(nt, last - u0);
     __syncthreads();
-    if (s_b < p.batch) break;
+    if (before_u >= last) break;
   }
   const int first_b = s_b;
   if (first_b >= p.batch) return;  // lengths that changed under the call
-  const int n_run = (int)(last - first);  // tiles of the run; tile i is warp i % kWarps's
+  // tiles of the run; tile i is warp i % kWarps's
+  const int n_run = (int)min(max(s_tiles[1] - s_tiles[0], 0ll), (long long)INT32_MAX);
 
   const int r = lane >> 2, c = lane & 3;
   uint8_t* ring = smem + warp * (S::kStages * S::kStage);
@@ -529,9 +555,11 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     Cursor k;
     k.b = first_b;
     k.sr = seq_range(p, first_b);
-    const long long v = first - s_before;
-    k.item = k.sr.tiles ? (int)(v / k.sr.tiles) : 0;
-    k.v = k.sr.tiles ? (int)(v % k.sr.tiles) : 0;
+    k.first_unit = s_before;
+    const long long u = first - s_before;
+    const int n = max(units_of(k.sr.tiles), 1);
+    k.item = (int)min(u / n, (long long)INT32_MAX);
+    k.v = max((int)(u % n) - kItemCost, 0);
     if (k.item >= per_seq) k.b = p.batch;  // lengths that changed under the call
     if (warp == 0) {
       advance(p, per_seq, k, 0);
@@ -629,9 +657,9 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     const int kvh = item / p.row_blocks, rb = item - kvh * p.row_blocks;
     // this warp's first tile: the run's tile i is warp i % kWarps's
     const int skew = (warp - done_tiles % kWarps + kWarps) % kWarps;
-    if (v0 == 0 && tid == 0) {  // where the item lies, for the join
+    if (v0 == 0 && tid == 0) {  // where the item's tiles lie in the list, for the join
       long long* info = reinterpret_cast<long long*>(p.info);
-      info[(int64_t)b * per_seq + item] = first + done_tiles;
+      info[(int64_t)b * per_seq + item] = k.first_unit + (long long)item * units_of(sr.tiles) + kItemCost;
     }
     done_tiles += v1 - v0;
 
@@ -813,8 +841,7 @@ __global__ void __launch_bounds__(256) attn_kv_join_kernel(const __grid_constant
   const int nu = seq_range(p, b).tiles;
   int k0 = 0, np = 0;
   if (nu > 0) {
-    const long long all = *p.total;
-    const long long nblk = used_blocks(all, blocks);
+    const long long all = p.total[0], nblk = p.total[1];
     const long long a = reinterpret_cast<const long long*>(p.info)[blockIdx.x], z = a + nu - 1;
     // block k has units [all k / nblk, all (k + 1) / nblk): the block of unit u
     auto block_of = [&](long long u) {
@@ -823,7 +850,7 @@ __global__ void __launch_bounds__(256) attn_kv_join_kernel(const __grid_constant
       while (all * (k + 1) / nblk <= u) ++k;
       return (int)k;
     };
-    if (all <= 0 || a < 0 || z >= all) return;
+    if (all <= 0 || nblk <= 0 || nblk > blocks || a < 0 || z >= all) return;
     k0 = block_of(a);
     np = block_of(z) - k0 + 1;
     if (np == 1) return;
