@@ -93,15 +93,14 @@ struct DecodeParams {
   int rows, row_blocks;  // query rows of a kv head (seqlen_q * group), and blocks of them
   float scale_log2;
   int o_f32;
-  int* info;       // per item: its first unit and its units
-  float* partial;  // per block: two pieces of an item
-  int64_t* total;  // units of the call; blocks that share them
+  int* info;       // per item: the first and the last run that work on it
+  float* partial;  // per run: two pieces of items
   int* status;
 };
 // Tiles of query columns (8 each) that one block of a call takes.
 int decode_col_tiles(int rows, int d_v);
 int decode_blocks(const DecodeParams& p, int num_sms);
-size_t decode_partial_floats(int rows_per_block, int d_v);  // of one piece
+size_t decode_partial_floats(int blocks, int rows_per_block, int d_v);
 cudaError_t launch_kv4_decode(const DecodeParams& p, bool bf16, int blocks, cudaStream_t st);
 
 }  // namespace attn

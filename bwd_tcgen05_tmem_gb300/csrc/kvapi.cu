@@ -535,12 +535,12 @@ attn_status_t check_decode(const attn_kv4_decode_params_t* p, const attn_kv4_cac
   kp.sinks = (int)(p->sinks < most ? p->sinks : most);
   kp.scale_log2 = p->softmax_scale * 1.4426950408889634f;
   kp.o_f32 = p->o_dtype == ATTN_FP32;
-  if ((int64_t)kp.batch * c->heads_kv * kp.row_blocks > INT32_MAX)
+  if ((int64_t)kp.batch * c->heads_kv * kp.row_blocks * per > INT32_MAX)
     return api_fail(ATTN_ERR_UNSUPPORTED, "batch * heads too large for the grid");
   return ATTN_OK;
 }
 
-// [256: units of the call][8 bytes an item: its first unit][two pieces a block]
+// [8 bytes an item: its first and last run][two partial results a run]
 struct DecodeLayout {
   size_t info, partial, total;
   int blocks;
@@ -549,11 +549,10 @@ DecodeLayout decode_layout(const attn::DecodeParams& kp) {
   DecodeLayout l;
   const size_t items = (size_t)kp.batch * kp.c.heads * kp.row_blocks;
   l.blocks = attn::decode_blocks(kp, attn::num_sms());
-  l.info = 256;
-  l.partial = l.info + up256(items * 8);
-  l.total = l.partial + (size_t)l.blocks * 2 *
-                            attn::decode_partial_floats(8 * attn::decode_col_tiles(kp.rows, kp.c.d_v),
-                                                        kp.c.d_v) * 4;
+  l.info = 0;
+  l.partial = up256(items * 8) + 256;
+  const int rows = 8 * attn::decode_col_tiles(kp.rows, kp.c.d_v);
+  l.total = l.partial + attn::decode_partial_floats(l.blocks, rows, kp.c.d_v) * 4;
   return l;
 }
 
@@ -624,7 +623,6 @@ attn_status_t attn_kv_decode(const attn_kv4_decode_params_t* p, const attn_kv4_c
   kp.seq_lens = seq_lens;
   kp.q_b = p->stride_q[0], kp.q_t = p->stride_q[1], kp.q_h = p->stride_q[2];
   kp.o_b = p->stride_o[0], kp.o_t = p->stride_o[1], kp.o_h = p->stride_o[2];
-  kp.total = (int64_t*)ws;
   kp.info = (int*)((char*)ws + l.info);
   kp.partial = (float*)((char*)ws + l.partial);
   kp.status = status;

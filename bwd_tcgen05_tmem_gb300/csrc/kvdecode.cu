@@ -48,10 +48,9 @@
 namespace attn {
 
 constexpr int kTile = 32;   // tokens of a warp's tile
-constexpr int kWarps = 8;   // of a block
-constexpr int kUnit = kTile * kWarps;
-constexpr int kSlots = 4;   // of the join
-constexpr int kItemCost = 12;  // in tiles: what an item costs a block besides them
+constexpr int kWarps = 4;   // of a block
+constexpr int kItemCost = 3;   // in tiles: what an item costs a warp besides them
+constexpr int kMinTiles = 2;   // of a warp's run
 constexpr int kExpMin = -80, kExpMax = 100;  // exponents of V's scales told apart
 
 // whether 128 registers hold a lane's share
@@ -66,13 +65,10 @@ struct DecShape {
   static constexpr int kKs = kTile * GK * 2, kVs = kTile * GV * 2;
   static constexpr int kStage = kKc + kVc + kKs + kVs;  // a multiple of 128
   // blocks of an SM: as many as its registers hold
-  static constexpr int kBlocks = light(DV, NT) ? 2 : 1;
-  static constexpr int kStages = DQK == 64 || (kBlocks == 1 && DQK < 256) ? 3 : 2;
+  static constexpr int kBlocks = light(DV, NT) ? 4 : 2;
+  static constexpr int kStages = light(DV, NT) && DQK > 64 ? 2 : DQK >= 256 ? 2 : 3;
   static constexpr int kRing = kWarps * kStages * kStage;
-  // the join of the warps: O [slot][row][dim], and (twice) maxima and sums [warp][row]
-  static constexpr int kJoin = kSlots * kRows * DV * 4;
-  static constexpr int kStats = 2 * 2 * kWarps * kRows * 4;
-  static constexpr int kSmem = kRing + kJoin + kStats;
+  static constexpr int kPart = kRows * (DV + 2);  // floats of a partial result
 };
 
 // ----------------------------------------------------------------- geometry
@@ -112,10 +108,11 @@ __device__ __forceinline__ long long tiles_before(int tiles, long long u) {
 __device__ __forceinline__ int tile_token(const SeqRange& s, int v) {
   return (v < s.n_sink ? v : s.lo + v - s.n_sink) * kTile;
 }
-// blocks that share a call's tiles: no more than give each of their warps one
-__host__ __device__ inline long long used_blocks(long long tiles, int grid) {
-  const long long n = (tiles + kWarps - 1) / kWarps;
-  return n < grid ? n : grid;
+// runs that a call's work is cut into: one for each warp, but none of less than
+// kMinTiles tiles
+__host__ __device__ inline long long used_runs(long long tiles, int blocks) {
+  const long long n = (tiles + kMinTiles - 1) / kMinTiles;
+  return n < (long long)blocks * kWarps ? n : (long long)blocks * kWarps;
 }
 
 // ----------------------------------------------------------------- operands
@@ -443,13 +440,12 @@ __device__ __forceinline__ void copies_wait() {  // all but the last N groups of
 struct Cursor {
   int b, item, v;
   SeqRange sr;
-  long long first_unit;  // of the sequence
 };
-// A warp's next tiles, kUnit tokens apart.
+// Tiles in a row that a warp copies next.
 struct __align__(16) Strip {
   const int32_t* row;  // of the block table
   int token, left;     // of the tile looked up last; tiles after it
-  int row_in, len;     // row within a page's [head][token]; tokens of the sequence
+  int head_row, len;   // first row of the kv head in a page; tokens of the sequence
 };
 // Moves `n` tiles on.  Past the end of the list (lengths that changed under the
 // call): b = batch.
@@ -459,7 +455,6 @@ __device__ __forceinline__ void advance(const DecodeParams& p, int per_seq, Curs
     k.v -= k.sr.tiles;
     if (k.sr.tiles == 0 || ++k.item == per_seq) {
       k.item = 0;
-      k.first_unit += (long long)units_of(k.sr.tiles) * per_seq;
       if (++k.b < p.batch) k.sr = seq_range(p, k.b);
     }
   }
@@ -471,17 +466,17 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
   using S = DecShape<DQK, DV, NT>;
   constexpr int kThreads = kWarps * 32;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Cursor cursor[kWarps + 1];  // of each warp's copies; of the next piece
+  __shared__ Cursor copy_at[kWarps], work_at[kWarps];
   __shared__ Strip strip[kWarps];
-  __shared__ long long s_sum[2 * kWarps], s_tiles[2];
-  __shared__ long long s_before;  // units before sequence s_b
-  __shared__ int s_b;
+  __shared__ long long s_sum[2 * kWarps], s_tiles[kWarps][2], s_before[kWarps], s_bound[kWarps + 1];
+  __shared__ int s_b[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    s_b = p.batch;
-    s_before = s_tiles[0] = s_tiles[1] = 0;
+  asm volatile("griddepcontrol.launch_dependents;");  // (the join waits for the whole grid)
+  if (tid < kWarps) {
+    s_b[tid] = p.batch;
+    s_before[tid] = s_tiles[tid][0] = s_tiles[tid][1] = 0;
   }
-  // ---- the list of work, and this block's run of it
+  // ---- the list of work, and its warps' runs of it
   const int per_seq = p.c.heads * p.row_blocks;  // items of a sequence
   long long units = 0, tiles = 0;
   for (int b = tid; b < p.batch; b += kThreads) {
@@ -500,11 +495,11 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) all += s_sum[w], all_tiles += s_sum[kWarps + w];
   all *= per_seq;
-  const long long nblk = used_blocks(all_tiles * per_seq, gridDim.x);
-  if (blockIdx.x == 0 && tid == 0) p.total[0] = all, p.total[1] = nblk;
-  if ((long long)blockIdx.x >= nblk) return;
-  const long long first = all * blockIdx.x / nblk, last = all * (blockIdx.x + 1) / nblk;
-  // the sequence that holds unit `first`, and the tiles before `first` and `last`
+  const long long n_runs = used_runs(all_tiles * per_seq, gridDim.x);
+  const long long run0 = (long long)blockIdx.x * kWarps;
+  if (run0 >= n_runs) return;
+  if (tid <= kWarps) s_bound[tid] = all * min(run0 + tid, n_runs) / n_runs;  // of the runs
+  // the sequences that hold the runs' first units, and the tiles before both ends
   long long before_u = 0, before_t = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
     const int b = b0 + tid;
@@ -520,6 +515,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     if (lane == 31) s_sum[warp] = iu, s_sum[kWarps + warp] = it;
     __syncthreads();
     long long u0 = before_u - n, t0 = before_t - m;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) u0 += s_sum[w], t0 += s_sum[kWarps + w];
       before_u += s_sum[w];
@@ -527,73 +523,67 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     }
     u0 += iu;
     t0 += it;  // units and tiles before sequence b
-    if (first >= u0 && first < u0 + n) {
-      s_b = b;
-      s_before = u0;
-      s_tiles[0] = t0 + tiles_before(nt, first - u0);
+    for (int w = 0; w < kWarps && run0 + w < n_runs; ++w) {
+      const long long first = s_bound[w], last = s_bound[w + 1];
+      if (first >= u0 && first < u0 + n) {
+        s_b[w] = b;
+        s_before[w] = u0;
+        s_tiles[w][0] = t0 + tiles_before(nt, first - u0);
+      }
+      if (last > u0 && last <= u0 + n) s_tiles[w][1] = t0 + tiles_before(nt, last - u0);
     }
-    if (last > u0 && last <= u0 + n) s_tiles[1] = t0 + tiles_before(nt, last - u0);
-    __syncthreads();
-    if (before_u >= last) break;
+    if (before_u >= s_bound[kWarps]) break;
   }
-  const int first_b = s_b;
-  if (first_b >= p.batch) return;  // lengths that changed under the call
-  // tiles of the run; tile i is warp i % kWarps's
-  const int n_run = (int)min(max(s_tiles[1] - s_tiles[0], 0ll), (long long)INT32_MAX);
+  __syncthreads();
+  // From here on the warps go their own ways.
+  const long long run = run0 + warp;
+  const int first_b = s_b[warp];
+  const int n_run = (int)min(max(s_tiles[warp][1] - s_tiles[warp][0], 0ll), (long long)INT32_MAX);
+  if (run >= n_runs || first_b >= p.batch || n_run == 0) return;
 
   const int r = lane >> 2, c = lane & 3;
   uint8_t* ring = smem + warp * (S::kStages * S::kStage);
-  float* jo = reinterpret_cast<float*>(smem + S::kRing);             // [slot][row][DV]
-  float* stats = reinterpret_cast<float*>(smem + S::kRing + S::kJoin);
-  // ---- copies.  A warp feeds its own ring, across the pieces of the run, by
+  // ---- copies.  A warp feeds its own ring, across the items of its run, by
   // 16-byte asynchronous copies of all its lanes (a tile of one array is one
   // run of bytes); it waits for its own copies alone.  Where the next tile lies
   // is looked up one tile ahead.
-  const int left_total = n_run > warp ? (n_run - warp + kWarps - 1) / kWarps : 0;  // this warp's tiles
   const bool small = p.c.page_size < kTile;  // a tile spans two pages
   if (lane == 0) {
     Cursor k;
     k.b = first_b;
     k.sr = seq_range(p, first_b);
-    k.first_unit = s_before;
-    const long long u = first - s_before;
+    const long long u = s_bound[warp] - s_before[warp];
     const int n = max(units_of(k.sr.tiles), 1);
     k.item = (int)min(u / n, (long long)INT32_MAX);
     k.v = max((int)(u % n) - kItemCost, 0);
     if (k.item >= per_seq) k.b = p.batch;  // lengths that changed under the call
-    if (warp == 0) {
-      advance(p, per_seq, k, 0);
-      cursor[kWarps] = k;
-    }
-    advance(p, per_seq, k, warp);
-    cursor[warp] = k;
+    advance(p, per_seq, k, 0);
+    copy_at[warp] = work_at[warp] = k;
+    strip[warp].left = 0;
   }
-  __syncthreads();
-  if (lane == 0) strip[warp].left = 0;
   int next_page = 0;  // of the tile to copy next (its first one, where it spans two)
   auto look_up = [&]() {
     __syncwarp();
-    if (strip[warp].left == 0) {  // a new strip: tiles in a row, kWarps apart
+    if (strip[warp].left == 0) {
       __syncwarp();
       if (lane == 0) {
-        Cursor k = cursor[warp];
+        Cursor k = copy_at[warp];
         Strip t{p.table, 0, 1, 0, 0};  // no tile (lengths that changed under the call)
         if (k.b < p.batch) {
-          const int end = k.v < k.sr.n_sink ? k.sr.n_sink : k.sr.tiles;
+          const int stop = k.v < k.sr.n_sink ? k.sr.n_sink : k.sr.tiles;
           t.row = p.table + (int64_t)k.b * p.table_stride;
-          t.token = tile_token(k.sr, k.v) - kUnit;
-          t.left = (end - k.v + kWarps - 1) / kWarps;
-          // (kUnit is a multiple of the page size: the same for every tile)
-          t.row_in = (k.item / p.row_blocks) * p.c.page_size + (t.token & (p.c.page_size - 1));
+          t.token = tile_token(k.sr, k.v) - kTile;
+          t.left = stop - k.v;
+          t.head_row = (k.item / p.row_blocks) * p.c.page_size;
           t.len = k.sr.len;
-          advance(p, per_seq, k, t.left * kWarps);
-          cursor[warp] = k;
+          advance(p, per_seq, k, t.left);
+          copy_at[warp] = k;
         }
         strip[warp] = t;
       }
       __syncwarp();
     }
-    const int token = strip[warp].token + kUnit, left = strip[warp].left - 1;
+    const int token = strip[warp].token + kTile, left = strip[warp].left - 1;
     if (token < strip[warp].len) next_page = strip[warp].row[token >> p.c.page_shift];
     __syncwarp();
     if (lane == 0) strip[warp].token = token, strip[warp].left = left;
@@ -625,7 +615,8 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
   auto copy = [&](int s) {
     __syncwarp();
     uint8_t* st = ring + s * S::kStage;
-    const int token = strip[warp].token, row = strip[warp].row_in, len = strip[warp].len;
+    const int token = strip[warp].token, len = strip[warp].len;
+    const int row = strip[warp].head_row + (token & (p.c.page_size - 1));
     if (token >= len) return;
     bool bad = (unsigned)next_page >= (unsigned)p.c.num_pages;
     if (!bad) copy_rows(st, next_page, row, small ? 0 : 2);
@@ -638,30 +629,32 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     }
     if (bad && lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
   };
-  int used = 0, pieces = 0;
-  if (left_total > 0) look_up();
+  int used = 0;
+  look_up();
   for (int i = 0; i < S::kStages; ++i) {
-    if (i < left_total) {
+    if (i < n_run) {
       copy(i);
-      if (i + 1 < left_total) look_up();
+      if (i + 1 < n_run) look_up();
     }
     copies_end();
   }
-  for (int done_tiles = 0; done_tiles < n_run;) {
-    // the piece: every warp goes by the same copy of the lengths, so that all
-    // of them meet the same barriers
-    const Cursor k = cursor[kWarps];
+  for (int pieces = 0; used < n_run; ++pieces) {
+    // the piece: the run's tiles of one item
+    const Cursor k = work_at[warp];
     if (k.b >= p.batch) break;
     const SeqRange sr = k.sr;
-    const int b = k.b, item = k.item, v0 = k.v, v1 = min(sr.tiles, v0 + n_run - done_tiles);
+    const int b = k.b, item = k.item, v0 = k.v, v1 = min(sr.tiles, v0 + n_run - used);
     const int kvh = item / p.row_blocks, rb = item - kvh * p.row_blocks;
-    // this warp's first tile: the run's tile i is warp i % kWarps's
-    const int skew = (warp - done_tiles % kWarps + kWarps) % kWarps;
-    if (v0 == 0 && tid == 0) {  // where the item's tiles lie in the list, for the join
-      long long* info = reinterpret_cast<long long*>(p.info);
-      info[(int64_t)b * per_seq + item] = k.first_unit + (long long)item * units_of(sr.tiles) + kItemCost;
+    __syncwarp();
+    if (lane == 0) {
+      // the first and the last run that work on the item, for the join
+      int* info = p.info + 2 * ((int64_t)b * per_seq + item);
+      if (v0 == 0) info[0] = (int)run;
+      if (v1 == sr.tiles) info[1] = (int)run;
+      Cursor n = k;
+      advance(p, per_seq, n, v1 - v0);
+      work_at[warp] = n;
     }
-    done_tiles += v1 - v0;
 
     Piece<DQK, DV, NT> z;
     const int row0 = rb * S::kRows;
@@ -719,7 +712,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
 
     const int whole_hi = pos_lo - (kTile - 1);
     const int whole_lo = p.window_left < 0 ? 0 : pos_hi - p.window_left;
-    for (int v = v0 + skew; v < v1; v += kWarps) {
+    for (int v = v0; v < v1; ++v) {
       const int s = used % S::kStages;
       ++used;
       copies_wait<S::kStages - 1>();
@@ -732,17 +725,16 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
       else
         do_tile<false>(z, st, p, sr.len, row0, t0, r, c);
       __syncwarp();
-      if (used - 1 + S::kStages < left_total) {
+      if (used - 1 + S::kStages < n_run) {
         copy(s);
-        if (used + S::kStages < left_total) look_up();
+        if (used + S::kStages < n_run) look_up();
       }
       copies_end();
     }
 
-    // ---- join the warps
-    float* jm = stats + (pieces & 1) * (2 * kWarps * S::kRows);  // [warp][row]
-    float* jl = jm + kWarps * S::kRows;
-    ++pieces;
+    // ---- the result, or a partial one: O and the sum relative to the reference
+    const bool done = v0 == 0 && v1 == sr.tiles;
+    float* part = p.partial + (run * 2 + (v0 == 0 ? 1 : 0)) * S::kPart;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -752,159 +744,85 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int row = t * 8 + 2 * c + e;
-        if (r == 0) jm[warp * S::kRows + row] = -z.ref[t][e], jl[warp * S::kRows + row] = sum;
+        if (row0 + row >= p.rows) continue;
+#pragma unroll
+        for (int g = 0; g < S::GV; ++g) {
+          const float4 y = make_float4(z.o[t][g][0][e] * 16777216.0f, z.o[t][g][0][2 + e] * 1048576.0f,
+                                       z.o[t][g][1][e] * 16777216.0f, z.o[t][g][1][2 + e] * 1048576.0f);
+          if (done)
+            write_row<BF16>(p, b, kvh, row0 + row, 8 * g + r, y, -z.ref[t][e], sum);
+          else
+            *reinterpret_cast<float4*>(part + row * DV + 32 * g + 4 * r) = y;
+        }
+        if (!done && r == 0) {
+          part[S::kRows * DV + row] = -z.ref[t][e];
+          part[S::kRows * (DV + 1) + row] = sum;
+        }
       }
-    __syncthreads();
-    if (tid == 0) {  // (read by all before this barrier, and again after the next)
-      Cursor n = k;
-      advance(p, per_seq, n, v1 - v0);
-      cursor[kWarps] = n;
-    }
-    #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {  // to the common maximum
-        const int row = t * 8 + 2 * c + e;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, jm[w * S::kRows + row]);
-        const float f = ex2(-z.ref[t][e] - mx) * 16777216.0f;
-#pragma unroll
-        for (int g = 0; g < S::GV; ++g)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) z.o[t][g][h][e] *= f, z.o[t][g][h][2 + e] *= f * 0.0625f;
-      }
-#pragma unroll
-    for (int round = 0; round * kSlots < kWarps; ++round) {
-      if (warp / kSlots == round) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int g = 0; g < S::GV; ++g) {
-              float4* dst = reinterpret_cast<float4*>(
-                  jo + ((warp % kSlots) * S::kRows + t * 8 + 2 * c + e) * DV + 32 * g + 4 * r);
-              float4 y = make_float4(z.o[t][g][0][e], z.o[t][g][0][2 + e], z.o[t][g][1][e], z.o[t][g][1][2 + e]);
-              if (round > 0) {
-                const float4 u = *dst;
-                y.x += u.x, y.y += u.y, y.z += u.z, y.w += u.w;
-              }
-              *dst = y;
-            }
-      }
-      __syncthreads();
-    }
-    const bool done = v0 == 0 && v1 == sr.tiles;  // the whole item: no partial result
-    float* part = p.partial + ((int64_t)blockIdx.x * 2 + (v0 == 0 ? 1 : 0)) * (S::kRows * (DV + 2));
-    for (int i = tid; i < S::kRows * (DV / 4); i += kWarps * 32) {
-      const int row = i / (DV / 4), d4 = i % (DV / 4);
-      float mx = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, jm[w * S::kRows + row]);
-      float sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        sum = fmaf(jl[w * S::kRows + row], ex2(jm[w * S::kRows + row] - mx), sum);
-      }
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < (kSlots < kWarps ? kSlots : kWarps); ++w) {
-        const float4 y = *reinterpret_cast<const float4*>(jo + (w * S::kRows + row) * DV + d4 * 4);
-        acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
-      }
-      if (!done) {
-        *reinterpret_cast<float4*>(part + row * DV + d4 * 4) = acc;
-        if (d4 == 0) part[S::kRows * DV + row] = mx, part[S::kRows * (DV + 1) + row] = sum;
-      } else if (row0 + row < p.rows) {
-        write_row<BF16>(p, b, kvh, row0 + row, d4, acc, mx, sum);
-      }
-    }
   }
   copies_wait<0>();
 }
 
 // ----------------------------------------------------------------- the join
-// One block for each item.  Items without a visible key get O = 0 and LSE =
-// -inf here; items that one block finished are left alone.  The pieces of the
-// others (in the order of the blocks) are shared out over the 8 warps, whose
-// sums are then added in warp order.
+// One block for each query row of an item.  Rows without a visible key get O =
+// 0 and LSE = -inf here; items that one warp finished are left alone.  The
+// pieces of the others (in the order of the runs) are shared out over the
+// block's warps, whose sums are then added in warp order.
 template <bool BF16, int DV, int ROWS>
 __global__ void __launch_bounds__(256) attn_kv_join_kernel(const __grid_constant__ DecodeParams p,
-                                                           int blocks) {
-  __shared__ float sm_m[8][ROWS], sm_l[8][ROWS];
-  extern __shared__ float so[];  // [8][ROWS * DV]
+                                                           int runs) {
+  constexpr int kLanes = DV / 4, kGroups = 256 / kLanes;  // lanes of a row, rows in flight
+  constexpr int kPart = ROWS * (DV + 2);
+  __shared__ float sm_m[8], sm_l[kGroups];
+  __shared__ float4 sm_o[kGroups][kLanes];
+  const int rows = min(ROWS, p.rows);
   const int per_seq = p.c.heads * p.row_blocks;
-  const int b = (int)(blockIdx.x / per_seq), item = (int)(blockIdx.x % per_seq);
-  const int kvh = item / p.row_blocks, row0 = (item - kvh * p.row_blocks) * ROWS;
+  const int row = (int)(blockIdx.x % rows), at = (int)(blockIdx.x / rows);
+  const int b = at / per_seq, item = at - b * per_seq;
+  const int kvh = item / p.row_blocks, row_all = (item - kvh * p.row_blocks) * ROWS + row;
+  if (row_all >= p.rows) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nu = seq_range(p, b).tiles;
-  int k0 = 0, np = 0;
-  if (nu > 0) {
-    const long long all = p.total[0], nblk = p.total[1];
-    const long long a = reinterpret_cast<const long long*>(p.info)[blockIdx.x], z = a + nu - 1;
-    // block k has units [all k / nblk, all (k + 1) / nblk): the block of unit u
-    auto block_of = [&](long long u) {
-      long long k = u * nblk / all;
-      while (k > 0 && all * k / nblk > u) --k;
-      while (all * (k + 1) / nblk <= u) ++k;
-      return (int)k;
-    };
-    if (all <= 0 || nblk <= 0 || nblk > blocks || a < 0 || z >= all) return;
-    k0 = block_of(a);
-    np = block_of(z) - k0 + 1;
-    if (np == 1) return;
+  const int nt = seq_range(p, b).tiles;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (nt == 0) {
+    if (tid < kLanes) write_row<BF16>(p, b, kvh, row_all, tid, make_float4(0.f, 0.f, 0.f, 0.f), 0.0f, 0.0f);
+    return;
   }
-  constexpr int kFloats = ROWS * (DV + 2);
-  const float* part = p.partial;
-  auto piece = [&](int i) { return part + ((int64_t)(k0 + i) * 2 + (i == 0 ? 1 : 0)) * kFloats; };
-  for (int row = warp; row < ROWS; row += 8) {  // the row's maximum over all pieces
-    float mx = -INFINITY;
-    for (int i = lane; i < np; i += 32) mx = fmaxf(mx, piece(i)[ROWS * DV + row]);
+  const int k0 = p.info[2 * (int64_t)at], np = p.info[2 * (int64_t)at + 1] - k0 + 1;
+  // (np < 2: one run finished it; out of range: lengths that changed under the call)
+  if (np < 2 || k0 < 0 || k0 + np > runs) return;
+  auto piece = [&](int i) { return p.partial + ((int64_t)(k0 + i) * 2 + (i == 0 ? 1 : 0)) * kPart; };
+  float mx = -INFINITY;  // the row's largest reference
+  for (int i = tid; i < np; i += 256) mx = fmaxf(mx, piece(i)[ROWS * DV + row]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0) sm_m[0][row] = mx;
-  }
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) sm_m[warp] = mx;
   __syncthreads();
-  constexpr int kVec = ROWS * DV / 4 / 32;  // float4 of a lane
-  float4 acc[kVec];
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.0f;  // lane < ROWS: of row `lane`
-  for (int i = warp; i < np; i += 8) {
+  for (int w = 0; w < 8; ++w) mx = fmaxf(mx, sm_m[w]);
+  const int g = tid / kLanes, d4 = tid % kLanes;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.0f;
+#pragma unroll 4
+  for (int i = g; i < np; i += kGroups) {
     const float* pc = piece(i);
-    float f = 0.0f;
-    if (lane < ROWS) {
-      const float mx = sm_m[0][lane];
-      f = ex2(pc[ROWS * DV + lane] - mx);
-      sum = fmaf(pc[ROWS * (DV + 1) + lane], f, sum);
-    }
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      const float4 y = *reinterpret_cast<const float4*>(pc + (j * 32 + lane) * 4);
-      const float fr = __shfl_sync(0xffffffffu, f, (j * 32 + lane) * 4 / DV);
-      acc[j].x = fmaf(y.x, fr, acc[j].x), acc[j].y = fmaf(y.y, fr, acc[j].y);
-      acc[j].z = fmaf(y.z, fr, acc[j].z), acc[j].w = fmaf(y.w, fr, acc[j].w);
-    }
+    const float4 y = *reinterpret_cast<const float4*>(pc + row * DV + d4 * 4);
+    const float f = ex2(pc[ROWS * DV + row] - mx);
+    sum = fmaf(pc[ROWS * (DV + 1) + row], f, sum);
+    acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y);
+    acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
   }
-#pragma unroll
-  for (int j = 0; j < kVec; ++j)
-    *reinterpret_cast<float4*>(so + warp * (ROWS * DV) + (j * 32 + lane) * 4) = acc[j];
-  if (lane < ROWS) sm_l[warp][lane] = sum;
+  sm_o[g][d4] = acc;
+  if (d4 == 0) sm_l[g] = sum;
   __syncthreads();
-  for (int i = tid; i < ROWS * DV / 4; i += 256) {
-    const int row = i * 4 / DV, d4 = i % (DV / 4);
-    if (row0 + row >= p.rows) continue;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    float s = 0.0f;
+  if (g > 0) return;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const float4 z = *reinterpret_cast<const float4*>(so + w * (ROWS * DV) + i * 4);
-      y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
-      s += sm_l[w][row];
-    }
-    write_row<BF16>(p, b, kvh, row0 + row, d4, y, sm_m[0][row], s);
+  for (int k = 1; k < kGroups; ++k) {
+    const float4 y = sm_o[k][d4];
+    acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
+    sum += sm_l[k];
   }
+  write_row<BF16>(p, b, kvh, row_all, d4, acc, mx, sum);
 }
 
 // ----------------------------------------------------------------- launches
@@ -914,13 +832,13 @@ int decode_col_tiles(int rows, int d_v) { return rows > 8 && d_v < 256 ? 2 : 1; 
 int decode_blocks(const DecodeParams& p, int num_sms) {
   // no more than the longest possible list of tiles keeps busy
   const int64_t tiles = (((int64_t)p.cols << p.c.page_shift) + kTile - 1) / kTile;
-  const int per_sm = light(p.c.d_v, decode_col_tiles(p.rows, p.c.d_v)) ? 2 : 1;
-  return (int)std::max<int64_t>(
-      used_blocks(tiles * p.batch * p.c.heads * p.row_blocks, num_sms * per_sm), 1);
+  const int most = num_sms * (light(p.c.d_v, decode_col_tiles(p.rows, p.c.d_v)) ? 4 : 2);
+  const int64_t runs = used_runs(tiles * p.batch * p.c.heads * p.row_blocks, most);
+  return (int)std::max<int64_t>((runs + kWarps - 1) / kWarps, 1);
 }
 
-size_t decode_partial_floats(int rows_per_block, int d_v) {
-  return (size_t)rows_per_block * (d_v + 2);
+size_t decode_partial_floats(int blocks, int rows_per_block, int d_v) {
+  return (size_t)blocks * kWarps * 2 * rows_per_block * (d_v + 2);
 }
 
 namespace {
@@ -935,15 +853,22 @@ cudaError_t dec_launch(const DecodeParams& p, int blocks, cudaStream_t st) {
   using S = DecShape<DQK, DV, NT>;
   auto* main = attn_kv_decode_kernel<BF16, DQK, DV, NT>;
   auto* join = attn_kv_join_kernel<BF16, DV, 8 * NT>;
-  const int join_smem = 8 * 8 * NT * DV * 4;
-  cudaError_t e = allow_smem(main, S::kSmem);
-  if (e == cudaSuccess) e = allow_smem(join, join_smem);
+  cudaError_t e = allow_smem(main, S::kRing);
   if (e != cudaSuccess) return e;
-  main<<<blocks, kWarps * 32, S::kSmem, st>>>(p);
+  main<<<blocks, kWarps * 32, S::kRing, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  join<<<p.batch * p.c.heads * p.row_blocks, 256, join_smem, st>>>(p, blocks);
-  return cudaGetLastError();
+  // the join is launched while the first kernel runs, and waits for its end
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.batch * p.c.heads * p.row_blocks * std::min(8 * NT, p.rows)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join, p, blocks * kWarps);
 }
 
 template <bool BF16, int NT>
