@@ -94,12 +94,14 @@ struct DecodeParams {
   float scale_log2;
   int o_f32;
   int* info;       // per item: the first and the last run that work on it
+  int* ends;       // per run: the item of others that it ends, or -1
   float* partial;  // per run: two pieces of items
   int* status;
 };
 // Tiles of query columns (8 each) that one block of a call takes.
 int decode_col_tiles(int rows, int d_v);
 int decode_blocks(const DecodeParams& p, int num_sms);
+size_t decode_runs(int blocks);
 size_t decode_partial_floats(int blocks, int rows_per_block, int d_v);
 cudaError_t launch_kv4_decode(const DecodeParams& p, bool bf16, int blocks, cudaStream_t st);
 

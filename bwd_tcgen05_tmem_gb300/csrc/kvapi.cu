@@ -540,17 +540,17 @@ attn_status_t check_decode(const attn_kv4_decode_params_t* p, const attn_kv4_cac
   return ATTN_OK;
 }
 
-// [8 bytes an item: its first and last run][two partial results a run]
+// [two ints for each item][one for each run][two partial results a run]
 struct DecodeLayout {
-  size_t info, partial, total;
+  size_t ends, partial, total;
   int blocks;
 };
 DecodeLayout decode_layout(const attn::DecodeParams& kp) {
   DecodeLayout l;
   const size_t items = (size_t)kp.batch * kp.c.heads * kp.row_blocks;
   l.blocks = attn::decode_blocks(kp, attn::num_sms());
-  l.info = 0;
-  l.partial = up256(items * 8) + 256;
+  l.ends = up256(items * 8);
+  l.partial = l.ends + up256(attn::decode_runs(l.blocks) * 4);
   const int rows = 8 * attn::decode_col_tiles(kp.rows, kp.c.d_v);
   l.total = l.partial + attn::decode_partial_floats(l.blocks, rows, kp.c.d_v) * 4;
   return l;
@@ -623,7 +623,8 @@ attn_status_t attn_kv_decode(const attn_kv4_decode_params_t* p, const attn_kv4_c
   kp.seq_lens = seq_lens;
   kp.q_b = p->stride_q[0], kp.q_t = p->stride_q[1], kp.q_h = p->stride_q[2];
   kp.o_b = p->stride_o[0], kp.o_t = p->stride_o[1], kp.o_h = p->stride_o[2];
-  kp.info = (int*)((char*)ws + l.info);
+  kp.info = (int*)ws;
+  kp.ends = (int*)((char*)ws + l.ends);
   kp.partial = (float*)((char*)ws + l.partial);
   kp.status = status;
   const cudaError_t e =

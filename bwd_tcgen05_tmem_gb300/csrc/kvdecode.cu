@@ -97,19 +97,25 @@ __device__ __forceinline__ SeqRange seq_range(const DecodeParams& p, int b) {
 }
 // An item's share of the list of work: its tiles, and kItemCost for what a block
 // does once for each item (q, the join of the warps).
-__host__ __device__ __forceinline__ int units_of(int tiles) { return tiles ? tiles + kItemCost : 0; }
+__device__ __forceinline__ int units_of(int tiles) { return tiles ? tiles + kItemCost : 0; }
+// u / n, u >= 0 (64-bit quotients are slow)
+__device__ __forceinline__ long long quotient(long long u, int n) {
+  return u <= INT32_MAX ? (int)u / n : u / n;
+}
 // tiles before position u of a sequence's items
 __device__ __forceinline__ long long tiles_before(int tiles, long long u) {
   if (tiles == 0) return 0;
-  const int n = units_of(tiles), x = (int)(u % n) - kItemCost;
-  return u / n * tiles + (x > 0 ? x : 0);
+  const int n = units_of(tiles);
+  const long long item = quotient(u, n);
+  const int x = (int)(u - item * n) - kItemCost;
+  return item * tiles + (x > 0 ? x : 0);
 }
 // first token of the v-th tile
 __device__ __forceinline__ int tile_token(const SeqRange& s, int v) {
   return (v < s.n_sink ? v : s.lo + v - s.n_sink) * kTile;
 }
-// runs that a call's work is cut into: one for each warp, but none of less than
-// kMinTiles tiles
+// Runs that a call's work is cut into: one for each warp, but none of less than
+// kMinTiles tiles.
 __host__ __device__ inline long long used_runs(long long tiles, int blocks) {
   const long long n = (tiles + kMinTiles - 1) / kMinTiles;
   return n < (long long)blocks * kWarps ? n : (long long)blocks * kWarps;
@@ -468,7 +474,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Cursor copy_at[kWarps], work_at[kWarps];
   __shared__ Strip strip[kWarps];
-  __shared__ long long s_sum[2 * kWarps], s_tiles[kWarps][2], s_before[kWarps], s_bound[kWarps + 1];
+  __shared__ long long s_sum[2 * kWarps], s_tiles[kWarps][2], s_before[kWarps];
   __shared__ int s_b[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;");  // (the join waits for the whole grid)
@@ -476,70 +482,73 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     s_b[tid] = p.batch;
     s_before[tid] = s_tiles[tid][0] = s_tiles[tid][1] = 0;
   }
-  // ---- the list of work, and its warps' runs of it
+  // ---- the list of work, and its warps' runs of it.  Each thread takes the
+  // sequences b = tid, tid + kThreads, ..: units and tiles are added up over
+  // chunks of kThreads sequences, first all of them for the totals (where there
+  // are more than one chunk), then as prefix sums.
   const int per_seq = p.c.heads * p.row_blocks;  // items of a sequence
-  long long units = 0, tiles = 0;
-  for (int b = tid; b < p.batch; b += kThreads) {
-    const int n = seq_range(p, b).tiles;
-    units += units_of(n);
-    tiles += n;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    units += __shfl_xor_sync(0xffffffffu, units, o);
-    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-  }
-  if (lane == 0) s_sum[warp] = units, s_sum[kWarps + warp] = tiles;
-  __syncthreads();
-  long long all = 0, all_tiles = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) all += s_sum[w], all_tiles += s_sum[kWarps + w];
-  all *= per_seq;
-  const long long n_runs = used_runs(all_tiles * per_seq, gridDim.x);
-  const long long run0 = (long long)blockIdx.x * kWarps;
-  if (run0 >= n_runs) return;
-  if (tid <= kWarps) s_bound[tid] = all * min(run0 + tid, n_runs) / n_runs;  // of the runs
-  // the sequences that hold the runs' first units, and the tiles before both ends
-  long long before_u = 0, before_t = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-    const int b = b0 + tid;
-    const int nt = b < p.batch ? seq_range(p, b).tiles : 0;
-    const long long n = (long long)units_of(nt) * per_seq, m = (long long)nt * per_seq;
-    long long iu = n, it = m;
+  long long before_u = 0, before_t = 0;  // of the chunks so far
+  int nt = 0;                      // this thread's sequence of the chunk
+  long long u0 = 0, t0 = 0;        // units and tiles before it (of one item of each sequence)
+  auto chunk = [&](int b0) {
+    nt = b0 + tid < p.batch ? seq_range(p, b0 + tid).tiles : 0;
+    const int mine = units_of(nt);
+    long long ju = mine, jt = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, iu, o), y = __shfl_up_sync(0xffffffffu, it, o);
-      if (lane >= o) iu += x, it += y;
+      const long long x = __shfl_up_sync(0xffffffffu, ju, o), y = __shfl_up_sync(0xffffffffu, jt, o);
+      if (lane >= o) ju += x, jt += y;
     }
     __syncthreads();
-    if (lane == 31) s_sum[warp] = iu, s_sum[kWarps + warp] = it;
+    if (lane == 31) s_sum[warp] = ju, s_sum[kWarps + warp] = jt;
     __syncthreads();
-    long long u0 = before_u - n, t0 = before_t - m;
+    u0 = before_u + ju - mine;
+    t0 = before_t + jt - nt;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) u0 += s_sum[w], t0 += s_sum[kWarps + w];
       before_u += s_sum[w];
       before_t += s_sum[kWarps + w];
     }
-    u0 += iu;
-    t0 += it;  // units and tiles before sequence b
+  };
+  chunk(0);
+  for (int b0 = kThreads; b0 < p.batch; b0 += kThreads) chunk(b0);
+  const long long all = before_u * per_seq;
+  const long long n_runs = used_runs(before_t * per_seq, gridDim.x);
+  const long long run0 = (long long)blockIdx.x * kWarps;
+  // blocks without a run: nothing to join there
+  if (tid < kWarps && run0 + tid >= n_runs) p.ends[run0 + tid] = -1;
+  if (run0 >= n_runs) return;
+  // run k has units [bound(k), bound(k + 1))
+  const long long each = quotient(all, (int)n_runs), more = all - each * n_runs;
+  auto bound = [&](long long k) { return each * k + min(k, more); };
+  // the sequences that hold the runs' first units, and the tiles before both ends
+  if (p.batch > kThreads) before_u = before_t = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+    if (p.batch > kThreads) chunk(b0);
+    const long long n = (long long)units_of(nt) * per_seq, first_u = u0 * per_seq;
     for (int w = 0; w < kWarps && run0 + w < n_runs; ++w) {
-      const long long first = s_bound[w], last = s_bound[w + 1];
-      if (first >= u0 && first < u0 + n) {
-        s_b[w] = b;
-        s_before[w] = u0;
-        s_tiles[w][0] = t0 + tiles_before(nt, first - u0);
+      const long long first = bound(run0 + w), last = bound(run0 + w + 1);
+      if (first >= first_u && first < first_u + n) {
+        s_b[w] = b0 + tid;
+        s_before[w] = first_u;
+        s_tiles[w][0] = t0 * per_seq + tiles_before(nt, first - first_u);
       }
-      if (last > u0 && last <= u0 + n) s_tiles[w][1] = t0 + tiles_before(nt, last - u0);
+      if (last > first_u && last <= first_u + n)
+        s_tiles[w][1] = t0 * per_seq + tiles_before(nt, last - first_u);
     }
-    if (before_u >= s_bound[kWarps]) break;
+    if (before_u * per_seq >= bound(min(run0 + kWarps, n_runs))) break;
   }
   __syncthreads();
   // From here on the warps go their own ways.
   const long long run = run0 + warp;
   const int first_b = s_b[warp];
   const int n_run = (int)min(max(s_tiles[warp][1] - s_tiles[warp][0], 0ll), (long long)INT32_MAX);
-  if (run >= n_runs || first_b >= p.batch || n_run == 0) return;
+  if (run >= n_runs) return;
+  if (first_b >= p.batch || n_run == 0) {
+    if (lane == 0) p.ends[run] = -1;
+    return;
+  }
 
   const int r = lane >> 2, c = lane & 3;
   uint8_t* ring = smem + warp * (S::kStages * S::kStage);
@@ -552,10 +561,11 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     Cursor k;
     k.b = first_b;
     k.sr = seq_range(p, first_b);
-    const long long u = s_bound[warp] - s_before[warp];
+    const long long u = bound(run) - s_before[warp];
     const int n = max(units_of(k.sr.tiles), 1);
-    k.item = (int)min(u / n, (long long)INT32_MAX);
-    k.v = max((int)(u % n) - kItemCost, 0);
+    const long long i = quotient(u, n);
+    k.item = (int)min(i, (long long)INT32_MAX);
+    k.v = max((int)(u - i * n) - kItemCost, 0);
     if (k.item >= per_seq) k.b = p.batch;  // lengths that changed under the call
     advance(p, per_seq, k, 0);
     copy_at[warp] = work_at[warp] = k;
@@ -641,16 +651,21 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
   for (int pieces = 0; used < n_run; ++pieces) {
     // the piece: the run's tiles of one item
     const Cursor k = work_at[warp];
-    if (k.b >= p.batch) break;
+    if (k.b >= p.batch) {  // lengths that changed under the call
+      if (pieces == 0 && lane == 0) p.ends[run] = -1;
+      break;
+    }
     const SeqRange sr = k.sr;
     const int b = k.b, item = k.item, v0 = k.v, v1 = min(sr.tiles, v0 + n_run - used);
     const int kvh = item / p.row_blocks, rb = item - kvh * p.row_blocks;
     __syncwarp();
     if (lane == 0) {
-      // the first and the last run that work on the item, for the join
+      // for the join: the first and the last run that work on an item, and
+      // the items that a run ends for others
       int* info = p.info + 2 * ((int64_t)b * per_seq + item);
       if (v0 == 0) info[0] = (int)run;
       if (v1 == sr.tiles) info[1] = (int)run;
+      if (pieces == 0) p.ends[run] = v0 > 0 && v1 == sr.tiles ? (int)(b * per_seq + item) : -1;
       Cursor n = k;
       advance(p, per_seq, n, v1 - v0);
       work_at[warp] = n;
@@ -764,65 +779,149 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
 }
 
 // ----------------------------------------------------------------- the join
-// One block for each query row of an item.  Rows without a visible key get O =
-// 0 and LSE = -inf here; items that one warp finished are left alone.  The
-// pieces of the others (in the order of the runs) are shared out over the
-// block's warps, whose sums are then added in warp order.
+// A thread takes four dims of a row.  Rows of sequences without a visible key
+// get O = 0 and LSE = -inf here.
+//
+// By item: a block for each row of each item, whose pieces are shared out over
+// groups of threads; the groups' sums are added in their order.  It spreads the
+// work best where few items are cut into many pieces.  By run: 128 threads look
+// at a run, and join the item that it ends for others (the whole block does
+// where that has many pieces): no more blocks than the runs need, however many
+// items there are.  Measured, whole call: 128 items (16 x 32K tokens) by item
+// 131 us, by run 137 us; 4096 items (512 x 1K) by item 170 us, by run 148 us.
+constexpr int kByItemPieces = 4;  // of an item on average: from there on by item
+constexpr int kTeamPieces = 8;    // joined by one team after another
+constexpr int kByItemThreads = 256, kTeam = 128, kByRunThreads = kTeam * kWarps;
+
+// Adds a piece of a row (reference m, sum l, O y) to what a thread holds.
+__device__ __forceinline__ void add_piece(float4& acc, float& sum, float& mx, float m, float l,
+                                          const float4& y) {
+  const float to = fmaxf(mx, m), f = ex2(m - to), a = mx == -INFINITY ? 0.0f : ex2(mx - to);
+  mx = to;
+  sum = fmaf(sum, a, l * f);
+  acc.x = fmaf(acc.x, a, y.x * f), acc.y = fmaf(acc.y, a, y.y * f);
+  acc.z = fmaf(acc.z, a, y.z * f), acc.w = fmaf(acc.w, a, y.w * f);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void empty_rows(const DecodeParams& p, int threads) {
+  const int q = p.c.d_v / 4;
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+    if (seq_range(p, b).tiles) continue;
+    for (int i = threadIdx.x; i < p.c.heads * p.rows * q; i += threads) {
+      const int row = i / q, kvh = row / p.rows;
+      write_row<BF16>(p, b, kvh, row - kvh * p.rows, i - row * q, make_float4(0.f, 0.f, 0.f, 0.f), 0.0f, 0.0f);
+    }
+  }
+}
+
 template <bool BF16, int DV, int ROWS>
-__global__ void __launch_bounds__(256) attn_kv_join_kernel(const __grid_constant__ DecodeParams p,
-                                                           int runs) {
-  constexpr int kLanes = DV / 4, kGroups = 256 / kLanes;  // lanes of a row, rows in flight
-  constexpr int kPart = ROWS * (DV + 2);
-  __shared__ float sm_m[8], sm_l[kGroups];
+__global__ void __launch_bounds__(kByItemThreads) attn_kv_join_items_kernel(
+    const __grid_constant__ DecodeParams p, int runs) {
+  constexpr int kPart = ROWS * (DV + 2), kLanes = DV / 4, kGroups = kByItemThreads / kLanes;
   __shared__ float4 sm_o[kGroups][kLanes];
+  __shared__ float sm_l[kGroups], sm_m[kGroups];
+  const int per_seq = p.c.heads * p.row_blocks, tid = threadIdx.x;
   const int rows = min(ROWS, p.rows);
-  const int per_seq = p.c.heads * p.row_blocks;
-  const int row = (int)(blockIdx.x % rows), at = (int)(blockIdx.x / rows);
+  const int at = blockIdx.x / rows, row = blockIdx.x - at * rows;
   const int b = at / per_seq, item = at - b * per_seq;
   const int kvh = item / p.row_blocks, row_all = (item - kvh * p.row_blocks) * ROWS + row;
-  if (row_all >= p.rows) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nt = seq_range(p, b).tiles;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (nt == 0) {
-    if (tid < kLanes) write_row<BF16>(p, b, kvh, row_all, tid, make_float4(0.f, 0.f, 0.f, 0.f), 0.0f, 0.0f);
-    return;
-  }
+  empty_rows<BF16>(p, kByItemThreads);
+  if (row_all >= p.rows || seq_range(p, b).tiles == 0) return;
   const int k0 = p.info[2 * (int64_t)at], np = p.info[2 * (int64_t)at + 1] - k0 + 1;
-  // (np < 2: one run finished it; out of range: lengths that changed under the call)
+  // (np 1: one run finished it; out of range: lengths that changed under the call)
   if (np < 2 || k0 < 0 || k0 + np > runs) return;
-  auto piece = [&](int i) { return p.partial + ((int64_t)(k0 + i) * 2 + (i == 0 ? 1 : 0)) * kPart; };
-  float mx = -INFINITY;  // the row's largest reference
-  for (int i = tid; i < np; i += 256) mx = fmaxf(mx, piece(i)[ROWS * DV + row]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) sm_m[warp] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) mx = fmaxf(mx, sm_m[w]);
   const int g = tid / kLanes, d4 = tid % kLanes;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.0f;
+  float sum = 0.0f, mx = -INFINITY;
 #pragma unroll 4
   for (int i = g; i < np; i += kGroups) {
-    const float* pc = piece(i);
-    const float4 y = *reinterpret_cast<const float4*>(pc + row * DV + d4 * 4);
-    const float f = ex2(pc[ROWS * DV + row] - mx);
-    sum = fmaf(pc[ROWS * (DV + 1) + row], f, sum);
-    acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y);
-    acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
+    const float* pc = p.partial + ((int64_t)(k0 + i) * 2 + (i == 0 ? 1 : 0)) * kPart;
+    add_piece(acc, sum, mx, pc[ROWS * DV + row], pc[ROWS * (DV + 1) + row],
+              *reinterpret_cast<const float4*>(pc + row * DV + d4 * 4));
   }
   sm_o[g][d4] = acc;
-  if (d4 == 0) sm_l[g] = sum;
+  if (d4 == 0) sm_l[g] = sum, sm_m[g] = mx;
   __syncthreads();
   if (g > 0) return;
 #pragma unroll
-  for (int k = 1; k < kGroups; ++k) {
-    const float4 y = sm_o[k][d4];
-    acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
-    sum += sm_l[k];
-  }
+  for (int k = 1; k < kGroups; ++k)
+    if (k < np) add_piece(acc, sum, mx, sm_m[k], sm_l[k], sm_o[k][d4]);
   write_row<BF16>(p, b, kvh, row_all, d4, acc, mx, sum);
+}
+
+template <bool BF16, int DV, int ROWS>
+__global__ void __launch_bounds__(kByRunThreads) attn_kv_join_runs_kernel(
+    const __grid_constant__ DecodeParams p) {
+  constexpr int kPart = ROWS * (DV + 2), kLanes = DV / 4, kEach = ROWS * kLanes / kTeam;
+  __shared__ float4 sm_o[kByRunThreads];
+  __shared__ float sm_l[kByRunThreads], sm_m[kByRunThreads];
+  __shared__ int s_at[kWarps], s_k0[kWarps], s_np[kWarps];
+  const int per_seq = p.c.heads * p.row_blocks, tid = threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  empty_rows<BF16>(p, kByRunThreads);
+  if (tid < kWarps) {
+    const int run = blockIdx.x * kWarps + tid, at = p.ends[run];
+    const int k0 = at < 0 ? 0 : p.info[2 * (int64_t)at];
+    s_at[tid] = at;
+    s_k0[tid] = k0;
+    s_np[tid] = at < 0 || k0 < 0 || k0 >= run ? 0 : run - k0 + 1;
+  }
+  __syncthreads();
+  auto piece = [&](int k0, int i) { return p.partial + ((int64_t)(k0 + i) * 2 + (i == 0 ? 1 : 0)) * kPart; };
+  // ---- items of many pieces: by the whole block, in groups
+  for (int w = 0; w < kWarps; ++w) {
+    const int np = s_np[w];
+    if (np <= kTeamPieces) continue;
+    const int b = s_at[w] / per_seq, item = s_at[w] - b * per_seq;
+    const int kvh = item / p.row_blocks, row0 = (item - kvh * p.row_blocks) * ROWS;
+    const int need = min(ROWS, p.rows - row0) * kLanes, groups = kByRunThreads / need;
+    const int g = tid / need, i0 = tid - g * need, row = i0 / kLanes, d4 = i0 % kLanes;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.0f, mx = -INFINITY;
+    if (g < groups) {
+#pragma unroll 4
+      for (int i = g; i < np; i += groups) {
+        const float* pc = piece(s_k0[w], i);
+        add_piece(acc, sum, mx, pc[ROWS * DV + row], pc[ROWS * (DV + 1) + row],
+                  *reinterpret_cast<const float4*>(pc + row * DV + d4 * 4));
+      }
+    }
+    __syncthreads();
+    sm_o[tid] = acc;
+    sm_l[tid] = sum;
+    sm_m[tid] = mx;
+    __syncthreads();
+    if (g > 0) continue;
+    for (int k = 1; k < groups; ++k)
+      add_piece(acc, sum, mx, sm_m[k * need + tid], sm_l[k * need + tid], sm_o[k * need + tid]);
+    write_row<BF16>(p, b, kvh, row0 + row, d4, acc, mx, sum);
+  }
+  // ---- the others: by a team each
+  const int w = tid / kTeam, t = tid % kTeam, np = s_np[w];
+  if (np < 2 || np > kTeamPieces) return;
+  const int b = s_at[w] / per_seq, item = s_at[w] - b * per_seq;
+  const int kvh = item / p.row_blocks, row0 = (item - kvh * p.row_blocks) * ROWS;
+  float4 acc[kEach];
+  float sum[kEach], mx[kEach];
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f), sum[j] = 0.0f, mx[j] = -INFINITY;
+#pragma unroll 2
+  for (int i = 0; i < np; ++i) {
+    const float* pc = piece(s_k0[w], i);
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {  // (rows past the last one are read too: they lie in the workspace)
+      const int at4 = j * kTeam + t, row = at4 / kLanes;
+      add_piece(acc[j], sum[j], mx[j], pc[ROWS * DV + row], pc[ROWS * (DV + 1) + row],
+                *reinterpret_cast<const float4*>(pc + at4 * 4));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int at4 = j * kTeam + t, row = at4 / kLanes;
+    if (row0 + row < p.rows) write_row<BF16>(p, b, kvh, row0 + row, at4 % kLanes, acc[j], mx[j], sum[j]);
+  }
 }
 
 // ----------------------------------------------------------------- launches
@@ -836,6 +935,8 @@ int decode_blocks(const DecodeParams& p, int num_sms) {
   const int64_t runs = used_runs(tiles * p.batch * p.c.heads * p.row_blocks, most);
   return (int)std::max<int64_t>((runs + kWarps - 1) / kWarps, 1);
 }
+
+size_t decode_runs(int blocks) { return (size_t)blocks * kWarps; }
 
 size_t decode_partial_floats(int blocks, int rows_per_block, int d_v) {
   return (size_t)blocks * kWarps * 2 * rows_per_block * (d_v + 2);
@@ -852,7 +953,6 @@ template <bool BF16, int DQK, int DV, int NT>
 cudaError_t dec_launch(const DecodeParams& p, int blocks, cudaStream_t st) {
   using S = DecShape<DQK, DV, NT>;
   auto* main = attn_kv_decode_kernel<BF16, DQK, DV, NT>;
-  auto* join = attn_kv_join_kernel<BF16, DV, 8 * NT>;
   cudaError_t e = allow_smem(main, S::kRing);
   if (e != cudaSuccess) return e;
   main<<<blocks, kWarps * 32, S::kRing, st>>>(p);
@@ -863,12 +963,19 @@ cudaError_t dec_launch(const DecodeParams& p, int blocks, cudaStream_t st) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.batch * p.c.heads * p.row_blocks * std::min(8 * NT, p.rows)));
-  cfg.blockDim = dim3(256);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join, p, blocks * kWarps);
+  const int64_t items = (int64_t)p.batch * p.c.heads * p.row_blocks;
+  const int runs = blocks * kWarps;
+  if (items * kByItemPieces <= runs) {
+    cfg.gridDim = dim3((unsigned)(items * std::min(8 * NT, p.rows)));
+    cfg.blockDim = dim3(kByItemThreads);
+    return cudaLaunchKernelEx(&cfg, attn_kv_join_items_kernel<BF16, DV, 8 * NT>, p, runs);
+  }
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kByRunThreads);
+  return cudaLaunchKernelEx(&cfg, attn_kv_join_runs_kernel<BF16, DV, 8 * NT>, p);
 }
 
 template <bool BF16, int NT>
