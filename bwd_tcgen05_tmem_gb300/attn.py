@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -119,6 +120,7 @@ class Kv4DecodeParams(ctypes.Structure):
 
 
 _lib = None
+_fast = None
 _lock = threading.Lock()
 
 
@@ -189,8 +191,42 @@ def load():
         lib.attn_kv_decode_workspace_size.restype = sz
         lib.attn_kv_decode.argtypes = [D, C] + [vp] * 6 + [sz, vp, vp]
         lib.attn_kv_decode.restype = ctypes.c_int
+        global _fast
+        _fast = _fast_handle()
         _lib = lib
         return lib
+
+
+# Calls that a serving step makes for every token take their parameter structs
+# as packed bytes, through a second handle of the library: filling a ctypes
+# structure field by field costs several microseconds, packing it less than one.
+_QK_PACK = struct.Struct("@11if18q").pack          # attn_qk_params_t
+_PLAN_PACK = struct.Struct("@6iq").pack            # attn_kv_plan_params_t
+_DECODE_PACK = struct.Struct("@5i6qiq2if0q").pack  # attn_kv4_decode_params_t
+
+
+def _fast_handle():
+    lib = ctypes.CDLL(LIB_PATH)
+    vp, sz, ci = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+    for name, args in (("attn_qk_norm_rope", [vp] * 12),
+                       ("attn_qk_norm_rope_bwd", [vp] * 15 + [sz, vp, vp]),
+                       ("attn_kv_plan", [vp] * 13),
+                       ("attn_kv_write", [vp, ci, ci] + [vp] * 7),
+                       ("attn_kv_read", [vp, ci, ci] + [vp] * 7),
+                       ("attn_kv_decode", [vp] * 8 + [sz, vp, vp])):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, ctypes.c_int
+    for name, args in (("attn_qk_norm_rope_bwd_workspace_size", [vp]),
+                       ("attn_kv_decode_workspace_size", [vp, vp])):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, sz
+    return lib
+
+
+def fast():
+    if _fast is None:
+        load()
+    return _fast
 
 
 def _check(rc):
@@ -488,90 +524,117 @@ def cp_relayout(src, dst, *, to_heads, cp, stream=None):
 
 # ----------------------------------------------------- norm and rotation of q and k
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_CODES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+
+
 def on_device(t, *others):
-    """The device of CUDA tensor ``t``, on which ``others`` (None apart) must lie too."""
-    if not t.is_cuda:
+    """The device index of CUDA tensor ``t``, on which ``others`` (None apart) must lie too."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    dev = t.device
     for o in others:
-        if o is not None and o.device != dev:
-            raise ValueError(f"tensors are on {dev} and {o.device}")
+        if o is not None and o.get_device() != dev:
+            raise ValueError(f"tensors are on {t.device} and {o.device}")
     return dev
 
 
-def launch(device, stream, fn, *args):
-    """fn(*args, stream) with ``device`` current; raises on an error status."""
-    if device.index == torch.cuda.current_device():
-        s = stream if stream is not None else torch.cuda.current_stream()
-        _check(fn(*args, s.cuda_stream))
-        return
-    with torch.cuda.device(device):
-        s = stream if stream is not None else torch.cuda.current_stream()
-        _check(fn(*args, s.cuda_stream))
+def launch(dev, stream, fn, *args):
+    """fn(*args, stream) with device ``dev`` current; raises on an error status."""
+    if stream is not None:
+        s = stream.cuda_stream
+    elif _raw_stream is not None:
+        s = _raw_stream(dev)
+    else:
+        s = torch.cuda.current_stream(dev).cuda_stream
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc:
+        _check(rc)
 
 
-def ptr(t):
-    return t.data_ptr() if t is not None else None
-
-
-def new(shape, dtype, device, stream):
+def new(shape, dtype, dev, stream):
     """A new tensor for work on ``stream`` (None: the current one): memory of that
     stream, so that it is not handed out again while the work is under way."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _qk_strides(t):
-    if t is None:
-        return (0, 0, 0)
-    if t.stride(-1) != 1:
-        raise ValueError("the head-dim axis must be contiguous")
+def _sized(dev, fn, *args):
+    """fn(*args) with device ``dev`` current (workspace sizes follow its SM count)."""
+    if dev == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _qk_strides(name, t, shape, dtype):
+    """{batch, token, head} strides of a tensor that must have this shape and dtype."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, q has {dtype}")
     s = t.stride()
-    return (0, s[0], s[1]) if len(s) == 3 else s[:3]
+    if s[-1] != 1:
+        raise ValueError("the head-dim axis must be contiguous")
+    return s[:3] if len(s) == 4 else (0, s[0], s[1])
 
 
-def _qk_params(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, qo, ko, dqo, dko, status):
-    thd = q.dim() == 3
-    if q.dim() not in (3, 4):
+_NO_STRIDES = (0, 0, 0)
+
+
+def _qk_pack(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, qo, ko, dqo, dko, status):
+    shape, dt = q.shape, q.dtype
+    if len(shape) == 4:
+        b, s, hq, d = shape
+    elif len(shape) == 3:
+        b = 1
+        s, hq, d = shape
+    else:
         raise ValueError("q must be [batch, seqlen, heads, d] or [total, heads, d]")
-    b, s = (1, q.shape[0]) if thd else q.shape[:2]
-    hq, d = q.shape[-2:]
-    hk = 0 if k is None else k.shape[-2]
-    for name, t, like in (("k", k, None), ("q_out", qo, q), ("k_out", ko, k), ("dq_out", dqo, q),
-                          ("dk_out", dko, k)):
-        if t is None:
-            continue
-        want = like.shape if like is not None else (*q.shape[:-2], hk, d)
-        if t.shape != want:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(want)}")
-        if t.dtype != q.dtype:
-            raise ValueError(f"{name} has dtype {t.dtype}, q has {q.dtype}")
+    hk, k_shape = 0, None
+    sk = sko = _NO_STRIDES
+    if k is not None:
+        if k.dim() != len(shape):
+            raise ValueError("k must have as many axes as q")
+        hk = k.shape[-2]
+        k_shape = (*shape[:-2], hk, d)
+        sk = _qk_strides("k", k, k_shape, dt)
+        sko = _qk_strides("k_out (dk)", ko, k_shape, dt)
+    elif ko is not None:
+        raise ValueError("an output for k without k")
     rot = max_pos = 0
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin must both be given or None")
-    if cos is not None:
+    if cos is not None and sin is not None:
         if (cos.shape != sin.shape or cos.dim() != 2 or cos.dtype != torch.float32
                 or sin.dtype != torch.float32 or not cos.is_contiguous() or not sin.is_contiguous()):
             raise ValueError("cos and sin must be contiguous float32 [max_pos, rotary_dim / 2]")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        max_pos, rot = cos.shape
+        rot *= 2
+    elif cos is not None or sin is not None:
+        raise ValueError("cos and sin must both be given or None")
     if positions is not None and (positions.dtype != torch.int32 or positions.numel() != b * s
                                   or not positions.is_contiguous()):
         raise ValueError("positions must be contiguous int32, one for each token")
-    wdt = None
-    for w in (wq, wk):
-        if w is None:
-            continue
-        if w.shape != (d,) or not w.is_contiguous() or (wdt is not None and w.dtype != wdt):
-            raise ValueError("norm weights must be contiguous [head_dim] and of one dtype")
-        wdt = w.dtype
+    wdt = torch.float32
+    if wq is not None or wk is not None:
+        wdt = (wq if wq is not None else wk).dtype
+        for w in (wq, wk):
+            if w is not None and (w.shape != (d,) or w.dtype != wdt or not w.is_contiguous()):
+                raise ValueError("norm weights must be contiguous [head_dim] and of one dtype")
     if status is not None and status.dtype != torch.int32:
         raise ValueError("status must be an int32 tensor")
-    return QkParams(_code(q.dtype), FP32 if wdt is None else _code(wdt), b, s, hq, hk, d, rot,
-                    int(bool(interleaved)), int(bool(norm)), max_pos, eps, _qk_strides(q),
-                    _qk_strides(k), _qk_strides(qo), _qk_strides(ko), _qk_strides(dqo),
-                    _qk_strides(dko))
+    sdq = _qk_strides("dq_out", dqo, shape, dt) if dqo is not None else _NO_STRIDES
+    sdk = _qk_strides("dk_out", dko, k_shape, dt) if dko is not None else _NO_STRIDES
+    if dt not in _CODES or wdt not in _CODES:
+        raise ValueError(f"unsupported dtypes {dt}, {wdt}")
+    return _QK_PACK(_CODES[dt], _CODES[wdt], b, s, hq, hk, d, rot, bool(interleaved), bool(norm),
+                    max_pos, eps, *_qk_strides("q", q, shape, dt), *sk,
+                    *_qk_strides("q_out (dq)", qo, shape, dt), *sko, *sdq, *sdk)
 
 
 def qk_norm_rope(q, k, cos, sin, *, positions=None, wq=None, wk=None, norm=True, eps=1e-6,
@@ -584,16 +647,21 @@ def qk_norm_rope(q, k, cos, sin, *, positions=None, wq=None, wk=None, norm=True,
     or [T], negative for padding rows (left as they are in ``q_out`` and
     ``k_out``), or None for 0, 1, ...; wq, wk: [d] or None.  ``q_out=q`` works
     in place.  ``status``: int32 device word (see include/attn.h), or None."""
-    lib = load()
+    lib = fast()
     dev = on_device(q, k, cos, sin, positions, wq, wk, q_out, k_out, status)
     if q_out is None:
         q_out = new(q.shape, q.dtype, dev, stream)
     if k_out is None and k is not None:
         k_out = new(k.shape, q.dtype, dev, stream)
-    p = _qk_params(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, q_out, k_out, None,
-                   None, status)
-    launch(dev, stream, lib.attn_qk_norm_rope, p, ptr(q), ptr(k), ptr(wq), ptr(wk), ptr(cos),
-           ptr(sin), ptr(positions), ptr(q_out), ptr(k_out), ptr(status))
+    p = _qk_pack(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, q_out, k_out, None,
+                 None, status)
+    launch(dev, stream, lib.attn_qk_norm_rope, p, q.data_ptr(),
+           None if k is None else k.data_ptr(), None if wq is None else wq.data_ptr(),
+           None if wk is None else wk.data_ptr(), None if cos is None else cos.data_ptr(),
+           None if sin is None else sin.data_ptr(),
+           None if positions is None else positions.data_ptr(), q_out.data_ptr(),
+           None if k_out is None else k_out.data_ptr(),
+           None if status is None else status.data_ptr())
     return q_out, k_out
 
 
@@ -603,39 +671,38 @@ def qk_norm_rope_bwd(q, k, cos, sin, dq_out, dk_out, *, positions=None, wq=None,
     """Gradient of qk_norm_rope: (dq, dk, dwq, dwk) from its inputs q, k and the
     gradients of its outputs.  dwq and dwk are float32 [d] (None without
     weights); rows of padding tokens are left as they are in dq and dk."""
-    lib = load()
+    lib = fast()
     dev = on_device(q, k, cos, sin, dq_out, dk_out, positions, wq, wk, dq, dk, dwq, dwk,
                     workspace, status)
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out must both be given or None")
+    d = q.shape[-1]
     if dq is None:
         dq = new(q.shape, q.dtype, dev, stream)
     if dk is None and k is not None:
         dk = new(k.shape, q.dtype, dev, stream)
     if wq is not None and dwq is None:
-        dwq = new(q.shape[-1:], torch.float32, dev, stream)
-    if wk is not None and dwk is None:
-        dwk = new(q.shape[-1:], torch.float32, dev, stream)
+        dwq = new((d,), torch.float32, dev, stream)
+    if wk is not None and dwk is None and k is not None:
+        dwk = new((d,), torch.float32, dev, stream)
     for w in (dwq, dwk):
-        if w is not None and (w.dtype != torch.float32 or w.shape != q.shape[-1:] or not w.is_contiguous()):
+        if w is not None and (w.dtype != torch.float32 or w.shape != (d,) or not w.is_contiguous()):
             raise ValueError("weight gradients must be contiguous float32 [head_dim]")
-    p = _qk_params(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, dq, dk, dq_out,
-                   dk_out, status)
+    p = _qk_pack(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, dq, dk, dq_out,
+                 dk_out, status)
     if workspace is None:
-        workspace = new(_sized(dev, lib.attn_qk_norm_rope_bwd_workspace_size, p), torch.uint8, dev,
-                        stream)
-    launch(dev, stream, lib.attn_qk_norm_rope_bwd, p, ptr(q), ptr(k), ptr(wq), ptr(wk), ptr(cos),
-           ptr(sin), ptr(positions), ptr(dq_out), ptr(dk_out), ptr(dq), ptr(dk), ptr(dwq), ptr(dwk),
-           ptr(workspace), workspace.numel() * workspace.element_size(), ptr(status))
+        workspace = new((_sized(dev, lib.attn_qk_norm_rope_bwd_workspace_size, p),), torch.uint8,
+                        dev, stream)
+    launch(dev, stream, lib.attn_qk_norm_rope_bwd, p, q.data_ptr(),
+           None if k is None else k.data_ptr(), None if wq is None else wq.data_ptr(),
+           None if wk is None else wk.data_ptr(), None if cos is None else cos.data_ptr(),
+           None if sin is None else sin.data_ptr(),
+           None if positions is None else positions.data_ptr(), dq_out.data_ptr(),
+           None if dk_out is None else dk_out.data_ptr(), dq.data_ptr(),
+           None if dk is None else dk.data_ptr(), None if dwq is None else dwq.data_ptr(),
+           None if dwk is None else dwk.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+           None if status is None else status.data_ptr())
     return dq, dk, dwq, dwk
-
-
-def _sized(device, fn, *args):
-    """fn(*args) with ``device`` current (workspace sizes follow its SM count)."""
-    if device.index == torch.cuda.current_device():
-        return fn(*args)
-    with torch.cuda.device(device):
-        return fn(*args)
 
 
 def rope_tables(max_pos, rotary_dim, *, base=10000.0, device="cuda"):

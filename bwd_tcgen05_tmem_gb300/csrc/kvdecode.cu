@@ -41,6 +41,7 @@
 // item is shared with other blocks, a partial result that a second kernel
 // joins in the order of the blocks.
 #include <algorithm>
+#include <atomic>
 
 #include "kcommon.cuh"
 #include "kv.h"
@@ -944,16 +945,26 @@ size_t decode_partial_floats(int blocks, int rows_per_block, int d_v) {
 
 namespace {
 
+// Dynamic shared memory beyond what every kernel may take, asked for once on
+// each device (`done`: a bit for each, of this kernel).
 template <typename F>
-cudaError_t allow_smem(F* f, int bytes) {
-  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+cudaError_t allow_smem(F* f, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 template <bool BF16, int DQK, int DV, int NT>
 cudaError_t dec_launch(const DecodeParams& p, int blocks, cudaStream_t st) {
   using S = DecShape<DQK, DV, NT>;
   auto* main = attn_kv_decode_kernel<BF16, DQK, DV, NT>;
-  cudaError_t e = allow_smem(main, S::kRing);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(main, S::kRing, done);
   if (e != cudaSuccess) return e;
   main<<<blocks, kWarps * 32, S::kRing, st>>>(p);
   e = cudaGetLastError();

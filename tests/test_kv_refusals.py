@@ -300,3 +300,21 @@ def test_reference_norm_rope_gradient_against_differences():
         e = dy * w
         assert torch.allclose(dw, (dy * x * n).sum((0, 1)), atol=1e-12)
         assert torch.allclose(dx, n * (e - x * n * n * (e * x).mean(-1, keepdim=True)), atol=1e-12)
+
+
+def test_packed_parameters_are_the_structs():
+    """The bytes that the bindings pass are those of the ctypes mirrors."""
+    import random
+    r = random.Random(1)
+    for pack, struct, floats in ((attn._QK_PACK, attn.QkParams, (11,)), (attn._PLAN_PACK, attn.KvPlanParams, ()),
+                                 (attn._DECODE_PACK, attn.Kv4DecodeParams, (15,))):
+        flat = [n for _, t in struct._fields_ for n in range(getattr(t, "_length_", 1))]
+        vals = [0.5 if i in floats else r.randrange(1, 1 << 20) for i in range(len(flat))]
+        it = iter(vals)
+        args = [tuple(next(it) for _ in range(t._length_)) if hasattr(t, "_length_") else next(it)
+                for _, t in struct._fields_]
+        got, want = struct.from_buffer_copy(pack(*vals)), struct(*args)
+        for name, t in struct._fields_:
+            a, b = getattr(got, name), getattr(want, name)
+            assert list(a) == list(b) if hasattr(t, "_length_") else a == b, name
+        assert len(pack(*vals)) == ctypes.sizeof(struct)
