@@ -45,13 +45,14 @@ struct QkParams {
   int batch, seqlen, d, rot, inter, norm, w_f32, max_pos;
   float eps;
   float* partial;             // backward: [blocks][d] partial sums of dw
-  int blocks[2];              // backward: blocks that work on each side
+  FastDiv seq_div, runs[2];   // by seqlen; by the runs of heads of a token
+  int blocks[2];              // blocks that work on each side
   int* status;
 };
 
-cudaError_t launch_qk_fwd(const QkParams& p, bool bf16, int num_sms, cudaStream_t st);
-// blocks of the backward for each side (fills p.blocks)
-void qk_bwd_blocks(QkParams& p, int num_sms);
+cudaError_t launch_qk_fwd(QkParams& p, bool bf16, int num_sms, cudaStream_t st);
+// blocks of the backward for each side (fills p.blocks); false: too many rows
+bool qk_bwd_blocks(QkParams& p, int num_sms);
 cudaError_t launch_qk_bwd(const QkParams& p, bool bf16, cudaStream_t st);
 
 struct PlanParams {

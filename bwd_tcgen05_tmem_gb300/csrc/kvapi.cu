@@ -201,12 +201,14 @@ attn_status_t check_qk_small(const attn_qk_params_t* p, const Region* outs, int 
   return ATTN_OK;
 }
 
+// 0: too many rows for a call
 size_t qk_partial_bytes(const attn_qk_params_t* p, attn::QkParams& kp) {
   kp.batch = p->batch;
   kp.seqlen = p->seqlen;
   kp.side[0].heads = p->heads_q;
   kp.side[1].heads = p->heads_k;
-  attn::qk_bwd_blocks(kp, attn::num_sms());
+  kp.d = p->head_dim;
+  if (!attn::qk_bwd_blocks(kp, attn::num_sms())) return 0;
   return up256((size_t)(kp.blocks[0] + kp.blocks[1]) * p->head_dim * 4);
 }
 
@@ -238,7 +240,7 @@ attn_status_t attn_qk_norm_rope(const attn_qk_params_t* p, const void* q, const 
   if ((s = check_qk_small(p, out, 2, w_q, w_k, cos, sin, positions, status))) return s;
   const cudaError_t e =
       attn::launch_qk_fwd(kp, p->dtype == ATTN_BF16, attn::num_sms(), (cudaStream_t)stream);
-  if (e == cudaErrorNotSupported) return api_fail(ATTN_ERR_UNSUPPORTED, "too many tokens for the grid");
+  if (e == cudaErrorNotSupported) return api_fail(ATTN_ERR_UNSUPPORTED, "too many rows for one call");
   return api_launched(e, 1, "norm and rotation kernel launch");
 }
 
@@ -290,6 +292,7 @@ attn_status_t attn_qk_norm_rope_bwd(const attn_qk_params_t* p, const void* q, co
                         qk_region(p, dq_out, p->stride_dqo, p->heads_q),
                         qk_region(p, dk_out, p->stride_dko, p->heads_k)};
   const size_t need = qk_partial_bytes(p, kp);
+  if (!need) return api_fail(ATTN_ERR_UNSUPPORTED, "too many rows for one call");
   if ((s = check_workspace(ws, ws_bytes, need))) return s;
   const int64_t wb = (int64_t)p->head_dim * 4;
   const Region out[5] = {qk_region(p, dq, p->stride_qo, p->heads_q),

@@ -11,6 +11,8 @@
 //   K row: word c * G + g      holds dims 32 g + 8 c .. + 7   (c < 4)
 //   V row: half-word r * G + g holds dims 32 g + 4 r .. + 3   (r < 8)
 // lowest nibble first.
+#include <algorithm>
+
 #include "kcommon.cuh"
 #include "kv.h"
 
@@ -152,33 +154,48 @@ cudaError_t launch_kv_plan(const PlanParams& p, int num_sms, cudaStream_t st) {
 // ----------------------------------------------------------------- rows in and out
 // A thread takes 8 neighbouring elements (16 bytes) of a row: a quarter of a
 // scale group, one word of codes.  The vectors of a token's K row and V row
-// are numbered through (H d_qk / 8, then H d_v / 8), so every lane works
-// whatever the head dim is; groups (4 lanes) and pairs of groups (8 lanes)
-// never straddle a warp or a row, because d is a multiple of 64.
-struct RowAt {
-  bool is_k;
-  int head, j;  // kv head, vector within the row
+// are numbered through (H d_qk / 8, then H d_v / 8); a thread keeps one number
+// and goes from token to token, so that all it computes for a token is where
+// its slot lies.  Where a token has fewer than 256 vectors a block takes
+// several tokens at a time; where it has more, blockIdx.y picks 256 of them.
+// Groups (4 lanes) and pairs of groups (8 lanes) never straddle a warp or a
+// row, because d is a multiple of 64.
+struct RowLane {
+  bool live, is_k;
+  int token;         // of the block's first pass
+  int step;          // tokens of a pass over the whole grid
+  int g, c, groups;  // scale group, quarter of it, groups of a row
+  int64_t in_row;    // elements from a token's row base to the vector
+  int64_t stride;    // elements between tokens
+  int64_t head_row;  // head * page_size: rows of the cache before the head's, within a page
 };
 
-__device__ __forceinline__ RowAt row_at(const KvRowsParams& p, uint32_t v) {
-  RowAt r;
+__device__ __forceinline__ RowLane row_lane(const KvRowsParams& p) {
+  RowLane r;
+  const uint32_t per = p.per_token.d;
+  const uint32_t many = per >= 256u ? 1u : 256u / per;  // tokens of a block
+  const uint32_t t = per >= 256u ? 0u : p.per_token.div(threadIdx.x);
+  uint32_t v = per >= 256u ? blockIdx.y * 256u + threadIdx.x : threadIdx.x - t * per;
+  r.live = t < many && v < per;
+  r.token = (int)(blockIdx.x * many + t);
+  r.step = (int)(gridDim.x * many);
   const uint32_t nk = (uint32_t)p.c.heads * p.vec_k.d;
   r.is_k = v < nk;
   if (!r.is_k) v -= nk;
-  r.head = (int)(r.is_k ? p.vec_k : p.vec_v).div(v);
-  r.j = (int)(v - (uint32_t)r.head * (r.is_k ? p.vec_k.d : p.vec_v.d));
+  const uint32_t vecs = r.is_k ? p.vec_k.d : p.vec_v.d;
+  const uint32_t head = (r.is_k ? p.vec_k : p.vec_v).div(v), j = v - head * vecs;
+  r.g = (int)(j >> 2);
+  r.c = (int)(j & 3u);
+  r.groups = (int)(vecs >> 2);
+  r.in_row = (int64_t)head * (r.is_k ? p.k_h : p.v_h) + j * 8;
+  r.stride = r.is_k ? p.k_t : p.v_t;
+  r.head_row = (int64_t)head * p.c.page_size;
   return r;
 }
 
-// Row index of (slot, head) in the cache arrays.
-__device__ __forceinline__ int64_t cache_row(const Kv4& c, int slot, int head) {
-  const int page = slot >> c.page_shift, off = slot & (c.page_size - 1);
-  return ((int64_t)page * c.heads + head) * c.page_size + off;
-}
-
 // Slot of token t: < 0 means "leave the row alone"; out of range is flagged.
-__device__ __forceinline__ int slot_of(const KvRowsParams& p, uint32_t t) {
-  const int s = p.slots[t];
+__device__ __forceinline__ int slot_of(const KvRowsParams& p, int t) {
+  const int s = __ldg(p.slots + t);
   if (s >= 0 && (s >> p.c.page_shift) >= p.c.num_pages) {
     if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
     return -1;
@@ -186,37 +203,88 @@ __device__ __forceinline__ int slot_of(const KvRowsParams& p, uint32_t t) {
   return s;
 }
 
+// Row of the cache arrays at (slot, the lane's head).
+__device__ __forceinline__ int64_t cache_row(const Kv4& c, int slot, const RowLane& r) {
+  return (int64_t)(slot >> c.page_shift) * (c.heads * c.page_size) + r.head_row +
+         (slot & (c.page_size - 1));
+}
+
+// The two elements of a 16-bit pair, in FP32.
+template <bool BF16>
+__device__ __forceinline__ uint64_t pair_f32(uint32_t w) {
+  if (BF16) return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return f2_pack(f.x, f.y);
+}
+
+// The codes of 8 elements whose scale s is a normal number, without a division:
+// the quotient is x * (1/s) corrected by its exact remainder.  A quotient that
+// lies midway between two codes has few bits, so the corrected product is that
+// number itself and rounds to even as the division would; any other is at
+// least 2^-13 away from the middle (x has 11 bits, s (2c + 1) / 2 has 12), 2^9
+// times the error of the product.  |x / s| < 7.03, so nothing needs clamping.
+// Adding 1.5 * 2^23 + 8 rounds to an integer: the sum's bits are 0x4B400000 +
+// code; the eight are put together by multiply-adds modulo 2^32.
+template <bool BF16>
+__device__ __forceinline__ uint32_t codes_of(const uint4& x, float s) {
+  float rs;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(s));
+  rs = fmaf(rs, fmaf(-s, rs, 1.0f), rs);
+  const uint64_t r2 = f2_pack(rs, rs), s2 = f2_pack(-s, -s), magic = f2_pack(12582920.0f, 12582920.0f);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t word = 0u - 0x4B400000u * 0x11111111u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t v = pair_f32<BF16>(w[i]);
+    uint64_t t = f2_mul(v, r2);
+    t = f2_add(f2_fma(f2_fma(t, s2, v), r2, t), magic);
+    float lo, hi;
+    f2_unpack(t, lo, hi);
+    word += __float_as_uint(lo) << (8 * i);
+    word += __float_as_uint(hi) << (8 * i + 4);
+  }
+  return word;
+}
+
+// The same for scales below the normal range (and for zero): by division.
+template <bool BF16>
+__device__ __noinline__ uint32_t tiny_codes_of(const uint4& x, float s) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t word = 0x88888888u;  // codes of zeros
+  if (s > 0.0f) {
+    word = 0u;
+    for (int e = 0; e < 8; ++e) {
+      const float v = Pack<BF16>::to_f((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+      const float t = rintf(__fdiv_rn(v, s));
+      word |= (uint32_t)((int)fminf(fmaxf(t, -7.0f), 7.0f) + 8) << (4 * e);
+    }
+  }
+  return word;
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(256) attn_kv_write_kernel(const __grid_constant__ KvRowsParams p) {
-  const uint32_t total = (uint32_t)p.tokens * p.per_token.d;  // < 2^31, checked at launch
-  const uint32_t step = gridDim.x * 256u;
+  const RowLane r = row_lane(p);
   constexpr int kU = 4;
   const int lane = threadIdx.x & 31;
-  // whole warps stay in the loop: the lanes exchange words
-  for (uint32_t base = blockIdx.x * 256u + (threadIdx.x & ~31u); base < total; base += step * kU) {
+  const uint16_t* base = (const uint16_t*)(r.is_k ? p.k : p.v) + r.in_row;
+  uint8_t* codes = r.is_k ? p.c.k_codes : p.c.v_codes;
+  uint16_t* scales = (r.is_k ? p.c.k_scales : p.c.v_scales) + r.g;
+  const uint32_t odd = (uint32_t)(lane >> 2) & 1u;  // odd group of a pair
+  // byte of the lane's word in a row of codes
+  const int at = 4 * (r.is_k ? r.c * r.groups + r.g : ((2 * r.c + (int)odd) * r.groups + (r.g & ~1)) / 2);
+  const int row_bytes = r.groups * 16;
+  // the lanes of a warp stay together: they exchange words
+  for (int t0 = r.token; __any_sync(0xffffffffu, r.live && t0 < p.tokens); t0 += r.step * kU) {
     uint4 x[kU];
-    int64_t row[kU];
-    RowAt at[kU];
-    int d[kU];
+    int slot[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const uint64_t i64 = (uint64_t)base + (uint64_t)u * step + lane;
-      row[u] = -1;
-      d[u] = 64;
+      const int64_t t = (int64_t)t0 + (int64_t)u * r.step;
+      const bool here = r.live && t < p.tokens;
+      slot[u] = here ? slot_of(p, (int)t) : -1;
       x[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (i64 < total) {
-        const uint32_t i = (uint32_t)i64, t = p.per_token.div(i);
-        at[u] = row_at(p, i - t * p.per_token.d);
-        const int slot = slot_of(p, t);
-        d[u] = at[u].is_k ? p.c.d_qk : p.c.d_v;
-        if (slot >= 0) {
-          const uint16_t* src =
-              (const uint16_t*)(at[u].is_k ? p.k : p.v) +
-              (int64_t)t * (at[u].is_k ? p.k_t : p.v_t) + (int64_t)at[u].head * (at[u].is_k ? p.k_h : p.v_h);
-          x[u] = *(reinterpret_cast<const uint4*>(src) + at[u].j);
-          row[u] = cache_row(p.c, slot, at[u].head);
-        }
-      }
+      if (here) x[u] = *reinterpret_cast<const uint4*>(base + t * r.stride);
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -227,121 +295,118 @@ __global__ void __launch_bounds__(256) attn_kv_write_kernel(const __grid_constan
       m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
       m = max(m & 0xffffu, m >> 16);
-      uint32_t word = 0x88888888u;  // codes of zeros
-      uint16_t sbits = 0x7fffu;     // a group with an infinity or a NaN: NaN
+      uint32_t word = 0x88888888u;
+      uint16_t sbits = 0x7fffu;  // a group with an infinity or a NaN: NaN
       if (m < (BF16 ? 0x7f80u : 0x7c00u)) {
+        // max / 7 as the division rounds it: the product corrected by its remainder
         const float amax = Pack<BF16>::to_f((uint16_t)m);
-        const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(amax, 7.0f));
+        float q = amax * (1.0f / 7.0f);
+        q = amax < 1e-30f ? __fdiv_rn(amax, 7.0f) : fmaf(fmaf(-q, 7.0f, amax), 1.0f / 7.0f, q);
+        const __nv_bfloat16 sb = __float2bfloat16_rn(q);
         sbits = __bfloat16_as_ushort(sb);
-        float s = __bfloat162float(sb);
-        if (s > 0.0f) {
-          // tiny groups: scaled by a power of two, so that 1 / s stays finite
-          const float f = s < 1e-30f ? 1.8446744e19f : 1.0f;  // 2^64
-          s *= f;
-          const float rs = __frcp_rn(s);
-          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-          word = 0u;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float xe = f * Pack<BF16>::to_f((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-            // The quotient x / s: x * (1/s) corrected by its exact remainder.
-            // A quotient that lies midway between two codes has few bits, so
-            // the corrected product is that number itself and rounds to even
-            // as the division would; any other is at least 2^-13 s away from
-            // the middle (x has 11 bits, s (2c + 1) / 2 has 12), 2^10 times
-            // the error of the product.
-            float t = xe * rs;
-            t = fmaf(fmaf(-t, s, xe), rs, t);
-            const int c = (int)fminf(fmaxf(rintf(t), -7.0f), 7.0f) + 8;
-            word |= (uint32_t)c << (4 * e);
-          }
-        }
+        const float s = __bfloat162float(sb);
+        word = s < 1e-30f ? tiny_codes_of<BF16>(x[u], s) : codes_of<BF16>(x[u], s);
       }
-      const uint32_t odd = (uint32_t)(lane >> 2) & 1u;  // odd group of the pair
       // V rows: two neighbouring groups exchange halves, so that each lane
       // holds the half-words (r, g), (r, g + 1) of one word
       const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? word & 0xffffu : word >> 16, 4);
-      if (row[u] < 0) continue;
-      const int G = d[u] / 32, g = at[u].j >> 2, c = at[u].j & 3;
-      if (at[u].is_k) {
-        reinterpret_cast<uint32_t*>(p.c.k_codes + row[u] * (d[u] / 2))[c * G + g] = word;
-      } else {
-        const uint32_t pair = odd ? (other | (word & 0xffff0000u)) : ((word & 0xffffu) | (other << 16));
-        const int r = 2 * c + (int)odd;
-        reinterpret_cast<uint32_t*>(p.c.v_codes + row[u] * (d[u] / 2))[(r * G + (g & ~1)) / 2] = pair;
-      }
-      if (c == 0) (at[u].is_k ? p.c.k_scales : p.c.v_scales)[row[u] * G + g] = sbits;
+      if (slot[u] < 0) continue;
+      if (!r.is_k) word = odd ? (other | (word & 0xffff0000u)) : ((word & 0xffffu) | (other << 16));
+      const int64_t row = cache_row(p.c, slot[u], r);
+      *reinterpret_cast<uint32_t*>(codes + row * row_bytes + at) = word;
+      if (r.c == 0) scales[row * r.groups] = sbits;
     }
   }
 }
 
+// The values of a word's 8 codes: (c - 8) s, rounded once.
+template <bool BF16>
+__device__ __forceinline__ uint4 values_of(uint32_t w, uint16_t sbits) {
+  uint32_t o[4];
+  if (BF16) {
+    // a product of a code (exact) and a bf16 scale, in bf16: one rounding
+    const __nv_bfloat162 s = __nv_bfloat162(__ushort_as_bfloat16(sbits), __ushort_as_bfloat16(sbits));
+    const __nv_bfloat162 off = __nv_bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));  // 136
+    uint32_t q[4];  // codes n and n + 4
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      uint32_t y;
+      asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xEA;" : "=r"(y) : "r"(w >> (4 * n)));  // 128 + code
+      const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<__nv_bfloat162*>(&y), off), s);
+      q[n] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    o[0] = __byte_perm(q[0], q[1], 0x5410), o[1] = __byte_perm(q[2], q[3], 0x5410);
+    o[2] = __byte_perm(q[0], q[1], 0x7632), o[3] = __byte_perm(q[2], q[3], 0x7632);
+  } else {
+    const float s = __uint_as_float((uint32_t)sbits << 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float lo = __uint_as_float(0x4b000000u | ((w >> (8 * i)) & 15u)) - 8388616.0f;
+      const float hi = __uint_as_float(0x4b000000u | ((w >> (8 * i + 4)) & 15u)) - 8388616.0f;
+      o[i] = Pack<BF16>::two(lo * s, hi * s);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(256) attn_kv_read_kernel(const __grid_constant__ KvRowsParams p) {
-  const uint32_t total = (uint32_t)p.tokens * p.per_token.d;
-  const uint32_t step = gridDim.x * 256u;
+  const RowLane r = row_lane(p);
   constexpr int kU = 4;
   const int lane = threadIdx.x & 31;
-  for (uint32_t base = blockIdx.x * 256u + (threadIdx.x & ~31u); base < total; base += step * kU) {
+  uint16_t* base = (uint16_t*)(r.is_k ? p.k : p.v) + r.in_row;
+  const uint8_t* codes = r.is_k ? p.c.k_codes : p.c.v_codes;
+  const uint16_t* scales = (r.is_k ? p.c.k_scales : p.c.v_scales) + r.g;
+  const uint32_t odd = (uint32_t)(lane >> 2) & 1u;
+  const int at = 4 * (r.is_k ? r.c * r.groups + r.g : ((2 * r.c + (int)odd) * r.groups + (r.g & ~1)) / 2);
+  const int row_bytes = r.groups * 16;
+  for (int t0 = r.token; __any_sync(0xffffffffu, r.live && t0 < p.tokens); t0 += r.step * kU) {
     uint32_t word[kU];
     uint16_t sc[kU];
-    uint4* dst[kU];
-    bool is_k[kU];
+    int slot[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const uint64_t i64 = (uint64_t)base + (uint64_t)u * step + lane;
-      dst[u] = nullptr;
+      const int64_t t = (int64_t)t0 + (int64_t)u * r.step;
+      slot[u] = r.live && t < p.tokens ? slot_of(p, (int)t) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
       word[u] = 0u;
       sc[u] = 0;
-      is_k[u] = true;
-      if (i64 < total) {
-        const uint32_t i = (uint32_t)i64, t = p.per_token.div(i);
-        const RowAt at = row_at(p, i - t * p.per_token.d);
-        const int slot = slot_of(p, t);
-        is_k[u] = at.is_k;
-        if (slot >= 0) {
-          const int d = at.is_k ? p.c.d_qk : p.c.d_v, G = d / 32, g = at.j >> 2, c = at.j & 3;
-          const int64_t row = cache_row(p.c, slot, at.head);
-          const int wi = at.is_k ? c * G + g : ((2 * c + (g & 1)) * G + (g & ~1)) / 2;
-          word[u] = reinterpret_cast<const uint32_t*>((at.is_k ? p.c.k_codes : p.c.v_codes) + row * (d / 2))[wi];
-          sc[u] = (at.is_k ? p.c.k_scales : p.c.v_scales)[row * G + g];
-          dst[u] = reinterpret_cast<uint4*>(
-                       (uint16_t*)(at.is_k ? p.k : p.v) + (int64_t)t * (at.is_k ? p.k_t : p.v_t) +
-                       (int64_t)at.head * (at.is_k ? p.k_h : p.v_h)) + at.j;
-        }
+      if (slot[u] >= 0) {
+        const int64_t row = cache_row(p.c, slot[u], r);
+        word[u] = *reinterpret_cast<const uint32_t*>(codes + row * row_bytes + at);
+        sc[u] = scales[row * r.groups];
       }
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const uint32_t odd = (uint32_t)(lane >> 2) & 1u;
       // a V lane of the even group holds (r, g), (r, g + 1) for r = 2c, one of
       // the odd group those for r = 2c + 1
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? word[u] & 0xffffu : word[u] >> 16, 4);
-      if (!dst[u]) continue;
-      const uint32_t w = is_k[u] ? word[u]
-                         : odd   ? (other | (word[u] & 0xffff0000u))
-                                 : ((word[u] & 0xffffu) | (other << 16));
-      const float s = __uint_as_float((uint32_t)sc[u] << 16);
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = (float)((int)((w >> (4 * e)) & 15u) - 8) * s;
-      *dst[u] = make_uint4(Pack<BF16>::two(f[0], f[1]), Pack<BF16>::two(f[2], f[3]),
-                           Pack<BF16>::two(f[4], f[5]), Pack<BF16>::two(f[6], f[7]));
+      uint32_t w = word[u];
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w & 0xffffu : w >> 16, 4);
+      if (slot[u] < 0) continue;
+      if (!r.is_k) w = odd ? (other | (w & 0xffff0000u)) : ((w & 0xffffu) | (other << 16));
+      const int64_t t = (int64_t)t0 + (int64_t)u * r.step;
+      *reinterpret_cast<uint4*>(base + t * r.stride) = values_of<BF16>(w, sc[u]);
     }
   }
 }
 
 namespace {
-unsigned rows_blocks(const KvRowsParams& p, int num_sms) {
-  const uint64_t total = (uint64_t)p.tokens * p.per_token.d;
-  uint64_t blocks = (total + 255) / 256;
-  const uint64_t cap = (uint64_t)num_sms * 8;
-  if (blocks > cap) blocks = cap;
-  return (unsigned)(blocks ? blocks : 1);
+dim3 rows_grid(const KvRowsParams& p, int num_sms) {
+  const uint32_t per = p.per_token.d;
+  const int64_t many = per >= 256u ? 1 : 256u / per;
+  const unsigned y = (per + 255u) / 256u;
+  int64_t x = (p.tokens + many - 1) / many;
+  const int64_t cap = std::max<int64_t>((int64_t)num_sms * 8 / y, 1);
+  if (x > cap) x = cap;
+  return dim3((unsigned)x, y);
 }
 }  // namespace
 
 cudaError_t launch_kv4_write(const KvRowsParams& p, bool bf16, int num_sms, cudaStream_t st) {
-  const unsigned b = rows_blocks(p, num_sms);
+  const dim3 b = rows_grid(p, num_sms);
   if (bf16)
     attn_kv_write_kernel<true><<<b, 256, 0, st>>>(p);
   else
@@ -350,7 +415,7 @@ cudaError_t launch_kv4_write(const KvRowsParams& p, bool bf16, int num_sms, cuda
 }
 
 cudaError_t launch_kv4_read(const KvRowsParams& p, bool bf16, int num_sms, cudaStream_t st) {
-  const unsigned b = rows_blocks(p, num_sms);
+  const dim3 b = rows_grid(p, num_sms);
   if (bf16)
     attn_kv_read_kernel<true><<<b, 256, 0, st>>>(p);
   else

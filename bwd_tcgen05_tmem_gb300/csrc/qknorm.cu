@@ -13,27 +13,31 @@
 //
 // Both are streams: 2 (forward) or 3 (gradient) rows of 16-bit elements are
 // moved for each row, with about one operation a byte, so the layout is made
-// for loads.  A lane takes "units" of two 8-element vectors that hold both
-// halves of 8 pairs (rows u and u + rot/16 of the row's vectors), so the
-// rotation needs no exchange between lanes; d / 16 units make a row, LPR lanes
-// share it and a warp works on 32 / LPR heads of ONE token at a time, kU of
-// them in flight: the token's cosines, sines and the weights are loaded once
-// and stay in registers.
+// for loads.  A lane takes a "unit" of two 8-element vectors that hold both
+// halves of 8 pairs (vectors u and u + rot/16 of the row), so the rotation
+// needs no exchange between lanes; d / 16 lanes make a row, and a warp works on
+// several heads of ONE token at a time: the token's cosines, sines and the
+// weights are loaded once for all of them.  The arithmetic is in packed FP32
+// pairs (fma.f32x2).  Rows come through a ring of asynchronous 16-byte copies:
+// each lane copies its own vectors a few jobs ahead and waits for its own
+// copies alone, so loads stay in flight while it computes, and no lane waits
+// for another.
+#include <algorithm>
+
 #include "kcommon.cuh"
 #include "kv.h"
 
 namespace attn {
 
 template <int D>
-struct QkShape {  // lanes that share a row, units of each lane
-  static constexpr int kUnits = D / 16;
-  static constexpr int kLpr = D == 192 ? 4 : kUnits;
-  static constexpr int kUpl = kUnits / kLpr;
-  static constexpr int kSlots = 32 / kLpr;  // rows a warp holds at a time
+struct QkShape {
+  static constexpr int kUnits = D / 16;                 // lanes of a row that work
+  static constexpr int kLpr = D == 192 ? 16 : kUnits;   // lanes of a row
+  static constexpr int kSlots = 32 / kLpr;              // rows a warp holds at a time
 };
 
-// The two vectors of unit u: both halves of 8 pairs, or two neighbours of the
-// part that does not rotate.
+// The two vectors of unit u: both halves of 8 pairs, or two of the part that
+// does not rotate.
 __device__ __forceinline__ void unit_vectors(int u, int rot, int units, int& a, int& b) {
   const int rh = rot >> 4;
   if (u < rh) {
@@ -45,20 +49,72 @@ __device__ __forceinline__ void unit_vectors(int u, int rot, int units, int& a, 
   }
 }
 
+// A unit's 8 pairs (P, Q) as packed FP32 pairs over e: pair e is (a[e], b[e])
+// of the two vectors or, interleaved, (a[2e], a[2e+1]) for e < 4, then b's.
+struct Pairs {
+  uint64_t p[4], q[4];
+};
+
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = Pack<BF16>::to_f((uint16_t)(w[i] & 0xffffu));
-    f[2 * i + 1] = Pack<BF16>::to_f((uint16_t)(w[i] >> 16));
+__device__ __forceinline__ void two_floats(uint32_t w, float& lo, float& hi) {
+  if (BF16) {
+    lo = __uint_as_float(w << 16);
+    hi = __uint_as_float(w & 0xffff0000u);
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    lo = f.x;
+    hi = f.y;
   }
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(Pack<BF16>::two(f[0], f[1]), Pack<BF16>::two(f[2], f[3]),
-                    Pack<BF16>::two(f[4], f[5]), Pack<BF16>::two(f[6], f[7]));
+template <bool INTER>
+__device__ __forceinline__ Pairs pairs_of(const float (&a)[8], const float (&b)[8]) {
+  Pairs r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (INTER) {
+      const float* v = i < 2 ? a : b;
+      const int j = (i & 1) * 4;
+      r.p[i] = f2_pack(v[j], v[j + 2]);
+      r.q[i] = f2_pack(v[j + 1], v[j + 3]);
+    } else {
+      r.p[i] = f2_pack(a[2 * i], a[2 * i + 1]);
+      r.q[i] = f2_pack(b[2 * i], b[2 * i + 1]);
+    }
+  }
+  return r;
+}
+
+template <bool BF16, bool INTER>
+__device__ __forceinline__ Pairs unpack(const uint4& va, const uint4& vb) {
+  const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+  float a[8], b[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    two_floats<BF16>(wa[i], a[2 * i], a[2 * i + 1]);
+    two_floats<BF16>(wb[i], b[2 * i], b[2 * i + 1]);
+  }
+  return pairs_of<INTER>(a, b);
+}
+
+template <bool BF16, bool INTER>
+__device__ __forceinline__ void pack(const Pairs& x, uint4& va, uint4& vb) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float p0, p1, q0, q1;
+    f2_unpack(x.p[i], p0, p1);
+    f2_unpack(x.q[i], q0, q1);
+    if (INTER) {
+      w[2 * i] = Pack<BF16>::two(p0, q0);
+      w[2 * i + 1] = Pack<BF16>::two(p1, q1);
+    } else {
+      w[i] = Pack<BF16>::two(p0, p1);
+      w[i + 4] = Pack<BF16>::two(q0, q1);
+    }
+  }
+  va = make_uint4(w[0], w[1], w[2], w[3]);
+  vb = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 template <bool BF16>
@@ -73,17 +129,19 @@ __device__ __forceinline__ void load_weights(const QkParams& p, const void* w, i
     f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
     f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
   } else {
-    unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(w) + vec), f);
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(w) + vec);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) two_floats<BF16>(u[i], f[2 * i], f[2 * i + 1]);
   }
 }
 
-// Cosines and sines of a unit's 8 pairs: pair e of a half-split unit is
-// (a[e], b[e]); of an interleaved one (a[2e], a[2e+1]) for e < 4, then b's.
+// Cosines and sines of a unit's 8 pairs, packed over e.
 __device__ __forceinline__ void load_angles(const QkParams& p, int pos, int u, int a, int b,
-                                            float (&c)[8], float (&s)[8]) {
+                                            uint64_t (&c)[4], uint64_t (&s)[4]) {
   if (u >= (p.rot >> 4)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = 1.0f, s[i] = 0.0f;
+    for (int i = 0; i < 4; ++i) c[i] = f2_pack(1.0f, 1.0f), s[i] = f2_pack(0.0f, 0.0f);
     return;
   }
   const int64_t row = (int64_t)pos * (p.rot >> 1);
@@ -92,125 +150,164 @@ __device__ __forceinline__ void load_angles(const QkParams& p, int pos, int u, i
   const float4 c1 = __ldg(reinterpret_cast<const float4*>(p.cos + row + i1));
   const float4 s0 = __ldg(reinterpret_cast<const float4*>(p.sin + row + i0));
   const float4 s1 = __ldg(reinterpret_cast<const float4*>(p.sin + row + i1));
-  c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-  s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+  c[0] = f2_pack(c0.x, c0.y), c[1] = f2_pack(c0.z, c0.w), c[2] = f2_pack(c1.x, c1.y), c[3] = f2_pack(c1.z, c1.w);
+  s[0] = f2_pack(s0.x, s0.y), s[1] = f2_pack(s0.z, s0.w), s[2] = f2_pack(s1.x, s1.y), s[3] = f2_pack(s1.z, s1.w);
 }
 
-// Turns the unit (a, b) by its angles; sign -1 turns back.
-__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&c)[8],
-                                     const float (&s)[8], int inter, float sign) {
-  if (inter) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x0 = a[2 * e], x1 = a[2 * e + 1], y0 = b[2 * e], y1 = b[2 * e + 1];
-      a[2 * e] = x0 * c[e] - x1 * (sign * s[e]);
-      a[2 * e + 1] = x1 * c[e] + x0 * (sign * s[e]);
-      b[2 * e] = y0 * c[e + 4] - y1 * (sign * s[e + 4]);
-      b[2 * e + 1] = y1 * c[e + 4] + y0 * (sign * s[e + 4]);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = a[e], y = b[e];
-      a[e] = x * c[e] - y * (sign * s[e]);
-      b[e] = y * c[e] + x * (sign * s[e]);
-    }
-  }
-}
+__device__ __forceinline__ uint64_t f2_neg(uint64_t v) { return v ^ 0x8000000080000000ull; }
+__device__ __forceinline__ uint64_t f2_both(float v) { return f2_pack(v, v); }
 
 template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
+__device__ __forceinline__ float row_sum(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  float s = lo + hi;
 #pragma unroll
-  for (int o = LPR / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = LPR / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
 }
 
-// The position of token (b, t): -1 (padding: the rows stay as they are), or
-// -2 where it lies outside the tables.
-__device__ __forceinline__ int token_position(const QkParams& p, int b, int t) {
-  const int pos = p.positions ? p.positions[(int64_t)b * p.seqlen + t] : t;
-  if (pos < 0) return -1;
-  if (pos >= p.max_pos && p.rot > 0) return -2;
-  return pos;
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
+               "l"((uint64_t)__cvta_generic_to_global(src))
+               : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the last N groups of this thread
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void flag_index(int* status) {
-  if (status) atomicCAS(status, DEV_OK, DEV_BAD_INDEX);
+// A job is one token and one run of kSlots * U of its heads, of one side; the
+// side's blocks share its jobs, a warp takes every (blocks * warps)-th.
+constexpr int kQkThreads = 128, kQkWarps = kQkThreads / 32;
+constexpr int kPad = -1, kNoAngle = -2;  // positions: padding; outside the tables
+
+__device__ __forceinline__ int token_position(const QkParams& p, uint32_t tok) {
+  const int pos = p.positions ? __ldg(p.positions + tok) : (int)(tok - p.seq_div.div(tok) * p.seq_div.d);
+  return pos < 0 ? kPad : pos >= p.max_pos && p.rot > 0 ? kNoAngle : pos;
+}
+
+// What both directions share: the ring.  NV vectors a lane and job (of x, and
+// of dz), the job's token and its position.
+template <int D, int U, int NV, int STAGES>
+struct QkRing {
+  uint4 v[STAGES][U * NV][kQkThreads];
+  uint32_t tok[STAGES][kQkWarps];
+  int pos[STAGES][kQkWarps];
+};
+
+// Copies the vectors of a lane's unit of `U` rows of one token.
+template <int U, int SLOTS, int NV, typename Stage>
+__device__ __forceinline__ void copy_rows(Stage& st, int off, const uint16_t* row0, int64_t head_stride,
+                                          int h0, int heads, bool active, int va, int vb) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int h = h0 + u * SLOTS;
+    if (h < heads && active) {
+      const uint4* row = reinterpret_cast<const uint4*>(row0 + (int64_t)h * head_stride);
+      copy16(&st[u * NV + off][threadIdx.x], row + va);
+      copy16(&st[u * NV + off + 1][threadIdx.x], row + vb);
+    }
+  }
 }
 
 // ----------------------------------------------------------------- forward
-// One warp: one token, one run of kSlots * kU heads of one side.
-template <bool BF16, int D, int U>
-__global__ void __launch_bounds__(128) attn_qk_fwd_kernel(const __grid_constant__ QkParams p,
-                                                          int runs_q, int runs) {
+template <bool BF16, int D, int U, bool INTER>
+__global__ void __launch_bounds__(kQkThreads, 6) attn_qk_fwd_kernel(
+    const __grid_constant__ QkParams p) {
   using S = QkShape<D>;
-  const int lane = threadIdx.x & 31, slot = lane / S::kLpr, l = lane % S::kLpr;
-  const int64_t job = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int64_t tok = job / runs;
-  const int run = (int)(job - tok * runs);
-  if (tok >= (int64_t)p.batch * p.seqlen) return;
-  const int b = (int)(tok / p.seqlen), t = (int)(tok - (int64_t)b * p.seqlen);
-  const bool is_k = run >= runs_q;
+  constexpr int kStages = 3;
+  __shared__ QkRing<D, U, 2, kStages> ring;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / S::kLpr, l = lane % S::kLpr;
+  const bool is_k = (int)blockIdx.x >= p.blocks[0], active = l < S::kUnits;
   const QkSide& sd = p.side[is_k ? 1 : 0];
-  const int h0 = (is_k ? run - runs_q : run) * (S::kSlots * U) + slot;
-  const int pos = token_position(p, b, t);
-  if (pos == -1) return;
-  if (pos == -2 && lane == 0) flag_index(p.status);
-
-  int va[S::kUpl], vb[S::kUpl];
-  uint4 xa[U][S::kUpl], xb[U][S::kUpl];
-#pragma unroll
-  for (int i = 0; i < S::kUpl; ++i) unit_vectors(i * S::kLpr + l, p.rot, S::kUnits, va[i], vb[i]);
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * S::kSlots;
-    const uint4* row = reinterpret_cast<const uint4*>((const uint16_t*)sd.x + b * sd.x_b +
-                                                      t * sd.x_t + (int64_t)h * sd.x_h);
-#pragma unroll
-    for (int i = 0; i < S::kUpl; ++i) {
-      xa[u][i] = xb[u][i] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < sd.heads) xa[u][i] = row[va[i]], xb[u][i] = row[vb[i]];
-    }
+  const int blk = is_k ? (int)blockIdx.x - p.blocks[0] : (int)blockIdx.x;
+  const FastDiv runs = p.runs[is_k ? 1 : 0];  // of a token; jobs: below 2^31, checked at launch
+  const uint32_t end = (uint32_t)p.batch * p.seq_div.d * runs.d;
+  const uint32_t step = (uint32_t)p.blocks[is_k ? 1 : 0] * kQkWarps, job0 = (uint32_t)blk * kQkWarps + warp;
+  int va, vb;
+  unit_vectors(active ? l : 0, p.rot, S::kUnits, va, vb);
+  Pairs w;
+  {
+    float a[8], b[8];
+    load_weights<BF16>(p, sd.w, va, a);
+    load_weights<BF16>(p, sd.w, vb, b);
+    w = pairs_of<INTER>(a, b);
   }
-  float rms[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < S::kUpl; ++i) {
-      float a[8], c[8];
-      unpack8<BF16>(xa[u][i], a);
-      unpack8<BF16>(xb[u][i], c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(c[e], c[e], ss));
+  uint32_t next = job0;  // the next job to copy
+  int next_pos = next < end ? token_position(p, runs.div(next)) : kPad;
+  auto copy = [&](int s) {
+    if (next < end) {
+      const uint32_t tok = runs.div(next), b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
+      const int h0 = (int)(next - tok * runs.d) * (S::kSlots * U) + slot;
+      if (next_pos != kPad)
+        copy_rows<U, S::kSlots, 2>(ring.v[s], 0, (const uint16_t*)sd.x + b * sd.x_b + t * sd.x_t, sd.x_h, h0,
+                                   sd.heads, active, va, vb);
+      if (lane == 0) ring.tok[s][warp] = tok, ring.pos[s][warp] = next_pos;
+      next += step;
+      if (next < end) next_pos = token_position(p, runs.div(next));
     }
-    ss = row_sum<S::kLpr>(ss);
-    rms[u] = p.norm ? rsqrtf(ss * (1.0f / D) + p.eps) : 1.0f;
-    if (pos == -2) rms[u] = __int_as_float(0x7fffffff);  // NaN: no such angle
-  }
+    copies_end();
+  };
 #pragma unroll
-  for (int i = 0; i < S::kUpl; ++i) {
-    float wa[8], wb[8], cs[8], sn[8];
-    load_weights<BF16>(p, sd.w, va[i], wa);
-    load_weights<BF16>(p, sd.w, vb[i], wb);
-    load_angles(p, pos < 0 ? 0 : pos, i * S::kLpr + l, va[i], vb[i], cs, sn);
+  for (int i = 0; i < kStages - 1; ++i) copy(i);
+  int s = 0;
+  for (uint32_t job = job0; job < end; job += step) {
+    copy(s == 0 ? kStages - 1 : s - 1);  // the stage used last
+    copies_wait<kStages - 1>();
+    __syncwarp();
+    const uint32_t tok = ring.tok[s][warp];
+    const int pos = ring.pos[s][warp];
+    if (pos != kPad) {
+      if (pos == kNoAngle && lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+      uint64_t pc[4], ps[4], qc[4], qs[4];  // weights times cosines and sines
+      load_angles(p, pos < 0 ? 0 : pos, active ? l : 0, va, vb, pc, ps);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * S::kSlots;
-      float a[8], c[8];
-      unpack8<BF16>(xa[u][i], a);
-      unpack8<BF16>(xb[u][i], c);
+      for (int i = 0; i < 4; ++i) {
+        qc[i] = f2_mul(w.q[i], pc[i]);
+        qs[i] = f2_neg(f2_mul(w.q[i], ps[i]));
+        pc[i] = f2_mul(w.p[i], pc[i]);
+        ps[i] = f2_mul(w.p[i], ps[i]);
+      }
+      const int h0 = (int)(job - tok * runs.d) * (S::kSlots * U) + slot;
+      const uint32_t b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
+      uint16_t* out0 = (uint16_t*)sd.out + b * sd.o_b + t * sd.o_t;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] *= rms[u] * wa[e], c[e] *= rms[u] * wb[e];
-      turn(a, c, cs, sn, p.inter, 1.0f);
-      if (h < sd.heads) {
-        uint4* out = reinterpret_cast<uint4*>((uint16_t*)sd.out + b * sd.o_b + t * sd.o_t +
-                                              (int64_t)h * sd.o_h);
-        out[va[i]] = pack8<BF16>(a);
-        out[vb[i]] = pack8<BF16>(c);
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * S::kSlots;
+        const bool here = h < sd.heads && active;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        const Pairs x = unpack<BF16, INTER>(here ? ring.v[s][2 * u][threadIdx.x] : zero,
+                                            here ? ring.v[s][2 * u + 1][threadIdx.x] : zero);
+        float r = 1.0f;
+        if (p.norm) {
+          uint64_t ss = f2_mul(x.p[0], x.p[0]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i) ss = f2_fma(x.p[i], x.p[i], ss);
+            ss = f2_fma(x.q[i], x.q[i], ss);
+          }
+          r = rsqrtf(row_sum<S::kLpr>(ss) * (1.0f / D) + p.eps);
+        }
+        if (pos == kNoAngle) r = __int_as_float(0x7fffffff);  // NaN
+        const uint64_t r2 = f2_both(r);
+        Pairs z;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z.p[i] = f2_mul(r2, f2_fma(x.q[i], qs[i], f2_mul(x.p[i], pc[i])));
+          z.q[i] = f2_mul(r2, f2_fma(x.p[i], ps[i], f2_mul(x.q[i], qc[i])));
+        }
+        if (here) {
+          uint4* out = reinterpret_cast<uint4*>(out0 + (int64_t)h * sd.o_h);
+          pack<BF16, INTER>(z, out[va], out[vb]);
+        }
       }
     }
+    __syncwarp();
+    s = s == kStages - 1 ? 0 : s + 1;
   }
+  copies_wait<0>();
 }
 
 // ----------------------------------------------------------------- gradient
@@ -218,119 +315,142 @@ __global__ void __launch_bounds__(128) attn_qk_fwd_kernel(const __grid_constant_
 // lane's share of dw stays in registers over all rows of its block; each block
 // leaves one row of partial sums, which a second kernel adds up in the order
 // of the blocks (no atomics: the result does not depend on who came first).
-template <bool BF16, int D, int U>
-__global__ void __launch_bounds__(256) attn_qk_bwd_kernel(const __grid_constant__ QkParams p) {
+template <bool BF16, int D, int U, bool INTER>
+__global__ void __launch_bounds__(kQkThreads, 4) attn_qk_bwd_kernel(
+    const __grid_constant__ QkParams p) {
   using S = QkShape<D>;
-  const int lane = threadIdx.x & 31, slot = lane / S::kLpr, l = lane % S::kLpr;
-  const bool is_k = (int)blockIdx.x >= p.blocks[0];
+  constexpr int kStages = 3;
+  __shared__ QkRing<D, U, 4, kStages> ring;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / S::kLpr, l = lane % S::kLpr;
+  const bool is_k = (int)blockIdx.x >= p.blocks[0], active = l < S::kUnits;
   const QkSide& sd = p.side[is_k ? 1 : 0];
   const int blk = is_k ? (int)blockIdx.x - p.blocks[0] : (int)blockIdx.x;
-  const int nblk = p.blocks[is_k ? 1 : 0];
-  const int runs = (sd.heads + S::kSlots * U - 1) / (S::kSlots * U);
-  const int64_t jobs = (int64_t)p.batch * p.seqlen * runs;
-  int va[S::kUpl], vb[S::kUpl];
-  float wa[S::kUpl][8], wb[S::kUpl][8], da[S::kUpl][8], db[S::kUpl][8];
+  const FastDiv runs = p.runs[is_k ? 1 : 0];  // of a token; jobs: below 2^31, checked at launch
+  const uint32_t end = (uint32_t)p.batch * p.seq_div.d * runs.d;
+  const uint32_t step = (uint32_t)p.blocks[is_k ? 1 : 0] * kQkWarps, job0 = (uint32_t)blk * kQkWarps + warp;
+  int va, vb;
+  unit_vectors(active ? l : 0, p.rot, S::kUnits, va, vb);
+  Pairs w, dw;
+  {
+    float a[8], b[8];
+    load_weights<BF16>(p, sd.w, va, a);
+    load_weights<BF16>(p, sd.w, vb, b);
+    w = pairs_of<INTER>(a, b);
 #pragma unroll
-  for (int i = 0; i < S::kUpl; ++i) {
-    unit_vectors(i * S::kLpr + l, p.rot, S::kUnits, va[i], vb[i]);
-    load_weights<BF16>(p, sd.w, va[i], wa[i]);
-    load_weights<BF16>(p, sd.w, vb[i], wb[i]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) da[i][e] = db[i][e] = 0.0f;
+    for (int i = 0; i < 4; ++i) dw.p[i] = dw.q[i] = f2_both(0.0f);
   }
-  for (int64_t job = (int64_t)blk * 8 + (threadIdx.x >> 5); job < jobs; job += (int64_t)nblk * 8) {
-    const int64_t tok = job / runs;
-    const int h0 = (int)(job - tok * runs) * (S::kSlots * U) + slot;
-    const int b = (int)(tok / p.seqlen), t = (int)(tok - (int64_t)b * p.seqlen);
-    const int pos = token_position(p, b, t);
-    if (pos == -1) continue;
-    if (pos == -2 && lane == 0) flag_index(p.status);
-    uint4 xa[U][S::kUpl], xb[U][S::kUpl], ga[U][S::kUpl], gb[U][S::kUpl];
+  uint32_t next = job0;
+  int next_pos = next < end ? token_position(p, runs.div(next)) : kPad;
+  auto copy = [&](int s) {
+    if (next < end) {
+      const uint32_t tok = runs.div(next), b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
+      const int h0 = (int)(next - tok * runs.d) * (S::kSlots * U) + slot;
+      if (next_pos != kPad) {
+        copy_rows<U, S::kSlots, 4>(ring.v[s], 0, (const uint16_t*)sd.x + b * sd.x_b + t * sd.x_t, sd.x_h, h0,
+                                   sd.heads, active, va, vb);
+        copy_rows<U, S::kSlots, 4>(ring.v[s], 2, (const uint16_t*)sd.dz + b * sd.dz_b + t * sd.dz_t, sd.dz_h, h0,
+                                   sd.heads, active, va, vb);
+      }
+      if (lane == 0) ring.tok[s][warp] = tok, ring.pos[s][warp] = next_pos;
+      next += step;
+      if (next < end) next_pos = token_position(p, runs.div(next));
+    }
+    copies_end();
+  };
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * S::kSlots;
-      const uint4* row = reinterpret_cast<const uint4*>((const uint16_t*)sd.x + b * sd.x_b +
-                                                        t * sd.x_t + (int64_t)h * sd.x_h);
-      const uint4* grow = reinterpret_cast<const uint4*>((const uint16_t*)sd.dz + b * sd.dz_b +
-                                                         t * sd.dz_t + (int64_t)h * sd.dz_h);
+  for (int i = 0; i < kStages - 1; ++i) copy(i);
+  int s = 0;
+  for (uint32_t job = job0; job < end; job += step) {
+    copy(s == 0 ? kStages - 1 : s - 1);
+    copies_wait<kStages - 1>();
+    __syncwarp();
+    const uint32_t tok = ring.tok[s][warp];
+    const int pos = ring.pos[s][warp];
+    if (pos != kPad) {
+      if (pos == kNoAngle && lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+      uint64_t c[4], sn[4];
+      load_angles(p, pos < 0 ? 0 : pos, active ? l : 0, va, vb, c, sn);
+      const int h0 = (int)(job - tok * runs.d) * (S::kSlots * U) + slot;
+      const uint32_t b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
+      uint16_t* out0 = (uint16_t*)sd.out + b * sd.o_b + t * sd.o_t;
 #pragma unroll
-      for (int i = 0; i < S::kUpl; ++i) {
-        xa[u][i] = xb[u][i] = ga[u][i] = gb[u][i] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < sd.heads) {
-          xa[u][i] = row[va[i]], xb[u][i] = row[vb[i]];
-          ga[u][i] = grow[va[i]], gb[u][i] = grow[vb[i]];
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * S::kSlots;
+        const bool here = h < sd.heads && active;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        const Pairs x = unpack<BF16, INTER>(here ? ring.v[s][4 * u][threadIdx.x] : zero,
+                                            here ? ring.v[s][4 * u + 1][threadIdx.x] : zero);
+        const Pairs z = unpack<BF16, INTER>(here ? ring.v[s][4 * u + 2][threadIdx.x] : zero,
+                                            here ? ring.v[s][4 * u + 3][threadIdx.x] : zero);
+        Pairs dy, g;
+        uint64_t ss = f2_both(0.0f), gx = f2_both(0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dy.p[i] = f2_fma(z.q[i], sn[i], f2_mul(z.p[i], c[i]));
+          dy.q[i] = f2_fma(z.p[i], f2_neg(sn[i]), f2_mul(z.q[i], c[i]));
+          g.p[i] = f2_mul(dy.p[i], w.p[i]);
+          g.q[i] = f2_mul(dy.q[i], w.q[i]);
+          ss = f2_fma(x.p[i], x.p[i], ss);
+          ss = f2_fma(x.q[i], x.q[i], ss);
+          gx = f2_fma(g.p[i], x.p[i], gx);
+          gx = f2_fma(g.q[i], x.q[i], gx);
+        }
+        float r = 1.0f, k = 0.0f;
+        if (p.norm) {
+          r = rsqrtf(row_sum<S::kLpr>(ss) * (1.0f / D) + p.eps);
+          k = r * r * (row_sum<S::kLpr>(gx) * (1.0f / D));
+        }
+        if (pos == kNoAngle) r = __int_as_float(0x7fffffff);
+        const uint64_t r2 = f2_both(r), k2 = f2_both(-k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dw.p[i] = f2_fma(dy.p[i], f2_mul(x.p[i], r2), dw.p[i]);
+          dw.q[i] = f2_fma(dy.q[i], f2_mul(x.q[i], r2), dw.q[i]);
+          g.p[i] = f2_mul(r2, f2_fma(x.p[i], k2, g.p[i]));
+          g.q[i] = f2_mul(r2, f2_fma(x.q[i], k2, g.q[i]));
+        }
+        if (here) {
+          uint4* out = reinterpret_cast<uint4*>(out0 + (int64_t)h * sd.o_h);
+          pack<BF16, INTER>(g, out[va], out[vb]);
         }
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * S::kSlots;
-      float ya[S::kUpl][8], yb[S::kUpl][8];  // dy
-      float ss = 0.0f, gx = 0.0f;
-#pragma unroll
-      for (int i = 0; i < S::kUpl; ++i) {
-        float a[8], c[8], cs[8], sn[8];
-        load_angles(p, pos < 0 ? 0 : pos, i * S::kLpr + l, va[i], vb[i], cs, sn);
-        unpack8<BF16>(ga[u][i], ya[i]);
-        unpack8<BF16>(gb[u][i], yb[i]);
-        turn(ya[i], yb[i], cs, sn, p.inter, -1.0f);
-        unpack8<BF16>(xa[u][i], a);
-        unpack8<BF16>(xb[u][i], c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ss = fmaf(a[e], a[e], fmaf(c[e], c[e], ss));
-          gx = fmaf(ya[i][e] * wa[i][e], a[e], fmaf(yb[i][e] * wb[i][e], c[e], gx));
-        }
-      }
-      ss = row_sum<S::kLpr>(ss);
-      gx = row_sum<S::kLpr>(gx);
-      float r = p.norm ? rsqrtf(ss * (1.0f / D) + p.eps) : 1.0f;
-      if (pos == -2) r = __int_as_float(0x7fffffff);
-      const float k = p.norm ? r * r * (gx * (1.0f / D)) : 0.0f;
-#pragma unroll
-      for (int i = 0; i < S::kUpl; ++i) {
-        float a[8], c[8];
-        unpack8<BF16>(xa[u][i], a);
-        unpack8<BF16>(xb[u][i], c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          da[i][e] = fmaf(ya[i][e], a[e] * r, da[i][e]);
-          db[i][e] = fmaf(yb[i][e], c[e] * r, db[i][e]);
-          a[e] = r * fmaf(-a[e], k, ya[i][e] * wa[i][e]);
-          c[e] = r * fmaf(-c[e], k, yb[i][e] * wb[i][e]);
-        }
-        if (h < sd.heads) {
-          uint4* out = reinterpret_cast<uint4*>((uint16_t*)sd.out + b * sd.o_b + t * sd.o_t +
-                                                (int64_t)h * sd.o_h);
-          out[va[i]] = pack8<BF16>(a);
-          out[vb[i]] = pack8<BF16>(c);
-        }
-      }
-    }
+    __syncwarp();
+    s = s == kStages - 1 ? 0 : s + 1;
   }
+  copies_wait<0>();
   if (!sd.dw) return;
-  // the block's sum of dw: over the rows a warp holds, then over its 8 warps
-  __shared__ float part[8][D];
+  // the block's sum of dw: over the rows a warp holds, then over its warps
+  float* part = reinterpret_cast<float*>(ring.v);  // [warp][D]
+  float f[16];  // as they lie in the two vectors
 #pragma unroll
-  for (int i = 0; i < S::kUpl; ++i)
+  for (int i = 0; i < 4; ++i) {
+    float p0, p1, q0, q1;
+    f2_unpack(dw.p[i], p0, p1);
+    f2_unpack(dw.q[i], q0, q1);
+    if (INTER) {
+      f[4 * i] = p0, f[4 * i + 1] = q0, f[4 * i + 2] = p1, f[4 * i + 3] = q1;
+    } else {
+      f[2 * i] = p0, f[2 * i + 1] = p1, f[8 + 2 * i] = q0, f[8 + 2 * i + 1] = q1;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+#pragma unroll
+    for (int o = S::kLpr; o < 32; o <<= 1) f[e] += __shfl_xor_sync(0xffffffffu, f[e], o);
+  __syncthreads();
+  if (slot == 0 && active)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-#pragma unroll
-      for (int o = S::kLpr; o < 32; o <<= 1) {
-        da[i][e] += __shfl_xor_sync(0xffffffffu, da[i][e], o);
-        db[i][e] += __shfl_xor_sync(0xffffffffu, db[i][e], o);
-      }
-      if (slot == 0) {
-        part[threadIdx.x >> 5][va[i] * 8 + e] = da[i][e];
-        part[threadIdx.x >> 5][vb[i] * 8 + e] = db[i][e];
-      }
+      part[warp * D + va * 8 + e] = f[e];
+      part[warp * D + vb * 8 + e] = f[8 + e];
     }
   __syncthreads();
-  for (int c = threadIdx.x; c < D; c += 256) {
-    float s = 0.0f;
+  for (int c = threadIdx.x; c < D; c += kQkThreads) {
+    float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) s += part[w][c];
-    p.partial[(int64_t)blockIdx.x * D + c] = s;
+    for (int k = 0; k < kQkWarps; ++k) sum += part[k * D + c];
+    p.partial[(int64_t)blockIdx.x * D + c] = sum;
   }
 }
 
@@ -356,31 +476,41 @@ __global__ void __launch_bounds__(256) attn_qk_dw_kernel(const __grid_constant__
 // ----------------------------------------------------------------- launches
 namespace {
 
-template <bool BF16, int D, int U>
+// Runs of `rows` heads of each side, and its blocks: `most` in all, shared out by
+// the sides' heads; never more than the jobs keep busy.  False: too many jobs.
+bool share_blocks(QkParams& p, int most, int rows) {
+  const int64_t tokens = (int64_t)p.batch * p.seqlen;
+  const int64_t heads = p.side[0].heads + p.side[1].heads;
+  p.seq_div = FastDiv::of((uint32_t)std::max(p.seqlen, 1));
+  bool ok = true;
+  for (int s = 0; s < 2; ++s) {
+    const int64_t h = p.side[s].heads, runs = std::max<int64_t>((h + rows - 1) / rows, 1);
+    p.runs[s] = FastDiv::of((uint32_t)runs);
+    ok = ok && tokens * runs < (1ll << 31) - (1 << 20);
+    int64_t n = heads ? (most * h + heads / 2) / heads : 0;
+    n = std::min(n, (tokens * runs + kQkWarps - 1) / kQkWarps);
+    p.blocks[s] = h > 0 ? (int)std::max<int64_t>(n, 1) : 0;
+  }
+  return ok;
+}
+
+int slots_of(int d) { return d == 192 ? 2 : 32 / (d / 16); }
+
+template <bool BF16, int D>
 cudaError_t fwd_launch(const QkParams& p, cudaStream_t st) {
-  const int per = QkShape<D>::kSlots * U;
-  const int rq = (p.side[0].heads + per - 1) / per, rk = (p.side[1].heads + per - 1) / per;
-  const int64_t blocks = ((int64_t)p.batch * p.seqlen * (rq + rk) + 3) / 4;
-  if (blocks > INT32_MAX) return cudaErrorNotSupported;
-  attn_qk_fwd_kernel<BF16, D, U><<<(unsigned)blocks, 128, 0, st>>>(p, rq, rq + rk);
+  if (p.inter)
+    attn_qk_fwd_kernel<BF16, D, 2, true><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
+  else
+    attn_qk_fwd_kernel<BF16, D, 2, false><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
-template <bool BF16>
-cudaError_t fwd_dispatch(const QkParams& p, cudaStream_t st) {
-  switch (p.d) {
-    case 64: return fwd_launch<BF16, 64, 4>(p, st);
-    case 128: return fwd_launch<BF16, 128, 4>(p, st);
-    case 192: return fwd_launch<BF16, 192, 1>(p, st);
-    case 256: return fwd_launch<BF16, 256, 4>(p, st);
-    case 512: return fwd_launch<BF16, 512, 4>(p, st);
-    default: return cudaErrorNotSupported;
-  }
-}
-
-template <bool BF16, int D, int U>
+template <bool BF16, int D>
 cudaError_t bwd_launch(const QkParams& p, cudaStream_t st) {
-  attn_qk_bwd_kernel<BF16, D, U><<<p.blocks[0] + p.blocks[1], 256, 0, st>>>(p);
+  if (p.inter)
+    attn_qk_bwd_kernel<BF16, D, 1, true><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
+  else
+    attn_qk_bwd_kernel<BF16, D, 1, false><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!p.side[0].dw && !p.side[1].dw)) return e;
   attn_qk_dw_kernel<<<dim3(D / 32, 2), 256, 0, st>>>(p);
@@ -388,39 +518,28 @@ cudaError_t bwd_launch(const QkParams& p, cudaStream_t st) {
 }
 
 template <bool BF16>
-cudaError_t bwd_dispatch(const QkParams& p, cudaStream_t st) {
+cudaError_t dispatch(const QkParams& p, bool fwd, cudaStream_t st) {
   switch (p.d) {
-    case 64: return bwd_launch<BF16, 64, 2>(p, st);
-    case 128: return bwd_launch<BF16, 128, 2>(p, st);
-    case 192: return bwd_launch<BF16, 192, 1>(p, st);
-    case 256: return bwd_launch<BF16, 256, 2>(p, st);
-    case 512: return bwd_launch<BF16, 512, 2>(p, st);
+    case 64: return fwd ? fwd_launch<BF16, 64>(p, st) : bwd_launch<BF16, 64>(p, st);
+    case 128: return fwd ? fwd_launch<BF16, 128>(p, st) : bwd_launch<BF16, 128>(p, st);
+    case 192: return fwd ? fwd_launch<BF16, 192>(p, st) : bwd_launch<BF16, 192>(p, st);
+    case 256: return fwd ? fwd_launch<BF16, 256>(p, st) : bwd_launch<BF16, 256>(p, st);
+    case 512: return fwd ? fwd_launch<BF16, 512>(p, st) : bwd_launch<BF16, 512>(p, st);
     default: return cudaErrorNotSupported;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_qk_fwd(const QkParams& p, bool bf16, int num_sms, cudaStream_t st) {
-  (void)num_sms;
-  return bf16 ? fwd_dispatch<true>(p, st) : fwd_dispatch<false>(p, st);
+cudaError_t launch_qk_fwd(QkParams& p, bool bf16, int num_sms, cudaStream_t st) {
+  if (!share_blocks(p, num_sms * 6, 2 * slots_of(p.d))) return cudaErrorNotSupported;
+  return bf16 ? dispatch<true>(p, true, st) : dispatch<false>(p, true, st);
 }
 
-// Two blocks an SM, shared out by the rows of each side; never more than one
-// for each 8 tokens.
-void qk_bwd_blocks(QkParams& p, int num_sms) {
-  const int64_t tokens = (int64_t)p.batch * p.seqlen;
-  const int64_t heads = p.side[0].heads + p.side[1].heads;
-  for (int s = 0; s < 2; ++s) {
-    int64_t n = heads ? (2 * (int64_t)num_sms * p.side[s].heads + heads / 2) / heads : 0;
-    const int64_t most = (tokens * p.side[s].heads + 7) / 8;
-    if (n > most) n = most;
-    p.blocks[s] = p.side[s].heads > 0 ? (int)(n > 1 ? n : 1) : 0;
-  }
-}
+bool qk_bwd_blocks(QkParams& p, int num_sms) { return share_blocks(p, num_sms * 4, slots_of(p.d)); }
 
 cudaError_t launch_qk_bwd(const QkParams& p, bool bf16, cudaStream_t st) {
-  return bf16 ? bwd_dispatch<true>(p, st) : bwd_dispatch<false>(p, st);
+  return bf16 ? dispatch<true>(p, false, st) : dispatch<false>(p, false, st);
 }
 
 }  // namespace attn
