@@ -193,20 +193,33 @@ __device__ __forceinline__ RowLane row_lane(const KvRowsParams& p) {
   return r;
 }
 
-// Slot of token t: < 0 means "leave the row alone"; out of range is flagged.
-__device__ __forceinline__ int slot_of(const KvRowsParams& p, int t) {
-  const int s = __ldg(p.slots + t);
-  if (s >= 0 && (s >> p.c.page_shift) >= p.c.num_pages) {
-    if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
-    return -1;
+// Where a lane's word and its group's scale lie in the cache.
+struct CacheLane {
+  uint8_t* codes;     // of row 0 of the lane's head in page 0
+  uint8_t* scales;
+  uint32_t page_codes, page_scales;  // bytes of a page (below 2^31: 2^16 heads, 2^8 rows, 2^7 bytes)
+  uint32_t row_codes, row_scales;    // of a row
+  __device__ __forceinline__ uint32_t* word(const Kv4& c, int slot) const {
+    return reinterpret_cast<uint32_t*>(codes + (uint64_t)(uint32_t)(slot >> c.page_shift) * page_codes +
+                                       (uint32_t)(slot & (c.page_size - 1)) * row_codes);
   }
-  return s;
-}
-
-// Row of the cache arrays at (slot, the lane's head).
-__device__ __forceinline__ int64_t cache_row(const Kv4& c, int slot, const RowLane& r) {
-  return (int64_t)(slot >> c.page_shift) * (c.heads * c.page_size) + r.head_row +
-         (slot & (c.page_size - 1));
+  __device__ __forceinline__ uint16_t* scale(const Kv4& c, int slot) const {
+    return reinterpret_cast<uint16_t*>(scales + (uint64_t)(uint32_t)(slot >> c.page_shift) * page_scales +
+                                       (uint32_t)(slot & (c.page_size - 1)) * row_scales);
+  }
+};
+__device__ __forceinline__ CacheLane cache_lane(const KvRowsParams& p, const RowLane& r, uint32_t odd) {
+  CacheLane c;
+  c.row_codes = (uint32_t)r.groups * 16u;
+  c.row_scales = (uint32_t)r.groups * 2u;
+  const uint32_t rows = (uint32_t)(p.c.heads * p.c.page_size);
+  c.page_codes = rows * c.row_codes;
+  c.page_scales = rows * c.row_scales;
+  // word of the lane in a row (two half-words of one r for V)
+  const int at = r.is_k ? r.c * r.groups + r.g : ((2 * r.c + (int)odd) * r.groups + (r.g & ~1)) / 2;
+  c.codes = (r.is_k ? p.c.k_codes : p.c.v_codes) + r.head_row * c.row_codes + 4 * at;
+  c.scales = (uint8_t*)((r.is_k ? p.c.k_scales : p.c.v_scales) + r.head_row * r.groups + r.g);
+  return c;
 }
 
 // The two elements of a 16-bit pair, in FP32.
@@ -248,13 +261,14 @@ __device__ __forceinline__ uint32_t codes_of(const uint4& x, float s) {
 
 // The same for scales below the normal range (and for zero): by division.
 template <bool BF16>
-__device__ __noinline__ uint32_t tiny_codes_of(const uint4& x, float s) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+__device__ __noinline__ uint32_t tiny_codes_of(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3,
+                                               float s) {
   uint32_t word = 0x88888888u;  // codes of zeros
   if (s > 0.0f) {
     word = 0u;
     for (int e = 0; e < 8; ++e) {
-      const float v = Pack<BF16>::to_f((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+      const uint32_t w = e < 2 ? w0 : e < 4 ? w1 : e < 6 ? w2 : w3;
+      const float v = Pack<BF16>::to_f((uint16_t)(w >> (16 * (e & 1))));
       const float t = rintf(__fdiv_rn(v, s));
       word |= (uint32_t)((int)fminf(fmaxf(t, -7.0f), 7.0f) + 8) << (4 * e);
     }
@@ -262,61 +276,77 @@ __device__ __noinline__ uint32_t tiny_codes_of(const uint4& x, float s) {
   return word;
 }
 
+// Rows come through a ring of asynchronous copies, kRing tokens deep; a thread
+// copies and reads its own vectors alone.
 template <bool BF16>
-__global__ void __launch_bounds__(256) attn_kv_write_kernel(const __grid_constant__ KvRowsParams p) {
+__global__ void __launch_bounds__(256, 4) attn_kv_write_kernel(const __grid_constant__ KvRowsParams p) {
+  constexpr int kRing = 8;
+  __shared__ uint4 ring[kRing][256];
+  __shared__ int ring_slot[kRing][256];
   const RowLane r = row_lane(p);
-  constexpr int kU = 4;
-  const int lane = threadIdx.x & 31;
-  const uint16_t* base = (const uint16_t*)(r.is_k ? p.k : p.v) + r.in_row;
-  uint8_t* codes = r.is_k ? p.c.k_codes : p.c.v_codes;
-  uint16_t* scales = (r.is_k ? p.c.k_scales : p.c.v_scales) + r.g;
-  const uint32_t odd = (uint32_t)(lane >> 2) & 1u;  // odd group of a pair
-  // byte of the lane's word in a row of codes
-  const int at = 4 * (r.is_k ? r.c * r.groups + r.g : ((2 * r.c + (int)odd) * r.groups + (r.g & ~1)) / 2);
-  const int row_bytes = r.groups * 16;
+  const uint32_t odd = (uint32_t)(threadIdx.x >> 2) & 1u;  // odd group of a pair
+  const CacheLane at = cache_lane(p, r, odd);
+  const uint16_t* src = (const uint16_t*)(r.is_k ? p.k : p.v) + r.in_row + (int64_t)r.token * r.stride;
+  const int64_t src_step = (int64_t)r.step * r.stride;
+  int next = r.token;  // the next token to copy
+  auto copy = [&](int s) {
+    if (r.live && next < p.tokens) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&ring[s][threadIdx.x])),
+                   "l"((uint64_t)__cvta_generic_to_global(src)) : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&ring_slot[s][threadIdx.x])),
+                   "l"((uint64_t)__cvta_generic_to_global(p.slots + next)) : "memory");
+    }
+    next += r.step;
+    src += src_step;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) copy(i);
+  int s = 0;
   // the lanes of a warp stay together: they exchange words
-  for (int t0 = r.token; __any_sync(0xffffffffu, r.live && t0 < p.tokens); t0 += r.step * kU) {
-    uint4 x[kU];
-    int slot[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int64_t t = (int64_t)t0 + (int64_t)u * r.step;
-      const bool here = r.live && t < p.tokens;
-      slot[u] = here ? slot_of(p, (int)t) : -1;
-      x[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (here) x[u] = *reinterpret_cast<const uint4*>(base + t * r.stride);
+  for (int t = r.token; __any_sync(0xffffffffu, r.live && t < p.tokens); t += r.step) {
+    copy((s + kRing - 1) % kRing);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    const bool here = r.live && t < p.tokens;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    int slot = -1;
+    if (here) x = ring[s][threadIdx.x], slot = ring_slot[s][threadIdx.x];
+    s = (s + 1) % kRing;
+    if (slot >= 0 && (slot >> p.c.page_shift) >= p.c.num_pages) {
+      if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+      slot = -1;
     }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      // max|x| of the group of 32: the bit patterns of magnitudes are ordered,
-      // infinities and NaN above all finite ones
-      uint32_t m = __vmaxu2(__vmaxu2(x[u].x & 0x7fff7fffu, x[u].y & 0x7fff7fffu),
-                            __vmaxu2(x[u].z & 0x7fff7fffu, x[u].w & 0x7fff7fffu));
-      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      m = max(m & 0xffffu, m >> 16);
-      uint32_t word = 0x88888888u;
-      uint16_t sbits = 0x7fffu;  // a group with an infinity or a NaN: NaN
-      if (m < (BF16 ? 0x7f80u : 0x7c00u)) {
-        // max / 7 as the division rounds it: the product corrected by its remainder
-        const float amax = Pack<BF16>::to_f((uint16_t)m);
-        float q = amax * (1.0f / 7.0f);
-        q = amax < 1e-30f ? __fdiv_rn(amax, 7.0f) : fmaf(fmaf(-q, 7.0f, amax), 1.0f / 7.0f, q);
-        const __nv_bfloat16 sb = __float2bfloat16_rn(q);
-        sbits = __bfloat16_as_ushort(sb);
-        const float s = __bfloat162float(sb);
-        word = s < 1e-30f ? tiny_codes_of<BF16>(x[u], s) : codes_of<BF16>(x[u], s);
-      }
-      // V rows: two neighbouring groups exchange halves, so that each lane
-      // holds the half-words (r, g), (r, g + 1) of one word
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? word & 0xffffu : word >> 16, 4);
-      if (slot[u] < 0) continue;
-      if (!r.is_k) word = odd ? (other | (word & 0xffff0000u)) : ((word & 0xffffu) | (other << 16));
-      const int64_t row = cache_row(p.c, slot[u], r);
-      *reinterpret_cast<uint32_t*>(codes + row * row_bytes + at) = word;
-      if (r.c == 0) scales[row * r.groups] = sbits;
+    // max|x| of the group of 32: the bit patterns of magnitudes are ordered,
+    // infinities and NaN above all finite ones
+    uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                          __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = max(m & 0xffffu, m >> 16);
+    // max / 7 as the division rounds it: the product corrected by its remainder
+    const float amax = Pack<BF16>::to_f((uint16_t)m);
+    float q = amax * (1.0f / 7.0f);
+    q = fmaf(fmaf(-q, 7.0f, amax), 1.0f / 7.0f, q);
+    __nv_bfloat16 sb = __float2bfloat16_rn(q);
+    uint16_t sbits = __bfloat16_as_ushort(sb);
+    uint32_t word = codes_of<BF16>(x, __bfloat162float(sb));
+    if (amax < 1e-29f) {  // zeros, and numbers so small that 1 / s or a remainder is not normal
+      sb = __float2bfloat16_rn(__fdiv_rn(amax, 7.0f));
+      sbits = __bfloat16_as_ushort(sb);
+      word = tiny_codes_of<BF16>(x.x, x.y, x.z, x.w, __bfloat162float(sb));
+    } else if (m >= (BF16 ? 0x7f80u : 0x7c00u)) {  // a group with an infinity or a NaN: NaN
+      sbits = 0x7fffu;
+      word = 0x88888888u;
     }
+    // V rows: two neighbouring groups exchange halves, so that each lane
+    // holds the half-words (r, g), (r, g + 1) of one word
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? word & 0xffffu : word >> 16, 4);
+    if (slot < 0) continue;
+    if (!r.is_k) word = odd ? (other | (word & 0xffff0000u)) : ((word & 0xffffu) | (other << 16));
+    *at.word(p.c, slot) = word;
+    if (r.c == 0) *at.scale(p.c, slot) = sbits;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // The values of a word's 8 codes: (c - 8) s, rounded once.
@@ -349,47 +379,57 @@ __device__ __forceinline__ uint4 values_of(uint32_t w, uint16_t sbits) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// kU tokens at a time: while their values are computed, the codes of the next
+// kU are on their way, and the slots of those after them.
 template <bool BF16>
-__global__ void __launch_bounds__(256) attn_kv_read_kernel(const __grid_constant__ KvRowsParams p) {
-  const RowLane r = row_lane(p);
+__global__ void __launch_bounds__(256, 4) attn_kv_read_kernel(const __grid_constant__ KvRowsParams p) {
   constexpr int kU = 4;
-  const int lane = threadIdx.x & 31;
-  uint16_t* base = (uint16_t*)(r.is_k ? p.k : p.v) + r.in_row;
-  const uint8_t* codes = r.is_k ? p.c.k_codes : p.c.v_codes;
-  const uint16_t* scales = (r.is_k ? p.c.k_scales : p.c.v_scales) + r.g;
-  const uint32_t odd = (uint32_t)(lane >> 2) & 1u;
-  const int at = 4 * (r.is_k ? r.c * r.groups + r.g : ((2 * r.c + (int)odd) * r.groups + (r.g & ~1)) / 2);
-  const int row_bytes = r.groups * 16;
-  for (int t0 = r.token; __any_sync(0xffffffffu, r.live && t0 < p.tokens); t0 += r.step * kU) {
-    uint32_t word[kU];
-    uint16_t sc[kU];
-    int slot[kU];
+  const RowLane r = row_lane(p);
+  const uint32_t odd = (uint32_t)(threadIdx.x >> 2) & 1u;
+  const CacheLane at = cache_lane(p, r, odd);
+  uint16_t* dst = (uint16_t*)(r.is_k ? p.k : p.v) + r.in_row + (int64_t)r.token * r.stride;
+  const int64_t dst_step = (int64_t)r.step * r.stride;
+  int slot[kU], slot1[kU], slot2[kU];  // of this group of tokens, the next, the one after
+  uint32_t word[kU], word1[kU];
+  uint16_t sc[kU], sc1[kU];
+  auto slots = [&](int t0, int (&s)[kU]) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int64_t t = (int64_t)t0 + (int64_t)u * r.step;
-      slot[u] = r.live && t < p.tokens ? slot_of(p, (int)t) : -1;
+      s[u] = r.live && t < p.tokens ? __ldg(p.slots + t) : -1;
     }
+  };
+  auto codes = [&](int (&s)[kU], uint32_t (&w)[kU], uint16_t (&c)[kU]) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      word[u] = 0u;
-      sc[u] = 0;
-      if (slot[u] >= 0) {
-        const int64_t row = cache_row(p.c, slot[u], r);
-        word[u] = *reinterpret_cast<const uint32_t*>(codes + row * row_bytes + at);
-        sc[u] = scales[row * r.groups];
+      w[u] = 0u;
+      c[u] = 0;
+      if (s[u] >= 0 && (s[u] >> p.c.page_shift) >= p.c.num_pages) {
+        if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+        s[u] = -1;
       }
+      if (s[u] >= 0) w[u] = *at.word(p.c, s[u]), c[u] = *at.scale(p.c, s[u]);
     }
+  };
+  const int group = r.step * kU;
+  slots(r.token, slot);
+  slots(r.token + group, slot1);
+  codes(slot, word, sc);
+  for (int t0 = r.token; __any_sync(0xffffffffu, r.live && t0 < p.tokens); t0 += group) {
+    slots(t0 + 2 * group, slot2);
+    codes(slot1, word1, sc1);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       // a V lane of the even group holds (r, g), (r, g + 1) for r = 2c, one of
       // the odd group those for r = 2c + 1
       uint32_t w = word[u];
       const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w & 0xffffu : w >> 16, 4);
-      if (slot[u] < 0) continue;
       if (!r.is_k) w = odd ? (other | (w & 0xffff0000u)) : ((w & 0xffffu) | (other << 16));
-      const int64_t t = (int64_t)t0 + (int64_t)u * r.step;
-      *reinterpret_cast<uint4*>(base + t * r.stride) = values_of<BF16>(w, sc[u]);
+      if (slot[u] >= 0) *reinterpret_cast<uint4*>(dst) = values_of<BF16>(w, sc[u]);
+      dst += dst_step;
     }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) slot[u] = slot1[u], slot1[u] = slot2[u], word[u] = word1[u], sc[u] = sc1[u];
   }
 }
 
@@ -399,7 +439,7 @@ dim3 rows_grid(const KvRowsParams& p, int num_sms) {
   const int64_t many = per >= 256u ? 1 : 256u / per;
   const unsigned y = (per + 255u) / 256u;
   int64_t x = (p.tokens + many - 1) / many;
-  const int64_t cap = std::max<int64_t>((int64_t)num_sms * 8 / y, 1);
+  const int64_t cap = std::max<int64_t>((int64_t)num_sms * 4 / y, 1);
   if (x > cap) x = cap;
   return dim3((unsigned)x, y);
 }

@@ -167,9 +167,10 @@ __device__ __forceinline__ float row_sum(uint64_t v) {
   return s;
 }
 
-__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
-               "l"((uint64_t)__cvta_generic_to_global(src))
+// A copy of 16 bytes, or of zeros.
+__device__ __forceinline__ void copy16(uint4* dst, const void* src, bool here) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
+               "l"((uint64_t)__cvta_generic_to_global(src)), "r"(here ? 16 : 0)
                : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -178,8 +179,6 @@ __device__ __forceinline__ void copies_wait() {  // all but the last N groups of
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A job is one token and one run of kSlots * U of its heads, of one side; the
-// side's blocks share its jobs, a warp takes every (blocks * warps)-th.
 constexpr int kQkThreads = 128, kQkWarps = kQkThreads / 32;
 constexpr int kPad = -1, kNoAngle = -2;  // positions: padding; outside the tables
 
@@ -188,124 +187,166 @@ __device__ __forceinline__ int token_position(const QkParams& p, uint32_t tok) {
   return pos < 0 ? kPad : pos >= p.max_pos && p.rot > 0 ? kNoAngle : pos;
 }
 
-// What both directions share: the ring.  NV vectors a lane and job (of x, and
-// of dz), the job's token and its position.
-template <int D, int U, int NV, int STAGES>
+// A job is one token and one run of kSlots * U of its heads, of one side; the
+// side's blocks share its jobs, a warp takes every (blocks * warps)-th.  A
+// lane's view of the side's tensors: byte offsets from its vector a of its row
+// (slot) of the first run.
+struct QkLane {
+  int64_t b, t, run, u;  // of a sequence, a token, a run, kSlots heads
+  __device__ __forceinline__ int64_t at(uint32_t bi, uint32_t ti, uint32_t ri) const {
+    return (int64_t)bi * b + (int64_t)ti * t + (int64_t)ri * run;
+  }
+};
+template <int SLOTS, int U>
+__device__ __forceinline__ QkLane qk_lane(int64_t sb, int64_t st, int64_t sh) {
+  return QkLane{sb * 2, st * 2, sh * (2 * SLOTS * U), sh * (2 * SLOTS)};
+}
+
+// The ring: NV vectors a lane and row (of x, and of dz), the job's token and
+// its position.
+template <int U, int NV, int STAGES>
 struct QkRing {
-  uint4 v[STAGES][U * NV][kQkThreads];
+  uint4 v[STAGES][U][NV][kQkThreads];
   uint32_t tok[STAGES][kQkWarps];
   int pos[STAGES][kQkWarps];
 };
 
-// Copies the vectors of a lane's unit of `U` rows of one token.
-template <int U, int SLOTS, int NV, typename Stage>
-__device__ __forceinline__ void copy_rows(Stage& st, int off, const uint16_t* row0, int64_t head_stride,
-                                          int h0, int heads, bool active, int va, int vb) {
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * SLOTS;
-    if (h < heads && active) {
-      const uint4* row = reinterpret_cast<const uint4*>(row0 + (int64_t)h * head_stride);
-      copy16(&st[u * NV + off][threadIdx.x], row + va);
-      copy16(&st[u * NV + off + 1][threadIdx.x], row + vb);
+// What both directions share: which jobs a warp has, and copying the next one.
+template <int D, int U, int NV, int STAGES>
+struct QkWarp {
+  using S = QkShape<D>;
+  const QkParams& p;
+  const QkSide& sd;
+  QkRing<U, NV, STAGES>& ring;
+  int warp, lane, slot;
+  bool active;
+  FastDiv runs;
+  uint32_t end, step, next;
+  int next_pos;
+  const char *x, *dz;
+  QkLane lx, lz;
+  int vb;  // bytes from vector a to b
+
+  __device__ __forceinline__ QkWarp(const QkParams& p_, QkRing<U, NV, STAGES>& r_, bool is_k, int a, int b)
+      : p(p_), sd(p_.side[is_k ? 1 : 0]), ring(r_) {
+    lane = threadIdx.x & 31;
+    warp = threadIdx.x >> 5;
+    slot = lane / S::kLpr;
+    active = lane % S::kLpr < S::kUnits;
+    runs = p.runs[is_k ? 1 : 0];
+    end = (uint32_t)p.batch * p.seq_div.d * runs.d;  // below 2^31, checked at launch
+    step = (uint32_t)p.blocks[is_k ? 1 : 0] * kQkWarps;
+    next = (blockIdx.x - (is_k ? (uint32_t)p.blocks[0] : 0u)) * kQkWarps + warp;
+    next_pos = next < end ? token_position(p, runs.div(next)) : kPad;
+    x = (const char*)sd.x + ((int64_t)slot * sd.x_h + a * 8) * 2;
+    lx = qk_lane<S::kSlots, U>(sd.x_b, sd.x_t, sd.x_h);
+    if (NV == 4) {
+      dz = (const char*)sd.dz + ((int64_t)slot * sd.dz_h + a * 8) * 2;
+      lz = qk_lane<S::kSlots, U>(sd.dz_b, sd.dz_t, sd.dz_h);
     }
+    vb = (b - a) * 16;
   }
-}
+  // Row groups of a run that hold a head, and whether this lane's row of group u does.
+  __device__ __forceinline__ int groups(uint32_t run) const {
+    return min(U, (sd.heads - (int)run * (S::kSlots * U) + S::kSlots - 1) / S::kSlots);
+  }
+  __device__ __forceinline__ bool here(uint32_t run, int u) const {
+    return active && (int)run * (S::kSlots * U) + u * S::kSlots + slot < sd.heads;
+  }
+  __device__ __forceinline__ void copy(int s) {
+    if (next < end) {
+      const uint32_t tok = runs.div(next), run = next - tok * runs.d;
+      if (next_pos != kPad) {
+        const uint32_t b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
+        const char* px = x + lx.at(b, t, run);
+        const char* pz = NV == 4 ? dz + lz.at(b, t, run) : nullptr;
+        const int n = groups(run);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (u >= n) break;
+          const bool is = here(run, u);  // (else the address is not used)
+          uint4(*v)[kQkThreads] = ring.v[s][u];
+          copy16(&v[0][threadIdx.x], is ? px : x, is);
+          copy16(&v[1][threadIdx.x], is ? px + vb : x, is);
+          px += lx.u;
+          if (NV == 4) {
+            copy16(&v[NV - 2][threadIdx.x], is ? pz : x, is);
+            copy16(&v[NV - 1][threadIdx.x], is ? pz + vb : x, is);
+            pz += lz.u;
+          }
+        }
+      }
+      if (lane == 0) ring.tok[s][warp] = tok, ring.pos[s][warp] = next_pos;
+      next += step;
+      if (next < end) next_pos = token_position(p, runs.div(next));
+    }
+    copies_end();
+  }
+};
 
 // ----------------------------------------------------------------- forward
 template <bool BF16, int D, int U, bool INTER>
 __global__ void __launch_bounds__(kQkThreads, 6) attn_qk_fwd_kernel(
     const __grid_constant__ QkParams p) {
   using S = QkShape<D>;
-  constexpr int kStages = 3;
-  __shared__ QkRing<D, U, 2, kStages> ring;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / S::kLpr, l = lane % S::kLpr;
-  const bool is_k = (int)blockIdx.x >= p.blocks[0], active = l < S::kUnits;
-  const QkSide& sd = p.side[is_k ? 1 : 0];
-  const int blk = is_k ? (int)blockIdx.x - p.blocks[0] : (int)blockIdx.x;
-  const FastDiv runs = p.runs[is_k ? 1 : 0];  // of a token; jobs: below 2^31, checked at launch
-  const uint32_t end = (uint32_t)p.batch * p.seq_div.d * runs.d;
-  const uint32_t step = (uint32_t)p.blocks[is_k ? 1 : 0] * kQkWarps, job0 = (uint32_t)blk * kQkWarps + warp;
+  constexpr int kStages = 2;
+  __shared__ QkRing<U, 2, kStages> ring;
+  const int l = min((int)(threadIdx.x & 31) % S::kLpr, S::kUnits - 1);
   int va, vb;
-  unit_vectors(active ? l : 0, p.rot, S::kUnits, va, vb);
-  Pairs w;
-  {
-    float a[8], b[8];
-    load_weights<BF16>(p, sd.w, va, a);
-    load_weights<BF16>(p, sd.w, vb, b);
-    w = pairs_of<INTER>(a, b);
-  }
-  uint32_t next = job0;  // the next job to copy
-  int next_pos = next < end ? token_position(p, runs.div(next)) : kPad;
-  auto copy = [&](int s) {
-    if (next < end) {
-      const uint32_t tok = runs.div(next), b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
-      const int h0 = (int)(next - tok * runs.d) * (S::kSlots * U) + slot;
-      if (next_pos != kPad)
-        copy_rows<U, S::kSlots, 2>(ring.v[s], 0, (const uint16_t*)sd.x + b * sd.x_b + t * sd.x_t, sd.x_h, h0,
-                                   sd.heads, active, va, vb);
-      if (lane == 0) ring.tok[s][warp] = tok, ring.pos[s][warp] = next_pos;
-      next += step;
-      if (next < end) next_pos = token_position(p, runs.div(next));
-    }
-    copies_end();
-  };
+  unit_vectors(l, p.rot, S::kUnits, va, vb);
+  QkWarp<D, U, 2, kStages> w(p, ring, (int)blockIdx.x >= p.blocks[0], va, vb);
+  char* out = (char*)w.sd.out + ((int64_t)w.slot * w.sd.o_h + va * 8) * 2;
+  const QkLane lo = qk_lane<S::kSlots, U>(w.sd.o_b, w.sd.o_t, w.sd.o_h);
+  uint32_t job = w.next;
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) copy(i);
-  int s = 0;
-  for (uint32_t job = job0; job < end; job += step) {
-    copy(s == 0 ? kStages - 1 : s - 1);  // the stage used last
+  for (int i = 0; i < kStages - 1; ++i) w.copy(i);
+  for (int s = 0; job < w.end; job += w.step, s = s == kStages - 1 ? 0 : s + 1) {
+    __syncwarp();
+    w.copy(s == 0 ? kStages - 1 : s - 1);  // the stage used last
     copies_wait<kStages - 1>();
     __syncwarp();
-    const uint32_t tok = ring.tok[s][warp];
-    const int pos = ring.pos[s][warp];
-    if (pos != kPad) {
-      if (pos == kNoAngle && lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
-      uint64_t pc[4], ps[4], qc[4], qs[4];  // weights times cosines and sines
-      load_angles(p, pos < 0 ? 0 : pos, active ? l : 0, va, vb, pc, ps);
+    const uint32_t tok = ring.tok[s][w.warp];
+    const int pos = ring.pos[s][w.warp];
+    if (pos == kPad) continue;
+    if (pos == kNoAngle && w.lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+    uint64_t pc[4], ps[4], qc[4], qs[4];  // weights times cosines and sines
+    {
+      float fa[8], fb[8];
+      load_weights<BF16>(p, w.sd.w, va, fa);
+      load_weights<BF16>(p, w.sd.w, vb, fb);
+      const Pairs wt = pairs_of<INTER>(fa, fb);
+      load_angles(p, pos < 0 ? 0 : pos, l, va, vb, pc, ps);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        qc[i] = f2_mul(w.q[i], pc[i]);
-        qs[i] = f2_neg(f2_mul(w.q[i], ps[i]));
-        pc[i] = f2_mul(w.p[i], pc[i]);
-        ps[i] = f2_mul(w.p[i], ps[i]);
-      }
-      const int h0 = (int)(job - tok * runs.d) * (S::kSlots * U) + slot;
-      const uint32_t b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
-      uint16_t* out0 = (uint16_t*)sd.out + b * sd.o_b + t * sd.o_t;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * S::kSlots;
-        const bool here = h < sd.heads && active;
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        const Pairs x = unpack<BF16, INTER>(here ? ring.v[s][2 * u][threadIdx.x] : zero,
-                                            here ? ring.v[s][2 * u + 1][threadIdx.x] : zero);
-        float r = 1.0f;
-        if (p.norm) {
-          uint64_t ss = f2_mul(x.p[0], x.p[0]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i) ss = f2_fma(x.p[i], x.p[i], ss);
-            ss = f2_fma(x.q[i], x.q[i], ss);
-          }
-          r = rsqrtf(row_sum<S::kLpr>(ss) * (1.0f / D) + p.eps);
-        }
-        if (pos == kNoAngle) r = __int_as_float(0x7fffffff);  // NaN
-        const uint64_t r2 = f2_both(r);
-        Pairs z;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z.p[i] = f2_mul(r2, f2_fma(x.q[i], qs[i], f2_mul(x.p[i], pc[i])));
-          z.q[i] = f2_mul(r2, f2_fma(x.p[i], ps[i], f2_mul(x.q[i], qc[i])));
-        }
-        if (here) {
-          uint4* out = reinterpret_cast<uint4*>(out0 + (int64_t)h * sd.o_h);
-          pack<BF16, INTER>(z, out[va], out[vb]);
-        }
+        qc[i] = f2_mul(wt.q[i], pc[i]);
+        qs[i] = f2_neg(f2_mul(wt.q[i], ps[i]));
+        pc[i] = f2_mul(wt.p[i], pc[i]);
+        ps[i] = f2_mul(wt.p[i], ps[i]);
       }
     }
-    __syncwarp();
-    s = s == kStages - 1 ? 0 : s + 1;
+    const uint32_t run = job - tok * w.runs.d, b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
+    char* po = out + lo.at(b, t, run);
+    const int n = w.groups(run);
+#pragma unroll 1
+    for (int u = 0; u < n; ++u, po += lo.u) {
+      const Pairs x = unpack<BF16, INTER>(ring.v[s][u][0][threadIdx.x], ring.v[s][u][1][threadIdx.x]);
+      float r = 1.0f;
+      if (p.norm) {
+        uint64_t ss = f2_mul(x.p[0], x.p[0]), st = f2_mul(x.q[0], x.q[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) ss = f2_fma(x.p[i], x.p[i], ss), st = f2_fma(x.q[i], x.q[i], st);
+        r = rsqrtf(row_sum<S::kLpr>(f2_add(ss, st)) * (1.0f / D) + p.eps);
+      }
+      if (pos == kNoAngle) r = __int_as_float(0x7fffffff);  // NaN
+      const uint64_t r2 = f2_both(r);
+      Pairs z;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        z.p[i] = f2_mul(r2, f2_fma(x.q[i], qs[i], f2_mul(x.p[i], pc[i])));
+        z.q[i] = f2_mul(r2, f2_fma(x.p[i], ps[i], f2_mul(x.q[i], qc[i])));
+      }
+      if (w.here(run, u)) pack<BF16, INTER>(z, *(uint4*)po, *(uint4*)(po + w.vb));
+    }
   }
   copies_wait<0>();
 }
@@ -319,107 +360,76 @@ template <bool BF16, int D, int U, bool INTER>
 __global__ void __launch_bounds__(kQkThreads, 4) attn_qk_bwd_kernel(
     const __grid_constant__ QkParams p) {
   using S = QkShape<D>;
-  constexpr int kStages = 3;
-  __shared__ QkRing<D, U, 4, kStages> ring;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / S::kLpr, l = lane % S::kLpr;
-  const bool is_k = (int)blockIdx.x >= p.blocks[0], active = l < S::kUnits;
-  const QkSide& sd = p.side[is_k ? 1 : 0];
-  const int blk = is_k ? (int)blockIdx.x - p.blocks[0] : (int)blockIdx.x;
-  const FastDiv runs = p.runs[is_k ? 1 : 0];  // of a token; jobs: below 2^31, checked at launch
-  const uint32_t end = (uint32_t)p.batch * p.seq_div.d * runs.d;
-  const uint32_t step = (uint32_t)p.blocks[is_k ? 1 : 0] * kQkWarps, job0 = (uint32_t)blk * kQkWarps + warp;
+  constexpr int kStages = 2;
+  __shared__ QkRing<U, 4, kStages> ring;
+  const int l = min((int)(threadIdx.x & 31) % S::kLpr, S::kUnits - 1);
   int va, vb;
-  unit_vectors(active ? l : 0, p.rot, S::kUnits, va, vb);
-  Pairs w, dw;
+  unit_vectors(l, p.rot, S::kUnits, va, vb);
+  QkWarp<D, U, 4, kStages> w(p, ring, (int)blockIdx.x >= p.blocks[0], va, vb);
+  char* out = (char*)w.sd.out + ((int64_t)w.slot * w.sd.o_h + va * 8) * 2;
+  const QkLane lo = qk_lane<S::kSlots, U>(w.sd.o_b, w.sd.o_t, w.sd.o_h);
+  Pairs wt, dw;
   {
-    float a[8], b[8];
-    load_weights<BF16>(p, sd.w, va, a);
-    load_weights<BF16>(p, sd.w, vb, b);
-    w = pairs_of<INTER>(a, b);
+    float fa[8], fb[8];
+    load_weights<BF16>(p, w.sd.w, va, fa);
+    load_weights<BF16>(p, w.sd.w, vb, fb);
+    wt = pairs_of<INTER>(fa, fb);
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw.p[i] = dw.q[i] = f2_both(0.0f);
   }
-  uint32_t next = job0;
-  int next_pos = next < end ? token_position(p, runs.div(next)) : kPad;
-  auto copy = [&](int s) {
-    if (next < end) {
-      const uint32_t tok = runs.div(next), b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
-      const int h0 = (int)(next - tok * runs.d) * (S::kSlots * U) + slot;
-      if (next_pos != kPad) {
-        copy_rows<U, S::kSlots, 4>(ring.v[s], 0, (const uint16_t*)sd.x + b * sd.x_b + t * sd.x_t, sd.x_h, h0,
-                                   sd.heads, active, va, vb);
-        copy_rows<U, S::kSlots, 4>(ring.v[s], 2, (const uint16_t*)sd.dz + b * sd.dz_b + t * sd.dz_t, sd.dz_h, h0,
-                                   sd.heads, active, va, vb);
-      }
-      if (lane == 0) ring.tok[s][warp] = tok, ring.pos[s][warp] = next_pos;
-      next += step;
-      if (next < end) next_pos = token_position(p, runs.div(next));
-    }
-    copies_end();
-  };
+  uint32_t job = w.next;
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) copy(i);
-  int s = 0;
-  for (uint32_t job = job0; job < end; job += step) {
-    copy(s == 0 ? kStages - 1 : s - 1);
+  for (int i = 0; i < kStages - 1; ++i) w.copy(i);
+  for (int s = 0; job < w.end; job += w.step, s = s == kStages - 1 ? 0 : s + 1) {
+    __syncwarp();
+    w.copy(s == 0 ? kStages - 1 : s - 1);
     copies_wait<kStages - 1>();
     __syncwarp();
-    const uint32_t tok = ring.tok[s][warp];
-    const int pos = ring.pos[s][warp];
-    if (pos != kPad) {
-      if (pos == kNoAngle && lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
-      uint64_t c[4], sn[4];
-      load_angles(p, pos < 0 ? 0 : pos, active ? l : 0, va, vb, c, sn);
-      const int h0 = (int)(job - tok * runs.d) * (S::kSlots * U) + slot;
-      const uint32_t b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
-      uint16_t* out0 = (uint16_t*)sd.out + b * sd.o_b + t * sd.o_t;
+    const uint32_t tok = ring.tok[s][w.warp];
+    const int pos = ring.pos[s][w.warp];
+    if (pos == kPad) continue;
+    if (pos == kNoAngle && w.lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+    uint64_t c[4], sn[4];
+    load_angles(p, pos < 0 ? 0 : pos, l, va, vb, c, sn);
+    const uint32_t run = job - tok * w.runs.d, b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
+    char* po = out + lo.at(b, t, run);
+    const int n = w.groups(run);
+#pragma unroll 1
+    for (int u = 0; u < n; ++u, po += lo.u) {
+      const Pairs x = unpack<BF16, INTER>(ring.v[s][u][0][threadIdx.x], ring.v[s][u][1][threadIdx.x]);
+      const Pairs z = unpack<BF16, INTER>(ring.v[s][u][2][threadIdx.x], ring.v[s][u][3][threadIdx.x]);
+      Pairs dy, g;
+      uint64_t ss = f2_both(0.0f), gx = f2_both(0.0f);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * S::kSlots;
-        const bool here = h < sd.heads && active;
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        const Pairs x = unpack<BF16, INTER>(here ? ring.v[s][4 * u][threadIdx.x] : zero,
-                                            here ? ring.v[s][4 * u + 1][threadIdx.x] : zero);
-        const Pairs z = unpack<BF16, INTER>(here ? ring.v[s][4 * u + 2][threadIdx.x] : zero,
-                                            here ? ring.v[s][4 * u + 3][threadIdx.x] : zero);
-        Pairs dy, g;
-        uint64_t ss = f2_both(0.0f), gx = f2_both(0.0f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dy.p[i] = f2_fma(z.q[i], sn[i], f2_mul(z.p[i], c[i]));
-          dy.q[i] = f2_fma(z.p[i], f2_neg(sn[i]), f2_mul(z.q[i], c[i]));
-          g.p[i] = f2_mul(dy.p[i], w.p[i]);
-          g.q[i] = f2_mul(dy.q[i], w.q[i]);
-          ss = f2_fma(x.p[i], x.p[i], ss);
-          ss = f2_fma(x.q[i], x.q[i], ss);
-          gx = f2_fma(g.p[i], x.p[i], gx);
-          gx = f2_fma(g.q[i], x.q[i], gx);
-        }
-        float r = 1.0f, k = 0.0f;
-        if (p.norm) {
-          r = rsqrtf(row_sum<S::kLpr>(ss) * (1.0f / D) + p.eps);
-          k = r * r * (row_sum<S::kLpr>(gx) * (1.0f / D));
-        }
-        if (pos == kNoAngle) r = __int_as_float(0x7fffffff);
-        const uint64_t r2 = f2_both(r), k2 = f2_both(-k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dw.p[i] = f2_fma(dy.p[i], f2_mul(x.p[i], r2), dw.p[i]);
-          dw.q[i] = f2_fma(dy.q[i], f2_mul(x.q[i], r2), dw.q[i]);
-          g.p[i] = f2_mul(r2, f2_fma(x.p[i], k2, g.p[i]));
-          g.q[i] = f2_mul(r2, f2_fma(x.q[i], k2, g.q[i]));
-        }
-        if (here) {
-          uint4* out = reinterpret_cast<uint4*>(out0 + (int64_t)h * sd.o_h);
-          pack<BF16, INTER>(g, out[va], out[vb]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        dy.p[i] = f2_fma(z.q[i], sn[i], f2_mul(z.p[i], c[i]));
+        dy.q[i] = f2_fma(z.p[i], f2_neg(sn[i]), f2_mul(z.q[i], c[i]));
+        g.p[i] = f2_mul(dy.p[i], wt.p[i]);
+        g.q[i] = f2_mul(dy.q[i], wt.q[i]);
+        ss = f2_fma(x.p[i], x.p[i], ss);
+        ss = f2_fma(x.q[i], x.q[i], ss);
+        gx = f2_fma(g.p[i], x.p[i], gx);
+        gx = f2_fma(g.q[i], x.q[i], gx);
       }
+      float r = 1.0f, k = 0.0f;
+      if (p.norm) {
+        r = rsqrtf(row_sum<S::kLpr>(ss) * (1.0f / D) + p.eps);
+        k = r * r * (row_sum<S::kLpr>(gx) * (1.0f / D));
+      }
+      if (pos == kNoAngle) r = __int_as_float(0x7fffffff);
+      const uint64_t r2 = f2_both(r), k2 = f2_both(-k);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dw.p[i] = f2_fma(dy.p[i], f2_mul(x.p[i], r2), dw.p[i]);
+        dw.q[i] = f2_fma(dy.q[i], f2_mul(x.q[i], r2), dw.q[i]);
+        g.p[i] = f2_mul(r2, f2_fma(x.p[i], k2, g.p[i]));
+        g.q[i] = f2_mul(r2, f2_fma(x.q[i], k2, g.q[i]));
+      }
+      if (w.here(run, u)) pack<BF16, INTER>(g, *(uint4*)po, *(uint4*)(po + w.vb));
     }
-    __syncwarp();
-    s = s == kStages - 1 ? 0 : s + 1;
   }
   copies_wait<0>();
-  if (!sd.dw) return;
+  if (!w.sd.dw) return;
   // the block's sum of dw: over the rows a warp holds, then over its warps
   float* part = reinterpret_cast<float*>(ring.v);  // [warp][D]
   float f[16];  // as they lie in the two vectors
@@ -439,11 +449,11 @@ __global__ void __launch_bounds__(kQkThreads, 4) attn_qk_bwd_kernel(
 #pragma unroll
     for (int o = S::kLpr; o < 32; o <<= 1) f[e] += __shfl_xor_sync(0xffffffffu, f[e], o);
   __syncthreads();
-  if (slot == 0 && active)
+  if (w.slot == 0 && w.active)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      part[warp * D + va * 8 + e] = f[e];
-      part[warp * D + vb * 8 + e] = f[8 + e];
+      part[w.warp * D + va * 8 + e] = f[e];
+      part[w.warp * D + vb * 8 + e] = f[8 + e];
     }
   __syncthreads();
   for (int c = threadIdx.x; c < D; c += kQkThreads) {
@@ -476,6 +486,8 @@ __global__ void __launch_bounds__(256) attn_qk_dw_kernel(const __grid_constant__
 // ----------------------------------------------------------------- launches
 namespace {
 
+constexpr int kFwdRows = 4, kBwdRows = 2;  // groups of rows of a job
+
 // Runs of `rows` heads of each side, and its blocks: `most` in all, shared out by
 // the sides' heads; never more than the jobs keep busy.  False: too many jobs.
 bool share_blocks(QkParams& p, int most, int rows) {
@@ -499,18 +511,18 @@ int slots_of(int d) { return d == 192 ? 2 : 32 / (d / 16); }
 template <bool BF16, int D>
 cudaError_t fwd_launch(const QkParams& p, cudaStream_t st) {
   if (p.inter)
-    attn_qk_fwd_kernel<BF16, D, 2, true><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
+    attn_qk_fwd_kernel<BF16, D, kFwdRows, true><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
   else
-    attn_qk_fwd_kernel<BF16, D, 2, false><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
+    attn_qk_fwd_kernel<BF16, D, kFwdRows, false><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 template <bool BF16, int D>
 cudaError_t bwd_launch(const QkParams& p, cudaStream_t st) {
   if (p.inter)
-    attn_qk_bwd_kernel<BF16, D, 1, true><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
+    attn_qk_bwd_kernel<BF16, D, kBwdRows, true><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
   else
-    attn_qk_bwd_kernel<BF16, D, 1, false><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
+    attn_qk_bwd_kernel<BF16, D, kBwdRows, false><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!p.side[0].dw && !p.side[1].dw)) return e;
   attn_qk_dw_kernel<<<dim3(D / 32, 2), 256, 0, st>>>(p);
@@ -532,11 +544,11 @@ cudaError_t dispatch(const QkParams& p, bool fwd, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_qk_fwd(QkParams& p, bool bf16, int num_sms, cudaStream_t st) {
-  if (!share_blocks(p, num_sms * 6, 2 * slots_of(p.d))) return cudaErrorNotSupported;
+  if (!share_blocks(p, num_sms * 6, kFwdRows * slots_of(p.d))) return cudaErrorNotSupported;
   return bf16 ? dispatch<true>(p, true, st) : dispatch<false>(p, true, st);
 }
 
-bool qk_bwd_blocks(QkParams& p, int num_sms) { return share_blocks(p, num_sms * 4, slots_of(p.d)); }
+bool qk_bwd_blocks(QkParams& p, int num_sms) { return share_blocks(p, num_sms * 4, kBwdRows * slots_of(p.d)); }
 
 cudaError_t launch_qk_bwd(const QkParams& p, bool bf16, cudaStream_t st) {
   return bf16 ? dispatch<true>(p, false, st) : dispatch<false>(p, false, st);
