@@ -23,7 +23,7 @@ namespace attn {
 // kilobytes that stay in L2, and a second launch would cost more than the
 // sums): each thread takes a run of neighbouring requests, the runs' sums are
 // scanned, and the prefix sums of the tokens and of the new pages stay in
-// shared memory.  Then each block writes its share of the rows: the request
+// shared memory, with what each request holds.  Then each block writes its share of the rows: the request
 // by binary search, its page from the table or, where the page is new, from
 // the free list (so no block waits for another's table entries).
 constexpr int kPlanThreads = 256;
@@ -31,28 +31,26 @@ constexpr int kPlanThreads = 256;
 __global__ void __launch_bounds__(kPlanThreads) attn_kv_plan_kernel(
     const __grid_constant__ PlanParams p) {
   extern __shared__ int sm[];
-  int* cu = sm;                  // [batch + 1] tokens before a request
-  int* pg = sm + p.batch + 1;    // [batch + 1] new pages before it
+  int* cu = sm;                   // [batch + 1] tokens before a request
+  int* pg = cu + p.batch + 1;     // [batch + 1] new pages before it
+  int* held_by = pg + p.batch + 1;  // [batch] tokens it holds
   __shared__ int wsum[2][kPlanThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = 1 << p.page_shift;
   const int per = (p.batch + kPlanThreads - 1) / kPlanThreads;
   const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+  const int head = p.free_head ? *p.free_head : 0;
   bool bad = false;
-  // what request b holds and what it gets; one whose lengths are negative or
-  // longer than its table row counts as empty
-  auto lengths = [&](int b, int& c, int& f) {
-    c = p.ctx[b];
-    f = p.fresh[b];
-    const bool ok = c >= 0 && f >= 0 && (int64_t)c + f <= (int64_t)p.cols << p.page_shift;
-    if (!ok) c = f = 0;
-    return ok;
-  };
   int nt = 0, np = 0;
+#pragma unroll 4
   for (int b = b0; b < b1; ++b) {
-    int c, f;
-    bad |= !lengths(b, c, f);
+    // what request b holds and what it gets; one whose lengths are negative or
+    // longer than its table row counts as empty
+    int c = p.ctx[b], f = p.fresh[b];
+    const bool ok = c >= 0 && f >= 0 && (int64_t)c + f <= (int64_t)p.cols << p.page_shift;
+    if (!ok) bad = true, c = f = 0;
     cu[b] = f;
+    held_by[b] = c;
     pg[b] = p.free_pages ? ((c + f + P - 1) >> p.page_shift) - ((c + P - 1) >> p.page_shift) : 0;
     nt = (int)min((unsigned)nt + (unsigned)f, (unsigned)INT32_MAX);
     np += pg[b];
@@ -71,10 +69,12 @@ __global__ void __launch_bounds__(kPlanThreads) attn_kv_plan_kernel(
     ot = (int)min((unsigned)ot + (unsigned)wsum[0][w], (unsigned)INT32_MAX);
     op += wsum[1][w];
   }
-  st = (int)min((unsigned)ot + (unsigned)st, (unsigned)INT32_MAX);
-  sp += op;
-  const int head = p.free_head ? *p.free_head : 0;
-  int rt = st - nt, rp = sp - np;
+  // (sums of the requests before this thread's, not differences: those that
+  // stay at 2^31 - 1 could not be taken back)
+  int rt = __shfl_up_sync(0xffffffffu, st, 1), rp = __shfl_up_sync(0xffffffffu, sp, 1);
+  if (lane == 0) rt = rp = 0;
+  rt = (int)min((unsigned)ot + (unsigned)rt, (unsigned)INT32_MAX);
+  rp += op;
   for (int b = b0; b < b1; ++b) {
     const int f = cu[b], need = pg[b];
     cu[b] = rt;
@@ -82,11 +82,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_kv_plan_kernel(
     rt = (int)min((unsigned)rt + (unsigned)f, (unsigned)INT32_MAX);
     rp += need;
   }
-  if (tid == kPlanThreads - 1) {
-    cu[p.batch] = st;
-    pg[p.batch] = sp;
-    if (st > p.rows) bad = true;
-    if (p.free_pages && (head < 0 || (int64_t)head + sp > p.n_free)) bad = true;
+  if (tid == kPlanThreads - 1) {  // (without requests of its own it holds the totals too)
+    cu[p.batch] = rt;
+    pg[p.batch] = rp;
+    if (rt > p.rows) bad = true;
+    if (p.free_pages && (head < 0 || (int64_t)head + rp > p.n_free)) bad = true;
   }
   if (bad && blockIdx.x == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
   __syncthreads();
@@ -99,33 +99,41 @@ __global__ void __launch_bounds__(kPlanThreads) attn_kv_plan_kernel(
   };
   const int gtid = blockIdx.x * kPlanThreads + tid, gn = gridDim.x * kPlanThreads;
   for (int b = gtid; b < p.batch; b += gn) {
-    int c, f;
-    lengths(b, c, f);
+    const int c = held_by[b];
     p.cu[b] = cu[b];
-    p.seq[b] = c + f;
-    const int need = pg[b + 1] - pg[b], held = (c + P - 1) >> p.page_shift;
-    for (int i = 0; i < need; ++i) {
-      const int page = page_of(pg[b] + i);
-      p.table[(int64_t)b * p.table_stride + held + i] = page;
-      if (page < 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+    const int f = p.fresh[b];
+    const bool ok = p.ctx[b] == c && f >= 0 && (int64_t)c + f <= (int64_t)p.cols << p.page_shift;
+    p.seq[b] = ok ? c + f : 0;
+  }
+  // the last request whose prefix sum is <= x
+  auto request_of = [&](const int* sums, int x) {
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sums[mid] <= x) lo = mid; else hi = mid;
     }
+    return lo;
+  };
+  const int new_pages = pg[p.batch];
+  for (int i = gtid; i < new_pages; i += gn) {
+    const int b = request_of(pg, i), held = (held_by[b] + P - 1) >> p.page_shift;
+    const int page = page_of(i);
+    p.table[(int64_t)b * p.table_stride + held + i - pg[b]] = page;
+    if (page < 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
   }
   if (gtid == 0) {
     p.cu[p.batch] = cu[p.batch];
     if (p.free_head_out) *p.free_head_out = (int)min((int64_t)head + pg[p.batch], (int64_t)INT32_MAX);
   }
   const int total = min(cu[p.batch], p.rows);
+#pragma unroll 2
   for (int t = gtid; t < p.rows; t += gn) {
     int pos = -1, slot = -1;
     if (t < total) {
-      int lo = 0, hi = p.batch;  // the last request with cu <= t
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= t) lo = mid; else hi = mid;
-      }
-      const int c = p.ctx[lo], held = (c + P - 1) >> p.page_shift;
+      const int lo = request_of(cu, t);
+      const int c = held_by[lo], held = (c + P - 1) >> p.page_shift;
       pos = c + t - cu[lo];
-      const int blk = pos >> p.page_shift;  // < cols: lengths() looked
+      const int blk = pos >> p.page_shift;  // < cols, as the lengths are
       const int page = p.free_pages && blk >= held ? page_of(pg[lo] + blk - held)
                                                    : p.table[(int64_t)lo * p.table_stride + blk];
       if ((unsigned)page < (unsigned)p.num_pages)
@@ -139,9 +147,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_kv_plan_kernel(
 }
 
 cudaError_t launch_kv_plan(const PlanParams& p, int num_sms, cudaStream_t st) {
+  const size_t smem = (size_t)(p.batch + 1) * 12;
   int64_t blocks = (int64_t)(p.rows > p.batch ? p.rows : p.batch) / (kPlanThreads * 2) + 1;
-  if (blocks > 2 * num_sms) blocks = 2 * num_sms;
-  const size_t smem = (size_t)(p.batch + 1) * 8;
+  // as many as run at once (200 KB of shared memory on an SM)
+  const int64_t most = (int64_t)num_sms * std::min<int64_t>(8, std::max<int64_t>(200000 / (int64_t)(smem + 1024), 1));
+  if (blocks > most) blocks = most;
   if (smem > 40000) {  // beyond what every kernel may take
     const cudaError_t e = cudaFuncSetAttribute(
         attn_kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -282,7 +292,6 @@ template <bool BF16>
 __global__ void __launch_bounds__(256, 4) attn_kv_write_kernel(const __grid_constant__ KvRowsParams p) {
   constexpr int kRing = 8;
   __shared__ uint4 ring[kRing][256];
-  __shared__ int ring_slot[kRing][256];
   const RowLane r = row_lane(p);
   const uint32_t odd = (uint32_t)(threadIdx.x >> 2) & 1u;  // odd group of a pair
   const CacheLane at = cache_lane(p, r, odd);
@@ -290,27 +299,25 @@ __global__ void __launch_bounds__(256, 4) attn_kv_write_kernel(const __grid_cons
   const int64_t src_step = (int64_t)r.step * r.stride;
   int next = r.token;  // the next token to copy
   auto copy = [&](int s) {
-    if (r.live && next < p.tokens) {
+    if (r.live && next < p.tokens)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&ring[s][threadIdx.x])),
                    "l"((uint64_t)__cvta_generic_to_global(src)) : "memory");
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&ring_slot[s][threadIdx.x])),
-                   "l"((uint64_t)__cvta_generic_to_global(p.slots + next)) : "memory");
-    }
     next += r.step;
     src += src_step;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int i = 0; i < kRing - 1; ++i) copy(i);
-  int s = 0;
+  int s = 0, next_slot = r.live && r.token < p.tokens ? __ldg(p.slots + r.token) : -1;
   // the lanes of a warp stay together: they exchange words
   for (int t = r.token; __any_sync(0xffffffffu, r.live && t < p.tokens); t += r.step) {
     copy((s + kRing - 1) % kRing);
     asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
     const bool here = r.live && t < p.tokens;
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    int slot = -1;
-    if (here) x = ring[s][threadIdx.x], slot = ring_slot[s][threadIdx.x];
+    int slot = next_slot;  // looked up one token ahead
+    next_slot = r.live && t + r.step < p.tokens ? __ldg(p.slots + t + r.step) : -1;
+    if (here) x = ring[s][threadIdx.x];
     s = (s + 1) % kRing;
     if (slot >= 0 && (slot >> p.c.page_shift) >= p.c.num_pages) {
       if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
