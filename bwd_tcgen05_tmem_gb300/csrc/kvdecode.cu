@@ -48,10 +48,10 @@
 
 namespace attn {
 
-constexpr int kTile = 32;   // tokens of a warp's tile
+constexpr int kTile = 64;   // tokens of a warp's tile
 constexpr int kWarps = 4;   // of a block
-constexpr int kItemCost = 3;   // in tiles: what an item costs a warp besides them
-constexpr int kMinTiles = 2;   // of a warp's run
+constexpr int kItemCost = 2;   // in tiles: what an item costs a warp besides them
+constexpr int kMinTiles = 1;   // of a warp's run
 constexpr int kExpMin = -80, kExpMax = 100;  // exponents of V's scales told apart
 
 // whether 128 registers hold a lane's share
@@ -61,14 +61,13 @@ template <int DQK, int DV, int NT>
 struct DecShape {
   static constexpr int GK = DQK / 32, GV = DV / 32;
   static constexpr int kRows = 8 * NT;
-  // a tile's codes and scales in shared memory
+  // a tile's codes and scales in shared memory, K and V apart
   static constexpr int kKc = kTile * DQK / 2, kVc = kTile * DV / 2;
-  static constexpr int kKs = kTile * GK * 2, kVs = kTile * GV * 2;
-  static constexpr int kStage = kKc + kVc + kKs + kVs;  // a multiple of 128
+  static constexpr int kKslot = kKc + kTile * GK * 2, kVslot = kVc + kTile * GV * 2;
   // blocks of an SM: as many as its registers hold
   static constexpr int kBlocks = light(DV, NT) ? 4 : 2;
-  static constexpr int kStages = light(DV, NT) && DQK > 64 ? 2 : DQK >= 256 ? 2 : 3;
-  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kDepth = DQK == 64 || (!light(DV, NT) && DQK < 256) ? 2 : 1;
+  static constexpr int kRing = kWarps * kDepth * (kKslot + kVslot);
   static constexpr int kPart = kRows * (DV + 2);  // floats of a partial result
 };
 
@@ -224,95 +223,103 @@ struct Piece {
   float lim, vlim;               // kf + 1; 2^e
 };
 
-// WHOLE: every query of the block sees every token of the tile.
+// S^T of a tile, in units of the products: blocks of 16 tokens, rows r, r + 8.
+// WHOLE: every query of the block sees every token of the tile; else blocks
+// past the last token are left out.
 template <bool WHOLE, int DQK, int DV, int NT>
-__device__ __forceinline__ void do_tile(Piece<DQK, DV, NT>& z, const uint8_t* st,
-                                        const DecodeParams& p, int len, int row0, int t0, int r,
-                                        int c) {
+__device__ __forceinline__ void tile_scores(const Piece<DQK, DV, NT>& z, const uint8_t* st, int left,
+                                            int r, int c, float (&x)[kTile / 16][NT][4]) {
   using S = DecShape<DQK, DV, NT>;
-  float x[2][NT][4];  // S^T of two blocks of 16 tokens: rows r, r + 8
-  uint32_t sa[2][S::GK / 2], sb[2][S::GK / 2];
-  uint32_t ka[2][S::GK], kb[2][S::GK];
 #pragma unroll
-  for (int mt = 0; mt < 2; ++mt) {
-    const int ta = mt * 16 + row_token(r), tb = ta + 8;
-    lds_words<S::GK>(st + ta * (DQK / 2) + c * 4 * S::GK, ka[mt]);
-    lds_words<S::GK>(st + tb * (DQK / 2) + c * 4 * S::GK, kb[mt]);
-    lds_words<S::GK / 2>(st + S::kKc + S::kVc + ta * 2 * S::GK, sa[mt]);
-    lds_words<S::GK / 2>(st + S::kKc + S::kVc + tb * 2 * S::GK, sb[mt]);
-  }
+  for (int m0 = 0; m0 < kTile / 16; m0 += 2) {
+    if (!WHOLE && m0 * 16 >= left) {
 #pragma unroll
-  for (int g = 0; g < S::GK; ++g) {
-    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    float low[NT][4];  // what the codes' offset of 8 adds up to
+      for (int i = 0; i < 2 * NT * 4; ++i) x[m0 + i / (NT * 4)][i / 4 % NT][i % 4] = -INFINITY;
+      continue;
+    }
+    uint32_t sa[2][S::GK / 2], sb[2][S::GK / 2];
+    uint32_t ka[2][S::GK], kb[2][S::GK];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const uint32_t* q = z.qf[t][g];
-      mma16816(low[t], kLow8, kLow8, kHigh8, kHigh8, q[0], q[1], zero);
-      mma16816(low[t], kLow8, kLow8, kHigh8, kHigh8, q[2], q[3]);
+    for (int i = 0; i < 2; ++i) {
+      const int ta = (m0 + i) * 16 + row_token(r), tb = ta + 8;
+      lds_words<S::GK>(st + ta * (DQK / 2) + c * 4 * S::GK, ka[i]);
+      lds_words<S::GK>(st + tb * (DQK / 2) + c * 4 * S::GK, kb[i]);
+      lds_words<S::GK / 2>(st + S::kKc + ta * 2 * S::GK, sa[i]);
+      lds_words<S::GK / 2>(st + S::kKc + tb * 2 * S::GK, sb[i]);
     }
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      uint32_t a[4], b[4];
-      codes8(ka[mt][g], a);
-      codes8(kb[mt][g], b);
-      const float fa = scale_of(sa[mt], g), fb = scale_of(sb[mt], g);
+    for (int g = 0; g < S::GK; ++g) {
+      const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float low[NT][4];  // what the codes' offset of 8 adds up to
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const uint32_t* q = z.qf[t][g];
-        float acc[4];
-        mma16816(acc, a[0], b[0], a[1], b[1], q[0], q[1], low[t]);
-        mma16816(acc, a[2], b[2], a[3], b[3], q[2], q[3]);
-        x[mt][t][0] = g ? fmaf(acc[0], fa, x[mt][t][0]) : acc[0] * fa;
-        x[mt][t][1] = g ? fmaf(acc[1], fa, x[mt][t][1]) : acc[1] * fa;
-        x[mt][t][2] = g ? fmaf(acc[2], fb, x[mt][t][2]) : acc[2] * fb;
-        x[mt][t][3] = g ? fmaf(acc[3], fb, x[mt][t][3]) : acc[3] * fb;
+        mma16816(low[t], kLow8, kLow8, kHigh8, kHigh8, q[0], q[1], zero);
+        mma16816(low[t], kLow8, kLow8, kHigh8, kHigh8, q[2], q[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t a[4], b[4];
+        codes8(ka[i][g], a);
+        codes8(kb[i][g], b);
+        const float fa = scale_of(sa[i], g), fb = scale_of(sb[i], g);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint32_t* q = z.qf[t][g];
+          float acc[4];
+          float(&y)[4] = x[m0 + i][t];
+          mma16816(acc, a[0], b[0], a[1], b[1], q[0], q[1], low[t]);
+          mma16816(acc, a[2], b[2], a[3], b[3], q[2], q[3]);
+          y[0] = g ? fmaf(acc[0], fa, y[0]) : acc[0] * fa;
+          y[1] = g ? fmaf(acc[1], fa, y[1]) : acc[1] * fa;
+          y[2] = g ? fmaf(acc[2], fb, y[2]) : acc[2] * fb;
+          y[3] = g ? fmaf(acc[3], fb, y[3]) : acc[3] * fb;
+        }
       }
     }
   }
-  // ---- running softmax in base 2.  The reference of a column moves only when
-  // a score passes it by more than 1: probabilities stay below 2 (times 2^kf, and
-  // times V's scales below 2^15), and most tiles need no exchange between lanes.
-  bool move = false;
+}
+
+// Hides what the lane's columns do not see.
+template <int DQK, int DV, int NT>
+__device__ __forceinline__ void tile_mask(const DecodeParams& p, int len, int row0, int t0, int r, int c,
+                                          float (&x)[kTile / 16][NT][4]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = row0 + t * 8 + 2 * c + e;
+      const int pos = len - p.seqlen_q + row / p.group;
+      const int hi = row < p.rows ? pos : -1;
+      const int lo = p.window_left < 0 ? 0 : max(0, pos - p.window_left);
+#pragma unroll
+      for (int i = 0; i < kTile / 8; ++i) {
+        const int j = t0 + i * 8 + row_token(r);
+        if (j > hi || (j < lo && j >= p.sinks)) x[i >> 1][t][2 * (i & 1) + e] = -INFINITY;
+      }
+    }
+}
+
+// Scores to probabilities, in base 2.  The reference of a column moves only when
+// a score passes it by more than 1: probabilities stay below 2 (times 2^kf, and
+// times V's scales below 2^15), and most tiles need no exchange between lanes.
+// top: the largest V scale of this lane's tokens.
+template <int DQK, int DV, int NT>
+__device__ __forceinline__ void tile_softmax(Piece<DQK, DV, NT>& z, float top,
+                                             float (&x)[kTile / 16][NT][4]) {
+  using S = DecShape<DQK, DV, NT>;
+  bool move = top >= z.vlim;
   float mx[NT][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      if (!WHOLE) {  // the tokens that this column's query sees
-        const int row = row0 + t * 8 + 2 * c + e;
-        const int pos = len - p.seqlen_q + row / p.group;
-        const int hi = row < p.rows ? pos : -1;
-        const int lo = p.window_left < 0 ? 0 : max(0, pos - p.window_left);
+      float y = fmaxf(x[0][t][e], x[0][t][2 + e]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = t0 + i * 8 + row_token(r);
-          if (j > hi || (j < lo && j >= p.sinks)) x[i >> 1][t][2 * (i & 1) + e] = -INFINITY;
-        }
-      }
-      mx[t][e] = z.xs[t][e] * fmaxf(fmax3(x[0][t][e], x[0][t][2 + e], x[1][t][e]), x[1][t][2 + e]);
+      for (int m = 1; m < kTile / 16; ++m) y = fmax3(y, x[m][t][e], x[m][t][2 + e]);
+      mx[t][e] = z.xs[t][e] * y;
       move |= mx[t][e] + z.ref[t][e] > z.lim;
     }
-  // the largest scale (NaN apart) of the tokens that a query sees: lane i looks
-  // at token i
-  float top;
-  {
-    const int lane = r * 4 + c;
-    uint32_t w[S::GV / 2];
-    lds_words<S::GV / 2>(st + S::kKc + S::kVc + S::kKs + lane * 2 * S::GV, w);
-    __nv_bfloat162 y = *reinterpret_cast<__nv_bfloat162*>(&w[0]);
-#pragma unroll
-    for (int i = 1; i < S::GV / 2; ++i) y = __hmax2(y, *reinterpret_cast<__nv_bfloat162*>(&w[i]));
-    const uint32_t u = *reinterpret_cast<uint32_t*>(&y);
-    top = fmaxf(scale_of(&u, 0), scale_of(&u, 1));
-    if (!WHOLE) {  // a token that no query sees: its scales may be anything
-      const int j = t0 + lane;
-      const int hi = len - p.seqlen_q + (min(row0 + S::kRows, p.rows) - 1) / p.group;
-      const int lo = p.window_left < 0 ? 0 : len - p.seqlen_q + row0 / p.group - p.window_left;
-      if (j > hi || (j < lo && j >= p.sinks)) top = 0.0f;
-    }
-  }
-  move |= top >= z.vlim;
   if (__any_sync(0xffffffffu, move)) {
     const float kf_old = z.lim - 1.0f;
     float f = 1.0f;
@@ -353,11 +360,11 @@ __device__ __forceinline__ void do_tile(Piece<DQK, DV, NT>& z, const uint8_t* st
     const uint64_t xs = f2_pack(z.xs[t][0], z.xs[t][1]), ref = f2_pack(z.ref[t][0], z.ref[t][1]);
     uint64_t sum = f2_pack(z.l[t][0], z.l[t][1]);
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+    for (int m = 0; m < kTile / 16; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float& y0 = x[mt][t][2 * h];
-        float& y1 = x[mt][t][2 * h + 1];
+        float& y0 = x[m][t][2 * h];
+        float& y1 = x[m][t][2 * h + 1];
         f2_unpack(f2_fma(f2_pack(y0, y1), xs, ref), y0, y1);
         y0 = ex2(y0);
         y1 = ex2(y1);
@@ -365,19 +372,49 @@ __device__ __forceinline__ void do_tile(Piece<DQK, DV, NT>& z, const uint8_t* st
       }
     f2_unpack(sum, z.l[t][0], z.l[t][1]);
   }
-  // ---- V's scales of tokens r and r + 8 of both blocks
-  uint32_t vs[2][2][S::GV / 2];
+}
+
+// The largest V scale (NaN apart) of tokens `lane` and `lane + 32` of a tile;
+// lo, hi, sinks: tokens that no query sees do not count, their scales may be anything.
+template <bool WHOLE, int DQK, int DV, int NT>
+__device__ __forceinline__ float tile_top(const DecodeParams& p, const uint8_t* st, int len, int row0,
+                                          int t0, int lane) {
+  using S = DecShape<DQK, DV, NT>;
+  float top = 0.0f;
 #pragma unroll
-  for (int mt = 0; mt < 2; ++mt)
+  for (int h = 0; h < kTile / 32; ++h) {
+    uint32_t w[S::GV / 2];
+    lds_words<S::GV / 2>(st + S::kVc + (h * 32 + lane) * 2 * S::GV, w);
+    __nv_bfloat162 y = *reinterpret_cast<__nv_bfloat162*>(&w[0]);
+#pragma unroll
+    for (int i = 1; i < S::GV / 2; ++i) y = __hmax2(y, *reinterpret_cast<__nv_bfloat162*>(&w[i]));
+    const uint32_t u = *reinterpret_cast<uint32_t*>(&y);
+    float m = fmaxf(scale_of(&u, 0), scale_of(&u, 1));
+    if (!WHOLE) {
+      const int j = t0 + h * 32 + lane;
+      const int hi = len - p.seqlen_q + (min(row0 + S::kRows, p.rows) - 1) / p.group;
+      const int lo = p.window_left < 0 ? 0 : len - p.seqlen_q + row0 / p.group - p.window_left;
+      if (j > hi || (j < lo && j >= p.sinks)) m = 0.0f;
+    }
+    top = fmaxf(top, m);
+  }
+  return top;
+}
+
+// O^T += V^T P^T
+template <bool WHOLE, int DQK, int DV, int NT>
+__device__ __forceinline__ void tile_values(Piece<DQK, DV, NT>& z, const uint8_t* st, int left, int r,
+                                            int c, const float (&x)[kTile / 16][NT][4]) {
+  using S = DecShape<DQK, DV, NT>;
+#pragma unroll
+  for (int mt = 0; mt < kTile / 16; ++mt) {
+    if (!WHOLE && mt * 16 >= left) break;
+    uint32_t vs[2][S::GV / 2];  // scales of tokens r and r + 8
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      lds_words<S::GV / 2>(st + S::kKc + S::kVc + S::kKs +
-                               (mt * 16 + h * 8 + row_token(r)) * 2 * S::GV, vs[mt][h]);
-  // ---- O^T += V^T P^T
-#pragma unroll
-  for (int mt = 0; mt < 2; ++mt) {
+      lds_words<S::GV / 2>(st + S::kVc + (mt * 16 + h * 8 + row_token(r)) * 2 * S::GV, vs[h]);
     uint32_t v0[S::GV / 2], v1[S::GV / 2], v2[S::GV / 2], v3[S::GV / 2];
-    const uint8_t* vb = st + S::kKc + r * 2 * S::GV;
+    const uint8_t* vb = st + r * 2 * S::GV;
     const int te = mt * 16 + row_token(2 * c), to = mt * 16 + row_token(2 * c + 1);
     lds_words<S::GV / 2>(vb + te * (DV / 2), v0);
     lds_words<S::GV / 2>(vb + to * (DV / 2), v1);
@@ -389,7 +426,7 @@ __device__ __forceinline__ void do_tile(Piece<DQK, DV, NT>& z, const uint8_t* st
       uint32_t a[4], b[4];
       signed8(__byte_perm(v0[g >> 1], v1[g >> 1], sel), a);
       signed8(__byte_perm(v2[g >> 1], v3[g >> 1], sel), b);
-      const float fa = scale_of(vs[mt][0], g), fb = scale_of(vs[mt][1], g);
+      const float fa = scale_of(vs[0], g), fb = scale_of(vs[1], g);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float p0, p1, p2, p3;
@@ -552,12 +589,13 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
   }
 
   const int r = lane >> 2, c = lane & 3;
-  uint8_t* ring = smem + warp * (S::kStages * S::kStage);
-  // ---- copies.  A warp feeds its own ring, across the items of its run, by
+  uint8_t* k_ring = smem + warp * (S::kDepth * (S::kKslot + S::kVslot));
+  uint8_t* v_ring = k_ring + S::kDepth * S::kKslot;
+  // ---- copies.  A warp feeds its own slots, across the items of its run, by
   // 16-byte asynchronous copies of all its lanes (a tile of one array is one
-  // run of bytes); it waits for its own copies alone.  Where the next tile lies
-  // is looked up one tile ahead.
-  const bool small = p.c.page_size < kTile;  // a tile spans two pages
+  // run of bytes); it waits for its own copies alone.  K and V have slots of
+  // their own: the next K is on its way while V is used, and the other way
+  // round.  Where the next tile lies is looked up one tile ahead.
   if (lane == 0) {
     Cursor k;
     k.b = first_b;
@@ -572,7 +610,9 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     copy_at[warp] = work_at[warp] = k;
     strip[warp].left = 0;
   }
-  int next_page = 0;  // of the tile to copy next (its first one, where it spans two)
+  // Page of the tile to copy next: lane i's is that of its tokens 16 (i % 4) ..
+  // (all the same for pages of a tile or more).
+  int next_page = 0;
   auto look_up = [&]() {
     __syncwarp();
     if (strip[warp].left == 0) {
@@ -595,59 +635,64 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
       __syncwarp();
     }
     const int token = strip[warp].token + kTile, left = strip[warp].left - 1;
-    if (token < strip[warp].len) next_page = strip[warp].row[token >> p.c.page_shift];
+    const int len = strip[warp].len;
+    if (token < len) next_page = strip[warp].row[min(token + 16 * (lane & 3), len - 1) >> p.c.page_shift];
     __syncwarp();
     if (lane == 0) strip[warp].token = token, strip[warp].left = left;
   };
-  // Chunks of 16 bytes of a stage: K codes, V codes, scales; `half`: only those
-  // of its first (0) or last (1) 16 tokens, 2: all.
-  auto copy_rows = [&](uint8_t* st, int page, int row, int half) {
-    const int64_t at = (int64_t)page * (p.c.heads * p.c.page_size) + row - (half == 1 ? 16 : 0);
-    const uint8_t* k = p.c.k_codes + at * (DQK / 2) + lane * 16;
-    const uint8_t* v = p.c.v_codes + at * (DV / 2) + lane * 16;
-    const uint32_t dst = smem_u32(st) + lane * 16;
+  // `n` rows from row `at` of an array pair into a slot, from token `first` on.
+  auto copy_rows = [&](uint8_t* slot, int codes_end, const uint8_t* codes, const uint16_t* scales, int64_t at,
+                       int first, int n, int width, int groups) {
+    const uint8_t* src = codes + at * width + lane * 16;
+    uint32_t dst = smem_u32(slot) + first * width + lane * 16;
 #pragma unroll
-    for (int i = 0; i < DQK / 32; ++i)
-      if (half == 2 || i / (DQK / 64) == half) copy16(dst + i * 512, k + i * 512);
-#pragma unroll
-    for (int i = 0; i < DV / 32; ++i)
-      if (half == 2 || i / (DV / 64) == half) copy16(dst + S::kKc + i * 512, v + i * 512);
-#pragma unroll
-    for (int i = 0; i < (DQK + DV) / 8; i += 32) {
-      const int j = lane + i;
-      const bool is_k = j < DQK / 8;
-      const int o = is_k ? j : j - DQK / 8;
-      const uint8_t* src = is_k ? (const uint8_t*)(p.c.k_scales + at * S::GK)
-                                : (const uint8_t*)(p.c.v_scales + at * S::GV);
-      if (j < (DQK + DV) / 8 && (half == 2 || o / (is_k ? DQK / 16 : DV / 16) == half))
-        copy16(dst + S::kKc + S::kVc + i * 16, src + o * 16);
+    for (int i = 0; i < n * width / 16; i += 32) {
+      if (n * width / 16 - i >= 32 || lane < n * width / 16 - i) copy16(dst + i * 16, src + i * 16);
     }
+    src = reinterpret_cast<const uint8_t*>(scales + at * groups) + lane * 16;
+    dst = smem_u32(slot) + codes_end + first * groups * 2 + lane * 16;
+#pragma unroll
+    for (int i = 0; i < n * groups / 8; i += 32)
+      if (n * groups / 8 - i >= 32 || lane < n * groups / 8 - i) copy16(dst + i * 16, src + i * 16);
   };
-  auto copy = [&](int s) {
+  auto copy = [&](bool is_k, uint8_t* slot) {
     __syncwarp();
-    uint8_t* st = ring + s * S::kStage;
     const int token = strip[warp].token, len = strip[warp].len;
-    const int row = strip[warp].head_row + (token & (p.c.page_size - 1));
+    const int64_t row = strip[warp].head_row + (token & (p.c.page_size - 1));
+    const int page_rows = p.c.heads * p.c.page_size;
     if (token >= len) return;
-    bool bad = (unsigned)next_page >= (unsigned)p.c.num_pages;
-    if (!bad) copy_rows(st, next_page, row, small ? 0 : 2);
-    if (small && token + p.c.page_size < len) {
-      const int page = strip[warp].row[(token >> p.c.page_shift) + 1];
-      if ((unsigned)page < (unsigned)p.c.num_pages)
-        copy_rows(st, page, row, 1);
+    auto rows = [&](int page, int first, int n) {
+      const int64_t at = (int64_t)page * page_rows + row;
+      if (is_k)
+        copy_rows(slot, S::kKc, p.c.k_codes, p.c.k_scales, at, first, n, DQK / 2, S::GK);
       else
-        bad = true;
+        copy_rows(slot, S::kVc, p.c.v_codes, p.c.v_scales, at, first, n, DV / 2, S::GV);
+    };
+    bool bad = false;
+    if (p.c.page_size >= kTile) {
+      bad = (unsigned)next_page >= (unsigned)p.c.num_pages;
+      if (!bad) rows(next_page, 0, kTile);
+    } else {
+      for (int first = 0; first < kTile && token + first < len; first += p.c.page_size) {
+        const int page = __shfl_sync(0xffffffffu, next_page, first / 16);
+        if ((unsigned)page >= (unsigned)p.c.num_pages)
+          bad = true;
+        else if (p.c.page_size == 16)
+          rows(page, first, 16);
+        else
+          rows(page, first, 32);
+      }
     }
     if (bad && lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
   };
   int used = 0;
   look_up();
-  for (int i = 0; i < S::kStages; ++i) {
-    if (i < n_run) {
-      copy(i);
-      if (i + 1 < n_run) look_up();
-    }
+  for (int i = 0; i < S::kDepth; ++i) {
+    if (i < n_run) copy(true, k_ring + i * S::kKslot);
     copies_end();
+    if (i < n_run) copy(false, v_ring + i * S::kVslot);
+    copies_end();
+    if (i + 1 < n_run) look_up();
   }
   for (int pieces = 0; used < n_run; ++pieces) {
     // the piece: the run's tiles of one item
@@ -729,21 +774,37 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     const int whole_hi = pos_lo - (kTile - 1);
     const int whole_lo = p.window_left < 0 ? 0 : pos_hi - p.window_left;
     for (int v = v0; v < v1; ++v) {
-      const int s = used % S::kStages;
+      const int s = used % S::kDepth;
+      const bool more = used + S::kDepth < n_run;
       ++used;
-      copies_wait<S::kStages - 1>();
-      __syncwarp();
-      const uint8_t* st = ring + s * S::kStage;
-      const int t0 = tile_token(sr, v);
+      const int t0 = tile_token(sr, v), left = sr.len - t0;
       const bool whole = t0 <= whole_hi && (t0 >= whole_lo || t0 + kTile <= p.sinks);
-      if (whole)
-        do_tile<true>(z, st, p, sr.len, row0, t0, r, c);
-      else
-        do_tile<false>(z, st, p, sr.len, row0, t0, r, c);
+      uint8_t *ks = k_ring + s * S::kKslot, *vs = v_ring + s * S::kVslot;
+      float x[kTile / 16][NT][4], top;
+      copies_wait<2 * S::kDepth - 1>();
       __syncwarp();
-      if (used - 1 + S::kStages < n_run) {
-        copy(s);
-        if (used + S::kStages < n_run) look_up();
+      if (whole) {
+        tile_scores<true>(z, ks, left, r, c, x);
+      } else {
+        tile_scores<false>(z, ks, left, r, c, x);
+        tile_mask<DQK, DV, NT>(p, sr.len, row0, t0, r, c, x);
+      }
+      if (more) copy(true, ks);
+      copies_end();
+      copies_wait<2 * S::kDepth - 1>();
+      __syncwarp();
+      if (whole)
+        top = tile_top<true, DQK, DV, NT>(p, vs, sr.len, row0, t0, lane);
+      else
+        top = tile_top<false, DQK, DV, NT>(p, vs, sr.len, row0, t0, lane);
+      tile_softmax(z, top, x);
+      if (whole)
+        tile_values<true>(z, vs, left, r, c, x);
+      else
+        tile_values<false>(z, vs, left, r, c, x);
+      if (more) {
+        copy(false, vs);
+        if (used + S::kDepth < n_run) look_up();
       }
       copies_end();
     }
