@@ -42,16 +42,16 @@
 // joins in the order of the blocks.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kcommon.cuh"
 #include "kv.h"
 
 namespace attn {
 
-constexpr int kTile = 64;   // tokens of a warp's tile
 constexpr int kWarps = 4;   // of a block
-constexpr int kItemCost = 2;   // in tiles: what an item costs a warp besides them
-constexpr int kMinTiles = 1;   // of a warp's run
+constexpr int kTile = 64;     // tokens of a warp's tile
+constexpr int kItemCost = 2;  // in tiles: what an item costs a warp besides them
 constexpr int kExpMin = -80, kExpMax = 100;  // exponents of V's scales told apart
 
 // whether 128 registers hold a lane's share
@@ -66,7 +66,7 @@ struct DecShape {
   static constexpr int kKslot = kKc + kTile * GK * 2, kVslot = kVc + kTile * GV * 2;
   // blocks of an SM: as many as its registers hold
   static constexpr int kBlocks = light(DV, NT) ? 4 : 2;
-  static constexpr int kDepth = DQK == 64 || (!light(DV, NT) && DQK < 256) ? 2 : 1;
+  static constexpr int kDepth = DQK == 64 && NT == 1 ? 2 : 1;  // slots of each
   static constexpr int kRing = kWarps * kDepth * (kKslot + kVslot);
   static constexpr int kPart = kRows * (DV + 2);  // floats of a partial result
 };
@@ -79,14 +79,15 @@ struct SeqRange {
   int tiles;    // all tiles of the sequence that some query sees
 };
 
+__device__ __forceinline__ int seq_len(const DecodeParams& p, int b) {
+  const int len = p.seq_lens[b], cap = p.cols << p.c.page_shift;
+  if (len >= 0 && len <= cap) return len;
+  if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+  return 0;
+}
 __device__ __forceinline__ SeqRange seq_range(const DecodeParams& p, int b) {
   SeqRange s;
-  s.len = p.seq_lens[b];
-  const int cap = p.cols << p.c.page_shift;
-  if (s.len < 0 || s.len > cap) {
-    if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
-    s.len = 0;
-  }
+  s.len = seq_len(p, b);
   // the first query's window starts at len - seqlen_q - window_left
   const int64_t w = p.window_left < 0 ? 0 : (int64_t)s.len - p.seqlen_q - p.window_left;
   s.lo = w > 0 ? (int)(w / kTile) : 0;
@@ -95,8 +96,7 @@ __device__ __forceinline__ SeqRange seq_range(const DecodeParams& p, int b) {
   s.tiles = s.n_sink + (s.len + kTile - 1) / kTile - s.lo;
   return s;
 }
-// An item's share of the list of work: its tiles, and kItemCost for what a block
-// does once for each item (q, the join of the warps).
+// An item's share of the list of work: its tiles, and what it costs besides them.
 __device__ __forceinline__ int units_of(int tiles) { return tiles ? tiles + kItemCost : 0; }
 // u / n, u >= 0 (64-bit quotients are slow)
 __device__ __forceinline__ long long quotient(long long u, int n) {
@@ -114,11 +114,9 @@ __device__ __forceinline__ long long tiles_before(int tiles, long long u) {
 __device__ __forceinline__ int tile_token(const SeqRange& s, int v) {
   return (v < s.n_sink ? v : s.lo + v - s.n_sink) * kTile;
 }
-// Runs that a call's work is cut into: one for each warp, but none of less than
-// kMinTiles tiles.
+// Runs that a call's work is cut into: one for each warp, but none without a tile.
 __host__ __device__ inline long long used_runs(long long tiles, int blocks) {
-  const long long n = (tiles + kMinTiles - 1) / kMinTiles;
-  return n < (long long)blocks * kWarps ? n : (long long)blocks * kWarps;
+  return tiles < (long long)blocks * kWarps ? tiles : (long long)blocks * kWarps;
 }
 
 // ----------------------------------------------------------------- operands
@@ -224,57 +222,40 @@ struct Piece {
 };
 
 // S^T of a tile, in units of the products: blocks of 16 tokens, rows r, r + 8.
-// WHOLE: every query of the block sees every token of the tile; else blocks
-// past the last token are left out.
-template <bool WHOLE, int DQK, int DV, int NT>
-__device__ __forceinline__ void tile_scores(const Piece<DQK, DV, NT>& z, const uint8_t* st, int left,
-                                            int r, int c, float (&x)[kTile / 16][NT][4]) {
+// lows: what the codes' offset of 8 adds up to, for each group and column pair.
+// (Past the last token and in pages out of range the slot's bytes are whatever
+// they were: the mask hides what comes of them.)
+template <int DQK, int DV, int NT>
+__device__ __forceinline__ void tile_scores(const Piece<DQK, DV, NT>& z, const uint8_t* st, const float4* lows, int r,
+                                            int c, float (&x)[kTile / 16][NT][4]) {
   using S = DecShape<DQK, DV, NT>;
 #pragma unroll
-  for (int m0 = 0; m0 < kTile / 16; m0 += 2) {
-    if (!WHOLE && m0 * 16 >= left) {
-#pragma unroll
-      for (int i = 0; i < 2 * NT * 4; ++i) x[m0 + i / (NT * 4)][i / 4 % NT][i % 4] = -INFINITY;
-      continue;
-    }
-    uint32_t sa[2][S::GK / 2], sb[2][S::GK / 2];
-    uint32_t ka[2][S::GK], kb[2][S::GK];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int ta = (m0 + i) * 16 + row_token(r), tb = ta + 8;
-      lds_words<S::GK>(st + ta * (DQK / 2) + c * 4 * S::GK, ka[i]);
-      lds_words<S::GK>(st + tb * (DQK / 2) + c * 4 * S::GK, kb[i]);
-      lds_words<S::GK / 2>(st + S::kKc + ta * 2 * S::GK, sa[i]);
-      lds_words<S::GK / 2>(st + S::kKc + tb * 2 * S::GK, sb[i]);
-    }
+  for (int m = 0; m < kTile / 16; ++m) {
+    uint32_t sa[S::GK / 2], sb[S::GK / 2], ka[S::GK], kb[S::GK];
+    const int ta = m * 16 + row_token(r), tb = ta + 8;
+    lds_words<S::GK>(st + ta * (DQK / 2) + c * 4 * S::GK, ka);
+    lds_words<S::GK>(st + tb * (DQK / 2) + c * 4 * S::GK, kb);
+    lds_words<S::GK / 2>(st + S::kKc + ta * 2 * S::GK, sa);
+    lds_words<S::GK / 2>(st + S::kKc + tb * 2 * S::GK, sb);
 #pragma unroll
     for (int g = 0; g < S::GK; ++g) {
-      const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      float low[NT][4];  // what the codes' offset of 8 adds up to
+      uint32_t a[4], b[4];
+      codes8(ka[g], a);
+      codes8(kb[g], b);
+      const float fa = scale_of(sa, g), fb = scale_of(sb, g);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const uint32_t* q = z.qf[t][g];
-        mma16816(low[t], kLow8, kLow8, kHigh8, kHigh8, q[0], q[1], zero);
-        mma16816(low[t], kLow8, kLow8, kHigh8, kHigh8, q[2], q[3]);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t a[4], b[4];
-        codes8(ka[i][g], a);
-        codes8(kb[i][g], b);
-        const float fa = scale_of(sa[i], g), fb = scale_of(sb[i], g);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const uint32_t* q = z.qf[t][g];
-          float acc[4];
-          float(&y)[4] = x[m0 + i][t];
-          mma16816(acc, a[0], b[0], a[1], b[1], q[0], q[1], low[t]);
-          mma16816(acc, a[2], b[2], a[3], b[3], q[2], q[3]);
-          y[0] = g ? fmaf(acc[0], fa, y[0]) : acc[0] * fa;
-          y[1] = g ? fmaf(acc[1], fa, y[1]) : acc[1] * fa;
-          y[2] = g ? fmaf(acc[2], fb, y[2]) : acc[2] * fb;
-          y[3] = g ? fmaf(acc[3], fb, y[3]) : acc[3] * fb;
-        }
+        float acc[4];
+        float(&y)[4] = x[m][t];
+        const float4 lv = lows[(t * S::GK + g) * 4 + c];
+        const float low[4] = {lv.x, lv.y, lv.z, lv.w};
+        mma16816(acc, a[0], b[0], a[1], b[1], q[0], q[1], low);
+        mma16816(acc, a[2], b[2], a[3], b[3], q[2], q[3]);
+        y[0] = g ? fmaf(acc[0], fa, y[0]) : acc[0] * fa;
+        y[1] = g ? fmaf(acc[1], fa, y[1]) : acc[1] * fa;
+        y[2] = g ? fmaf(acc[2], fb, y[2]) : acc[2] * fb;
+        y[3] = g ? fmaf(acc[3], fb, y[3]) : acc[3] * fb;
       }
     }
   }
@@ -284,6 +265,7 @@ __device__ __forceinline__ void tile_scores(const Piece<DQK, DV, NT>& z, const u
 template <int DQK, int DV, int NT>
 __device__ __forceinline__ void tile_mask(const DecodeParams& p, int len, int row0, int t0, int r, int c,
                                           float (&x)[kTile / 16][NT][4]) {
+  using S = DecShape<DQK, DV, NT>;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -374,13 +356,15 @@ __device__ __forceinline__ void tile_softmax(Piece<DQK, DV, NT>& z, float top,
   }
 }
 
-// The largest V scale (NaN apart) of tokens `lane` and `lane + 32` of a tile;
-// lo, hi, sinks: tokens that no query sees do not count, their scales may be anything.
-template <bool WHOLE, int DQK, int DV, int NT>
-__device__ __forceinline__ float tile_top(const DecodeParams& p, const uint8_t* st, int len, int row0,
-                                          int t0, int lane) {
+// The largest V scale (NaN apart) of this lane's tokens (every 32nd) of a tile.
+// Where some query does not see all of it: tokens that no query sees do not
+// count, their scales may be anything; those past the last token are set to
+// zero in the slot, and `odd` is set if a scale of the others is not finite.
+template <int DQK, int DV, int NT>
+__device__ __forceinline__ float tile_top(const DecodeParams& p, uint8_t* st, bool whole, int len, int row0,
+                                          int t0, int lane, bool& odd) {
   using S = DecShape<DQK, DV, NT>;
-  float top = 0.0f;
+  float top[kTile / 32];
 #pragma unroll
   for (int h = 0; h < kTile / 32; ++h) {
     uint32_t w[S::GV / 2];
@@ -389,26 +373,34 @@ __device__ __forceinline__ float tile_top(const DecodeParams& p, const uint8_t* 
 #pragma unroll
     for (int i = 1; i < S::GV / 2; ++i) y = __hmax2(y, *reinterpret_cast<__nv_bfloat162*>(&w[i]));
     const uint32_t u = *reinterpret_cast<uint32_t*>(&y);
-    float m = fmaxf(scale_of(&u, 0), scale_of(&u, 1));
-    if (!WHOLE) {
-      const int j = t0 + h * 32 + lane;
-      const int hi = len - p.seqlen_q + (min(row0 + S::kRows, p.rows) - 1) / p.group;
-      const int lo = p.window_left < 0 ? 0 : len - p.seqlen_q + row0 / p.group - p.window_left;
-      if (j > hi || (j < lo && j >= p.sinks)) m = 0.0f;
-    }
-    top = fmaxf(top, m);
+    top[h] = fmaxf(scale_of(&u, 0), scale_of(&u, 1));
   }
-  return top;
+  if (!whole) {
+    const int hi = len - p.seqlen_q + (min(row0 + S::kRows, p.rows) - 1) / p.group;
+    const int lo = p.window_left < 0 ? 0 : len - p.seqlen_q + row0 / p.group - p.window_left;
+#pragma unroll
+    for (int h = 0; h < kTile / 32; ++h) {
+      const int j = t0 + h * 32 + lane;
+      uint32_t* w = reinterpret_cast<uint32_t*>(st + S::kVc + (h * 32 + lane) * 2 * S::GV);
+#pragma unroll
+      for (int i = 0; i < S::GV / 2; ++i) {
+        if (j >= len) w[i] = 0u;
+        odd |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+      }
+      if (j > hi || (j < lo && j >= p.sinks)) top[h] = 0.0f;
+    }
+    __syncwarp();
+  }
+  return fmaxf(top[0], top[1]);
 }
 
-// O^T += V^T P^T
-template <bool WHOLE, int DQK, int DV, int NT>
-__device__ __forceinline__ void tile_values(Piece<DQK, DV, NT>& z, const uint8_t* st, int left, int r,
-                                            int c, const float (&x)[kTile / 16][NT][4]) {
+// O^T += V^T P^T.  ODD: a scale is not finite, and hidden pairs must not see it.
+template <bool ODD, int DQK, int DV, int NT>
+__device__ __forceinline__ void tile_values(Piece<DQK, DV, NT>& z, const uint8_t* st, int r, int c,
+                                            const float (&x)[kTile / 16][NT][4]) {
   using S = DecShape<DQK, DV, NT>;
 #pragma unroll
   for (int mt = 0; mt < kTile / 16; ++mt) {
-    if (!WHOLE && mt * 16 >= left) break;
     uint32_t vs[2][S::GV / 2];  // scales of tokens r and r + 8
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -432,7 +424,7 @@ __device__ __forceinline__ void tile_values(Piece<DQK, DV, NT>& z, const uint8_t
         float p0, p1, p2, p3;
         f2_unpack(f2_mul(f2_pack(x[mt][t][0], x[mt][t][2]), f2_pack(fa, fb)), p0, p2);
         f2_unpack(f2_mul(f2_pack(x[mt][t][1], x[mt][t][3]), f2_pack(fa, fb)), p1, p3);
-        if (!WHOLE) {  // a masked token's scale is not looked at: it may be anything
+        if (ODD) {
           p0 = x[mt][t][0] == 0.0f ? 0.0f : p0;
           p1 = x[mt][t][1] == 0.0f ? 0.0f : p1;
           p2 = x[mt][t][2] == 0.0f ? 0.0f : p2;
@@ -512,6 +504,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Cursor copy_at[kWarps], work_at[kWarps];
   __shared__ Strip strip[kWarps];
+  __shared__ float4 lows[kWarps][NT * S::GK * 4];
   __shared__ long long s_sum[2 * kWarps], s_tiles[kWarps][2], s_before[kWarps];
   __shared__ int s_b[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -610,8 +603,8 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     copy_at[warp] = work_at[warp] = k;
     strip[warp].left = 0;
   }
-  // Page of the tile to copy next: lane i's is that of its tokens 16 (i % 4) ..
-  // (all the same for pages of a tile or more).
+  // Page of the tile to copy next: lane i's is that of its tokens
+  // 16 (i % (kTile / 16)) .. (all the same for pages of a tile or more).
   int next_page = 0;
   auto look_up = [&]() {
     __syncwarp();
@@ -636,61 +629,56 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     }
     const int token = strip[warp].token + kTile, left = strip[warp].left - 1;
     const int len = strip[warp].len;
-    if (token < len) next_page = strip[warp].row[min(token + 16 * (lane & 3), len - 1) >> p.c.page_shift];
+    if (token < len) next_page = strip[warp].row[min(token + 16 * (lane % (kTile / 16)), len - 1) >> p.c.page_shift];
     __syncwarp();
     if (lane == 0) strip[warp].token = token, strip[warp].left = left;
   };
-  // `n` rows from row `at` of an array pair into a slot, from token `first` on.
-  auto copy_rows = [&](uint8_t* slot, int codes_end, const uint8_t* codes, const uint16_t* scales, int64_t at,
-                       int first, int n, int width, int groups) {
-    const uint8_t* src = codes + at * width + lane * 16;
-    uint32_t dst = smem_u32(slot) + first * width + lane * 16;
-#pragma unroll
-    for (int i = 0; i < n * width / 16; i += 32) {
-      if (n * width / 16 - i >= 32 || lane < n * width / 16 - i) copy16(dst + i * 16, src + i * 16);
+  // Tokens first .. first + ROWS of the tile looked up last, its K or its V:
+  // they lie in one page.
+  auto copy_rows = [&](auto is_k, auto rows, uint8_t* slot, int page, int first) {
+    constexpr bool K = decltype(is_k)::value;
+    constexpr int ROWS = decltype(rows)::value, W = K ? DQK / 2 : DV / 2, G = K ? S::GK : S::GV;
+    if ((unsigned)page >= (unsigned)p.c.num_pages) {
+      if (lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+      return;
     }
-    src = reinterpret_cast<const uint8_t*>(scales + at * groups) + lane * 16;
-    dst = smem_u32(slot) + codes_end + first * groups * 2 + lane * 16;
+    const int row = strip[warp].head_row + ((strip[warp].token + first) & (p.c.page_size - 1));
+    const int64_t at = (int64_t)page * (p.c.heads * p.c.page_size) + row;
+    auto run = [&](uint32_t dst, const uint8_t* src, auto bytes_of) {
+      constexpr int N = ROWS * decltype(bytes_of)::value;
+      dst += first * decltype(bytes_of)::value + lane * 16;
+      src += at * decltype(bytes_of)::value + lane * 16;
 #pragma unroll
-    for (int i = 0; i < n * groups / 8; i += 32)
-      if (n * groups / 8 - i >= 32 || lane < n * groups / 8 - i) copy16(dst + i * 16, src + i * 16);
-  };
-  auto copy = [&](bool is_k, uint8_t* slot) {
-    __syncwarp();
-    const int token = strip[warp].token, len = strip[warp].len;
-    const int64_t row = strip[warp].head_row + (token & (p.c.page_size - 1));
-    const int page_rows = p.c.heads * p.c.page_size;
-    if (token >= len) return;
-    auto rows = [&](int page, int first, int n) {
-      const int64_t at = (int64_t)page * page_rows + row;
-      if (is_k)
-        copy_rows(slot, S::kKc, p.c.k_codes, p.c.k_scales, at, first, n, DQK / 2, S::GK);
-      else
-        copy_rows(slot, S::kVc, p.c.v_codes, p.c.v_scales, at, first, n, DV / 2, S::GV);
+      for (int i = 0; i < N; i += 512)
+        if (N - i >= 512 || lane * 16 < N - i) copy16(dst + i, src + i);
     };
-    bool bad = false;
-    if (p.c.page_size >= kTile) {
-      bad = (unsigned)next_page >= (unsigned)p.c.num_pages;
-      if (!bad) rows(next_page, 0, kTile);
-    } else {
-      for (int first = 0; first < kTile && token + first < len; first += p.c.page_size) {
-        const int page = __shfl_sync(0xffffffffu, next_page, first / 16);
-        if ((unsigned)page >= (unsigned)p.c.num_pages)
-          bad = true;
-        else if (p.c.page_size == 16)
-          rows(page, first, 16);
-        else
-          rows(page, first, 32);
-      }
-    }
-    if (bad && lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+    run(smem_u32(slot), K ? p.c.k_codes : p.c.v_codes, std::integral_constant<int, W>());
+    run(smem_u32(slot) + kTile * W, reinterpret_cast<const uint8_t*>(K ? p.c.k_scales : p.c.v_scales),
+        std::integral_constant<int, 2 * G>());
+  };
+  auto copy = [&](auto is_k, uint8_t* slot) {
+    __syncwarp();
+    const int left = strip[warp].len - strip[warp].token;
+    if (left <= 0) return;
+    auto pieces = [&](auto rows) {
+      constexpr int ROWS = decltype(rows)::value;
+#pragma unroll
+      for (int i = 0; i < kTile; i += ROWS)
+        if (i < left) copy_rows(is_k, rows, slot, __shfl_sync(0xffffffffu, next_page, i / 16), i);
+    };
+    if (p.c.page_size >= kTile)
+      copy_rows(is_k, std::integral_constant<int, kTile>(), slot, next_page, 0);
+    else if (p.c.page_size == 32)
+      pieces(std::integral_constant<int, 32>());
+    else
+      pieces(std::integral_constant<int, 16>());
   };
   int used = 0;
   look_up();
   for (int i = 0; i < S::kDepth; ++i) {
-    if (i < n_run) copy(true, k_ring + i * S::kKslot);
+    if (i < n_run) copy(std::true_type(), k_ring + i * S::kKslot);
     copies_end();
-    if (i < n_run) copy(false, v_ring + i * S::kVslot);
+    if (i < n_run) copy(std::false_type(), v_ring + i * S::kVslot);
     copies_end();
     if (i + 1 < n_run) look_up();
   }
@@ -752,7 +740,9 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        z.xs[t][e] = p.scale_log2 * 16777216.0f * __shfl_sync(0xffffffffu, pow2(ex), (2 * c + e) * 4);
+        // (not 0, whatever the scale: times -inf that would be NaN)
+        z.xs[t][e] = fmaxf(p.scale_log2 * 16777216.0f * __shfl_sync(0xffffffffu, pow2(ex), (2 * c + e) * 4),
+                           1.17549435e-38f);
         z.ref[t][e] = 1e30f;  // nothing seen yet: a reference below any score
         z.l[t][e] = 0.0f;
       }
@@ -763,6 +753,18 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
 #pragma unroll
           for (int e = 0; e < 4; ++e) z.o[t][g][h][e] = 0.0f;
     }
+    __syncwarp();
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int g = 0; g < S::GK; ++g) {
+        const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float low[4];
+        mma16816(low, kLow8, kLow8, kHigh8, kHigh8, z.qf[t][g][0], z.qf[t][g][1], zero);
+        mma16816(low, kLow8, kLow8, kHigh8, kHigh8, z.qf[t][g][2], z.qf[t][g][3]);
+        if (r == 0) lows[warp][(t * S::GK + g) * 4 + c] = make_float4(low[0], low[1], low[2], low[3]);
+      }
+    __syncwarp();
     z.lim = (float)(15 - kExpMin);
     z.vlim = pow2(kExpMin);
     // every query of the item sees token j if j <= pos_lo and (j >= pos_hi -
@@ -777,33 +779,27 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
       const int s = used % S::kDepth;
       const bool more = used + S::kDepth < n_run;
       ++used;
-      const int t0 = tile_token(sr, v), left = sr.len - t0;
+      const int t0 = tile_token(sr, v);
       const bool whole = t0 <= whole_hi && (t0 >= whole_lo || t0 + kTile <= p.sinks);
       uint8_t *ks = k_ring + s * S::kKslot, *vs = v_ring + s * S::kVslot;
-      float x[kTile / 16][NT][4], top;
+      float x[kTile / 16][NT][4];
       copies_wait<2 * S::kDepth - 1>();
       __syncwarp();
-      if (whole) {
-        tile_scores<true>(z, ks, left, r, c, x);
-      } else {
-        tile_scores<false>(z, ks, left, r, c, x);
-        tile_mask<DQK, DV, NT>(p, sr.len, row0, t0, r, c, x);
-      }
-      if (more) copy(true, ks);
+      tile_scores(z, ks, lows[warp], r, c, x);
+      if (!whole) tile_mask<DQK, DV, NT>(p, sr.len, row0, t0, r, c, x);
+      if (more) copy(std::true_type(), ks);
       copies_end();
       copies_wait<2 * S::kDepth - 1>();
       __syncwarp();
-      if (whole)
-        top = tile_top<true, DQK, DV, NT>(p, vs, sr.len, row0, t0, lane);
-      else
-        top = tile_top<false, DQK, DV, NT>(p, vs, sr.len, row0, t0, lane);
+      bool odd = false;
+      const float top = tile_top<DQK, DV, NT>(p, vs, whole, sr.len, row0, t0, lane, odd);
       tile_softmax(z, top, x);
-      if (whole)
-        tile_values<true>(z, vs, left, r, c, x);
+      if (__any_sync(0xffffffffu, odd))
+        tile_values<true>(z, vs, r, c, x);
       else
-        tile_values<false>(z, vs, left, r, c, x);
+        tile_values<false>(z, vs, r, c, x);
       if (more) {
-        copy(false, vs);
+        copy(std::false_type(), vs);
         if (used + S::kDepth < n_run) look_up();
       }
       copies_end();
@@ -869,7 +865,7 @@ template <bool BF16>
 __device__ __forceinline__ void empty_rows(const DecodeParams& p, int threads) {
   const int q = p.c.d_v / 4;
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-    if (seq_range(p, b).tiles) continue;
+    if (seq_len(p, b)) continue;
     for (int i = threadIdx.x; i < p.c.heads * p.rows * q; i += threads) {
       const int row = i / q, kvh = row / p.rows;
       write_row<BF16>(p, b, kvh, row - kvh * p.rows, i - row * q, make_float4(0.f, 0.f, 0.f, 0.f), 0.0f, 0.0f);
@@ -890,10 +886,11 @@ __global__ void __launch_bounds__(kByItemThreads) attn_kv_join_items_kernel(
   const int kvh = item / p.row_blocks, row_all = (item - kvh * p.row_blocks) * ROWS + row;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   empty_rows<BF16>(p, kByItemThreads);
-  if (row_all >= p.rows || seq_range(p, b).tiles == 0) return;
-  const int k0 = p.info[2 * (int64_t)at], np = p.info[2 * (int64_t)at + 1] - k0 + 1;
-  // (np 1: one run finished it; out of range: lengths that changed under the call)
-  if (np < 2 || k0 < 0 || k0 + np > runs) return;
+  if (row_all >= p.rows || seq_len(p, b) == 0) return;
+  const int k0 = p.info[2 * (int64_t)at], k1 = p.info[2 * (int64_t)at + 1];
+  // (equal: one run finished it; out of range: lengths that changed under the call)
+  if (k0 < 0 || k1 <= k0 || k1 >= runs) return;
+  const int np = k1 - k0 + 1;
   const int g = tid / kLanes, d4 = tid % kLanes;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.0f, mx = -INFINITY;
