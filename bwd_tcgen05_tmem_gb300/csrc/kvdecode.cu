@@ -12,18 +12,23 @@
 //     rows for each kv head, and this side wastes the least;
 //   * codes go from shared memory to operand registers without a detour: the
 //     cache is laid out (see kvcache.cu) so that a lane's vectors hold exactly
-//     the codes of its operand registers.  Two codes become two fp16 numbers by
-//     one mask into the mantissa of 1024 and one exact fused multiply-add
-//     (1024 + c - 1032, or (1024 + 16 c) / 16 - 72: the second form saves the
-//     shift of every other code).
+//     the codes of its operand registers.  One mask makes two fp16 numbers of
+//     two codes: below fp16's normal range a number's bits are its value in
+//     units of 2^-24, and the products take such numbers exactly.  Every other
+//     code stays four bits up, in units of 2^-20, which saves its shift: q is
+//     held divided by 16 there, O is multiplied by 16 at the end.
 //     K: pairs of one register are dims n, n + 4 of a word of one token.
 //     V: they are the same dim of two tokens (one byte permute joins the
 //     half-words of both);
+//   * the codes' offset of 8: K's enters as the start value of the products,
+//     -8 times the sum of q, worked out once for each piece; V's is taken off
+//     the codes, exactly, by one packed add.  (As a start value it would have
+//     to cancel in O, and the tensor cores' sums do not hold enough bits.)
 //   * both products are in fp16, which holds q and the probabilities better
 //     than bf16 where the range allows: a bf16 q row is held times a power of
 //     two that brings its largest element to 2^13 .. 2^14 (exact, but for
 //     elements 2^27 times smaller), and a warp keeps a power of two that brings
-//     the largest probability times V scale of its tokens to 2^13 .. 2^14;
+//     the largest probability times V scale of its tokens to 2^13 .. 2^15;
 //   * scales stay out of the operands: K's multiply the FP32 products of each
 //     32-dim group, V's multiply the probabilities before these are rounded.
 //
@@ -31,15 +36,28 @@
 // second product O^T = V^T P^T wants them along its depth: movmatrix
 // transposes 8 x 8 blocks in registers.
 //
-// Split: every (sequence, kv head, block of query rows) is an item of
-// ceil(tiles / 8) units (a unit: 8 tiles of 32 tokens, one for each warp).  The
-// call's units are one list, cut into equal runs, one for each block of a grid
-// that fills the card, so ragged lengths balance; lengths are read on the
-// device, so a captured graph serves any lengths.  A block keeps a piece's
-// running maximum, sum and O in registers of its 8 warps, joins them through
-// shared memory at the end of the piece, and writes the result, or, where the
-// item is shared with other blocks, a partial result that a second kernel
-// joins in the order of the blocks.
+// Split: every (sequence, kv head, block of 8 or 16 query rows) is an item, its
+// tiles of 64 tokens are a stretch of one list, and the list is cut into equal
+// runs, one for each warp of a grid that fills the card, so ragged lengths
+// balance; an item counts kItemCost tiles more than it has, for what comes once
+// for each.  Lengths are read on the device, so a captured graph serves any
+// lengths.  Warps wait for nobody but their own copies.  A warp holds a piece's
+// running sum and O in registers and writes the result, or, where the item is
+// shared with other warps, a partial result that a second kernel joins in the
+// order of the runs.
+//
+// Measured on a GB300 (graph replays, 8 kv heads, 4 query heads each, bf16):
+// 16 x 32768 tokens of head dim 128 119 us = 5.1 TB/s (75% of a plain copy's
+// rate), 31 ragged ones up to 32768 94 us, 128 x 4096 129 us, 512 x 1023 151 us,
+// 2048 x 250 220 us (an item's start and end weigh 4 tiles); head dim 64 75 us,
+// 192 / 128 161 us, 256 (8 requests) 134 us; 16 query rows a kv head 186 us.
+// What bounds the long ones: the instructions of a tile (about 1150 a warp for
+// 64 tokens of head dim 128, half of them on the ALU pipe, 60% of the issue
+// slots taken); with the copies left out they take 115 us, the copies alone
+// 99 us.  Tiles of 64 tokens against 32: 16 x 32K tokens 121 / 131 us, head dim
+// 64 75 / 94 us, 16 query rows 187 / 219 us, a window of 4095 (24 requests, 4
+// new tokens, 192 / 128) 35.3 / 33.0 us, where the tiles that the window's ends
+// cut weigh more.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -51,7 +69,8 @@ namespace attn {
 
 constexpr int kWarps = 4;   // of a block
 constexpr int kTile = 64;     // tokens of a warp's tile
-constexpr int kItemCost = 2;  // in tiles: what an item costs a warp besides them
+// in tiles: what an item costs a warp besides them (q, the list, the result)
+constexpr int kItemCost = 2;
 constexpr int kExpMin = -80, kExpMax = 100;  // exponents of V's scales told apart
 
 // whether 128 registers hold a lane's share
@@ -282,12 +301,30 @@ __device__ __forceinline__ void tile_mask(const DecodeParams& p, int len, int ro
     }
 }
 
+// What tile_top says without the infinite scales: those make the products
+// infinite anyway, and must not take the others' precision.
+__device__ __forceinline__ float tile_top_finite(const DecodeParams& p, const uint8_t* scales, int groups, int rows,
+                                              int len, int row0, int t0) {
+  const int hi = len - p.seqlen_q + (min(row0 + rows, p.rows) - 1) / p.group;
+  const int lo = p.window_left < 0 ? 0 : len - p.seqlen_q + row0 / p.group - p.window_left;
+  float top = 0.0f;
+  for (int i = threadIdx.x & 31; i < kTile; i += 32) {
+    const int j = t0 + i;
+    if (j > hi || (j < lo && j >= p.sinks)) continue;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(scales + i * 2 * groups);
+    for (int g = 0; g < groups; ++g)
+      if (scale_of(w, g) <= 3.40282347e38f) top = fmaxf(top, scale_of(w, g));
+  }
+  return top;
+}
+
 // Scores to probabilities, in base 2.  The reference of a column moves only when
 // a score passes it by more than 1: probabilities stay below 2 (times 2^kf, and
 // times V's scales below 2^15), and most tiles need no exchange between lanes.
-// top: the largest V scale of this lane's tokens.
+// top: the largest V scale of this lane's tokens; st: the tile's V.
 template <int DQK, int DV, int NT>
-__device__ __forceinline__ void tile_softmax(Piece<DQK, DV, NT>& z, float top,
+__device__ __forceinline__ void tile_softmax(const DecodeParams& p, Piece<DQK, DV, NT>& z, const uint8_t* st,
+                                             int len, int row0, int t0, float top,
                                              float (&x)[kTile / 16][NT][4]) {
   using S = DecShape<DQK, DV, NT>;
   bool move = top >= z.vlim;
@@ -302,7 +339,17 @@ __device__ __forceinline__ void tile_softmax(Piece<DQK, DV, NT>& z, float top,
       mx[t][e] = z.xs[t][e] * y;
       move |= mx[t][e] + z.ref[t][e] > z.lim;
     }
-  if (__any_sync(0xffffffffu, move)) {
+  bool any = __any_sync(0xffffffffu, move);
+  if (any && __any_sync(0xffffffffu, top > 3.40282347e38f)) {
+    top = tile_top_finite(p, st + S::kVc, S::GV, S::kRows, len, row0, t0);
+    move = top >= z.vlim;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) move |= mx[t][e] + z.ref[t][e] > z.lim;
+    any = __any_sync(0xffffffffu, move);
+  }
+  if (any) {
     const float kf_old = z.lim - 1.0f;
     float f = 1.0f;
     {
@@ -793,7 +840,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
       __syncwarp();
       bool odd = false;
       const float top = tile_top<DQK, DV, NT>(p, vs, whole, sr.len, row0, t0, lane, odd);
-      tile_softmax(z, top, x);
+      tile_softmax(p, z, vs, sr.len, row0, t0, top, x);
       if (__any_sync(0xffffffffu, odd))
         tile_values<true>(z, vs, r, c, x);
       else

@@ -463,6 +463,53 @@ def test_decode_empty_batch_and_partial_results_merge():
     within(m[None], ml[None], ref, UNIT[BF])
 
 
+def test_decode_one_long_and_many_short_requests():
+    """Cut by runs: an item that many runs share among hundreds that none do."""
+    x = Held([30000] + [21] * 500 + [9000], 2, 64, 64, 64, FP, seed=13)
+    x.check(x.q(1, 4))
+    x.check(x.q(3, 8))
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e-6])
+def test_decode_tiny_scale_is_a_mean(scale):
+    """Hidden tokens stay hidden where every score is next to nothing."""
+    x = Held([70, 5, 0, 130], 2, 128, 128, 64, BF, seed=14)
+    x.check(x.q(3, 8, scale=0.0), scale=scale)
+    x.check(x.q(3, 8), scale=scale, window_left=9, sinks=2)
+
+
+def test_decode_hidden_scales_may_be_infinite():
+    x = Held([200, 64], 2, 128, 128, 64, BF, seed=15)
+    q = x.q(4, 4)
+    want = kv.kv4_decode(q, x.cache, x.t, x.l, window_left=20, sinks=3)
+    for j in (3, 100, 175):  # no query sees these
+        x.cache.v_scales[x.table[0][j // 64], :, j % 64] = float("inf")
+        x.cache.k_scales[x.table[0][j // 64], :, j % 64] = float("-inf")
+    got = kv.kv4_decode(q, x.cache, x.t, x.l, window_left=20, sinks=3)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    x.cache.v_scales[x.table[0][199 // 64], :, 199 % 64] = float("inf")  # the last query alone
+    got = kv.kv4_decode(q, x.cache, x.t, x.l, window_left=20, sinks=3)
+    assert torch.equal(got[0][:, :3], want[0][:, :3]) and torch.equal(got[0][1], want[0][1])
+    assert not torch.isfinite(got[0][0, 3]).any()
+
+
+def test_decode_two_streams_at_once():
+    x = [Held([3000, 40, 900], 2, 128, 128, 64, BF, seed=16), Held([5000], 4, 64, 64, 32, FP, seed=17)]
+    q = [x[0].q(1, 8), x[1].q(2, 8)]
+    want = [kv.kv4_decode(a, y.cache, y.t, y.l) for a, y in zip(q, x)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(kv.kv4_decode(q[i], x[i].cache, x[i].t, x[i].l))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
 # ------------------------------------------------------------------ together
 
 def test_serving_steps():
