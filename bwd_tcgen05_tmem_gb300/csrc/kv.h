@@ -92,6 +92,7 @@ struct DecodeParams {
   int64_t q_b, q_t, q_h, o_b, o_t, o_h, table_stride;
   int batch, seqlen_q, heads_q, group, cols, window_left, sinks;
   int rows, row_blocks;  // query rows of a kv head (seqlen_q * group), and blocks of them
+  FastDiv by_group, by_blocks;  // by group; by row_blocks
   float scale_log2;
   int o_f32;
   int* info;       // per item: the first and the last run that work on it

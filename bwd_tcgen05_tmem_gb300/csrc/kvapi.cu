@@ -530,6 +530,8 @@ attn_status_t check_decode(const attn_kv4_decode_params_t* p, const attn_kv4_cac
   kp.rows = p->seqlen_q * kp.group;
   const int per = 8 * attn::decode_col_tiles(kp.rows, c->d_v);
   kp.row_blocks = (kp.rows + per - 1) / per;
+  kp.by_group = attn::FastDiv::of((uint32_t)kp.group);
+  kp.by_blocks = attn::FastDiv::of((uint32_t)std::max(kp.row_blocks, 1));
   kp.cols = p->cols;
   kp.table_stride = p->table_stride;
   // a window as long as the longest sequence hides nothing

@@ -290,7 +290,7 @@ __device__ __forceinline__ void tile_mask(const DecodeParams& p, int len, int ro
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int row = row0 + t * 8 + 2 * c + e;
-      const int pos = len - p.seqlen_q + row / p.group;
+      const int pos = len - p.seqlen_q + (int)p.by_group.div(row);
       const int hi = row < p.rows ? pos : -1;
       const int lo = p.window_left < 0 ? 0 : max(0, pos - p.window_left);
 #pragma unroll
@@ -305,8 +305,8 @@ __device__ __forceinline__ void tile_mask(const DecodeParams& p, int len, int ro
 // infinite anyway, and must not take the others' precision.
 __device__ __forceinline__ float tile_top_finite(const DecodeParams& p, const uint8_t* scales, int groups, int rows,
                                               int len, int row0, int t0) {
-  const int hi = len - p.seqlen_q + (min(row0 + rows, p.rows) - 1) / p.group;
-  const int lo = p.window_left < 0 ? 0 : len - p.seqlen_q + row0 / p.group - p.window_left;
+  const int hi = len - p.seqlen_q + (int)p.by_group.div(min(row0 + rows, p.rows) - 1);
+  const int lo = p.window_left < 0 ? 0 : len - p.seqlen_q + (int)p.by_group.div(row0) - p.window_left;
   float top = 0.0f;
   for (int i = threadIdx.x & 31; i < kTile; i += 32) {
     const int j = t0 + i;
@@ -423,8 +423,8 @@ __device__ __forceinline__ float tile_top(const DecodeParams& p, uint8_t* st, bo
     top[h] = fmaxf(scale_of(&u, 0), scale_of(&u, 1));
   }
   if (!whole) {
-    const int hi = len - p.seqlen_q + (min(row0 + S::kRows, p.rows) - 1) / p.group;
-    const int lo = p.window_left < 0 ? 0 : len - p.seqlen_q + row0 / p.group - p.window_left;
+    const int hi = len - p.seqlen_q + (int)p.by_group.div(min(row0 + S::kRows, p.rows) - 1);
+    const int lo = p.window_left < 0 ? 0 : len - p.seqlen_q + (int)p.by_group.div(row0) - p.window_left;
 #pragma unroll
     for (int h = 0; h < kTile / 32; ++h) {
       const int j = t0 + h * 32 + lane;
@@ -486,25 +486,37 @@ __device__ __forceinline__ void tile_values(Piece<DQK, DV, NT>& z, const uint8_t
   }
 }
 
-// Four dims of a finished row: O = acc / sum, LSE = (mx + log2 sum) ln 2.
+// Where a finished row goes: O = acc / sum, LSE = (mx + log2 sum) ln 2.
+struct RowOut {
+  int64_t o, lse;
+  __device__ __forceinline__ RowOut(const DecodeParams& p, int b, int kvh, int row) {
+    const int qi = (int)p.by_group.div(row), qh = kvh * p.group + row - qi * p.group;
+    o = b * p.o_b + qi * p.o_t + qh * p.o_h;
+    lse = ((int64_t)b * p.heads_q + qh) * p.seqlen_q + qi;
+  }
+  // dims 4 d4 .. + 3
+  template <bool BF16>
+  __device__ __forceinline__ void write(const DecodeParams& p, int d4, const float4& y) const {
+    if (p.o_f32)
+      *reinterpret_cast<float4*>((float*)p.o + o + d4 * 4) = y;
+    else
+      *reinterpret_cast<uint2*>((uint16_t*)p.o + o + d4 * 4) =
+          make_uint2(Pack<BF16>::two(y.x, y.y), Pack<BF16>::two(y.z, y.w));
+  }
+  __device__ __forceinline__ void write_lse(const DecodeParams& p, float mx, float sum) const {
+    p.lse[lse] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+  }
+};
+// 1 / sum; 0 where no token is visible (sum is NaN where a score is, and O with it)
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+// Four dims of a row, and with the first of them its LSE.
 template <bool BF16>
 __device__ __forceinline__ void write_row(const DecodeParams& p, int b, int kvh, int row, int d4,
-                                          float4 acc, float mx, float sum) {
-  const int qi = row / p.group, qh = kvh * p.group + row % p.group;
-  // no visible token: sum is 0 (it is NaN where all scores are)
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  if (sum == 0.0f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-  if (sum != sum) acc.x = acc.y = acc.z = acc.w = sum;
-  const int64_t off = b * p.o_b + qi * p.o_t + qh * p.o_h + d4 * 4;
-  if (p.o_f32)
-    *reinterpret_cast<float4*>((float*)p.o + off) = acc;
-  else
-    *reinterpret_cast<uint2*>((uint16_t*)p.o + off) =
-        make_uint2(Pack<BF16>::two(acc.x, acc.y), Pack<BF16>::two(acc.z, acc.w));
-  if (d4 == 0)
-    p.lse[((int64_t)b * p.heads_q + qh) * p.seqlen_q + qi] =
-        sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+                                          const float4& acc, float mx, float sum) {
+  const RowOut out(p, b, kvh, row);
+  const float inv = inverse(sum);
+  out.write<BF16>(p, d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  if (d4 == 0) out.write_lse(p, mx, sum);
 }
 
 // ----------------------------------------------------------------- the kernel
@@ -665,7 +677,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
           t.row = p.table + (int64_t)k.b * p.table_stride;
           t.token = tile_token(k.sr, k.v) - kTile;
           t.left = stop - k.v;
-          t.head_row = (k.item / p.row_blocks) * p.c.page_size;
+          t.head_row = ((int)p.by_blocks.div(k.item)) * p.c.page_size;
           t.len = k.sr.len;
           advance(p, per_seq, k, t.left);
           copy_at[warp] = k;
@@ -738,7 +750,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     }
     const SeqRange sr = k.sr;
     const int b = k.b, item = k.item, v0 = k.v, v1 = min(sr.tiles, v0 + n_run - used);
-    const int kvh = item / p.row_blocks, rb = item - kvh * p.row_blocks;
+    const int kvh = (int)p.by_blocks.div(item), rb = item - kvh * p.row_blocks;
     __syncwarp();
     if (lane == 0) {
       // for the join: the first and the last run that work on an item, and
@@ -757,7 +769,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int row = row0 + t * 8 + r;
-      const int qi = row / p.group, qh = kvh * p.group + row % p.group;
+      const int qi = (int)p.by_group.div(row), qh = kvh * p.group + row - qi * p.group;
       const uint16_t* src = (const uint16_t*)p.q + b * p.q_b + qi * p.q_t + qh * p.q_h + 8 * c;
       uint4 qv[S::GK];
       uint32_t top = 0;  // largest magnitude: as bits they are ordered
@@ -817,8 +829,8 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     // every query of the item sees token j if j <= pos_lo and (j >= pos_hi -
     // window_left or j < sinks); columns past the last row hold zeros, and what
     // they sum up is not written
-    const int pos_lo = sr.len - p.seqlen_q + row0 / p.group;
-    const int pos_hi = sr.len - p.seqlen_q + (min(row0 + S::kRows, p.rows) - 1) / p.group;
+    const int pos_lo = sr.len - p.seqlen_q + (int)p.by_group.div(row0);
+    const int pos_hi = sr.len - p.seqlen_q + (int)p.by_group.div(min(row0 + S::kRows, p.rows) - 1);
 
     const int whole_hi = pos_lo - (kTile - 1);
     const int whole_lo = p.window_left < 0 ? 0 : pos_hi - p.window_left;
@@ -863,20 +875,28 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
         sum += __shfl_xor_sync(0xffffffffu, sum, 4);
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        const int row = t * 8 + 2 * c + e;
-        if (row0 + row >= p.rows) continue;
+        const int row = t * 8 + 2 * c + e, row_all = row0 + row;
+        if (row_all >= p.rows) continue;
+        // dims 32 g + 4 r .. + 3 times f
+        auto dims = [&](int g, float f) {
+          const float lo = f * 16777216.0f, hi = f * 1048576.0f;
+          return make_float4(z.o[t][g][0][e] * lo, z.o[t][g][0][2 + e] * hi, z.o[t][g][1][e] * lo,
+                             z.o[t][g][1][2 + e] * hi);
+        };
+        if (done) {
+          const RowOut out(p, b, kvh, row_all);
+          const float inv = inverse(sum);
 #pragma unroll
-        for (int g = 0; g < S::GV; ++g) {
-          const float4 y = make_float4(z.o[t][g][0][e] * 16777216.0f, z.o[t][g][0][2 + e] * 1048576.0f,
-                                       z.o[t][g][1][e] * 16777216.0f, z.o[t][g][1][2 + e] * 1048576.0f);
-          if (done)
-            write_row<BF16>(p, b, kvh, row0 + row, 8 * g + r, y, -z.ref[t][e], sum);
-          else
-            *reinterpret_cast<float4*>(part + row * DV + 32 * g + 4 * r) = y;
-        }
-        if (!done && r == 0) {
-          part[S::kRows * DV + row] = -z.ref[t][e];
-          part[S::kRows * (DV + 1) + row] = sum;
+          for (int g = 0; g < S::GV; ++g) out.write<BF16>(p, 8 * g + r, dims(g, inv));
+          if (r == 0) out.write_lse(p, -z.ref[t][e], sum);
+        } else {
+#pragma unroll
+          for (int g = 0; g < S::GV; ++g)
+            *reinterpret_cast<float4*>(part + row * DV + 32 * g + 4 * r) = dims(g, 1.0f);
+          if (r == 0) {
+            part[S::kRows * DV + row] = -z.ref[t][e];
+            part[S::kRows * (DV + 1) + row] = sum;
+          }
         }
       }
   }
@@ -908,14 +928,21 @@ __device__ __forceinline__ void add_piece(float4& acc, float& sum, float& mx, fl
   acc.z = fmaf(acc.z, a, y.z * f), acc.w = fmaf(acc.w, a, y.w * f);
 }
 
+// Sequences blockIdx.x, + gridDim.x, ..: this comes before the wait, since it
+// needs nothing of the first kernel.
 template <bool BF16>
 __device__ __forceinline__ void empty_rows(const DecodeParams& p, int threads) {
-  const int q = p.c.d_v / 4;
-  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-    if (seq_len(p, b)) continue;
-    for (int i = threadIdx.x; i < p.c.heads * p.rows * q; i += threads) {
-      const int row = i / q, kvh = row / p.rows;
-      write_row<BF16>(p, b, kvh, row - kvh * p.rows, i - row * q, make_float4(0.f, 0.f, 0.f, 0.f), 0.0f, 0.0f);
+  const int q = p.c.d_v / 4, n = p.c.heads * p.rows * q;
+  for (int64_t b0 = blockIdx.x; b0 < p.batch; b0 += (int64_t)threads * gridDim.x) {
+    const int64_t mine = b0 + (int64_t)threadIdx.x * gridDim.x;
+    const bool empty = mine < p.batch && seq_len(p, (int)mine) == 0;
+    if (!__syncthreads_or(empty)) continue;
+    for (int64_t b = b0; b < p.batch && b < b0 + (int64_t)threads * gridDim.x; b += gridDim.x) {
+      if (seq_len(p, (int)b)) continue;
+      for (int i = threadIdx.x; i < n; i += threads) {
+        const int row = i / q, kvh = row / p.rows;
+        write_row<BF16>(p, (int)b, kvh, row - kvh * p.rows, i - row * q, make_float4(0.f, 0.f, 0.f, 0.f), 0.0f, 0.0f);
+      }
     }
   }
 }
@@ -930,9 +957,9 @@ __global__ void __launch_bounds__(kByItemThreads) attn_kv_join_items_kernel(
   const int rows = min(ROWS, p.rows);
   const int at = blockIdx.x / rows, row = blockIdx.x - at * rows;
   const int b = at / per_seq, item = at - b * per_seq;
-  const int kvh = item / p.row_blocks, row_all = (item - kvh * p.row_blocks) * ROWS + row;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int kvh = (int)p.by_blocks.div(item), row_all = (item - kvh * p.row_blocks) * ROWS + row;
   empty_rows<BF16>(p, kByItemThreads);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row_all >= p.rows || seq_len(p, b) == 0) return;
   const int k0 = p.info[2 * (int64_t)at], k1 = p.info[2 * (int64_t)at + 1];
   // (equal: one run finished it; out of range: lengths that changed under the call)
@@ -965,8 +992,8 @@ __global__ void __launch_bounds__(kByRunThreads) attn_kv_join_runs_kernel(
   __shared__ float sm_l[kByRunThreads], sm_m[kByRunThreads];
   __shared__ int s_at[kWarps], s_k0[kWarps], s_np[kWarps];
   const int per_seq = p.c.heads * p.row_blocks, tid = threadIdx.x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   empty_rows<BF16>(p, kByRunThreads);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid < kWarps) {
     const int run = blockIdx.x * kWarps + tid, at = p.ends[run];
     const int k0 = at < 0 ? 0 : p.info[2 * (int64_t)at];
@@ -981,7 +1008,7 @@ __global__ void __launch_bounds__(kByRunThreads) attn_kv_join_runs_kernel(
     const int np = s_np[w];
     if (np <= kTeamPieces) continue;
     const int b = s_at[w] / per_seq, item = s_at[w] - b * per_seq;
-    const int kvh = item / p.row_blocks, row0 = (item - kvh * p.row_blocks) * ROWS;
+    const int kvh = (int)p.by_blocks.div(item), row0 = (item - kvh * p.row_blocks) * ROWS;
     const int need = min(ROWS, p.rows - row0) * kLanes, groups = kByRunThreads / need;
     const int g = tid / need, i0 = tid - g * need, row = i0 / kLanes, d4 = i0 % kLanes;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1008,7 +1035,7 @@ __global__ void __launch_bounds__(kByRunThreads) attn_kv_join_runs_kernel(
   const int w = tid / kTeam, t = tid % kTeam, np = s_np[w];
   if (np < 2 || np > kTeamPieces) return;
   const int b = s_at[w] / per_seq, item = s_at[w] - b * per_seq;
-  const int kvh = item / p.row_blocks, row0 = (item - kvh * p.row_blocks) * ROWS;
+  const int kvh = (int)p.by_blocks.div(item), row0 = (item - kvh * p.row_blocks) * ROWS;
   float4 acc[kEach];
   float sum[kEach], mx[kEach];
 #pragma unroll
