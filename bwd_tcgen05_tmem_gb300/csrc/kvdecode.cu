@@ -47,17 +47,20 @@
 // order of the runs.
 //
 // Measured on a GB300 (graph replays, 8 kv heads, 4 query heads each, bf16):
-// 16 x 32768 tokens of head dim 128 119 us = 5.1 TB/s (75% of a plain copy's
-// rate), 31 ragged ones up to 32768 94 us, 128 x 4096 129 us, 512 x 1023 151 us,
-// 2048 x 250 220 us (an item's start and end weigh 4 tiles); head dim 64 75 us,
-// 192 / 128 161 us, 256 (8 requests) 134 us; 16 query rows a kv head 186 us.
+// 16 x 32768 tokens of head dim 128 116 us = 5.2 TB/s (77% of a plain copy's
+// rate), 48 ragged ones up to 32768 91 us, 128 x 4096 126 us, 512 x 1023 136 us,
+// 2048 x 250 187 us (an item's start and end weigh about two tiles); head dim 64
+// 74 us, 192 / 128 157 us, 256 (8 requests) 130 us; 16 query rows a kv head 172
+// us; pages of 16 tokens 142 us, of 32 132 us.
 // What bounds the long ones: the instructions of a tile (about 1150 a warp for
-// 64 tokens of head dim 128, half of them on the ALU pipe, 60% of the issue
-// slots taken); with the copies left out they take 115 us, the copies alone
-// 99 us.  Tiles of 64 tokens against 32: 16 x 32K tokens 121 / 131 us, head dim
-// 64 75 / 94 us, 16 query rows 187 / 219 us, a window of 4095 (24 requests, 4
-// new tokens, 192 / 128) 35.3 / 33.0 us, where the tiles that the window's ends
-// cut weigh more.
+// 64 tokens of head dim 128, half of them on the ALU pipe; 60% of the issue
+// slots are taken) beside the copies: when the whole took 121 us, the tiles' work
+// without copies took 115 us and the copies alone 99 us.  Short requests wait for instructions too (the
+// loop and what surrounds it do not fit the first instruction cache).
+// Tiles of 64 tokens against 32: 16 x 32K tokens 121 / 131 us, head dim 64 75 /
+// 94 us, 16 query rows 187 / 219 us; a window of 4095 (24 requests, 4 new tokens,
+// 192 / 128) 35.3 / 33.0 us, where the tiles that the window's ends cut weigh
+// more.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -67,10 +70,9 @@
 
 namespace attn {
 
-constexpr int kWarps = 4;   // of a block
+constexpr int kWarps = 4;     // of a block
 constexpr int kTile = 64;     // tokens of a warp's tile
-// in tiles: what an item costs a warp besides them (q, the list, the result)
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 2;  // in tiles: what an item costs a warp besides them (q, the list, the result)
 constexpr int kExpMin = -80, kExpMax = 100;  // exponents of V's scales told apart
 
 // whether 128 registers hold a lane's share
@@ -933,16 +935,17 @@ __device__ __forceinline__ void add_piece(float4& acc, float& sum, float& mx, fl
 // needs nothing of the first kernel.
 template <bool BF16>
 __device__ __forceinline__ void empty_rows(const DecodeParams& p, int threads) {
-  const int q = p.c.d_v / 4, n = p.c.heads * p.rows * q;
+  const int q = p.c.d_v / 4, lanes = threads / q;  // rows at a time
+  const int r0 = threadIdx.x / q, d4 = threadIdx.x - r0 * q;
   for (int64_t b0 = blockIdx.x; b0 < p.batch; b0 += (int64_t)threads * gridDim.x) {
     const int64_t mine = b0 + (int64_t)threadIdx.x * gridDim.x;
     const bool empty = mine < p.batch && seq_len(p, (int)mine) == 0;
     if (!__syncthreads_or(empty)) continue;
     for (int64_t b = b0; b < p.batch && b < b0 + (int64_t)threads * gridDim.x; b += gridDim.x) {
       if (seq_len(p, (int)b)) continue;
-      for (int i = threadIdx.x; i < n; i += threads) {
-        const int row = i / q, kvh = row / p.rows;
-        write_row<BF16>(p, (int)b, kvh, row - kvh * p.rows, i - row * q, make_float4(0.f, 0.f, 0.f, 0.f), 0.0f, 0.0f);
+      for (int64_t i = r0; i < (int64_t)p.c.heads * p.rows; i += lanes) {
+        const int kvh = (int)(i / p.rows), row = (int)(i - (int64_t)kvh * p.rows);
+        write_row<BF16>(p, (int)b, kvh, row, d4, make_float4(0.f, 0.f, 0.f, 0.f), 0.0f, 0.0f);
       }
     }
   }

@@ -482,10 +482,13 @@ attn_status_t attn_kv_read(const attn_kv4_cache_t* cache, attn_dtype_t dtype, in
  * (natural log; a query that sees nothing, of an empty sequence or at a
  * negative position, gets O = 0, LSE = -inf).  Entries of the table past a
  * sequence's last page, and what a page holds past its last token, are not
- * looked at.  Sums are FP32; probabilities times V's scales are rounded to
- * dtype for the second product.  The result does not depend on other
- * sequences' lengths beyond the order of its sums, and is bitwise
- * reproducible for the same call on the same device.
+ * looked at.  Sums are FP32.  A bf16 q row enters the first product in FP16,
+ * times a power of two that keeps all but elements 2^27 times smaller than its
+ * largest; probabilities times V's scales are rounded to FP16, in units set by
+ * the largest V scale of the tokens met so far: beside a token whose V is 2^24
+ * times the others', the others lose bits.  The result does not depend on other
+ * sequences' lengths beyond the order of its sums, and is bitwise reproducible
+ * for the same call on the same device.
  * Lengths are read on the device: a captured call serves any lengths.
  * seq_lens out of [0, cols * page_size] count as 0 and set the status word; so
  * does a page outside the cache (that sequence's result is then undefined).
