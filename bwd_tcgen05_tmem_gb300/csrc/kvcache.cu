@@ -174,12 +174,12 @@ cudaError_t launch_kv_plan(const PlanParams& p, int num_sms, cudaStream_t st) {
 // several tokens at a time; where it has more, blockIdx.y picks 256 of them.
 // Groups (4 lanes) and pairs of groups (8 lanes) never straddle a warp or a
 // row, because d is a multiple of 64.
-// Streams, bound by HBM if a word of codes costs few enough instructions: about
-// 140 a warp and vector to store (60% of the issue slots taken), 80 to read
-// back.  Measured on a GB300 (graph replays, 32768 tokens, 8 kv heads, 128 / 128,
-// bf16): stored in 43 us (172 MB, 4.0 TB/s, 59% of a plain copy's rate), read
-// back in 31 us (5.6 TB/s, 83%); 64 tokens stored and read back 4.2 us, two
-// launches.  One thread a vector without the ring of copies: 155 us for both.
+// Streams, bound by HBM if a word of codes costs few enough instructions: to
+// read back takes about 80 a warp and vector, to store somewhat more (its issue
+// slots are 60 to 70% taken).  Measured on a GB300 (graph replays, 32768 tokens, 8
+// kv heads, 128 / 128, bf16): stored in 37 us (172 MB, 4.7 TB/s, 69% of a plain
+// copy's rate), read back in 31 us (5.5 TB/s, 82%); 64 tokens stored and read
+// back 4.5 us, two launches.  Without the ring of copies: 155 us for both.
 struct RowLane {
   bool live, is_k;
   int token;         // of the block's first pass
@@ -296,72 +296,100 @@ __device__ __noinline__ uint32_t tiny_codes_of(uint32_t w0, uint32_t w1, uint32_
   return word;
 }
 
-// Rows come through a ring of asynchronous copies, kRing tokens deep; a thread
-// copies and reads its own vectors alone.
+// Rows come through a ring of asynchronous copies, kRing times kU tokens deep; a
+// thread copies and reads its own vectors alone.  kU tokens at a time share what
+// a pass of the loop costs and hide each other's exchanges (1: 76 us, 2: 67 us, 3:
+// 66 us, 4: 70 us for 32768 tokens stored and read back).
 template <bool BF16>
 __global__ void __launch_bounds__(256, 4) attn_kv_write_kernel(const __grid_constant__ KvRowsParams p) {
-  constexpr int kRing = 8;
-  __shared__ uint4 ring[kRing][256];
+  constexpr int kRing = 3, kU = 3;
+  __shared__ uint4 ring[kRing][kU][256];
   const RowLane r = row_lane(p);
   const uint32_t odd = (uint32_t)(threadIdx.x >> 2) & 1u;  // odd group of a pair
   const CacheLane at = cache_lane(p, r, odd);
-  const uint16_t* src = (const uint16_t*)(r.is_k ? p.k : p.v) + r.in_row + (int64_t)r.token * r.stride;
-  const int64_t src_step = (int64_t)r.step * r.stride;
-  int next = r.token;  // the next token to copy
+  const int64_t src_step = (int64_t)r.step * r.stride * 2;
+  const char* src = (const char*)((const uint16_t*)(r.is_k ? p.k : p.v) + r.in_row + (int64_t)r.token * r.stride);
+  // tokens of this thread that are still to copy, and to store
+  int to_copy = r.live && r.token < p.tokens ? (p.tokens - r.token + r.step - 1) / r.step : 0, left = to_copy;
+  const uint32_t my = smem_u32(&ring[0][0][threadIdx.x]);
   auto copy = [&](int s) {
-    if (r.live && next < p.tokens)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&ring[s][threadIdx.x])),
-                   "l"((uint64_t)__cvta_generic_to_global(src)) : "memory");
-    next += r.step;
-    src += src_step;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (u < to_copy)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(my + (s * kU + u) * 4096),
+                     "l"((uint64_t)__cvta_generic_to_global(src)) : "memory");
+      src += src_step;
+    }
+    to_copy -= kU;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int i = 0; i < kRing - 1; ++i) copy(i);
-  int s = 0, next_slot = r.live && r.token < p.tokens ? __ldg(p.slots + r.token) : -1;
+  // slots are looked up one group ahead
+  const int32_t* slot_at = p.slots + r.token;
+  int next_slot[kU];
+  auto look_up = [&](int n) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) next_slot[u] = u < n ? __ldg(slot_at + (int64_t)u * r.step) : -1;
+    slot_at += (int64_t)kU * r.step;
+  };
+  look_up(left);
+  int s = 0;
   // the lanes of a warp stay together: they exchange words
-  for (int t = r.token; __any_sync(0xffffffffu, r.live && t < p.tokens); t += r.step) {
+  for (; __any_sync(0xffffffffu, left > 0); left -= kU) {
     copy((s + kRing - 1) % kRing);
     asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-    const bool here = r.live && t < p.tokens;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    int slot = next_slot;  // looked up one token ahead
-    next_slot = r.live && t + r.step < p.tokens ? __ldg(p.slots + t + r.step) : -1;
-    if (here) x = ring[s][threadIdx.x];
+    int slot[kU];
+    uint4 x[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      slot[u] = next_slot[u];
+      x[u] = make_uint4(0x3c003c00u, 0u, 0u, 0u);  // (zeros would take the slow way below)
+      if (u < left) x[u] = ring[s][u][threadIdx.x];
+    }
+    look_up(left - kU);
     s = (s + 1) % kRing;
-    if (slot >= 0 && (slot >> p.c.page_shift) >= p.c.num_pages) {
-      if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
-      slot = -1;
+    uint32_t word[kU];
+    uint16_t sbits[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      // max|x| of the group of 32: the bit patterns of magnitudes are ordered,
+      // infinities and NaN above all finite ones
+      uint32_t m = __vmaxu2(__vmaxu2(x[u].x & 0x7fff7fffu, x[u].y & 0x7fff7fffu),
+                            __vmaxu2(x[u].z & 0x7fff7fffu, x[u].w & 0x7fff7fffu));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      m = max(m & 0xffffu, m >> 16);
+      // max / 7 as the division rounds it: the product corrected by its remainder
+      const float amax = Pack<BF16>::to_f((uint16_t)m);
+      float q = amax * (1.0f / 7.0f);
+      q = fmaf(fmaf(-q, 7.0f, amax), 1.0f / 7.0f, q);
+      __nv_bfloat16 sb = __float2bfloat16_rn(q);
+      sbits[u] = __bfloat16_as_ushort(sb);
+      word[u] = codes_of<BF16>(x[u], __bfloat162float(sb));
+      if (amax < 1e-29f) {  // zeros, and numbers so small that 1 / s or a remainder is not normal
+        sb = __float2bfloat16_rn(__fdiv_rn(amax, 7.0f));
+        sbits[u] = __bfloat16_as_ushort(sb);
+        word[u] = tiny_codes_of<BF16>(x[u].x, x[u].y, x[u].z, x[u].w, __bfloat162float(sb));
+      } else if (m >= (BF16 ? 0x7f80u : 0x7c00u)) {  // a group with an infinity or a NaN: NaN
+        sbits[u] = 0x7fffu;
+        word[u] = 0x88888888u;
+      }
     }
-    // max|x| of the group of 32: the bit patterns of magnitudes are ordered,
-    // infinities and NaN above all finite ones
-    uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                          __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    m = max(m & 0xffffu, m >> 16);
-    // max / 7 as the division rounds it: the product corrected by its remainder
-    const float amax = Pack<BF16>::to_f((uint16_t)m);
-    float q = amax * (1.0f / 7.0f);
-    q = fmaf(fmaf(-q, 7.0f, amax), 1.0f / 7.0f, q);
-    __nv_bfloat16 sb = __float2bfloat16_rn(q);
-    uint16_t sbits = __bfloat16_as_ushort(sb);
-    uint32_t word = codes_of<BF16>(x, __bfloat162float(sb));
-    if (amax < 1e-29f) {  // zeros, and numbers so small that 1 / s or a remainder is not normal
-      sb = __float2bfloat16_rn(__fdiv_rn(amax, 7.0f));
-      sbits = __bfloat16_as_ushort(sb);
-      word = tiny_codes_of<BF16>(x.x, x.y, x.z, x.w, __bfloat162float(sb));
-    } else if (m >= (BF16 ? 0x7f80u : 0x7c00u)) {  // a group with an infinity or a NaN: NaN
-      sbits = 0x7fffu;
-      word = 0x88888888u;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      // V rows: two neighbouring groups exchange halves, so that each lane
+      // holds the half-words (r, g), (r, g + 1) of one word
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? word[u] & 0xffffu : word[u] >> 16, 4);
+      if (slot[u] < 0) continue;
+      if ((slot[u] >> p.c.page_shift) >= p.c.num_pages) {
+        if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+        continue;
+      }
+      if (!r.is_k) word[u] = odd ? (other | (word[u] & 0xffff0000u)) : ((word[u] & 0xffffu) | (other << 16));
+      *at.word(p.c, slot[u]) = word[u];
+      if (r.c == 0) *at.scale(p.c, slot[u]) = sbits[u];
     }
-    // V rows: two neighbouring groups exchange halves, so that each lane
-    // holds the half-words (r, g), (r, g + 1) of one word
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? word & 0xffffu : word >> 16, 4);
-    if (slot < 0) continue;
-    if (!r.is_k) word = odd ? (other | (word & 0xffff0000u)) : ((word & 0xffffu) | (other << 16));
-    *at.word(p.c, slot) = word;
-    if (r.c == 0) *at.scale(p.c, slot) = sbits;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
