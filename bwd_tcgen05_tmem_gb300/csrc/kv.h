@@ -35,6 +35,7 @@ struct QkSide {  // queries or keys
   const void* w;   // the norm's weights, or null
   int64_t x_b, x_t, x_h, dz_b, dz_t, dz_h, o_b, o_t, o_h;
   int heads;
+  int per_job;     // tokens of a job (above 1 where a token's heads leave lanes idle)
   float* dw;       // backward: [d], or null
 };
 

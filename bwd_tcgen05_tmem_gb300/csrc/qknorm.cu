@@ -30,6 +30,7 @@
 // 3 x 1001 tokens of 6 + 2 heads of 192 13 us, two dependent launches and the
 // join of dw.  Loads into registers instead of the ring: 155 and 173 us.
 #include <algorithm>
+#include <type_traits>
 
 #include "kcommon.cuh"
 #include "kv.h"
@@ -143,10 +144,10 @@ __device__ __forceinline__ void load_weights(const QkParams& p, const void* w, i
   }
 }
 
-// Cosines and sines of a unit's 8 pairs, packed over e.
+// Cosines and sines of a unit's 8 pairs, packed over e (none at a negative pos).
 __device__ __forceinline__ void load_angles(const QkParams& p, int pos, int u, int a, int b,
                                             uint64_t (&c)[4], uint64_t (&s)[4]) {
-  if (u >= (p.rot >> 4)) {
+  if (pos < 0 || u >= (p.rot >> 4)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = f2_pack(1.0f, 1.0f), s[i] = f2_pack(0.0f, 0.0f);
     return;
@@ -174,6 +175,13 @@ __device__ __forceinline__ float row_sum(uint64_t v) {
   return s;
 }
 
+// 1 / sqrt(sum / D + eps).  Finite for rows of zeros at eps = 0 too (they stay
+// zeros): lanes without a row hold such, and must add nothing to dw.
+template <int D>
+__device__ __forceinline__ float rms_inverse(float sum, float eps) {
+  return rsqrtf(fmaxf(fmaf(sum, 1.0f / D, eps), 1.17549435e-38f));
+}
+
 // A copy of 16 bytes, or of zeros.
 __device__ __forceinline__ void copy16(uint4* dst, const void* src, bool here) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
@@ -189,14 +197,19 @@ __device__ __forceinline__ void copies_wait() {  // all but the last N groups of
 constexpr int kQkThreads = 128, kQkWarps = kQkThreads / 32;
 constexpr int kPad = -1, kNoAngle = -2;  // positions: padding; outside the tables
 
+template <bool MANY>
 __device__ __forceinline__ int token_position(const QkParams& p, uint32_t tok) {
+  if (MANY && tok >= (uint32_t)p.batch * p.seq_div.d) return kPad;  // behind the last token
   const int pos = p.positions ? __ldg(p.positions + tok) : (int)(tok - p.seq_div.div(tok) * p.seq_div.d);
   return pos < 0 ? kPad : pos >= p.max_pos && p.rot > 0 ? kNoAngle : pos;
 }
 
-// A job is one token and one run of kSlots * U of its heads, of one side; the
-// side's blocks share its jobs, a warp takes every (blocks * warps)-th.  A
-// lane's view of the side's tensors: byte offsets from its vector a of its row
+// A job is one token and one run of kSlots * U of its heads, of one side; where
+// half of the kSlots rows that a warp holds at a time or more would be idle, it
+// is several tokens in a row with all of their heads (48K tokens of 2 + 2 heads of
+// 64, gradient: 29 us, one token a job 85 us; only calls with such a side run that
+// form, which costs the others 4%).  The side's blocks share its
+// jobs, a warp takes every (blocks * warps)-th.  A lane's view of the side's tensors: byte offsets from its vector a of its row
 // (slot) of the first run.
 struct QkLane {
   int64_t b, t, run, u;  // of a sequence, a token, a run, kSlots heads
@@ -209,23 +222,24 @@ __device__ __forceinline__ QkLane qk_lane(int64_t sb, int64_t st, int64_t sh) {
   return QkLane{sb * 2, st * 2, sh * (2 * SLOTS * U), sh * (2 * SLOTS)};
 }
 
-// The ring: NV vectors a lane and row (of x, and of dz), the job's token and
-// its position.
+// The ring: NV vectors a lane and row (of x, and of dz), and for each lane its
+// token and that one's position.
 template <int U, int NV, int STAGES>
 struct QkRing {
   uint4 v[STAGES][U][NV][kQkThreads];
-  uint32_t tok[STAGES][kQkWarps];
-  int pos[STAGES][kQkWarps];
+  uint2 job[STAGES][kQkThreads];
 };
 
 // What both directions share: which jobs a warp has, and copying the next one.
-template <int D, int U, int NV, int STAGES>
+// MANY: jobs may have several tokens, so tokens and positions differ between lanes.
+template <int D, int U, int NV, int STAGES, bool MANY>
 struct QkWarp {
   using S = QkShape<D>;
   const QkParams& p;
   const QkSide& sd;
   QkRing<U, NV, STAGES>& ring;
-  int warp, lane, slot;
+  int warp, lane, slot;  // slot: the lane's head of a group of rows
+  int sub, per_job;      // its token of the job, the job's tokens
   bool active;
   FastDiv runs;
   uint32_t end, step, next;
@@ -239,12 +253,21 @@ struct QkWarp {
     lane = threadIdx.x & 31;
     warp = threadIdx.x >> 5;
     slot = lane / S::kLpr;
+    per_job = 1;
+    sub = 0;
+    if (MANY) {
+      per_job = sd.per_job;
+      const int heads = S::kSlots / per_job;  // (a power of two)
+      sub = slot / heads;
+      slot -= sub * heads;
+    }
     active = lane % S::kLpr < S::kUnits;
     runs = p.runs[is_k ? 1 : 0];
-    end = (uint32_t)p.batch * p.seq_div.d * runs.d;  // below 2^31, checked at launch
+    // below 2^31, checked at launch
+    end = ((uint32_t)p.batch * p.seq_div.d + per_job - 1) / per_job * runs.d;
     step = (uint32_t)p.blocks[is_k ? 1 : 0] * kQkWarps;
     next = (blockIdx.x - (is_k ? (uint32_t)p.blocks[0] : 0u)) * kQkWarps + warp;
-    next_pos = next < end ? token_position(p, runs.div(next)) : kPad;
+    next_pos = next < end ? token_position<MANY>(p, token(next)) : kPad;
     x = (const char*)sd.x + ((int64_t)slot * sd.x_h + a * 8) * 2;
     lx = qk_lane<S::kSlots, U>(sd.x_b, sd.x_t, sd.x_h);
     if (NV == 4) {
@@ -253,17 +276,22 @@ struct QkWarp {
     }
     vb = (b - a) * 16;
   }
-  // Row groups of a run that hold a head, and whether this lane's row of group u does.
+  __device__ __forceinline__ uint32_t token(uint32_t job) const {
+    return runs.div(job) * (uint32_t)per_job + sub;
+  }
+  // Row groups of a run that hold a head.
   __device__ __forceinline__ int groups(uint32_t run) const {
     return min(U, (sd.heads - (int)run * (S::kSlots * U) + S::kSlots - 1) / S::kSlots);
   }
-  __device__ __forceinline__ bool here(uint32_t run, int u) const {
-    return active && (int)run * (S::kSlots * U) + u * S::kSlots + slot < sd.heads;
+  // Whether this lane's row of group u is one.
+  __device__ __forceinline__ bool here(uint32_t run, int u, int pos) const {
+    return active && (int)run * (S::kSlots * U) + u * S::kSlots + slot < sd.heads && !(MANY && pos == kPad);
   }
   __device__ __forceinline__ void copy(int s) {
     if (next < end) {
-      const uint32_t tok = runs.div(next), run = next - tok * runs.d;
-      if (next_pos != kPad) {
+      const uint32_t first = runs.div(next), run = next - first * runs.d;
+      const uint32_t tok = first * (uint32_t)per_job + sub;
+      if (MANY ? __any_sync(0xffffffffu, next_pos != kPad) : next_pos != kPad) {
         const uint32_t b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
         const char* px = x + lx.at(b, t, run);
         const char* pz = NV == 4 ? dz + lz.at(b, t, run) : nullptr;
@@ -271,7 +299,7 @@ struct QkWarp {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if (u >= n) break;
-          const bool is = here(run, u);  // (else the address is not used)
+          const bool is = here(run, u, next_pos);  // (else zeros; the address is not used)
           uint4(*v)[kQkThreads] = ring.v[s][u];
           copy16(&v[0][threadIdx.x], is ? px : x, is);
           copy16(&v[1][threadIdx.x], is ? px + vb : x, is);
@@ -283,16 +311,16 @@ struct QkWarp {
           }
         }
       }
-      if (lane == 0) ring.tok[s][warp] = tok, ring.pos[s][warp] = next_pos;
+      if (MANY || lane == 0) ring.job[s][MANY ? threadIdx.x : warp] = make_uint2(tok, (uint32_t)next_pos);
       next += step;
-      if (next < end) next_pos = token_position(p, runs.div(next));
+      if (next < end) next_pos = token_position<MANY>(p, token(next));
     }
     copies_end();
   }
 };
 
 // ----------------------------------------------------------------- forward
-template <bool BF16, int D, int U, bool INTER>
+template <bool BF16, int D, int U, bool INTER, bool MANY>
 __global__ void __launch_bounds__(kQkThreads, 6) attn_qk_fwd_kernel(
     const __grid_constant__ QkParams p) {
   using S = QkShape<D>;
@@ -301,7 +329,7 @@ __global__ void __launch_bounds__(kQkThreads, 6) attn_qk_fwd_kernel(
   const int l = min((int)(threadIdx.x & 31) % S::kLpr, S::kUnits - 1);
   int va, vb;
   unit_vectors(l, p.rot, S::kUnits, va, vb);
-  QkWarp<D, U, 2, kStages> w(p, ring, (int)blockIdx.x >= p.blocks[0], va, vb);
+  QkWarp<D, U, 2, kStages, MANY> w(p, ring, (int)blockIdx.x >= p.blocks[0], va, vb);
   char* out = (char*)w.sd.out + ((int64_t)w.slot * w.sd.o_h + va * 8) * 2;
   const QkLane lo = qk_lane<S::kSlots, U>(w.sd.o_b, w.sd.o_t, w.sd.o_h);
   uint32_t job = w.next;
@@ -312,17 +340,18 @@ __global__ void __launch_bounds__(kQkThreads, 6) attn_qk_fwd_kernel(
     w.copy(s == 0 ? kStages - 1 : s - 1);  // the stage used last
     copies_wait<kStages - 1>();
     __syncwarp();
-    const uint32_t tok = ring.tok[s][w.warp];
-    const int pos = ring.pos[s][w.warp];
-    if (pos == kPad) continue;
-    if (pos == kNoAngle && w.lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+    const uint2 at = ring.job[s][MANY ? threadIdx.x : w.warp];
+    const uint32_t tok = at.x;
+    const int pos = (int)at.y;
+    if (MANY ? __all_sync(0xffffffffu, pos == kPad) : pos == kPad) continue;
+    if (pos == kNoAngle && w.slot == 0 && l == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
     uint64_t pc[4], ps[4], qc[4], qs[4];  // weights times cosines and sines
     {
       float fa[8], fb[8];
       load_weights<BF16>(p, w.sd.w, va, fa);
       load_weights<BF16>(p, w.sd.w, vb, fb);
       const Pairs wt = pairs_of<INTER>(fa, fb);
-      load_angles(p, pos < 0 ? 0 : pos, l, va, vb, pc, ps);
+      load_angles(p, pos, l, va, vb, pc, ps);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         qc[i] = f2_mul(wt.q[i], pc[i]);
@@ -331,7 +360,8 @@ __global__ void __launch_bounds__(kQkThreads, 6) attn_qk_fwd_kernel(
         ps[i] = f2_mul(wt.p[i], ps[i]);
       }
     }
-    const uint32_t run = job - tok * w.runs.d, b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
+    const uint32_t run = job - (MANY ? w.runs.div(job) : tok) * w.runs.d;
+    const uint32_t b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
     char* po = out + lo.at(b, t, run);
     const int n = w.groups(run);
 #pragma unroll 1
@@ -342,7 +372,7 @@ __global__ void __launch_bounds__(kQkThreads, 6) attn_qk_fwd_kernel(
         uint64_t ss = f2_mul(x.p[0], x.p[0]), st = f2_mul(x.q[0], x.q[0]);
 #pragma unroll
         for (int i = 1; i < 4; ++i) ss = f2_fma(x.p[i], x.p[i], ss), st = f2_fma(x.q[i], x.q[i], st);
-        r = rsqrtf(row_sum<S::kLpr>(f2_add(ss, st)) * (1.0f / D) + p.eps);
+        r = rms_inverse<D>(row_sum<S::kLpr>(f2_add(ss, st)), p.eps);
       }
       if (pos == kNoAngle) r = __int_as_float(0x7fffffff);  // NaN
       const uint64_t r2 = f2_both(r);
@@ -352,7 +382,7 @@ __global__ void __launch_bounds__(kQkThreads, 6) attn_qk_fwd_kernel(
         z.p[i] = f2_mul(r2, f2_fma(x.q[i], qs[i], f2_mul(x.p[i], pc[i])));
         z.q[i] = f2_mul(r2, f2_fma(x.p[i], ps[i], f2_mul(x.q[i], qc[i])));
       }
-      if (w.here(run, u)) pack<BF16, INTER>(z, *(uint4*)po, *(uint4*)(po + w.vb));
+      if (w.here(run, u, pos)) pack<BF16, INTER>(z, *(uint4*)po, *(uint4*)(po + w.vb));
     }
   }
   copies_wait<0>();
@@ -363,7 +393,7 @@ __global__ void __launch_bounds__(kQkThreads, 6) attn_qk_fwd_kernel(
 // lane's share of dw stays in registers over all rows of its block; each block
 // leaves one row of partial sums, which a second kernel adds up in the order
 // of the blocks (no atomics: the result does not depend on who came first).
-template <bool BF16, int D, int U, bool INTER>
+template <bool BF16, int D, int U, bool INTER, bool MANY>
 __global__ void __launch_bounds__(kQkThreads, 4) attn_qk_bwd_kernel(
     const __grid_constant__ QkParams p) {
   using S = QkShape<D>;
@@ -373,7 +403,7 @@ __global__ void __launch_bounds__(kQkThreads, 4) attn_qk_bwd_kernel(
   const int l = min((int)(threadIdx.x & 31) % S::kLpr, S::kUnits - 1);
   int va, vb;
   unit_vectors(l, p.rot, S::kUnits, va, vb);
-  QkWarp<D, U, 4, kStages> w(p, ring, (int)blockIdx.x >= p.blocks[0], va, vb);
+  QkWarp<D, U, 4, kStages, MANY> w(p, ring, (int)blockIdx.x >= p.blocks[0], va, vb);
   char* out = (char*)w.sd.out + ((int64_t)w.slot * w.sd.o_h + va * 8) * 2;
   const QkLane lo = qk_lane<S::kSlots, U>(w.sd.o_b, w.sd.o_t, w.sd.o_h);
   Pairs wt, dw;
@@ -393,13 +423,15 @@ __global__ void __launch_bounds__(kQkThreads, 4) attn_qk_bwd_kernel(
     w.copy(s == 0 ? kStages - 1 : s - 1);
     copies_wait<kStages - 1>();
     __syncwarp();
-    const uint32_t tok = ring.tok[s][w.warp];
-    const int pos = ring.pos[s][w.warp];
-    if (pos == kPad) continue;
-    if (pos == kNoAngle && w.lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+    const uint2 at = ring.job[s][MANY ? threadIdx.x : w.warp];
+    const uint32_t tok = at.x;
+    const int pos = (int)at.y;
+    if (MANY ? __all_sync(0xffffffffu, pos == kPad) : pos == kPad) continue;
+    if (pos == kNoAngle && w.slot == 0 && l == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
     uint64_t c[4], sn[4];
-    load_angles(p, pos < 0 ? 0 : pos, l, va, vb, c, sn);
-    const uint32_t run = job - tok * w.runs.d, b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
+    load_angles(p, pos, l, va, vb, c, sn);
+    const uint32_t run = job - (MANY ? w.runs.div(job) : tok) * w.runs.d;
+    const uint32_t b = p.seq_div.div(tok), t = tok - b * p.seq_div.d;
     char* po = out + lo.at(b, t, run);
     const int n = w.groups(run);
 #pragma unroll 1
@@ -421,7 +453,7 @@ __global__ void __launch_bounds__(kQkThreads, 4) attn_qk_bwd_kernel(
       }
       float r = 1.0f, k = 0.0f;
       if (p.norm) {
-        r = rsqrtf(row_sum<S::kLpr>(ss) * (1.0f / D) + p.eps);
+        r = rms_inverse<D>(row_sum<S::kLpr>(ss), p.eps);
         k = r * r * (row_sum<S::kLpr>(gx) * (1.0f / D));
       }
       if (pos == kNoAngle) r = __int_as_float(0x7fffffff);
@@ -433,7 +465,7 @@ __global__ void __launch_bounds__(kQkThreads, 4) attn_qk_bwd_kernel(
         g.p[i] = f2_mul(r2, f2_fma(x.p[i], k2, g.p[i]));
         g.q[i] = f2_mul(r2, f2_fma(x.q[i], k2, g.q[i]));
       }
-      if (w.here(run, u)) pack<BF16, INTER>(g, *(uint4*)po, *(uint4*)(po + w.vb));
+      if (w.here(run, u, pos)) pack<BF16, INTER>(g, *(uint4*)po, *(uint4*)(po + w.vb));
     }
   }
   copies_wait<0>();
@@ -457,7 +489,7 @@ __global__ void __launch_bounds__(kQkThreads, 4) attn_qk_bwd_kernel(
 #pragma unroll
     for (int o = S::kLpr; o < 32; o <<= 1) f[e] += __shfl_xor_sync(0xffffffffu, f[e], o);
   __syncthreads();
-  if (w.slot == 0 && w.active)
+  if (w.lane < S::kLpr && w.active)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       part[w.warp * D + va * 8 + e] = f[e];
@@ -502,21 +534,25 @@ constexpr int kJobCost = 4;  // (1: 127 us, 2: 122 us, 4: 116 us for 32K tokens 
 // all, shared out by the sides' costs (a job costs kJobCost groups besides its
 // own); never more than leave each warp `least` jobs.  False: too many jobs.
 bool share_blocks(QkParams& p, int most, int slots, int groups, int least) {
-  const int64_t tokens = (int64_t)p.batch * p.seqlen;
+  const int64_t all_tokens = (int64_t)p.batch * p.seqlen;
   p.seq_div = FastDiv::of((uint32_t)std::max(p.seqlen, 1));
   bool ok = true;
-  int64_t runs[2], cost[2];
+  int64_t runs[2], cost[2], tokens[2];
   for (int s = 0; s < 2; ++s) {
     const int64_t h = p.side[s].heads;
+    int per = slots;
+    while (per > 1 && per * h > slots) per /= 2;
+    p.side[s].per_job = per;
+    tokens[s] = (all_tokens + per - 1) / per;
     runs[s] = std::max<int64_t>((h + slots * groups - 1) / (slots * groups), 1);
-    cost[s] = h ? runs[s] * kJobCost + (h + slots - 1) / slots : 0;
+    cost[s] = h ? tokens[s] * (runs[s] * kJobCost + (h + slots - 1) / slots) : 0;
     p.runs[s] = FastDiv::of((uint32_t)runs[s]);
-    ok = ok && tokens * runs[s] < (1ll << 31) - (1 << 20);
+    ok = ok && tokens[s] * runs[s] < (1ll << 31) - (1 << 20);
   }
   for (int s = 0; s < 2; ++s) {
     const int64_t all = std::max<int64_t>(cost[0] + cost[1], 1);
-    int64_t n = (most * cost[s] + all / 2) / all;
-    n = std::min(n, (tokens * runs[s] + least * kQkWarps - 1) / (least * kQkWarps));
+    int64_t n = (int64_t)((double)most * cost[s] / all + 0.5);
+    n = std::min(n, (tokens[s] * runs[s] + least * kQkWarps - 1) / (least * kQkWarps));
     p.blocks[s] = p.side[s].heads > 0 ? (int)std::max<int64_t>(n, 1) : 0;
   }
   return ok;
@@ -524,21 +560,33 @@ bool share_blocks(QkParams& p, int most, int slots, int groups, int least) {
 
 int slots_of(int d) { return d == 192 ? 2 : 32 / (d / 16); }
 
+// f with the call's order of pairs, and whether a side's jobs have several tokens
+template <typename F>
+void variants(const QkParams& p, F&& f) {
+  const bool many = p.side[0].per_job > 1 || (p.side[1].heads && p.side[1].per_job > 1);
+  using Y = std::true_type;
+  using N = std::false_type;
+  if (p.inter)
+    many ? f(Y(), Y()) : f(Y(), N());
+  else
+    many ? f(N(), Y()) : f(N(), N());
+}
+
 template <bool BF16, int D>
 cudaError_t fwd_launch(const QkParams& p, cudaStream_t st) {
-  if (p.inter)
-    attn_qk_fwd_kernel<BF16, D, kFwdRows, true><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
-  else
-    attn_qk_fwd_kernel<BF16, D, kFwdRows, false><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
+  variants(p, [&](auto inter, auto many) {
+    attn_qk_fwd_kernel<BF16, D, kFwdRows, decltype(inter)::value, decltype(many)::value>
+        <<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
+  });
   return cudaGetLastError();
 }
 
 template <bool BF16, int D>
 cudaError_t bwd_launch(const QkParams& p, cudaStream_t st) {
-  if (p.inter)
-    attn_qk_bwd_kernel<BF16, D, kBwdRows, true><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
-  else
-    attn_qk_bwd_kernel<BF16, D, kBwdRows, false><<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
+  variants(p, [&](auto inter, auto many) {
+    attn_qk_bwd_kernel<BF16, D, kBwdRows, decltype(inter)::value, decltype(many)::value>
+        <<<p.blocks[0] + p.blocks[1], kQkThreads, 0, st>>>(p);
+  });
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!p.side[0].dw && !p.side[1].dw)) return e;
   cudaLaunchAttribute attr;

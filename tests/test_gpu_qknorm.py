@@ -277,3 +277,60 @@ def test_with_attention_training():
     for t, w in ((o, o64.detach()), *zip(got, [y.grad for y in x])):
         rel = float((t.double() - w).norm() / w.norm())
         assert rel < 0.008 + 4 * 2.0 ** -8 / 3 ** 0.5, rel
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 1), (2, 1), (3, 2), (4, 3)])
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+def test_few_heads(hq, hk, d):
+    """Several tokens share a warp where a token's heads leave it lanes."""
+    cos, sin = attn.rope_tables(5000, 64)
+    for b, s in ((1, 1), (1, 7), (3, 43)):
+        check(make(b, s, hq, hk, d, BF, seed=d + hq + s), cos, sin, False)
+
+
+def test_few_heads_with_padding_between_tokens():
+    m = make(3, 21, 2, 1, 64, BF, seed=21)
+    cos, sin = attn.rope_tables(5000, 64)
+    kw = dict(wq=m["wq"], wk=m["wk"])
+    whole = attn.qk_norm_rope(m["q"], m["k"], cos, sin, positions=m["pos"], **kw)
+    full = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], positions=m["pos"], **kw)
+    pos = m["pos"].clone()
+    pos[:, ::3] = -1
+    pos[1] = -7
+    pad = pos < 0
+    q, k = (torch.full(t.shape, 5.0, dtype=BF, device="cuda") for t in whole)
+    attn.qk_norm_rope(m["q"], m["k"], cos, sin, positions=pos, q_out=q, k_out=k, **kw)
+    dq, dk = torch.full_like(q, 5.0), torch.full_like(k, 5.0)
+    g = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], positions=pos, dq=dq, dk=dk, **kw)
+    for got, want in zip((q, k, dq, dk), whole + full[:2]):
+        assert (got[pad] == 5.0).all() and torch.equal(got[~pad], want[~pad])
+    # dw of the rows that are left, from the float64 form
+    c, s = cos[pos.clamp(min=0).long()].double(), sin[pos.clamp(min=0).long()].double()
+    for x, w, dz, dw in ((m["q"], m["wq"], m["dqo"], g[2]), (m["k"], m["wk"], m["dko"], g[3])):
+        w64 = w.double().requires_grad_()
+        z = kvref.norm_rope(x.double(), w64, c, s, True, 1e-6, False)
+        ((z * dz.double())[~pad]).sum().backward()
+        r = 1 / torch.sqrt(x.double().pow(2).mean(-1, keepdim=True) + 1e-6)
+        total = (pair_length(dz.double(), 64, False) * (x.double() * r).abs())[~pad].sum((0, 1))
+        close(dw, w64.grad, 2.0 ** -24 * (63 * x.shape[2] + 64) * total)
+
+
+@pytest.mark.parametrize("heads,d", [((5, 2), 128), ((1, 1), 64), ((3, 1), 192)])
+def test_gradient_without_eps(heads, d):
+    """Lanes without a row add nothing to the weights' gradient, at eps = 0 either."""
+    cos, sin = attn.rope_tables(5000, 64)
+    check(make(2, 19, *heads, d, BF, seed=22, spread=False), cos, sin, False, eps=0.0)
+
+
+def test_tables_without_positions():
+    """max_pos = 0: every position is outside, and nothing is read."""
+    m = make(1, 9, 4, 2, 128, BF, seed=23)
+    cos, sin = (t[:0] for t in attn.rope_tables(8, 128))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    try:
+        z = attn.qk_norm_rope(m["q"], m["k"], cos, sin, positions=m["pos"], status=status)
+    except attn.AttnError:
+        return  # (an empty tensor without an address is refused)
+    assert torch.isnan(z[0]).all() and torch.isnan(z[1]).all()
+    with pytest.raises(attn.AttnError, match="out of range"):
+        attn.query_status(status)
