@@ -26,7 +26,7 @@
 // Measured on a GB300 (graph replays, bf16, head dim 128, 32 + 8 heads): forward
 // of 32768 tokens 116 us, 5.9 TB/s (88% of a plain copy's rate); gradient of
 // 16384 tokens 97 us, 5.2 TB/s (77%: bound by instruction issue beside the
-// copies, about 25 a pair of elements); 8 tokens 3.1 us, a launch; a gradient of
+// copies, about 44 a pair of elements); 8 tokens 3.1 us, a launch; a gradient of
 // 3 x 1001 tokens of 6 + 2 heads of 192 13 us, two dependent launches and the
 // join of dw.  Loads into registers instead of the ring: 155 and 173 us.
 #include <algorithm>

@@ -349,7 +349,8 @@ attn_status_t attn_cp_relayout(int to_heads, int cp, int64_t seqlen, int heads, 
 /*
  * Norm of each query and key head and rotation by its position, in one pass.
  * For every row x (token, head; head_dim elements), in FP32:
- *     y = x / sqrt(mean(x^2) + eps) * w        (norm = 0: y = x, w = NULL)
+ *     y = x / sqrt(mean(x^2) + eps) * w        (norm = 0: y = x, w = NULL; a row of
+ *                                               zeros stays zeros, at eps = 0 too)
  *     z = y turned by the angles of the token's position on its first
  *         rotary_dim elements: pairs (i, i + rotary_dim/2), or (2i, 2i+1) with
  *         interleaved = 1:  (a, b) -> (a cos - b sin, b cos + a sin)
