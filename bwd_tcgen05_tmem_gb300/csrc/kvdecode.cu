@@ -912,14 +912,18 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
 //
 // By item: a block for each row of each item, whose pieces are shared out over
 // groups of threads; the groups' sums are added in their order.  It spreads the
-// work best where few items are cut into many pieces.  By run: 128 threads look
+// work best where few items are cut into many pieces; where they are cut into very
+// many, the blocks are larger (one request of 65536 tokens, 8 kv heads: 256
+// threads 34.8 us, 1024 29.7 us; 10^6 tokens, one kv head: 111 and 63 us; 16 x 32K
+// tokens: 117 and 125 us).  By run: 128 threads look
 // at a run, and join the item that it ends for others (the whole block does
 // where that has many pieces): no more blocks than the runs need, however many
 // items there are.  Measured, whole call: 128 items (16 x 32K tokens) by item
 // 131 us, by run 137 us; 4096 items (512 x 1K) by item 170 us, by run 148 us.
 constexpr int kByItemPieces = 4;  // of an item on average: from there on by item
 constexpr int kTeamPieces = 8;    // joined by one team after another
-constexpr int kByItemThreads = 256, kTeam = 128, kByRunThreads = kTeam * kWarps;
+constexpr int kManyPieces = 64;   // of an item on average: from there on by item in larger blocks
+constexpr int kByItemThreads = 256, kManyThreads = 1024, kTeam = 128, kByRunThreads = kTeam * kWarps;
 
 // Adds a piece of a row (reference m, sum l, O y) to what a thread holds.
 __device__ __forceinline__ void add_piece(float4& acc, float& sum, float& mx, float m, float l,
@@ -951,10 +955,10 @@ __device__ __forceinline__ void empty_rows(const DecodeParams& p, int threads) {
   }
 }
 
-template <bool BF16, int DV, int ROWS>
-__global__ void __launch_bounds__(kByItemThreads) attn_kv_join_items_kernel(
+template <bool BF16, int DV, int ROWS, int THREADS>
+__global__ void __launch_bounds__(THREADS) attn_kv_join_items_kernel(
     const __grid_constant__ DecodeParams p, int runs) {
-  constexpr int kPart = ROWS * (DV + 2), kLanes = DV / 4, kGroups = kByItemThreads / kLanes;
+  constexpr int kPart = ROWS * (DV + 2), kLanes = DV / 4, kGroups = THREADS / kLanes;
   __shared__ float4 sm_o[kGroups][kLanes];
   __shared__ float sm_l[kGroups], sm_m[kGroups];
   const int per_seq = p.c.heads * p.row_blocks, tid = threadIdx.x;
@@ -962,7 +966,7 @@ __global__ void __launch_bounds__(kByItemThreads) attn_kv_join_items_kernel(
   const int at = blockIdx.x / rows, row = blockIdx.x - at * rows;
   const int b = at / per_seq, item = at - b * per_seq;
   const int kvh = (int)p.by_blocks.div(item), row_all = (item - kvh * p.row_blocks) * ROWS + row;
-  empty_rows<BF16>(p, kByItemThreads);
+  empty_rows<BF16>(p, THREADS);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row_all >= p.rows || seq_len(p, b) == 0) return;
   const int k0 = p.info[2 * (int64_t)at], k1 = p.info[2 * (int64_t)at + 1];
@@ -972,7 +976,7 @@ __global__ void __launch_bounds__(kByItemThreads) attn_kv_join_items_kernel(
   const int g = tid / kLanes, d4 = tid % kLanes;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.0f, mx = -INFINITY;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = g; i < np; i += kGroups) {
     const float* pc = p.partial + ((int64_t)(k0 + i) * 2 + (i == 0 ? 1 : 0)) * kPart;
     add_piece(acc, sum, mx, pc[ROWS * DV + row], pc[ROWS * (DV + 1) + row],
@@ -1117,8 +1121,10 @@ cudaError_t dec_launch(const DecodeParams& p, int blocks, cudaStream_t st) {
   const int runs = blocks * kWarps;
   if (items * kByItemPieces <= runs) {
     cfg.gridDim = dim3((unsigned)(items * std::min(8 * NT, p.rows)));
-    cfg.blockDim = dim3(kByItemThreads);
-    return cudaLaunchKernelEx(&cfg, attn_kv_join_items_kernel<BF16, DV, 8 * NT>, p, runs);
+    const bool many = items * kManyPieces <= runs;
+    cfg.blockDim = dim3(many ? kManyThreads : kByItemThreads);
+    return many ? cudaLaunchKernelEx(&cfg, attn_kv_join_items_kernel<BF16, DV, 8 * NT, kManyThreads>, p, runs)
+                : cudaLaunchKernelEx(&cfg, attn_kv_join_items_kernel<BF16, DV, 8 * NT, kByItemThreads>, p, runs);
   }
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kByRunThreads);
