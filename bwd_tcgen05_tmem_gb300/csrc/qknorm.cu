@@ -175,11 +175,19 @@ __device__ __forceinline__ float row_sum(uint64_t v) {
   return s;
 }
 
-// 1 / sqrt(sum / D + eps).  Finite for rows of zeros at eps = 0 too (they stay
-// zeros): lanes without a row hold such, and must add nothing to dw.
+// 1 / sqrt(sum / D + eps); 0 where that is 1 / 0, so that rows of zeros give zeros
+// at eps = 0 too and lanes without a row, which hold zeros, add nothing to dw.  A
+// NaN stays one: a row with a NaN is NaN in all of its elements.
 template <int D>
 __device__ __forceinline__ float rms_inverse(float sum, float eps) {
-  return rsqrtf(fmaxf(fmaf(sum, 1.0f / D, eps), 1.17549435e-38f));
+  const float v = fmaf(sum, 1.0f / D, eps);
+  float r;
+  if (v < 1.17549435e-38f) {  // (rare) below the normal range: 2^12 rsqrt(2^24 v)
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 16777216.0f));
+    return v == 0.0f ? 0.0f : r * 4096.0f;
+  }
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // A copy of 16 bytes, or of zeros.
@@ -454,7 +462,7 @@ __global__ void __launch_bounds__(kQkThreads, 4) attn_qk_bwd_kernel(
       float r = 1.0f, k = 0.0f;
       if (p.norm) {
         r = rms_inverse<D>(row_sum<S::kLpr>(ss), p.eps);
-        k = r * r * (row_sum<S::kLpr>(gx) * (1.0f / D));
+        k = (r * (1.0f / D)) * (r * row_sum<S::kLpr>(gx));  // (r^2 itself may pass FP32's range)
       }
       if (pos == kNoAngle) r = __int_as_float(0x7fffffff);
       const uint64_t r2 = f2_both(r), k2 = f2_both(-k);

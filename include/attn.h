@@ -349,12 +349,13 @@ attn_status_t attn_cp_relayout(int to_heads, int cp, int64_t seqlen, int heads, 
 /*
  * Norm of each query and key head and rotation by its position, in one pass.
  * For every row x (token, head; head_dim elements), in FP32:
- *     y = x / sqrt(mean(x^2) + eps) * w        (norm = 0: y = x, w = NULL; a row of
- *                                               zeros stays zeros, at eps = 0 too)
+ *     y = x / sqrt(mean(x^2) + eps) * w        (norm = 0: y = x, w = NULL)
  *     z = y turned by the angles of the token's position on its first
  *         rotary_dim elements: pairs (i, i + rotary_dim/2), or (2i, 2i+1) with
  *         interleaved = 1:  (a, b) -> (a cos - b sin, b cos + a sin)
- * rounded once to dtype.  cos/sin: FP32 [max_pos][rotary_dim/2], contiguous,
+ * rounded once to dtype.  At eps = 0 a row whose mean square is 0 in FP32 (below
+ * 2^-150) gives zeros, in the gradient too.  A NaN in a row makes all of it NaN.
+ * cos/sin: FP32 [max_pos][rotary_dim/2], contiguous,
  * 16-byte aligned (make them in FP64: angles of far positions need it).
  * positions: int32 [batch][seqlen], contiguous, or NULL for 0, 1, .. in each
  * sequence (packed THD tensors: batch 1, seqlen = total).  A negative position

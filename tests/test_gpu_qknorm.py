@@ -334,3 +334,76 @@ def test_tables_without_positions():
     assert torch.isnan(z[0]).all() and torch.isnan(z[1]).all()
     with pytest.raises(attn.AttnError, match="out of range"):
         attn.query_status(status)
+
+
+def special_rows(m, value, cos, sin, **kw):
+    """`value` in one element of one query and one key row: outputs, gradients and
+    their float64 forms (differentiated by autograd)."""
+    at = {"q": (0, 3, 0, 7), "k": (1, 5, m["k"].shape[2] - 1, m["k"].shape[3] - 1)}
+    for n, i in at.items():
+        m[n][i] = value
+    z = attn.qk_norm_rope(m["q"], m["k"], cos, sin, positions=m["pos"], wq=m["wq"], wk=m["wk"], **kw)
+    g = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], positions=m["pos"], wq=m["wq"],
+                              wk=m["wk"], **kw)
+    c, s = cos[m["pos"].long()].double(), sin[m["pos"].long()].double()
+    for n, got, w, dz, dx, dw in (("q", z[0], m["wq"], m["dqo"], g[0], g[2]), ("k", z[1], m["wk"], m["dko"], g[1], g[3])):
+        x64, w64 = m[n].double().requires_grad_(), w.double().requires_grad_()
+        want = kvref.norm_rope(x64, w64, c, s, True, kw.get("eps", 1e-6), False)
+        (want * dz.double()).sum().backward()
+        yield at[n], (got, want.detach()), (dx, x64.grad), (dw, w64.grad)
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("heads,d", [((5, 2), 128), ((1, 1), 64), ((3, 1), 192), ((4, 4), 512)])
+def test_nan_in_a_row(heads, d, dt):
+    """A NaN makes its row NaN, forward and gradient, and all of dw; no other row
+    changes."""
+    cos, sin = attn.rope_tables(5000, 64)
+    m = make(2, 11, *heads, d, dt, seed=24, spread=False)
+    kw = dict(positions=m["pos"], wq=m["wq"], wk=m["wk"])
+    clean = attn.qk_norm_rope(m["q"], m["k"], cos, sin, **kw)
+    clean_g = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], **kw)
+    for i, (at, z, dx, dw) in enumerate(special_rows(m, float("nan"), cos, sin)):
+        others = torch.ones(z[0].shape[:3], dtype=torch.bool)
+        others[at[:3]] = False
+        for (got, want), before in ((z, clean[i]), (dx, clean_g[i])):
+            assert torch.isnan(want[~others]).all() and torch.isnan(got[~others]).all()
+            assert torch.equal(got[others], before[others])
+        assert torch.isnan(dw[1]).all() and torch.isnan(dw[0]).all()
+
+
+@pytest.mark.parametrize("heads,d", [((5, 2), 128), ((1, 1), 64), ((3, 1), 192)])
+def test_tiny_rows_without_eps(heads, d):
+    """Rows of about 2^-64 at eps = 0, whose mean square 2^-128 is below FP32's
+    normal range: a square or sum there is off by 2^-150 at most, 2^-22 of a mean
+    square, so the bounds are twice those of ordinary rows.  Rows of zeros: zeros."""
+    cos, sin = attn.rope_tables(5000, 64)
+    m = make(2, 11, *heads, d, BF, seed=25, spread=False)
+    for t in (m["q"], m["k"]):
+        t.mul_(2.0 ** -64)
+    m["q"][0, 0, 0] = 0.0
+    zero = torch.zeros(2, 11, heads[0], dtype=torch.bool)
+    zero[0, 0, 0] = True
+    kw = dict(positions=m["pos"], wq=m["wq"], wk=m["wk"], eps=0.0)
+    z = attn.qk_norm_rope(m["q"], m["k"], cos, sin, **kw)
+    g = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], **kw)
+    assert (z[0][zero] == 0).all() and (g[0][zero] == 0).all()
+    m["q"][0, 0, 0] = 1.0  # (for the float64 form)
+    dz = m["dqo"].double()
+    dz[0, 0, 0] = 0.0
+    c, s = cos[m["pos"].long()].double(), sin[m["pos"].long()].double()
+    u = UNIT[BF]
+    for x, w, dz, got, dx, dw, skip in ((m["q"], m["wq"], dz, z[0], g[0], g[2], zero),
+                                        (m["k"], m["wk"], m["dko"].double(), z[1], g[1], g[3], None)):
+        live = slice(None) if skip is None else ~skip
+        x64, w64 = x.double().requires_grad_(), w.double().requires_grad_()
+        want = kvref.norm_rope(x64, w64, c, s, True, 0.0, False)
+        length = pair_length(kvref.norm_rope(x64, w64, None, None, True, 0.0, False).detach(), 64, False)
+        close(got[live], want.detach()[live], (u * want.detach().abs() + 2.0 ** -17 * length + 2.0 ** -25)[live])
+        (want * dz).sum().backward()
+        r = 1 / x.double().pow(2).mean(-1, keepdim=True).sqrt()
+        gl = pair_length(dz, 64, False) * w.double().abs()
+        size = r * (gl + x.double().abs() * r * r * (gl * x.double().abs()).mean(-1, keepdim=True))
+        close(dx[live], x64.grad[live], (u * x64.grad.abs() + 2.0 ** -16 * size)[live])
+        total = (gl / w.double().abs() * (x.double() * r).abs()).sum((0, 1, 2))
+        close(dw, w64.grad, 2.0 ** -24 * (22 * x.shape[2] + 128) * total)
