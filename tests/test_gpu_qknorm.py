@@ -407,3 +407,53 @@ def test_tiny_rows_without_eps(heads, d):
         close(dx[live], x64.grad[live], (u * x64.grad.abs() + 2.0 ** -16 * size)[live])
         total = (gl / w.double().abs() * (x.double() * r).abs()).sum((0, 1, 2))
         close(dw, w64.grad, 2.0 ** -24 * (22 * x.shape[2] + 128) * total)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("heads,d", [((5, 2), 128), ((1, 1), 64), ((3, 1), 192), ((4, 4), 512)])
+def test_infinity_in_a_row(heads, d, dt, value):
+    """With the norm an infinity becomes NaN, as what it is turned with does, and
+    leaves zeros beside it; its row of dx is NaN, dw where the float64 form is."""
+    cos, sin = attn.rope_tables(5000, 64)
+    m = make(2, 11, *heads, d, dt, seed=24, spread=False)
+    kw = dict(positions=m["pos"], wq=m["wq"], wk=m["wk"])
+    clean = attn.qk_norm_rope(m["q"], m["k"], cos, sin, **kw)
+    clean_g = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], **kw)
+    # |dy x r| of the untouched rows bounds what the sums of dw add up
+    total = [(pair_length(dz.double(), 64, False) * x.double().abs()
+              / x.double().pow(2).mean(-1, keepdim=True).sqrt()).sum((0, 1, 2))
+             for x, dz in ((m["q"], m["dqo"]), (m["k"], m["dko"]))]
+    for i, (at, z, dx, dw) in enumerate(special_rows(m, value, cos, sin)):
+        row = at[:3]
+        others = torch.ones(z[0].shape[:3], dtype=torch.bool)
+        others[row] = False
+        for (got, want), before in ((z, clean[i]), (dx, clean_g[i])):
+            assert torch.equal(got[others], before[others])
+            assert torch.equal(torch.isnan(got[row]), torch.isnan(want[row]))
+            assert (got[row].nan_to_num() == 0).all()
+        bad = torch.isnan(dw[1])
+        assert torch.equal(torch.isnan(dw[0]), bad) and bad.any()
+        close(dw[0][~bad], dw[1][~bad], 2.0 ** -24 * (22 * heads[i] + 64) * total[i][~bad])
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d,rot", [(128, 64), (192, 16), (64, 0), (256, 256)])
+def test_elements_that_do_not_turn_do_not_meet(d, rot, inter):
+    """Without the norm an infinity or a NaN reaches the element it is turned with
+    and no other, forward and gradient."""
+    cos, sin = attn.rope_tables(5000, rot) if rot else (None, None)
+    m = make(1, 7, 3, 2, d, BF, seed=27, spread=False)
+    kw = dict(positions=m["pos"], norm=False, interleaved=inter)
+    c, s = (cos[m["pos"].long()].double(), sin[m["pos"].long()].double()) if rot else (None, None)
+    for j in {0, 1, rot // 2, max(rot - 1, 0), min(rot, d - 1), d // 2, d - 9, d - 1}:
+        for value in (float("inf"), float("nan")):
+            x, dz = m["q"].clone(), m["dqo"].clone()
+            x[0, 3, 1, j] = dz[0, 4, 2, j] = value
+            z, _ = attn.qk_norm_rope(x, None, cos, sin, **kw)
+            want = kvref.norm_rope(x.double(), None, c, s, False, 0.0, inter)
+            dx, _, _, _ = attn.qk_norm_rope_bwd(m["q"], None, cos, sin, dz, None, **kw)
+            grad = kvref.turn(dz.double(), c, s, inter, -1) if rot else dz.double()
+            for got, ref in ((z, want), (dx, grad)):
+                assert torch.equal(torch.isnan(got), torch.isnan(ref))
+                assert torch.equal(torch.isinf(got), torch.isinf(ref))
