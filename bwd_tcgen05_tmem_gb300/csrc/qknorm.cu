@@ -309,8 +309,10 @@ struct QkWarp {
           if (u >= n) break;
           const bool is = here(run, u, next_pos);  // (else zeros; the address is not used)
           uint4(*v)[kQkThreads] = ring.v[s][u];
-          copy16(&v[0][threadIdx.x], is ? px : x, is);
-          copy16(&v[1][threadIdx.x], is ? px + vb : x, is);
+          // (the gradient without the norm does not depend on x, whatever that holds)
+          const bool is_x = is && (NV == 2 || p.norm);
+          copy16(&v[0][threadIdx.x], is_x ? px : x, is_x);
+          copy16(&v[1][threadIdx.x], is_x ? px + vb : x, is_x);
           px += lx.u;
           if (NV == 4) {
             copy16(&v[NV - 2][threadIdx.x], is ? pz : x, is);

@@ -457,3 +457,14 @@ def test_elements_that_do_not_turn_do_not_meet(d, rot, inter):
             for got, ref in ((z, want), (dx, grad)):
                 assert torch.equal(torch.isnan(got), torch.isnan(ref))
                 assert torch.equal(torch.isinf(got), torch.isinf(ref))
+
+
+@pytest.mark.parametrize("heads", [(5, 2), (1, 1)])
+def test_gradient_without_norm_does_not_depend_on_x(heads):
+    m = make(2, 11, *heads, 128, BF, seed=28, spread=False)
+    cos, sin = attn.rope_tables(5000, 64)
+    kw = dict(positions=m["pos"], norm=False)
+    want = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], **kw)
+    m["q"][0, 2, 0, 3], m["k"][1, 4, -1, 70], m["q"][1, 1] = float("inf"), float("nan"), 3e38
+    got = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
