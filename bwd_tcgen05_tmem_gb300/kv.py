@@ -60,8 +60,8 @@ def plan(context, fresh, block_table, *, page_size, num_pages, rows, free_pages=
 
     context, fresh: int32 [batch], tokens that each request holds and gets;
     block_table: int32 [batch, cols], updated in place; rows: room for new
-    tokens; free_pages [n] and free_head [1]: the pages to take from (None: the
-    table is complete and only read).  ``out``: a Plan to write into."""
+    tokens; free_pages [n] and free_head [1]: the pages to take from (empty: none is
+    left; None: the table is complete and only read).  ``out``: a Plan to write into."""
     lib = fast()
     b = context.shape[0]
     _ints("context", context, b)
@@ -87,9 +87,11 @@ def plan(context, fresh, block_table, *, page_size, num_pages, rows, free_pages=
                 _ints(name, t, n)
         if take and out.free_head is None:
             raise ValueError("free_pages needs out.free_head")
+    # an empty tensor has no address, but NULL would mean a call without a free list
+    pages = (free_pages.data_ptr() or free_head.data_ptr()) if take else None
     launch(dev, stream, lib.attn_kv_plan,
            _PLAN_PACK(b, cols, page_size, num_pages, rows, n_free, row), context.data_ptr(),
-           fresh.data_ptr(), block_table.data_ptr(), free_pages.data_ptr() if take else None,
+           fresh.data_ptr(), block_table.data_ptr(), pages,
            free_head.data_ptr() if take else None, out.cu_seqlens.data_ptr(),
            out.seq_lens.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
            out.free_head.data_ptr() if take else None,

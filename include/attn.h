@@ -410,9 +410,9 @@ attn_status_t attn_qk_norm_rope_bwd(const attn_qk_params_t* p, const void* q, co
  * With free_pages (int32 [n_free]) the pages that the new tokens need beyond
  * those held, ceil((context + fresh) / page_size) - ceil(context / page_size)
  * a request, are taken in order from free_pages[free_head[0] ..], written into
- * block_table, and free_head_out[0] = free_head[0] + pages taken.  With
- * free_pages NULL the table is only read (a map of tokens that have pages
- * already) and free_head, free_head_out are ignored.
+ * block_table, and free_head_out[0] = free_head[0] + pages taken; an empty list is
+ * any address with n_free = 0.  With free_pages NULL the table is only read (a map
+ * of tokens that have pages already) and free_head, free_head_out are ignored.
  * Out of range (status word): lengths that are negative or longer than cols *
  * page_size (the request counts as empty), more tokens than rows (the rest is
  * left out), pages outside [0, num_pages) or past n_free (slot -1, table entry -1).

@@ -563,3 +563,25 @@ def test_prompt_chunk_over_a_cached_prefix():
     assert ((o.double() - ro).abs() <= u * ro.abs() + (2 * u + 2.0 ** -12) * mag + 2 * u * big.transpose(1, 2)[..., None] * mag).all()
     o2, lse2 = kv.kv4_decode(q, x.cache, x.t, x.l)
     within(o2, lse2, (ro, rl, mag, big), u)
+
+
+def test_plan_with_an_empty_free_list():
+    """No page is left: tokens past the held pages get none, whatever the table
+    holds there; without need of a page the head passes through."""
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    for free in (none, i32([4, 5])[2:]):
+        t = i32([[3, 5], [2, 1]])  # (entries 5 and 1 are valid pages that are not held)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        p = kv.plan(i32([10, 16]), i32([10, 1]), t, page_size=16, num_pages=8, rows=12, free_pages=free,
+                    free_head=i32([4]), status=status)
+        assert p.positions.tolist() == list(range(10, 20)) + [16, -1]
+        assert p.slots.tolist() == list(range(58, 64)) + [-1] * 6
+        assert t.tolist() == [[3, -1], [2, -1]] and p.free_head.tolist() == [6]
+        with pytest.raises(attn.AttnError, match="out of range"):
+            attn.query_status(status)
+        t = i32([[3, 5]])
+        status.zero_()
+        p = kv.plan(i32([10]), i32([6]), t, page_size=16, num_pages=8, rows=6, free_pages=free, free_head=i32([0]),
+                    status=status)
+        assert p.slots.tolist() == list(range(58, 64)) and t.tolist() == [[3, 5]] and p.free_head.tolist() == [0]
+        attn.query_status(status)
