@@ -354,13 +354,14 @@ __device__ __forceinline__ void tile_softmax(const DecodeParams& p, Piece<DQK, D
   }
   if (any) {
     const float kf_old = z.lim - 1.0f;
-    float f = 1.0f;
+    float f0 = 1.0f, f1 = 1.0f;  // 2^(e_old - e), whose exponent may be below a number's
     {
       // (positive numbers: their bits are ordered)
       const uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(top, 0.0f)));
       const int e = min(max((int)(u >> 23) - 126, kExpMin), kExpMax), e_old = 15 - (int)z.lim;
       if (e > e_old) {
-        f = pow2(max(e_old - e, -126));
+        f0 = pow2(max(e_old - e, -126));
+        f1 = pow2(e_old - e - max(e_old - e, -126));
         z.lim = (float)(15 - e);
         z.vlim = pow2(e);
       }
@@ -375,9 +376,9 @@ __device__ __forceinline__ void tile_softmax(const DecodeParams& p, Piece<DQK, D
         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
         y = fmaxf(y, m);
-        const float a = ex2(m - y) * f;
+        const float b = ex2(m - y), a = b * f0 * f1;
         z.ref[t][e] = z.lim - 1.0f - y;
-        z.l[t][e] *= a;
+        z.l[t][e] = z.l[t][e] * b * f0 * f1;  // (the sum is up to 2^95: a alone may be 0)
 #pragma unroll
         for (int g = 0; g < S::GV; ++g)
 #pragma unroll
@@ -867,8 +868,11 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
       copies_end();
     }
 
-    // ---- the result, or a partial one: O and the sum relative to the reference
+    // ---- the result, or a partial one: O and the sum relative to the reference m.
+    // (2^-kf is taken off a partial one: the join's weights are differences of
+    // references, and two warps' units may be 2^180 apart.)
     const bool done = v0 == 0 && v1 == sr.tiles;
+    const float unit = pow2(1 - (int)z.lim);
     float* part = p.partial + (run * 2 + (v0 == 0 ? 1 : 0)) * S::kPart;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -895,10 +899,10 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
         } else {
 #pragma unroll
           for (int g = 0; g < S::GV; ++g)
-            *reinterpret_cast<float4*>(part + row * DV + 32 * g + 4 * r) = dims(g, 1.0f);
+            *reinterpret_cast<float4*>(part + row * DV + 32 * g + 4 * r) = dims(g, unit);
           if (r == 0) {
-            part[S::kRows * DV + row] = -z.ref[t][e];
-            part[S::kRows * (DV + 1) + row] = sum;
+            part[S::kRows * DV + row] = z.lim - 1.0f - z.ref[t][e];
+            part[S::kRows * (DV + 1) + row] = sum * unit;
           }
         }
       }

@@ -585,3 +585,20 @@ def test_plan_with_an_empty_free_list():
                     status=status)
         assert p.slots.tolist() == list(range(58, 64)) and t.tolist() == [[3, 5]] and p.free_head.tolist() == [0]
         attn.query_status(status)
+
+
+@pytest.mark.parametrize("power", [40, 50, 70, 95])
+@pytest.mark.parametrize("n", [200, 300000])
+def test_decode_large_values_after_empty_ones(n, power):
+    """Tiles of 64 tokens whose V is zero, before and between tiles of values of
+    about 2^power: the sum and the LSE keep all of their tokens.  n = 300000 gives
+    a warp two tiles; with n = 200 the join meets the pieces."""
+    x = Held([n], 1, 64, 64, 64, BF, seed=18)
+    at = torch.arange(n)
+    pages = torch.tensor(x.table[0])[at // 64]
+    even = at // 64 % 2 == 0
+    x.cache.v_scales[pages[even], :, at[even] % 64] = 0.0
+    odd = (pages[~even].cuda(), slice(None), at[~even].cuda() % 64)
+    x.cache.v_scales[odd] = x.cache.v_scales[odd] * 2.0 ** power
+    x.check(x.q(1, 4))
+    x.check(x.q(3, 4), o_dtype=torch.float32)
