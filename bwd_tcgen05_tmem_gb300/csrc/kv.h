@@ -64,6 +64,7 @@ struct PlanParams {
   int batch, cols, page_shift, num_pages, rows, n_free;
   int* status;
 };
+constexpr int kPlanMaxBatch = 8192;  // 12 bytes of shared memory each
 cudaError_t launch_kv_plan(const PlanParams& p, int num_sms, cudaStream_t st);
 
 struct Kv4 {  // the cache

@@ -326,7 +326,8 @@ attn_status_t attn_kv_plan(const attn_kv_plan_params_t* p, const int32_t* contex
   if (!p) return api_fail(ATTN_ERR_INVALID_ARG, "params is NULL");
   if (p->batch < 0 || p->cols < 0 || p->rows < 0 || p->num_pages < 0 || p->n_free < 0)
     return api_fail(ATTN_ERR_INVALID_ARG, "a size is negative");
-  if (p->batch > 8192) return api_fail(ATTN_ERR_UNSUPPORTED, "batch %d > 8192", p->batch);
+  if (p->batch > attn::kPlanMaxBatch)
+    return api_fail(ATTN_ERR_UNSUPPORTED, "batch %d > %d", p->batch, attn::kPlanMaxBatch);
   int shift = 0;
   while ((1 << shift) < p->page_size && shift < 8) ++shift;
   if (p->page_size < 16 || (1 << shift) != p->page_size)

@@ -157,8 +157,9 @@ cudaError_t launch_kv_plan(const PlanParams& p, int num_sms, cudaStream_t st) {
   const int64_t most = (int64_t)num_sms * std::min<int64_t>(8, std::max<int64_t>(200000 / (int64_t)(smem + 1024), 1));
   if (blocks > most) blocks = most;
   if (smem > 40000) {  // beyond what every kernel may take
-    const cudaError_t e = cudaFuncSetAttribute(
-        attn_kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the largest call's, not this one's: calls of other threads share the limit)
+    const cudaError_t e = cudaFuncSetAttribute(attn_kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (kPlanMaxBatch + 1) * 12);
     if (e != cudaSuccess) return e;
   }
   attn_kv_plan_kernel<<<(unsigned)blocks, kPlanThreads, smem, st>>>(p);

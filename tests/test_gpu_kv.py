@@ -602,3 +602,39 @@ def test_decode_large_values_after_empty_ones(n, power):
     x.cache.v_scales[odd] = x.cache.v_scales[odd] * 2.0 ** power
     x.check(x.q(1, 4))
     x.check(x.q(3, 4), o_dtype=torch.float32)
+
+
+def test_plan_from_several_threads():
+    """Batches that need different amounts of shared memory, planned at once.
+    (Packed calls, so that the threads meet within the library.)"""
+    import threading
+    lib, failed = attn.fast(), []
+    batches = [8192, 3500] * 4
+    jobs = []
+    for b in batches:
+        t = [i32([0] * b), i32([1] * b), torch.zeros(b, 1, dtype=torch.int32, device="cuda")]
+        out = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (b + 1, b, 1, 1)]
+        jobs.append((b, t, out, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    start = threading.Barrier(len(jobs))
+
+    def work(b, t, out, stream):
+        p = attn._PLAN_PACK(b, 1, 16, 1, 1, 0, 1)
+        args = (p, *(x.data_ptr() for x in t), None, None, *(x.data_ptr() for x in out), None, None,
+                stream.cuda_stream)
+        start.wait()
+        for _ in range(300):
+            rc = lib.attn_kv_plan(*args)
+            if rc:
+                failed.append((b, rc))
+                return
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for b, _, out, _ in jobs:
+        assert out[0].tolist() == list(range(b + 1)) and out[1].tolist() == [1] * b
