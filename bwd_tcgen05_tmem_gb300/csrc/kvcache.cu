@@ -101,8 +101,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_kv_plan_kernel(
     if ((unsigned)page >= (unsigned)p.num_pages) page = -1;
     return page;
   };
-  const int gtid = blockIdx.x * kPlanThreads + tid, gn = gridDim.x * kPlanThreads;
-  for (int b = gtid; b < p.batch; b += gn) {
+  // (unsigned: the last step of the loops below may pass 2^31 - 1)
+  const uint32_t gtid = blockIdx.x * kPlanThreads + tid, gn = gridDim.x * kPlanThreads;
+  for (uint32_t b = gtid; b < (uint32_t)p.batch; b += gn) {
     const int c = held_by[b];
     p.cu[b] = cu[b];
     const int f = p.fresh[b];
@@ -119,10 +120,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_kv_plan_kernel(
     return lo;
   };
   const int new_pages = pg[p.batch];
-  for (int i = gtid; i < new_pages; i += gn) {
-    const int b = request_of(pg, i), held = (held_by[b] + P - 1) >> p.page_shift;
-    const int page = page_of(i);
-    p.table[(int64_t)b * p.table_stride + held + i - pg[b]] = page;
+  for (uint32_t i = gtid; i < (uint32_t)new_pages; i += gn) {
+    const int b = request_of(pg, (int)i), held = (held_by[b] + P - 1) >> p.page_shift;
+    const int page = page_of((int)i);
+    p.table[(int64_t)b * p.table_stride + held + ((int)i - pg[b])] = page;
     if (page < 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
   }
   if (gtid == 0) {
@@ -131,12 +132,12 @@ __global__ void __launch_bounds__(kPlanThreads) attn_kv_plan_kernel(
   }
   const int total = min(cu[p.batch], p.rows);
 #pragma unroll 2
-  for (int t = gtid; t < p.rows; t += gn) {
+  for (uint32_t t = gtid; t < (uint32_t)p.rows; t += gn) {
     int pos = -1, slot = -1;
-    if (t < total) {
-      const int lo = request_of(cu, t);
+    if (t < (uint32_t)total) {
+      const int lo = request_of(cu, (int)t);
       const int c = held_by[lo], held = (c + P - 1) >> p.page_shift;
-      pos = c + t - cu[lo];
+      pos = c + ((int)t - cu[lo]);
       const int blk = pos >> p.page_shift;  // < cols, as the lengths are
       const int page = p.free_pages && blk >= held ? page_of(pg[lo] + blk - held)
                                                    : p.table[(int64_t)lo * p.table_stride + blk];

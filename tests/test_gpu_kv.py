@@ -638,3 +638,19 @@ def test_plan_from_several_threads():
     assert not failed, failed
     for b, _, out, _ in jobs:
         assert out[0].tolist() == list(range(b + 1)) and out[1].tolist() == [1] * b
+
+
+def test_plan_with_as_many_rows_as_an_int_counts():
+    """rows = 2^31 - 1: the loops' last steps pass that, and nothing lands before
+    the arrays."""
+    rows, guard = 2 ** 31 - 1, 1 << 20
+    if torch.cuda.mem_get_info()[0] < 2 * (rows + guard) * 4 + (8 << 30):
+        pytest.skip("needs 17 GB")
+    whole = torch.full((2, rows + guard), 77, dtype=torch.int32, device="cuda")
+    out = kv.Plan(i32([0, 0, 0]), i32([0, 0]), whole[0, guard:], whole[1, guard:], None)
+    kv.plan(i32([5, 0]), i32([2, 3]), i32([[1], [4]]), page_size=16, num_pages=8, rows=rows, out=out)
+    assert out.positions[:5].tolist() == [5, 6, 0, 1, 2] and out.slots[:5].tolist() == [21, 22, 64, 65, 66]
+    for t in out[2:4]:
+        lo, hi = torch.aminmax(t[5:])
+        assert lo == -1 and hi == -1
+    assert (whole[:, :guard] == 77).all()
