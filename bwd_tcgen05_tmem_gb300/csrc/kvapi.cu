@@ -129,7 +129,7 @@ attn_status_t setup_qk(const attn_qk_params_t* p, const void* q, const void* k, 
   attn_status_t s;
   if (!p->norm && (w_q || w_k))
     return api_fail(ATTN_ERR_INVALID_ARG, "norm weights without norm");
-  if (p->rotary_dim > 0) {
+  if (p->rotary_dim > 0 && p->max_pos > 0) {  // (tables of no rows are not read)
     if (!cos || !sin) return api_fail(ATTN_ERR_INVALID_ARG, "cos or sin is NULL");
     if ((uintptr_t)cos % 16 || (uintptr_t)sin % 16)
       return api_fail(ATTN_ERR_ALIGNMENT, "cos and sin must be 16-byte aligned");

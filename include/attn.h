@@ -360,7 +360,8 @@ attn_status_t attn_cp_relayout(int to_heads, int cp, int64_t seqlen, int heads, 
  * positions: int32 [batch][seqlen], contiguous, or NULL for 0, 1, .. in each
  * sequence (packed THD tensors: batch 1, seqlen = total).  A negative position
  * marks padding: its rows are neither read nor written.  A position >= max_pos
- * gives NaN rows and sets the status word.
+ * gives NaN rows and sets the status word (with max_pos = 0 all do, and cos and sin
+ * may be NULL).
  * w_q / w_k: [head_dim] of w_dtype (FP32 or dtype), or NULL for ones.
  * q, k (and their strides) as in attn_fwd; heads_k may be 0 (queries alone),
  * then the k arguments are ignored.  Views of one projection are fine.

@@ -468,3 +468,41 @@ def test_gradient_without_norm_does_not_depend_on_x(heads):
     m["q"][0, 2, 0, 3], m["k"][1, 4, -1, 70], m["q"][1, 1] = float("inf"), float("nan"), 3e38
     got = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], **kw)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_empty_tables():
+    """Tables of no rows: every position is outside, and nothing is read."""
+    m = make(2, 9, 4, 2, 128, BF, seed=26)
+    cos = sin = torch.empty(0, 64, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m["pos"][0, 3] = -1
+    kw = dict(positions=m["pos"], wq=m["wq"], wk=m["wk"])
+    out = [torch.full(t.shape, 5.0, dtype=BF, device="cuda") for t in (m["q"], m["k"])]
+    z = attn.qk_norm_rope(m["q"], m["k"], cos, sin, status=status, q_out=out[0], k_out=out[1], **kw)
+    g = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], **kw)
+    live = m["pos"] >= 0
+    for t in (*z, g[0], g[1]):
+        assert torch.isnan(t[live]).all()
+    for t in z:
+        assert (t[~live] == 5.0).all()
+    assert torch.isnan(g[2]).all() and torch.isnan(g[3]).all()
+    with pytest.raises(attn.AttnError, match="out of range"):
+        attn.query_status(status)
+
+
+def test_tables_of_no_rows_are_not_read():
+    """The C entry point with real addresses and max_pos = 0."""
+    m = make(1, 9, 4, 2, 128, BF, seed=29)
+    cos, sin = attn.rope_tables(16, 128)
+    out = [torch.zeros_like(m[n], memory_format=torch.contiguous_format) for n in ("q", "k")]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    p = attn.QkParams(0, 2, 1, 9, 4, 2, 128, 128, 0, 1, 0, 1e-6, m["q"].stride()[:3], m["k"].stride()[:3],
+                      out[0].stride()[:3], out[1].stride()[:3])
+    rc = attn.load().attn_qk_norm_rope(p, m["q"].data_ptr(), m["k"].data_ptr(), None, None, cos.data_ptr(),
+                                       sin.data_ptr(), None, out[0].data_ptr(), out[1].data_ptr(),
+                                       status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    for t in out:
+        assert torch.isnan(t).all()
+    with pytest.raises(attn.AttnError, match="out of range"):
+        attn.query_status(status)
