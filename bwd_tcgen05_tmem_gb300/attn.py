@@ -539,6 +539,14 @@ def on_device(t, *others):
     return dev
 
 
+def check_buffers(status, workspace=None):
+    """What the kernels write as words and bytes from an address on (None: not given)."""
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status must be an int32 tensor of one element or more")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def launch(dev, stream, fn, *args):
     """fn(*args, stream) with device ``dev`` current; raises on an error status."""
     if stream is not None:
@@ -588,7 +596,7 @@ def _qk_strides(name, t, shape, dtype):
 _NO_STRIDES = (0, 0, 0)
 
 
-def _qk_pack(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, qo, ko, dqo, dko, status):
+def _qk_pack(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, qo, ko, dqo, dko):
     shape, dt = q.shape, q.dtype
     if len(shape) == 4:
         b, s, hq, d = shape
@@ -626,8 +634,6 @@ def _qk_pack(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, qo, ko, 
         for w in (wq, wk):
             if w is not None and (w.shape != (d,) or w.dtype != wdt or not w.is_contiguous()):
                 raise ValueError("norm weights must be contiguous [head_dim] and of one dtype")
-    if status is not None and status.dtype != torch.int32:
-        raise ValueError("status must be an int32 tensor")
     sdq = _qk_strides("dq_out", dqo, shape, dt) if dqo is not None else _NO_STRIDES
     sdk = _qk_strides("dk_out", dko, k_shape, dt) if dko is not None else _NO_STRIDES
     if dt not in _CODES or wdt not in _CODES:
@@ -647,6 +653,7 @@ def qk_norm_rope(q, k, cos, sin, *, positions=None, wq=None, wk=None, norm=True,
     or [T], negative for padding rows (left as they are in ``q_out`` and
     ``k_out``), or None for 0, 1, ...; wq, wk: [d] or None.  ``q_out=q`` works
     in place.  ``status``: int32 device word (see include/attn.h), or None."""
+    check_buffers(status)
     lib = fast()
     dev = on_device(q, k, cos, sin, positions, wq, wk, q_out, k_out, status)
     if q_out is None:
@@ -654,7 +661,7 @@ def qk_norm_rope(q, k, cos, sin, *, positions=None, wq=None, wk=None, norm=True,
     if k_out is None and k is not None:
         k_out = new(k.shape, q.dtype, dev, stream)
     p = _qk_pack(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, q_out, k_out, None,
-                 None, status)
+                 None)
     launch(dev, stream, lib.attn_qk_norm_rope, p, q.data_ptr(),
            None if k is None else k.data_ptr(), None if wq is None else wq.data_ptr(),
            None if wk is None else wk.data_ptr(), None if cos is None else cos.data_ptr(),
@@ -671,6 +678,7 @@ def qk_norm_rope_bwd(q, k, cos, sin, dq_out, dk_out, *, positions=None, wq=None,
     """Gradient of qk_norm_rope: (dq, dk, dwq, dwk) from its inputs q, k and the
     gradients of its outputs.  dwq and dwk are float32 [d] (None without
     weights); rows of padding tokens are left as they are in dq and dk."""
+    check_buffers(status, workspace)
     lib = fast()
     dev = on_device(q, k, cos, sin, dq_out, dk_out, positions, wq, wk, dq, dk, dwq, dwk,
                     workspace, status)
@@ -689,7 +697,7 @@ def qk_norm_rope_bwd(q, k, cos, sin, dq_out, dk_out, *, positions=None, wq=None,
         if w is not None and (w.dtype != torch.float32 or w.shape != (d,) or not w.is_contiguous()):
             raise ValueError("weight gradients must be contiguous float32 [head_dim]")
     p = _qk_pack(q, k, cos, sin, positions, wq, wk, norm, eps, interleaved, dq, dk, dq_out,
-                 dk_out, status)
+                 dk_out)
     if workspace is None:
         workspace = new((_sized(dev, lib.attn_qk_norm_rope_bwd_workspace_size, p),), torch.uint8,
                         dev, stream)

@@ -23,8 +23,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .attn import (_CODES, _DECODE_PACK, _PLAN_PACK, Kv4CacheDesc, _sized, fast, launch, new,
-                   on_device)
+from .attn import (_CODES, _DECODE_PACK, _PLAN_PACK, Kv4CacheDesc, _sized, check_buffers, fast,
+                   launch, new, on_device)
 
 _STRIDES_PACK = struct.Struct("@2q").pack
 _I32 = torch.int32
@@ -62,6 +62,7 @@ def plan(context, fresh, block_table, *, page_size, num_pages, rows, free_pages=
     block_table: int32 [batch, cols], updated in place; rows: room for new
     tokens; free_pages [n] and free_head [1]: the pages to take from (empty: none is
     left; None: the table is complete and only read).  ``out``: a Plan to write into."""
+    check_buffers(status)
     lib = fast()
     b = context.shape[0]
     _ints("context", context, b)
@@ -137,6 +138,7 @@ def _rows(cache, name, t, tokens, d):
 
 
 def _move(fn, cache, k, v, slots, t, status, stream):
+    check_buffers(status)
     dev = on_device(cache.k_codes, k, v, slots, status)
     _ints("slots", slots, t)
     dt = k.dtype
@@ -173,6 +175,7 @@ def kv4_decode(q, cache, block_table, seq_lens, *, scale=None, window_left=-1, s
     (attn_kv_decode).  q [B, Sq, Hq, d_qk]; block_table int32 [B, cols];
     seq_lens int32 [B], the new tokens among them.  Returns (o [B, Sq, Hq, d_v],
     lse float32 [B, Hq, Sq])."""
+    check_buffers(status, workspace)
     lib = fast()
     dev = on_device(cache.k_codes, q, block_table, seq_lens, out, lse, workspace, status)
     b, sq, hq, d = q.shape

@@ -318,3 +318,23 @@ def test_packed_parameters_are_the_structs():
             a, b = getattr(got, name), getattr(want, name)
             assert list(a) == list(b) if hasattr(t, "_length_") else a == b, name
         assert len(pack(*vals)) == ctypes.sizeof(struct)
+
+
+@pytest.mark.parametrize("call", ["plan", "write", "read", "decode", "qk", "qk_bwd"])
+def test_python_refuses_status_words_and_workspaces_of_other_shapes(call):
+    """The kernels write four bytes at the status' address and whole bytes from the
+    workspace's on (looked at first, so no GPU is needed)."""
+    from bwd_tcgen05_tmem_gb300 import kv
+    ints, x = torch.zeros(4, dtype=torch.int32), torch.zeros(1, 2, 4, 128, dtype=torch.bfloat16)
+    f = dict(plan=lambda **kw: kv.plan(ints, ints, ints.view(4, 1), page_size=16, num_pages=1, rows=1, **kw),
+             write=lambda **kw: kv.kv4_write(None, x[0], x[0], ints, **kw),
+             read=lambda **kw: kv.kv4_read(None, ints, k=x[0], v=x[0], **kw),
+             decode=lambda **kw: kv.kv4_decode(x, None, ints, ints, **kw),
+             qk=lambda **kw: attn.qk_norm_rope(x, x, None, None, **kw),
+             qk_bwd=lambda **kw: attn.qk_norm_rope_bwd(x, x, None, None, x, x, **kw))[call]
+    for bad in (torch.zeros(1, dtype=torch.uint8), torch.zeros(1), torch.zeros(0, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="status"):
+            f(status=bad)
+    if call in ("decode", "qk_bwd"):
+        with pytest.raises(ValueError, match="workspace"):
+            f(workspace=torch.zeros(1 << 16, dtype=torch.uint8)[::2])
