@@ -701,10 +701,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
   auto copy_rows = [&](auto is_k, auto rows, uint8_t* slot, int page, int first) {
     constexpr bool K = decltype(is_k)::value;
     constexpr int ROWS = decltype(rows)::value, W = K ? DQK / 2 : DV / 2, G = K ? S::GK : S::GV;
-    if ((unsigned)page >= (unsigned)p.c.num_pages) {
-      if (lane == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
-      return;
-    }
+    if ((unsigned)page >= (unsigned)p.c.num_pages) return;
     const int row = strip[warp].head_row + ((strip[warp].token + first) & (p.c.page_size - 1));
     const int64_t at = (int64_t)page * (p.c.heads * p.c.page_size) + row;
     auto run = [&](uint32_t dst, const uint8_t* src, auto bytes_of) {
@@ -723,6 +720,14 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
     __syncwarp();
     const int left = strip[warp].len - strip[warp].token;
     if (left <= 0) return;
+    if (decltype(is_k)::value && (unsigned)next_page >= (unsigned)p.c.num_pages && p.status) {
+      // A page outside the cache is not copied.  One that no query looks into,
+      // between the first tokens and the window, may be gone: what the slot held
+      // before is masked like any hidden token.
+      const int i = 16 * (lane % (kTile / 16)), t = strip[warp].token + i;
+      if (i < left && (p.window_left < 0 || t < p.sinks || t + 16 > strip[warp].len - p.seqlen_q - p.window_left))
+        atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+    }
     auto pieces = [&](auto rows) {
       constexpr int ROWS = decltype(rows)::value;
 #pragma unroll

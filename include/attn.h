@@ -484,8 +484,9 @@ attn_status_t attn_kv_read(const attn_kv4_cache_t* cache, attn_dtype_t dtype, in
  *     o   [batch][seqlen_q][heads_q][d_v] of o_dtype, lse FP32 [batch][heads_q][seqlen_q]
  * (natural log; a query that sees nothing, of an empty sequence or at a
  * negative position, gets O = 0, LSE = -inf).  Entries of the table past a
- * sequence's last page, and what a page holds past its last token, are not
- * looked at.  Sums are FP32.  A bf16 q row enters the first product in FP16,
+ * sequence's last page, entries of pages that no query sees a token of (behind
+ * the window: such pages may be given away), and what a page holds past its last
+ * token, are not looked at.  Sums are FP32.  A bf16 q row enters the first product in FP16,
  * times a power of two that keeps all but elements 2^27 times smaller than its
  * largest; probabilities times V's scales are rounded to FP16, in units set by
  * the largest V scale of the tokens met so far: beside a token whose V is 2^24

@@ -654,3 +654,28 @@ def test_plan_with_as_many_rows_as_an_int_counts():
         lo, hi = torch.aminmax(t[5:])
         assert lo == -1 and hi == -1
     assert (whole[:, :guard] == 77).all()
+
+
+@pytest.mark.parametrize("page", [16, 32])
+def test_decode_pages_behind_the_window_may_be_gone(page):
+    """Pages all of whose tokens lie before the window and after the first tokens
+    are not looked at, also where they share a tile with visible ones."""
+    x = Held([500, 333, 64, 17], 2, 128, 128, page, BF, seed=19)
+    for sq, window, sinks in ((1, 20, 0), (3, 70, 5), (2, 100, 40), (1, 0, 1), (4, 130, 64)):
+        q = x.q(sq, 8)
+        want = kv.kv4_decode(q, x.cache, x.t, x.l, window_left=window, sinks=sinks)
+        gone = x.t.clone()
+        for b, n in enumerate(x.lens):
+            for j in range(-(-n // page)):
+                if (j + 1) * page <= n - sq - window and j * page >= sinks:
+                    gone[b, j] = (-1, 2 ** 31 - 1)[j % 2]
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = kv.kv4_decode(q, x.cache, gone, x.l, window_left=window, sinks=sinks, status=status)
+        attn.query_status(status)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        if window:  # the first page that is needed
+            need = max(0, 500 - sq - window) // page
+            gone[0, need] = -1
+            kv.kv4_decode(q, x.cache, gone, x.l, window_left=window, sinks=sinks, status=status)
+            with pytest.raises(attn.AttnError, match="out of range"):
+                attn.query_status(status)
