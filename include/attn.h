@@ -486,13 +486,15 @@ attn_status_t attn_kv_read(const attn_kv4_cache_t* cache, attn_dtype_t dtype, in
  * negative position, gets O = 0, LSE = -inf).  Entries of the table past a
  * sequence's last page, entries of pages that no query sees a token of (behind
  * the window: such pages may be given away), and what a page holds past its last
- * token, are not looked at.  Sums are FP32.  A bf16 q row enters the first product in FP16,
- * times a power of two that keeps all but elements 2^27 times smaller than its
- * largest; probabilities times V's scales are rounded to FP16, in units set by
- * the largest V scale of the tokens met so far: beside a token whose V is 2^24
- * times the others', the others lose bits.  The result does not depend on other
- * sequences' lengths beyond the order of its sums, and is bitwise reproducible
- * for the same call on the same device.
+ * token, are not looked at.  Sums are FP32.  A bf16 q row enters the first
+ * product in FP16, times a power of two that keeps all but elements 2^27 times
+ * smaller than its largest; probabilities times V's scales are rounded to FP16, in
+ * units set by the largest V scale, of any group of dims, of the tokens met so far:
+ * beside a V scale 2^24 times the others', the others lose bits.  So O carries an
+ * error of up to 2^-11 of sum p |v|, with an FP32 output as with a 16-bit one.  V
+ * scales of 2^101 and more (values above 10^30) may give infinities.  The result
+ * does not depend on other sequences' lengths beyond the order of its sums, and is
+ * bitwise reproducible for the same call on the same device.
  * Lengths are read on the device: a captured call serves any lengths.
  * seq_lens out of [0, cols * page_size] count as 0 and set the status word; so
  * does a page outside the cache (that sequence's result is then undefined).
@@ -502,7 +504,7 @@ attn_status_t attn_kv_read(const attn_kv4_cache_t* cache, attn_dtype_t dtype, in
  */
 typedef struct {
   attn_dtype_t dtype;    /* q: BF16 or FP16 */
-  attn_dtype_t o_dtype;  /* == dtype, or FP32 */
+  attn_dtype_t o_dtype;  /* == dtype, or FP32: the sums as they are (probabilities have 11 bits) */
   int batch, seqlen_q, heads_q;  /* heads_q % heads_kv == 0, heads_q / heads_kv <= 128 */
   int64_t stride_q[3], stride_o[3]; /* {batch, token, head} */
   int cols;              /* columns of block_table; cols * page_size <= 2^30 */

@@ -679,3 +679,35 @@ def test_decode_pages_behind_the_window_may_be_gone(page):
             kv.kv4_decode(q, x.cache, gone, x.l, window_left=window, sinks=sinks, status=status)
             with pytest.raises(attn.AttnError, match="out of range"):
                 attn.query_status(status)
+
+
+def within_11_bits(o, lse, ref, dt):
+    """within, with the second product's operand as the kernel holds it: fp16, half
+    a step 2^-11, whatever q's type; only the result is rounded to ``dt``."""
+    ro, rl, mag, big = ref
+    score = 2.0 ** -20 * big
+    out = UNIT[dt] if o.dtype != torch.float32 else 0.0
+    tol = out * ro.abs() + (2.0 ** -11 + 2.0 ** -13) * mag + score.transpose(1, 2)[..., None] * mag + 2.0 ** -25
+    err = (o.double() - ro).abs()
+    assert torch.isfinite(o).all() and (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("o_dtype", [BF, torch.float32])
+@pytest.mark.parametrize("dqk,dv", [(64, 64), (128, 128), (192, 128), (256, 256)])
+@pytest.mark.parametrize("group,sq,page,kw", [(4, 1, 64, {}), (8, 2, 16, {}), (5, 3, 32, dict(window_left=40, sinks=33)),
+                                              (2, 1, 256, dict(window_left=255, sinks=4))])
+def test_decode_probabilities_have_11_bits(dqk, dv, group, sq, page, kw, o_dtype):
+    x = Held(LENS + [5000], 2, dqk, dv, page, BF, seed=20)
+    q = x.q(sq, 2 * group)
+    o, lse = kv.kv4_decode(q, x.cache, x.t, x.l, o_dtype=o_dtype, **kw)
+    ref = x.reference(q, **kw)
+    within(o, lse, ref, UNIT[BF])
+    within_11_bits(o, lse, ref, BF)
+
+
+def test_decode_probabilities_have_11_bits_in_large_batches():
+    for lens in ([33] * 300, list(range(0, 600)), [30000] + [21] * 200):
+        x = Held(lens, 2, 64, 64, 64, BF, seed=21)
+        q = x.q(1, 8)
+        o, lse = kv.kv4_decode(q, x.cache, x.t, x.l, o_dtype=torch.float32)
+        within_11_bits(o, lse, x.reference(q), BF)
