@@ -15,23 +15,33 @@ attn_status_t api_fail(attn_status_t s, const char* fmt, ...);
 // cudaSuccess: adds n to the launch count; otherwise ATTN_ERR_CUDA
 attn_status_t api_launched(cudaError_t e, int n, const char* what);
 
-// Where a strided tensor lies: `rows` rows of `width` bytes, `pitch` bytes
-// apart, from `lo` on.  Two tensors that are slices of one buffer (queries and
-// keys of one projection) have interleaved rows: same pitch, other columns.
+// Where a strided tensor lies: `bytes` bytes from `lo` on and, closer, one or more
+// ways to see it as rows of `width` bytes, `pitch` bytes apart (cut between any two
+// of its axes whose outer strides allow that).  Each way covers all of the tensor,
+// so two tensors that are slices of one buffer along any axis (queries and keys of
+// one projection) are apart if some pitch shows them in different columns.
 struct Region {
+  struct Rows {
+    int64_t pitch, width;
+  };
   uintptr_t lo = 0;
-  int64_t rows = 0, pitch = 0, width = 0;
-  uintptr_t hi() const { return rows > 0 ? lo + (uintptr_t)((rows - 1) * pitch + width) : lo; }
+  int64_t bytes = 0;
+  Rows rows[3];
+  int ways = 0;
 };
 
 inline bool regions_overlap(const Region& a, const Region& b) {
-  if (a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
-  if (a.lo >= b.hi() || b.lo >= a.hi()) return false;
-  if (a.pitch != b.pitch || a.width > a.pitch || b.width > b.pitch) return true;
-  // same pitch: compare the columns, modulo the pitch
-  const int64_t d = (int64_t)((a.lo <= b.lo ? b.lo - a.lo : a.lo - b.lo) % (uintptr_t)a.pitch);
-  const int64_t w0 = a.lo <= b.lo ? a.width : b.width, w1 = a.lo <= b.lo ? b.width : a.width;
-  return d < w0 || d + w1 > a.pitch;
+  if (a.bytes <= 0 || b.bytes <= 0) return false;
+  if (a.lo >= b.lo + (uintptr_t)b.bytes || b.lo >= a.lo + (uintptr_t)a.bytes) return false;
+  const Region &x = a.lo <= b.lo ? a : b, &y = a.lo <= b.lo ? b : a;
+  for (int i = 0; i < x.ways; ++i)
+    for (int j = 0; j < y.ways; ++j) {
+      const Region::Rows r = x.rows[i], q = y.rows[j];
+      if (r.pitch != q.pitch) continue;
+      const int64_t at = (int64_t)((y.lo - x.lo) % (uintptr_t)r.pitch);  // y's first column
+      if (at >= r.width && at + q.width <= r.pitch) return false;
+    }
+  return true;
 }
 
 }  // namespace attn

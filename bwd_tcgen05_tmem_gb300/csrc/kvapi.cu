@@ -78,20 +78,31 @@ Region region_of(const void* ptr, const int64_t s[3], int64_t batch, int64_t tok
   Region r;
   r.lo = (uintptr_t)ptr;
   if (batch <= 0 || tokens <= 0 || heads <= 0) return r;
-  const int64_t width = (heads - 1) * s[2] + d;
-  const int64_t span = (batch - 1) * s[0] + (tokens - 1) * s[1] + width;
-  const bool even = s[1] >= width && (batch == 1 || (s[1] > 0 && s[0] % s[1] == 0));
-  r.rows = even ? (batch > 1 ? (batch - 1) * (s[0] / s[1]) : 0) + tokens : 1;
-  r.pitch = (even ? s[1] : span) * es;
-  r.width = (even ? width : span) * es;
+  // the axes that go anywhere, by stride
+  const int64_t n[3] = {batch, tokens, heads};
+  int ax[3], m = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1 || s[i] == 0) continue;
+    int j = m++;
+    for (; j > 0 && s[ax[j - 1]] > s[i]; --j) ax[j] = ax[j - 1];
+    ax[j] = i;
+  }
+  int64_t width = d;  // of the axes inside the cut
+  for (int k = 0; k < m; ++k) {
+    const int64_t pitch = s[ax[k]];
+    bool even = pitch >= width;
+    for (int j = k + 1; j < m; ++j) even = even && s[ax[j]] % pitch == 0;
+    if (even) r.rows[r.ways++] = {pitch * es, width * es};
+    width += (n[ax[k]] - 1) * pitch;
+  }
+  r.bytes = width * es;
   return r;
 }
 
 Region flat(const void* ptr, int64_t bytes) {
   Region r;
   r.lo = (uintptr_t)ptr;
-  r.rows = bytes > 0 ? 1 : 0;
-  r.pitch = r.width = bytes;
+  r.bytes = bytes;
   return r;
 }
 

@@ -506,3 +506,26 @@ def test_tables_of_no_rows_are_not_read():
         assert torch.isnan(t).all()
     with pytest.raises(attn.AttnError, match="out of range"):
         attn.query_status(status)
+
+
+@pytest.mark.parametrize("order", [(1, 0, 2), (0, 2, 1), (2, 0, 1)])
+def test_in_place_in_other_layouts(order):
+    """Views of one projection whose axes lie in another order, written in place."""
+    m = make(3, 20, 4, 2, 64, BF, seed=30)
+    cos, sin = attn.rope_tables(5000, 64)
+    kw = dict(positions=m["pos"], wq=m["wq"], wk=m["wk"])
+    want = attn.qk_norm_rope(m["q"], m["k"], cos, sin, **kw)
+    grad = attn.qk_norm_rope_bwd(m["q"], m["k"], cos, sin, m["dqo"], m["dko"], **kw)
+
+    def merged(a, b):  # both as views of one buffer [.. in that order .., d]
+        x = torch.cat((a, b, b), 2).permute(*order, 3).contiguous().permute(*(order.index(i) for i in range(3)), 3)
+        return x, x[:, :, :4], x[:, :, 4:6]
+
+    x, q, k = merged(m["q"], m["k"])
+    rest = x[:, :, 6:].clone()
+    g, dq, dk = merged(m["dqo"], m["dko"])
+    got = attn.qk_norm_rope_bwd(q, k, cos, sin, dq, dk, dq=dq, dk=dk, **kw)
+    for a, b in zip(got, grad):
+        assert torch.equal(a, b)
+    attn.qk_norm_rope(q, k, cos, sin, q_out=q, k_out=k, **kw)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(x[:, :, 6:], rest)

@@ -338,3 +338,68 @@ def test_python_refuses_status_words_and_workspaces_of_other_shapes(call):
     if call in ("decode", "qk_bwd"):
         with pytest.raises(ValueError, match="workspace"):
             f(workspace=torch.zeros(1 << 16, dtype=torch.uint8)[::2])
+
+
+def qk_overlap(lib, q, qs, q_out, os, shape, k=None, ks=None, k_out=None, kos=None, hk=0):
+    """What refuses a call whose outputs lie where its tables do, which is looked at
+    last: the tables, if everything else is apart (so nothing is ever launched)."""
+    b, s, hq, d = shape
+    st = lambda x: x or (0, 0, 0)  # noqa: E731
+    p = attn.QkParams(0, 2, b, s, hq, hk, d, d, 0, 1, 4096, 1e-6, st(qs), st(ks), st(os), st(kos))
+    rc = qk_call(lib, p, q=q, k=k, wq=None, wk=None, pos=None, qo=q_out, ko=k_out, cos=q_out, status=None)
+    assert rc == INVALID
+    return b"tables" not in lib.attn_last_error()
+
+
+@pytest.mark.parametrize("layout", ["bshd", "sbhd", "bhsd", "hbsd", "shbd", "hsbd"])
+def test_qk_slices_of_one_buffer_in_any_layout(lib, layout):
+    """Slices along one axis of a buffer are apart, in whatever order its axes lie;
+    in place they are the same; one vector of 8 elements further they overlap."""
+    size = dict(b=3, s=50, h=8)
+    stride, at_end = {}, 64
+    for a in reversed(layout[:3]):
+        stride[a], at_end = at_end, at_end * size[a]
+    st = tuple(stride[a] for a in "bsh")
+    base = 64 * MB
+    ptr = lambda el: ctypes.c_void_p(base + 2 * el)  # noqa: E731
+    # q heads 0 .. 3, k heads 4, 5, each in place
+    k = ptr(4 * stride["h"])
+    assert not qk_overlap(lib, ptr(0), st, ptr(0), st, (3, 50, 4, 64), k, st, k, st, 2)
+    k = ptr(4 * stride["h"] - 8)
+    assert qk_overlap(lib, ptr(0), st, ptr(0), st, (3, 50, 4, 64), k, st, k, st, 2)
+    # half of the tokens into the others, one sequence into the next
+    assert not qk_overlap(lib, ptr(0), st, ptr(25 * stride["s"]), st, (3, 25, 8, 64))
+    assert qk_overlap(lib, ptr(0), st, ptr(24 * stride["s"]), st, (3, 25, 8, 64))
+    assert not qk_overlap(lib, ptr(0), st, ptr(stride["b"]), st, (1, 50, 8, 64))
+    # (sequences 2 and 3 of 3: the last one is behind the buffer, or the next token's or
+    # head's first one, which the output holds)
+    assert qk_overlap(lib, ptr(2 * stride["b"]), st, ptr(0), st, (2, 50, 8, 64)) == (layout[0] != "b")
+
+
+def test_qk_overlaps_are_never_missed(lib):
+    """Against the set of vectors of 8 elements that the tensors hold."""
+    import random
+    r = random.Random(7)
+    apart = 0
+    for _ in range(1500):
+        shape = tuple(r.randint(1, 4) for _ in range(3))
+
+        def tensor(output):
+            order, st, inner = r.sample(range(3), 3), [0] * 3, 8
+            for a in order:
+                st[a] = inner * 8 * r.choice((1, 1, 1, 2, 3))
+                inner = st[a] // 8 * shape[a]
+                if not output and r.random() < 0.15:
+                    st[a] = 0
+            base = r.randrange(0, 2000) * 8
+            held = {(base + i * st[0] + j * st[1] + h * st[2]) // 8 + e for i in range(shape[0])
+                    for j in range(shape[1]) for h in range(shape[2]) for e in range(8)}
+            return tuple(st), base, held
+
+        (qs, qb, held), (os, ob, out) = tensor(False), tensor(True)
+        if qb == ob and qs == os:
+            continue
+        got = qk_overlap(lib, ctypes.c_void_p(64 * MB + 2 * qb), qs, ctypes.c_void_p(64 * MB + 2 * ob), os, (*shape, 64))
+        assert got or not held & out
+        apart += not got
+    assert apart > 300
