@@ -12,11 +12,11 @@
 //     rows for each kv head, and this side wastes the least;
 //   * codes go from shared memory to operand registers without a detour: the
 //     cache is laid out (see kvcache.cu) so that a lane's vectors hold exactly
-//     the codes of its operand registers.  One mask makes two fp16 numbers of
-//     two codes: below fp16's normal range a number's bits are its value in
-//     units of 2^-24, and the products take such numbers exactly.  Every other
-//     code stays four bits up, in units of 2^-20, which saves its shift: q is
-//     held divided by 16 there, O is multiplied by 16 at the end.
+//     the codes of its operand registers.  One mask makes two fp16 numbers of two
+//     codes: below fp16's normal range a number's bits are its value in units of
+//     2^-24, and the products take such numbers.  Every other code stays four bits
+//     up, in units 16 times as large, which saves its shift: q is held divided by
+//     16 there, O is multiplied by 16 at the end (head dim 256 differs, see KCodes).
 //     K: pairs of one register are dims n, n + 4 of a word of one token.
 //     V: they are the same dim of two tokens (one byte permute joins the
 //     half-words of both);
@@ -159,24 +159,46 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         "f"(c[3]));
 }
 
-// The 8 codes of a word as pairs of fp16 numbers: pair n holds codes n and n + 4,
-// times 2^-24 for even n, 2^-20 for odd n (fp16 numbers below the normal range,
-// which the products take exactly).
-__device__ __forceinline__ void codes8(uint32_t w, uint32_t (&p)[4]) {
+// The 8 codes of a word as pairs of fp16 numbers below the normal range: pair n
+// holds codes n and n + 4.  The tensor cores take such numbers exactly, but line
+// their products up by the range's lowest exponent, so that sums miss a bit for
+// each zero above a code.
+// K's stand high, since a score is such a sum.  Error of the LSE of few tokens of head
+// dim 64, in 2^-24 of sum |q k|: codes in bits 0 and 4 (no shift for the first two
+// pairs) up to 26, in bits 2 and 6 4.6, all in bit 4 1.7, normal numbers 1.5; time of
+// 16 x 32K tokens of head dim 128 117, 118, 123, 120 us, 8 x 32K of 256 132, 140, 131,
+// 139 us.
+template <int DQK>
+struct KCodes {
+  static constexpr bool kLevel = DQK == 256;  // all pairs in bit 4; else the odd ones 16 fold
+  static constexpr float kOdd = kLevel ? 1.0f : 0.0625f;          // what their q is multiplied with
+  static constexpr float kUnit = kLevel ? 1048576.0f : 4194304.0f;  // 1 / (a code of 1 in the even ones)
+  static constexpr uint32_t kEven8 = kLevel ? 0x80808080u : 0x80208020u, kOdd8 = kLevel ? 0x80808080u : 0x82008200u;  // -8
+  static __device__ __forceinline__ void of(uint32_t w, uint32_t (&p)[4]) {
+    if (kLevel) {
+      p[0] = (w << 4) & 0x00f000f0u;
+      p[1] = w & 0x00f000f0u;
+      p[2] = (w >> 4) & 0x00f000f0u;
+      p[3] = (w >> 8) & 0x00f000f0u;
+    } else {
+      p[0] = (w << 2) & 0x003c003cu;
+      p[1] = (w << 2) & 0x03c003c0u;
+      p[2] = (w >> 6) & 0x003c003cu;
+      p[3] = (w >> 6) & 0x03c003c0u;
+    }
+  }
+};
+// V's, less 8 each (exact), in units of 2^-24, those of odd n 16 fold: their sums
+// keep 18 bits, the probabilities have 11.
+__device__ __forceinline__ void signed8(uint32_t w, uint32_t (&p)[4]) {
   p[0] = w & 0x000f000fu;
   p[1] = w & 0x00f000f0u;
   w >>= 8;
   p[2] = w & 0x000f000fu;
   p[3] = w & 0x00f000f0u;
-}
-// -8 in both units
-constexpr uint32_t kLow8 = 0x80088008u, kHigh8 = 0x80808080u;
-// codes8 less 8 each: exact
-__device__ __forceinline__ void signed8(uint32_t w, uint32_t (&p)[4]) {
-  codes8(w, p);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t o = i & 1 ? kHigh8 : kLow8;
+    const uint32_t o = i & 1 ? 0x80808080u : 0x80088008u;  // -8
     const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&p[i]), *reinterpret_cast<const __half2*>(&o));
     p[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
@@ -230,8 +252,7 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)
 template <int DQK, int DV, int NT>
 struct Piece {
   using S = DecShape<DQK, DV, NT>;
-  // dims (8c + i, 8c + i + 4) of group g; those of odd i (whose codes come in
-  // sixteenfold units) divided by 16
+  // dims (8c + i, 8c + i + 4) of group g; those of odd i in KCodes' unit for them
   uint32_t qf[NT][S::GK][4];
   float xs[NT][2];               // from products to scores in base 2
   float o[NT][S::GV][2][4];      // dims 32 g + 4 r + {0,1}, {2,3} (odd ones 16 fold)
@@ -261,8 +282,8 @@ __device__ __forceinline__ void tile_scores(const Piece<DQK, DV, NT>& z, const u
 #pragma unroll
     for (int g = 0; g < S::GK; ++g) {
       uint32_t a[4], b[4];
-      codes8(ka[g], a);
-      codes8(kb[g], b);
+      KCodes<DQK>::of(ka[g], a);
+      KCodes<DQK>::of(kb[g], b);
       const float fa = scale_of(sa, g), fb = scale_of(sb, g);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -802,14 +823,14 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
         float f[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          f[i] = Pack<BF16>::to_f((uint16_t)(w[i >> 1] >> (16 * (i & 1)))) * ((i & 1) ? inv * 0.0625f : inv);
+          f[i] = Pack<BF16>::to_f((uint16_t)(w[i >> 1] >> (16 * (i & 1)))) * ((i & 1) ? inv * KCodes<DQK>::kOdd : inv);
 #pragma unroll
         for (int i = 0; i < 4; ++i) z.qf[t][g][i] = Pack<false>::two(f[i], f[i + 4]);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         // (not 0, whatever the scale: times -inf that would be NaN)
-        z.xs[t][e] = fmaxf(p.scale_log2 * 16777216.0f * __shfl_sync(0xffffffffu, pow2(ex), (2 * c + e) * 4),
+        z.xs[t][e] = fmaxf(p.scale_log2 * KCodes<DQK>::kUnit * __shfl_sync(0xffffffffu, pow2(ex), (2 * c + e) * 4),
                            1.17549435e-38f);
         z.ref[t][e] = 1e30f;  // nothing seen yet: a reference below any score
         z.l[t][e] = 0.0f;
@@ -828,8 +849,9 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
       for (int g = 0; g < S::GK; ++g) {
         const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         float low[4];
-        mma16816(low, kLow8, kLow8, kHigh8, kHigh8, z.qf[t][g][0], z.qf[t][g][1], zero);
-        mma16816(low, kLow8, kLow8, kHigh8, kHigh8, z.qf[t][g][2], z.qf[t][g][3]);
+        constexpr uint32_t even = KCodes<DQK>::kEven8, odd = KCodes<DQK>::kOdd8;
+        mma16816(low, even, even, odd, odd, z.qf[t][g][0], z.qf[t][g][1], zero);
+        mma16816(low, even, even, odd, odd, z.qf[t][g][2], z.qf[t][g][3]);
         if (r == 0) lows[warp][(t * S::GK + g) * 4 + c] = make_float4(low[0], low[1], low[2], low[3]);
       }
     __syncwarp();

@@ -711,3 +711,14 @@ def test_decode_probabilities_have_11_bits_in_large_batches():
         q = x.q(1, 8)
         o, lse = kv.kv4_decode(q, x.cache, x.t, x.l, o_dtype=torch.float32)
         within_11_bits(o, lse, x.reference(q), BF)
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("dqk,dv", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("scale", [1.5, 6.0])
+def test_decode_scores_of_few_tokens(dqk, dv, scale, dt):
+    """The LSE of one to twenty tokens is a score or nearly one: nothing averages the
+    products' sums out."""
+    for seed in range(6):
+        x = Held([1, 2, 3, 5, 9, 20] * 8, 3, dqk, dv, 64, dt, seed=seed)
+        x.check(x.q(1, 24, scale=scale))
