@@ -28,7 +28,7 @@ namespace attn {
 // where the page is new, from the free list (so no block waits for another's
 // table entries).
 // Latency bounds it.  Measured on a GB300 (graph replays): 64 requests of one
-// new token 3.3 us (a launch); 1021 requests of up to 500 new tokens 11.1 us, most of it
+// new token 3.5 us (a launch); 1021 requests of up to 500 new tokens 11.4 us, most of it
 // the sums that every block makes and the searches.
 constexpr int kPlanThreads = 256;
 
@@ -179,9 +179,10 @@ cudaError_t launch_kv_plan(const PlanParams& p, int num_sms, cudaStream_t st) {
 // Streams, bound by HBM if a word of codes costs few enough instructions: to
 // read back takes about 80 a warp and vector, to store somewhat more (its issue
 // slots are 60 to 70% taken).  Measured on a GB300 (graph replays, 32768 tokens, 8
-// kv heads, 128 / 128, bf16): stored in 37 us (172 MB, 4.7 TB/s, 69% of a plain
-// copy's rate), read back in 31 us (5.5 TB/s, 82%); 64 tokens stored and read
-// back 4.5 us, two launches.  Without the ring of copies: 155 us for both.
+// kv heads, 128 / 128): stored in 37 us in bf16 (172 MB, 4.6 TB/s, 68% of a plain
+// copy's rate), 38 us in fp16, read back in 32 (5.4 TB/s, 80%) and 33 us; 64 tokens
+// stored and read back 4.7 us, two launches.  Without the ring of copies: 155 us for
+// both.
 struct RowLane {
   bool live, is_k;
   int token;         // of the block's first pass
@@ -253,7 +254,8 @@ __device__ __forceinline__ uint64_t pair_f32(uint32_t w) {
 }
 
 // The codes of 8 elements whose scale s is a normal number, without a division:
-// the quotient is x * (1/s) corrected by its exact remainder.  A quotient that
+// the quotient is x * (1/s) corrected by its exact remainder (P. W. Markstein, IBM
+// Journal of Research and Development 34, 1990).  A quotient that
 // lies midway between two codes has few bits, so the corrected product is that
 // number itself and rounds to even as the division would; any other is at
 // least 2^-13 away from the middle (x has 11 bits, s (2c + 1) / 2 has 12), 2^9

@@ -47,16 +47,21 @@
 // order of the runs.
 //
 // Measured on a GB300 (graph replays, 8 kv heads, 4 query heads each, bf16):
-// 16 x 32768 tokens of head dim 128 116 us = 5.2 TB/s (77% of a plain copy's
-// rate), 48 ragged ones up to 32768 91 us, 128 x 4096 126 us, 512 x 1023 136 us,
-// 2048 x 250 187 us (an item's start and end weigh about two tiles); head dim 64
-// 74 us, 192 / 128 157 us, 256 (8 requests) 130 us; 16 query rows a kv head 172
-// us; pages of 16 tokens 142 us, of 32 132 us.
-// What bounds the long ones: the instructions of a tile (about 1150 a warp for
-// 64 tokens of head dim 128, half of them on the ALU pipe; 60% of the issue
+// 16 x 32768 tokens of head dim 128 118.5 us = 5.1 TB/s (75% of a plain copy's
+// rate), 48 ragged ones up to 32768 94 us, 512 x 1023 140 us, 2048 x 250 192 us (an
+// item's start and end weigh about two tiles); head dim 64 74 us, 192 / 128 157 us,
+// 256 (8 requests) 130 us; 16 query rows a kv head 176 us; pages of 16 tokens 142
+// us, of 32 129 us.
+// What bounds the long ones: the instructions of a tile (about 1180 a warp for
+// 64 tokens of head dim 128, half of them on the ALU pipe; 62% of the issue
 // slots are taken) beside the copies: when the whole took 121 us, the tiles' work
-// without copies took 115 us and the copies alone 99 us.  Short requests wait for instructions too (the
-// loop and what surrounds it do not fit the first instruction cache).
+// without copies took 115 us and the copies alone 99 us.  Short requests wait for
+// instructions too (the loop and what surrounds it do not fit the first instruction
+// cache).  From 9 rows a kv head on 8 warps an SM are left to hide latencies.
+// Every 16 rows a kv head are an item of their own, which reads and converts the
+// cache again: 4 x 8192 tokens, 4 query heads a kv head, 1, 8, 32, 128, 256 query
+// tokens 20, 35, 100, 331, 647 us, where reading the cache back and attn_fwd take
+// 90, 90, 90, 92, 140 us.
 // Tiles of 64 tokens against 32: 16 x 32K tokens 121 / 131 us, head dim 64 75 /
 // 94 us, 16 query rows 187 / 219 us; a window of 4095 (24 requests, 4 new tokens,
 // 192 / 128) 35.3 / 33.0 us, where the tiles that the window's ends cut weigh
@@ -75,7 +80,9 @@ constexpr int kTile = 64;     // tokens of a warp's tile
 constexpr int kItemCost = 2;  // in tiles: what an item costs a warp besides them (q, the list, the result)
 constexpr int kExpMin = -80, kExpMax = 100;  // exponents of V's scales told apart
 
-// whether 128 registers hold a lane's share
+// Whether a lane's share is to fit 128 registers (four blocks an SM, two otherwise).
+// Not all of it does: of head dims 192 / 128 156 bytes a thread spill, of 64 with 16
+// rows 144, of 128 32.
 __host__ __device__ constexpr bool light(int dv, int nt) { return dv * nt <= 128; }
 
 template <int DQK, int DV, int NT>

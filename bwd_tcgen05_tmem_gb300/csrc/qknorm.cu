@@ -25,8 +25,8 @@
 //
 // Measured on a GB300 (graph replays, bf16, head dim 128, 32 + 8 heads): forward
 // of 32768 tokens 116 us, 5.9 TB/s (88% of a plain copy's rate); gradient of
-// 16384 tokens 97 us, 5.2 TB/s (77%: bound by instruction issue beside the
-// copies, about 44 a pair of elements); 8 tokens 3.1 us, a launch; a gradient of
+// 16384 tokens 96 us, 5.3 TB/s (78%: bound by instruction issue beside the
+// copies, about 47 a pair of elements); 8 tokens 3.2 us, a launch; a gradient of
 // 3 x 1001 tokens of 6 + 2 heads of 192 13 us, two dependent launches and the
 // join of dw.  Loads into registers instead of the ring: 155 and 173 us.
 #include <algorithm>
@@ -215,7 +215,7 @@ __device__ __forceinline__ int token_position(const QkParams& p, uint32_t tok) {
 // A job is one token and one run of kSlots * U of its heads, of one side; where
 // half of the kSlots rows that a warp holds at a time or more would be idle, it
 // is several tokens in a row with all of their heads (48K tokens of 2 + 2 heads of
-// 64, gradient: 29 us, one token a job 85 us; only calls with such a side run that
+// 64, gradient: 28 us, one token a job 85 us; only calls with such a side run that
 // form, which costs the others 4%).  The side's blocks share its
 // jobs, a warp takes every (blocks * warps)-th.  A lane's view of the side's tensors: byte offsets from its vector a of its row
 // (slot) of the first run.
@@ -331,7 +331,7 @@ struct QkWarp {
 
 // ----------------------------------------------------------------- forward
 // FULL: all elements turn, and no lane asks whether its own do (32K tokens of 32 + 8
-// heads of 128: 116 us; with the question 120 us, which half of each row turning takes).
+// heads of 128: 116 us; with the question, as where half of each row turns, 120 us).
 template <bool BF16, int D, int U, bool INTER, bool MANY, bool FULL>
 __global__ void __launch_bounds__(kQkThreads, 6) attn_qk_fwd_kernel(
     const __grid_constant__ QkParams p) {

@@ -354,7 +354,8 @@ attn_status_t attn_cp_relayout(int to_heads, int cp, int64_t seqlen, int heads, 
  *         rotary_dim elements: pairs (i, i + rotary_dim/2), or (2i, 2i+1) with
  *         interleaved = 1:  (a, b) -> (a cos - b sin, b cos + a sin)
  * rounded once to dtype.  At eps = 0 a row whose mean square is 0 in FP32 (below
- * 2^-150) gives zeros, in the gradient too.  A NaN in a row makes all of it NaN.
+ * 2^-150) gives zeros, in the gradient too.  A NaN in a row makes all of it NaN; a
+ * mean square beyond FP32's range leaves zeros, and NaN for what was infinite.
  * cos/sin: FP32 [max_pos][rotary_dim/2], contiguous,
  * 16-byte aligned (make them in FP64: angles of far positions need it).
  * positions: int32 [batch][seqlen], contiguous, or NULL for 0, 1, .. in each
@@ -476,7 +477,9 @@ attn_status_t attn_kv_read(const attn_kv4_cache_t* cache, attn_dtype_t dtype, in
 
 /*
  * Attention of the last seqlen_q tokens of each sequence (1 to 256: a decode
- * step, drafted tokens, a short chunk) over the 4-bit cache.  Sequence b holds
+ * step, drafted tokens, a short chunk) over the 4-bit cache.  (It reads the cache
+ * once for every 16 query rows a kv head, 8 at d_v = 256: from about 100 rows on,
+ * attn_kv_read and attn_fwd are quicker.)  Sequence b holds
  * seq_lens[b] tokens, those seqlen_q among them, in the pages of row b of
  * block_table.  Query i stands at pos = seq_lens[b] - seqlen_q + i and sees
  * tokens j <= pos with window_left < 0, or j >= pos - window_left, or
