@@ -36,7 +36,7 @@ EXPORTED = ["attn_fwd_workspace_size", "attn_bwd_workspace_size", "attn_fwd", "a
             "attn_fwd_bwd_host_stages", "attn_bwd_path",
             "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_size",
             "attn_kv_plan", "attn_kv_write", "attn_kv_read", "attn_kv_decode",
-            "attn_kv_decode_workspace_size"]
+            "attn_kv_decode_workspace_size", "attn_kv_weights", "attn_kv_evict"]
 # attn_fwd_bwd_host_stages stage bits
 HOST_UPLOAD, HOST_COMPUTE, HOST_DOWNLOAD, HOST_ALL = 1, 2, 4, 7
 # attn_bwd_path results: which backward kernels run (and the stage order)
@@ -119,6 +119,26 @@ class Kv4DecodeParams(ctypes.Structure):
     ]
 
 
+class Kv4WeightsParams(ctypes.Structure):
+    """Mirror of attn_kv4_weights_params_t."""
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("batch", ctypes.c_int), ("seqlen_q", ctypes.c_int),
+        ("heads_q", ctypes.c_int), ("stride_q", ctypes.c_int64 * 3),
+        ("cols", ctypes.c_int), ("table_stride", ctypes.c_int64),
+        ("window_left", ctypes.c_int), ("sinks", ctypes.c_int), ("softmax_scale", ctypes.c_float),
+        ("accumulate", ctypes.c_int), ("capacity", ctypes.c_int), ("stride_w", ctypes.c_int64 * 2),
+    ]
+
+
+class Kv4EvictParams(ctypes.Structure):
+    """Mirror of attn_kv4_evict_params_t."""
+    _fields_ = [
+        ("batch", ctypes.c_int), ("cols", ctypes.c_int), ("table_stride", ctypes.c_int64),
+        ("keep", ctypes.c_int), ("recent", ctypes.c_int), ("capacity", ctypes.c_int),
+        ("stride_w", ctypes.c_int64 * 2), ("stride_wo", ctypes.c_int64 * 2), ("n_free", ctypes.c_int),
+    ]
+
+
 _lib = None
 _fast = None
 _lock = threading.Lock()
@@ -191,6 +211,10 @@ def load():
         lib.attn_kv_decode_workspace_size.restype = sz
         lib.attn_kv_decode.argtypes = [D, C] + [vp] * 6 + [sz, vp, vp]
         lib.attn_kv_decode.restype = ctypes.c_int
+        lib.attn_kv_weights.argtypes = [ctypes.POINTER(Kv4WeightsParams), C] + [vp] * 7
+        lib.attn_kv_weights.restype = ctypes.c_int
+        lib.attn_kv_evict.argtypes = [ctypes.POINTER(Kv4EvictParams), C] + [vp] * 12
+        lib.attn_kv_evict.restype = ctypes.c_int
         global _fast
         _fast = _fast_handle()
         _lib = lib
@@ -203,6 +227,8 @@ def load():
 _QK_PACK = struct.Struct("@11if18q").pack          # attn_qk_params_t
 _PLAN_PACK = struct.Struct("@6iq").pack            # attn_kv_plan_params_t
 _DECODE_PACK = struct.Struct("@5i6qiq2if0q").pack  # attn_kv4_decode_params_t
+_WEIGHTS_PACK = struct.Struct("@4i3qiq2if2i2q").pack  # attn_kv4_weights_params_t
+_EVICT_PACK = struct.Struct("@2iq3i4qi0q").pack       # attn_kv4_evict_params_t
 
 
 def _fast_handle():
@@ -213,7 +239,8 @@ def _fast_handle():
                        ("attn_kv_plan", [vp] * 13),
                        ("attn_kv_write", [vp, ci, ci] + [vp] * 7),
                        ("attn_kv_read", [vp, ci, ci] + [vp] * 7),
-                       ("attn_kv_decode", [vp] * 8 + [sz, vp, vp])):
+                       ("attn_kv_decode", [vp] * 8 + [sz, vp, vp]),
+                       ("attn_kv_weights", [vp] * 9), ("attn_kv_evict", [vp] * 14)):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, ctypes.c_int
     for name, args in (("attn_qk_norm_rope_bwd_workspace_size", [vp]),

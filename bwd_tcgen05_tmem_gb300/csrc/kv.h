@@ -109,4 +109,33 @@ size_t decode_runs(int blocks);
 size_t decode_partial_floats(int blocks, int rows_per_block, int d_v);
 cudaError_t launch_kv4_decode(const DecodeParams& p, bool bf16, int blocks, cudaStream_t st);
 
+struct WeightsParams {
+  Kv4 c;
+  const void* q;
+  const float* lse;  // [batch][heads_q][seqlen_q]
+  float* w;          // [batch][heads][capacity], strides w_b, w_h
+  const int32_t *table, *seq_lens;
+  int64_t q_b, q_t, q_h, table_stride, w_b, w_h;
+  int batch, seqlen_q, heads_q, group, cols, capacity, window_left, sinks, add;
+  int rows;          // query rows of a kv head (seqlen_q * group)
+  FastDiv by_group;
+  float scale_log2;
+  int* status;
+};
+cudaError_t launch_kv4_weights(const WeightsParams& p, bool bf16, int num_sms, cudaStream_t st);
+
+struct EvictParams {
+  Kv4 c;
+  const int32_t *table, *seq_lens, *first;  // first: or null
+  const float* w;
+  float* w_out;
+  int32_t *kept, *seq_out;
+  const int32_t* free_head;  // null: no pages are given back
+  int32_t *free_pages, *free_head_out;
+  int64_t table_stride, w_b, w_h, wo_b, wo_h;
+  int batch, cols, capacity, keep, recent, n_free;
+  int* status;
+};
+cudaError_t launch_kv4_evict(const EvictParams& p, int num_sms, cudaStream_t st);
+
 }  // namespace attn

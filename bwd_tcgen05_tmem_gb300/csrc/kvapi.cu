@@ -1,6 +1,6 @@
 // kvapi.cu -- C entry points of the operators around the attention kernels:
-// attn_qk_norm_rope (and its gradient), attn_kv_plan, attn_kv_write / _read and
-// attn_kv_decode.  Host-side checks and dispatch; nothing is allocated.
+// attn_qk_norm_rope (and its gradient), attn_kv_plan, attn_kv_write / _read,
+// attn_kv_decode, attn_kv_weights and attn_kv_evict.  Host-side checks and dispatch; nothing is allocated.
 #include <cmath>
 #include <cstring>
 
@@ -647,6 +647,193 @@ attn_status_t attn_kv_decode(const attn_kv4_decode_params_t* p, const attn_kv4_c
   const cudaError_t e =
       attn::launch_kv4_decode(kp, p->dtype == ATTN_BF16, l.blocks, (cudaStream_t)stream);
   return api_launched(e, 2, "cache attention launch");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ weights and eviction
+namespace {
+
+// Rows [batch][heads] of `capacity` floats.
+attn_status_t check_weight_rows(const char* name, const float* w, const int64_t s[2], int64_t batch,
+                                int64_t heads, int64_t capacity, bool output) {
+  if (batch && capacity) {
+    if (!w) return api_fail(ATTN_ERR_INVALID_ARG, "%s is NULL", name);
+    if ((uintptr_t)w % 4) return api_fail(ATTN_ERR_ALIGNMENT, "%s is not 4-byte aligned", name);
+  }
+  if (s[0] < 0 || s[1] < 0) return api_fail(ATTN_ERR_INVALID_ARG, "a stride of %s is negative", name);
+  if (!output) return ATTN_OK;
+  // the smaller stride steps over a row, the larger one over all of those
+  const bool heads_inner = batch <= 1 || (heads > 1 && s[1] <= s[0]);
+  const int64_t in = heads_inner ? s[1] : s[0], n_in = heads_inner ? heads : batch;
+  const int64_t out = heads_inner ? s[0] : s[1], n_out = heads_inner ? batch : heads;
+  const int64_t extent = capacity + (n_in > 1 ? (n_in - 1) * in : 0);
+  if ((n_in > 1 && in < capacity) || (n_out > 1 && out < extent))
+    return api_fail(ATTN_ERR_INVALID_ARG, "rows of %s share memory", name);
+  return ATTN_OK;
+}
+
+Region weight_region(const float* w, const int64_t s[2], int64_t batch, int64_t heads, int64_t capacity) {
+  const int64_t s3[3] = {0, s[0], s[1]};
+  return capacity ? region_of(w, s3, 1, batch, heads, capacity, 4) : flat(w, 0);
+}
+
+Region table_region(const int32_t* t, int batch, int cols, int64_t stride) {
+  return flat(t, batch && cols ? ((batch - 1) * stride + cols) * 4 : 0);
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status_t attn_kv_weights(const attn_kv4_weights_params_t* p, const attn_kv4_cache_t* cache,
+                              const void* q, const int32_t* block_table, const int32_t* seq_lens,
+                              const float* lse, float* weights, int32_t* status,
+                              attn_stream_t stream) {
+  api_begin();
+  if (!p) return api_fail(ATTN_ERR_INVALID_ARG, "params is NULL");
+  // what both calls take is checked as attn_kv_decode does
+  attn_kv4_decode_params_t d;
+  memset(&d, 0, sizeof(d));
+  d.dtype = d.o_dtype = p->dtype;
+  d.batch = p->batch, d.seqlen_q = p->seqlen_q, d.heads_q = p->heads_q;
+  d.cols = p->cols, d.table_stride = p->table_stride;
+  d.window_left = p->window_left, d.sinks = p->sinks, d.softmax_scale = p->softmax_scale;
+  attn::DecodeParams dp;
+  attn_status_t s = check_decode(&d, cache, dp);
+  if (s) return s;
+  if (p->capacity < 0) return api_fail(ATTN_ERR_INVALID_ARG, "capacity < 0");
+  if ((s = check_status_word(status))) return s;
+  if (p->batch == 0 || p->seqlen_q == 0) return ATTN_OK;
+  if ((s = check_rows("q", q, p->stride_q, p->batch, p->seqlen_q, p->heads_q, cache->d_qk, 2, false)) ||
+      (s = check_weight_rows("weights", weights, p->stride_w, p->batch, cache->heads_kv, p->capacity, true)) ||
+      (s = check_ints("lse", lse)) || (s = check_ints("seq_lens", seq_lens)) ||
+      (p->cols && (s = check_ints("block_table", block_table))))
+    return s;
+  Region held[4];
+  cache_regions(cache, held);
+  const Region in[8] = {held[0], held[1], held[2], held[3],
+                        region_of(q, p->stride_q, p->batch, p->seqlen_q, p->heads_q, cache->d_qk, 2),
+                        table_region(block_table, p->batch, p->cols, p->table_stride),
+                        flat(seq_lens, p->batch * 4ll),
+                        flat(lse, (int64_t)p->batch * p->heads_q * p->seqlen_q * 4)};
+  const Region out[2] = {weight_region(weights, p->stride_w, p->batch, cache->heads_kv, p->capacity),
+                         flat(status, status ? 4 : 0)};
+  for (const Region& o : out)
+    for (const Region& r : in)
+      if (regions_overlap(o, r)) return api_fail(ATTN_ERR_INVALID_ARG, "an output overlaps an input");
+  if (regions_overlap(out[0], out[1])) return api_fail(ATTN_ERR_INVALID_ARG, "outputs overlap");
+  attn::WeightsParams kp;
+  memset(&kp, 0, sizeof(kp));
+  kp.c = dp.c;
+  kp.q = q;
+  kp.lse = lse;
+  kp.w = weights;
+  kp.table = block_table;
+  kp.seq_lens = seq_lens;
+  kp.q_b = p->stride_q[0], kp.q_t = p->stride_q[1], kp.q_h = p->stride_q[2];
+  kp.table_stride = p->table_stride;
+  kp.w_b = p->stride_w[0], kp.w_h = p->stride_w[1];
+  kp.batch = p->batch;
+  kp.seqlen_q = p->seqlen_q;
+  kp.heads_q = p->heads_q;
+  kp.group = dp.group;
+  kp.cols = p->cols;
+  kp.capacity = p->capacity;
+  kp.window_left = dp.window_left;
+  kp.sinks = dp.sinks;
+  kp.add = p->accumulate ? 1 : 0;
+  kp.rows = dp.rows;
+  kp.by_group = dp.by_group;
+  kp.scale_log2 = dp.scale_log2;
+  kp.status = status;
+  return api_launched(
+      attn::launch_kv4_weights(kp, p->dtype == ATTN_BF16, attn::num_sms(), (cudaStream_t)stream), 1,
+      "cache weights launch");
+}
+
+attn_status_t attn_kv_evict(const attn_kv4_evict_params_t* p, const attn_kv4_cache_t* cache,
+                            const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* first, const float* weights, float* weights_out,
+                            int32_t* kept, int32_t* seq_lens_out, int32_t* free_pages,
+                            const int32_t* free_head, int32_t* free_head_out, int32_t* status,
+                            attn_stream_t stream) {
+  api_begin();
+  attn::EvictParams kp;
+  memset(&kp, 0, sizeof(kp));
+  attn_status_t s = check_cache(cache, kp.c);
+  if (s) return s;
+  if (!p) return api_fail(ATTN_ERR_INVALID_ARG, "params is NULL");
+  if (p->batch < 0 || p->cols < 0 || p->capacity < 0 || p->n_free < 0 || p->recent < 0)
+    return api_fail(ATTN_ERR_INVALID_ARG, "a size is negative");
+  if (p->keep < 1) return api_fail(ATTN_ERR_INVALID_ARG, "keep < 1");
+  if (((int64_t)p->cols << kp.c.page_shift) > (1 << 30) || p->capacity > (1 << 30) || p->keep > (1 << 30))
+    return api_fail(ATTN_ERR_UNSUPPORTED, "cols * page_size, capacity or keep > 2^30");
+  if ((int64_t)p->batch * cache->heads_kv > (1 << 24) || (int64_t)p->batch * p->cols > INT32_MAX)
+    return api_fail(ATTN_ERR_UNSUPPORTED, "batch * heads_kv > 2^24, or batch * cols >= 2^31");
+  if (p->batch > 1 && p->table_stride < 0)
+    return api_fail(ATTN_ERR_INVALID_ARG, "table_stride < 0");
+  if ((s = check_status_word(status))) return s;
+  if (free_head && ((s = check_ints("free_head", free_head)) || (s = check_ints("free_head_out", free_head_out)) ||
+                    (p->n_free && (s = check_ints("free_pages", free_pages)))))
+    return s;
+  const Region lists[3] = {flat(free_head, free_head ? 4 : 0), flat(free_head_out, free_head ? 4 : 0),
+                           flat(free_pages, free_head ? p->n_free * 4ll : 0)};
+  if (p->batch == 0) {  // nothing is given back
+    if (!free_head) return ATTN_OK;
+    if (regions_overlap(lists[0], lists[1])) return api_fail(ATTN_ERR_INVALID_ARG, "free_head_out overlaps free_head");
+    return api_launched(cudaMemcpyAsync(free_head_out, free_head, 4, cudaMemcpyDeviceToDevice, (cudaStream_t)stream), 0,
+                        "free_head copy");
+  }
+  const int64_t heads = cache->heads_kv;
+  if ((s = check_weight_rows("weights", weights, p->stride_w, p->batch, heads, p->capacity, false)) ||
+      (s = check_weight_rows("weights_out", weights_out, p->stride_wo, p->batch, heads, p->capacity, true)) ||
+      (s = check_ints("kept", kept)) || (s = check_ints("seq_lens", seq_lens)) ||
+      (s = check_ints("seq_lens_out", seq_lens_out)) || (p->cols && (s = check_ints("block_table", block_table))))
+    return s;
+  if ((uintptr_t)first % 4) return api_fail(ATTN_ERR_ALIGNMENT, "first is not 4-byte aligned");
+  const bool inplace = weights_out == weights && (p->batch == 1 || p->stride_w[0] == p->stride_wo[0]) &&
+                       (heads == 1 || p->stride_w[1] == p->stride_wo[1]);
+  const Region in[5] = {table_region(block_table, p->batch, p->cols, p->table_stride),
+                        flat(seq_lens, p->batch * 4ll), flat(first, first ? p->batch * 4ll : 0), lists[0],
+                        weight_region(weights, p->stride_w, p->batch, heads, p->capacity)};
+  Region out[10] = {weight_region(weights_out, p->stride_wo, p->batch, heads, p->capacity),
+                    flat(kept, p->batch * heads * p->keep * 4),
+                    flat(seq_lens_out, p->batch * 4ll),
+                    lists[1],
+                    lists[2],
+                    flat(status, status ? 4 : 0)};
+  Region held[4];
+  cache_regions(cache, held);
+  for (int i = 0; i < 4; ++i) out[6 + i] = held[i];
+  for (int i = 0; i < 10; ++i) {
+    for (int j = 0; j < 5; ++j)
+      if (!(i == 0 && j == 4 && inplace) && regions_overlap(out[i], in[j]))
+        return api_fail(ATTN_ERR_INVALID_ARG, "an output or the cache overlaps an input");
+    for (int j = i + 1; j < 10; ++j)
+      if (regions_overlap(out[i], out[j])) return api_fail(ATTN_ERR_INVALID_ARG, "outputs or the cache overlap");
+  }
+  kp.table = block_table;
+  kp.seq_lens = seq_lens;
+  kp.first = first;
+  kp.w = weights;
+  kp.w_out = weights_out;
+  kp.kept = kept;
+  kp.seq_out = seq_lens_out;
+  kp.free_head = free_head;
+  kp.free_pages = free_pages;
+  kp.free_head_out = free_head_out;
+  kp.table_stride = p->table_stride;
+  kp.w_b = p->stride_w[0], kp.w_h = p->stride_w[1];
+  kp.wo_b = p->stride_wo[0], kp.wo_h = p->stride_wo[1];
+  kp.batch = p->batch;
+  kp.cols = p->cols;
+  kp.capacity = p->capacity;
+  kp.keep = p->keep;
+  kp.recent = p->recent;
+  kp.n_free = free_head ? p->n_free : 0;
+  kp.status = status;
+  return api_launched(attn::launch_kv4_evict(kp, attn::num_sms(), (cudaStream_t)stream), 1, "eviction launch");
 }
 
 }  // extern "C"

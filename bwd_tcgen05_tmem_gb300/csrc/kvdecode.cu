@@ -72,6 +72,7 @@
 
 #include "kcommon.cuh"
 #include "kv.h"
+#include "kvtile.cuh"
 
 namespace attn {
 
@@ -148,24 +149,6 @@ __host__ __device__ inline long long used_runs(long long tiles, int blocks) {
 }
 
 // ----------------------------------------------------------------- operands
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// d = c + a b
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1,
-                                         const float (&c)[4]) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
-        "f"(c[3]));
-}
-
 // The 8 codes of a word as pairs of fp16 numbers below the normal range: pair n
 // holds codes n and n + 4.  The tensor cores take such numbers exactly, but line
 // their products up by the range's lowest exponent, so that sums miss a bit for
@@ -217,31 +200,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// N words from shared memory, in the widest loads their alignment allows
-template <int N>
-__device__ __forceinline__ void lds_words(const uint8_t* s, uint32_t (&w)[N]) {
-  if constexpr (N % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const uint4 v = reinterpret_cast<const uint4*>(s)[i];
-      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-    }
-  } else if constexpr (N % 2 == 0) {
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      const uint2 v = reinterpret_cast<const uint2*>(s)[i];
-      w[2 * i] = v.x, w[2 * i + 1] = v.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t*>(s)[i];
-  }
-}
-// scale g of the pairs in w
-__device__ __forceinline__ float scale_of(const uint32_t* w, int g) {
-  return __uint_as_float((g & 1) ? (w[g >> 1] & 0xffff0000u) : (w[g >> 1] << 16));
-}
-
 // Token of row r (of 8) of a tile's block of 8: the four tokens of rows 2c and
 // the four of rows 2c + 1 are neighbours, so a warp's V loads (rows 2c of all
 // four c) cover 256 bytes in a row, and rows 2q, 2q + 1 lie in different
@@ -249,9 +207,6 @@ __device__ __forceinline__ float scale_of(const uint32_t* w, int g) {
 __device__ __forceinline__ int row_token(int r) {
   return (r & 1) ? 4 + ((r >> 1) ^ 1) : r >> 1;
 }
-
-// A power of two from its exponent (-126 .. 127).
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // ----------------------------------------------------------------- a tile
 // What a lane holds of its warp's piece: the query operand, O^T, and for its
@@ -552,17 +507,6 @@ __device__ __forceinline__ void write_row(const DecodeParams& p, int b, int kvh,
 }
 
 // ----------------------------------------------------------------- the kernel
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-               "l"((uint64_t)__cvta_generic_to_global(src))
-               : "memory");
-}
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {  // all but the last N groups of this thread
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // A place in the list of tiles: tile v of an item of a sequence.
 struct Cursor {
   int b, item, v;

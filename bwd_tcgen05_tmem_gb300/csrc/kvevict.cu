@@ -1,0 +1,381 @@
+// kvevict.cu -- eviction from the 4-bit cache: of a sequence longer than its
+// budget, each kv head keeps `keep` tokens, the first ones, the last ones and of
+// those between the ones with the largest weights, and its rows move together.
+//
+// One cluster of blocks works on one (sequence, kv head):
+//   * the border: the room-th largest weight, by a radix selection over the bits of
+//     the weights (as whole numbers they are ordered; 11, 11 and 10 bits at a time).
+//     Each block counts its slice of the candidates in shared memory, the blocks add
+//     up each other's counts over the cluster's distributed shared memory;
+//   * the list: every candidate above the border stays, and of those on it the first
+//     ones.  Blocks count theirs, exchange the counts, and write `kept` in order;
+//   * the rows: row i becomes what row kept[i] >= i was.  Rows are taken in rounds of
+//     ascending i: all blocks copy a round's rows into shared memory, meet at the
+//     cluster's barrier, and only then write.  What later rounds read lies behind
+//     what earlier rounds write, so the next round's rows are on their way meanwhile.
+// Nothing is kept in memory between the steps but the list; rows in front of the
+// first evicted token do not move.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "kcommon.cuh"
+#include "kv.h"
+#include "kvtile.cuh"
+
+namespace attn {
+
+namespace cg = cooperative_groups;
+
+namespace {
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kKeys = 16384;  // candidates of a block whose weights stay in shared memory
+constexpr int kStage = 40960;  // bytes of a round's rows of a block
+
+// A weight as a number whose order is the weights': NaN below all, -0 like 0.
+__device__ __forceinline__ uint32_t order_of(float w) {
+  if (w != w) return 0u;
+  const uint32_t u = __float_as_uint(w + 0.0f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"((uint64_t)__cvta_generic_to_global(src))
+               : "memory");
+}
+
+// Inclusive sum over the block (all threads); `total` is everybody's.
+__device__ __forceinline__ int block_scan(int x, int* s_warp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int y = s_warp[w];
+    if (w < warp) x += y;
+    total += y;
+  }
+  return x;
+}
+}  // namespace
+
+__device__ __forceinline__ int evict_len(const EvictParams& p, int b) {
+  const int n = p.seq_lens[b], most = min(p.cols << p.c.page_shift, p.capacity);
+  if (n >= 0 && n <= most) return n;
+  if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+  return 0;
+}
+// Pages of a sequence that an eviction leaves without tokens: columns from .. to - 1.
+__device__ __forceinline__ int pages_of(const EvictParams& p, int n) { return (n + p.c.page_size - 1) >> p.c.page_shift; }
+__device__ __forceinline__ int pages_gone(const EvictParams& p, int n) {
+  return n > p.keep ? pages_of(p, n) - pages_of(p, p.keep) : 0;
+}
+
+// The new length of sequence b, and its pages for the free list, in front of the
+// pages taken: those of all sequences in order, each one's in order of its columns.
+__device__ void evict_lists(const EvictParams& p, int b, int n, int* s_warp) {
+  if (threadIdx.x == 0) p.seq_out[b] = min(n, p.keep);
+  if (!p.free_head) return;
+  int before = 0, all = 0;
+  for (int i = threadIdx.x; i < p.batch; i += kThreads) {
+    const int g = pages_gone(p, evict_len(p, i));
+    all += g;
+    if (i < b) before += g;
+  }
+  int n_all, n_before;
+  block_scan(all, s_warp, n_all);
+  block_scan(before, s_warp, n_before);
+  const int head = *p.free_head;
+  const bool fits = head >= n_all && head <= p.n_free;
+  if (threadIdx.x == 0 && b == 0) *p.free_head_out = fits ? head - n_all : head;
+  if (!fits) {
+    if (threadIdx.x == 0 && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+    return;
+  }
+  const int32_t* row = p.table + (int64_t)b * p.table_stride;
+  const int from = pages_of(p, p.keep), gone = pages_gone(p, n);
+  for (int i = threadIdx.x; i < gone; i += kThreads) {
+    int page = row[from + i];
+    if ((unsigned)page >= (unsigned)p.c.num_pages) {
+      page = -1;
+      if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+    }
+    p.free_pages[head - n_all + n_before + i] = page;
+  }
+}
+
+template <int DQK, int DV>
+struct EvictShape {
+  static constexpr int kCodes = (DQK + DV) / 2 / 16;   // 16-byte vectors of a row's codes
+  static constexpr int kScales = (DQK + DV) / 32 / 2;  // words of its scales
+  static constexpr int kRow = kCodes * 16 + kScales * 4 + 4;  // and its weight
+  static constexpr int kRows = kStage / kRow / 32 * 32;       // of a block's round
+  static constexpr int kUnion = 2 * kRows * kRow > kKeys * 4 ? 2 * kRows * kRow : kKeys * 4;
+  static constexpr int kSmem = 3 * kBins * 4 + kUnion;
+};
+
+template <int DQK, int DV>
+__global__ void __launch_bounds__(kThreads, 2) attn_kv_evict_kernel(const __grid_constant__ EvictParams p) {
+  using S = EvictShape<DQK, DV>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  int* hist = reinterpret_cast<int*>(smem);                        // [3][kBins]
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + 3 * kBins * 4);  // then the rounds' rows
+  uint8_t* stage = smem + 3 * kBins * 4;
+  __shared__ int s_warp[kWarps], s_bin, s_above;
+  __shared__ int s_count[3];  // of this block's candidates: above the border, on it; the first that goes
+  __shared__ long long s_src[2][S::kRows];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int item = blockIdx.x / C, b = item / p.c.heads, h = item - b * p.c.heads;
+  const int n = evict_len(p, b);
+  if (h == 0 && rank == 0) evict_lists(p, b, n, s_warp);
+  const float* w = p.w + (int64_t)b * p.w_b + (int64_t)h * p.w_h;
+  float* w_out = p.w_out + (int64_t)b * p.wo_b + (int64_t)h * p.wo_h;
+  int32_t* kept = p.kept + ((int64_t)b * p.c.heads + h) * p.keep;
+  const int all = C * kThreads, me = rank * kThreads + tid;
+  if (n <= p.keep) {  // within the budget (the whole cluster)
+    for (int64_t i = me; i < p.keep; i += all) kept[i] = i < n ? (int)i : -1;
+    if (w_out != w)
+      for (int i = me; i < n; i += all) w_out[i] = w[i];
+    return;
+  }
+  const int first = p.first ? min(max(p.first[b], 0), p.keep) : 0;
+  const int recent = min(p.recent, p.keep - first);
+  const int room = p.keep - first - recent;       // for the tokens between
+  const int m = n - first - recent;               // of those (more than room)
+  const int per = ((m + C - 1) / C + 31) & ~31;   // of a block
+  const int c0 = min(rank * per, m), mine = min(m - c0, per);
+  const bool held = per <= kKeys;
+  const float* wc = w + first + c0;
+  auto key = [&](int i) { return held ? keys[i] : order_of(wc[i]); };
+
+  // ---- the border
+  for (int i = tid; i < 3 * kBins; i += kThreads) hist[i] = 0;
+  if (held)
+    for (int i = tid; i < mine; i += kThreads) keys[i] = order_of(wc[i]);
+  __syncthreads();
+  uint32_t border = 0;  // its digits so far
+  int need = room;      // of the candidates that share them
+  constexpr int kShift[3] = {21, 10, 0};
+  constexpr int kDigits[3] = {kBins, kBins, kBins / 2};
+  if (room > 0) {
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      int* mine_h = hist + pass * kBins;
+      for (int i0 = warp * 32; i0 < mine; i0 += kThreads) {
+        const int i = i0 + lane;
+        const uint32_t k = i < mine ? key(i) : 0u;
+        const bool in = i < mine && (pass == 0 || (k >> kShift[pass - 1]) == (border >> kShift[pass - 1]));
+        const int d = in ? (int)((k >> kShift[pass]) & (kDigits[pass] - 1)) : -1;
+        // equal digits of a warp are counted together: weights of one size share the first
+        const unsigned same = __match_any_sync(0xffffffffu, d);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&mine_h[d], __popc(same));
+      }
+      cluster.sync();
+      // every block adds up all blocks' counts; thread t takes digits from the top on
+      constexpr int kEach = kBins / kThreads;
+      const int each = kDigits[pass] / kThreads;
+      int cnt[kEach], sum = 0;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        cnt[j] = 0;
+        if (j < each) {
+          const int d = kDigits[pass] - 1 - (tid * each + j);
+          for (int q = 0; q < C; ++q) cnt[j] += cluster.map_shared_rank(mine_h, q)[d];
+          sum += cnt[j];
+        }
+      }
+      int total;
+      int above = block_scan(sum, s_warp, total) - sum;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j)
+        if (j < each) {
+          if (above < need && above + cnt[j] >= need) s_bin = kDigits[pass] - 1 - (tid * each + j), s_above = above;
+          above += cnt[j];
+        }
+      __syncthreads();
+      border |= (uint32_t)s_bin << kShift[pass];
+      need -= s_above;
+      __syncthreads();
+    }
+  } else {
+    border = 0xffffffffu;  // (no weight's number)
+  }
+  // ---- the list: `need` of the candidates on the border stay
+  int above = 0, on = 0;
+  for (int i = tid; i < mine; i += kThreads) {
+    const uint32_t k = key(i);
+    above += k > border;
+    on += k == border;
+  }
+  int t_above, t_on;
+  block_scan(above, s_warp, t_above);
+  block_scan(on, s_warp, t_on);
+  if (tid == 0) s_count[0] = t_above, s_count[1] = t_on;
+  cluster.sync();
+  int to = first, on_before = 0;
+  for (int q = 0; q < rank; ++q) {
+    const int* s = cluster.map_shared_rank(s_count, q);
+    to += s[0] + min(max(need - on_before, 0), s[1]);
+    on_before += s[1];
+  }
+  int gone = INT32_MAX;  // the first that goes, of this thread's
+  for (int i0 = 0; i0 < mine; i0 += kThreads) {
+    const int i = i0 + tid;
+    const uint32_t k = i < mine ? key(i) : 0u;
+    const bool is_on = i < mine && k == border;
+    int n_on, n_stay;
+    const int nth = on_before + block_scan(is_on, s_warp, n_on);
+    const bool stay = i < mine && (k > border || (is_on && nth <= need));
+    const int at = to + block_scan(stay, s_warp, n_stay);
+    if (stay) kept[at - 1] = first + c0 + i;
+    if (i < mine && !stay) gone = min(gone, first + c0 + i);
+    to += n_stay;
+    on_before += n_on;
+  }
+  for (int i = me; i < first; i += all) kept[i] = i;
+  for (int i = me; i < recent; i += all) kept[p.keep - recent + i] = n - recent + i;
+  gone = (int)__reduce_min_sync(0xffffffffu, (unsigned)gone);
+  __syncthreads();
+  if (lane == 0) s_warp[warp] = gone;
+  __syncthreads();
+  if (tid == 0) {
+    for (int i = 1; i < kWarps; ++i) gone = min(gone, s_warp[i]);
+    s_count[2] = gone;
+  }
+  cluster.sync();  // (the list too)
+  int start = INT32_MAX;  // rows in front of it stay where they are
+  for (int q = 0; q < C; ++q) start = min(start, cluster.map_shared_rank(s_count, q)[2]);
+  start = min(start, p.keep);
+
+  // ---- the rows
+  const bool apart = w_out != w;
+  if (apart)
+    for (int i = me; i < start; i += all) w_out[i] = w[i];
+  const int32_t* row = p.table + (int64_t)b * p.table_stride;
+  auto slot_row = [&](int t) -> long long {  // of the cache's rows; -1: a page outside it
+    const int page = row[t >> p.c.page_shift];
+    if ((unsigned)page >= (unsigned)p.c.num_pages) {
+      if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+      return -1;
+    }
+    return ((long long)page * p.c.heads + h) * p.c.page_size + (t & (p.c.page_size - 1));
+  };
+  // a row in shared memory, vector by vector over the round's rows: K's codes, V's,
+  // K's scales, V's, the weight
+  constexpr int kVk = DQK / 32, kSk = DQK / 64;
+  auto load = [&](int base, int buf) {
+    const int rows = min(p.keep - base, S::kRows);
+    uint8_t* st = stage + buf * (S::kRows * S::kRow);
+    for (int i = tid; i < rows; i += kThreads) {
+      const int src = __ldcg(kept + base + i);
+      s_src[buf][i] = slot_row(src);
+      copy4(smem_u32(st + S::kRows * (S::kRow - 4) + i * 4), w + src);
+    }
+    __syncthreads();
+    for (int j = tid; j < rows * S::kCodes; j += kThreads) {
+      const int i = j / S::kCodes, u = j - i * S::kCodes;
+      const long long at = s_src[buf][i];
+      if (at < 0) continue;
+      const uint8_t* src = u < kVk ? p.c.k_codes + at * (DQK / 2) + u * 16 : p.c.v_codes + at * (DV / 2) + (u - kVk) * 16;
+      copy16(smem_u32(st + j * 16), src);
+    }
+    for (int j = tid; j < rows * S::kScales; j += kThreads) {
+      const int i = j / S::kScales, u = j - i * S::kScales;
+      const long long at = s_src[buf][i];
+      if (at < 0) continue;
+      const uint16_t* src = u < kSk ? p.c.k_scales + at * (DQK / 32) + u * 2 : p.c.v_scales + at * (DV / 32) + (u - kSk) * 2;
+      copy4(smem_u32(st + S::kRows * S::kCodes * 16 + j * 4), src);
+    }
+  };
+  auto store = [&](int base, int buf) {
+    const int rows = min(p.keep - base, S::kRows);
+    const uint8_t* st = stage + buf * (S::kRows * S::kRow);
+    for (int j = tid; j < rows * S::kCodes; j += kThreads) {
+      const int i = j / S::kCodes, u = j - i * S::kCodes;
+      const long long at = s_src[buf][i] < 0 ? -1 : slot_row(base + i);
+      if (at < 0) continue;
+      uint8_t* dst = u < kVk ? p.c.k_codes + at * (DQK / 2) + u * 16 : p.c.v_codes + at * (DV / 2) + (u - kVk) * 16;
+      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(st + j * 16);
+    }
+    for (int j = tid; j < rows * S::kScales; j += kThreads) {
+      const int i = j / S::kScales, u = j - i * S::kScales;
+      const long long at = s_src[buf][i] < 0 ? -1 : slot_row(base + i);
+      if (at < 0) continue;
+      uint16_t* dst = u < kSk ? p.c.k_scales + at * (DQK / 32) + u * 2 : p.c.v_scales + at * (DV / 32) + (u - kSk) * 2;
+      *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(st + S::kRows * S::kCodes * 16 + j * 4);
+    }
+    for (int i = tid; i < rows; i += kThreads)
+      w_out[base + i] = *reinterpret_cast<const float*>(st + S::kRows * (S::kRow - 4) + i * 4);
+  };
+  // (a cluster's blocks all take part in every round's barrier, with rows or without)
+  const int step = C * S::kRows;
+  int base = start + rank * S::kRows;
+  if (base < p.keep) load(base, 0);
+  copies_end();
+  for (int round = start, buf = 0; round < p.keep; round += step, base += step, buf ^= 1) {
+    if (base + step < p.keep) load(base + step, buf ^ 1);
+    copies_end();
+    copies_wait<1>();
+    cluster.sync();
+    if (base < p.keep) store(base, buf);
+    __syncthreads();
+  }
+  copies_wait<0>();
+  cluster.sync();  // (no block leaves while others may read its counts)
+}
+
+namespace {
+template <int DQK, int DV>
+cudaError_t evict_launch(const EvictParams& p, int num_sms, cudaStream_t st) {
+  using S = EvictShape<DQK, DV>;
+  auto* k = attn_kv_evict_kernel<DQK, DV>;
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
+  // as large a cluster as leaves all of them on the card at once
+  const int64_t items = (int64_t)p.batch * p.c.heads;
+  int c = kMaxCluster;
+  while (c > 1 && items * c > 2 * num_sms) c /= 2;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)c;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * c));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, p);
+}
+}  // namespace
+
+cudaError_t launch_kv4_evict(const EvictParams& p, int num_sms, cudaStream_t st) {
+  if (p.c.d_qk == 64 && p.c.d_v == 64) return evict_launch<64, 64>(p, num_sms, st);
+  if (p.c.d_qk == 128 && p.c.d_v == 128) return evict_launch<128, 128>(p, num_sms, st);
+  if (p.c.d_qk == 192 && p.c.d_v == 128) return evict_launch<192, 128>(p, num_sms, st);
+  if (p.c.d_qk == 256 && p.c.d_v == 256) return evict_launch<256, 256>(p, num_sms, st);
+  return cudaErrorNotSupported;
+}
+
+}  // namespace attn

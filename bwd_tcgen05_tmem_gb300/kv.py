@@ -23,8 +23,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .attn import (_CODES, _DECODE_PACK, _PLAN_PACK, Kv4CacheDesc, _sized, check_buffers, fast,
-                   launch, new, on_device)
+from .attn import (_CODES, _DECODE_PACK, _EVICT_PACK, _PLAN_PACK, _WEIGHTS_PACK, Kv4CacheDesc,
+                   _sized, check_buffers, fast, launch, new, on_device)
 
 _STRIDES_PACK = struct.Struct("@2q").pack
 _I32 = torch.int32
@@ -217,3 +217,105 @@ def decode_workspace_size(q, cache, block_table, *, o_dtype=None):
     p = _DECODE_PACK(_CODES[q.dtype], _CODES[o_dtype or q.dtype], b, sq, hq, 0, 0, 0, 0, 0, 0, cols,
                      row, -1, 0, 1.0 / math.sqrt(d))
     return _sized(on_device(q), fast().attn_kv_decode_workspace_size, p, cache._desc)
+
+
+def _weight_rows(name, t, batch, heads):
+    """(capacity, {batch, head} strides) of attention weights."""
+    if t.dim() != 3 or t.shape[:2] != (batch, heads) or t.dtype != torch.float32:
+        raise ValueError(f"{name} must be float32 {[batch, heads, 'capacity']}, not {t.dtype} {tuple(t.shape)}")
+    s = t.stride()
+    if s[2] != 1 and t.shape[2] > 1:
+        raise ValueError(f"rows of {name} must be contiguous")
+    return t.shape[2], s[:2]
+
+
+def kv4_weights(q, cache, block_table, seq_lens, lse, weights, *, scale=None, window_left=-1, sinks=0,
+                accumulate=True, status=None, stream=None):
+    """Adds the attention weights that the last q.shape[1] tokens of each sequence
+    give its cached tokens to ``weights`` (attn_kv_weights); returns that.
+
+    q, scale, window_left, sinks: as given to kv4_decode, whose ``lse`` this takes.
+    weights: float32 [B, heads_kv, capacity]; entries of the newest q.shape[1] tokens
+    are set, older ones added to (``accumulate=False``: all are set)."""
+    check_buffers(status)
+    lib = fast()
+    dev = on_device(cache.k_codes, q, block_table, seq_lens, lse, weights, status)
+    b, sq, hq, d = q.shape
+    s0, s1, s2, s3 = q.stride()
+    if d != cache.d_qk:
+        raise ValueError(f"q has head dim {d}, the cache {cache.d_qk}")
+    if s3 != 1:
+        raise ValueError("the head-dim axis must be contiguous")
+    if q.dtype not in _CODES:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    _ints("seq_lens", seq_lens, b)
+    cols, row = _table(block_table, b)
+    if lse.shape != (b, hq, sq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [B, Hq, Sq]")
+    cap, (w0, w1) = _weight_rows("weights", weights, b, cache.heads_kv)
+    p = _WEIGHTS_PACK(_CODES[q.dtype], b, sq, hq, s0, s1, s2, cols, row, window_left, sinks,
+                      1.0 / math.sqrt(d) if scale is None else scale, bool(accumulate), cap, w0, w1)
+    launch(dev, stream, lib.attn_kv_weights, p, cache._desc, q.data_ptr(), block_table.data_ptr(),
+           seq_lens.data_ptr(), lse.data_ptr(), weights.data_ptr(),
+           None if status is None else status.data_ptr())
+    return weights
+
+
+class Evicted(NamedTuple):
+    seq_lens: torch.Tensor     # int32 [batch], tokens held now
+    weights: torch.Tensor      # float32 [batch, heads_kv, capacity], moved with their tokens
+    kept: torch.Tensor         # int32 [batch, heads_kv, keep]: the row that each row was; -1 past the last
+    free_head: Optional[torch.Tensor]  # int32 [1], the next free page
+
+
+def kv4_evict(cache, block_table, seq_lens, weights, *, keep, first=None, recent=0, weights_out=None, kept=None,
+              seq_lens_out=None, free_pages=None, free_head=None, free_head_out=None, status=None, stream=None):
+    """Cuts each sequence of more than ``keep`` tokens down to that many, each kv head
+    by itself: the first first[b], the last ``recent`` and of the others those with the
+    largest weight; the cache's rows move together in their order (attn_kv_evict).
+    Returns an Evicted.
+
+    weights: float32 [B, heads_kv, capacity], changed in place unless ``weights_out``
+    is given.  first: int32 [B] or None.  free_pages and free_head (as kv.plan takes
+    them): pages that are left over are put in front of free_head."""
+    check_buffers(status)
+    lib = fast()
+    b = seq_lens.shape[0]
+    dev = on_device(cache.k_codes, block_table, seq_lens, weights, first, weights_out, kept, seq_lens_out,
+                    free_pages, free_head, free_head_out, status)
+    _ints("seq_lens", seq_lens, b)
+    cols, row = _table(block_table, b)
+    if first is not None:
+        _ints("first", first, b)
+    h = cache.heads_kv
+    cap, strides = _weight_rows("weights", weights, b, h)
+    if weights_out is None:
+        weights_out = weights
+    cap_out, strides_out = _weight_rows("weights_out", weights_out, b, h)
+    if cap_out != cap:
+        raise ValueError("weights and weights_out differ in shape")
+    if (free_pages is None) != (free_head is None):
+        raise ValueError("free_pages and free_head must both be given or None")
+    n_free = 0
+    if free_head is not None:
+        n_free = free_pages.numel()
+        _ints("free_pages", free_pages, n_free)
+        _ints("free_head", free_head, 1)
+        if free_head_out is None:
+            free_head_out = new((1,), _I32, dev, stream)
+        _ints("free_head_out", free_head_out, 1)
+    elif free_head_out is not None:
+        raise ValueError("free_head_out without free_head")
+    if kept is None:
+        kept = new((b, h, keep), _I32, dev, stream)
+    elif kept.shape != (b, h, keep) or kept.dtype != _I32 or not kept.is_contiguous():
+        raise ValueError("kept must be contiguous int32 [B, heads_kv, keep]")
+    if seq_lens_out is None:
+        seq_lens_out = new((b,), _I32, dev, stream)
+    _ints("seq_lens_out", seq_lens_out, b)
+    launch(dev, stream, lib.attn_kv_evict, _EVICT_PACK(b, cols, row, keep, recent, cap, *strides, *strides_out, n_free),
+           cache._desc, block_table.data_ptr(), seq_lens.data_ptr(), None if first is None else first.data_ptr(),
+           weights.data_ptr(), weights_out.data_ptr(), kept.data_ptr(), seq_lens_out.data_ptr(),
+           None if free_head is None else free_pages.data_ptr(), None if free_head is None else free_head.data_ptr(),
+           None if free_head is None else free_head_out.data_ptr(), None if status is None else status.data_ptr())
+    return Evicted(seq_lens_out, weights_out, kept, free_head_out)

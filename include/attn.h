@@ -1,7 +1,8 @@
 /*
  * attn.h -- C ABI of libattn.so: fused causal scaled-dot-product attention
  * (forward, backward, LSE merge), the norm and rotation of its queries and
- * keys, and attention over a paged 4-bit cache, for NVIDIA GB300 (sm_103a).
+ * keys, and attention over a paged 4-bit cache (shared prefixes, eviction), for
+ * NVIDIA GB300 (sm_103a).
  *
  * Sources for the operations (web pages on Blackwell attention backends):
  *  - TransformerEngine PR #3527, "cuDNN FROST attention backend for head_dim in
@@ -521,6 +522,85 @@ attn_status_t attn_kv_decode(const attn_kv4_decode_params_t* p, const attn_kv4_c
                               const void* q, const int32_t* block_table,
                               const int32_t* seq_lens, void* o, float* lse, void* workspace,
                               size_t workspace_bytes, int32_t* status, attn_stream_t stream);
+
+/*
+ * The attention weights that cached tokens receive from the last seqlen_q tokens of
+ * each sequence, from the log-sum-exp of those tokens' attention over this cache (lse
+ * as attn_kv_decode writes it, with the same scale, window and first tokens):
+ *     weights[b][h][j] (+)= sum over i < seqlen_q and the query heads a of kv head h
+ *                           of exp(softmax_scale q[b][i][a] k[b][h][j] - lse[b][a][i])
+ * over the queries i that see token j.  FP32, tokens contiguous, {batch, head} strides
+ * stride_w, `capacity` entries a row.  accumulate = 1: entries of tokens that were
+ * there before (j < seq_lens[b] - seqlen_q) are added to, those of the seqlen_q
+ * newest are set; entries of tokens that no query sees stay.  accumulate = 0: the
+ * entries of all seq_lens[b] tokens are set.  Entries from seq_lens[b] on are not
+ * touched.  What table entries and page contents are not looked at, is as in
+ * attn_kv_decode.  Scores are those of attn_kv_decode, to rounding; sums are FP32 in
+ * an order that does not depend on the other sequences: bitwise reproducible.
+ * seq_lens out of [0, min(cols * page_size, capacity)] count as 0 and set the status
+ * word; so does a page outside the cache that holds a visible token (that sequence's
+ * entries are then undefined).
+ */
+typedef struct {
+  attn_dtype_t dtype;    /* q: BF16 or FP16 */
+  int batch, seqlen_q, heads_q;  /* as in attn_kv_decode */
+  int64_t stride_q[3];   /* {batch, token, head} */
+  int cols;
+  int64_t table_stride;
+  int window_left, sinks;
+  float softmax_scale;
+  int accumulate;
+  int capacity;          /* entries of a row of weights */
+  int64_t stride_w[2];   /* {batch, head}, in elements; rows must not overlap */
+} attn_kv4_weights_params_t;
+attn_status_t attn_kv_weights(const attn_kv4_weights_params_t* p, const attn_kv4_cache_t* cache,
+                              const void* q, const int32_t* block_table, const int32_t* seq_lens,
+                              const float* lse, float* weights, int32_t* status,
+                              attn_stream_t stream);
+
+/*
+ * Eviction: each sequence of more than `keep` tokens is cut down to that many, each kv
+ * head by itself.  Of n = seq_lens[b] tokens there stay the first f = min(first[b],
+ * keep) (first NULL: none), the last r = min(recent, keep - f) and, of those
+ * between, the keep - f - r with the largest weight; of equal ones those with the lower
+ * index; NaN lies below all numbers.  They keep their order: row i of a kept sequence
+ * is what row kept[b][h][i] was, codes, scales and weight.
+ *     kept         int32 [batch][heads_kv][keep], contiguous; -1 past the tokens held
+ *     seq_lens_out int32 [batch]: min(seq_lens, keep)
+ *     weights_out  FP32, strides {batch, head} stride_wo; may be `weights` itself (same
+ *                  strides).  Entries past the tokens held are not touched.
+ * The keys of the cache are rotated already, so attention over what stays is attention
+ * over those tokens; positions of later tokens are the caller's (plan's, plus what was
+ * evicted).  Rows in front of the first evicted token are not written: a prefix that
+ * other sequences share may stay in front under `first`.  Pages that hold other tokens
+ * of an evicted sequence must be its own.
+ * With free_head the pages past ceil(keep / page_size) go back to the list that
+ * attn_kv_plan takes from: with g of them in all, free_pages[free_head[0] - g ..
+ * free_head[0]) is written, sequence after sequence, and free_head_out[0] =
+ * free_head[0] - g.  If there are not g entries in front of free_head[0], or that lies
+ * past n_free, no page is given back, free_head_out[0] = free_head[0] and the status word
+ * is set.  A page outside the cache is given back as -1 and sets the status word, as one
+ * that holds a row to move does (that row then stays).  free_head NULL: free_pages and
+ * free_head_out are ignored.
+ * block_table is not changed: its entries past the tokens held are not looked at by
+ * the other calls, and attn_kv_plan writes them again.
+ * seq_lens out of [0, min(cols * page_size, capacity)] count as 0 and set the status
+ * word.  Nothing depends on the order in which blocks run.
+ */
+typedef struct {
+  int batch, cols;
+  int64_t table_stride;
+  int keep, recent;      /* keep >= 1, recent >= 0 */
+  int capacity;          /* entries of a row of weights and weights_out */
+  int64_t stride_w[2], stride_wo[2];
+  int n_free;            /* entries of free_pages */
+} attn_kv4_evict_params_t;
+attn_status_t attn_kv_evict(const attn_kv4_evict_params_t* p, const attn_kv4_cache_t* cache,
+                            const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* first, const float* weights, float* weights_out,
+                            int32_t* kept, int32_t* seq_lens_out, int32_t* free_pages,
+                            const int32_t* free_head, int32_t* free_head_out, int32_t* status,
+                            attn_stream_t stream);
 
 /* Synchronises `stream` and returns the status word in `workspace`
  * (ATTN_OK, ATTN_ERR_BAD_METADATA, ATTN_ERR_TIMEOUT or, for the head-dim-512
