@@ -36,7 +36,8 @@ EXPORTED = ["attn_fwd_workspace_size", "attn_bwd_workspace_size", "attn_fwd", "a
             "attn_fwd_bwd_host_stages", "attn_bwd_path",
             "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_size",
             "attn_kv_plan", "attn_kv_write", "attn_kv_read", "attn_kv_decode",
-            "attn_kv_decode_workspace_size", "attn_kv_weights", "attn_kv_evict"]
+            "attn_kv_decode_workspace_size", "attn_kv_decode_shared",
+            "attn_kv_decode_shared_workspace_size", "attn_kv_weights", "attn_kv_evict"]
 # attn_fwd_bwd_host_stages stage bits
 HOST_UPLOAD, HOST_COMPUTE, HOST_DOWNLOAD, HOST_ALL = 1, 2, 4, 7
 # attn_bwd_path results: which backward kernels run (and the stage order)
@@ -211,6 +212,10 @@ def load():
         lib.attn_kv_decode_workspace_size.restype = sz
         lib.attn_kv_decode.argtypes = [D, C] + [vp] * 6 + [sz, vp, vp]
         lib.attn_kv_decode.restype = ctypes.c_int
+        lib.attn_kv_decode_shared_workspace_size.argtypes = [D, C, ctypes.c_int]
+        lib.attn_kv_decode_shared_workspace_size.restype = sz
+        lib.attn_kv_decode_shared.argtypes = [D, C, ctypes.c_int] + [vp] * 8 + [sz, vp, vp]
+        lib.attn_kv_decode_shared.restype = ctypes.c_int
         lib.attn_kv_weights.argtypes = [ctypes.POINTER(Kv4WeightsParams), C] + [vp] * 7
         lib.attn_kv_weights.restype = ctypes.c_int
         lib.attn_kv_evict.argtypes = [ctypes.POINTER(Kv4EvictParams), C] + [vp] * 12
@@ -240,11 +245,13 @@ def _fast_handle():
                        ("attn_kv_write", [vp, ci, ci] + [vp] * 7),
                        ("attn_kv_read", [vp, ci, ci] + [vp] * 7),
                        ("attn_kv_decode", [vp] * 8 + [sz, vp, vp]),
+                       ("attn_kv_decode_shared", [vp, vp, ci] + [vp] * 8 + [sz, vp, vp]),
                        ("attn_kv_weights", [vp] * 9), ("attn_kv_evict", [vp] * 14)):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, ctypes.c_int
     for name, args in (("attn_qk_norm_rope_bwd_workspace_size", [vp]),
-                       ("attn_kv_decode_workspace_size", [vp, vp])):
+                       ("attn_kv_decode_workspace_size", [vp, vp]),
+                       ("attn_kv_decode_shared_workspace_size", [vp, vp, ci])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, sz
     return lib

@@ -91,6 +91,7 @@ struct DecodeParams {
   void* o;
   float* lse;  // [batch][heads_q][seqlen_q]
   const int32_t *table, *seq_lens;
+  const int32_t* starts;  // null, or per sequence the first token to look at (a multiple of 64, below its length)
   int64_t q_b, q_t, q_h, o_b, o_t, o_h, table_stride;
   int batch, seqlen_q, heads_q, group, cols, window_left, sinks;
   int rows, row_blocks;  // query rows of a kv head (seqlen_q * group), and blocks of them
@@ -108,6 +109,33 @@ int decode_blocks(const DecodeParams& p, int num_sms);
 size_t decode_runs(int blocks);
 size_t decode_partial_floats(int blocks, int rows_per_block, int d_v);
 cudaError_t launch_kv4_decode(const DecodeParams& p, bool bf16, int blocks, cudaStream_t st);
+
+struct SharedParams {  // attention of batches whose requests share their first tokens
+  Kv4 c;
+  const void* q;
+  void* o;
+  float* lse;  // [batch][heads_q][seqlen_q]
+  const int32_t *table, *seq_lens, *group_starts, *shared_lens;
+  int64_t q_b, q_t, q_h, o_b, o_t, o_h, table_stride;
+  int batch, seqlen_q, heads_q, group, cols, groups;
+  int rows;                    // query rows of a request and kv head (seqlen_q * group)
+  int row_tile, key_tile;      // shared_tiles()
+  FastDiv by_group, by_rows;
+  float scale_log2;
+  int o_f32;
+  // workspace
+  void* group_info;            // [groups] (shared_group_bytes() each)
+  long long* total_units;
+  int32_t *starts, *group_of;  // [batch]: tokens of the shared prefix, and whose
+  float *own_o, *own_lse;      // of each request's own tokens, FP32, like o and lse, contiguous
+  float *row_o, *row_ml;       // parts of items that one run finished: [2][batch][heads][rows][d_v], [..][2]
+  float *cut_o, *cut_ml;       // parts of the others: [num_sms][2][row_tile][d_v], [..][2]
+  int* status;
+};
+void shared_tiles(int d_v, int& row_tile, int& key_tile);
+size_t shared_group_bytes();
+cudaError_t launch_kv4_shared_prefix(const SharedParams& p, bool bf16, int num_sms, cudaStream_t st);
+cudaError_t launch_kv4_shared_join(const SharedParams& p, bool bf16, int num_sms, cudaStream_t st);
 
 struct WeightsParams {
   Kv4 c;

@@ -1,6 +1,6 @@
 // kvapi.cu -- C entry points of the operators around the attention kernels:
 // attn_qk_norm_rope (and its gradient), attn_kv_plan, attn_kv_write / _read,
-// attn_kv_decode, attn_kv_weights and attn_kv_evict.  Host-side checks and dispatch; nothing is allocated.
+// attn_kv_decode, attn_kv_decode_shared, attn_kv_weights and attn_kv_evict.  Host-side checks and dispatch; nothing is allocated.
 #include <cmath>
 #include <cstring>
 
@@ -834,6 +834,166 @@ attn_status_t attn_kv_evict(const attn_kv4_evict_params_t* p, const attn_kv4_cac
   kp.n_free = free_head ? p->n_free : 0;
   kp.status = status;
   return api_launched(attn::launch_kv4_evict(kp, attn::num_sms(), (cudaStream_t)stream), 1, "eviction launch");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ shared prefixes
+namespace {
+
+attn_status_t check_shared(const attn_kv4_decode_params_t* p, const attn_kv4_cache_t* c, int groups,
+                           attn::DecodeParams& kp) {
+  attn_status_t s = check_decode(p, c, kp);
+  if (s) return s;
+  if (p->window_left != -1)
+    return api_fail(ATTN_ERR_UNSUPPORTED, "a window: use attn_kv_decode, which reads what the window shows");
+  if (groups < 0) return api_fail(ATTN_ERR_INVALID_ARG, "groups < 0");
+  if (groups > p->batch) return api_fail(ATTN_ERR_INVALID_ARG, "more groups than requests");
+  kp.sinks = 0;
+  return ATTN_OK;
+}
+
+// [attn_kv_decode's][groups][units][two ints a request][own O, LSE][parts of whole items][of cut ones]
+struct SharedLayout {
+  size_t groups, units, starts, group_of, own_o, own_lse, row_o, row_ml, cut_o, cut_ml, total;
+};
+SharedLayout shared_layout(const attn::DecodeParams& kp, int groups, const DecodeLayout& d) {
+  SharedLayout l;
+  int row_tile, key_tile;
+  attn::shared_tiles(kp.c.d_v, row_tile, key_tile);
+  const size_t rows = (size_t)kp.batch * kp.c.heads * kp.rows, cut = (size_t)attn::num_sms() * 2 * row_tile;
+  size_t at = up256(d.total);
+  auto take = [&](size_t bytes) {
+    const size_t x = at;
+    at += up256(bytes);
+    return x;
+  };
+  l.groups = take((size_t)groups * attn::shared_group_bytes());
+  l.units = take(8);
+  l.starts = take((size_t)kp.batch * 4);
+  l.group_of = take((size_t)kp.batch * 4);
+  l.own_o = take(rows * kp.c.d_v * 4);
+  l.own_lse = take(rows * 4);
+  l.row_o = take(2 * rows * kp.c.d_v * 4);
+  l.row_ml = take(2 * rows * 8);
+  l.cut_o = take(cut * kp.c.d_v * 4);
+  l.cut_ml = take(cut * 8);
+  l.total = at;
+  return l;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t attn_kv_decode_shared_workspace_size(const attn_kv4_decode_params_t* p, const attn_kv4_cache_t* cache,
+                                            int groups) {
+  attn::DecodeParams kp;
+  if (check_shared(p, cache, groups, kp)) return 256;
+  return shared_layout(kp, groups, decode_layout(kp)).total;
+}
+
+attn_status_t attn_kv_decode_shared(const attn_kv4_decode_params_t* p, const attn_kv4_cache_t* cache, int groups,
+                                    const int32_t* group_starts, const int32_t* shared_lens, const void* q,
+                                    const int32_t* block_table, const int32_t* seq_lens, void* o, float* lse,
+                                    void* ws, size_t ws_bytes, int32_t* status, attn_stream_t stream) {
+  api_begin();
+  attn::DecodeParams dp;
+  attn_status_t s = check_shared(p, cache, groups, dp);
+  if (s) return s;
+  if ((s = check_status_word(status))) return s;
+  const DecodeLayout dl = decode_layout(dp);
+  const SharedLayout l = shared_layout(dp, groups, dl);
+  if ((s = check_workspace(ws, ws_bytes, l.total))) return s;
+  if (p->batch == 0 || p->seqlen_q == 0) return ATTN_OK;
+  const int oe = dp.o_f32 ? 4 : 2;
+  if ((s = check_rows("q", q, p->stride_q, p->batch, p->seqlen_q, p->heads_q, cache->d_qk, 2, false)) ||
+      (s = check_rows("o", o, p->stride_o, p->batch, p->seqlen_q, p->heads_q, cache->d_v, oe, true)) ||
+      (s = check_ints("lse", lse)) || (s = check_ints("seq_lens", seq_lens)) ||
+      (p->cols && (s = check_ints("block_table", block_table))) ||
+      (groups && ((s = check_ints("group_starts", group_starts)) || (s = check_ints("shared_lens", shared_lens)))))
+    return s;
+  Region held[4];
+  cache_regions(cache, held);
+  const Region in[9] = {held[0], held[1], held[2], held[3],
+                        region_of(q, p->stride_q, p->batch, p->seqlen_q, p->heads_q, cache->d_qk, 2),
+                        table_region(block_table, p->batch, p->cols, p->table_stride), flat(seq_lens, p->batch * 4ll),
+                        flat(group_starts, groups ? (groups + 1) * 4ll : 0), flat(shared_lens, groups * 4ll)};
+  const Region out[4] = {region_of(o, p->stride_o, p->batch, p->seqlen_q, p->heads_q, cache->d_v, oe),
+                         flat(lse, (int64_t)p->batch * p->heads_q * p->seqlen_q * 4), flat(ws, (int64_t)l.total),
+                         flat(status, status ? 4 : 0)};
+  for (int i = 0; i < 4; ++i) {
+    for (const Region& r : in)
+      if (regions_overlap(out[i], r))
+        return api_fail(ATTN_ERR_INVALID_ARG, "an output or the workspace overlaps an input");
+    for (int j = i + 1; j < 4; ++j)
+      if (regions_overlap(out[i], out[j])) return api_fail(ATTN_ERR_INVALID_ARG, "outputs overlap");
+  }
+  char* const w = (char*)ws;
+  dp.q = q;
+  dp.o = o;
+  dp.lse = lse;
+  dp.table = block_table;
+  dp.seq_lens = seq_lens;
+  dp.q_b = p->stride_q[0], dp.q_t = p->stride_q[1], dp.q_h = p->stride_q[2];
+  dp.o_b = p->stride_o[0], dp.o_t = p->stride_o[1], dp.o_h = p->stride_o[2];
+  dp.info = (int*)w;
+  dp.ends = (int*)(w + dl.ends);
+  dp.partial = (float*)(w + dl.partial);
+  dp.status = status;
+  const bool bf16 = p->dtype == ATTN_BF16;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (groups == 0)  // nobody shares anything
+    return api_launched(attn::launch_kv4_decode(dp, bf16, dl.blocks, st), 2, "cache attention launch");
+  attn::SharedParams kp;
+  memset(&kp, 0, sizeof(kp));
+  kp.c = dp.c;
+  kp.q = q;
+  kp.o = o;
+  kp.lse = lse;
+  kp.table = block_table;
+  kp.seq_lens = seq_lens;
+  kp.group_starts = group_starts;
+  kp.shared_lens = shared_lens;
+  kp.q_b = dp.q_b, kp.q_t = dp.q_t, kp.q_h = dp.q_h;
+  kp.o_b = dp.o_b, kp.o_t = dp.o_t, kp.o_h = dp.o_h;
+  kp.table_stride = p->table_stride;
+  kp.batch = p->batch;
+  kp.seqlen_q = p->seqlen_q;
+  kp.heads_q = p->heads_q;
+  kp.group = dp.group;
+  kp.cols = p->cols;
+  kp.groups = groups;
+  kp.rows = dp.rows;
+  attn::shared_tiles(cache->d_v, kp.row_tile, kp.key_tile);
+  kp.by_group = dp.by_group;
+  kp.by_rows = attn::FastDiv::of((uint32_t)dp.rows);
+  kp.scale_log2 = dp.scale_log2;
+  kp.o_f32 = dp.o_f32;
+  kp.group_info = w + l.groups;
+  kp.total_units = (long long*)(w + l.units);
+  kp.starts = (int32_t*)(w + l.starts);
+  kp.group_of = (int32_t*)(w + l.group_of);
+  kp.own_o = (float*)(w + l.own_o);
+  kp.own_lse = (float*)(w + l.own_lse);
+  kp.row_o = (float*)(w + l.row_o);
+  kp.row_ml = (float*)(w + l.row_ml);
+  kp.cut_o = (float*)(w + l.cut_o);
+  kp.cut_ml = (float*)(w + l.cut_ml);
+  kp.status = status;
+  // the requests' own tokens: into the workspace, in FP32
+  dp.o = kp.own_o;
+  dp.lse = kp.own_lse;
+  dp.o_f32 = 1;
+  dp.o_h = cache->d_v;
+  dp.o_t = (int64_t)p->heads_q * cache->d_v;
+  dp.o_b = dp.o_t * p->seqlen_q;
+  dp.starts = kp.starts;
+  const int sms = attn::num_sms();
+  if ((s = api_launched(attn::launch_kv4_shared_prefix(kp, bf16, sms, st), 2, "shared prefix launch")) ||
+      (s = api_launched(attn::launch_kv4_decode(dp, bf16, dl.blocks, st), 2, "cache attention launch")))
+    return s;
+  return api_launched(attn::launch_kv4_shared_join(kp, bf16, sms, st), 1, "shared prefix join launch");
 }
 
 }  // extern "C"

@@ -120,6 +120,7 @@ __device__ __forceinline__ SeqRange seq_range(const DecodeParams& p, int b) {
   // the first query's window starts at len - seqlen_q - window_left
   const int64_t w = p.window_left < 0 ? 0 : (int64_t)s.len - p.seqlen_q - p.window_left;
   s.lo = w > 0 ? (int)(w / kTile) : 0;
+  if (p.starts) s.lo = min(p.starts[b], s.len) / kTile;  // (a call without window and first tokens)
   const int sink_tiles = (int)(((int64_t)p.sinks + kTile - 1) / kTile);
   s.n_sink = min(sink_tiles, s.lo);
   s.tiles = s.n_sink + (s.len + kTile - 1) / kTile - s.lo;

@@ -169,15 +169,8 @@ def kv4_read(cache, slots, *, dtype=torch.bfloat16, k=None, v=None, status=None,
     return k, v
 
 
-def kv4_decode(q, cache, block_table, seq_lens, *, scale=None, window_left=-1, sinks=0, out=None,
-               lse=None, o_dtype=None, workspace=None, status=None, stream=None):
-    """Attention of the last q.shape[1] tokens of each sequence over the cache
-    (attn_kv_decode).  q [B, Sq, Hq, d_qk]; block_table int32 [B, cols];
-    seq_lens int32 [B], the new tokens among them.  Returns (o [B, Sq, Hq, d_v],
-    lse float32 [B, Hq, Sq])."""
-    check_buffers(status, workspace)
-    lib = fast()
-    dev = on_device(cache.k_codes, q, block_table, seq_lens, out, lse, workspace, status)
+def _decode_pack(q, cache, block_table, seq_lens, scale, window_left, sinks, out, lse, o_dtype, dev, stream):
+    """(out, lse, packed parameters) of attention over the cache."""
     b, sq, hq, d = q.shape
     s0, s1, s2, s3 = q.stride()
     if d != cache.d_qk:
@@ -199,8 +192,21 @@ def kv4_decode(q, cache, block_table, seq_lens, *, scale=None, window_left=-1, s
         raise ValueError("lse must be contiguous float32 [B, Hq, Sq]")
     if q.dtype not in _CODES or out.dtype not in _CODES:
         raise ValueError(f"unsupported dtypes {q.dtype}, {out.dtype}")
-    p = _DECODE_PACK(_CODES[q.dtype], _CODES[out.dtype], b, sq, hq, s0, s1, s2, o0, o1, o2, cols,
-                     row, window_left, sinks, 1.0 / math.sqrt(d) if scale is None else scale)
+    return out, lse, _DECODE_PACK(_CODES[q.dtype], _CODES[out.dtype], b, sq, hq, s0, s1, s2, o0, o1, o2, cols,
+                                  row, window_left, sinks, 1.0 / math.sqrt(d) if scale is None else scale)
+
+
+def kv4_decode(q, cache, block_table, seq_lens, *, scale=None, window_left=-1, sinks=0, out=None,
+               lse=None, o_dtype=None, workspace=None, status=None, stream=None):
+    """Attention of the last q.shape[1] tokens of each sequence over the cache
+    (attn_kv_decode).  q [B, Sq, Hq, d_qk]; block_table int32 [B, cols];
+    seq_lens int32 [B], the new tokens among them.  Returns (o [B, Sq, Hq, d_v],
+    lse float32 [B, Hq, Sq])."""
+    check_buffers(status, workspace)
+    lib = fast()
+    dev = on_device(cache.k_codes, q, block_table, seq_lens, out, lse, workspace, status)
+    out, lse, p = _decode_pack(q, cache, block_table, seq_lens, scale, window_left, sinks, out, lse, o_dtype, dev,
+                               stream)
     if workspace is None:
         workspace = new((_sized(dev, lib.attn_kv_decode_workspace_size, p, cache._desc),),
                         torch.uint8, dev, stream)
@@ -210,13 +216,45 @@ def kv4_decode(q, cache, block_table, seq_lens, *, scale=None, window_left=-1, s
     return out, lse
 
 
-def decode_workspace_size(q, cache, block_table, *, o_dtype=None):
-    """Bytes of workspace kv4_decode needs for these tensors (any lengths)."""
+def kv4_decode_shared(q, cache, block_table, seq_lens, group_starts, shared_lens, *, scale=None, out=None, lse=None,
+                      o_dtype=None, workspace=None, status=None, stream=None):
+    """kv4_decode (without a window) for requests that share their first tokens
+    (attn_kv_decode_shared): requests group_starts[g] .. group_starts[g + 1] - 1 name
+    the same pages for their first shared_lens[g] tokens, which are read once for all of
+    them.  group_starts: int32 [groups + 1]; shared_lens: int32 [groups]."""
+    check_buffers(status, workspace)
+    lib = fast()
+    dev = on_device(cache.k_codes, q, block_table, seq_lens, group_starts, shared_lens, out, lse, workspace, status)
+    groups = shared_lens.shape[0]
+    _ints("shared_lens", shared_lens, groups)
+    _ints("group_starts", group_starts, groups + 1)
+    out, lse, p = _decode_pack(q, cache, block_table, seq_lens, scale, -1, 0, out, lse, o_dtype, dev, stream)
+    if workspace is None:
+        workspace = new((_sized(dev, lib.attn_kv_decode_shared_workspace_size, p, cache._desc, groups),),
+                        torch.uint8, dev, stream)
+    launch(dev, stream, lib.attn_kv_decode_shared, p, cache._desc, groups, group_starts.data_ptr(),
+           shared_lens.data_ptr(), q.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+           lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, None if status is None else status.data_ptr())
+    return out, lse
+
+
+def _decode_sizes(q, cache, block_table, o_dtype):
     b, sq, hq, d = q.shape
     cols, row = _table(block_table, b)
-    p = _DECODE_PACK(_CODES[q.dtype], _CODES[o_dtype or q.dtype], b, sq, hq, 0, 0, 0, 0, 0, 0, cols,
-                     row, -1, 0, 1.0 / math.sqrt(d))
-    return _sized(on_device(q), fast().attn_kv_decode_workspace_size, p, cache._desc)
+    return _DECODE_PACK(_CODES[q.dtype], _CODES[o_dtype or q.dtype], b, sq, hq, 0, 0, 0, 0, 0, 0, cols,
+                        row, -1, 0, 1.0 / math.sqrt(d))
+
+
+def decode_workspace_size(q, cache, block_table, *, o_dtype=None):
+    """Bytes of workspace kv4_decode needs for these tensors (any lengths)."""
+    return _sized(on_device(q), fast().attn_kv_decode_workspace_size, _decode_sizes(q, cache, block_table, o_dtype),
+                  cache._desc)
+
+
+def decode_shared_workspace_size(q, cache, block_table, groups, *, o_dtype=None):
+    """Bytes of workspace kv4_decode_shared needs for these tensors (any lengths and prefixes)."""
+    return _sized(on_device(q), fast().attn_kv_decode_shared_workspace_size,
+                  _decode_sizes(q, cache, block_table, o_dtype), cache._desc, groups)
 
 
 def _weight_rows(name, t, batch, heads):

@@ -524,6 +524,42 @@ attn_status_t attn_kv_decode(const attn_kv4_decode_params_t* p, const attn_kv4_c
                               size_t workspace_bytes, int32_t* status, attn_stream_t stream);
 
 /*
+ * attn_kv_decode for batches whose requests share their first tokens (a system prompt,
+ * a document, samples of one request): the same results, to rounding, but what a
+ * group's requests share is read and converted once for all of them, and multiplied
+ * with all their query rows at a time.
+ * Requests group_starts[g] .. group_starts[g + 1] - 1 are group g (int32 [groups + 1],
+ * ascending; requests outside all groups share nothing), and the first shared_lens[g]
+ * tokens of each of them lie in the same pages: their rows of block_table name the same
+ * pages there, which the call relies on and does not check.  A prefix counts in whole
+ * multiples of 64 tokens; the rest of it is read as each request's own.  A request that
+ * has fewer tokens than the prefix and the seqlen_q newest shares nothing, and neither
+ * does a group with fewer than two that do.
+ * p as in attn_kv_decode, without a window (window_left = -1; sinks is ignored).  Scores
+ * and probabilities of the shared part are rounded as attn_kv_decode's are: O carries
+ * an error of up to 2^-11 of sum p |v|, and beside a V scale 2^24 times the others', in
+ * the shared part, the others lose bits.
+ * group_starts that do not ascend within [0, batch] (no group shares anything then),
+ * shared_lens out of [0, cols * page_size] (that group shares nothing) set the status
+ * word, beside what attn_kv_decode reports.  Every wait of the kernels has a limit (2 s);
+ * when one runs out the status word tells ATTN_ERR_TIMEOUT.
+ * Bitwise reproducible for the same call on the same device.  Lengths, groups and prefixes
+ * are read on the device: a captured call serves any.
+ * workspace: 256-byte aligned, attn_kv_decode_shared_workspace_size() bytes (of the
+ * current device); it needs no preparation, and calls that may overlap in time need
+ * one each.
+ */
+size_t attn_kv_decode_shared_workspace_size(const attn_kv4_decode_params_t* p,
+                                            const attn_kv4_cache_t* cache, int groups);
+attn_status_t attn_kv_decode_shared(const attn_kv4_decode_params_t* p,
+                                    const attn_kv4_cache_t* cache, int groups,
+                                    const int32_t* group_starts, const int32_t* shared_lens,
+                                    const void* q, const int32_t* block_table,
+                                    const int32_t* seq_lens, void* o, float* lse,
+                                    void* workspace, size_t workspace_bytes, int32_t* status,
+                                    attn_stream_t stream);
+
+/*
  * The attention weights that cached tokens receive from the last seqlen_q tokens of
  * each sequence, from the log-sum-exp of those tokens' attention over this cache (lse
  * as attn_kv_decode writes it, with the same scale, window and first tokens):
