@@ -120,12 +120,12 @@ struct SharedParams {  // attention of batches whose requests share their first 
   int batch, seqlen_q, heads_q, group, cols, groups;
   int rows;                    // query rows of a request and kv head (seqlen_q * group)
   int row_tile, key_tile;      // shared_tiles()
-  FastDiv by_group, by_rows;
+  FastDiv by_group, by_rows, by_request;  // by group; rows; rows * kv heads
   float scale_log2;
   int o_f32;
   // workspace
   void* group_info;            // [groups] (shared_group_bytes() each)
-  long long* total_units;
+  int* total_units;            // [2]: units of work, items
   int32_t *starts, *group_of;  // [batch]: tokens of the shared prefix, and whose
   float *own_o, *own_lse;      // of each request's own tokens, FP32, like o and lse, contiguous
   float *row_o, *row_ml;       // parts of items that one run finished: [2][batch][heads][rows][d_v], [..][2]

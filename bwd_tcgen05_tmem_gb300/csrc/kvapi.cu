@@ -849,6 +849,11 @@ attn_status_t check_shared(const attn_kv4_decode_params_t* p, const attn_kv4_cac
     return api_fail(ATTN_ERR_UNSUPPORTED, "a window: use attn_kv_decode, which reads what the window shows");
   if (groups < 0) return api_fail(ATTN_ERR_INVALID_ARG, "groups < 0");
   if (groups > p->batch) return api_fail(ATTN_ERR_INVALID_ARG, "more groups than requests");
+  int row_tile, key_tile;
+  attn::shared_tiles(c->d_v, row_tile, key_tile);
+  const double items = c->heads_kv * ((double)kp.batch * kp.rows / row_tile + groups + 1);
+  if (items * (((double)p->cols * c->page_size) / key_tile + 1) > INT32_MAX)
+    return api_fail(ATTN_ERR_UNSUPPORTED, "too many tiles of queries and keys for one call");
   kp.sinks = 0;
   return ATTN_OK;
 }
@@ -869,7 +874,7 @@ SharedLayout shared_layout(const attn::DecodeParams& kp, int groups, const Decod
     return x;
   };
   l.groups = take((size_t)groups * attn::shared_group_bytes());
-  l.units = take(8);
+  l.units = take(16);
   l.starts = take((size_t)kp.batch * 4);
   l.group_of = take((size_t)kp.batch * 4);
   l.own_o = take(rows * kp.c.d_v * 4);
@@ -943,7 +948,7 @@ attn_status_t attn_kv_decode_shared(const attn_kv4_decode_params_t* p, const att
   dp.status = status;
   const bool bf16 = p->dtype == ATTN_BF16;
   cudaStream_t st = (cudaStream_t)stream;
-  if (groups == 0)  // nobody shares anything
+  if (groups == 0 || cache->num_pages == 0)  // nobody shares anything
     return api_launched(attn::launch_kv4_decode(dp, bf16, dl.blocks, st), 2, "cache attention launch");
   attn::SharedParams kp;
   memset(&kp, 0, sizeof(kp));
@@ -968,10 +973,11 @@ attn_status_t attn_kv_decode_shared(const attn_kv4_decode_params_t* p, const att
   attn::shared_tiles(cache->d_v, kp.row_tile, kp.key_tile);
   kp.by_group = dp.by_group;
   kp.by_rows = attn::FastDiv::of((uint32_t)dp.rows);
+  kp.by_request = attn::FastDiv::of((uint32_t)(dp.rows * cache->heads_kv));
   kp.scale_log2 = dp.scale_log2;
   kp.o_f32 = dp.o_f32;
   kp.group_info = w + l.groups;
-  kp.total_units = (long long*)(w + l.units);
+  kp.total_units = (int*)(w + l.units);
   kp.starts = (int32_t*)(w + l.starts);
   kp.group_of = (int32_t*)(w + l.group_of);
   kp.own_o = (float*)(w + l.own_o);

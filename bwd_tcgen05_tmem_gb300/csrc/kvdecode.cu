@@ -545,6 +545,11 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
   __shared__ int s_b[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;");  // (the join waits for the whole grid)
+  // Beside a shared prefix this grid starts before the prefix kernel ends, and must
+  // not end before it does: the joins wait for this one alone.
+  auto leave = [&]() {
+    if (p.starts && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
   if (tid < kWarps) {
     s_b[tid] = p.batch;
     s_before[tid] = s_tiles[tid][0] = s_tiles[tid][1] = 0;
@@ -585,7 +590,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
   const long long run0 = (long long)blockIdx.x * kWarps;
   // blocks without a run: nothing to join there
   if (tid < kWarps && run0 + tid >= n_runs) p.ends[run0 + tid] = -1;
-  if (run0 >= n_runs) return;
+  if (run0 >= n_runs) return leave();
   // run k has units [bound(k), bound(k + 1))
   const long long each = quotient(all, (int)n_runs), more = all - each * n_runs;
   auto bound = [&](long long k) { return each * k + min(k, more); };
@@ -611,10 +616,10 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
   const long long run = run0 + warp;
   const int first_b = s_b[warp];
   const int n_run = (int)min(max(s_tiles[warp][1] - s_tiles[warp][0], 0ll), (long long)INT32_MAX);
-  if (run >= n_runs) return;
+  if (run >= n_runs) return leave();
   if (first_b >= p.batch || n_run == 0) {
     if (lane == 0) p.ends[run] = -1;
-    return;
+    return leave();
   }
 
   const int r = lane >> 2, c = lane & 3;
@@ -887,6 +892,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecShape<DQK, DV, NT>::kBlocks)
       }
   }
   copies_wait<0>();
+  leave();
 }
 
 // ----------------------------------------------------------------- the join
@@ -1089,17 +1095,22 @@ cudaError_t dec_launch(const DecodeParams& p, int blocks, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(main, S::kRing, done);
   if (e != cudaSuccess) return e;
-  main<<<blocks, kWarps * 32, S::kRing, st>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // the join is launched while the first kernel runs, and waits for its end
+  // the join is launched while the first kernel runs, and waits for its end (beside a
+  // shared prefix the first kernel is launched like that too)
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = st;
   cfg.attrs = &attr;
+  cfg.numAttrs = p.starts ? 1 : 0;
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = S::kRing;
+  e = cudaLaunchKernelEx(&cfg, main, p);
+  if (e != cudaSuccess) return e;
   cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = 0;
   const int64_t items = (int64_t)p.batch * p.c.heads * p.row_blocks;
   const int runs = blocks * kWarps;
   if (items * kByItemPieces <= runs) {

@@ -12,26 +12,32 @@
 //
 // The prefix kernel.  One block an SM, 20 warps:
 //   warps 0..7   softmax: two groups of 128 threads, one TMEM lane (query row) each;
-//   warps 8..11  K codes to the fp16 operand, warps 12..15 V codes: a thread takes a
-//                token's row, its codes loaded a tile ahead;
-//   warp 16      issues S = Q K^T, warp 17 O += P V.
+//   warps 8..11  K's codes to the fp16 operand, warps 12..15 V's: two of the four take the
+//                even tiles, two the odd ones, half of the tile's tokens each, four lanes a
+//                row, the next tile's codes on their way in registers; no warp waits for
+//                another one;
+//   warps 16, 19 issue S = Q K^T, one for each softmax group, warp 17 O += P V;
+//   warp 18      looks up where the tokens of the tiles to come lie, and asks for them in L2.
 // A block's run of work is a stretch of the list (group, kv head, 256 query rows, tile
-// of keys), cut into equal runs.  With more than 128 rows the two softmax groups have
+// of 64 keys), cut into equal runs.  With more than 128 rows the two softmax groups have
 // 128 rows each and share every converted tile; with fewer they take turns at the tiles
-// for the same rows, each with its own O (two parts for the join).  At head dim 256 O
-// fills half of TMEM: one group, tiles of 64 keys, 128 rows.
+// for the same rows, each with its own O (two parts for the join).  Each group reads its
+// scores into registers at once, so that the next ones are computed while it works, and
+// has two P buffers in TMEM.  At head dim 256
+// O fills half of TMEM: one softmax group, 128 rows.
 //
 // Numbers: code - 8 is exact in fp16 and so is its product with a bf16 scale (4 + 8
-// bits), times a power of two: K's makes the tile's largest scale 2^11 .. 2^12 and comes
-// back with the scores; V's does for the largest scale of the tiles so far (with room
-// for 2^3), and O follows when it grows.  q is held as in kvdecode.cu.  Probabilities
-// are FP32 in the sum and rounded to fp16 for the second product, times 2^14: their
-// reference moves when a score passes it by 1, so they stay below 2^15, and those 2^-38
-// below the row's maximum are still told from 0.
+// bits), times a power of two that makes the largest scale of half a tile 2^11 .. 2^12.
+// K's comes back with the scores; V's goes into the probabilities, relative to the largest
+// of the row's tiles so far (with room for 2^3), which O follows when it grows.
+// q is held as in kvdecode.cu.  Probabilities are FP32 in the sum and rounded to fp16 for
+// the second product, times 2^11: their reference moves when a score passes it by 2^4, so
+// they stay below 2^15, and those 2^-35 below the row's maximum are still told from 0.
 // In a row of 8 dims the operand's order is 0 4 1 5 2 6 3 7 (a mask of a word of codes
 // makes pairs n, n + 4): Q is stored the same way, O's columns are put back at the end.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kcommon.cuh"
 #include "kv.h"
@@ -41,21 +47,25 @@ namespace attn {
 
 namespace {
 
-constexpr int kGranule = 64;  // tokens: prefixes are taken in whole ones, the rest is the requests' own
-constexpr float kBias = 14.0f;  // probabilities are held times 2^14 (2^15 where the reference lags)
-constexpr int kXRing = 8;
+constexpr int KT = 64;  // keys of a tile: prefixes are taken in whole ones, the rest is the requests' own
+constexpr float kLag = 4.0f, kBias = 15.0f - kLag;  // a row's reference may lag its maximum; probabilities are held times 2^kBias
+constexpr int kXRing = 16;
+constexpr int kJoinParts = 12;  // of an item on average: from there on a block joins a row
+constexpr int kRowRing = 8;  // tiles that are looked up ahead
 constexpr int kThreads = 640;
+// Registers of a thread: 96 at the launch; the softmax groups, which hold a row of
+// scores, take what the issuing warps give up (2 * 112 + 2 * 96 + 56 <= 5 * 96).
+constexpr int kSoftmaxRegs = 112, kIssueRegs = 56;
 
 template <int DQK, int DV>
 struct ShShape {
   static constexpr bool kWide = DV > 128;
-  static constexpr int KT = kWide ? 64 : 128;      // keys of a tile
   static constexpr int kSlots = kWide ? 1 : 2;     // softmax groups
   static constexpr int kRT = 128 * kSlots;         // query rows of an item
   static constexpr int kKSlot = KT * 128;          // 64 dims of a tile
   static constexpr int kKTile = kKSlot * (DQK / 64), kVTile = kKSlot * (DV / 64);
   static constexpr int kQTile = kSlotBytes * (DQK / 64);
-  static constexpr int kKS = DQK == 64 ? 4 : 2, kVS = DQK == 64 ? 4 : DQK == 192 ? 1 : 2;  // stages
+  static constexpr int kKS = kWide ? 2 : DQK == 192 ? 3 : 4, kVS = kKS;  // stages
   static constexpr int kSmem = kSlots * kQTile + kKS * kKTile + kVS * kVTile + 1024;
   static constexpr int kTmemO = 256;
 };
@@ -65,27 +75,28 @@ struct ShShape {
 // ----------------------------------------------------------------- the list of work
 // What the first kernel finds out about a group.
 struct ShGroup {
-  long long unit0;  // units (a tile of an item) of the groups before it
-  int tokens;       // of the prefix that its requests share, a multiple of kGranule
+  int unit0;        // units (a tile of an item) of the groups before it
+  int tokens;       // of the prefix that its requests share, a multiple of KT
   int request;      // one that shares it (its table row is read)
   int first, members;
 };
 
 __device__ __forceinline__ int sh_row_tiles(const SharedParams& p, const ShGroup& g) {
-  return (int)(((long long)g.members * p.rows + p.row_tile - 1) / p.row_tile);
+  return (int)(((long long)g.members * p.rows + p.row_tile - 1) >> (p.row_tile == 256 ? 8 : 7));
 }
 __device__ __forceinline__ int sh_key_tiles(const SharedParams& p, const ShGroup& g) {
-  return (g.tokens + p.key_tile - 1) / p.key_tile;
+  return g.tokens / KT;
 }
 
 // One block: which requests share what.
 __global__ void __launch_bounds__(1024) attn_kv_shared_plan_kernel(const __grid_constant__ SharedParams p) {
   __shared__ int s_bad;
-  __shared__ long long s_sum[32];
+  __shared__ int s_items, s_sum[32];
   ShGroup* groups = (ShGroup*)p.group_info;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t cap = (int64_t)p.cols << p.c.page_shift;
-  if (tid == 0) s_bad = 0;
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (tid == 0) s_bad = 0, s_items = 0;
   __syncthreads();
   bool bad = false;
   for (int g = tid; g <= p.groups; g += 1024) {
@@ -102,7 +113,7 @@ __global__ void __launch_bounds__(1024) attn_kv_shared_plan_kernel(const __grid_
     bad |= !ok;
     ShGroup x;
     x.unit0 = 0;
-    x.tokens = none || !ok ? 0 : n / kGranule * kGranule;
+    x.tokens = none || !ok ? 0 : n / KT * KT;
     x.request = INT32_MAX;
     x.first = none ? 0 : p.group_starts[g];
     x.members = 0;
@@ -137,22 +148,26 @@ __global__ void __launch_bounds__(1024) attn_kv_shared_plan_kernel(const __grid_
     p.starts[b] = g >= 0 ? groups[g].tokens : 0;
   }
   __syncthreads();
-  long long before = 0;
+  int before = 0, items = 0;  // (the host has refused calls whose units could pass 2^31)
   for (int g0 = 0; g0 < p.groups; g0 += 1024) {
     const int g = g0 + tid;
     ShGroup x;
-    long long units = 0;
+    int units = 0;
     if (g < p.groups) {
       x.first = groups[g].first;
       x.request = __ldcg(&groups[g].request);  // (atomics are done in L2)
       x.tokens = __ldcg(&groups[g].members) < 2 ? 0 : groups[g].tokens;
       x.members = none ? 0 : p.group_starts[g + 1] - x.first;
-      if (x.tokens) units = (long long)p.c.heads * sh_row_tiles(p, x) * sh_key_tiles(p, x);
+      if (x.tokens) {
+        const int n = p.c.heads * sh_row_tiles(p, x);
+        items += n;
+        units = n * sh_key_tiles(p, x);
+      }
     }
-    long long j = units;
+    int j = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, j, o);
+      const int y = __shfl_up_sync(0xffffffffu, j, o);
       if (lane >= o) j += y;
     }
     __syncthreads();
@@ -165,33 +180,50 @@ __global__ void __launch_bounds__(1024) attn_kv_shared_plan_kernel(const __grid_
     }
     if (g < p.groups) groups[g] = x;
   }
-  if (tid == 0) *p.total_units = before;
+  if (items) atomicAdd(&s_items, items);
+  __syncthreads();
+  if (tid == 0) p.total_units[0] = before, p.total_units[1] = s_items;
+}
+
+// Starts kernel k while the one before it on the stream still runs (it waits itself).
+template <typename... A>
+cudaError_t launch_early(void (*k)(A...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
 // The list is cut into `runs` equal runs.
 struct ShRuns {
-  long long total, each, more;
-  int runs;
-  __device__ __forceinline__ ShRuns(long long total_, int most) {
+  int total, each, more, runs;
+  __device__ __forceinline__ ShRuns(int total_, int most) {
     total = total_;
-    runs = (int)min((long long)most, total);
+    runs = min(most, total);
     each = runs ? total / runs : 0;
     more = total - each * runs;
   }
-  __device__ __forceinline__ long long start(int k) const { return each * k + min((long long)k, more); }
-  __device__ __forceinline__ int of(long long u) const {
-    const long long big = more * (each + 1);
-    return (int)(u < big ? u / (each + 1) : more + (u - big) / each);
+  __device__ __forceinline__ int start(int k) const { return each * k + min(k, more); }
+  __device__ __forceinline__ int of(int u) const {
+    const int big = more * (each + 1);
+    return u < big ? u / (each + 1) : more + (u - big) / each;
   }
 };
 
 // The next piece of a run: tiles kt .. kt_end - 1 of one item.
 struct ShPiece {
-  long long u, end;  // what is left of the run
+  int u, end;  // what is left of the run
   int g;
   ShGroup info;
   int head, row_tile, kt, kt_end, key_tiles;
-  __device__ __forceinline__ void begin(const SharedParams& p, long long u0, long long u1) {
+  __device__ __forceinline__ void begin(const SharedParams& p, int u0, int u1) {
     u = u0;
     end = u1;
     const ShGroup* groups = (const ShGroup*)p.group_info;
@@ -209,16 +241,16 @@ struct ShPiece {
     for (;;) {
       key_tiles = sh_key_tiles(p, info);
       const int row_tiles = sh_row_tiles(p, info);
-      const long long n = info.tokens ? (long long)p.c.heads * row_tiles * key_tiles : 0, at = u - info.unit0;
+      const int n = info.tokens ? p.c.heads * row_tiles * key_tiles : 0, at = u - info.unit0;
       if (at >= n) {  // (groups without units are passed by)
         info = groups[++g];
         continue;
       }
-      const int item = (int)(at / key_tiles);
-      kt = (int)(at - (long long)item * key_tiles);
+      const int item = at / key_tiles;
+      kt = at - item * key_tiles;
       head = item / row_tiles;
       row_tile = item - head * row_tiles;
-      kt_end = (int)min((long long)key_tiles, kt + (end - u));
+      kt_end = min(key_tiles, kt + (end - u));
       u += kt_end - kt;
       return true;
     }
@@ -250,16 +282,12 @@ __device__ __forceinline__ uint4 scaled_codes(uint32_t w, __half2 s) {
   return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-__device__ __forceinline__ void group_sync(int id) {  // 128 threads
-  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
-}
-
 constexpr int kExpLow = -110;  // exponents of scales from there on are told apart
 
 struct ShBars {
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
-  uint64_t s_full[2], p_full[2], o_done[2];
-  uint64_t q_full, q_empty, x_full[kXRing], drain[2];
+  uint64_t s_full[2], s_free[2], p_full[2][2], o_done[2][2];  // of a softmax group's S, and its P buffers
+  uint64_t q_full, q_empty, x_full[kXRing], rows_full[kRowRing], rows_empty[kRowRing], drain[3];
 };
 
 template <int N>
@@ -272,305 +300,331 @@ __device__ __forceinline__ void row_words(const uint8_t* s, uint32_t (&w)[N]) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(s) + i);
+    for (int i = 0; i < N / 2; ++i) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(s) + i);
+      w[2 * i] = v.x, w[2 * i + 1] = v.y;
+    }
   }
 }
 
-// The group of four warps that turns one side's codes into its operand.  Two threads
-// share a token's row where a tile has 64 keys.
+// Where a tile's tokens lie: the cache's rows of each 16 of them (-1: none).
+struct ShRows {
+  long long row[4];
+};
+
+// One side of a tile in a lane: the words of its quarter (4 G bytes) of the rows 8 i +
+// row8, and of those rows' scales the groups c, c + 4.
+template <int D, int SETS>
+struct ShSide {
+  static constexpr int G = D / 32, kOwn = (G + 3) / 4;
+  uint32_t w[SETS][G];
+  uint32_t s[SETS][kOwn];
+  __half2 h[SETS][kOwn];
+
+  // (Where there are no tokens row 0 is read, and counts with scales of 0.)
+  __device__ __forceinline__ void load_scales(const uint16_t* scales, const long long* rows, int row8, int c) {
+    const uint16_t* const mine = scales + row8 * G + min(c, G - 1);
+#pragma unroll
+    for (int i = 0; i < SETS; ++i) {
+      const long long at = rows[i >> 1];
+      const uint16_t* src = mine + max(at, 0ll) * G + (i & 1) * 8 * G;
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j) {
+        s[i][j] = G % 4 == 0 || c + 4 * j < G ? __ldg(src + 4 * j) : 0u;
+        if (at < 0) s[i][j] = 0u;
+      }
+    }
+  }
+  __device__ __forceinline__ void load_codes(const uint8_t* codes, const long long* rows, int row8, int c) {
+    const uint8_t* const mine = codes + row8 * (D / 2) + c * 4 * G;
+#pragma unroll
+    for (int i = 0; i < SETS; ++i) row_words<G>(mine + max(rows[i >> 1], 0ll) * (D / 2) + (i & 1) * 8 * (D / 2), w[i]);
+  }
+  // the largest finite scale's bits
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < SETS; ++i)
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j) {
+        const uint32_t x = s[i][j] & 0x7fffu;
+        if (x < 0x7f80u) m = max(m, x);
+      }
+    return __reduce_max_sync(0xffffffffu, m);
+  }
+  __device__ __forceinline__ void halves(float f) {
+#pragma unroll
+    for (int i = 0; i < SETS; ++i)
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j) h[i][j] = __float2half2_rn(__uint_as_float(s[i][j] << 16) * f);
+  }
+  // dst: row row8 of the warp's tokens in the operand (rows of 128 bytes, swizzled).
+  // (Lanes 8 p .. + 7 hold rows p and p + 4, whose chunks lie in different banks.)
+  template <bool K>
+  __device__ __forceinline__ void store(uint32_t dst, int slot_bytes, int row8, int c) const {
+    const int quad = (threadIdx.x & 31) & ~3;
+#pragma unroll
+    for (int i = 0; i < SETS; ++i)
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const uint32_t sb = __shfl_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&h[i][g >> 2]), quad | (g & 3));
+        const uint32_t x = K ? w[i][g] : __byte_perm(w[i][g >> 1], w[i][(G + g) >> 1], (g & 1) ? 0x7632 : 0x5410);
+        const uint4 y = scaled_codes(x, *reinterpret_cast<const __half2*>(&sb));
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         dst + (g >> 1) * slot_bytes + i * 1024 + ((((g & 1) * 4 + c) ^ row8) << 4)),
+                     "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                     : "memory");
+      }
+  }
+};
+
+// One of the four warps that turn a side's codes into its operand.
 template <int DQK, int DV, bool K>
-__device__ __forceinline__ void sh_convert(const SharedParams& p, uint8_t* ring, ShBars& bars, int* x_exp,
-                                           uint32_t (*s_top)[4], long long u0, long long u1, const Abort& ab) {
+__device__ __forceinline__ void sh_convert(const SharedParams& p, uint8_t* operand, ShBars& bars, int (*x_exp)[2],
+                                           const ShRows* rows, int n, const Abort& ab) {
   using S = ShShape<DQK, DV>;
-  constexpr int D = K ? DQK : DV, G = D / 32, KT = S::KT, kParts = 128 / KT, kStages = K ? S::kKS : S::kVS;
-  constexpr int kTileBytes = K ? S::kKTile : S::kVTile;
-  constexpr int NW = D / 8 / kParts, NS = (G / 2 + kParts - 1) / kParts;  // words of codes and of scales of a thread
-  static_assert(kParts == 1 || G % (4 * kParts) == 0, "halves of a row");
-  const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
-  const int row = tid % KT, part = tid / KT;
+  constexpr int D = K ? DQK : DV, kStages = K ? S::kKS : S::kVS, kTileBytes = K ? S::kKTile : S::kVTile;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, half = warp & 1;
+  const int c = lane & 3, row8 = (lane >> 3) + ((lane >> 2) & 1) * 4;
   const uint8_t* codes = K ? p.c.k_codes : p.c.v_codes;
-  const uint8_t* scales = reinterpret_cast<const uint8_t*>(K ? p.c.k_scales : p.c.v_scales);
+  const uint16_t* scales = K ? p.c.k_scales : p.c.v_scales;
   uint64_t* full = K ? bars.kfull : bars.vfull;
   uint64_t* empty = K ? bars.kempty : bars.vempty;
-
-  // tiles are looked up two ahead (the page), loaded one ahead (the codes)
-  ShPiece look;
-  look.begin(p, u0, u1);
-  bool more = look.next(p);
-  int look_kt = look.kt;
-  struct Tile {
-    int page, head, offset;
-    bool first;  // of its piece
+  const uint32_t dst = smem_u32(operand) + (half * 32 + row8) * 128;
+  ShSide<D, 4> x;
+  auto load = [&](int t) {
+    const int slot = t % kRowRing;
+    if (!mbar_wait_warp(&bars.rows_full[slot], (uint32_t)(t / kRowRing) & 1u, ab)) return false;
+    x.load_scales(scales, &rows[slot].row[half * 2], row8, c);
+    x.load_codes(codes, &rows[slot].row[half * 2], row8, c);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.rows_empty[slot]);
+    return true;
   };
-  auto look_up = [&]() {
-    Tile t{-1, 0, 0, false};
-    if (!more) return t;
-    t.first = look_kt == look.kt;
-    t.head = look.head;
-    const int token = look_kt * KT + row;
-    t.offset = token & (p.c.page_size - 1);
-    if (token < look.info.tokens) {
-      t.page = p.table[(int64_t)look.info.request * p.table_stride + (token >> p.c.page_shift)];
-      if ((unsigned)t.page >= (unsigned)p.c.num_pages) {
-        t.page = -1;
-        if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
-      }
-    }
-    if (++look_kt == look.kt_end) {
-      more = look.next(p);
-      look_kt = look.kt;
-    }
-    return t;
-  };
-  uint32_t w[NW], sc[NS], wn[NW], scn[NS];
-  auto load = [&](const Tile& t, uint32_t (&w)[NW], uint32_t (&sc)[NS]) {
-    if (t.page < 0) {  // zeros
-#pragma unroll
-      for (int i = 0; i < NW; ++i) w[i] = 0x88888888u;
-#pragma unroll
-      for (int i = 0; i < NS; ++i) sc[i] = 0u;
-      return;
-    }
-    const int64_t at = ((int64_t)t.page * p.c.heads + t.head) * p.c.page_size + t.offset;
-    if constexpr (kParts == 1) {
-      row_words<NW>(codes + at * (D / 2), w);
-      row_words<NS>(scales + at * (2 * G), sc);
-    } else {
-      // groups part * G / 2 .. of the row: K words c G + g, V half-words r G + g
-      constexpr int H = G / kParts;
-      row_words<NS>(scales + at * (2 * G) + part * 2 * H, sc);
-      if (K) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t x[H];
-          row_words<H>(codes + at * (D / 2) + (c * G + part * H) * 4, x);
-#pragma unroll
-          for (int g = 0; g < H; ++g) w[c * H + g] = x[g];
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          uint32_t x[H / 2];
-          row_words<H / 2>(codes + at * (D / 2) + (r * G + part * H) * 2, x);
-#pragma unroll
-          for (int g = 0; g < H / 2; ++g) w[r * (H / 2) + g] = x[g];
-        }
-      }
-    }
-  };
-  const long long n = u1 - u0;
-  Tile next = look_up();
-  load(next, w, sc);
-  bool first = next.first;
-  next = look_up();
-  int ref = 0;
-  bool live = true;  // (after a wait that gave up the group's barriers go on, so that none of its warps is left there)
-  for (long long t = 0; t < n; ++t) {
-    load(next, wn, scn);
-    const bool next_first = next.first;
-    next = look_up();
-    // ---- the tile's largest finite scale
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const uint32_t lo = sc[i] & 0x7fffu, hi = (sc[i] >> 16) & 0x7fffu;
-      if (lo < 0x7f80u) top = max(top, lo);
-      if (hi < 0x7f80u) top = max(top, hi);
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    uint32_t* tops = s_top[t & 1];
-    if (lane == 0) tops[warp] = top;
-    group_sync(K ? 1 : 2);
-    top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-    const int e = max((int)(top >> 7) - 127, kExpLow);
-    if (K)
-      ref = e;
-    else if (first)
-      ref = e;
-    else if (e > ref)
-      ref = min(e + 3, 127);
-    if (tid == 0) {
-      x_exp[t % kXRing] = ref;
+  int t = warp >> 1;
+  if (t >= n || !load(t)) return;
+  for (; t < n; t += 2) {
+    const int e = max((int)(x.top() >> 7) - 127, kExpLow), stage = t % kStages;
+    if (lane == 0) {
+      x_exp[t % kXRing][half] = e;
       mbar_arrive(&bars.x_full[t % kXRing]);
     }
-    const float f = pow2(11 - ref);
-    __half2 s[2 * NS];
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      s[2 * i] = __float2half2_rn(scale_of(sc, 2 * i) * f);
-      s[2 * i + 1] = __float2half2_rn(scale_of(sc, 2 * i + 1) * f);
-    }
-    const int stage = (int)(t % kStages);
-    live = live && (t < kStages || mbar_wait_warp(&empty[stage], (uint32_t)((t / kStages) - 1) & 1u, ab));
-    uint8_t* dst = ring + stage * kTileBytes + row * 128;
-    constexpr int H = G / kParts;
-    if (live) {
-#pragma unroll
-      for (int g = 0; g < H; ++g)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t x;
-          if (K)
-            x = w[c * H + g];
-          else
-            x = __byte_perm(w[(2 * c * H + g) >> 1], w[((2 * c + 1) * H + g) >> 1], (g & 1) ? 0x7632 : 0x5410);
-          const int gg = part * H + g, chunk = (gg & 1) * 4 + c;
-          *reinterpret_cast<uint4*>(dst + (gg >> 1) * S::kKSlot + ((chunk ^ (row & 7)) << 4)) = scaled_codes(x, s[g]);
-        }
-      fence_proxy_async();
+    x.halves(pow2(11 - e));
+    if (t >= kStages && !mbar_wait_warp(&empty[stage], (uint32_t)(t / kStages - 1) & 1u, ab)) return;
+    x.template store<K>(dst + stage * kTileBytes, S::kKSlot, row8, c);
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[stage]);
+    if (t + 2 < n && !load(t + 2)) return;
+  }
+}
+
+// The warp that looks up the tiles' tokens, a few tiles ahead of those that load them.
+template <int DQK, int DV>
+__device__ __forceinline__ void sh_look_up(const SharedParams& p, ShBars& bars, ShRows* rows, int u0, int u1,
+                                           const Abort& ab) {
+  constexpr int kChunks = KT / 16;  // of 16 tokens, each in one page
+  const int lane = threadIdx.x & 31;
+  ShPiece look;
+  look.begin(p, u0, u1);
+  int t = 0;
+  while (look.next(p)) {
+    const int32_t* table = p.table + (int64_t)look.info.request * p.table_stride;
+    for (int kt = look.kt; kt < look.kt_end; ++kt, ++t) {
+      const int slot = t % kRowRing, token = kt * KT + 16 * lane;
+      const bool here = lane < kChunks && token < look.info.tokens;
+      const int page = here ? __ldg(table + (token >> p.c.page_shift)) : -1;
+      if (t >= kRowRing && !mbar_wait_warp(&bars.rows_empty[slot], (uint32_t)(t / kRowRing - 1) & 1u, ab)) return;
+      const bool inside = (unsigned)page < (unsigned)p.c.num_pages;
+      if (here && !inside && p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+      const long long row = inside ? ((long long)page * p.c.heads + look.head) * p.c.page_size + (token & (p.c.page_size - 1)) : -1;
+      if (lane < kChunks) rows[slot].row[lane] = row;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[stage]);
+      if (lane == 0) mbar_arrive(&bars.rows_full[slot]);
+      // lines of 128 bytes of the rows' codes and scales
+      auto fetch = [&](auto width_of, const uint8_t* base) {
+        constexpr int W = decltype(width_of)::value, kLines = (16 * W + 127) / 128;  // bytes of a row; lines of a chunk
+#pragma unroll
+        for (int i = 0; i < kChunks * kLines; i += 32) {
+          const int chunk = (i + lane) / kLines, line = i + lane - chunk * kLines;
+          const long long at = __shfl_sync(0xffffffffu, row, chunk & 31);
+          if (chunk < kChunks && at >= 0)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"((uint64_t)__cvta_generic_to_global(base + at * W + line * 128)));
+        }
+      };
+      fetch(std::integral_constant<int, DQK / 2>(), p.c.k_codes);
+      fetch(std::integral_constant<int, DV / 2>(), p.c.v_codes);
+      fetch(std::integral_constant<int, DQK / 16>(), reinterpret_cast<const uint8_t*>(p.c.k_scales));
+      fetch(std::integral_constant<int, DV / 16>(), reinterpret_cast<const uint8_t*>(p.c.v_scales));
     }
-#pragma unroll
-    for (int i = 0; i < NW; ++i) w[i] = wn[i];
-#pragma unroll
-    for (int i = 0; i < NS; ++i) sc[i] = scn[i];
-    first = next_first;
   }
 }
 
 template <bool BF16, int DQK, int DV>
 __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __grid_constant__ SharedParams p) {
   using S = ShShape<DQK, DV>;
-  constexpr int KT = S::KT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + S::kSlots * S::kQTile;
   uint8_t* sV = sK + S::kKS * S::kKTile;
   __shared__ ShBars bars;
-  __shared__ int k_exp[kXRing], v_exp[kXRing];
-  __shared__ uint32_t s_top[2][2][4];
+  __shared__ __align__(8) int k_exp[kXRing][2], v_exp[kXRing][2];  // of the halves of a tile
+  __shared__ ShRows rows[kRowRing];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5;
 
-  const ShRuns runs(*p.total_units, gridDim.x);
-  if ((int)blockIdx.x >= runs.runs) return;
-  const long long u0 = runs.start(blockIdx.x), u1 = runs.start(blockIdx.x + 1);
   Abort ab{&abort_flag, p.status, kWaitLimitNs};
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&bars.kfull[i], 4);
-      mbar_init(&bars.vfull[i], 4);
-      mbar_init(&bars.kempty[i], 1);
+      mbar_init(&bars.kfull[i], 2);
+      mbar_init(&bars.vfull[i], 2);
+      mbar_init(&bars.kempty[i], S::kSlots);
       mbar_init(&bars.vempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.p_full[i], 128);
-      mbar_init(&bars.o_done[i], 1);
-      mbar_init(&bars.drain[i], 1);
+      mbar_init(&bars.s_free[i], 128);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&bars.p_full[i][k], 128);
+        mbar_init(&bars.o_done[i][k], 1);
+      }
     }
+    for (int i = 0; i < 3; ++i) mbar_init(&bars.drain[i], 1);
     mbar_init(&bars.q_full, 128 * S::kSlots);
-    mbar_init(&bars.q_empty, 1);
-    for (int i = 0; i < kXRing; ++i) mbar_init(&bars.x_full[i], 2);
+    mbar_init(&bars.q_empty, S::kSlots);
+    for (int i = 0; i < kXRing; ++i) mbar_init(&bars.x_full[i], 4);
+    for (int i = 0; i < kRowRing; ++i) {
+      mbar_init(&bars.rows_full[i], 1);
+      mbar_init(&bars.rows_empty[i], 4);
+    }
     fence_barrier_init();
   }
   if (warp == 16) {
     tmem_alloc(&tmem_base_sh, 512);
     tmem_relinquish();
   }
+  // All of that comes before the first kernel's end, and the next kernel may come
+  // before this one's (it needs what the first one found out, and waits for this one
+  // before it ends itself).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
-
-  if (warp >= 8 && warp < 12) {
-    sh_convert<DQK, DV, true>(p, sK, bars, k_exp, s_top[0], u0, u1, ab);
-  } else if (warp >= 12 && warp < 16) {
-    sh_convert<DQK, DV, false>(p, sV, bars, v_exp, s_top[1], u0, u1, ab);
-  } else if (warp == 16 || warp == 17) {
+  const ShRuns runs(__ldcg(p.total_units), gridDim.x);
+  const bool idle = (int)blockIdx.x >= runs.runs;
+  const int u0 = idle ? 0 : runs.start(blockIdx.x), u1 = idle ? 0 : runs.start(blockIdx.x + 1);
+  if (idle) {
+    // (no run for this block)
+  } else if (warp >= 8 && warp < 16) {
+    if (warp < 12)
+      sh_convert<DQK, DV, true>(p, sK, bars, k_exp, rows, u1 - u0, ab);
+    else
+      sh_convert<DQK, DV, false>(p, sV, bars, v_exp, rows, u1 - u0, ab);
+  } else if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 18) sh_look_up<DQK, DV>(p, bars, rows, u0, u1, ab);
+    if (warp == 17 || warp == 16 || (warp == 19 && S::kSlots == 2)) {
     // ------------------------------------------------------------ MMA issuers
-    // Tile t of the run goes to S buffers first .. last: both where two row tiles share
-    // it, else one after the other.  (At head dim 256 the one group has two buffers.)
-    const bool s_role = warp == 16;
+    // Tile t of the run goes to both softmax groups where two row tiles share it, else to
+    // one after the other.  A group's n-th tile uses its P buffer n % 2.
     constexpr uint32_t idesc_s = make_idesc(128, KT, false, false, false);
     constexpr uint32_t idesc_o = make_idesc(128, DV, false, false, true);
-    const uint64_t qdesc = make_sdesc(smem_u32(sQ), 16, 1024);
-    const uint64_t kdesc = make_sdesc(smem_u32(sK), 16, 1024);
-    const uint64_t vdesc = make_sdesc(smem_u32(sV), S::kKSlot, 1024);
-    uint32_t used[2] = {0, 0};  // tiles that a buffer had so far
     uint32_t t = 0, pieces = 0;
     bool ok = true;
     ShPiece pc;
     pc.begin(p, u0, u1);
-    while (ok && pc.next(p)) {
-      const bool both = S::kSlots == 2 && pc.row_slots(p) == 2;
-      if (s_role && !mbar_wait_warp(&bars.q_full, pieces & 1u, ab)) break;
-      tc_fence_after();
-      for (int kt = pc.kt; kt < pc.kt_end && ok; ++kt, ++t) {
-        const int first = both ? 0 : (kt - pc.kt) & 1, last = both ? 1 : first;
-        if (s_role) {
+    if (warp != 17) {
+      const int g = warp == 19 ? 1 : 0;
+      const uint64_t kdesc = make_sdesc(smem_u32(sK), 16, 1024);
+      uint32_t n = 0;  // tiles that the group had so far
+      while (ok && pc.next(p)) {
+        const bool both = S::kSlots == 2 && pc.row_slots(p) == 2;
+        const uint64_t qa = make_sdesc(smem_u32(sQ + (both ? g : 0) * S::kQTile), 16, 1024);
+        if (!mbar_wait_warp(&bars.q_full, pieces & 1u, ab)) break;
+        for (int kt = pc.kt; kt < pc.kt_end; ++kt, ++t) {
           const uint32_t st = t % S::kKS;
+          const bool mine = both || S::kSlots == 1 || ((kt - pc.kt) & 1) == g;
           ok = mbar_wait_warp(&bars.kfull[st], (t / S::kKS) & 1u, ab);
-          for (int b = first; b <= last && ok; ++b) {
-            // the buffer's earlier P has been read
-            if (used[b] && !mbar_wait_warp(&bars.o_done[b], (used[b] - 1) & 1u, ab)) {
-              ok = false;
-              break;
-            }
-            ++used[b];
-            tc_fence_after();
-            const uint64_t qa = qdesc + (uint64_t)((both ? b : 0) * (S::kQTile >> 4));
-            const uint64_t kb = kdesc + (uint64_t)(st * (S::kKTile >> 4));
-            if (elect_sync()) {
+          // the scores before these have been read
+          if (ok && mine && n) ok = mbar_wait_warp(&bars.s_free[g], (n - 1) & 1u, ab);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + g * 128;
+          const uint64_t kb = kdesc + (uint64_t)(st * (S::kKTile >> 4));
+          if (elect_sync()) {
+            if (mine) {
 #pragma unroll
               for (int c = 0; c < DQK / 64; ++c)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  mma_ss(tmem + b * 128, qa + (uint64_t)(c * (kSlotBytes >> 4)) + 2 * k,
-                         kb + (uint64_t)(c * (S::kKSlot >> 4)) + 2 * k, idesc_s, (c | k) ? 1u : 0u);
-              mma_commit(&bars.s_full[b]);
-              if (b == last) mma_commit(&bars.kempty[st]);
-              if (b == last && kt + 1 == pc.kt_end) mma_commit(&bars.q_empty);
+                  mma_ss(d, qa + (uint64_t)(c * (kSlotBytes >> 4)) + 2 * k, kb + (uint64_t)(c * (S::kKSlot >> 4)) + 2 * k,
+                         idesc_s, (c | k) ? 1u : 0u);
+              mma_commit(&bars.s_full[g]);
+              mma_commit(&bars.kempty[st]);
+            } else {
+              mbar_arrive(&bars.kempty[st]);
             }
-            __syncwarp();
+            if (kt + 1 == pc.kt_end) mma_commit(&bars.q_empty);
           }
-        } else {
+          __syncwarp();
+          n += mine;
+        }
+        ++pieces;
+      }
+    } else {
+      const uint64_t vdesc = make_sdesc(smem_u32(sV), S::kKSlot, 1024);
+      uint32_t used[2] = {0, 0};
+      while (ok && pc.next(p)) {
+        const bool both = S::kSlots == 2 && pc.row_slots(p) == 2;
+        for (int kt = pc.kt; kt < pc.kt_end && ok; ++kt, ++t) {
+          const int first = both || S::kSlots == 1 ? 0 : (kt - pc.kt) & 1, last = both ? 1 : first;
           const uint32_t st = t % S::kVS;
           ok = mbar_wait_warp(&bars.vfull[st], (t / S::kVS) & 1u, ab);
-          for (int b = first; b <= last && ok; ++b) {
-            ok = mbar_wait_warp(&bars.p_full[b], used[b] & 1u, ab);
+          for (int g = first; g <= last && ok; ++g) {
+            const uint32_t n = used[g]++, buf = n & 1u;
+            ok = mbar_wait_warp(&bars.p_full[g][buf], (n >> 1) & 1u, ab);
             if (!ok) break;
-            ++used[b];
             tc_fence_after();
             const uint64_t vb = vdesc + (uint64_t)(st * (S::kVTile >> 4));
-            const uint32_t d = tmem + S::kTmemO + (S::kSlots == 2 ? b * DV : 0);
-            // O starts anew with its first tile of the piece
+            const uint32_t d = tmem + S::kTmemO + g * DV, a = tmem + g * 128 + KT + buf * 32;
+            // O starts anew with the group's first tile of the piece
             const uint32_t add = kt - pc.kt >= (S::kSlots == 2 && !both ? 2 : 1) ? 1u : 0u;
             if (elect_sync()) {
-              mma_ts(d, tmem + b * 128, vb, idesc_o, add);
+              mma_ts(d, a, vb, idesc_o, add);
 #pragma unroll
-              for (int k = 1; k < KT / 16; ++k) mma_ts(d, tmem + b * 128 + k * 8, vb + k * 128, idesc_o, 1u);
-              mma_commit(&bars.o_done[b]);
-              if (b == last) mma_commit(&bars.vempty[st]);
+              for (int k = 1; k < KT / 16; ++k) mma_ts(d, a + k * 8, vb + k * 128, idesc_o, 1u);
+              mma_commit(&bars.o_done[g][buf]);
+              if (g == last) mma_commit(&bars.vempty[st]);
             }
             __syncwarp();
           }
         }
       }
-      ++pieces;
     }
     // every MMA has ended before TMEM and shared memory are given back
-    uint64_t* drain = &bars.drain[s_role ? 0 : 1];
+    uint64_t* drain = &bars.drain[warp == 17 ? 1 : warp == 16 ? 0 : 2];
     if (elect_sync()) {
       mma_commit(drain);
       mbar_wait_quiet(drain, 0, kWaitLimitNs);
     }
     __syncwarp();
+    }
   } else if (warp < 4 * S::kSlots) {
     // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int slot = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    uint32_t used[2] = {0, 0}, t = 0, pieces = 0;
+    uint32_t used = 0, t = 0, pieces = 0;
     bool ok = true;
     ShPiece pc;
     pc.begin(p, u0, u1);
     while (ok && pc.next(p)) {
       const bool both = S::kSlots == 2 && pc.row_slots(p) == 2;
       // ---- the query row, times a power of two, in the operand's order
-      if (pieces && !mbar_wait_warp(&bars.q_empty, (pieces - 1) & 1u, ab)) break;
       const long long grow_row = (long long)pc.row_tile * S::kRT + (both ? slot * 128 : 0) + r;  // of the group
       const bool live = grow_row < (long long)pc.info.members * p.rows;
       const int member = live ? (int)p.by_rows.div((uint32_t)grow_row) : 0;
@@ -580,32 +634,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
       float xs;
       {
         const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)p.q + (int64_t)b * p.q_b + qi * p.q_t + qh * p.q_h);
+        constexpr int kPart = DQK / 8 < 16 ? DQK / 8 : 16;  // vectors held at a time
+        uint4 v[kPart];
+        auto load = [&](int i0) {
+#pragma unroll
+          for (int i = 0; i < kPart; ++i)
+            v[i] = live && i0 + i < DQK / 8 ? __ldg(src + i0 + i) : make_uint4(0u, 0u, 0u, 0u);
+        };
         uint32_t top = 0;
-        if (live)
-#pragma unroll 8
-          for (int i = 0; i < DQK / 8; ++i) {
-            const uint4 v = __ldg(src + i);
-            const uint32_t mx = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                         __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+#pragma unroll
+        for (int i0 = 0; i0 < DQK / 8; i0 += kPart) {
+          load(i0);
+#pragma unroll
+          for (int i = 0; i < kPart; ++i) {
+            const uint32_t mx = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                         __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
             top = max(top, max(mx & 0xffffu, mx >> 16));
           }
+        }
         const uint32_t tf = __float_as_uint(Pack<BF16>::to_f((uint16_t)top));
         const int ex = min(max((int)(tf >> 23) - 127 - 13, -100), 100);  // largest at 2^13 .. 2^14
         const float inv = pow2(-ex);
         xs = p.scale_log2 * pow2(ex);
         if (both || slot == 0) {
           uint8_t* dst = sQ + (both ? slot : 0) * S::kQTile + r * 128;
-#pragma unroll 4
-          for (int i = 0; i < DQK / 8; ++i) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (live) v = __ldg(src + i);
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-            float f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = Pack<BF16>::to_f((uint16_t)(x[e >> 1] >> (16 * (e & 1)))) * inv;
-            *reinterpret_cast<uint4*>(dst + (i >> 3) * kSlotBytes + (((i & 7) ^ (r & 7)) << 4)) =
-                make_uint4(Pack<false>::two(f[0], f[4]), Pack<false>::two(f[1], f[5]), Pack<false>::two(f[2], f[6]),
-                           Pack<false>::two(f[3], f[7]));
+          for (int i0 = 0; i0 < DQK / 8; i0 += kPart) {
+            if (DQK / 8 > kPart) load(i0);  // (else they are still there)
+#pragma unroll
+            for (int k = 0; k < kPart; ++k) {
+              const int i = i0 + k;
+              if (i >= DQK / 8) break;
+              const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+              float f[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] = Pack<BF16>::to_f((uint16_t)(x[e >> 1] >> (16 * (e & 1)))) * inv;
+              *reinterpret_cast<uint4*>(dst + (i >> 3) * kSlotBytes + (((i & 7) ^ (r & 7)) << 4)) =
+                  make_uint4(Pack<false>::two(f[0], f[4]), Pack<false>::two(f[1], f[5]), Pack<false>::two(f[2], f[6]),
+                             Pack<false>::two(f[3], f[7]));
+            }
           }
         }
         fence_proxy_async();
@@ -614,77 +681,88 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
       float m_run = -INFINITY, l_run = 0.0f;
       int v_ref = 0, tiles = 0;  // of this group's O
       for (int kt = pc.kt; kt < pc.kt_end; ++kt, ++t) {
-        const int buf = S::kSlots == 2 ? slot : (kt - pc.kt) & 1;
         if (S::kSlots == 2 && !both && ((kt - pc.kt) & 1) != slot) continue;
+        const uint32_t n = used++, buf = n & 1u;
         ok = mbar_wait_warp(&bars.x_full[t % kXRing], (t / kXRing) & 1u, ab) &&
-             mbar_wait_warp(&bars.s_full[buf], used[buf] & 1u, ab);
+             mbar_wait_warp(&bars.s_full[slot], n & 1u, ab);
         if (!ok) break;
-        ++used[buf];
         tc_fence_after();
-        const float xt = fminf(xs * pow2(k_exp[t % kXRing] - 11), 3.40282347e38f);
-        const int v_new = v_exp[t % kXRing];
-        const uint32_t sb = tmem + lane_off + buf * 128;
-        const int chunks = min(KT, pc.info.tokens - kt * KT) / 32;  // (whole granules)
-        // the row's maximum
-        float mx = -INFINITY;
+        const uint32_t sb = tmem + lane_off + slot * 128;
+        // the row's scores, read at once: then the next ones may be computed
+        uint32_t s[2][32];
+        tmem_ld32(sb, s[0]);
+        tmem_ld32(sb + 32, s[1]);
+        const int2 ke2 = *reinterpret_cast<const int2*>(k_exp[t % kXRing]);
+        const int2 ve2 = *reinterpret_cast<const int2*>(v_exp[t % kXRing]);
+        const int ke[2] = {ke2.x, ke2.y}, ve[2] = {ve2.x, ve2.y};
+        // V's unit: the largest exponent of the piece's tiles
+        const int top = max(ve[0], ve[1]);
+        const int v_new = tiles == 0 ? top : top > v_ref ? min(top + 3, 127) : v_ref;
+        float xt[2];
 #pragma unroll
-        for (int c = 0; c < KT / 32; ++c) {
-          if (c >= chunks) break;
-          uint32_t rr[32];
-          tmem_ld32(sb + c * 32, rr);
-          tmem_ld_wait();
+        for (int c = 0; c < 2; ++c) xt[c] = fminf(fmaxf(xs * pow2(ke[c] - 11), 1.17549435e-38f), 3.40282347e38f);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(&bars.s_free[slot]);
+        float m_half[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          auto score = [&](int i) { return __uint_as_float(s[c][i]); };
           float m4[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            m4[i] = fmax3(__uint_as_float(rr[8 * i]), __uint_as_float(rr[8 * i + 1]),
-                          fmax3(__uint_as_float(rr[8 * i + 2]), __uint_as_float(rr[8 * i + 3]),
-                                fmax3(__uint_as_float(rr[8 * i + 4]), __uint_as_float(rr[8 * i + 5]),
-                                      fmaxf(__uint_as_float(rr[8 * i + 6]), __uint_as_float(rr[8 * i + 7])))));
-          mx = fmax3(mx, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          for (int i = 0; i < 4; ++i) m4[i] = fmaxf(score(i), score(4 + i));
+#pragma unroll
+          for (int k = 8; k < 32; k += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m4[i] = fmax3(m4[i], score(k + i), score(k + 4 + i));
+          m_half[c] = xt[c] * fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
         }
-        const float m_tile = mx * xt;
-        const bool grow = m_tile > m_run + 1.0f;
-        const float m_new = grow ? m_tile : m_run;
-        float alpha = grow ? ex2(m_run - m_new) : 1.0f;
-        m_run = m_new;
+        const float m_tile = fmaxf(m_half[0], m_half[1]);
+        float alpha = 1.0f;
+        if (m_tile > m_run + kLag) {
+          alpha = ex2(m_run - m_tile);
+          m_run = m_tile;
+        }
         const float off = m_run == -INFINITY ? 0.0f : kBias - m_run;
-        const uint64_t x2 = f2_pack(xt, xt), off2 = f2_pack(off, off);
-        uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int c = 0; c < KT / 32; ++c) {
-          uint32_t pk[16];
-          if (c < chunks) {
-            uint32_t rr[32];
-            tmem_ld32(sb + c * 32, rr);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float y0, y1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(rr[2 * i]), __uint_as_float(rr[2 * i + 1])), x2, off2), y0, y1);
-              const float e0 = ex2(y0), e1 = ex2(y1);
-              acc2[i & 3] = f2_add(acc2[i & 3], f2_pack(e0, e1));
-              pk[i] = Pack<false>::two(e0, e1);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = 0u;
-          }
-          tmem_st16(sb + c * 16, pk);
+        // the buffer's earlier P has been read
+        if (n >= 2 && !mbar_wait_warp(&bars.o_done[slot][buf], ((n >> 1) - 1) & 1u, ab)) {
+          ok = false;
+          break;
         }
-        float s0, s1, s2, s3;
-        f2_unpack(f2_add(acc2[0], acc2[1]), s0, s1);
-        f2_unpack(f2_add(acc2[2], acc2[3]), s2, s3);
-        l_run = l_run * alpha + ((s0 + s1) + (s2 + s3));
+        tc_fence_after();
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          // (not above 0; from 2^-39 down P is 0 in fp16, but must not be in the sum)
+          const int lift = max(ve[c] - v_new, -60);
+          const float oc = off + (float)lift;
+          const uint64_t x2 = f2_pack(xt[c], xt[c]), off2 = f2_pack(oc, oc);
+          uint64_t acc2[2] = {0ull, 0ull};
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float y0, y1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), x2, off2), y0, y1);
+            const float e0 = ex2(y0), e1 = ex2(y1);
+            acc2[i & 1] = f2_add(acc2[i & 1], f2_pack(e0, e1));
+            pk[i] = Pack<false>::two(e0, e1);
+          }
+          tmem_st16(sb + KT + buf * 32 + c * 16, pk);
+          float s0, s1;
+          f2_unpack(f2_add(acc2[0], acc2[1]), s0, s1);
+          sum = fmaf(s0 + s1, pow2(-lift), sum);
+        }
+        l_run = l_run * alpha + sum;
         // O of this row so far: the maximum grew, or V's unit did
         if (tiles > 0) {
           if (v_new > v_ref) alpha *= pow2(max(v_ref - v_new, -126));
           if (__any_sync(0xffffffffu, alpha != 1.0f)) {
-            if (S::kSlots == 1 && !mbar_wait_warp(&bars.o_done[buf ^ 1], (used[buf ^ 1] - 1) & 1u, ab)) {
+            if (!mbar_wait_warp(&bars.o_done[slot][buf ^ 1u], ((n - 1) >> 1) & 1u, ab)) {  // (the last product)
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t ob = tmem + lane_off + S::kTmemO + (S::kSlots == 2 ? slot * DV : 0);
+            const uint32_t ob = tmem + lane_off + S::kTmemO + slot * DV;
 #pragma unroll
             for (int c = 0; c < DV / 32; ++c) {
               uint32_t rr[32], lo16[16], hi16[16];
@@ -704,17 +782,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
         ++tiles;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&bars.p_full[buf]);
+        mbar_arrive(&bars.p_full[slot][buf]);
       }
       if (!ok) break;
       // ---- the piece's part: O, maximum and sum of each row
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int buf = S::kSlots == 2 ? slot : i;
-        if (S::kSlots == 2 && i) break;
-        if (used[buf] && !mbar_wait_warp(&bars.o_done[buf], (used[buf] - 1) & 1u, ab)) ok = false;
-      }
-      if (!ok) break;
+      for (uint32_t n = used > 2 ? used - 2 : 0; n < used && ok; ++n)
+        ok = mbar_wait_warp(&bars.o_done[slot][n & 1u], (n >> 1) & 1u, ab);
+      // (nothing reads Q any more, the other group's tiles included)
+      if (!ok || !mbar_wait_warp(&bars.q_empty, pieces & 1u, ab)) break;
       tc_fence_after();
       const bool whole = pc.kt == 0 && pc.kt_end == pc.key_tiles;
       // (where the groups take turns, the second one's part lies beside the first's)
@@ -731,23 +806,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
       }
       if (live) *reinterpret_cast<float2*>(ml) = make_float2(m_run - kBias, l_run);
       if (tiles > 0) {
-        const uint32_t ob = tmem + lane_off + S::kTmemO + (S::kSlots == 2 ? slot * DV : 0);
+        const uint32_t ob = tmem + lane_off + S::kTmemO + slot * DV;
         const float unit = pow2(v_ref - 11);
+        // 32 columns at a time through the warp's part of Q's memory (its MMAs have ended), so
+        // that eight lanes write a row's 128 bytes
+        const int lane = threadIdx.x & 31;
+        float4* tile = reinterpret_cast<float4*>(sQ + slot * S::kQTile + (warp & 3) * 4096);  // [32][8], swizzled
+        const unsigned long long mine = live ? (unsigned long long)o : 0ull;
 #pragma unroll
         for (int c = 0; c < DV / 32; ++c) {
           uint32_t rr[32];
           tmem_ld32(ob + c * 32, rr);
           tmem_ld_wait();
-          if (live)
+          __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float f[8];
+          for (int i = 0; i < 4; ++i) {
+            float f[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(rr[8 * i + e]) * unit;
-              float4* dst = reinterpret_cast<float4*>(o + c * 32 + i * 8);
-              dst[0] = make_float4(f[0], f[2], f[4], f[6]);
-              dst[1] = make_float4(f[1], f[3], f[5], f[7]);
-            }
+            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(rr[8 * i + e]) * unit;
+            tile[lane * 8 + ((2 * i) ^ (lane & 7))] = make_float4(f[0], f[2], f[4], f[6]);
+            tile[lane * 8 + ((2 * i + 1) ^ (lane & 7))] = make_float4(f[1], f[3], f[5], f[7]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = i * 4 + (lane >> 3), col = lane & 7;
+            const unsigned long long dst = __shfl_sync(0xffffffffu, mine, row);
+            if (dst) reinterpret_cast<float4*>(dst)[c * 8 + col] = tile[row * 8 + (col ^ (row & 7))];
+          }
         }
       }
       tc_fence_before();
@@ -762,55 +848,74 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
 }
 
 // ----------------------------------------------------------------- the join
-// A thread takes four dims of a row: the parts of the prefix, in the order of the runs,
-// and the request's own tokens.
+// A group of d_v / 4 threads takes a row, four dims each: its own tokens and the parts
+// of the prefix, in the order of the runs.  Where items are cut into many parts a whole
+// block takes a row, its groups share out the parts and the first one adds up theirs.
 template <bool BF16, int DV>
 __global__ void __launch_bounds__(256) attn_kv_shared_join_kernel(const __grid_constant__ SharedParams p, int most_runs) {
-  constexpr int kLanes = DV / 4, kRows = 256 / kLanes;
+  constexpr int kLanes = DV / 4, kGroups = 256 / kLanes;
+  __shared__ float4 s_acc[kGroups][kLanes];
+  __shared__ float s_mx[kGroups], s_l[kGroups];
   const int64_t all = (int64_t)p.batch * p.c.heads * p.rows;
-  const int d4 = threadIdx.x % kLanes;
-  const ShRuns runs(*p.total_units, most_runs);
-  for (int64_t at = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes; at < all; at += (int64_t)gridDim.x * kRows) {
-    const int b = (int)(at / (p.c.heads * p.rows)), in = (int)(at - (int64_t)b * p.c.heads * p.rows);
-    const int head = in / p.rows, rest = in - head * p.rows;
+  const int d4 = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const ShRuns runs(__ldcg(p.total_units), most_runs);
+  const bool together = runs.runs >= kJoinParts * __ldcg(p.total_units + 1);
+  const int per = together ? 1 : kGroups;
+  for (int64_t at0 = (int64_t)blockIdx.x * per; at0 < all; at0 += (int64_t)gridDim.x * per) {
+    const int64_t at = at0 + (together ? 0 : group);
+    const bool live = at < all;
+    const int b = live ? (int)p.by_request.div((uint32_t)at) : 0, in = live ? (int)(at - (int64_t)b * p.c.heads * p.rows) : 0;
+    const int head = (int)p.by_rows.div(in), rest = in - head * p.rows;
     const int qi = (int)p.by_group.div(rest), qh = head * p.group + rest - qi * p.group;
-    const int64_t own = ((int64_t)b * p.seqlen_q + qi) * p.heads_q + qh;
     const int64_t lse_at = ((int64_t)b * p.heads_q + qh) * p.seqlen_q + qi;
-    float4 acc = *reinterpret_cast<const float4*>(p.own_o + own * DV + d4 * 4);
-    float lse = p.own_lse[lse_at];
-    const int g = p.group_of[b];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float mx = -INFINITY, sum = 0.0f, lse = -INFINITY;
+    auto add = [&](const float4& y, float m, float l) {
+      if (l == 0.0f) return;  // a part without tiles
+      const float to = fmaxf(mx, m), f = ex2(m - to), a = mx == -INFINITY ? 0.0f : ex2(mx - to);
+      mx = to;
+      sum = fmaf(sum, a, l * f);
+      acc.x = fmaf(acc.x, a, y.x * f), acc.y = fmaf(acc.y, a, y.y * f);
+      acc.z = fmaf(acc.z, a, y.z * f), acc.w = fmaf(acc.w, a, y.w * f);
+    };
+    const int g = live ? p.group_of[b] : -1;
+    if (live && (!together || group == 0)) {  // its own tokens
+      acc = *reinterpret_cast<const float4*>(p.own_o + (((int64_t)b * p.seqlen_q + qi) * p.heads_q + qh) * DV + d4 * 4);
+      lse = p.own_lse[lse_at];
+      mx = lse * 1.4426950408889634f;
+      sum = 1.0f;
+    }
     if (g >= 0) {
       const ShGroup info = ((const ShGroup*)p.group_info)[g];
       const int key_tiles = sh_key_tiles(p, info), row_tiles = sh_row_tiles(p, info);
       const long long row = (long long)(b - info.first) * p.rows + rest;
-      const int rt = (int)(row / p.row_tile), r = (int)(row - (long long)rt * p.row_tile);
+      const int rt = (int)(row >> (p.row_tile == 256 ? 8 : 7)), r = (int)(row & (p.row_tile - 1));
       const long long left = (long long)info.members * p.rows - (long long)rt * p.row_tile;
-      const int parts = p.row_tile == 256 && left <= 128 ? 2 : 1;
-      const long long u = info.unit0 + ((long long)head * row_tiles + rt) * key_tiles;
-      const int k0 = runs.of(u), k1 = runs.of(u + key_tiles - 1);
-      float mx = lse * 1.4426950408889634f, sum = 1.0f;
-      auto add = [&](const float* o, const float* ml) {
-        const float2 s = *reinterpret_cast<const float2*>(ml);
-        if (s.y == 0.0f) return;  // a part without tiles
-        const float4 y = *reinterpret_cast<const float4*>(o + d4 * 4);
-        const float to = fmaxf(mx, s.x), f = ex2(s.x - to), a = ex2(mx - to);
-        mx = to;
-        sum = fmaf(sum, a, s.y * f);
-        acc.x = fmaf(acc.x, a, y.x * f), acc.y = fmaf(acc.y, a, y.y * f);
-        acc.z = fmaf(acc.z, a, y.z * f), acc.w = fmaf(acc.w, a, y.w * f);
-      };
-      for (int part = 0; part < parts; ++part) {
-        if (k0 == k1) {
-          const int64_t i = part * all + at;
-          add(p.row_o + i * DV, p.row_ml + i * 2);
-        } else {
+      const int halves = p.row_tile == 256 && left <= 128 ? 2 : 1;
+      const int u = info.unit0 + (head * row_tiles + rt) * key_tiles;
+      const int k0 = runs.of(u), np = runs.of(u + key_tiles - 1) - k0 + 1;
+      const int step = together ? kGroups : 1;
 #pragma unroll 4
-          for (int k = k0; k <= k1; ++k) {
-            const int64_t i = ((int64_t)k * 2 + (k == k0 ? 1 : 0)) * p.row_tile + part * 128 + r;
-            add(p.cut_o + i * DV, p.cut_ml + i * 2);
-          }
-        }
+      for (int i = together ? group : 0; i < halves * np; i += step) {
+        const int half = i >= np, k = i - half * np;
+        const int64_t x = np == 1 ? half * all + at
+                                  : ((int64_t)(k0 + k) * 2 + (k == 0 ? 1 : 0)) * p.row_tile + half * 128 + r;
+        const float2 s = *reinterpret_cast<const float2*>((np == 1 ? p.row_ml : p.cut_ml) + x * 2);
+        add(*reinterpret_cast<const float4*>((np == 1 ? p.row_o : p.cut_o) + x * DV + d4 * 4), s.x, s.y);
       }
+    }
+    if (together) {
+      __syncthreads();
+      s_acc[group][d4] = acc;
+      if (d4 == 0) s_mx[group] = mx, s_l[group] = sum;
+      __syncthreads();
+      if (group > 0) continue;
+#pragma unroll
+      for (int k = 1; k < kGroups; ++k) add(s_acc[k][d4], s_mx[k], s_l[k]);
+    }
+    if (!live) continue;
+    if (g >= 0) {
       const float inv = 1.0f / sum;
       acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       lse = (mx + log2f(sum)) * 0.6931471805599453f;
@@ -841,8 +946,7 @@ cudaError_t sh_launch(const SharedParams& p, int num_sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  k<<<num_sms, kThreads, S::kSmem, st>>>(p);
-  return cudaGetLastError();
+  return launch_early(k, (unsigned)num_sms, kThreads, S::kSmem, st, p);
 }
 
 template <bool BF16>
@@ -856,21 +960,20 @@ cudaError_t sh_dims(const SharedParams& p, int num_sms, cudaStream_t st) {
 
 template <bool BF16>
 cudaError_t sh_join(const SharedParams& p, int num_sms, cudaStream_t st) {
-  const int64_t rows = (int64_t)p.batch * p.c.heads * p.rows, per = 256 / (p.c.d_v / 4);
-  const unsigned blocks = (unsigned)std::min<int64_t>((rows + per - 1) / per, (int64_t)num_sms * 8);
+  const int64_t rows = (int64_t)p.batch * p.c.heads * p.rows;
+  const unsigned blocks = (unsigned)std::min<int64_t>(rows, (int64_t)num_sms * 8);
   switch (p.c.d_v) {
-    case 64: attn_kv_shared_join_kernel<BF16, 64><<<blocks, 256, 0, st>>>(p, num_sms); break;
-    case 128: attn_kv_shared_join_kernel<BF16, 128><<<blocks, 256, 0, st>>>(p, num_sms); break;
-    default: attn_kv_shared_join_kernel<BF16, 256><<<blocks, 256, 0, st>>>(p, num_sms); break;
+    case 64: return launch_early(attn_kv_shared_join_kernel<BF16, 64>, blocks, 256, 0, st, p, num_sms);
+    case 128: return launch_early(attn_kv_shared_join_kernel<BF16, 128>, blocks, 256, 0, st, p, num_sms);
+    default: return launch_early(attn_kv_shared_join_kernel<BF16, 256>, blocks, 256, 0, st, p, num_sms);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace
 
 void shared_tiles(int d_v, int& row_tile, int& key_tile) {
   row_tile = d_v > 128 ? 128 : 256;
-  key_tile = d_v > 128 ? 64 : 128;
+  key_tile = KT;
 }
 size_t shared_group_bytes() { return sizeof(ShGroup); }
 

@@ -108,6 +108,31 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, c
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab));
 }
 
+// mbar_wait_warp for kernels whose warps compete for issue slots: the hardware may
+// hold the warp back for a while instead of a loop that polls.
+__device__ __forceinline__ bool mbar_wait_warp_lean(uint64_t* bar, uint32_t parity, const Abort& ab) {
+  const uint32_t addr = smem_u32(bar);
+  unsigned long long t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity), "r"(1000u)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok != 0)) return true;
+    const unsigned long long now = globaltimer();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > ab.limit_ns) {
+      if (ab.status && !*ab.flag) atomicExch(ab.status, DEV_TIMEOUT);
+      *ab.flag = 1;
+    }
+    if (__any_sync(0xffffffffu, *ab.flag != 0)) return false;
+  }
+}
+
 // Wait without raising the abort flag (used while unwinding after an abort
 // to let copies in flight land).  Returns false after `limit_ns`.
 __device__ __forceinline__ bool mbar_wait_quiet(uint64_t* bar, uint32_t parity,
@@ -258,6 +283,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
         "=r"(r[31])
+      : "r"(taddr));
+}
+// 32 lanes x 16 columns
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_ld_wait() {

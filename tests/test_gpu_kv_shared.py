@@ -178,6 +178,16 @@ def test_shared_values_that_grow(step, dqk, dv):
         x.check(x.q(1, 4))
 
 
+def test_shared_values_of_nothing():
+    """Quarters of tiles whose V is zero, or 2^-60 of the others, still count in the sum."""
+    x = Groups([(1024, [3] * 40)], 1, 128, 128, 64, BF, seed=16)
+    at = torch.arange(len(x.slots)) // 32 % 4
+    for small in (0.0, 2.0 ** -60, 2.0 ** -100):
+        x.v = (torch.randn(x.v.shape, generator=x.g) * torch.where(at == 1, small, 1.0)[:, None, None]).to(BF)
+        x.write()
+        x.check(x.q(1, 4))
+
+
 def test_shared_scores_far_apart():
     """Rows whose maximum moves by hundreds from tile to tile, and back."""
     x = Groups([(1024, [3] * 40)], 1, 128, 128, 64, BF, seed=6)
