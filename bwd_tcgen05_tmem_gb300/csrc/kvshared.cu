@@ -335,6 +335,7 @@ struct ShSide {
       }
     }
   }
+  // V's half-words of two quarters of a group are put side by side, as K's words hold them.
   __device__ __forceinline__ void load_codes(const uint8_t* codes, const long long* rows, int row8, int c) {
     const uint8_t* const mine = codes + row8 * (D / 2) + c * 4 * G;
 #pragma unroll
@@ -360,7 +361,16 @@ struct ShSide {
   }
   // dst: row row8 of the warp's tokens in the operand (rows of 128 bytes, swizzled).
   // (Lanes 8 p .. + 7 hold rows p and p + 4, whose chunks lie in different banks.)
-  template <bool K>
+  __device__ __forceinline__ void pair_halves() {
+#pragma unroll
+    for (int i = 0; i < SETS; ++i) {
+      uint32_t y[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) y[g] = __byte_perm(w[i][g >> 1], w[i][(G + g) >> 1], (g & 1) ? 0x7632 : 0x5410);
+#pragma unroll
+      for (int g = 0; g < G; ++g) w[i][g] = y[g];
+    }
+  }
   __device__ __forceinline__ void store(uint32_t dst, int slot_bytes, int row8, int c) const {
     const int quad = (threadIdx.x & 31) & ~3;
 #pragma unroll
@@ -368,8 +378,7 @@ struct ShSide {
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const uint32_t sb = __shfl_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&h[i][g >> 2]), quad | (g & 3));
-        const uint32_t x = K ? w[i][g] : __byte_perm(w[i][g >> 1], w[i][(G + g) >> 1], (g & 1) ? 0x7632 : 0x5410);
-        const uint4 y = scaled_codes(x, *reinterpret_cast<const __half2*>(&sb));
+        const uint4 y = scaled_codes(w[i][g], *reinterpret_cast<const __half2*>(&sb));
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
                          dst + (g >> 1) * slot_bytes + i * 1024 + ((((g & 1) * 4 + c) ^ row8) << 4)),
                      "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
@@ -378,18 +387,15 @@ struct ShSide {
   }
 };
 
-// One of the four warps that turn a side's codes into its operand.
-template <int DQK, int DV, bool K>
-__device__ __forceinline__ void sh_convert(const SharedParams& p, uint8_t* operand, ShBars& bars, int (*x_exp)[2],
+// One of the four warps that turn a side's codes (D dims) into its operand.  (K's and V's
+// share this code where they can: the loops of an SM's warps do not fit its first
+// instruction cache.)
+template <int D, int STAGES>
+__device__ __forceinline__ void sh_convert(const uint8_t* codes, const uint16_t* scales, bool is_k, uint8_t* operand,
+                                           uint64_t* full, uint64_t* empty, ShBars& bars, int (*x_exp)[2],
                                            const ShRows* rows, int n, const Abort& ab) {
-  using S = ShShape<DQK, DV>;
-  constexpr int D = K ? DQK : DV, kStages = K ? S::kKS : S::kVS, kTileBytes = K ? S::kKTile : S::kVTile;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, half = warp & 1;
   const int c = lane & 3, row8 = (lane >> 3) + ((lane >> 2) & 1) * 4;
-  const uint8_t* codes = K ? p.c.k_codes : p.c.v_codes;
-  const uint16_t* scales = K ? p.c.k_scales : p.c.v_scales;
-  uint64_t* full = K ? bars.kfull : bars.vfull;
-  uint64_t* empty = K ? bars.kempty : bars.vempty;
   const uint32_t dst = smem_u32(operand) + (half * 32 + row8) * 128;
   ShSide<D, 4> x;
   auto load = [&](int t) {
@@ -401,17 +407,18 @@ __device__ __forceinline__ void sh_convert(const SharedParams& p, uint8_t* opera
     if (lane == 0) mbar_arrive(&bars.rows_empty[slot]);
     return true;
   };
-  int t = warp >> 1;
-  if (t >= n || !load(t)) return;
-  for (; t < n; t += 2) {
-    const int e = max((int)(x.top() >> 7) - 127, kExpLow), stage = t % kStages;
+#pragma unroll 1
+  for (int t = warp >> 1; t < n; t += 2) {
+    if (t < 2 && !load(t)) return;
+    const int e = max((int)(x.top() >> 7) - 127, kExpLow), stage = t % STAGES;
     if (lane == 0) {
       x_exp[t % kXRing][half] = e;
       mbar_arrive(&bars.x_full[t % kXRing]);
     }
     x.halves(pow2(11 - e));
-    if (t >= kStages && !mbar_wait_warp(&empty[stage], (uint32_t)(t / kStages - 1) & 1u, ab)) return;
-    x.template store<K>(dst + stage * kTileBytes, S::kKSlot, row8, c);
+    if (!is_k) x.pair_halves();
+    if (t >= STAGES && !mbar_wait_warp(&empty[stage], (uint32_t)(t / STAGES - 1) & 1u, ab)) return;
+    x.store(dst + stage * (KT * 2 * D), KT * 128, row8, c);
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(&full[stage]);
@@ -520,10 +527,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
   if (idle) {
     // (no run for this block)
   } else if (warp >= 8 && warp < 16) {
-    if (warp < 12)
-      sh_convert<DQK, DV, true>(p, sK, bars, k_exp, rows, u1 - u0, ab);
+    const bool is_k = warp < 12;
+    if (DQK == DV || is_k)
+      sh_convert<DQK, S::kKS>(is_k ? p.c.k_codes : p.c.v_codes, is_k ? p.c.k_scales : p.c.v_scales, is_k, is_k ? sK : sV,
+                              is_k ? bars.kfull : bars.vfull, is_k ? bars.kempty : bars.vempty, bars,
+                              is_k ? k_exp : v_exp, rows, u1 - u0, ab);
     else
-      sh_convert<DQK, DV, false>(p, sV, bars, v_exp, rows, u1 - u0, ab);
+      sh_convert<DV, S::kVS>(p.c.v_codes, p.c.v_scales, false, sV, bars.vfull, bars.vempty, bars, v_exp, rows, u1 - u0, ab);
   } else if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 18) sh_look_up<DQK, DV>(p, bars, rows, u0, u1, ab);
