@@ -312,12 +312,14 @@ struct ShRows {
   long long row[4];
 };
 
-// One side of a tile in a lane: the words of its quarter (4 G bytes) of the rows 8 i +
-// row8, and of those rows' scales the groups c, c + 4.
-template <int D, int SETS>
+// One side of a tile in a lane: the words of its quarter (4 G bytes, G groups of 32 dims)
+// of the rows 8 i + row8, and of those rows' scales the groups c, c + 4.  K has GK
+// groups, V GV.
+template <int GK, int GV, int SETS>
 struct ShSide {
-  static constexpr int G = D / 32, kOwn = (G + 3) / 4;
-  uint32_t w[SETS][G];
+  static constexpr int GM = GK > GV ? GK : GV, kOwn = (GM + 3) / 4;
+  int G;
+  uint32_t w[SETS][GM];
   uint32_t s[SETS][kOwn];
   __half2 h[SETS][kOwn];
 
@@ -330,16 +332,27 @@ struct ShSide {
       const uint16_t* src = mine + max(at, 0ll) * G + (i & 1) * 8 * G;
 #pragma unroll
       for (int j = 0; j < kOwn; ++j) {
-        s[i][j] = G % 4 == 0 || c + 4 * j < G ? __ldg(src + 4 * j) : 0u;
+        s[i][j] = (GK == GV && GM % 4 == 0) || c + 4 * j < G ? __ldg(src + 4 * j) : 0u;
         if (at < 0) s[i][j] = 0u;
       }
     }
   }
-  // V's half-words of two quarters of a group are put side by side, as K's words hold them.
   __device__ __forceinline__ void load_codes(const uint8_t* codes, const long long* rows, int row8, int c) {
-    const uint8_t* const mine = codes + row8 * (D / 2) + c * 4 * G;
+    const uint8_t* const mine = codes + row8 * (16 * G) + c * 4 * G;
 #pragma unroll
-    for (int i = 0; i < SETS; ++i) row_words<G>(mine + max(rows[i >> 1], 0ll) * (D / 2) + (i & 1) * 8 * (D / 2), w[i]);
+    for (int i = 0; i < SETS; ++i) {
+      const uint8_t* src = mine + max(rows[i >> 1], 0ll) * (16 * G) + (i & 1) * 8 * (16 * G);
+      if constexpr (GK == GV) {
+        row_words<GM>(src, w[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < GM; j += 2)
+          if (j < min(GK, GV) || j < G) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src) + j / 2);
+            w[i][j] = v.x, w[i][j + 1] = v.y;
+          }
+      }
+    }
   }
   // the largest finite scale's bits
   __device__ __forceinline__ uint32_t top() const {
@@ -359,45 +372,51 @@ struct ShSide {
 #pragma unroll
       for (int j = 0; j < kOwn; ++j) h[i][j] = __float2half2_rn(__uint_as_float(s[i][j] << 16) * f);
   }
-  // dst: row row8 of the warp's tokens in the operand (rows of 128 bytes, swizzled).
-  // (Lanes 8 p .. + 7 hold rows p and p + 4, whose chunks lie in different banks.)
+  // V's half-words of two quarters of a group side by side, as K's words hold them
   __device__ __forceinline__ void pair_halves() {
 #pragma unroll
     for (int i = 0; i < SETS; ++i) {
-      uint32_t y[G];
+      uint32_t y[GV];
 #pragma unroll
-      for (int g = 0; g < G; ++g) y[g] = __byte_perm(w[i][g >> 1], w[i][(G + g) >> 1], (g & 1) ? 0x7632 : 0x5410);
+      for (int g = 0; g < GV; ++g) y[g] = __byte_perm(w[i][g >> 1], w[i][(GV + g) >> 1], (g & 1) ? 0x7632 : 0x5410);
 #pragma unroll
-      for (int g = 0; g < G; ++g) w[i][g] = y[g];
+      for (int g = 0; g < GV; ++g) w[i][g] = y[g];
     }
   }
-  __device__ __forceinline__ void store(uint32_t dst, int slot_bytes, int row8, int c) const {
+  // dst: row row8 of the warp's tokens in the operand (rows of 128 bytes, swizzled).
+  // (Lanes 8 p .. + 7 hold rows p and p + 4, whose chunks lie in different banks.)
+  __device__ __forceinline__ void store(uint32_t dst, int row8, int c) const {
     const int quad = (threadIdx.x & 31) & ~3;
 #pragma unroll
     for (int i = 0; i < SETS; ++i)
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
+      for (int g = 0; g < GM; ++g) {
+        if (g >= min(GK, GV) && g >= G) break;
         const uint32_t sb = __shfl_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&h[i][g >> 2]), quad | (g & 3));
         const uint4 y = scaled_codes(w[i][g], *reinterpret_cast<const __half2*>(&sb));
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                         dst + (g >> 1) * slot_bytes + i * 1024 + ((((g & 1) * 4 + c) ^ row8) << 4)),
+                         dst + (g >> 1) * (KT * 128) + i * 1024 + ((((g & 1) * 4 + c) ^ row8) << 4)),
                      "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
                      : "memory");
       }
   }
 };
 
-// One of the four warps that turn a side's codes (D dims) into its operand.  (K's and V's
-// share this code where they can: the loops of an SM's warps do not fit its first
-// instruction cache.)
-template <int D, int STAGES>
+// One of the four warps that turn a side's codes into its operand.  (K's and V's share this
+// code, and loops that run rarely are not unrolled: what an SM's warps run in a tile has
+// to fit its first instruction cache.  With two copies 256 requests over 32K tokens took
+// 233 us, 192 us with one.)
+template <int DQK, int DV>
 __device__ __forceinline__ void sh_convert(const uint8_t* codes, const uint16_t* scales, bool is_k, uint8_t* operand,
                                            uint64_t* full, uint64_t* empty, ShBars& bars, int (*x_exp)[2],
                                            const ShRows* rows, int n, const Abort& ab) {
+  constexpr int kStages = ShShape<DQK, DV>::kKS;
+  static_assert(kStages == ShShape<DQK, DV>::kVS, "one code for both sides");
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, half = warp & 1;
   const int c = lane & 3, row8 = (lane >> 3) + ((lane >> 2) & 1) * 4;
   const uint32_t dst = smem_u32(operand) + (half * 32 + row8) * 128;
-  ShSide<D, 4> x;
+  ShSide<DQK / 32, DV / 32, 4> x;
+  x.G = is_k ? DQK / 32 : DV / 32;
   auto load = [&](int t) {
     const int slot = t % kRowRing;
     if (!mbar_wait_warp(&bars.rows_full[slot], (uint32_t)(t / kRowRing) & 1u, ab)) return false;
@@ -408,20 +427,21 @@ __device__ __forceinline__ void sh_convert(const uint8_t* codes, const uint16_t*
     return true;
   };
 #pragma unroll 1
-  for (int t = warp >> 1; t < n; t += 2) {
-    if (t < 2 && !load(t)) return;
-    const int e = max((int)(x.top() >> 7) - 127, kExpLow), stage = t % STAGES;
-    if (lane == 0) {
-      x_exp[t % kXRing][half] = e;
-      mbar_arrive(&bars.x_full[t % kXRing]);
+  for (int t = (warp >> 1) - 2; t < n; t += 2) {
+    if (t >= 0) {
+      const int e = max((int)(x.top() >> 7) - 127, kExpLow), stage = t % kStages;
+      if (lane == 0) {
+        x_exp[t % kXRing][half] = e;
+        mbar_arrive(&bars.x_full[t % kXRing]);
+      }
+      x.halves(pow2(11 - e));
+      if (!is_k) x.pair_halves();
+      if (t >= kStages && !mbar_wait_warp(&empty[stage], (uint32_t)(t / kStages - 1) & 1u, ab)) return;
+      x.store(dst + stage * (KT * 64 * x.G), row8, c);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[stage]);
     }
-    x.halves(pow2(11 - e));
-    if (!is_k) x.pair_halves();
-    if (t >= STAGES && !mbar_wait_warp(&empty[stage], (uint32_t)(t / STAGES - 1) & 1u, ab)) return;
-    x.store(dst + stage * (KT * 2 * D), KT * 128, row8, c);
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&full[stage]);
     if (t + 2 < n && !load(t + 2)) return;
   }
 }
@@ -528,12 +548,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
     // (no run for this block)
   } else if (warp >= 8 && warp < 16) {
     const bool is_k = warp < 12;
-    if (DQK == DV || is_k)
-      sh_convert<DQK, S::kKS>(is_k ? p.c.k_codes : p.c.v_codes, is_k ? p.c.k_scales : p.c.v_scales, is_k, is_k ? sK : sV,
-                              is_k ? bars.kfull : bars.vfull, is_k ? bars.kempty : bars.vempty, bars,
-                              is_k ? k_exp : v_exp, rows, u1 - u0, ab);
-    else
-      sh_convert<DV, S::kVS>(p.c.v_codes, p.c.v_scales, false, sV, bars.vfull, bars.vempty, bars, v_exp, rows, u1 - u0, ab);
+    sh_convert<DQK, DV>(is_k ? p.c.k_codes : p.c.v_codes, is_k ? p.c.k_scales : p.c.v_scales, is_k, is_k ? sK : sV,
+                        is_k ? bars.kfull : bars.vfull, is_k ? bars.kempty : bars.vempty, bars, is_k ? k_exp : v_exp,
+                        rows, u1 - u0, ab);
   } else if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 18) sh_look_up<DQK, DV>(p, bars, rows, u0, u1, ab);
@@ -644,15 +661,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
       float xs;
       {
         const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)p.q + (int64_t)b * p.q_b + qi * p.q_t + qh * p.q_h);
-        constexpr int kPart = DQK / 8 < 16 ? DQK / 8 : 16;  // vectors held at a time
+        constexpr int kPart = 8;  // vectors held at a time
         uint4 v[kPart];
         auto load = [&](int i0) {
 #pragma unroll
-          for (int i = 0; i < kPart; ++i)
-            v[i] = live && i0 + i < DQK / 8 ? __ldg(src + i0 + i) : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < kPart; ++i) v[i] = live ? __ldg(src + i0 + i) : make_uint4(0u, 0u, 0u, 0u);
         };
         uint32_t top = 0;
-#pragma unroll
+#pragma unroll 1
         for (int i0 = 0; i0 < DQK / 8; i0 += kPart) {
           load(i0);
 #pragma unroll
@@ -668,18 +684,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
         xs = p.scale_log2 * pow2(ex);
         if (both || slot == 0) {
           uint8_t* dst = sQ + (both ? slot : 0) * S::kQTile + r * 128;
-#pragma unroll
-          for (int i0 = 0; i0 < DQK / 8; i0 += kPart) {
-            if (DQK / 8 > kPart) load(i0);  // (else they are still there)
+#pragma unroll 1
+          for (int i0 = 0; i0 < DQK / 8; i0 += kPart, dst += kSlotBytes) {
+            load(i0);
 #pragma unroll
             for (int k = 0; k < kPart; ++k) {
-              const int i = i0 + k;
-              if (i >= DQK / 8) break;
               const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
               float f[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) f[e] = Pack<BF16>::to_f((uint16_t)(x[e >> 1] >> (16 * (e & 1)))) * inv;
-              *reinterpret_cast<uint4*>(dst + (i >> 3) * kSlotBytes + (((i & 7) ^ (r & 7)) << 4)) =
+              *reinterpret_cast<uint4*>(dst + ((k ^ (r & 7)) << 4)) =
                   make_uint4(Pack<false>::two(f[0], f[4]), Pack<false>::two(f[1], f[5]), Pack<false>::two(f[2], f[6]),
                              Pack<false>::two(f[3], f[7]));
             }
@@ -773,18 +787,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
             }
             tc_fence_after();
             const uint32_t ob = tmem + lane_off + S::kTmemO + slot * DV;
-#pragma unroll
-            for (int c = 0; c < DV / 32; ++c) {
-              uint32_t rr[32], lo16[16], hi16[16];
-              tmem_ld32(ob + c * 32, rr);
+#pragma unroll 1
+            for (int c = 0; c < DV; c += 16) {
+              uint32_t rr[16];
+              tmem_ld16(ob + c, rr);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                lo16[i] = __float_as_uint(__uint_as_float(rr[i]) * alpha);
-                hi16[i] = __float_as_uint(__uint_as_float(rr[16 + i]) * alpha);
-              }
-              tmem_st16(ob + c * 32, lo16);
-              tmem_st16(ob + c * 32 + 16, hi16);
+              for (int i = 0; i < 16; ++i) rr[i] = __float_as_uint(__uint_as_float(rr[i]) * alpha);
+              tmem_st16(ob + c, rr);
             }
           }
         }
@@ -823,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
         const int lane = threadIdx.x & 31;
         float4* tile = reinterpret_cast<float4*>(sQ + slot * S::kQTile + (warp & 3) * 4096);  // [32][8], swizzled
         const unsigned long long mine = live ? (unsigned long long)o : 0ull;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < DV / 32; ++c) {
           uint32_t rr[32];
           tmem_ld32(ob + c * 32, rr);
