@@ -955,6 +955,7 @@ __global__ void __launch_bounds__(THREADS) attn_kv_join_items_kernel(
   const int at = blockIdx.x / rows, row = blockIdx.x - at * rows;
   const int b = at / per_seq, item = at - b * per_seq;
   const int kvh = (int)p.by_blocks.div(item), row_all = (item - kvh * p.row_blocks) * ROWS + row;
+  asm volatile("griddepcontrol.launch_dependents;");  // (a kernel that joins this with other parts)
   empty_rows<BF16>(p, THREADS);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row_all >= p.rows || seq_len(p, b) == 0) return;
@@ -989,6 +990,7 @@ __global__ void __launch_bounds__(kByRunThreads) attn_kv_join_runs_kernel(
   __shared__ float sm_l[kByRunThreads], sm_m[kByRunThreads];
   __shared__ int s_at[kWarps], s_k0[kWarps], s_np[kWarps];
   const int per_seq = p.c.heads * p.row_blocks, tid = threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;");
   empty_rows<BF16>(p, kByRunThreads);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid < kWarps) {

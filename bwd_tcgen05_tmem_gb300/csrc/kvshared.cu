@@ -660,44 +660,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
       const int b = pc.info.first + member;
       float xs;
       {
-        const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)p.q + (int64_t)b * p.q_b + qi * p.q_t + qh * p.q_h);
-        constexpr int kPart = 8;  // vectors held at a time
-        uint4 v[kPart];
-        auto load = [&](int i0) {
-#pragma unroll
-          for (int i = 0; i < kPart; ++i) v[i] = live ? __ldg(src + i0 + i) : make_uint4(0u, 0u, 0u, 0u);
+        // The warp copies its 32 rows as they are, whole lines at a time, to where their operand
+        // goes (the second group's is not used where the groups share the rows); then each
+        // thread converts its own row there.
+        constexpr int kVecs = DQK / 8;
+        const unsigned long long src =
+            live ? (unsigned long long)((const uint16_t*)p.q + (int64_t)b * p.q_b + qi * p.q_t + qh * p.q_h) : 0ull;
+        uint8_t* const tile = sQ + slot * S::kQTile;
+        auto place = [&](int row, int i) {
+          return reinterpret_cast<uint4*>(tile + (i >> 3) * kSlotBytes + row * 128 + (((i & 7) ^ (row & 7)) << 4));
         };
+        const int lane = threadIdx.x & 31, row0 = r - lane;
+#pragma unroll 4
+        for (int k = 0; k < kVecs; ++k) {
+          const int at = k * 32 + lane, row = at / kVecs, i = at - row * kVecs;
+          const unsigned long long from = __shfl_sync(0xffffffffu, src, row);
+          *place(row0 + row, i) = from ? __ldg(reinterpret_cast<const uint4*>(from) + i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
         uint32_t top = 0;
-#pragma unroll 1
-        for (int i0 = 0; i0 < DQK / 8; i0 += kPart) {
-          load(i0);
-#pragma unroll
-          for (int i = 0; i < kPart; ++i) {
-            const uint32_t mx = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
-                                         __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
-            top = max(top, max(mx & 0xffffu, mx >> 16));
-          }
+#pragma unroll 8
+        for (int i = 0; i < kVecs; ++i) {
+          const uint4 v = *place(r, i);
+          const uint32_t mx = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+          top = max(top, max(mx & 0xffffu, mx >> 16));
         }
         const uint32_t tf = __float_as_uint(Pack<BF16>::to_f((uint16_t)top));
         const int ex = min(max((int)(tf >> 23) - 127 - 13, -100), 100);  // largest at 2^13 .. 2^14
         const float inv = pow2(-ex);
         xs = p.scale_log2 * pow2(ex);
-        if (both || slot == 0) {
-          uint8_t* dst = sQ + (both ? slot : 0) * S::kQTile + r * 128;
-#pragma unroll 1
-          for (int i0 = 0; i0 < DQK / 8; i0 += kPart, dst += kSlotBytes) {
-            load(i0);
+#pragma unroll 4
+        for (int i = 0; i < kVecs; ++i) {
+          const uint4 v = *place(r, i);
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+          float f[8];
 #pragma unroll
-            for (int k = 0; k < kPart; ++k) {
-              const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-              float f[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] = Pack<BF16>::to_f((uint16_t)(x[e >> 1] >> (16 * (e & 1)))) * inv;
-              *reinterpret_cast<uint4*>(dst + ((k ^ (r & 7)) << 4)) =
-                  make_uint4(Pack<false>::two(f[0], f[4]), Pack<false>::two(f[1], f[5]), Pack<false>::two(f[2], f[6]),
-                             Pack<false>::two(f[3], f[7]));
-            }
-          }
+          for (int e = 0; e < 8; ++e) f[e] = Pack<BF16>::to_f((uint16_t)(x[e >> 1] >> (16 * (e & 1)))) * inv;
+          *place(r, i) = make_uint4(Pack<false>::two(f[0], f[4]), Pack<false>::two(f[1], f[5]), Pack<false>::two(f[2], f[6]),
+                                    Pack<false>::two(f[3], f[7]));
         }
         fence_proxy_async();
         mbar_arrive(&bars.q_full);
@@ -872,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
 // of the prefix, in the order of the runs.  Where items are cut into many parts a whole
 // block takes a row, its groups share out the parts and the first one adds up theirs.
 template <bool BF16, int DV>
-__global__ void __launch_bounds__(256) attn_kv_shared_join_kernel(const __grid_constant__ SharedParams p, int most_runs) {
+__global__ void __launch_bounds__(256, 6) attn_kv_shared_join_kernel(const __grid_constant__ SharedParams p, int most_runs) {
   constexpr int kLanes = DV / 4, kGroups = 256 / kLanes;
   __shared__ float4 s_acc[kGroups][kLanes];
   __shared__ float s_mx[kGroups], s_l[kGroups];

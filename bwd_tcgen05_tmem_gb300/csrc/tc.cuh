@@ -108,31 +108,6 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, c
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab));
 }
 
-// mbar_wait_warp for kernels whose warps compete for issue slots: the hardware may
-// hold the warp back for a while instead of a loop that polls.
-__device__ __forceinline__ bool mbar_wait_warp_lean(uint64_t* bar, uint32_t parity, const Abort& ab) {
-  const uint32_t addr = smem_u32(bar);
-  unsigned long long t0 = 0;
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(addr), "r"(parity), "r"(1000u)
-        : "memory");
-    if (__all_sync(0xffffffffu, ok != 0)) return true;
-    const unsigned long long now = globaltimer();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > ab.limit_ns) {
-      if (ab.status && !*ab.flag) atomicExch(ab.status, DEV_TIMEOUT);
-      *ab.flag = 1;
-    }
-    if (__any_sync(0xffffffffu, *ab.flag != 0)) return false;
-  }
-}
-
 // Wait without raising the abort flag (used while unwinding after an abort
 // to let copies in flight land).  Returns false after `limit_ns`.
 __device__ __forceinline__ bool mbar_wait_quiet(uint64_t* bar, uint32_t parity,
