@@ -19,6 +19,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kcommon.cuh"
 #include "kv.h"
@@ -33,7 +34,8 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kKeys = 16384;  // candidates of a block whose weights stay in shared memory
-constexpr int kStage = 40960;  // bytes of a round's rows of a block
+constexpr int kStage = 45056;  // bytes of a round's rows of a block, at most
+constexpr int kMinSlice = 2048;  // candidates of a block: fewer are not worth another block's barriers
 
 // A weight as a number whose order is the weights': NaN below all, -0 like 0.
 __device__ __forceinline__ uint32_t order_of(float w) {
@@ -42,28 +44,33 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"((uint64_t)__cvta_generic_to_global(src))
-               : "memory");
+template <int N>
+__device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src) {
+  if constexpr (N == 16)
+    copy16(dst, src);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"((uint64_t)__cvta_generic_to_global(src)),
+                 "n"(N)
+                 : "memory");
 }
 
-// Inclusive sum over the block (all threads); `total` is everybody's.
-__device__ __forceinline__ int block_scan(int x, int* s_warp, int& total) {
+// Inclusive sums over the block of two counts (all threads); the totals are everybody's.
+__device__ __forceinline__ int2 block_scan(int2 x, int2* s_warp, int2& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int y0 = __shfl_up_sync(0xffffffffu, x.x, o), y1 = __shfl_up_sync(0xffffffffu, x.y, o);
+    if (lane >= o) x.x += y0, x.y += y1;
   }
   __syncthreads();
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  total = 0;
+  total = make_int2(0, 0);
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const int y = s_warp[w];
-    if (w < warp) x += y;
-    total += y;
+    const int2 y = s_warp[w];
+    if (w < warp) x.x += y.x, x.y += y.y;
+    total.x += y.x, total.y += y.y;
   }
   return x;
 }
@@ -83,7 +90,7 @@ __device__ __forceinline__ int pages_gone(const EvictParams& p, int n) {
 
 // The new length of sequence b, and its pages for the free list, in front of the
 // pages taken: those of all sequences in order, each one's in order of its columns.
-__device__ void evict_lists(const EvictParams& p, int b, int n, int* s_warp) {
+__device__ void evict_lists(const EvictParams& p, int b, int n, int2* s_warp) {
   if (threadIdx.x == 0) p.seq_out[b] = min(n, p.keep);
   if (!p.free_head) return;
   int before = 0, all = 0;
@@ -92,9 +99,9 @@ __device__ void evict_lists(const EvictParams& p, int b, int n, int* s_warp) {
     all += g;
     if (i < b) before += g;
   }
-  int n_all, n_before;
-  block_scan(all, s_warp, n_all);
-  block_scan(before, s_warp, n_before);
+  int2 sums;
+  block_scan(make_int2(all, before), s_warp, sums);
+  const int n_all = sums.x, n_before = sums.y;
   const int head = *p.free_head;
   const bool fits = head >= n_all && head <= p.n_free;
   if (threadIdx.x == 0 && b == 0) *p.free_head_out = fits ? head - n_all : head;
@@ -117,25 +124,37 @@ __device__ void evict_lists(const EvictParams& p, int b, int n, int* s_warp) {
 template <int DQK, int DV>
 struct EvictShape {
   static constexpr int kCodes = (DQK + DV) / 2 / 16;   // 16-byte vectors of a row's codes
-  static constexpr int kScales = (DQK + DV) / 32 / 2;  // words of its scales
-  static constexpr int kRow = kCodes * 16 + kScales * 4 + 4;  // and its weight
-  static constexpr int kRows = kStage / kRow / 32 * 32;       // of a block's round
-  static constexpr int kUnion = 2 * kRows * kRow > kKeys * 4 ? 2 * kRows * kRow : kKeys * 4;
-  static constexpr int kSmem = 3 * kBins * 4 + kUnion;
+  // the widest pieces of a row's scales (DQK / 16 and DV / 16 bytes) that their alignment allows
+  static constexpr int kPieceK = DQK / 16 % 16 == 0 ? 16 : DQK / 16 % 8 == 0 ? 8 : 4;
+  static constexpr int kPieceV = DV / 16 % 16 == 0 ? 16 : DV / 16 % 8 == 0 ? 8 : 4;
+  static constexpr int kRow = kCodes * 16 + (DQK + DV) / 16 + 4;  // and its weight
+  static constexpr int kMost = kStage / kRow / 32 * 32, kRows = kMost < 256 ? kMost : 256;  // of a block's round
+  // where a round's rows lie, array by array: K's codes first
+  static constexpr int kAtV = kRows * DQK / 2, kAtKs = kAtV + kRows * DV / 2, kAtVs = kAtKs + kRows * DQK / 16,
+                       kAtW = kAtVs + kRows * DV / 16;
+  static constexpr int kSelect = 3 * kBins * 4 + kKeys * 4;
+  static constexpr int kSmem = 2 * kRows * kRow > kSelect ? 2 * kRows * kRow : kSelect;
 };
 
 template <int DQK, int DV>
 __global__ void __launch_bounds__(kThreads, 2) attn_kv_evict_kernel(const __grid_constant__ EvictParams p) {
   using S = EvictShape<DQK, DV>;
-  extern __shared__ __align__(16) uint8_t smem[];
-  int* hist = reinterpret_cast<int*>(smem);                        // [3][kBins]
-  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + 3 * kBins * 4);  // then the rounds' rows
-  uint8_t* stage = smem + 3 * kBins * 4;
-  __shared__ int s_warp[kWarps], s_bin, s_above;
+  extern __shared__ __align__(16) uint8_t smem[];  // counts and weights, then the rounds' rows
+  int* hist = reinterpret_cast<int*>(smem);  // [3][kBins]
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + 3 * kBins * 4);
+  __shared__ int2 s_warp[kWarps];
+  __shared__ int s_bin, s_above, s_first[kWarps];
   __shared__ int s_count[3];  // of this block's candidates: above the border, on it; the first that goes
-  __shared__ long long s_src[2][S::kRows];
+  __shared__ long long s_src[3][S::kRows], s_dst[3][S::kRows];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  // all blocks of the cluster, and what they have written
+  auto meet = [&]() {
+    if (C == 1)
+      __syncthreads();
+    else
+      cluster.sync();
+  };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int item = blockIdx.x / C, b = item / p.c.heads, h = item - b * p.c.heads;
   const int n = evict_len(p, b);
@@ -178,11 +197,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_evict_kernel(const __grid
         const uint32_t k = i < mine ? key(i) : 0u;
         const bool in = i < mine && (pass == 0 || (k >> kShift[pass - 1]) == (border >> kShift[pass - 1]));
         const int d = in ? (int)((k >> kShift[pass]) & (kDigits[pass] - 1)) : -1;
-        // equal digits of a warp are counted together: weights of one size share the first
-        const unsigned same = __match_any_sync(0xffffffffu, d);
-        if (in && lane == __ffs(same) - 1) atomicAdd(&mine_h[d], __popc(same));
+        // (equal digits throughout, as of weights that are all alike, are one addition)
+        const int d0 = __shfl_sync(0xffffffffu, d, 0);
+        if (__all_sync(0xffffffffu, d == d0)) {
+          if (lane == 0 && d0 >= 0) atomicAdd(&mine_h[d0], 32);
+        } else if (in) {
+          atomicAdd(&mine_h[d], 1);
+        }
       }
-      cluster.sync();
+      meet();
       // every block adds up all blocks' counts; thread t takes digits from the top on
       constexpr int kEach = kBins / kThreads;
       const int each = kDigits[pass] / kThreads;
@@ -196,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_evict_kernel(const __grid
           sum += cnt[j];
         }
       }
-      int total;
-      int above = block_scan(sum, s_warp, total) - sum;
+      int2 total;
+      int above = block_scan(make_int2(sum, 0), s_warp, total).x - sum;
 #pragma unroll
       for (int j = 0; j < kEach; ++j)
         if (j < each) {
@@ -212,18 +235,18 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_evict_kernel(const __grid
   } else {
     border = 0xffffffffu;  // (no weight's number)
   }
-  // ---- the list: `need` of the candidates on the border stay
-  int above = 0, on = 0;
-  for (int i = tid; i < mine; i += kThreads) {
+  // ---- the list: `need` of the candidates on the border stay, the first ones.  A thread
+  // takes candidates in a row (an odd number of them: no two lanes' lie in one bank).
+  const int run = ((mine + kThreads - 1) / kThreads) | 1, i0 = min(tid * run, mine), i1 = min(i0 + run, mine);
+  int2 own = make_int2(0, 0), sums;  // above the border, on it
+  for (int i = i0; i < i1; ++i) {
     const uint32_t k = key(i);
-    above += k > border;
-    on += k == border;
+    own.x += k > border;
+    own.y += k == border;
   }
-  int t_above, t_on;
-  block_scan(above, s_warp, t_above);
-  block_scan(on, s_warp, t_on);
-  if (tid == 0) s_count[0] = t_above, s_count[1] = t_on;
-  cluster.sync();
+  const int2 upto = block_scan(own, s_warp, sums);
+  if (tid == 0) s_count[0] = sums.x, s_count[1] = sums.y;
+  meet();
   int to = first, on_before = 0;
   for (int q = 0; q < rank; ++q) {
     const int* s = cluster.map_shared_rank(s_count, q);
@@ -231,30 +254,29 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_evict_kernel(const __grid
     on_before += s[1];
   }
   int gone = INT32_MAX;  // the first that goes, of this thread's
-  for (int i0 = 0; i0 < mine; i0 += kThreads) {
-    const int i = i0 + tid;
-    const uint32_t k = i < mine ? key(i) : 0u;
-    const bool is_on = i < mine && k == border;
-    int n_on, n_stay;
-    const int nth = on_before + block_scan(is_on, s_warp, n_on);
-    const bool stay = i < mine && (k > border || (is_on && nth <= need));
-    const int at = to + block_scan(stay, s_warp, n_stay);
-    if (stay) kept[at - 1] = first + c0 + i;
-    if (i < mine && !stay) gone = min(gone, first + c0 + i);
-    to += n_stay;
-    on_before += n_on;
+  {
+    const int on0 = upto.y - own.y, room0 = max(need - on_before, 0);  // of the block: before this thread; for it
+    int at = to + upto.x - own.x + min(on0, room0), left = max(room0 - on0, 0);
+    for (int i = i0; i < i1; ++i) {
+      const uint32_t k = key(i);
+      const bool on = k == border, stay = k > border || (on && left > 0);
+      left -= on;
+      if (stay)
+        kept[at++] = first + c0 + i;
+      else
+        gone = min(gone, first + c0 + i);
+    }
   }
   for (int i = me; i < first; i += all) kept[i] = i;
   for (int i = me; i < recent; i += all) kept[p.keep - recent + i] = n - recent + i;
   gone = (int)__reduce_min_sync(0xffffffffu, (unsigned)gone);
-  __syncthreads();
-  if (lane == 0) s_warp[warp] = gone;
+  if (lane == 0) s_first[warp] = gone;
   __syncthreads();
   if (tid == 0) {
-    for (int i = 1; i < kWarps; ++i) gone = min(gone, s_warp[i]);
+    for (int i = 1; i < kWarps; ++i) gone = min(gone, s_first[i]);
     s_count[2] = gone;
   }
-  cluster.sync();  // (the list too)
+  meet();  // (the list too)
   int start = INT32_MAX;  // rows in front of it stay where they are
   for (int q = 0; q < C; ++q) start = min(start, cluster.map_shared_rank(s_count, q)[2]);
   start = min(start, p.keep);
@@ -272,68 +294,82 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_evict_kernel(const __grid
     }
     return ((long long)page * p.c.heads + h) * p.c.page_size + (t & (p.c.page_size - 1));
   };
-  // a row in shared memory, vector by vector over the round's rows: K's codes, V's,
-  // K's scales, V's, the weight
-  constexpr int kVk = DQK / 32, kSk = DQK / 64;
-  auto load = [&](int base, int buf) {
-    const int rows = min(p.keep - base, S::kRows);
-    uint8_t* st = stage + buf * (S::kRows * S::kRow);
-    for (int i = tid; i < rows; i += kThreads) {
+  // where a round's rows come from and go to
+  auto find = [&](int base, int slot) {
+    for (int i = tid; i < S::kRows && base + i < p.keep; i += kThreads) {
       const int src = __ldcg(kept + base + i);
-      s_src[buf][i] = slot_row(src);
-      copy4(smem_u32(st + S::kRows * (S::kRow - 4) + i * 4), w + src);
-    }
-    __syncthreads();
-    for (int j = tid; j < rows * S::kCodes; j += kThreads) {
-      const int i = j / S::kCodes, u = j - i * S::kCodes;
-      const long long at = s_src[buf][i];
-      if (at < 0) continue;
-      const uint8_t* src = u < kVk ? p.c.k_codes + at * (DQK / 2) + u * 16 : p.c.v_codes + at * (DV / 2) + (u - kVk) * 16;
-      copy16(smem_u32(st + j * 16), src);
-    }
-    for (int j = tid; j < rows * S::kScales; j += kThreads) {
-      const int i = j / S::kScales, u = j - i * S::kScales;
-      const long long at = s_src[buf][i];
-      if (at < 0) continue;
-      const uint16_t* src = u < kSk ? p.c.k_scales + at * (DQK / 32) + u * 2 : p.c.v_scales + at * (DV / 32) + (u - kSk) * 2;
-      copy4(smem_u32(st + S::kRows * S::kCodes * 16 + j * 4), src);
+      // (a row that comes from or goes to a page outside the cache is not written)
+      const long long from = slot_row(src), dst = slot_row(base + i);
+      s_src[slot][i] = from;
+      s_dst[slot][i] = from < 0 ? -1 : dst;
     }
   };
-  auto store = [&](int base, int buf) {
+  // Pieces of N bytes of the rows' W bytes of one array: a thread keeps its piece and goes
+  // from row to row.  f(piece's place in the array's row 0, in the round's rows, row).
+  auto pieces = [&](auto width, auto piece, const void* array, int at, int rows, auto&& f) {
+    constexpr int W = decltype(width)::value, N = decltype(piece)::value, kEach = W / N, kPer = kThreads / kEach;
+    const int r0 = tid / kEach, u = tid - r0 * kEach;
+    if (r0 >= kPer) return;
+    uint8_t* const mine = (uint8_t*)array + u * N;
+#pragma unroll 2
+    for (int i = r0; i < rows; i += kPer) f(mine, at + i * W + u * N, i);
+  };
+  using std::integral_constant;
+  auto arrays = [&](int rows, auto&& f) {
+    pieces(integral_constant<int, DQK / 2>(), integral_constant<int, 16>(), p.c.k_codes, 0, rows, [&](uint8_t* a, int s, int i) { f(integral_constant<int, 16>(), integral_constant<int, DQK / 2>(), a, s, i); });
+    pieces(integral_constant<int, DV / 2>(), integral_constant<int, 16>(), p.c.v_codes, S::kAtV, rows, [&](uint8_t* a, int s, int i) { f(integral_constant<int, 16>(), integral_constant<int, DV / 2>(), a, s, i); });
+    pieces(integral_constant<int, DQK / 16>(), integral_constant<int, S::kPieceK>(), p.c.k_scales, S::kAtKs, rows, [&](uint8_t* a, int s, int i) { f(integral_constant<int, S::kPieceK>(), integral_constant<int, DQK / 16>(), a, s, i); });
+    pieces(integral_constant<int, DV / 16>(), integral_constant<int, S::kPieceV>(), p.c.v_scales, S::kAtVs, rows, [&](uint8_t* a, int s, int i) { f(integral_constant<int, S::kPieceV>(), integral_constant<int, DV / 16>(), a, s, i); });
+  };
+  auto load = [&](int base, int buf, int slot) {
     const int rows = min(p.keep - base, S::kRows);
-    const uint8_t* st = stage + buf * (S::kRows * S::kRow);
-    for (int j = tid; j < rows * S::kCodes; j += kThreads) {
-      const int i = j / S::kCodes, u = j - i * S::kCodes;
-      const long long at = s_src[buf][i] < 0 ? -1 : slot_row(base + i);
-      if (at < 0) continue;
-      uint8_t* dst = u < kVk ? p.c.k_codes + at * (DQK / 2) + u * 16 : p.c.v_codes + at * (DV / 2) + (u - kVk) * 16;
-      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(st + j * 16);
-    }
-    for (int j = tid; j < rows * S::kScales; j += kThreads) {
-      const int i = j / S::kScales, u = j - i * S::kScales;
-      const long long at = s_src[buf][i] < 0 ? -1 : slot_row(base + i);
-      if (at < 0) continue;
-      uint16_t* dst = u < kSk ? p.c.k_scales + at * (DQK / 32) + u * 2 : p.c.v_scales + at * (DV / 32) + (u - kSk) * 2;
-      *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(st + S::kRows * S::kCodes * 16 + j * 4);
-    }
-    for (int i = tid; i < rows; i += kThreads)
-      w_out[base + i] = *reinterpret_cast<const float*>(st + S::kRows * (S::kRow - 4) + i * 4);
+    const uint32_t st = smem_u32(smem) + buf * (S::kRows * S::kRow);
+    for (int i = tid; i < rows; i += kThreads) copy_bytes<4>(st + S::kAtW + i * 4, w + __ldcg(kept + base + i));
+    if (p.c.num_pages == 0) return;  // (else row 0 is read where there is none)
+    arrays(rows, [&](auto bytes, auto width, uint8_t* array, int at, int i) {
+      copy_bytes<decltype(bytes)::value>(st + at, array + max(s_src[slot][i], 0ll) * decltype(width)::value);
+    });
   };
-  // (a cluster's blocks all take part in every round's barrier, with rows or without)
+  auto store = [&](int base, int buf, int slot) {
+    const int rows = min(p.keep - base, S::kRows);
+    const uint8_t* st = smem + buf * (S::kRows * S::kRow);
+    arrays(rows, [&](auto bytes, auto width, uint8_t* array, int at, int i) {
+      using T = std::conditional_t<decltype(bytes)::value == 16, uint4, std::conditional_t<decltype(bytes)::value == 8, uint2, uint32_t>>;
+      const long long to = s_dst[slot][i];
+      if (to >= 0) *reinterpret_cast<T*>(array + to * decltype(width)::value) = *reinterpret_cast<const T*>(st + at);
+    });
+    for (int i = tid; i < rows; i += kThreads) w_out[base + i] = *reinterpret_cast<const float*>(st + S::kAtW + i * 4);
+  };
+  // (A cluster's blocks all take part in every round's barrier, with rows or without.)
+  // While a round's rows are written the next one's are on their way, and where those after
+  // them lie has been looked up.
   const int step = C * S::kRows;
   int base = start + rank * S::kRows;
-  if (base < p.keep) load(base, 0);
+  find(base, 0);
+  __syncthreads();
+  if (base < p.keep) load(base, 0, 0);
   copies_end();
-  for (int round = start, buf = 0; round < p.keep; round += step, base += step, buf ^= 1) {
-    if (base + step < p.keep) load(base + step, buf ^ 1);
+  find(base + step, 1);
+  __syncthreads();
+  for (int round = start, buf = 0, slot = 0; round < p.keep; round += step, base += step, buf ^= 1) {
+    const int slot1 = slot == 2 ? 0 : slot + 1, slot2 = slot1 == 2 ? 0 : slot1 + 1;
+    if (base + step < p.keep) load(base + step, buf ^ 1, slot1);
     copies_end();
+    find(base + 2 * step, slot2);
     copies_wait<1>();
-    cluster.sync();
-    if (base < p.keep) store(base, buf);
     __syncthreads();
+    // (The rows have arrived, and no block needs to see what another one has written: the
+    // cluster's barrier without its fences is enough.)
+    if (C > 1) {
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    }
+    if (base < p.keep) store(base, buf, slot);
+    __syncthreads();
+    slot = slot1;
   }
   copies_wait<0>();
-  cluster.sync();  // (no block leaves while others may read its counts)
+  meet();  // (no block leaves while others may read its counts)
 }
 
 namespace {
@@ -351,10 +387,11 @@ cudaError_t evict_launch(const EvictParams& p, int num_sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  // as large a cluster as leaves all of them on the card at once
+  // as large a cluster as leaves all of them on the card at once, and its blocks enough to do
   const int64_t items = (int64_t)p.batch * p.c.heads;
+  const int64_t most = std::min<int64_t>((int64_t)p.cols << p.c.page_shift, p.capacity);
   int c = kMaxCluster;
-  while (c > 1 && items * c > 2 * num_sms) c /= 2;
+  while (c > 1 && (items * c > 2 * num_sms || most < (int64_t)c * kMinSlice)) c /= 2;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = (unsigned)c;
