@@ -4,7 +4,7 @@
 //
 // One cluster of blocks works on one (sequence, kv head):
 //   * the border: the room-th largest weight, by a radix selection over the bits of
-//     the weights (as whole numbers they are ordered; 11, 11 and 10 bits at a time).
+//     the weights (as whole numbers they are ordered; 10, 8, 7 and 7 bits at a time).
 //     Each block counts its slice of the candidates in shared memory, the blocks add
 //     up each other's counts over the cluster's distributed shared memory;
 //   * the list: every candidate above the border stays, and of those on it the first
@@ -30,11 +30,11 @@ namespace attn {
 namespace cg = cooperative_groups;
 
 namespace {
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kBlocks = 4;  // blocks of an SM
+constexpr int kPasses = 4, kBins = 1536;  // of the selection: 10, 8, 7 and 7 bits; their counts
 constexpr int kMaxCluster = 8;
-constexpr int kKeys = 16384;  // candidates of a block whose weights stay in shared memory
-constexpr int kStage = 45056;  // bytes of a round's rows of a block, at most
+constexpr int kKeys = 8192;  // candidates of a block whose weights stay in shared memory
+constexpr int kStage = 19456;  // bytes of a round's rows of a block, at most
 constexpr int kMinSlice = 2048;  // candidates of a block: fewer are not worth another block's barriers
 
 // A weight as a number whose order is the weights': NaN below all, -0 like 0.
@@ -128,20 +128,20 @@ struct EvictShape {
   static constexpr int kPieceK = DQK / 16 % 16 == 0 ? 16 : DQK / 16 % 8 == 0 ? 8 : 4;
   static constexpr int kPieceV = DV / 16 % 16 == 0 ? 16 : DV / 16 % 8 == 0 ? 8 : 4;
   static constexpr int kRow = kCodes * 16 + (DQK + DV) / 16 + 4;  // and its weight
-  static constexpr int kMost = kStage / kRow / 32 * 32, kRows = kMost < 256 ? kMost : 256;  // of a block's round
+  static constexpr int kMost = kStage / kRow / 32 * 32, kRows = kMost < 128 ? kMost : 128;  // of a block's round
   // where a round's rows lie, array by array: K's codes first
   static constexpr int kAtV = kRows * DQK / 2, kAtKs = kAtV + kRows * DV / 2, kAtVs = kAtKs + kRows * DQK / 16,
                        kAtW = kAtVs + kRows * DV / 16;
-  static constexpr int kSelect = 3 * kBins * 4 + kKeys * 4;
+  static constexpr int kSelect = kBins * 4 + kKeys * 4;
   static constexpr int kSmem = 2 * kRows * kRow > kSelect ? 2 * kRows * kRow : kSelect;
 };
 
 template <int DQK, int DV>
-__global__ void __launch_bounds__(kThreads, 2) attn_kv_evict_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kThreads, kBlocks) attn_kv_evict_kernel(const __grid_constant__ EvictParams p) {
   using S = EvictShape<DQK, DV>;
   extern __shared__ __align__(16) uint8_t smem[];  // counts and weights, then the rounds' rows
-  int* hist = reinterpret_cast<int*>(smem);  // [3][kBins]
-  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + 3 * kBins * 4);
+  int* hist = reinterpret_cast<int*>(smem);  // pass by pass
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + kBins * 4);
   __shared__ int2 s_warp[kWarps];
   __shared__ int s_bin, s_above, s_first[kWarps];
   __shared__ int s_count[3];  // of this block's candidates: above the border, on it; the first that goes
@@ -180,18 +180,18 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_evict_kernel(const __grid
   auto key = [&](int i) { return held ? keys[i] : order_of(wc[i]); };
 
   // ---- the border
-  for (int i = tid; i < 3 * kBins; i += kThreads) hist[i] = 0;
+  for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
   if (held)
     for (int i = tid; i < mine; i += kThreads) keys[i] = order_of(wc[i]);
   __syncthreads();
   uint32_t border = 0;  // its digits so far
   int need = room;      // of the candidates that share them
-  constexpr int kShift[3] = {21, 10, 0};
-  constexpr int kDigits[3] = {kBins, kBins, kBins / 2};
+  constexpr int kShift[kPasses] = {22, 14, 7, 0};
+  constexpr int kDigits[kPasses] = {1024, 256, 128, 128}, kFirst[kPasses] = {0, 1024, 1280, 1408};
   if (room > 0) {
 #pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      int* mine_h = hist + pass * kBins;
+    for (int pass = 0; pass < kPasses; ++pass) {
+      int* mine_h = hist + kFirst[pass];
       for (int i0 = warp * 32; i0 < mine; i0 += kThreads) {
         const int i = i0 + lane;
         const uint32_t k = i < mine ? key(i) : 0u;
@@ -207,15 +207,16 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_evict_kernel(const __grid
       }
       meet();
       // every block adds up all blocks' counts; thread t takes digits from the top on
-      constexpr int kEach = kBins / kThreads;
-      const int each = kDigits[pass] / kThreads;
+      constexpr int kEach = 1024 / kThreads;
+      const int each = max(kDigits[pass] / kThreads, 1);
+      const bool digits = tid * each < kDigits[pass];
       int cnt[kEach], sum = 0;
 #pragma unroll
       for (int j = 0; j < kEach; ++j) {
         cnt[j] = 0;
-        if (j < each) {
+        if (j < each && digits) {
           const int d = kDigits[pass] - 1 - (tid * each + j);
-          for (int q = 0; q < C; ++q) cnt[j] += cluster.map_shared_rank(mine_h, q)[d];
+          for (int q = 0; q < C; ++q) cnt[j] += (C == 1 ? mine_h : cluster.map_shared_rank(mine_h, q))[d];
           sum += cnt[j];
         }
       }
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv_evict_kernel(const __grid
       int above = block_scan(make_int2(sum, 0), s_warp, total).x - sum;
 #pragma unroll
       for (int j = 0; j < kEach; ++j)
-        if (j < each) {
+        if (j < each && digits) {
           if (above < need && above + cnt[j] >= need) s_bin = kDigits[pass] - 1 - (tid * each + j), s_above = above;
           above += cnt[j];
         }
@@ -391,7 +392,7 @@ cudaError_t evict_launch(const EvictParams& p, int num_sms, cudaStream_t st) {
   const int64_t items = (int64_t)p.batch * p.c.heads;
   const int64_t most = std::min<int64_t>((int64_t)p.cols << p.c.page_shift, p.capacity);
   int c = kMaxCluster;
-  while (c > 1 && (items * c > 2 * num_sms || most < (int64_t)c * kMinSlice)) c /= 2;
+  while (c > 1 && (items * c > kBlocks * num_sms || most < (int64_t)c * kMinSlice)) c /= 2;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = (unsigned)c;
