@@ -738,7 +738,7 @@ attn_status_t attn_kv_weights(const attn_kv4_weights_params_t* p, const attn_kv4
   kp.seqlen_q = p->seqlen_q;
   kp.heads_q = p->heads_q;
   kp.group = dp.group;
-  kp.cols = p->cols;
+  kp.cols = cache->num_pages ? p->cols : 0;  // (without pages no sequence can have tokens)
   kp.capacity = p->capacity;
   kp.window_left = dp.window_left;
   kp.sinks = dp.sinks;

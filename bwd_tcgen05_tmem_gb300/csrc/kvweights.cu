@@ -14,10 +14,19 @@
 // the cache (its layout gives a lane whole vectors, and a warp whole lines), one
 // unit ahead of what they compute with, and the pages one unit ahead of those.
 //
+// What bounds it: the instructions of a tile, 411 a warp for 32 tokens of head dim 128
+// and 4 query rows (unpacking 80, scales on the sums 50, exponentials and sums 60,
+// addresses and pages 60); the schedulers issue in three cycles of four and the memory
+// runs at half its rate.  16 x 32K tokens of 8 kv heads, head dim 128, one GB300: 84 us,
+// 4.0 TB/s of the 6.7 that a copy reaches; head dim 64 56, 192 102, 256 128, 16 query
+// rows 102; the last 32 queries of 8 prompts of 32K (128 rows a head) 320.
+//
 // The products are those of attention over the cache: the cache as the 16-row
-// operand, 8 query rows as the other, in fp16 (code - 8 is exact, q is held times a
-// power of two that brings its row's largest element to 2^13 .. 2^14), the scales
-// of the 32-dim groups on the FP32 sums.
+// operand, 8 query rows as the other, in fp16 (q is held times a power of two that
+// brings its row's largest element to 2^13 .. 2^14), the scales of the 32-dim groups on
+// the FP32 sums.  Up to 16 query rows the codes are operands as they are, and their
+// offset of 8 is the products' start value, as in kvdecode.cu; for more rows, which
+// share the operand, 8 is taken off first.
 #include <algorithm>
 
 #include "kcommon.cuh"
@@ -32,10 +41,14 @@ constexpr int kTile = 32;               // tokens of a warp's tile
 constexpr int kUnit = kWarps * kTile;   // of a block's unit
 constexpr int kManyBlocks = 8;          // blocks of 8 query rows held at a time where there are many
 
-// Blocks an SM: as many as leave a lane's registers room for two tiles, the
-// operands and the query rows.
+// Blocks an SM.  A lane holds two tiles of codes, the query operand and (of few rows)
+// its start values, 128 registers at four blocks of 128 threads, 168 at three, 255 at
+// two: where they do not fit, a block more costs more than it hides.  16 x 32K tokens,
+// 8 kv heads, one GB300, us, more blocks against two: head dim 64 56 / 66 (four), 128
+// with 4 rows 84 / 149 (four), 192 102 / 114 (three), 256 224 / 128 (three / two), 128
+// with 16 rows 151 / 102 (three / two); 8 prompts of 32 query tokens 34 / 38 (three).
 constexpr int blocks_of(int dqk, int nb) {
-  return dqk == 64 || (dqk == 128 && nb == 1) ? 4 : dqk == 128 || nb == 1 ? 3 : 2;
+  return dqk == 64 || (dqk == 128 && nb == 1) ? 4 : (dqk == 128 && nb == kManyBlocks) || (dqk == 192 && nb == 1) ? 3 : 2;
 }
 }  // namespace
 
@@ -113,8 +126,10 @@ __global__ void __launch_bounds__(kThreads, blocks_of(DQK, NB)) attn_kv_weights_
     const __grid_constant__ WeightsParams p) {
   constexpr int G = DQK / 32;
   constexpr bool kMany = NB == kManyBlocks;
+  constexpr bool kHold = NB * G <= 8, kHoldLow = NB * G <= 4;  // the query operand, and the start values, stay in registers
   __shared__ uint4 s_q[NB][G][32];            // operand registers of a lane
   __shared__ float s_xs[NB * 8], s_lse[NB * 8];  // from products to base-2 scores; LSE in base 2
+  __shared__ float4 s_low[kWarps][kMany || kHoldLow ? 1 : NB][kHoldLow ? 1 : G][4];
   __shared__ long long s_sum[kWarps];
   __shared__ int s_b;
   __shared__ long long s_before;
@@ -168,10 +183,17 @@ __global__ void __launch_bounds__(kThreads, blocks_of(DQK, NB)) attn_kv_weights_
     float* w = p.w + (int64_t)b * p.w_b + (int64_t)kvh * p.w_h;
     const int pos0 = ur.len - p.seqlen_q;  // position of query 0
     // first token of the warp's tile of unit u of the segment
+    constexpr int kPast = INT32_MAX - (2 * kTile - 1);  // a tile past any length, on a tile's boundary as all are
+    static_assert(kPast % kTile == 0, "its rows in page 0 are read");
     auto token_of = [&](int u) {
-      u += v;
-      return (u < ur.n_sink ? u : ur.lo + u - ur.n_sink) * kUnit + warp * kTile;
+      const int x = u + v;
+      return u < n ? (x < ur.n_sink ? x : ur.lo + x - ur.n_sink) * kUnit + warp * kTile : kPast;
     };
+    // the lane's part of the head's first row in page 0 (pages of a side take less than 2^31 bytes)
+    const int64_t row0_of = (int64_t)kvh * p.c.page_size + r;
+    const uint8_t* const my_codes = p.c.k_codes + row0_of * (DQK / 2) + c * 4 * G;
+    const uint8_t* const my_scales = reinterpret_cast<const uint8_t*>(p.c.k_scales) + row0_of * (2 * G);
+    const uint32_t rows_of = (uint32_t)(p.c.heads * p.c.page_size), page_codes = rows_of * (DQK / 2), page_scales = rows_of * (2 * G);
     for (int row0 = 0; row0 < p.rows; row0 += NB * 8) {
       const int nb = min(NB, (p.rows - row0 + 7) / 8);
       // ---- the query rows
@@ -200,27 +222,43 @@ __global__ void __launch_bounds__(kThreads, blocks_of(DQK, NB)) attn_kv_weights_
           const uint32_t x[4] = {qv[g].x, qv[g].y, qv[g].z, qv[g].w};
           float f[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = Pack<BF16>::to_f((uint16_t)(x[e >> 1] >> (16 * (e & 1)))) * inv;
+          for (int e = 0; e < 8; ++e)
+            f[e] = Pack<BF16>::to_f((uint16_t)(x[e >> 1] >> (16 * (e & 1)))) * (kMany || !(e & 1) ? inv : inv * KCodes<DQK>::kOdd);
           s_q[i][g][lane] = make_uint4(Pack<false>::two(f[0], f[4]), Pack<false>::two(f[1], f[5]),
                                        Pack<false>::two(f[2], f[6]), Pack<false>::two(f[3], f[7]));
         }
         if (c == 0) {
-          s_xs[i * 8 + r] = p.scale_log2 * pow2(ex);
+          s_xs[i * 8 + r] = p.scale_log2 * (kMany ? 1.0f : KCodes<DQK>::kUnit) * pow2(ex);
           const float lse = qrow < p.rows ? p.lse[((int64_t)b * p.heads_q + qh) * p.seqlen_q + qi] : 0.0f;
           s_lse[i * 8 + r] = lse * 1.4426950408889634f;
         }
       }
       __syncthreads();
-      uint4 qf[kMany ? 1 : NB][G];
+      uint4 qf[kHold ? NB : 1][G];
+      float4 low[kHoldLow ? NB : 1][G];  // what the codes' offset adds up to
       float xs[kMany ? 1 : NB][2], ls[kMany ? 1 : NB][2];
       if constexpr (!kMany) {
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
 #pragma unroll
-          for (int g = 0; g < G; ++g) qf[i][g] = s_q[i < nb ? i : 0][g][lane];
+          for (int g = 0; g < G; ++g)
+            if (kHold) qf[i][g] = s_q[i][g][lane];
 #pragma unroll
           for (int e = 0; e < 2; ++e) xs[i][e] = s_xs[i * 8 + 2 * c + e], ls[i][e] = s_lse[i * 8 + 2 * c + e];
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            constexpr uint32_t even = KCodes<DQK>::kEven8, odd = KCodes<DQK>::kOdd8;
+            float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const uint4 q = s_q[i][g][lane];
+            mma16816(x, even, even, odd, odd, q.x, q.y);
+            mma16816(x, even, even, odd, odd, q.z, q.w);
+            if (kHoldLow)
+              low[i][g] = make_float4(x[0], x[1], x[2], x[3]);
+            else if (r == 0)
+              s_low[warp][i][g][c] = make_float4(x[0], x[1], x[2], x[3]);
+          }
         }
+        __syncwarp();
       }
       // every query of these rows sees tokens whole_lo .. pos_lo; none sees one above
       // pos_hi, or below any_lo but the first `sinks`
@@ -232,71 +270,76 @@ __global__ void __launch_bounds__(kThreads, blocks_of(DQK, NB)) attn_kv_weights_
       const bool later = row0 > 0;
       const int set_from = later ? INT32_MAX : p.add ? max(pos0, 0) : 0;
 
-      int page[4];
-      auto pages_of = [&](int u) {
-        const int t0 = token_of(u);
+      // Pages of the two halves (16 tokens) of the tile at token t0.  A half that no query
+      // sees a token of is not looked at, and page 0 is read in its place; of one that some do
+      // all 16 rows are read.  Whatever hidden rows hold, their weights are 0.
+      const int seen_end = min(ur.len, pos_hi + 1);
+      int page[2];
+      auto pages_of = [&](int t0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = t0 + 8 * i + r;
-          page[i] = -1;
-          if (u < n && t < ur.len && t <= pos_hi && (t >= any_lo || t < p.sinks)) {
-            page[i] = __ldg(row + (t >> p.c.page_shift));
-            if ((unsigned)page[i] >= (unsigned)p.c.num_pages) {
-              page[i] = -1;
-              if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
-            }
-          }
+        for (int h = 0; h < 2; ++h) {
+          const int t = t0 + 16 * h;
+          page[h] = 0;
+          if (t < seen_end && (t + 15 >= any_lo || t < p.sinks)) page[h] = __ldg(row + (t >> p.c.page_shift));
         }
       };
-      auto load = [&](int u, KTile<G>& z) {  // (of the pages looked up last)
-        const int t0 = token_of(u);
+      auto load = [&](int t0, KTile<G>& z) {  // (of the pages looked up last)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (page[i] < 0) {
-#pragma unroll
-            for (int g = 0; g < G; ++g) z.k[i][g] = 0x88888888u;
-#pragma unroll
-            for (int g = 0; g < G / 2; ++g) z.s[i][g] = 0u;
-            continue;
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pg = (uint32_t)page[h];
+          if (pg >= (uint32_t)p.c.num_pages) {
+            if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
+            pg = 0;
           }
-          const int64_t at = ((int64_t)page[i] * p.c.heads + kvh) * p.c.page_size +
-                             ((t0 + 8 * i + r) & (p.c.page_size - 1));
-          ldg_words<G>(p.c.k_codes + at * (DQK / 2) + c * 4 * G, z.k[i]);
-          ldg_words<G / 2>(reinterpret_cast<const uint8_t*>(p.c.k_scales) + at * (2 * G), z.s[i]);
+          const uint32_t in_page = (uint32_t)(t0 + 16 * h) & (uint32_t)(p.c.page_size - 1);
+          const uint8_t* codes = my_codes + (uint64_t)pg * page_codes + in_page * (DQK / 2);
+          const uint8_t* scales = my_scales + (uint64_t)pg * page_scales + in_page * (2 * G);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            ldg_words<G>(codes + i * 8 * (DQK / 2), z.k[2 * h + i]);
+            ldg_words<G / 2>(scales + i * 8 * (2 * G), z.s[2 * h + i]);
+          }
         }
         const int t = t0 + 8 * c + r;
         z.old = 0.0f;
-        if (u < n && t < ur.len && t < set_from) z.old = w[t];
+        if (t < ur.len && t < set_from) z.old = w[t];
       };
-      KTile<G> next;
-      pages_of(0);
-      load(0, next);
-      pages_of(1);
-      for (int u = 0; u < n; ++u) {
-        const KTile<G> z = next;
-        load(u + 1, next);
-        pages_of(u + 2);
-        const int t0 = token_of(u);
-        if (t0 >= ur.len) continue;
-        const bool whole = t0 + kTile - 1 <= pos_lo && (t0 >= whole_lo || t0 + kTile <= p.sinks) &&
-                           row0 + nb * 8 <= p.rows;
+      const bool full_cols = row0 + nb * 8 <= p.rows;
+      bool col[kMany ? 1 : NB][2];
+      if constexpr (!kMany) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) col[i][e] = row0 + i * 8 + 2 * c + e < p.rows;
+      }
+      auto tile = [&](int t0, const KTile<G>& z) {
+        if (t0 >= ur.len) return;
+        const bool whole = t0 + kTile - 1 <= pos_lo && (t0 >= whole_lo || t0 + kTile <= p.sinks);
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           uint32_t ka[G][4], kb[G][4];
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            signed_codes(z.k[2 * m][g], ka[g]);
-            signed_codes(z.k[2 * m + 1][g], kb[g]);
+            if constexpr (kMany) {
+              signed_codes(z.k[2 * m][g], ka[g]);
+              signed_codes(z.k[2 * m + 1][g], kb[g]);
+            } else {
+              KCodes<DQK>::of(z.k[2 * m][g], ka[g]);
+              KCodes<DQK>::of(z.k[2 * m + 1][g], kb[g]);
+            }
           }
-          auto rows8 = [&](const uint4* q, float xs0, float xs1, float ls0, float ls1, int i) {
+          // (start: of the products; see0, see1: whether columns 2c, 2c + 1 are query rows)
+          auto rows8 = [&](auto&& q, auto&& start, float xs0, float xs1, float ls0, float ls1, bool see0, bool see1, int i) {
             float y[4];
 #pragma unroll
             for (int g = 0; g < G; ++g) {
               const float fa = scale_of(z.s[2 * m], g), fb = scale_of(z.s[2 * m + 1], g);
-              const uint4 qg = q[kMany ? g * 32 : g];
-              float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              mma16816(acc, ka[g][0], kb[g][0], ka[g][1], kb[g][1], qg.x, qg.y);
+              const uint4 qg = q(g);
+              const float4 l = start(g);
+              const float first[4] = {l.x, l.y, l.z, l.w};
+              float acc[4];
+              mma16816(acc, ka[g][0], kb[g][0], ka[g][1], kb[g][1], qg.x, qg.y, first);
               mma16816(acc, ka[g][2], kb[g][2], ka[g][3], kb[g][3], qg.z, qg.w);
               y[0] = g ? fmaf(acc[0], fa, y[0]) : acc[0] * fa;
               y[1] = g ? fmaf(acc[1], fa, y[1]) : acc[1] * fa;
@@ -310,16 +353,18 @@ __global__ void __launch_bounds__(kThreads, blocks_of(DQK, NB)) attn_kv_weights_
             if (!whole) {  // (whatever a hidden token's scale is, its weight is 0)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int qrow = row0 + i * 8 + 2 * c + e;
-                const int pos = pos0 + (int)p.by_group.div(qrow);
-                const int hi = qrow < p.rows ? pos : -1;
+                const int pos = pos0 + (int)p.by_group.div(row0 + i * 8 + 2 * c + e);
                 const int lo = p.window_left < 0 ? 0 : pos - p.window_left;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const int t = t0 + 16 * m + 8 * h + r;
-                  if (t > hi || (t < lo && t >= p.sinks)) y[2 * h + e] = 0.0f;
+                  if (t > pos || (t < lo && t >= p.sinks)) y[2 * h + e] = 0.0f;
                 }
               }
+            }
+            if (!full_cols) {  // columns past the last row
+              y[0] = see0 ? y[0] : 0.0f, y[2] = see0 ? y[2] : 0.0f;
+              y[1] = see1 ? y[1] : 0.0f, y[3] = see1 ? y[3] : 0.0f;
             }
             sum[2 * m] += y[0] + y[1];
             sum[2 * m + 1] += y[2] + y[3];
@@ -328,12 +373,18 @@ __global__ void __launch_bounds__(kThreads, blocks_of(DQK, NB)) attn_kv_weights_
             for (int i = 0; i < nb; ++i) {
               const float2 x = *reinterpret_cast<const float2*>(s_xs + i * 8 + 2 * c);
               const float2 l = *reinterpret_cast<const float2*>(s_lse + i * 8 + 2 * c);
-              rows8(&s_q[i][0][lane], x.x, x.y, l.x, l.y, i);
+              const int first_row = row0 + i * 8 + 2 * c;
+              rows8([&](int g) { return s_q[i][g][lane]; }, [&](int) { return make_float4(0.0f, 0.0f, 0.0f, 0.0f); }, x.x, x.y, l.x,
+                    l.y, first_row < p.rows, first_row + 1 < p.rows, i);
             }
           } else {
 #pragma unroll
             for (int i = 0; i < NB; ++i)
-              if (i < nb) rows8(qf[i], xs[i][0], xs[i][1], ls[i][0], ls[i][1], i);
+              rows8([&](int g) { return kHold ? qf[kHold ? i : 0][g] : s_q[i][g][lane]; },
+                    [&](int g) {
+                      return kHoldLow ? low[kHoldLow ? i : 0][g] : s_low[warp][kHoldLow ? 0 : i][kHoldLow ? 0 : g][c];
+                    },
+                    xs[i][0], xs[i][1], ls[i][0], ls[i][1], col[i][0], col[i][1], i);
           }
         }
         float total = 0.0f;
@@ -346,6 +397,24 @@ __global__ void __launch_bounds__(kThreads, blocks_of(DQK, NB)) attn_kv_weights_
         }
         const int t = t0 + 8 * c + r;
         if (t < ur.len) w[t] = t < set_from ? z.old + total : total;
+      };
+      // two tiles in registers: one is computed with while the other one comes
+      KTile<G> ping, pong;
+      int here = token_of(0), next = token_of(1);  // (past the segment: past any length)
+      pages_of(here);
+      load(here, ping);
+      pages_of(next);
+      for (int u = 0; u < n; u += 2) {
+        load(next, pong);
+        const int after = token_of(u + 2);
+        pages_of(after);
+        tile(here, ping);
+        load(after, ping);
+        here = after;
+        const int last = next;
+        next = token_of(u + 3);
+        pages_of(next);
+        tile(last, pong);
       }
     }
     left -= n;
