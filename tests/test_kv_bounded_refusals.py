@@ -56,6 +56,16 @@ def test_shared_refusals(lib, change, cache, ptrs, code):
     assert lib.attn_last_error()
 
 
+def test_shared_too_many_tiles(lib):
+    """Tiles of query rows times tiles of keys are counted in 32 bits."""
+    size, c = lib.attn_kv_decode_shared_workspace_size, cache_desc(num_pages=2 ** 20)
+    few = dict(batch=4096, cols=2 ** 18, table_stride=2 ** 18)
+    assert size(decode_params(**few), c, 2) > MB
+    assert size(decode_params(**few, seqlen_q=256), c, 2) == 256  # (what a refused call is told)
+    assert shared_call(lib, dict(few, seqlen_q=256), dict(num_pages=2 ** 20)) == UNSUPPORTED
+    assert "too many tiles" in str(lib.attn_last_error())
+
+
 def test_shared_nothing_to_do(lib):
     none = dict(starts=None, shared=None, q=None, table=None, lens=None, o=None, lse=None, status=None)
     assert shared_call(lib, dict(batch=0), groups=0, **none) == OK
