@@ -12,14 +12,16 @@
 // a grid that fills the card; lengths are read on the device.  A warp takes 32 of a
 // unit's tokens.  Its lanes load the codes of their operand registers straight from
 // the cache (its layout gives a lane whole vectors, and a warp whole lines), one
-// unit ahead of what they compute with, and the pages one unit ahead of those.
+// unit ahead of what they compute with, and the pages one unit ahead of those.  More
+// than 16 query rows take turns, 64 at a time, at a tile that is converted once for them.
 //
 // What bounds it: the instructions of a tile, 411 a warp for 32 tokens of head dim 128
 // and 4 query rows (unpacking 80, scales on the sums 50, exponentials and sums 60,
 // addresses and pages 60); the schedulers issue in three cycles of four and the memory
 // runs at half its rate.  16 x 32K tokens of 8 kv heads, head dim 128, one GB300: 84 us,
 // 4.0 TB/s of the 6.7 that a copy reaches; head dim 64 56, 192 102, 256 128, 16 query
-// rows 102; the last 32 queries of 8 prompts of 32K (128 rows a head) 320.
+// rows 102.  128 rows a head (the last 32 queries of 8 prompts of 32K tokens) take 276:
+// a block of 8 rows costs 8 products, 16 scalings, 8 exponentials and their sums.
 //
 // The products are those of attention over the cache: the cache as the 16-row
 // operand, 8 query rows as the other, in fp16 (q is held times a power of two that
@@ -46,9 +48,10 @@ constexpr int kManyBlocks = 8;          // blocks of 8 query rows held at a time
 // two: where they do not fit, a block more costs more than it hides.  16 x 32K tokens,
 // 8 kv heads, one GB300, us, more blocks against two: head dim 64 56 / 66 (four), 128
 // with 4 rows 84 / 149 (four), 192 102 / 114 (three), 256 224 / 128 (three / two), 128
-// with 16 rows 151 / 102 (three / two); 8 prompts of 32 query tokens 34 / 38 (three).
+// with 16 rows 151 / 102 (three / two), with 128 rows (8 x 32K) 286 / 276 (three / two),
+// 9 prompts of 32 query tokens of head dim 64 29 / 35 (four).
 constexpr int blocks_of(int dqk, int nb) {
-  return dqk == 64 || (dqk == 128 && nb == 1) ? 4 : (dqk == 128 && nb == kManyBlocks) || (dqk == 192 && nb == 1) ? 3 : 2;
+  return dqk == 64 || (dqk == 128 && nb == 1) ? 4 : dqk == 192 && nb == 1 ? 3 : 2;
 }
 }  // namespace
 
@@ -312,81 +315,52 @@ __global__ void __launch_bounds__(kThreads, blocks_of(DQK, NB)) attn_kv_weights_
 #pragma unroll
           for (int e = 0; e < 2; ++e) col[i][e] = row0 + i * 8 + 2 * c + e < p.rows;
       }
-      auto tile = [&](int t0, const KTile<G>& z) {
-        if (t0 >= ur.len) return;
-        const bool whole = t0 + kTile - 1 <= pos_lo && (t0 >= whole_lo || t0 + kTile <= p.sinks);
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      // 16 tokens times 8 query rows: their products with the scales on them (a lane has tokens
+      // r, r + 8 in y[0 .. 1], y[2 .. 3], rows 2c, 2c + 1), and what those add to the tokens' sums
+      auto products = [&](const uint32_t (&ka)[G][4], const uint32_t (&kb)[G][4], const uint32_t (&sa)[G / 2],
+                          const uint32_t (&sb)[G / 2], const uint4 (&q)[G], const float4* start, float (&y)[4]) {
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint32_t ka[G][4], kb[G][4];
+        for (int g = 0; g < G; ++g) {
+          const float fa = scale_of(sa, g), fb = scale_of(sb, g);
+          const float4 l = kMany ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : start[g];
+          const float first[4] = {l.x, l.y, l.z, l.w};
+          float acc[4];
+          mma16816(acc, ka[g][0], kb[g][0], ka[g][1], kb[g][1], q[g].x, q[g].y, first);
+          mma16816(acc, ka[g][2], kb[g][2], ka[g][3], kb[g][3], q[g].z, q[g].w);
+          y[0] = g ? fmaf(acc[0], fa, y[0]) : acc[0] * fa;
+          y[1] = g ? fmaf(acc[1], fa, y[1]) : acc[1] * fa;
+          y[2] = g ? fmaf(acc[2], fb, y[2]) : acc[2] * fb;
+          y[3] = g ? fmaf(acc[3], fb, y[3]) : acc[3] * fb;
+        }
+      };
+      // (i: block of 8 rows; see0, see1: whether 2c, 2c + 1 of it are query rows; m: half of the tile)
+      auto add = [&](float (&y)[4], int t0, int m, bool whole, int i, float xs0, float xs1, float ls0, float ls1, bool see0,
+                     bool see1, float (&sum)[4]) {
+        y[0] = ex2(fmaf(y[0], xs0, -ls0));
+        y[1] = ex2(fmaf(y[1], xs1, -ls1));
+        y[2] = ex2(fmaf(y[2], xs0, -ls0));
+        y[3] = ex2(fmaf(y[3], xs1, -ls1));
+        if (!whole) {  // (whatever a hidden token's scale is, its weight is 0)
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            if constexpr (kMany) {
-              signed_codes(z.k[2 * m][g], ka[g]);
-              signed_codes(z.k[2 * m + 1][g], kb[g]);
-            } else {
-              KCodes<DQK>::of(z.k[2 * m][g], ka[g]);
-              KCodes<DQK>::of(z.k[2 * m + 1][g], kb[g]);
+          for (int e = 0; e < 2; ++e) {
+            const int pos = pos0 + (int)p.by_group.div(row0 + i * 8 + 2 * c + e);
+            const int lo = p.window_left < 0 ? 0 : pos - p.window_left;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int t = t0 + 16 * m + 8 * h + r;
+              if (t > pos || (t < lo && t >= p.sinks)) y[2 * h + e] = 0.0f;
             }
-          }
-          // (start: of the products; see0, see1: whether columns 2c, 2c + 1 are query rows)
-          auto rows8 = [&](auto&& q, auto&& start, float xs0, float xs1, float ls0, float ls1, bool see0, bool see1, int i) {
-            float y[4];
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-              const float fa = scale_of(z.s[2 * m], g), fb = scale_of(z.s[2 * m + 1], g);
-              const uint4 qg = q(g);
-              const float4 l = start(g);
-              const float first[4] = {l.x, l.y, l.z, l.w};
-              float acc[4];
-              mma16816(acc, ka[g][0], kb[g][0], ka[g][1], kb[g][1], qg.x, qg.y, first);
-              mma16816(acc, ka[g][2], kb[g][2], ka[g][3], kb[g][3], qg.z, qg.w);
-              y[0] = g ? fmaf(acc[0], fa, y[0]) : acc[0] * fa;
-              y[1] = g ? fmaf(acc[1], fa, y[1]) : acc[1] * fa;
-              y[2] = g ? fmaf(acc[2], fb, y[2]) : acc[2] * fb;
-              y[3] = g ? fmaf(acc[3], fb, y[3]) : acc[3] * fb;
-            }
-            y[0] = ex2(fmaf(y[0], xs0, -ls0));
-            y[1] = ex2(fmaf(y[1], xs1, -ls1));
-            y[2] = ex2(fmaf(y[2], xs0, -ls0));
-            y[3] = ex2(fmaf(y[3], xs1, -ls1));
-            if (!whole) {  // (whatever a hidden token's scale is, its weight is 0)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int pos = pos0 + (int)p.by_group.div(row0 + i * 8 + 2 * c + e);
-                const int lo = p.window_left < 0 ? 0 : pos - p.window_left;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const int t = t0 + 16 * m + 8 * h + r;
-                  if (t > pos || (t < lo && t >= p.sinks)) y[2 * h + e] = 0.0f;
-                }
-              }
-            }
-            if (!full_cols) {  // columns past the last row
-              y[0] = see0 ? y[0] : 0.0f, y[2] = see0 ? y[2] : 0.0f;
-              y[1] = see1 ? y[1] : 0.0f, y[3] = see1 ? y[3] : 0.0f;
-            }
-            sum[2 * m] += y[0] + y[1];
-            sum[2 * m + 1] += y[2] + y[3];
-          };
-          if constexpr (kMany) {
-            for (int i = 0; i < nb; ++i) {
-              const float2 x = *reinterpret_cast<const float2*>(s_xs + i * 8 + 2 * c);
-              const float2 l = *reinterpret_cast<const float2*>(s_lse + i * 8 + 2 * c);
-              const int first_row = row0 + i * 8 + 2 * c;
-              rows8([&](int g) { return s_q[i][g][lane]; }, [&](int) { return make_float4(0.0f, 0.0f, 0.0f, 0.0f); }, x.x, x.y, l.x,
-                    l.y, first_row < p.rows, first_row + 1 < p.rows, i);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-              rows8([&](int g) { return kHold ? qf[kHold ? i : 0][g] : s_q[i][g][lane]; },
-                    [&](int g) {
-                      return kHoldLow ? low[kHoldLow ? i : 0][g] : s_low[warp][kHoldLow ? 0 : i][kHoldLow ? 0 : g][c];
-                    },
-                    xs[i][0], xs[i][1], ls[i][0], ls[i][1], col[i][0], col[i][1], i);
           }
         }
+        if (!full_cols) {  // columns past the last row
+          y[0] = see0 ? y[0] : 0.0f, y[2] = see0 ? y[2] : 0.0f;
+          y[1] = see1 ? y[1] : 0.0f, y[3] = see1 ? y[3] : 0.0f;
+        }
+        sum[2 * m] += y[0] + y[1];
+        sum[2 * m + 1] += y[2] + y[3];
+      };
+      auto is_whole = [&](int t0) { return t0 + kTile - 1 <= pos_lo && (t0 >= whole_lo || t0 + kTile <= p.sinks); };
+      auto store = [&](int t0, const float (&sum)[4], float old) {
         float total = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -396,25 +370,97 @@ __global__ void __launch_bounds__(kThreads, blocks_of(DQK, NB)) attn_kv_weights_
           if (c == i) total = x;
         }
         const int t = t0 + 8 * c + r;
-        if (t < ur.len) w[t] = t < set_from ? z.old + total : total;
+        if (t < ur.len) w[t] = t < set_from ? old + total : total;
       };
-      // two tiles in registers: one is computed with while the other one comes
-      KTile<G> ping, pong;
-      int here = token_of(0), next = token_of(1);  // (past the segment: past any length)
-      pages_of(here);
-      load(here, ping);
-      pages_of(next);
-      for (int u = 0; u < n; u += 2) {
-        load(next, pong);
-        const int after = token_of(u + 2);
-        pages_of(after);
-        tile(here, ping);
-        load(after, ping);
-        here = after;
-        const int last = next;
-        next = token_of(u + 3);
+
+      if constexpr (kMany) {
+        // The tile's operands serve all row blocks, so they are made first, and the next
+        // tile comes into the codes' registers; both halves of the tile go through a row block together.
+        KTile<G> z;
+        int here = token_of(0);
+        pages_of(here);
+        load(here, z);
+        pages_of(token_of(1));
+        for (int u = 0; u < n; ++u) {
+          uint32_t k[4][G][4], s[4][G / 2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) signed_codes(z.k[i][g], k[i][g]);
+#pragma unroll
+            for (int g = 0; g < G / 2; ++g) s[i][g] = z.s[i][g];
+          }
+          const float old = z.old;
+          const int t0 = here;
+          here = token_of(u + 1);
+          load(here, z);
+          pages_of(token_of(u + 2));
+          if (t0 >= ur.len) continue;
+          const bool whole = is_whole(t0);
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int i = 0; i < nb; ++i) {
+            const float2 x = *reinterpret_cast<const float2*>(s_xs + i * 8 + 2 * c);
+            const float2 l = *reinterpret_cast<const float2*>(s_lse + i * 8 + 2 * c);
+            const bool see0 = row0 + i * 8 + 2 * c < p.rows, see1 = row0 + i * 8 + 2 * c + 1 < p.rows;
+            uint4 qi[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) qi[g] = s_q[i][g][lane];
+            float y[2][4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+              products(k[2 * m], k[2 * m + 1], s[2 * m], s[2 * m + 1], qi, nullptr, y[m]);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) add(y[m], t0, m, whole, i, x.x, x.y, l.x, l.y, see0, see1, sum);
+          }
+          store(t0, sum, old);
+        }
+      } else {
+        auto tile = [&](int t0, const KTile<G>& z) {
+          if (t0 >= ur.len) return;
+          const bool whole = is_whole(t0);
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            uint32_t ka[G][4], kb[G][4];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              KCodes<DQK>::of(z.k[2 * m][g], ka[g]);
+              KCodes<DQK>::of(z.k[2 * m + 1][g], kb[g]);
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              uint4 qi[G];
+              float4 start[G];
+#pragma unroll
+              for (int g = 0; g < G; ++g) {
+                qi[g] = kHold ? qf[kHold ? i : 0][g] : s_q[i][g][lane];
+                start[g] = kHoldLow ? low[kHoldLow ? i : 0][g] : s_low[warp][kHoldLow ? 0 : i][kHoldLow ? 0 : g][c];
+              }
+              float y[4];
+              products(ka, kb, z.s[2 * m], z.s[2 * m + 1], qi, start, y);
+              add(y, t0, m, whole, i, xs[i][0], xs[i][1], ls[i][0], ls[i][1], col[i][0], col[i][1], sum);
+            }
+          }
+          store(t0, sum, z.old);
+        };
+        // two tiles in registers: one is computed with while the other one comes
+        KTile<G> ping, pong;
+        int here = token_of(0), next = token_of(1);  // (past the segment: past any length)
+        pages_of(here);
+        load(here, ping);
         pages_of(next);
-        tile(last, pong);
+        for (int u = 0; u < n; u += 2) {
+          load(next, pong);
+          const int after = token_of(u + 2);
+          pages_of(after);
+          tile(here, ping);
+          load(after, ping);
+          here = after;
+          const int last = next;
+          next = token_of(u + 3);
+          pages_of(next);
+          tile(last, pong);
+        }
       }
     }
     left -= n;
