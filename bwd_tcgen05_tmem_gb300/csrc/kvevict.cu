@@ -15,6 +15,13 @@
 //     what earlier rounds write, so the next round's rows are on their way meanwhile.
 // Nothing is kept in memory between the steps but the list; rows in front of the
 // first evicted token do not move.
+//
+// What bounds it: the rows' bytes, read and written, once behind the other.  64 x 4160
+// tokens of 8 kv heads of 128 / 128 cut down to 4096, one GB300: 133 us for 629 MB, 70 %
+// of what a copy reaches (a block of 1024 threads an SM, a scan for every 512
+// candidates and fenced barriers in the rounds took 214); 8 x 65536 to 32768 175 us for
+// 640 MB; 16 x 32768 to 4096 80 us, where the selection is half of the time; one request of
+// 1087 tokens 19 us: four counting passes, the list and two rounds one after the other.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -30,12 +37,19 @@ namespace attn {
 namespace cg = cooperative_groups;
 
 namespace {
-constexpr int kThreads = 256, kWarps = kThreads / 32, kBlocks = 4;  // blocks of an SM
+// Blocks of an SM: as many as their rows and counts leave room for (16 x 32768 tokens to 4096
+// 80 us, with three 178; the block of 1024 threads that the head names has the SM to itself).
+constexpr int kThreads = 256, kWarps = kThreads / 32, kBlocks = 4;
 constexpr int kPasses = 4, kBins = 1536;  // of the selection: 10, 8, 7 and 7 bits; their counts
 constexpr int kMaxCluster = 8;
-constexpr int kKeys = 8192;  // candidates of a block whose weights stay in shared memory
+// Candidates of a block whose weights stay in shared memory: 8 x 65536 tokens take 175 us,
+// with none 200.  11264 leave room for three blocks an SM (252).
+constexpr int kKeys = 8192;
+constexpr int kAhead = 4;  // candidates that a thread loads together
 constexpr int kStage = 19456;  // bytes of a round's rows of a block, at most
-constexpr int kMinSlice = 2048;  // candidates of a block: fewer are not worth another block's barriers
+// Candidates of a block, of which fewer are not worth another block's barriers: one
+// request of 1087 tokens takes 25 us with 2048, 21 with 512, 19 with 256, 19 with 128.
+constexpr int kMinSlice = 256;
 
 // A weight as a number whose order is the weights': NaN below all, -0 like 0.
 __device__ __forceinline__ uint32_t order_of(float w) {
@@ -192,34 +206,48 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attn_kv_evict_kernel(const 
 #pragma unroll
     for (int pass = 0; pass < kPasses; ++pass) {
       int* mine_h = hist + kFirst[pass];
-      for (int i0 = warp * 32; i0 < mine; i0 += kThreads) {
-        const int i = i0 + lane;
-        const uint32_t k = i < mine ? key(i) : 0u;
-        const bool in = i < mine && (pass == 0 || (k >> kShift[pass - 1]) == (border >> kShift[pass - 1]));
-        const int d = in ? (int)((k >> kShift[pass]) & (kDigits[pass] - 1)) : -1;
-        // (equal digits throughout, as of weights that are all alike, are one addition)
-        const int d0 = __shfl_sync(0xffffffffu, d, 0);
-        if (__all_sync(0xffffffffu, d == d0)) {
-          if (lane == 0 && d0 >= 0) atomicAdd(&mine_h[d0], 32);
-        } else if (in) {
-          atomicAdd(&mine_h[d], 1);
+      for (int i0 = warp * 32; i0 < mine; i0 += kAhead * kThreads) {
+        uint32_t k[kAhead];  // (loaded together: those that are not held come from far)
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const int i = i0 + a * kThreads + lane;
+          k[a] = i < mine ? key(i) : 0u;
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const int i = i0 + a * kThreads + lane;
+          const bool in = i < mine && (pass == 0 || (k[a] >> kShift[pass - 1]) == (border >> kShift[pass - 1]));
+          const int d = in ? (int)((k[a] >> kShift[pass]) & (kDigits[pass] - 1)) : -1;
+          // (equal digits throughout, as of weights that are all alike, are one addition)
+          const int d0 = __shfl_sync(0xffffffffu, d, 0);
+          if (__all_sync(0xffffffffu, d == d0)) {
+            if (lane == 0 && d0 >= 0) atomicAdd(&mine_h[d0], 32);
+          } else if (in) {
+            atomicAdd(&mine_h[d], 1);
+          }
         }
       }
       meet();
       // every block adds up all blocks' counts; thread t takes digits from the top on
       constexpr int kEach = 1024 / kThreads;
-      const int each = max(kDigits[pass] / kThreads, 1);
+      static_assert(kEach == 4, "a vector of counts, or one");
+      const int each = kDigits[pass] == 1024 ? kEach : 1;
       const bool digits = tid * each < kDigits[pass];
       int cnt[kEach], sum = 0;
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) {
-        cnt[j] = 0;
-        if (j < each && digits) {
-          const int d = kDigits[pass] - 1 - (tid * each + j);
-          for (int q = 0; q < C; ++q) cnt[j] += (C == 1 ? mine_h : cluster.map_shared_rank(mine_h, q))[d];
-          sum += cnt[j];
+      for (int j = 0; j < kEach; ++j) cnt[j] = 0;
+      if (digits)
+        for (int q = 0; q < C; ++q) {
+          const int* h_q = C == 1 ? mine_h : cluster.map_shared_rank(mine_h, q);
+          if (each == 4) {
+            const int4 x = *reinterpret_cast<const int4*>(h_q + kDigits[pass] - 4 - tid * 4);
+            cnt[0] += x.w, cnt[1] += x.z, cnt[2] += x.y, cnt[3] += x.x;
+          } else {
+            cnt[0] += h_q[kDigits[pass] - 1 - tid];
+          }
         }
-      }
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) sum += cnt[j];
       int2 total;
       int above = block_scan(make_int2(sum, 0), s_warp, total).x - sum;
 #pragma unroll
@@ -237,10 +265,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attn_kv_evict_kernel(const 
     border = 0xffffffffu;  // (no weight's number)
   }
   // ---- the list: `need` of the candidates on the border stay, the first ones.  A thread
-  // takes candidates in a row (an odd number of them: no two lanes' lie in one bank).
-  const int run = ((mine + kThreads - 1) / kThreads) | 1, i0 = min(tid * run, mine), i1 = min(i0 + run, mine);
+  // takes candidates in a row (an odd number of them: no two lanes' lie in one bank); of
+  // those that are not held a warp does, whole lines at a time.
+  const int run = held ? ((mine + kThreads - 1) / kThreads) | 1 : ((mine + kThreads - 1) / kThreads) * 32;
+  const int i0 = min((held ? tid : warp) * run, mine), i1 = min(i0 + run, mine), lane0 = held ? 0 : lane, next = held ? 1 : 32;
   int2 own = make_int2(0, 0), sums;  // above the border, on it
-  for (int i = i0; i < i1; ++i) {
+#pragma unroll 4
+  for (int i = i0 + lane0; i < i1; i += next) {
     const uint32_t k = key(i);
     own.x += k > border;
     own.y += k == border;
@@ -255,17 +286,45 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attn_kv_evict_kernel(const 
     on_before += s[1];
   }
   int gone = INT32_MAX;  // the first that goes, of this thread's
-  {
-    const int on0 = upto.y - own.y, room0 = max(need - on_before, 0);  // of the block: before this thread; for it
+  const int room0 = max(need - on_before, 0), last = p.keep - recent;  // for the block's on the border; the list's end
+  // (The list is full early only if another kernel changes the weights meanwhile.)
+  if (!held) {
+    int above0 = __shfl_sync(0xffffffffu, upto.x - own.x, 0), on0 = __shfl_sync(0xffffffffu, upto.y - own.y, 0);
+    const uint32_t before = (1u << lane) - 1u;
+    for (int i = i0; i < i1; i += kAhead * 32) {
+      uint32_t k[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) k[a] = i + a * 32 + lane < i1 ? key(i + a * 32 + lane) : 0u;
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int j = i + a * 32 + lane;
+        const bool there = j < i1;
+        const uint32_t above = __ballot_sync(0xffffffffu, there && k[a] > border);
+        const uint32_t on = __ballot_sync(0xffffffffu, there && k[a] == border);
+        const int on_here = on0 + __popc(on & before), at = to + above0 + __popc(above & before) + min(on_here, room0);
+        const bool stay = k[a] > border || (k[a] == border && on_here < room0);
+        if (there && !stay) gone = min(gone, first + c0 + j);
+        if (there && stay && at < last) kept[at] = first + c0 + j;
+        above0 += __popc(above), on0 += __popc(on);
+      }
+    }
+  } else {
+    const int on0 = upto.y - own.y;  // of the block's, before this thread
     int at = to + upto.x - own.x + min(on0, room0), left = max(room0 - on0, 0);
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t k = key(i);
-      const bool on = k == border, stay = k > border || (on && left > 0);
-      left -= on;
-      if (stay)
-        kept[at++] = first + c0 + i;
-      else
-        gone = min(gone, first + c0 + i);
+    for (int i = i0; i < i1; i += kAhead) {
+      uint32_t k[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) k[a] = i + a < i1 ? key(i + a) : 0u;
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        if (i + a >= i1) break;
+        const bool on = k[a] == border, stay = k[a] > border || (on && left > 0);
+        left -= on;
+        if (!stay)
+          gone = min(gone, first + c0 + i + a);
+        else if (at < last)
+          kept[at++] = first + c0 + i + a;
+      }
     }
   }
   for (int i = me; i < first; i += all) kept[i] = i;
@@ -295,10 +354,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attn_kv_evict_kernel(const 
     }
     return ((long long)page * p.c.heads + h) * p.c.page_size + (t & (p.c.page_size - 1));
   };
+  // (of such weights the list may lack entries: any token of the sequence stands in)
+  auto kept_at = [&](int i) { return (int)min((unsigned)__ldcg(kept + i), (unsigned)(n - 1)); };
   // where a round's rows come from and go to
   auto find = [&](int base, int slot) {
     for (int i = tid; i < S::kRows && base + i < p.keep; i += kThreads) {
-      const int src = __ldcg(kept + base + i);
+      const int src = kept_at(base + i);
       // (a row that comes from or goes to a page outside the cache is not written)
       const long long from = slot_row(src), dst = slot_row(base + i);
       s_src[slot][i] = from;
@@ -325,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attn_kv_evict_kernel(const 
   auto load = [&](int base, int buf, int slot) {
     const int rows = min(p.keep - base, S::kRows);
     const uint32_t st = smem_u32(smem) + buf * (S::kRows * S::kRow);
-    for (int i = tid; i < rows; i += kThreads) copy_bytes<4>(st + S::kAtW + i * 4, w + __ldcg(kept + base + i));
+    for (int i = tid; i < rows; i += kThreads) copy_bytes<4>(st + S::kAtW + i * 4, w + kept_at(base + i));
     if (p.c.num_pages == 0) return;  // (else row 0 is read where there is none)
     arrays(rows, [&](auto bytes, auto width, uint8_t* array, int at, int i) {
       copy_bytes<decltype(bytes)::value>(st + at, array + max(s_src[slot][i], 0ll) * decltype(width)::value);

@@ -323,6 +323,15 @@ def test_evict_batches(lens, h, keep):
     x.check(keep, [4] * len(lens), min(50, keep // 3), "spread")
 
 
+@pytest.mark.parametrize("kind", ["ties", "odd"])
+@pytest.mark.parametrize("lens,h,keep", [([100001, 90000, 66000], 2, 30000), ([9001] * 310, 1, 4000)])
+def test_evict_long_with_equal_weights(lens, h, keep, kind):
+    """Equal weights on the border, of candidates that shared memory does not hold: of a
+    cluster of 8 blocks, of single ones."""
+    x = Full(lens, h, 64, 64, 128, seed=keep)
+    x.check(keep, [i % 7 for i in range(len(lens))], 100, kind)
+
+
 def test_evict_again_and_again():
     """The budget of a running sequence: what stays is what a list says."""
     x = Full([257], 2, 128, 128, 16, seed=4)
