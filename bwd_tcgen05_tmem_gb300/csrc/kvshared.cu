@@ -33,6 +33,15 @@
 // q is held as in kvdecode.cu.  Probabilities are FP32 in the sum and rounded to fp16 for
 // the second product, times 2^11: their reference moves when a score passes it by 2^4, so
 // they stay below 2^15, and those 2^-35 below the row's maximum are still told from 0.
+//
+// What bounds it: instructions (59 % issue, the ALU pipe at 45 %, the tensor pipe at 44 %)
+// and the wait of each softmax row for its scores.  256 requests of 4 rows over 32K tokens, 8 kv
+// heads of 128, one GB300: 185 us, the prefix kernel 145 of them (0.95 PFLOP/s); plan 4,
+// own tokens 20, the two joins 14.  64 requests over 8K tokens 67 us.  The first
+// instruction cache is what K's and V's conversion in one loop, and loops that are not
+// unrolled, are for: apart they took 233 us.  Tiles of 128 keys 250, four softmax groups of
+// half a row 269.
+//
 // In a row of 8 dims the operand's order is 0 4 1 5 2 6 3 7 (a mask of a word of codes
 // makes pairs n, n + 4): Q is stored the same way, O's columns are put back at the end.
 #include <algorithm>
@@ -49,8 +58,11 @@ namespace {
 
 constexpr int KT = 64;  // keys of a tile: prefixes are taken in whole ones, the rest is the requests' own
 constexpr float kLag = 4.0f, kBias = 15.0f - kLag;  // a row's reference may lag its maximum; probabilities are held times 2^kBias
-constexpr int kXRing = 16;
-constexpr int kJoinParts = 12;  // of an item on average: from there on a block joins a row
+constexpr int kXRing = 16;  // factors of tiles on their way to the softmax groups
+// Parts of an item on average from which on a block joins a row: 256 requests over 32K take
+// 185 us with 12 and with 40, 205 with 3 (few parts, many rows); 4 samples of 1K tokens 31 with
+// 12, 42 with 40.
+constexpr int kJoinParts = 12;
 constexpr int kRowRing = 8;  // tiles that are looked up ahead
 constexpr int kThreads = 640;
 // Registers of a thread: 96 at the launch; the softmax groups, which hold a row of
@@ -88,18 +100,21 @@ __device__ __forceinline__ int sh_key_tiles(const SharedParams& p, const ShGroup
   return g.tokens / KT;
 }
 
+// Threads of the first kernel; the second where there are no more requests and groups (its
+// barriers are cheaper: 4 samples of 1K tokens 30.8 us, 31.6 with 1024).
+constexpr int kPlanThreads = 1024, kPlanFew = 256;
 // One block: which requests share what.
-__global__ void __launch_bounds__(1024) attn_kv_shared_plan_kernel(const __grid_constant__ SharedParams p) {
+__global__ void __launch_bounds__(kPlanThreads) attn_kv_shared_plan_kernel(const __grid_constant__ SharedParams p) {
   __shared__ int s_bad;
   __shared__ int s_items, s_sum[32];
   ShGroup* groups = (ShGroup*)p.group_info;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int T = (int)blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t cap = (int64_t)p.cols << p.c.page_shift;
   asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) s_bad = 0, s_items = 0;
   __syncthreads();
   bool bad = false;
-  for (int g = tid; g <= p.groups; g += 1024) {
+  for (int g = tid; g <= p.groups; g += T) {
     const int at = p.group_starts[g];
     bad |= at < 0 || at > p.batch || (g > 0 && p.group_starts[g - 1] > at);
   }
@@ -107,7 +122,7 @@ __global__ void __launch_bounds__(1024) attn_kv_shared_plan_kernel(const __grid_
   __syncthreads();
   const bool none = s_bad != 0;  // groups that are not in order share nothing
   bad = none;
-  for (int g = tid; g < p.groups; g += 1024) {
+  for (int g = tid; g < p.groups; g += T) {
     const int n = p.shared_lens[g];
     const bool ok = n >= 0 && n <= cap;
     bad |= !ok;
@@ -132,7 +147,7 @@ __global__ void __launch_bounds__(1024) attn_kv_shared_plan_kernel(const __grid_
     const int n = groups[lo].tokens, len = p.seq_lens[b];
     return n > 0 && len <= cap && len - p.seqlen_q >= n ? lo : -1;
   };
-  for (int b = tid; b < p.batch; b += 1024) {
+  for (int b = tid; b < p.batch; b += T) {
     const int g = group_of(b);
     p.group_of[b] = g;
     if (g >= 0) {
@@ -142,14 +157,14 @@ __global__ void __launch_bounds__(1024) attn_kv_shared_plan_kernel(const __grid_
   }
   __syncthreads();
   // a prefix that one request has alone is that request's own
-  for (int b = tid; b < p.batch; b += 1024) {
+  for (int b = tid; b < p.batch; b += T) {
     int g = p.group_of[b];
     if (g >= 0 && __ldcg(&groups[g].members) < 2) p.group_of[b] = g = -1;
     p.starts[b] = g >= 0 ? groups[g].tokens : 0;
   }
   __syncthreads();
   int before = 0, items = 0;  // (the host has refused calls whose units could pass 2^31)
-  for (int g0 = 0; g0 < p.groups; g0 += 1024) {
+  for (int g0 = 0; g0 < p.groups; g0 += T) {
     const int g = g0 + tid;
     ShGroup x;
     int units = 0;
@@ -174,7 +189,7 @@ __global__ void __launch_bounds__(1024) attn_kv_shared_plan_kernel(const __grid_
     if (lane == 31) s_sum[warp] = j;
     __syncthreads();
     x.unit0 = before + j - units;
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < T / 32; ++w) {
       if (w < warp) x.unit0 += s_sum[w];
       before += s_sum[w];
     }
@@ -999,7 +1014,8 @@ void shared_tiles(int d_v, int& row_tile, int& key_tile) {
 size_t shared_group_bytes() { return sizeof(ShGroup); }
 
 cudaError_t launch_kv4_shared_prefix(const SharedParams& p, bool bf16, int num_sms, cudaStream_t st) {
-  attn_kv_shared_plan_kernel<<<1, 1024, 0, st>>>(p);
+  const int threads = std::max(p.batch, p.groups + 1) <= kPlanFew ? kPlanFew : kPlanThreads;
+  attn_kv_shared_plan_kernel<<<1, threads, 0, st>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return bf16 ? sh_dims<true>(p, num_sms, st) : sh_dims<false>(p, num_sms, st);
