@@ -9,6 +9,14 @@ A step of a serving loop:
   kv.kv4_write(cache, k, v, p.slots)
   o, lse = kv.kv4_decode(q, cache, table, p.seq_lens)
 
+Requests that share a prompt's pages read it once for all of them, and a batch can
+be held to a budget of tokens by the attention that they receive:
+
+  o, lse = kv.kv4_decode_shared(q, cache, table, p.seq_lens, group_starts, shared_lens)
+  kv.kv4_weights(q, cache, table, p.seq_lens, lse, weights)
+  e = kv.kv4_evict(cache, table, p.seq_lens, weights, keep=budget, first=prompt, recent=64,
+                   free_pages=free, free_head=p.free_head)  # lengths and free pages for plan
+
 Longer chunks of a prompt read their prefix back instead (plan with
 free_pages=None maps tokens that are held already, kv4_read returns their rows)
 and use attn.fwd.  Nothing here copies to the host or synchronises, so a step
