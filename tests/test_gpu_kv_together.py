@@ -161,3 +161,34 @@ def test_captured_steps_are_the_same():
         assert all(torch.equal(s, t) for s, t in zip(a.state(), b.state())), i
     attn.query_status(a.status)
     attn.query_status(b.status)
+
+
+def test_pages_and_rows_past_32_bits():
+    """The same requests in the first pages of a cache of 9 GB and in its last ones, and
+    with rows 4 GB apart: the same bits from each operator."""
+    h, d, page, pages, lens = 8, 64, 256, 70000, [700, 530]
+    c = kv.KV4Cache.empty(pages, h, d, d, page_size=page)
+    tables = [[[3, 1, 2], [3, 1, 4]], [[pages - 1, pages - 3, pages - 2], [pages - 1, pages - 3, pages - 4]]]
+    g = torch.Generator().manual_seed(23)
+    k, v = (torch.randn(512 + 188 + 18, h, d, generator=g).to(BF).cuda() for _ in range(2))
+    q = torch.randn(2, 1, 16, d, generator=g).to(BF).cuda()
+    far = 2 ** 31 + 1024
+    buf = torch.empty(far + 16 * d, dtype=BF, device="cuda")
+    q_far = buf.as_strided(q.shape, (far, 16 * d, d, 1))
+    q_far.copy_(q)
+    n, starts, shared = i32(lens), i32([0, 2]), i32([512])
+    got = []
+    for i, t in enumerate(tables):
+        at = [t[0][j // page] * page + j % page for j in range(700)] + [t[1][2] * page + j for j in range(18)]
+        kv.kv4_write(c, k, v, i32(at))
+        table, status = i32(t), torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = q_far if i else None  # (q is not needed any more where o goes)
+        o, lse = kv.kv4_decode_shared(q if i else q_far, c, table, n, starts, shared, out=out, status=status)
+        w = kv.kv4_weights(q, c, table, n, lse, torch.zeros(2, h, 768, device="cuda"), status=status)
+        before = w.clone()
+        e = kv.kv4_evict(c, table, n, w, keep=525, first=i32([512, 512]), recent=4, status=status)
+        attn.query_status(status)
+        slots = i32([[t[b][j // page] * page + j % page for j in range(525)] for b in range(2)])
+        got.append([o.clone(), lse, before, w, e.kept, e.seq_lens, *kv.kv4_read(c, slots.flatten())])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
