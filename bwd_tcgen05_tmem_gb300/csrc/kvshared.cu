@@ -36,8 +36,8 @@
 //
 // What bounds it: instructions (59 % issue, the ALU pipe at 45 %, the tensor pipe at 44 %)
 // and the wait of each softmax row for its scores.  256 requests of 4 rows over 32K tokens, 8 kv
-// heads of 128, one GB300: 185 us, the prefix kernel 145 of them (0.95 PFLOP/s); plan 4,
-// own tokens 20, the two joins 14.  64 requests over 8K tokens 67 us.  The first
+// heads of 128, one GB300: 182 us, the prefix kernel 145 of them (0.95 PFLOP/s); plan 4,
+// own tokens 20, the two joins 14.  64 requests over 8K tokens 64.5 us.  The first
 // instruction cache is what K's and V's conversion in one loop, and loops that are not
 // unrolled, are for: apart they took 233 us.  Tiles of 128 keys 250, four softmax groups of
 // half a row 269.
@@ -60,7 +60,7 @@ constexpr int KT = 64;  // keys of a tile: prefixes are taken in whole ones, the
 constexpr float kLag = 4.0f, kBias = 15.0f - kLag;  // a row's reference may lag its maximum; probabilities are held times 2^kBias
 constexpr int kXRing = 16;  // factors of tiles on their way to the softmax groups
 // Parts of an item on average from which on a block joins a row: 256 requests over 32K take
-// 185 us with 12 and with 40, 205 with 3 (few parts, many rows); 4 samples of 1K tokens 31 with
+// 185 us with 12 and with 40 (one build), 205 with 3 (few parts, many rows); 4 samples of 1K tokens 31 with
 // 12, 42 with 40.
 constexpr int kJoinParts = 12;
 constexpr int kRowRing = 8;  // tiles that are looked up ahead
