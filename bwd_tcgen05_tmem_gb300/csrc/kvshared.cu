@@ -59,7 +59,7 @@ namespace {
 constexpr int KT = 64;  // keys of a tile: prefixes are taken in whole ones, the rest is the requests' own
 constexpr float kLag = 4.0f, kBias = 15.0f - kLag;  // a row's reference may lag its maximum; probabilities are held times 2^kBias
 constexpr int kXRing = 16;  // factors of tiles on their way to the softmax groups
-// Parts of an item on average from which on a block joins a row: 256 requests over 32K take
+// Parts of an item on average above which a block joins a row: 256 requests over 32K take
 // 185 us with 12 and with 40 (one build), 205 with 3 (few parts, many rows); 4 samples of 1K tokens 31 with
 // 12, 42 with 40.
 constexpr int kJoinParts = 12;
@@ -896,7 +896,7 @@ __global__ void __launch_bounds__(256, 6) attn_kv_shared_join_kernel(const __gri
   const int d4 = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const ShRuns runs(__ldcg(p.total_units), most_runs);
-  const bool together = runs.runs >= kJoinParts * __ldcg(p.total_units + 1);
+  const bool together = runs.runs > kJoinParts * __ldcg(p.total_units + 1);  // (not where nothing is shared)
   const int per = together ? 1 : kGroups;
   for (int64_t at0 = (int64_t)blockIdx.x * per; at0 < all; at0 += (int64_t)gridDim.x * per) {
     const int64_t at = at0 + (together ? 0 : group);
