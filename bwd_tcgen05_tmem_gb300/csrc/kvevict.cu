@@ -96,10 +96,17 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int b) {
   if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);
   return 0;
 }
-// Pages of a sequence that an eviction leaves without tokens: columns from .. to - 1.
 __device__ __forceinline__ int pages_of(const EvictParams& p, int n) { return (n + p.c.page_size - 1) >> p.c.page_shift; }
-__device__ __forceinline__ int pages_gone(const EvictParams& p, int n) {
-  return n > p.keep ? pages_of(p, n) - pages_of(p, p.keep) : 0;
+// Pages of a sequence that an eviction leaves without tokens: columns from .. from + count - 1.
+// (One that holds a protected token is not among them, though that token goes where more
+// are protected than stay: other sequences may hold the page too.)
+struct PagesGone {
+  int from, count;
+};
+__device__ __forceinline__ PagesGone pages_gone(const EvictParams& p, int b, int n) {
+  if (n <= p.keep) return {0, 0};
+  const int from = pages_of(p, p.first ? max(p.keep, min(p.first[b], n)) : p.keep);
+  return {from, pages_of(p, n) - from};
 }
 
 // The new length of sequence b, and its pages for the free list, in front of the
@@ -109,7 +116,7 @@ __device__ void evict_lists(const EvictParams& p, int b, int n, int2* s_warp) {
   if (!p.free_head) return;
   int before = 0, all = 0;
   for (int i = threadIdx.x; i < p.batch; i += kThreads) {
-    const int g = pages_gone(p, evict_len(p, i));
+    const int g = pages_gone(p, i, evict_len(p, i)).count;
     all += g;
     if (i < b) before += g;
   }
@@ -124,9 +131,9 @@ __device__ void evict_lists(const EvictParams& p, int b, int n, int2* s_warp) {
     return;
   }
   const int32_t* row = p.table + (int64_t)b * p.table_stride;
-  const int from = pages_of(p, p.keep), gone = pages_gone(p, n);
-  for (int i = threadIdx.x; i < gone; i += kThreads) {
-    int page = row[from + i];
+  const PagesGone gone = pages_gone(p, b, n);
+  for (int i = threadIdx.x; i < gone.count; i += kThreads) {
+    int page = row[gone.from + i];
     if ((unsigned)page >= (unsigned)p.c.num_pages) {
       page = -1;
       if (p.status) atomicCAS(p.status, DEV_OK, DEV_BAD_INDEX);

@@ -323,7 +323,8 @@ def kv4_evict(cache, block_table, seq_lens, weights, *, keep, first=None, recent
 
     weights: float32 [B, heads_kv, capacity], changed in place unless ``weights_out``
     is given.  first: int32 [B] or None.  free_pages and free_head (as kv.plan takes
-    them): pages that are left over are put in front of free_head."""
+    them): pages that are left over are put in front of free_head, but none that holds a
+    token below first[b] (a budget shorter than a prefix that is shared: see the header)."""
     check_buffers(status)
     lib = fast()
     b = seq_lens.shape[0]

@@ -610,10 +610,15 @@ attn_status_t attn_kv_weights(const attn_kv4_weights_params_t* p, const attn_kv4
  * evicted).  Rows in front of the first evicted token are not written: a prefix that
  * other sequences share may stay in front under `first`.  Pages that hold other tokens
  * of an evicted sequence must be its own.
- * With free_head the pages past ceil(keep / page_size) go back to the list that
- * attn_kv_plan takes from: with g of them in all, free_pages[free_head[0] - g ..
+ * With free_head the pages of evicted sequences that hold neither one of the `keep` tokens
+ * nor a first one (columns from ceil(max(keep, first[b]) / page_size) on) go back to the list
+ * that attn_kv_plan takes from: with g of them in all, free_pages[free_head[0] - g ..
  * free_head[0]) is written, sequence after sequence, and free_head_out[0] =
- * free_head[0] - g.  If there are not g entries in front of free_head[0], or that lies
+ * free_head[0] - g.  (Where first[b] > keep, a budget shorter than what it protects, pages
+ * of the first tokens that go are the caller's to give back once, since other sequences may
+ * hold them; and unless keep is a multiple of page_size the sequence ends inside such a page,
+ * in which attn_kv_plan would put its next tokens: if others hold it, the caller
+ * gives the sequence a copy of that page before.)  If there are not g entries in front of free_head[0], or that lies
  * past n_free, no page is given back, free_head_out[0] = free_head[0] and the status word
  * is set.  A page outside the cache is given back as -1 and sets the status word, as one
  * that holds a row to move does (that row then stays).  free_head NULL: free_pages and

@@ -452,3 +452,38 @@ def test_evict_a_shared_prefix_stays_in_place():
     x.table[1][:3] = x.table[0][:3]
     x.t.copy_(i32(x.table))
     x.check(150, [96, 96], 10)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("keep", [1, 40, 64, 127, 128, 129])
+def test_evict_gives_no_page_of_protected_tokens_back(page, keep):
+    """Sequences over one prefix of 128 tokens, longer than the budget or not: its pages stay
+    out of the free list, the sequences' own ones come back once each."""
+    x = Full([200, 131, 128, 300, 250], 2, 64, 64, page, seed=12)
+    for row in x.table[1:4]:
+        row[:128 // page] = x.table[0][:128 // page]
+    x.t.copy_(i32(x.table))
+    first = [128, 128, 128, 128, 2 ** 31 - 1]  # (the last one is protected as a whole)
+    back = [x.table[b][j] for b, n in enumerate(x.lens) if n > keep
+            for j in range(-(-max(keep, min(first[b], n)) // page), -(-n // page))]
+    assert len(set(back)) == len(back) > 0
+    # what no longer fits the list, and what does
+    for head in (len(back) - 1, len(back)):
+        free, status = torch.full((40,), -9, dtype=torch.int32, device="cuda"), zero()
+        before = [a.clone() for a in (x.cache.k_codes, x.cache.v_codes)] if keep <= 128 else []
+        r = kv.kv4_evict(x.cache, x.t, x.l, x.weights("spread").cuda(), keep=keep, first=i32(first), free_pages=free,
+                         free_head=i32([head]), status=status)
+        assert r.seq_lens.tolist() == [min(n, keep) for n in x.lens]
+        if head < len(back):
+            assert r.free_head.tolist() == [head] and (free == -9).all()
+            with pytest.raises(attn.AttnError, match="out of range"):
+                attn.query_status(status)
+        else:
+            assert r.free_head.tolist() == [0] and free.tolist() == back + [-9] * (40 - len(back))
+            attn.query_status(status)
+        for a, b in zip(before, (x.cache.k_codes, x.cache.v_codes)):
+            assert torch.equal(a, b)  # (nothing to move: what stays is the first tokens)
+        stay = torch.arange(keep, dtype=torch.int32)
+        for b, n in enumerate(x.lens):
+            if n > keep and keep <= 128:
+                assert torch.equal(r.kept[b].cpu(), stay.expand(2, -1))
