@@ -43,7 +43,7 @@ HOST_UPLOAD, HOST_COMPUTE, HOST_DOWNLOAD, HOST_ALL = 1, 2, 4, 7
 # attn_bwd_path results: which backward kernels run (and the stage order)
 BWD_RECOMPUTE, BWD_DS, BWD_PDS = 0, 1, 2
 # attn_debug_inject kernel bits (test only)
-DEBUG_FWD, DEBUG_DQ, DEBUG_DKDV, DEBUG_SCORES = 1, 2, 4, 8
+DEBUG_FWD, DEBUG_DQ, DEBUG_DKDV, DEBUG_SCORES, DEBUG_SHARED = 1, 2, 4, 8, 16
 
 
 class AttnError(RuntimeError):
@@ -520,8 +520,8 @@ def lse_merge(o_parts, lse_parts, row0, nrows, rows, *, out=None, lse_out=None,
 
 
 def debug_inject(kernel_mask, drop_load, wait_limit_ns=0):
-    """TEST ONLY: arm attn_debug_inject for the next attn_fwd / attn_bwd call on
-    this thread (the first CTA of each selected kernel leaves out load
+    """TEST ONLY: arm attn_debug_inject for the next attn_fwd / attn_bwd /
+    attn_kv_decode_shared call on this thread (the first CTA of each selected kernel leaves out load
     ``drop_load`` and waits at most ``wait_limit_ns``; 0 keeps 2 s)."""
     load().attn_debug_inject(int(kernel_mask), int(drop_load), int(wait_limit_ns))
 

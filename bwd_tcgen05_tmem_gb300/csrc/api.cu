@@ -74,6 +74,7 @@ int num_sms() {
   if (dev >= 0 && dev < 64) cache[dev] = n;
   return n;
 }
+DebugInject api_inject(unsigned kernel_bit) { return inject_for(take_inject(), kernel_bit); }
 void api_begin() {
   g_err[0] = 0;
   g_launches = 0;

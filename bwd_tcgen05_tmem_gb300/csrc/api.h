@@ -6,12 +6,14 @@
 #include <stdint.h>
 
 #include "../../include/attn.h"
+#include "kcommon.cuh"
 
 namespace attn {
 
 int num_sms();  // of the current device
 void api_begin();  // clears this thread's error string and launch count
 attn_status_t api_fail(attn_status_t s, const char* fmt, ...);
+DebugInject api_inject(unsigned kernel_bit);  // what attn_debug_inject asks of this call (and no later one)
 // cudaSuccess: adds n to the launch count; otherwise ATTN_ERR_CUDA
 attn_status_t api_launched(cudaError_t e, int n, const char* what);
 

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kcommon.cuh"
+
 namespace attn {
 
 // Quotients by a number known at launch: n / d for 0 <= n < 2^31, d >= 1
@@ -131,6 +133,7 @@ struct SharedParams {  // attention of batches whose requests share their first 
   float *row_o, *row_ml;       // parts of items that one run finished: [2][batch][heads][rows][d_v], [..][2]
   float *cut_o, *cut_ml;       // parts of the others: [num_sms][2][row_tile][d_v], [..][2]
   int* status;
+  DebugInject dbg;
 };
 void shared_tiles(int d_v, int& row_tile, int& key_tile);
 size_t shared_group_bytes();

@@ -903,6 +903,7 @@ attn_status_t attn_kv_decode_shared(const attn_kv4_decode_params_t* p, const att
                                     const int32_t* block_table, const int32_t* seq_lens, void* o, float* lse,
                                     void* ws, size_t ws_bytes, int32_t* status, attn_stream_t stream) {
   api_begin();
+  const attn::DebugInject dbg = attn::api_inject(ATTN_DEBUG_SHARED);
   attn::DecodeParams dp;
   attn_status_t s = check_shared(p, cache, groups, dp);
   if (s) return s;
@@ -987,6 +988,7 @@ attn_status_t attn_kv_decode_shared(const attn_kv4_decode_params_t* p, const att
   kp.cut_o = (float*)(w + l.cut_o);
   kp.cut_ml = (float*)(w + l.cut_ml);
   kp.status = status;
+  kp.dbg = dbg;
   // the requests' own tokens: into the workspace, in FP32
   dp.o = kp.own_o;
   dp.lse = kp.own_lse;

@@ -424,7 +424,7 @@ struct ShSide {
 template <int DQK, int DV>
 __device__ __forceinline__ void sh_convert(const uint8_t* codes, const uint16_t* scales, bool is_k, uint8_t* operand,
                                            uint64_t* full, uint64_t* empty, ShBars& bars, int (*x_exp)[2],
-                                           const ShRows* rows, int n, const Abort& ab) {
+                                           const ShRows* rows, int n, int dropped, const Abort& ab) {
   constexpr int kStages = ShShape<DQK, DV>::kKS;
   static_assert(kStages == ShShape<DQK, DV>::kVS, "one code for both sides");
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, half = warp & 1;
@@ -455,9 +455,37 @@ __device__ __forceinline__ void sh_convert(const uint8_t* codes, const uint16_t*
       x.store(dst + stage * (KT * 64 * x.G), row8, c);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[stage]);
+      if (lane == 0 && !(is_k && t == dropped)) mbar_arrive(&full[stage]);
     }
     if (t + 2 < n && !load(t + 2)) return;
+  }
+}
+
+// Where the part of a row lies, of the rows of whole items or of cut ones.  (Where the
+// softmax groups take turns, the second one's part lies beside the first's.)
+template <class S>
+__device__ __forceinline__ int64_t sh_part_row(const SharedParams& p, const ShPiece& pc, bool both, int slot, int r,
+                                               int b, int rest, bool& whole) {
+  whole = pc.kt == 0 && pc.kt_end == pc.key_tiles;
+  const int part = S::kSlots == 2 && !both ? slot : 0;
+  if (whole) return ((int64_t)part * p.batch + b) * p.c.heads * p.rows + (int64_t)pc.head * p.rows + rest;
+  return ((int64_t)blockIdx.x * 2 + (pc.kt == 0 ? 1 : 0)) * S::kRT + (both ? slot * 128 : part * 128) + r;
+}
+
+// A softmax thread's rows where its block gave up: sums of NaN, which the join turns into
+// rows of NaN.  (It must not take what the workspace held before for this call's parts.)
+template <class S>
+__device__ __noinline__ void sh_give_up(const SharedParams& p, int u0, int u1, int slot, int r) {
+  ShPiece pc;
+  pc.begin(p, u0, u1);
+  while (pc.next(p)) {
+    const bool both = S::kSlots == 2 && pc.row_slots(p) == 2;
+    const long long row = (long long)pc.row_tile * S::kRT + (both ? slot * 128 : 0) + r;
+    if (row >= (long long)pc.info.members * p.rows) continue;
+    const int member = (int)p.by_rows.div((uint32_t)row), rest = (int)(row - (long long)member * p.rows);
+    bool whole;
+    const int64_t at = sh_part_row<S>(p, pc, both, slot, r, pc.info.first + member, rest, whole);
+    *reinterpret_cast<float2*>((whole ? p.row_ml : p.cut_ml) + at * 2) = make_float2(0.0f, NAN);
   }
 }
 
@@ -517,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5;
 
-  Abort ab{&abort_flag, p.status, kWaitLimitNs};
+  Abort ab{&abort_flag, p.status, wait_limit(p.dbg)};
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int i = 0; i < 4; ++i) {
@@ -565,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
     const bool is_k = warp < 12;
     sh_convert<DQK, DV>(is_k ? p.c.k_codes : p.c.v_codes, is_k ? p.c.k_scales : p.c.v_scales, is_k, is_k ? sK : sV,
                         is_k ? bars.kfull : bars.vfull, is_k ? bars.kempty : bars.vempty, bars, is_k ? k_exp : v_exp,
-                        rows, u1 - u0, ab);
+                        rows, u1 - u0, dropped_load(p.dbg), ab);
   } else if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 18) sh_look_up<DQK, DV>(p, bars, rows, u0, u1, ab);
@@ -651,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
     uint64_t* drain = &bars.drain[warp == 17 ? 1 : warp == 16 ? 0 : 2];
     if (elect_sync()) {
       mma_commit(drain);
-      mbar_wait_quiet(drain, 0, kWaitLimitNs);
+      mbar_wait_quiet(drain, 0, ab.limit_ns);
     }
     __syncwarp();
     }
@@ -820,26 +848,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
         tc_fence_before();
         mbar_arrive(&bars.p_full[slot][buf]);
       }
-      if (!ok) break;
+      if (!ok) {  // (what has been stored is there before TMEM is given back)
+        tmem_st_wait();
+        tc_fence_before();
+        break;
+      }
       // ---- the piece's part: O, maximum and sum of each row
       for (uint32_t n = used > 2 ? used - 2 : 0; n < used && ok; ++n)
         ok = mbar_wait_warp(&bars.o_done[slot][n & 1u], (n >> 1) & 1u, ab);
       // (nothing reads Q any more, the other group's tiles included)
-      if (!ok || !mbar_wait_warp(&bars.q_empty, pieces & 1u, ab)) break;
+      ok = ok && mbar_wait_warp(&bars.q_empty, pieces & 1u, ab);
+      if (!ok) break;
       tc_fence_after();
-      const bool whole = pc.kt == 0 && pc.kt_end == pc.key_tiles;
-      // (where the groups take turns, the second one's part lies beside the first's)
-      const int part = S::kSlots == 2 && !both ? slot : 0;
-      float *o, *ml;
-      if (whole) {
-        const int64_t at = ((int64_t)part * p.batch + b) * p.c.heads * p.rows + (int64_t)pc.head * p.rows + rest;
-        o = p.row_o + at * DV;
-        ml = p.row_ml + at * 2;
-      } else {
-        const int64_t at = ((int64_t)blockIdx.x * 2 + (pc.kt == 0 ? 1 : 0)) * S::kRT + (both ? slot * 128 : part * 128) + r;
-        o = p.cut_o + at * DV;
-        ml = p.cut_ml + at * 2;
-      }
+      bool whole;
+      const int64_t at = sh_part_row<S>(p, pc, both, slot, r, b, rest, whole);
+      float* const o = (whole ? p.row_o : p.cut_o) + at * DV;
+      float* const ml = (whole ? p.row_ml : p.cut_ml) + at * 2;
       if (live) *reinterpret_cast<float2*>(ml) = make_float2(m_run - kBias, l_run);
       if (tiles > 0) {
         const uint32_t ob = tmem + lane_off + S::kTmemO + slot * DV;
@@ -875,6 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
       tc_fence_before();
       ++pieces;
     }
+    if (!ok) sh_give_up<S>(p, u0, u1, slot, r);
   }
   __syncthreads();
   if (warp == 16) {

@@ -541,8 +541,9 @@ attn_status_t attn_kv_decode(const attn_kv4_decode_params_t* p, const attn_kv4_c
  * the shared part, the others lose bits.
  * group_starts that do not ascend within [0, batch] (no group shares anything then),
  * shared_lens out of [0, cols * page_size] (that group shares nothing) set the status
- * word, beside what attn_kv_decode reports.  Every wait of the kernels has a limit (2 s);
- * when one runs out the status word tells ATTN_ERR_TIMEOUT.
+ * word, beside what attn_kv_decode reports.  Every wait of the kernels on an mbarrier has a
+ * limit (2 s); when one runs out the status word tells ATTN_ERR_TIMEOUT, and rows of O and LSE
+ * that lack a part for it are NaN.
  * Bitwise reproducible for the same call on the same device.  Lengths, groups and prefixes
  * are read on the device: a captured call serves any.
  * workspace: 256-byte aligned, attn_kv_decode_shared_workspace_size() bytes (of the
@@ -662,8 +663,8 @@ int attn_last_launch_count(void);
  * word, lets its in-flight copies land, drains its MMAs, frees its TMEM and
  * returns -- no kernel traps or hangs (PR #3699's bot review found a
  * "missing wait" on a reused barrier phase; this is the guard against that
- * class of bug).  This call arms the NEXT attn_fwd / attn_bwd* call on the
- * calling thread, then clears itself: in every kernel selected by
+ * class of bug).  This call arms the NEXT attn_fwd / attn_bwd* /
+ * attn_kv_decode_shared call on the calling thread, then clears itself: in every kernel selected by
  * `kernel_mask` (ATTN_DEBUG_* bits), one CTA leaves out load number
  * `drop_load` (-1: none) and, if `wait_limit_ns` is non-zero, waits at most
  * that long instead of 2 s.  In the dQ kernel, which runs work items from a
@@ -672,16 +673,18 @@ int attn_last_launch_count(void);
  * item, and every CTA of the launch uses the shorter limit (a healthy wait
  * lasts microseconds); in the other
  * kernels it is the first CTA (block 0,0,0), the load number counts its
- * stage/ring loads, and only that CTA uses the shorter limit.  No other call
+ * stage/ring loads (in the shared prefix's kernel the K tiles that it converts),
+ * and only that CTA uses the shorter limit.  No other call
  * is affected.  A dropped load makes a wait run out, so the call reports
  * ATTN_ERR_TIMEOUT through attn_query_status and leaves its outputs
- * undefined; the device stays usable and later calls are unaffected.
+ * undefined (attn_kv_decode_shared: as stated there); the device stays usable and later calls are unaffected.
  */
 enum {
   ATTN_DEBUG_FWD = 1,    /* forward kernel */
   ATTN_DEBUG_DQ = 2,     /* dQ kernel, or the dQ GEMM of the materialising backward */
   ATTN_DEBUG_DKDV = 4,   /* dK/dV kernel, or the dK/dV GEMMs of the materialising backward */
-  ATTN_DEBUG_SCORES = 8  /* P/dS scores kernel of the materialising backward */
+  ATTN_DEBUG_SCORES = 8, /* P/dS scores kernel of the materialising backward */
+  ATTN_DEBUG_SHARED = 16 /* prefix kernel of attn_kv_decode_shared */
 };
 void attn_debug_inject(unsigned kernel_mask, int drop_load, uint64_t wait_limit_ns);
 

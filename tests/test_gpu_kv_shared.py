@@ -343,3 +343,32 @@ def test_shared_nothing():
     assert torch.equal(o, a) and torch.equal(lse, b)
     o, lse = kv.kv4_decode_shared(q[:0], x.cache, x.t[:0], x.l[:0], i32([0]), none)
     assert o.shape == (0, 1, 2, 64)
+
+
+@pytest.mark.parametrize("dropped", [0, 1, 5])
+@pytest.mark.parametrize("members", [3, 40])
+@pytest.mark.parametrize("dqk,dv", DIMS)
+def test_shared_wait_that_runs_out(dqk, dv, members, dropped):
+    """One tile's K is never announced, and the first block gives up after 20 ms: the call
+    returns, says so, and its rows (of the first kv head's first row tile) are NaN instead of
+    numbers that take an earlier call's parts; the others and the next call are right.
+    (3 requests: the softmax groups take turns; 40: they have rows of their own.)"""
+    x = Groups([(40960, [3] * members), (128, [5, 6])], 2, dqk, dv, 64, BF, seed=17, loose=2)
+    q, status = x.q(1, 8), zero()
+    ws = torch.empty(kv.decode_shared_workspace_size(q, x.cache, x.t, 2), dtype=torch.uint8, device="cuda")
+    o, lse = x.call(q, workspace=ws, status=status)
+    attn.query_status(status)
+    for word in (status, None):
+        attn.debug_inject(attn.DEBUG_SHARED, dropped, 20_000_000)
+        bad, bad_lse = x.call(q, workspace=ws, status=word)
+        lost = torch.zeros(len(x.lens), 8, dtype=torch.bool, device="cuda")
+        lost[2:2 + min(members, 32 if dv > 128 else 64), :4] = True  # 128 or 256 rows, 4 of a request
+        assert torch.equal(torch.isnan(bad_lse[:, :, 0]), lost) and torch.equal(bad_lse[:, :, 0][~lost], lse[:, :, 0][~lost])
+        assert torch.isnan(bad[:, 0][lost]).all() and torch.equal(bad[:, 0][~lost], o[:, 0][~lost])
+    with pytest.raises(attn.AttnError) as e:
+        attn.query_status(status)
+    assert e.value.code == 6  # ATTN_ERR_TIMEOUT
+    status.zero_()
+    o2, lse2 = x.call(q, workspace=ws, status=status)
+    attn.query_status(status)
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
