@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_kv_shared_plan_kernel(const
       if (p.group_starts[mid] <= b) lo = mid; else hi = mid;
     }
     const int n = groups[lo].tokens, len = p.seq_lens[b];
-    return n > 0 && len <= cap && len - p.seqlen_q >= n ? lo : -1;
+    return n > 0 && len <= cap && len >= n + p.seqlen_q ? lo : -1;
   };
   for (int b = tid; b < p.batch; b += T) {
     const int g = group_of(b);

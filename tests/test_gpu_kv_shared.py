@@ -372,3 +372,21 @@ def test_shared_wait_that_runs_out(dqk, dv, members, dropped):
     o2, lse2 = x.call(q, workspace=ws, status=status)
     attn.query_status(status)
     assert torch.equal(o2, o) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("sq", [1, 3])
+@pytest.mark.parametrize("bad", [-2 ** 31, -2 ** 31 + 1, -2 ** 31 + 2, -2 ** 31 + 3, -300])
+def test_shared_lengths_far_below_zero(bad, sq):
+    """They count as 0 too, so their requests share nothing (and leave a group of two alone)."""
+    x = Groups([(256, [5, 6, 7]), (192, [8, 9])], 1, 64, 64, 64, BF, seed=18)
+    q = x.q(sq, 4)
+    ref = x.reference(q)
+    for at in (1, 4):
+        status, lens = zero(), list(x.lens)
+        lens[at] = bad
+        o, lse = kv.kv4_decode_shared(q, x.cache, x.t, i32(lens), x.s, x.n, status=status)
+        with pytest.raises(attn.AttnError, match="out of range"):
+            attn.query_status(status)
+        assert (o[at] == 0).all() and torch.isneginf(lse[at]).all()
+        keep = [b for b in range(5) if b != at]
+        within(o[keep], lse[keep], [r[keep] for r in ref])
