@@ -704,10 +704,13 @@ attn_status_t attn_kv_weights(const attn_kv4_weights_params_t* p, const attn_kv4
   if (s) return s;
   if (p->capacity < 0) return api_fail(ATTN_ERR_INVALID_ARG, "capacity < 0");
   if ((s = check_status_word(status))) return s;
-  if (p->batch == 0 || p->seqlen_q == 0) return ATTN_OK;
-  if ((s = check_rows("q", q, p->stride_q, p->batch, p->seqlen_q, p->heads_q, cache->d_qk, 2, false)) ||
+  // (without queries there is nothing to add, and what is set is 0)
+  if (p->batch == 0 || (p->seqlen_q == 0 && p->accumulate)) return ATTN_OK;
+  if ((p->seqlen_q &&
+       ((s = check_rows("q", q, p->stride_q, p->batch, p->seqlen_q, p->heads_q, cache->d_qk, 2, false)) ||
+        (s = check_ints("lse", lse)))) ||
       (s = check_weight_rows("weights", weights, p->stride_w, p->batch, cache->heads_kv, p->capacity, true)) ||
-      (s = check_ints("lse", lse)) || (s = check_ints("seq_lens", seq_lens)) ||
+      (s = check_ints("seq_lens", seq_lens)) ||
       (p->cols && (s = check_ints("block_table", block_table))))
     return s;
   Region held[4];

@@ -477,6 +477,16 @@ __global__ void __launch_bounds__(kThreads, blocks_of(DQK, NB)) attn_kv_weights_
   }
 }
 
+// No query at all: what is set is 0.
+__global__ void __launch_bounds__(256) attn_kv_weights_clear_kernel(const __grid_constant__ WeightsParams p) {
+  const int64_t all = (int64_t)p.batch * p.c.heads;
+  for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
+    const int b = (int)(i / p.c.heads), h = (int)(i - (int64_t)b * p.c.heads), n = unit_range(p, b).len;
+    float* w = p.w + b * p.w_b + h * p.w_h;
+    for (int t = threadIdx.x; t < n; t += 256) w[t] = 0.0f;
+  }
+}
+
 namespace {
 template <bool BF16, int DQK, int NB>
 cudaError_t weights_launch(const WeightsParams& p, int num_sms, cudaStream_t st) {
@@ -506,6 +516,11 @@ cudaError_t weights_type(const WeightsParams& p, int num_sms, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_kv4_weights(const WeightsParams& p, bool bf16, int num_sms, cudaStream_t st) {
+  if (p.rows == 0) {
+    const unsigned blocks = (unsigned)std::min<int64_t>((int64_t)p.batch * p.c.heads, 8 * num_sms);
+    attn_kv_weights_clear_kernel<<<blocks, 256, 0, st>>>(p);
+    return cudaGetLastError();
+  }
   return bf16 ? weights_type<true>(p, num_sms, st) : weights_type<false>(p, num_sms, st);
 }
 

@@ -570,7 +570,8 @@ attn_status_t attn_kv_decode_shared(const attn_kv4_decode_params_t* p,
  * stride_w, `capacity` entries a row.  accumulate = 1: entries of tokens that were
  * there before (j < seq_lens[b] - seqlen_q) are added to, those of the seqlen_q
  * newest are set; entries of tokens that no query sees stay.  accumulate = 0: the
- * entries of all seq_lens[b] tokens are set.  Entries from seq_lens[b] on are not
+ * entries of all seq_lens[b] tokens are set (to 0 where no query sees them; with seqlen_q = 0
+ * all of them are, and q and lse are not looked at).  Entries from seq_lens[b] on are not
  * touched.  What table entries and page contents are not looked at, is as in
  * attn_kv_decode.  Scores are those of attn_kv_decode, to rounding; sums are FP32 in
  * an order that does not depend on the other sequences: bitwise reproducible.

@@ -216,6 +216,25 @@ def test_weights_captured_with_other_lengths():
         assert torch.equal(w, kv.kv4_weights(q, x.cache, x.t, lens, lse, torch.full_like(w, 2.0)))
 
 
+@pytest.mark.parametrize("lens", [[50, 0, 700, 3], [5] * 2000])
+def test_weights_of_no_queries(lens):
+    """Nothing is added; what is set is 0, up to each length."""
+    x = Held(lens, 3, 64, 64, 64, BF, seed=14)
+    q, lse = x.q(1, 6)[:, :0], torch.empty(len(lens), 6, 0, device="cuda")
+    held = torch.rand(len(lens), 3, 750, generator=x.g).cuda() + 1
+    status = zero()
+    assert torch.equal(kv.kv4_weights(q, x.cache, x.t, x.l, lse, held.clone(), status=status), held)
+    got = kv.kv4_weights(q, x.cache, x.t, x.l, lse, held.clone(), accumulate=False, status=status)
+    attn.query_status(status)
+    past = torch.arange(750, device="cuda") >= x.l[:, None, None]
+    assert torch.equal(got, torch.where(past, held, 0.0))
+    lens = [-1] + lens[1:]
+    got = kv.kv4_weights(q, x.cache, x.t, i32(lens), lse, held.clone(), accumulate=False, status=status)
+    assert torch.equal(got[0], held[0]) and (got[1, :, :lens[1]] == 0).all()
+    with pytest.raises(attn.AttnError, match="out of range"):
+        attn.query_status(status)
+
+
 # ------------------------------------------------------------------ eviction
 
 class Full:

@@ -117,6 +117,14 @@ def test_weights_nothing_to_do(lib):
     assert lib.attn_kv_weights(weights_params(seqlen_q=0), cache_desc(), *none) == OK
 
 
+def test_weights_of_no_queries_are_set_to_something(lib):
+    """Without queries, accumulate = 0 still writes: what it writes to is checked, q and lse are not needed."""
+    a = dict(q=None, table=at(2), lens=at(3), lse=None, w=at(14), status=at(4))
+    for change in (dict(w=None), dict(lens=None), dict(table=None), dict(w=at(2)), dict(w=at(100)), dict(status=at(14))):
+        args = {**a, **change}.values()
+        assert lib.attn_kv_weights(weights_params(seqlen_q=0, accumulate=0), cache_desc(), *args, None) == INVALID
+
+
 # ------------------------------------------------------------------ eviction
 
 def evict_params(**kw):
