@@ -776,6 +776,9 @@ attn_status_t attn_kv_evict(const attn_kv4_evict_params_t* p, const attn_kv4_cac
     return api_fail(ATTN_ERR_UNSUPPORTED, "batch * heads_kv > 2^24, or batch * cols >= 2^31");
   if (p->batch > 1 && p->table_stride < 0)
     return api_fail(ATTN_ERR_INVALID_ARG, "table_stride < 0");
+  // every sequence's first block adds up the pages of all: 2^24 sequences would take the GPU for minutes
+  if (free_head && p->batch > (1 << 16))
+    return api_fail(ATTN_ERR_UNSUPPORTED, "more than 2^16 sequences with a free list");
   if ((s = check_status_word(status))) return s;
   if (free_head && ((s = check_ints("free_head", free_head)) || (s = check_ints("free_head_out", free_head_out)) ||
                     (p->n_free && (s = check_ints("free_pages", free_pages)))))

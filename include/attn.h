@@ -628,7 +628,8 @@ attn_status_t attn_kv_weights(const attn_kv4_weights_params_t* p, const attn_kv4
  * block_table is not changed: its entries past the tokens held are not looked at by
  * the other calls, and attn_kv_plan writes them again.
  * seq_lens out of [0, min(cols * page_size, capacity)] count as 0 and set the status
- * word.  Nothing depends on the order in which blocks run.
+ * word.  Nothing depends on the order in which blocks run.  batch * heads_kv <= 2^24, with a
+ * free list batch <= 2^16.
  */
 typedef struct {
   int batch, cols;

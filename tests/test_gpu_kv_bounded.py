@@ -506,3 +506,17 @@ def test_evict_gives_no_page_of_protected_tokens_back(page, keep):
         for b, n in enumerate(x.lens):
             if n > keep and keep <= 128:
                 assert torch.equal(r.kept[b].cpu(), stay.expand(2, -1))
+
+
+def test_evict_largest_batch_with_a_free_list():
+    """Every sequence gives a page back."""
+    b, page = 2 ** 16, 16
+    c = kv.KV4Cache.empty(2 * b, 1, 64, 64, page_size=page)
+    g = torch.Generator(device="cuda").manual_seed(13)
+    table = torch.randperm(2 * b, generator=g, device="cuda").int().view(b, 2)
+    free, status = torch.full((b + 5,), -9, dtype=torch.int32, device="cuda"), zero()
+    lens, w = torch.full((b,), 17, dtype=torch.int32, device="cuda"), torch.zeros(b, 1, 17, device="cuda")
+    r = kv.kv4_evict(c, table, lens, w, keep=16, free_pages=free, free_head=i32([b + 2]), status=status)
+    attn.query_status(status)
+    assert r.free_head.tolist() == [2] and torch.equal(free[2:b + 2], table[:, 1])
+    assert (free[:2] == -9).all() and (free[b + 2:] == -9).all() and (r.seq_lens == 16).all()

@@ -155,6 +155,15 @@ def test_evict_refusals(lib, change, cache, ptrs, code):
     assert lib.attn_last_error()
 
 
+def test_evict_refuses_more_sequences_than_a_free_list_takes(lib):
+    """Each sequence adds up the pages of all: the time grows with the batch's square."""
+    many = evict_params(batch=2 ** 16 + 1, cols=1, table_stride=1)
+    a = dict(table=at(2), lens=at(3), first=at(7), w=at(14), w_out=at(14), kept=at(16), lens_out=at(5), free=at(8),
+             head=at(9), head_out=at(11), status=at(4))
+    assert lib.attn_kv_evict(many, cache_desc(), *a.values(), None) == UNSUPPORTED
+    assert "2^16 sequences" in str(lib.attn_last_error())
+
+
 def test_evict_nothing_to_do(lib):
     assert lib.attn_kv_evict(evict_params(batch=0), cache_desc(), *[None] * 12) == OK
 
