@@ -28,11 +28,12 @@
 //
 // Numbers: code - 8 is exact in fp16 and so is its product with a bf16 scale (4 + 8
 // bits), times a power of two that makes the largest scale of half a tile 2^11 .. 2^12.
-// K's comes back with the scores; V's goes into the probabilities, relative to the largest
-// of the row's tiles so far (with room for 2^3), which O follows when it grows.
+// K's comes back with the scores; V's goes into the probabilities, in units that the row's
+// largest probability times V's largest scale of half a tile sets: O's reference follows it
+// when it grows, the sum's follows the largest probability alone.
 // q is held as in kvdecode.cu.  Probabilities are FP32 in the sum and rounded to fp16 for
-// the second product, times 2^11: their reference moves when a score passes it by 2^4, so
-// they stay below 2^15, and those 2^-35 below the row's maximum are still told from 0.
+// the second product, times 2^11: a reference moves when what it follows passes it by 2^4, so
+// they stay below 2^15, and those 2^-35 below the largest are still told from 0.
 //
 // What bounds it: instructions (59 % issue, the ALU pipe at 45 %, the tensor pipe at 44 %)
 // and the wait of each softmax row for its scores.  256 requests of 4 rows over 32K tokens, 8 kv
@@ -423,7 +424,7 @@ struct ShSide {
 // 233 us, 192 us with one.)
 template <int DQK, int DV>
 __device__ __forceinline__ void sh_convert(const uint8_t* codes, const uint16_t* scales, bool is_k, uint8_t* operand,
-                                           uint64_t* full, uint64_t* empty, ShBars& bars, int (*x_exp)[2],
+                                           uint64_t* full, uint64_t* empty, ShBars& bars, float (*x_exp)[2],
                                            const ShRows* rows, int n, int dropped, const Abort& ab) {
   constexpr int kStages = ShShape<DQK, DV>::kKS;
   static_assert(kStages == ShShape<DQK, DV>::kVS, "one code for both sides");
@@ -446,7 +447,7 @@ __device__ __forceinline__ void sh_convert(const uint8_t* codes, const uint16_t*
     if (t >= 0) {
       const int e = max((int)(x.top() >> 7) - 127, kExpLow), stage = t % kStages;
       if (lane == 0) {
-        x_exp[t % kXRing][half] = e;
+        x_exp[t % kXRing][half] = is_k ? pow2(e - 11) : (float)e;
         mbar_arrive(&bars.x_full[t % kXRing]);
       }
       x.halves(pow2(11 - e));
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
   uint8_t* sK = sQ + S::kSlots * S::kQTile;
   uint8_t* sV = sK + S::kKS * S::kKTile;
   __shared__ ShBars bars;
-  __shared__ __align__(8) int k_exp[kXRing][2], v_exp[kXRing][2];  // of the halves of a tile
+  __shared__ __align__(8) float k_exp[kXRing][2], v_exp[kXRing][2];  // of the halves of a tile: K's unit, V's exponent
   __shared__ ShRows rows[kRowRing];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
@@ -746,8 +747,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
         fence_proxy_async();
         mbar_arrive(&bars.q_full);
       }
-      float m_run = -INFINITY, l_run = 0.0f;
-      int v_ref = 0, tiles = 0;  // of this group's O
+      // l is held times 2^(kBias - m_run), O times 2^(22 - o_run); both references are whole
+      // numbers, and follow their maxima when those pass them by more than kLag.
+      float m_run = -INFINITY, o_run = -INFINITY, l_run = 0.0f;
+      int tiles = 0;  // of this group's O
       for (int kt = pc.kt; kt < pc.kt_end; ++kt, ++t) {
         if (S::kSlots == 2 && !both && ((kt - pc.kt) & 1) != slot) continue;
         const uint32_t n = used++, buf = n & 1u;
@@ -760,15 +763,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
         uint32_t s[2][32];
         tmem_ld32(sb, s[0]);
         tmem_ld32(sb + 32, s[1]);
-        const int2 ke2 = *reinterpret_cast<const int2*>(k_exp[t % kXRing]);
-        const int2 ve2 = *reinterpret_cast<const int2*>(v_exp[t % kXRing]);
-        const int ke[2] = {ke2.x, ke2.y}, ve[2] = {ve2.x, ve2.y};
-        // V's unit: the largest exponent of the piece's tiles
-        const int top = max(ve[0], ve[1]);
-        const int v_new = tiles == 0 ? top : top > v_ref ? min(top + 3, 127) : v_ref;
+        const float2 ku2 = *reinterpret_cast<const float2*>(k_exp[t % kXRing]);
+        const float2 ve2 = *reinterpret_cast<const float2*>(v_exp[t % kXRing]);
+        const float ku[2] = {ku2.x, ku2.y}, ve[2] = {ve2.x, ve2.y};
         float xt[2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) xt[c] = fminf(fmaxf(xs * pow2(ke[c] - 11), 1.17549435e-38f), 3.40282347e38f);
+        for (int c = 0; c < 2; ++c) xt[c] = fminf(fmaxf(xs * ku[c], 1.17549435e-38f), 3.40282347e38f);
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(&bars.s_free[slot]);
@@ -786,12 +786,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
           m_half[c] = xt[c] * fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
         }
         const float m_tile = fmaxf(m_half[0], m_half[1]);
-        float alpha = 1.0f;
         if (m_tile > m_run + kLag) {
-          alpha = ex2(m_run - m_tile);
-          m_run = m_tile;
+          const float m = ceilf(m_tile);
+          l_run *= ex2(m_run - m);
+          m_run = m;
         }
-        const float off = m_run == -INFINITY ? 0.0f : kBias - m_run;
+        const float o_tile = fmaxf(m_half[0] + ve[0], m_half[1] + ve[1]);
+        float alpha = 1.0f;
+        if (o_tile > o_run + kLag) {
+          const float o = ceilf(o_tile);
+          alpha = ex2(o_run - o);
+          o_run = o;
+        }
+        const bool none = m_run == -INFINITY;
+        const float off = none ? 0.0f : kBias - m_run, from = none ? 0.0f : m_run - o_run;
         // the buffer's earlier P has been read
         if (n >= 2 && !mbar_wait_warp(&bars.o_done[slot][buf], ((n >> 1) - 1) & 1u, ab)) {
           ok = false;
@@ -801,9 +809,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
         float sum = 0.0f;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          // (not above 0; from 2^-39 down P is 0 in fp16, but must not be in the sum)
-          const int lift = max(ve[c] - v_new, -60);
-          const float oc = off + (float)lift;
+          // (from 2^-39 down P is 0 in fp16, but must not be in the sum)
+          const float lift = fmaxf(from + ve[c], -60.0f);
+          const float oc = off + lift;
           const uint64_t x2 = f2_pack(xt[c], xt[c]), off2 = f2_pack(oc, oc);
           uint64_t acc2[2] = {0ull, 0ull};
           uint32_t pk[16];
@@ -818,12 +826,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
           tmem_st16(sb + KT + buf * 32 + c * 16, pk);
           float s0, s1;
           f2_unpack(f2_add(acc2[0], acc2[1]), s0, s1);
-          sum = fmaf(s0 + s1, pow2(-lift), sum);
+          sum = fmaf(s0 + s1, pow2(-min((int)lift, 126)), sum);
         }
-        l_run = l_run * alpha + sum;
-        // O of this row so far: the maximum grew, or V's unit did
+        l_run += sum;
+        // O of this row so far, if its reference moved
         if (tiles > 0) {
-          if (v_new > v_ref) alpha *= pow2(max(v_ref - v_new, -126));
           if (__any_sync(0xffffffffu, alpha != 1.0f)) {
             if (!mbar_wait_warp(&bars.o_done[slot][buf ^ 1u], ((n - 1) >> 1) & 1u, ab)) {  // (the last product)
               ok = false;
@@ -842,7 +849,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
             }
           }
         }
-        v_ref = v_new;
         ++tiles;
         tmem_st_wait();
         tc_fence_before();
@@ -867,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
       if (live) *reinterpret_cast<float2*>(ml) = make_float2(m_run - kBias, l_run);
       if (tiles > 0) {
         const uint32_t ob = tmem + lane_off + S::kTmemO + slot * DV;
-        const float unit = pow2(v_ref - 11);
+        const float unit = pow2(max(min((int)(o_run - m_run), 127) - 11, -126));
         // 32 columns at a time through the warp's part of Q's memory (its MMAs have ended), so
         // that eight lanes write a row's 128 bytes
         const int lane = threadIdx.x & 31;

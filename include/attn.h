@@ -496,7 +496,8 @@ attn_status_t attn_kv_read(const attn_kv4_cache_t* cache, attn_dtype_t dtype, in
  * units set by the largest V scale, of any group of dims, of the tokens met so far:
  * beside a V scale 2^24 times the others', the others lose bits.  So O carries an
  * error of up to 2^-11 of sum p |v|, with an FP32 output as with a 16-bit one.  V
- * scales of 2^101 and more (values above 10^30) may give infinities.  The result
+ * scales of 2^101 and more (values above 10^30) may give infinities, and so may scores
+ * of 2^22 and more (FP32 tells those in the exponentials no better than 1/4).  The result
  * does not depend on other sequences' lengths beyond the order of its sums, and is
  * bitwise reproducible for the same call on the same device.
  * Lengths are read on the device: a captured call serves any lengths.
@@ -535,10 +536,13 @@ attn_status_t attn_kv_decode(const attn_kv4_decode_params_t* p, const attn_kv4_c
  * multiples of 64 tokens; the rest of it is read as each request's own.  A request that
  * has fewer tokens than the prefix and the seqlen_q newest shares nothing, and neither
  * does a group with fewer than two that do.
- * p as in attn_kv_decode, without a window (window_left = -1; sinks is ignored).  Scores
- * and probabilities of the shared part are rounded as attn_kv_decode's are: O carries
- * an error of up to 2^-11 of sum p |v|, and beside a V scale 2^24 times the others', in
- * the shared part, the others lose bits.
+ * p as in attn_kv_decode, without a window (window_left = -1; sinks is ignored).  Of the
+ * shared part, codes times scales are FP16 operands: exact, but elements of K whose scale is
+ * below 2^-28 of the largest one S_k of the 32 tokens around them are off by up to 2^-32 S_k.
+ * Probabilities are rounded to FP16, in units that the row's largest product of a probability
+ * and a V scale sets (the largest of each in any 32 tokens): O carries an error of up to 2^-11
+ * of sum p |v|, as attn_kv_decode's does, and for each token one of up to 2^-31 of that
+ * product.
  * group_starts that do not ascend within [0, batch] (no group shares anything then),
  * shared_lens out of [0, cols * page_size] (that group shares nothing) set the status
  * word, beside what attn_kv_decode reports.  Every wait of the kernels on an mbarrier has a

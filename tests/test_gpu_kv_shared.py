@@ -390,3 +390,75 @@ def test_shared_lengths_far_below_zero(bad, sq):
         assert (o[at] == 0).all() and torch.isneginf(lse[at]).all()
         keep = [b for b in range(5) if b != at]
         within(o[keep], lse[keep], [r[keep] for r in ref])
+
+
+@pytest.mark.parametrize("hidden", [-80, -18])
+@pytest.mark.parametrize("large", [0, 12, 16, 20, 24, 28])
+@pytest.mark.parametrize("where", ["first", "last"])
+def test_shared_many_small_probabilities_beside_large_values(large, where, hidden):
+    """One token of probability 0.6 and 960 that share the rest, beside a tile of V scales 2^k
+    times theirs that nobody looks at, or hardly: a token's probability p enters as p 2^(11 + e - r), 2^e its V
+    scale's exponent and 2^r the reference, at most twice the largest product m of a probability and a
+    V scale; half a step below fp16's normal range, 2^-25, is 2^(-36 - e + r) |v| in O, |v| < 2^(e + 4): 2^-31 m.
+    (As many heads as blocks, so that a block's run holds the whole prefix, and all of it in even
+    tiles: the softmax groups take turns.)"""
+    h, n, dt = 160, 1024, BF
+    x = Groups([(n, [1, 1])], h, 64, 64, 64, dt, seed=19)
+    scale, q0 = 1 / 8, 8.0
+    of = lambda p: math.log(p) / (scale * q0)  # noqa: E731  (dim 0 of a key whose probability is p times the largest's)
+    slots = {s: i for i, s in enumerate(x.slots)}
+    at = torch.tensor([slots[x.table[0][j // 64] * 64 + j % 64] for j in range(n)])
+    big = at[:64] if where == "first" else at[-128:-64]
+    x.k.zero_()
+    x.v.fill_(1.0)
+    x.k[:, :, 0] = of(1.37 * 2.0 ** -11)
+    x.k[at[520], :, 0] = 0.0
+    x.k[big, :, 0] = of(2.0 ** hidden)
+    x.v[big] = 2.0 ** large
+    x.write()
+    q = torch.zeros(2, 1, h, 64)
+    q[..., 0] = q0
+    q = q.to(dt).cuda()
+    status = zero()
+    o, lse = x.call(q, o_dtype=torch.float32, status=status)
+    attn.query_status(status)
+    ro, rl, mag, _ = x.reference(q)
+    p_max = torch.exp(-rl).transpose(1, 2)[..., None]  # (the largest score is 0, scales are 1 / 7 and 2^large / 7)
+    most = 1.01 / 7 * max(1.0, 2.0 ** (large + hidden + 0.2))  # (0.2: of K's scale in bf16, 2^-8 of 80 and less)
+    err = (o.double() - ro).abs()
+    assert (err <= (2.0 ** -11 + 2.0 ** -13) * mag + n * 2.0 ** -31 * most * p_max).all(), float(err.max())
+    assert (lse.double() - rl).abs().max() <= 2.0 ** -19 + 2.0 ** -20 * 8
+
+
+@pytest.mark.parametrize("apart", [8, 20, 26, 30])
+def test_shared_keys_of_very_different_scales(apart):
+    """Every other token's K is 2^apart times the others' and far below them in score: what the
+    others lose is at most 2^-32 of its scale an element (half a step of the scale's operand, 2^-25 below
+    fp16's normal range, times 8 for the code, and one for the product, all in units of 2^-11 of the scale)."""
+    x = Groups([(512, [3] * 5)], 1, 128, 128, 64, BF, seed=20)
+    slots = {s: i for i, s in enumerate(x.slots)}
+    at = torch.tensor([slots[x.table[0][j // 64] * 64 + j % 64] for j in range(512)])
+    x.k[:, :, :32] = 0.0
+    x.k = (x.k.double() * 2.0 ** -apart).to(BF)
+    x.k[at[::2]] = 0.0
+    x.k[at[::2], :, 0] = -1.0
+    x.write()
+    q = x.q(1, 4).double() * 2.0 ** apart
+    q[..., 0] = 2.0 ** (apart + 5)
+    q[..., 1:32] = 0.0
+    q = q.to(BF)
+    status = zero()
+    o, lse = x.call(q, o_dtype=torch.float32, status=status)
+    attn.query_status(status)
+    ro, rl, mag, _ = x.reference(q)
+    scale = 1 / math.sqrt(128)
+    # of the tokens that count: 2^-20 of sum |q k|, and the loss beside a scale of 1 / 7
+    small = x.k.double().cuda().clone()
+    small[at[::2]] = 0.0
+    d = scale * (2.0 ** -20 * (q.double().abs()[:, 0] @ small[:, 0].abs().T).amax(-1)
+                 + 2.0 ** -32 / 7 * 1.01 * q.double().abs()[:, 0].sum(-1))[..., None]
+    assert float(rl.min()) + 2.0 ** (apart + 4) * scale > 0  # (the large ones' scores are that far below 0)
+    grow = torch.expm1(d)
+    assert ((lse.double() - rl).abs() <= grow + 2.0 ** -21 * rl.abs() + 2.0 ** -19).all()
+    tol = (2.0 ** -11 + 2.0 ** -13 + 2 * grow[:, None]) * mag + 2.0 ** -25
+    assert ((o.double() - ro).abs() <= tol).all()
