@@ -16,6 +16,15 @@ be held to a budget of tokens by the attention that they receive:
   kv.kv4_weights(q, cache, table, p.seq_lens, lse, weights)
   e = kv.kv4_evict(cache, table, p.seq_lens, weights, keep=budget, first=prompt, recent=64,
                    free_pages=free, free_head=p.free_head)  # lengths and free pages for plan
+  gone += p.seq_lens - e.seq_lens                           # int32 [batch], from 0 on
+
+plan counts the tokens that are held.  The keys in the cache are rotated at their places in
+the text, so once tokens are gone new ones are rotated that much further on (and the tables
+of angles reach as far as the text does, not only the budget):
+
+  request = torch.searchsorted(p.cu_seqlens[1:], row, right=True)  # row: arange(rows), int32
+  positions = torch.where(p.positions < 0, -1, p.positions + gone[request.clamp(max=batch - 1)])
+  q, k = attn.qk_norm_rope(q, k, cos, sin, positions=positions, ...)
 
 Longer chunks of a prompt read their prefix back instead (plan with
 free_pages=None maps tokens that are held already, kv4_read returns their rows)
@@ -320,7 +329,7 @@ def kv4_evict(cache, block_table, seq_lens, weights, *, keep, first=None, recent
     """Cuts each sequence of more than ``keep`` tokens down to that many, each kv head
     by itself: the first first[b], the last ``recent`` and of the others those with the
     largest weight; the cache's rows move together in their order (attn_kv_evict).
-    Returns an Evicted.
+    Returns an Evicted.  Positions of later tokens: see the head of this module.
 
     weights: float32 [B, heads_kv, capacity], changed in place unless ``weights_out``
     is given.  first: int32 [B] or None.  free_pages and free_head (as kv.plan takes

@@ -192,3 +192,59 @@ def test_pages_and_rows_past_32_bits():
         got.append([o.clone(), lse, before, w, e.kept, e.seq_lens, *kv.kv4_read(c, slots.flatten())])
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def test_positions_after_evictions_are_those_of_the_text():
+    """The loop that kv's head describes, with budgets that are passed often: every row of the
+    cache is what a cache without a budget holds at that token's place in the text, bit for bit."""
+    b, hk, d, page, keep, steps = 4, 2, 64, 16, 40, 30
+    g = torch.Generator().manual_seed(24)
+    fresh = torch.randint(0, 6, (steps, b), generator=g).int()
+    fresh[0] = torch.tensor([30, 45, 8, 0], dtype=torch.int32)
+    rows = int(fresh.sum(1).max()) + 3
+    total = fresh.sum(0)
+    cos, sin = attn.rope_tables(int(total.max()), d)
+    cache, table = empty_cache(40, hk, d, d, page), torch.full((b, 8), -1, dtype=torch.int32, device="cuda")
+    free, status = torch.randperm(40, generator=g).int().cuda(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    head, ctx, gone, first = i32([0]), i32([0] * b), i32([0] * b), i32([4, 0, 4, 2])
+    w = torch.zeros(b, hk, 8 * page, device="cuda")
+    row = torch.arange(rows, dtype=torch.int32, device="cuda")
+    held = [[[] for _ in range(hk)] for _ in range(b)]  # places in the text of the tokens held
+    text_k, text_v = [[] for _ in range(b)], [[] for _ in range(b)]
+    for new in fresh:
+        q, k, v = (torch.randn(rows, hk, d, generator=g).to(BF).cuda() for _ in range(3))
+        p = kv.plan(ctx, new.cuda(), table, page_size=page, num_pages=40, rows=rows, free_pages=free, free_head=head,
+                    status=status)
+        request = torch.searchsorted(p.cu_seqlens[1:], row, right=True)
+        positions = torch.where(p.positions < 0, -1, p.positions + gone[request.clamp(max=b - 1)])
+        _, turned = attn.qk_norm_rope(q, k, cos, sin, positions=positions, status=status)
+        kv.kv4_write(cache, turned, v, p.slots, status=status)
+        w += torch.rand(w.shape, generator=g).cuda()
+        r = kv.kv4_evict(cache, table, p.seq_lens, w, keep=keep, first=first, recent=3, free_pages=free,
+                         free_head=p.free_head, status=status)
+        gone += p.seq_lens - r.seq_lens
+        head, ctx = r.free_head, r.seq_lens
+        at, kept = 0, r.kept.tolist()
+        for i, n in enumerate(new.tolist()):
+            done = len(text_k[i])
+            text_k[i] += list(k[at:at + n])
+            text_v[i] += list(v[at:at + n])
+            at += n
+            for h in range(hk):
+                places = held[i][h] + list(range(done, done + n))
+                held[i][h] = [places[j] for j in kept[i][h] if j >= 0]
+    attn.query_status(status)
+    assert (total > keep).sum() >= 3 and gone.tolist() == (total - torch.tensor(ctx.tolist())).tolist()
+    for i in range(b):
+        n, m = len(text_k[i]), int(ctx[i])
+        whole = empty_cache(n // page + 1, hk, d, d, page)
+        k, v = torch.stack(text_k[i]), torch.stack(text_v[i])
+        place = torch.arange(n, dtype=torch.int32, device="cuda")
+        _, turned = attn.qk_norm_rope(k, k, cos, sin, positions=place)
+        kv.kv4_write(whole, turned, v, place)
+        want = kv.kv4_read(whole, place)
+        t = table[i].tolist()
+        got = kv.kv4_read(cache, i32([t[j // page] * page + j % page for j in range(m)]))
+        for h in range(hk):
+            for a, c in zip(got, want):
+                assert torch.equal(a[:, h], c[torch.tensor(held[i][h]), h]), (i, h)
