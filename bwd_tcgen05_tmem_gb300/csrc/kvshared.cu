@@ -747,8 +747,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
         fence_proxy_async();
         mbar_arrive(&bars.q_full);
       }
-      // l is held times 2^(kBias - m_run), O times 2^(22 - o_run); both references are whole
-      // numbers, and follow their maxima when those pass them by more than kLag.
+      // l is held times 2^(kBias - m_run), O times 2^(22 - o_run).  The references follow their
+      // maxima when those pass them by more than kLag; o_run lies a whole number from m_run then,
+      // so that the probability that m_run is of is exact in fp16.
       float m_run = -INFINITY, o_run = -INFINITY, l_run = 0.0f;
       int tiles = 0;  // of this group's O
       for (int kt = pc.kt; kt < pc.kt_end; ++kt, ++t) {
@@ -787,14 +788,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
         }
         const float m_tile = fmaxf(m_half[0], m_half[1]);
         if (m_tile > m_run + kLag) {
-          const float m = ceilf(m_tile);
-          l_run *= ex2(m_run - m);
-          m_run = m;
+          l_run *= ex2(m_run - m_tile);
+          m_run = m_tile;
         }
         const float o_tile = fmaxf(m_half[0] + ve[0], m_half[1] + ve[1]);
         float alpha = 1.0f;
         if (o_tile > o_run + kLag) {
-          const float o = ceilf(o_tile);
+          const float o = m_run + ceilf(o_tile - m_run);
           alpha = ex2(o_run - o);
           o_run = o;
         }
@@ -826,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
           tmem_st16(sb + KT + buf * 32 + c * 16, pk);
           float s0, s1;
           f2_unpack(f2_add(acc2[0], acc2[1]), s0, s1);
-          sum = fmaf(s0 + s1, pow2(-min((int)lift, 126)), sum);
+          sum = fmaf(s0 + s1, ex2(-lift), sum);
         }
         l_run += sum;
         // O of this row so far, if its reference moved
@@ -873,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kv_shared_kernel(const __gri
       if (live) *reinterpret_cast<float2*>(ml) = make_float2(m_run - kBias, l_run);
       if (tiles > 0) {
         const uint32_t ob = tmem + lane_off + S::kTmemO + slot * DV;
-        const float unit = pow2(max(min((int)(o_run - m_run), 127) - 11, -126));
+        const float unit = ex2(fmaxf(o_run - m_run - 11.0f, -126.0f));
         // 32 columns at a time through the warp's part of Q's memory (its MMAs have ended), so
         // that eight lanes write a row's 128 bytes
         const int lane = threadIdx.x & 31;
