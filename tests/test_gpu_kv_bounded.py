@@ -520,3 +520,56 @@ def test_evict_largest_batch_with_a_free_list():
     attn.query_status(status)
     assert r.free_head.tolist() == [2] and torch.equal(free[2:b + 2], table[:, 1])
     assert (free[:2] == -9).all() and (free[b + 2:] == -9).all() and (r.seq_lens == 16).all()
+
+
+@pytest.mark.parametrize("page_id", [-1, -2 ** 31, 10 ** 9, None])
+@pytest.mark.parametrize("col", [0, 1, 2, 3, 5, 7])
+def test_evict_around_a_page_outside_the_cache(col, page_id):
+    """Rows that come from or go to such a page stay as they are, every other row of that
+    sequence and of the others moves, weights and lists are as without it; if the page goes back it does as
+    -1.  Only a page that nothing moves in and that does not go back is not noticed."""
+    x = Full([128, 100, 70], 2, 128, 128, 16, seed=14)
+    keep, first, recent = 60, [20, 20, 0], 7
+    x.table[0][col] = x.cache.num_pages if page_id is None else page_id
+    t, w = i32(x.table), x.weights("spread")
+    want, out = [a.clone() for a in x.arrays], w.clone()
+    kept = torch.full((3, 2, keep), -1, dtype=torch.int32)
+    for b, n in enumerate(x.lens):
+        for a in range(2):
+            src = boundedref.stays(w[b, a, :n].tolist(), keep, first[b], recent)
+            kept[b, a] = torch.tensor(src, dtype=torch.int32)
+            out[b, a, :keep] = w[b, a, src]
+            place = lambda j: (x.table[b][j // 16], j % 16)  # noqa: E731
+            moves = [(place(j), place(i)) for i, j in enumerate(src)]
+            for was, arr in zip(x.arrays, want):
+                for (p0, r0), (p1, r1) in moves:
+                    if 0 <= p0 < x.cache.num_pages and 0 <= p1 < x.cache.num_pages:
+                        arr[p1, a, r1] = was[p0, a, r0]
+    back = [p if 0 <= p < x.cache.num_pages else -1 for p in boundedref.pages_back(x.table, x.lens, keep, 16)]
+    free, status, wd = torch.full((30,), -9, dtype=torch.int32, device="cuda"), zero(), w.cuda()
+    r = kv.kv4_evict(x.cache, t, x.l, wd, keep=keep, first=i32(first), recent=recent, free_pages=free,
+                     free_head=i32([25]), status=status)
+    torch.cuda.synchronize()
+    x.same(want)
+    assert torch.equal(r.kept.cpu(), kept) and torch.equal(wd.cpu(), out) and r.seq_lens.tolist() == [keep] * 3
+    assert r.free_head.tolist() == [25 - len(back)] and free.tolist() == [-9] * (25 - len(back)) + back + [-9] * 5
+    assert (-1 in back) == (col >= 4)
+    if col == 0:
+        attn.query_status(status)
+    else:
+        with pytest.raises(attn.AttnError, match="out of range"):
+            attn.query_status(status)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_weights_beside_an_infinite_scale(sign):
+    """It changes its own token's entry of its head alone."""
+    x = Held([200, 200], 2, 128, 128, 64, BF, seed=15)
+    q = x.q(1, 8)
+    lse = kv.kv4_decode(q, x.cache, x.t, x.l)[1]
+    w = kv.kv4_weights(q, x.cache, x.t, x.l, lse, torch.ones(2, 2, 200, device="cuda"))
+    x.cache.k_scales[x.table[0][1], 1, 7, 2] = sign * float("inf")
+    got = kv.kv4_weights(q, x.cache, x.t, x.l, lse, torch.ones(2, 2, 200, device="cuda"))
+    other = torch.ones_like(w, dtype=torch.bool)
+    other[0, 1, 71] = False
+    assert torch.equal(got[other], w[other])

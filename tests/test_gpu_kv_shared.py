@@ -462,3 +462,25 @@ def test_shared_keys_of_very_different_scales(apart):
     assert ((lse.double() - rl).abs() <= grow + 2.0 ** -21 * rl.abs() + 2.0 ** -19).all()
     tol = (2.0 ** -11 + 2.0 ** -13 + 2 * grow[:, None]) * mag + 2.0 ** -25
     assert ((o.double() - ro).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dqk,dv", DIMS)
+@pytest.mark.parametrize("side", ["k", "v"])
+@pytest.mark.parametrize("members", [3, 40])
+def test_shared_infinite_scales(side, members, dqk, dv):
+    """An infinite scale does to its own dims (of V) or rows (of K) what infinities and 0 * inf do in
+    the formula, and nothing to the others, whose precision it must not take."""
+    x = Groups([(256, [5] * members), (256, [5, 6])], 2, dqk, dv, 64, BF, seed=21)
+    getattr(x.cache, side + "_scales")[x.table[0][1], 1, 9, 1] = float("inf")
+    q, status = x.q(1, 8), zero()
+    o, lse = x.call(q, status=status)
+    attn.query_status(status)
+    ro, rl, mag, big = x.reference(q)
+    for got, want in ((o, ro), (lse, rl)):
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(torch.isinf(got), torch.isinf(want)) and (got[torch.isinf(got)] == want[torch.isinf(got)]).all()
+    bad = ~torch.isfinite(ro)
+    assert int(bad.sum()) == members * 4 * (dv if side == "k" else 32)
+    fine = torch.isfinite(rl)
+    within(torch.where(bad, 0.0, o), torch.where(fine, lse, 0.0), (torch.where(bad, 0.0, ro), torch.where(fine, rl, 0.0),
+                                                                   torch.where(bad, 0.0, mag), torch.where(fine, big, 0.0)))
