@@ -35,9 +35,9 @@
 // the second product, times 2^11: a reference moves when what it follows passes it by 2^4, so
 // they stay below 2^15, and those 2^-35 below the largest are still told from 0.
 //
-// What bounds it: instructions (59 % issue, the ALU pipe at 45 %, the tensor pipe at 44 %)
+// What bounds it: instructions (60 % issue, the ALU pipe at 45 %, the tensor pipe at 44 %)
 // and the wait of each softmax row for its scores.  256 requests of 4 rows over 32K tokens, 8 kv
-// heads of 128, one GB300: 182 us, the prefix kernel 145 of them (0.95 PFLOP/s); plan 4,
+// heads of 128, one GB300: 182 us, the prefix kernel 142 of them (0.97 PFLOP/s); plan 4,
 // own tokens 20, the two joins 14.  64 requests over 8K tokens 64.5 us.  The first
 // instruction cache is what K's and V's conversion in one loop, and loops that are not
 // unrolled, are for: apart they took 233 us.  Tiles of 128 keys 250, four softmax groups of

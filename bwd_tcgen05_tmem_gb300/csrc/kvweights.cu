@@ -18,7 +18,7 @@
 // What bounds it: the instructions of a tile, 411 a warp for 32 tokens of head dim 128
 // and 4 query rows (unpacking 80, scales on the sums 50, exponentials and sums 60,
 // addresses and pages 60); the schedulers issue in 60 % of the cycles, the ALU pipe is
-// busy in 47 %, the memory runs at half its rate.  16 x 32K tokens of 8 kv heads, head dim 128, one GB300: 84 us,
+// busy in 47 %.  16 x 32K tokens of 8 kv heads, head dim 128, one GB300: 84 us,
 // 4.0 TB/s of the 6.7 that a copy reaches; head dim 64 56, 192 102, 256 128, 16 query
 // rows 102.  128 rows a head (the last 32 queries of 8 prompts of 32K tokens) take 276:
 // a block of 8 rows costs 8 products, 16 scalings, 8 exponentials and their sums.

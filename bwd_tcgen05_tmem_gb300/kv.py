@@ -238,7 +238,8 @@ def kv4_decode_shared(q, cache, block_table, seq_lens, group_starts, shared_lens
     """kv4_decode (without a window) for requests that share their first tokens
     (attn_kv_decode_shared): requests group_starts[g] .. group_starts[g + 1] - 1 name
     the same pages for their first shared_lens[g] tokens, which are read once for all of
-    them.  group_starts: int32 [groups + 1]; shared_lens: int32 [groups].
+    them: quicker than kv4_decode for long prefixes of many requests, slower for few or
+    short ones (see the header).  group_starts: int32 [groups + 1]; shared_lens: int32 [groups].
     Rows that lack a part because a wait of the kernels ran out are NaN."""
     check_buffers(status, workspace)
     lib = fast()

@@ -528,7 +528,9 @@ attn_status_t attn_kv_decode(const attn_kv4_decode_params_t* p, const attn_kv4_c
  * attn_kv_decode for batches whose requests share their first tokens (a system prompt,
  * a document, samples of one request): the same results, to rounding, but what a
  * group's requests share is read and converted once for all of them, and multiplied
- * with all their query rows at a time.
+ * with all their query rows at a time.  (On a GB300 that pays where attn_kv_decode would read
+ * 300 MB of shared codes and scales over and over, say 16 requests over 16K tokens of 8 kv heads of
+ * 128, and costs 10 to 30 us more than attn_kv_decode for few requests or short prefixes.)
  * Requests group_starts[g] .. group_starts[g + 1] - 1 are group g (int32 [groups + 1],
  * ascending; requests outside all groups share nothing), and the first shared_lens[g]
  * tokens of each of them lie in the same pages: their rows of block_table name the same
